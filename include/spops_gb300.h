@@ -289,6 +289,91 @@ SPOPS_API int spops_masked_adam_csr(float* param, float* exp_avg, float* exp_avg
                                     int32_t nnz, int32_t step, double lr, double beta1, double beta2, double eps,
                                     int maximize, void* stream);
 
+/* ---------------------------------------------------------------- low-rank adapters */
+
+/* The low-rank half of a RoSA adapter (a low-rank and a sparse update beside one frozen
+ * projection; the sparse half is csr_add / sddmm above), for one adapter or for the adapters
+ * of many requests in one batch. Adapter i is A_i (rank x in_features) and B_i
+ * (out_features x rank) with the factor s_i = scale_all * scale[i] (scale NULL: 1); the
+ * adapters lie one behind the other in A [n_adapters, rank, in_features] and
+ * B [n_adapters, out_features, rank]. Adapters of a smaller rank are padded with zeros.
+ * Activations are token-major: row t of X, Y, ... is token t, rows ld elements apart (ld at
+ * least the columns), so a slice of a fused projection's columns can be an operand.
+ * rank <= SPOPS_LORA_MAX_RANK. Products accumulate in fp32; X A_i^T stays in 32 bits (on the
+ * tensor cores as the sum of two 16-bit parts, which hold at least 16 of its bits), and every
+ * output is rounded once. A token's result depends on no other token and on no other
+ * adapter's weights (infinities and NaN stay where they are). Deterministic. */
+#define SPOPS_LORA_MAX_RANK 128
+
+/* Bytes of the plan of a batch. */
+SPOPS_API size_t spops_lora_plan_size(int32_t tokens, int32_t n_adapters);
+
+/* The plan of a batch: its tokens sorted by adapter, for every projection of every layer that
+ * the batch runs through. adapter_ids [tokens] int32: the adapter of each token, in any order
+ * (NULL: all tokens use adapter 0); a token whose id lies outside 0 .. n_adapters - 1 (-1 by
+ * convention) has no adapter. plan: 16-byte aligned buffer of at least spops_lora_plan_size
+ * bytes, owned by the caller and left unchanged by the operators. */
+SPOPS_API int spops_lora_plan_build(const int32_t* adapter_ids, int32_t tokens, int32_t n_adapters, void* plan,
+                                    size_t plan_size, void* stream);
+
+/* Y[t] = base[t] + s_i (X[t] A_i^T) B_i^T for every token t of adapter i; Y[t] = base[t] for a
+ * token without one. base NULL: zeros. Y == base (same row stride): in place. h [tokens, rank]
+ * fp32 (may be NULL) receives X[t] A_i^T (zeros for tokens without an adapter), which
+ * spops_lora_grad takes. Y may be NULL when h is not. The outputs must not overlap the other
+ * arrays. */
+SPOPS_API int spops_lora_add(const void* X, int64_t ldx, const void* A, const void* B, const float* scale,
+                             float scale_all, int dtype, int32_t tokens, int32_t in_features, int32_t out_features,
+                             int32_t rank, int32_t n_adapters, const void* base, int64_t ldb, void* Y, int64_t ldy,
+                             float* h, const void* plan, void* stream);
+
+/* Scratch bytes spops_lora_grad needs. */
+SPOPS_API size_t spops_lora_grad_workspace_size(int32_t tokens, int32_t rank);
+
+/* The gradients of spops_lora_add for the output gradient dY [tokens, out_features]:
+ *   dX[t] = dX_base[t] + s_i (dY[t] B_i) A_i        (dX_base NULL: zeros; dX == dX_base: in place)
+ *   dA_i  = s_i sum over i's tokens of (dY[t] B_i)^T X[t]     [n_adapters, rank, in_features]
+ *   dB_i  = s_i sum over i's tokens of dY[t]^T (X[t] A_i^T)   [n_adapters, out_features, rank]
+ * (adapters without tokens get zeros). h: the one spops_lora_add wrote for this X, or NULL to
+ * form it here. Each of dX, dA and dB may be NULL: not computed. workspace: 16-byte aligned,
+ * at least spops_lora_grad_workspace_size bytes. */
+SPOPS_API int spops_lora_grad(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* A, const void* B,
+                              const float* scale, float scale_all, int dtype, int32_t tokens, int32_t in_features,
+                              int32_t out_features, int32_t rank, int32_t n_adapters, const float* h,
+                              const void* dX_base, int64_t ldb, void* dX, int64_t lddx, void* dA, void* dB,
+                              const void* plan, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- gradient norm, clipping */
+
+/* Bytes of a set of gradients. */
+SPOPS_API size_t spops_grad_set_size(int32_t tensors);
+
+/* The table of a set of gradients that are clipped together, written to the device buffer
+ * `set` (16-byte aligned, at least spops_grad_set_size bytes). grads, outs, counts and dtypes
+ * are HOST arrays, read before the call returns: gradient i has counts[i] elements of
+ * dtypes[i] (spops_dtype) at the device pointer grads[i] and goes to outs[i] (outs NULL, or
+ * outs[i] == grads[i]: in place). No output may overlap another gradient or output. The set
+ * holds the pointers, not the values: it serves every later call while those buffers live.
+ * *chunks_out and *in_place_out are passed to the calls below. */
+SPOPS_API int spops_grad_set_build(const void* const* grads, void* const* outs, const int64_t* counts,
+                                   const int32_t* dtypes, int32_t tensors, void* set, size_t set_size,
+                                   int64_t* chunks_out, int32_t* in_place_out, void* stream);
+
+/* Scratch bytes of spops_grad_norm and spops_clip_grads. */
+SPOPS_API size_t spops_grad_norm_workspace_size(void);
+
+/* *norm_out (device fp32) = the 2-norm of all gradients of the set together; 0 for an empty
+ * set. Squares are summed in at least 32 bits, the sums in 64 (no overflow or underflow of the
+ * squares), in one order: deterministic. */
+SPOPS_API int spops_grad_norm(const void* set, int32_t tensors, int64_t chunks, float* norm_out, void* workspace,
+                              size_t ws_bytes, void* stream);
+
+/* spops_grad_norm, then out = c * grad for every gradient with c = min(1, max_norm / (norm +
+ * 1e-6)), each product rounded once. max_norm >= 0 (infinity: c = 1). With c = 1 gradients in
+ * place are left alone. An infinite norm gives c = 0 and a NaN one c = NaN, as the formula
+ * says. Nothing is read back to the host. */
+SPOPS_API int spops_clip_grads(const void* set, int32_t tensors, int64_t chunks, int in_place, double max_norm,
+                               float* norm_out, void* workspace, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- checks */
 
 /* Scratch bytes spops_check_csr needs (a bitmap of m bits for the permutation check). */

@@ -409,3 +409,8 @@ __all__ += ["Transpose", "csr_transpose", "permute_values", "spmm_grad_b", "mask
 from .layer import SparseLinear, SparseLinearFunction  # noqa: E402  (uses the functions above)
 
 __all__ += ["SparseLinear", "SparseLinearFunction"]
+
+from .lora import LoraPlan, lora_add, lora_grad, lora_plan  # noqa: E402
+from .clip import GradSet, clip_grads, grad_norm  # noqa: E402
+
+__all__ += ["LoraPlan", "lora_plan", "lora_add", "lora_grad", "GradSet", "grad_norm", "clip_grads"]

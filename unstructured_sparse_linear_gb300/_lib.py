@@ -14,6 +14,8 @@ _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _INT = ctypes.c_int
 _SZ = ctypes.c_size_t
+_I64 = ctypes.c_int64
+_F32 = ctypes.c_float
 
 # name -> (restype, argtypes), in the order of include/spops_gb300.h
 SIGNATURES = {
@@ -47,6 +49,18 @@ SIGNATURES = {
                                  ctypes.c_double, ctypes.c_double, _INT, _P]),
     "spops_masked_adam_csr": (_INT, [_P, _P, _P, _P, _INT, _P, _P, _INT, _I32, _I32, _I32, _I32, ctypes.c_double,
                                      ctypes.c_double, ctypes.c_double, ctypes.c_double, _INT, _P]),
+    "spops_lora_plan_size": (_SZ, [_I32, _I32]),
+    "spops_lora_plan_build": (_INT, [_P, _I32, _I32, _P, _SZ, _P]),
+    "spops_lora_add": (_INT, [_P, _I64, _P, _P, _P, _F32, _INT, _I32, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P,
+                              _P, _P]),
+    "spops_lora_grad_workspace_size": (_SZ, [_I32, _I32]),
+    "spops_lora_grad": (_INT, [_P, _I64, _P, _I64, _P, _P, _P, _F32, _INT, _I32, _I32, _I32, _I32, _I32, _P, _P, _I64,
+                               _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "spops_grad_set_size": (_SZ, [_I32]),
+    "spops_grad_set_build": (_INT, [_P, _P, _P, _P, _I32, _P, _SZ, ctypes.POINTER(_I64), ctypes.POINTER(_I32), _P]),
+    "spops_grad_norm_workspace_size": (_SZ, []),
+    "spops_grad_norm": (_INT, [_P, _I32, _I64, _P, _P, _SZ, _P]),
+    "spops_clip_grads": (_INT, [_P, _I32, _I64, _INT, ctypes.c_double, _P, _P, _SZ, _P]),
 }
 
 _lib = None

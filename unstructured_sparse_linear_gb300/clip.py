@@ -1,0 +1,88 @@
+"""The global 2-norm of many gradients, and clipping by it.
+
+    norm = sqrt(sum of g^2 over every gradient),  g <- g min(1, max_norm / (norm + 1e-6))
+
+The step between an adapter's gradients (sddmm, lora_grad) and masked_adam. Two kernel launches
+whatever the number of tensors, and nothing is read back to the host: the norm stays on the
+device. A training loop whose gradient buffers stay where they are keeps a ``GradSet`` of them.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _DTYPE, _L, _check, _req
+from .lora import _on, _raw_stream
+
+__all__ = ["GradSet", "grad_norm", "clip_grads"]
+
+
+class GradSet:
+    """Gradients that are clipped together (fp32, fp16 and bf16 mixed; contiguous; on one
+    device). Holds the tensors and a device table of their addresses, so it serves every step
+    that writes its gradients into the same buffers; new buffers need a new set. out: tensors
+    of the same sizes and types that receive the clipped gradients (default: in place)."""
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients and {len(self.out)} outputs")
+        n = len(self.grads)
+        self.device = self.grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            _req(g, f"gradient {i}", dtypes=_DTYPE, device=self.device)
+            if o is not g:
+                _req(o, f"output {i}", dtype=g.dtype, device=self.device)
+                if o.numel() != g.numel():
+                    raise ValueError(f"gradient {i} has {g.numel()} elements and its output {o.numel()}")
+        lib = _L()
+        size = lib.spops_grad_set_size(n)
+        chunks, in_place = ctypes.c_int64(0), ctypes.c_int32(0)
+        with torch.cuda.device(self.device):
+            self._table = torch.empty(max(size, 16), dtype=torch.uint8, device=self.device)
+            _check(lib.spops_grad_set_build(
+                (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads]),
+                (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.out]),
+                (ctypes.c_int64 * n)(*[g.numel() for g in self.grads]),
+                (ctypes.c_int32 * n)(*[_DTYPE[g.dtype] for g in self.grads]), n, self._table.data_ptr(), size,
+                ctypes.byref(chunks), ctypes.byref(in_place), _raw_stream(self.device.index)), "grad_set_build")
+        self._ptr, self._n = self._table.data_ptr(), n
+        self._chunks, self._in_place = chunks.value, in_place.value
+        self._ws = int(lib.spops_grad_norm_workspace_size())
+
+    def __len__(self):
+        return self._n
+
+
+def _set(grads) -> GradSet:
+    return grads if isinstance(grads, GradSet) else GradSet(grads)
+
+
+def grad_norm(grads) -> torch.Tensor:
+    """The 2-norm of all gradients together: an fp32 scalar on the device. grads: a GradSet or
+    a list of tensors."""
+    s = _set(grads)
+    dev = s.device
+    with _on(dev):
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        ws = torch.empty(s._ws, dtype=torch.uint8, device=dev)
+        _check(_L().spops_grad_norm(s._ptr, s._n, s._chunks, norm.data_ptr(), ws.data_ptr(), s._ws,
+                                    _raw_stream(dev.index)), "grad_norm")
+    return norm
+
+
+def clip_grads(grads, max_norm: float) -> torch.Tensor:
+    """Scales every gradient by min(1, max_norm / (norm + 1e-6)), in place or into the set's
+    outputs, and returns the norm before clipping (an fp32 scalar on the device). An infinite
+    norm scales by 0 and a NaN one by NaN, as the formula says: check the returned norm where
+    that matters. grads: a GradSet or a list of tensors."""
+    s = _set(grads)
+    dev = s.device
+    with _on(dev):
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        ws = torch.empty(s._ws, dtype=torch.uint8, device=dev)
+        _check(_L().spops_clip_grads(s._ptr, s._n, s._chunks, s._in_place, float(max_norm), norm.data_ptr(),
+                                     ws.data_ptr(), s._ws, _raw_stream(dev.index)), "clip_grads")
+    return norm

@@ -3,12 +3,18 @@
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
+#include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <mutex>
+#include <new>
+#include <vector>
 
 #include "../../include/spops_gb300.h"
+#include "clip.h"
 #include "common.cuh"
 #include "internal.h"
+#include "lora.h"
 #include "panel.h"
 #include "plan.h"
 
@@ -235,6 +241,50 @@ int check_adam(const float* param, const float* exp_avg, const float* exp_avg_sq
     if (overlaps(param, sb, exp_avg, sb) || overlaps(param, sb, exp_avg_sq, sb) || overlaps(exp_avg, sb, exp_avg_sq, sb) ||
         overlaps(param, sb, grad, gb) || overlaps(exp_avg, sb, grad, gb) || overlaps(exp_avg_sq, sb, grad, gb))
         return fail(SPOPS_ERR_INVALID_ARG, "param, exp_avg, exp_avg_sq and grad must not overlap");
+    return SPOPS_OK;
+}
+
+// Whether two row-strided matrices of `rows` rows share an element (leading dimensions and
+// columns in elements of es bytes). With one row stride, columns side by side do not.
+bool rows_overlap(const void* a, int64_t lda, int64_t acols, const void* b, int64_t ldb, int64_t bcols, int64_t rows,
+                  size_t es) {
+    if (!a || !b || rows <= 0 || acols <= 0 || bcols <= 0) return false;
+    if (!overlaps(a, (size_t)((rows - 1) * lda + acols) * es, b, (size_t)((rows - 1) * ldb + bcols) * es)) return false;
+    if (lda != ldb || rows == 1) return true;
+    uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    if (x > y) {
+        std::swap(x, y);
+        std::swap(acols, bcols);
+    }
+    const uintptr_t pitch = (uintptr_t)lda * es, m = (y - x) % pitch;
+    return m < (uintptr_t)acols * es || m + (uintptr_t)bcols * es > pitch;
+}
+
+// A row-strided operand: [rows, cols] with ld >= cols (one row may have any ld).
+int check_rows(const char* name, const void* p, int64_t ld, int64_t cols, int32_t rows, size_t es) {
+    if (!p) return fail(SPOPS_ERR_INVALID_ARG, "%s is NULL", name);
+    if (!aligned(p, es)) return fail(SPOPS_ERR_INVALID_ARG, "%s is not aligned to its dtype", name);
+    if (rows > 1 && ld < cols)
+        return fail(SPOPS_ERR_INVALID_ARG, "%s: row stride %lld is smaller than its %lld columns", name, (long long)ld,
+                    (long long)cols);
+    return SPOPS_OK;
+}
+
+int check_lora(const void* A, const void* B, const float* scale, float scale_all, int dtype, int32_t tokens,
+               int32_t in_features, int32_t out_features, int32_t rank, int32_t n_adapters, const void* plan) {
+    if (dtype < SPOPS_F32 || dtype > SPOPS_BF16) return fail(SPOPS_ERR_INVALID_ARG, "dtype %d is not a spops_dtype", dtype);
+    if (tokens < 0 || in_features < 1 || out_features < 1 || rank < 1 || n_adapters < 1)
+        return fail(SPOPS_ERR_INVALID_ARG, "need tokens >= 0 and in, out, rank, n_adapters >= 1 (got %d, %d, %d, %d, %d)",
+                    tokens, in_features, out_features, rank, n_adapters);
+    if (rank > SPOPS_LORA_MAX_RANK)
+        return fail(SPOPS_ERR_UNSUPPORTED, "rank %d is above the largest supported, %d", rank, SPOPS_LORA_MAX_RANK);
+    if (!A || !B) return fail(SPOPS_ERR_INVALID_ARG, "A or B is NULL");
+    if (!aligned(A, dtype_size(dtype)) || !aligned(B, dtype_size(dtype)))
+        return fail(SPOPS_ERR_INVALID_ARG, "A or B is not aligned to its dtype");
+    if (scale && !aligned(scale, 4)) return fail(SPOPS_ERR_INVALID_ARG, "scale is not 4-byte aligned");
+    if (!std::isfinite(scale_all)) return fail(SPOPS_ERR_INVALID_ARG, "scale_all is not finite");
+    if (tokens > 0 && (!plan || !aligned(plan, 16)))
+        return fail(SPOPS_ERR_INVALID_ARG, "plan is NULL or not 16-byte aligned");
     return SPOPS_OK;
 }
 
@@ -505,6 +555,281 @@ int spops_get_device_error(void* stream, int32_t* code_out) {
     if (e != cudaSuccess) return cuda_status(e, "clear device error word");
     *code_out = v;
     return ok();
+}
+
+/* ---------------------------------------------------------------- low-rank adapters */
+
+size_t spops_lora_plan_size(int32_t tokens, int32_t n_adapters) {
+    return tokens < 0 || n_adapters < 1 ? 0 : lora_plan_bytes(tokens, n_adapters);
+}
+
+int spops_lora_plan_build(const int32_t* adapter_ids, int32_t tokens, int32_t n_adapters, void* plan, size_t plan_size,
+                          void* stream) {
+    if (tokens < 0 || n_adapters < 1)
+        return fail(SPOPS_ERR_INVALID_ARG, "need tokens >= 0 and n_adapters >= 1 (got %d, %d)", tokens, n_adapters);
+    if (adapter_ids && !aligned(adapter_ids, 4)) return fail(SPOPS_ERR_INVALID_ARG, "adapter_ids is not 4-byte aligned");
+    if (tokens == 0) return ok();
+    if (!plan || !aligned(plan, 16) || plan_size < spops_lora_plan_size(tokens, n_adapters))
+        return fail(SPOPS_ERR_WORKSPACE, "the plan needs a 16-byte aligned buffer of %zu bytes (got %zu)",
+                    spops_lora_plan_size(tokens, n_adapters), plan_size);
+    return cuda_status(launch_lora_plan(adapter_ids, lora_plan_view(plan, tokens, n_adapters), (cudaStream_t)stream),
+                       "lora_plan_build launch");
+}
+
+int spops_lora_add(const void* X, int64_t ldx, const void* A, const void* B, const float* scale, float scale_all,
+                   int dtype, int32_t tokens, int32_t in_features, int32_t out_features, int32_t rank,
+                   int32_t n_adapters, const void* base, int64_t ldb, void* Y, int64_t ldy, float* h, const void* plan,
+                   void* stream) {
+    int st = check_lora(A, B, scale, scale_all, dtype, tokens, in_features, out_features, rank, n_adapters, plan);
+    if (st != SPOPS_OK) return st;
+    if (tokens == 0) return ok();
+    const size_t es = dtype_size(dtype);
+    if ((st = check_rows("X", X, ldx, in_features, tokens, es)) != SPOPS_OK) return st;
+    if (!Y && !h) return fail(SPOPS_ERR_INVALID_ARG, "Y and h are both NULL");
+    if (Y && (st = check_rows("Y", Y, ldy, out_features, tokens, es)) != SPOPS_OK) return st;
+    if (base && (st = check_rows("base", base, ldb, out_features, tokens, es)) != SPOPS_OK) return st;
+    if (h && !aligned(h, 4)) return fail(SPOPS_ERR_INVALID_ARG, "h is not 4-byte aligned");
+    const size_t wa = (size_t)n_adapters * rank * in_features * es, wb = (size_t)n_adapters * rank * out_features * es;
+    const size_t yb = Y ? ((size_t)(tokens - 1) * ldy + out_features) * es : 0;
+    const size_t hb = h ? (size_t)tokens * rank * 4 : 0;
+    if (rows_overlap(Y, ldy, out_features, X, ldx, in_features, tokens, es) || overlaps(Y, yb, A, wa) ||
+        overlaps(Y, yb, B, wb) || overlaps(Y, yb, scale, (size_t)n_adapters * 4))
+        return fail(SPOPS_ERR_INVALID_ARG, "Y overlaps X, A, B or scale");
+    if (!(base == Y && (ldb == ldy || tokens == 1)) &&
+        rows_overlap(Y, ldy, out_features, base, ldb, out_features, tokens, es))
+        return fail(SPOPS_ERR_INVALID_ARG, "Y overlaps base without being it");
+    if (overlaps(h, hb, Y, yb) ||
+        overlaps(h, hb, X, ((size_t)(tokens - 1) * ldx + in_features) * es) || overlaps(h, hb, A, wa) ||
+        overlaps(h, hb, B, wb) || overlaps(h, hb, scale, (size_t)n_adapters * 4) ||
+        (base && overlaps(h, hb, base, ((size_t)(tokens - 1) * ldb + out_features) * es)))
+        return fail(SPOPS_ERR_INVALID_ARG, "h overlaps another array");
+    LoraArgs a;
+    a.U = X;
+    a.ldu = ldx;
+    a.K = in_features;
+    a.A = A;
+    a.B = B;
+    a.scale = scale;
+    a.scale_all = scale_all;
+    a.rank = rank;
+    a.base = base;
+    a.ldb = ldb;
+    a.O = Y;
+    a.ldo = ldy;
+    a.N = out_features;
+    a.P = h;
+    return cuda_status(launch_lora(dtype, false, a, lora_plan_view(plan, tokens, n_adapters), (cudaStream_t)stream),
+                       "lora_add launch");
+}
+
+size_t spops_lora_grad_workspace_size(int32_t tokens, int32_t rank) {
+    // dY B (and X A^T, where the caller has no h), fp32
+    return tokens < 1 || rank < 1 ? 16 : 2 * align_up((size_t)tokens * rank * 4, 256);
+}
+
+int spops_lora_grad(const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* A, const void* B,
+                    const float* scale, float scale_all, int dtype, int32_t tokens, int32_t in_features,
+                    int32_t out_features, int32_t rank, int32_t n_adapters, const float* h, const void* dX_base,
+                    int64_t ldb, void* dX, int64_t lddx, void* dA, void* dB, const void* plan, void* workspace,
+                    size_t ws_bytes, void* stream) {
+    int st = check_lora(A, B, scale, scale_all, dtype, tokens, in_features, out_features, rank, n_adapters, plan);
+    if (st != SPOPS_OK) return st;
+    const size_t es = dtype_size(dtype);
+    cudaStream_t s = (cudaStream_t)stream;
+    const size_t wa = (size_t)n_adapters * rank * in_features * es, wb = (size_t)n_adapters * rank * out_features * es;
+    if ((dA && !aligned(dA, es)) || (dB && !aligned(dB, es)))
+        return fail(SPOPS_ERR_INVALID_ARG, "dA or dB is not aligned to its dtype");
+    if (overlaps(dA, wa, dB, wb) || overlaps(dA, wa, A, wa) || overlaps(dA, wa, B, wb) || overlaps(dB, wb, A, wa) ||
+        overlaps(dB, wb, B, wb))
+        return fail(SPOPS_ERR_INVALID_ARG, "dA or dB overlaps another array");
+    if (tokens == 0) {  // no token: the weights' gradients are zero
+        cudaError_t e = cudaSuccess;
+        if (dA) e = cudaMemsetAsync(dA, 0, wa, s);
+        if (dB && e == cudaSuccess) e = cudaMemsetAsync(dB, 0, wb, s);
+        return cuda_status(e, "lora_grad memset");
+    }
+    if (!dX && !dA && !dB) return ok();
+    if ((st = check_rows("dY", dY, lddy, out_features, tokens, es)) != SPOPS_OK) return st;
+    if ((st = check_rows("X", X, ldx, in_features, tokens, es)) != SPOPS_OK) return st;
+    if (dX && (st = check_rows("dX", dX, lddx, in_features, tokens, es)) != SPOPS_OK) return st;
+    if (dX && dX_base && (st = check_rows("dX_base", dX_base, ldb, in_features, tokens, es)) != SPOPS_OK) return st;
+    if (h && !aligned(h, 4)) return fail(SPOPS_ERR_INVALID_ARG, "h is not 4-byte aligned");
+    const size_t xb = ((size_t)(tokens - 1) * ldx + in_features) * es;
+    const size_t dyb = ((size_t)(tokens - 1) * lddy + out_features) * es;
+    const size_t dxb = dX ? ((size_t)(tokens - 1) * lddx + in_features) * es : 0;
+    const size_t hb = (size_t)tokens * rank * 4;
+    auto clash = [&](const void* p, size_t n) {  // an output against every input
+        return overlaps(p, n, h, hb) || overlaps(p, n, scale, (size_t)n_adapters * 4) || overlaps(p, n, A, wa) ||
+               overlaps(p, n, B, wb);
+    };
+    if (rows_overlap(dX, lddx, in_features, X, ldx, in_features, tokens, es) ||
+        rows_overlap(dX, lddx, in_features, dY, lddy, out_features, tokens, es) || clash(dX, dxb) ||
+        overlaps(dX, dxb, dA, wa) || overlaps(dX, dxb, dB, wb))
+        return fail(SPOPS_ERR_INVALID_ARG, "dX overlaps another array");
+    if (dX && !(dX_base == dX && (ldb == lddx || tokens == 1)) &&
+        rows_overlap(dX, lddx, in_features, dX_base, ldb, in_features, tokens, es))
+        return fail(SPOPS_ERR_INVALID_ARG, "dX overlaps dX_base without being it");
+    if (clash(dA, dA ? wa : 0) || clash(dB, dB ? wb : 0) || overlaps(dA, wa, X, xb) || overlaps(dA, wa, dY, dyb) ||
+        overlaps(dB, wb, X, xb) || overlaps(dB, wb, dY, dyb))
+        return fail(SPOPS_ERR_INVALID_ARG, "dA or dB overlaps another array");
+    const size_t need = spops_lora_grad_workspace_size(tokens, rank);
+    if (!workspace || !aligned(workspace, 16) || ws_bytes < need)
+        return fail(SPOPS_ERR_WORKSPACE, "lora_grad needs a 16-byte aligned workspace of %zu bytes (got %zu)", need,
+                    ws_bytes);
+    const LoraPlanView v = lora_plan_view(plan, tokens, n_adapters);
+    float* dp = static_cast<float*>(workspace);
+    float* hw = reinterpret_cast<float*>(static_cast<char*>(workspace) + need / 2);
+    LoraArgs a;
+    a.A = A;
+    a.B = B;
+    a.scale = scale;
+    a.scale_all = scale_all;
+    a.rank = rank;
+    if (dB && !h) {
+        a.U = X;
+        a.ldu = ldx;
+        a.K = in_features;
+        a.N = out_features;
+        a.P = hw;
+        if ((st = cuda_status(launch_lora(dtype, false, a, v, s), "lora_grad h launch")) != SPOPS_OK) return st;
+        h = hw;
+    }
+    if (dX || dA) {
+        a.U = dY;
+        a.ldu = lddy;
+        a.K = out_features;
+        a.N = in_features;
+        a.P = dA ? dp : nullptr;
+        a.base = dX ? dX_base : nullptr;
+        a.ldb = ldb;
+        a.O = dX;
+        a.ldo = lddx;
+        if ((st = cuda_status(launch_lora(dtype, true, a, v, s), "lora_grad dX launch")) != SPOPS_OK) return st;
+    }
+    LoraWgradArgs w[2];
+    int nw = 0;
+    if (dA) {
+        w[nw].U = X;
+        w[nw].ldu = ldx;
+        w[nw].N = in_features;
+        w[nw].P = dp;
+        w[nw].G = dA;
+        ++nw;
+    }
+    if (dB) {
+        w[nw].U = dY;
+        w[nw].ldu = lddy;
+        w[nw].N = out_features;
+        w[nw].P = h;
+        w[nw].G = dB;
+        w[nw].rank_minor = true;
+        ++nw;
+    }
+    if (nw == 0) return ok();
+    return cuda_status(launch_lora_wgrad(dtype, w, nw, rank, scale, scale_all, v, s), "lora_grad dA dB launch");
+}
+
+/* ---------------------------------------------------------------- gradient norm and clipping */
+
+size_t spops_grad_set_size(int32_t tensors) { return tensors < 0 ? 0 : grad_set_bytes(tensors); }
+
+int spops_grad_set_build(const void* const* grads, void* const* outs, const int64_t* counts, const int32_t* dtypes,
+                         int32_t tensors, void* set, size_t set_size, int64_t* chunks_out, int32_t* in_place_out,
+                         void* stream) {
+    if (tensors < 0) return fail(SPOPS_ERR_INVALID_ARG, "negative number of tensors (%d)", tensors);
+    if (!chunks_out || !in_place_out) return fail(SPOPS_ERR_INVALID_ARG, "chunks_out or in_place_out is NULL");
+    if (tensors > 0 && (!grads || !counts || !dtypes))
+        return fail(SPOPS_ERR_INVALID_ARG, "grads, counts or dtypes is NULL");
+    if (!set || !aligned(set, 16) || set_size < spops_grad_set_size(tensors))
+        return fail(SPOPS_ERR_WORKSPACE, "the set needs a 16-byte aligned buffer of %zu bytes (got %zu)",
+                    spops_grad_set_size(tensors), set_size);
+    struct Span {
+        uintptr_t lo, hi;
+        bool write;
+    };
+    std::vector<Span> spans;
+    try {
+        spans.reserve(2 * (size_t)tensors);
+    } catch (const std::bad_alloc&) {
+        return fail(SPOPS_ERR_UNSUPPORTED, "out of host memory for %d tensors", tensors);
+    }
+    int64_t chunks = 0;
+    bool in_place = true;
+    for (int32_t i = 0; i < tensors; ++i) {
+        if (dtypes[i] < SPOPS_F32 || dtypes[i] > SPOPS_BF16)
+            return fail(SPOPS_ERR_INVALID_ARG, "dtype %d of gradient %d is not a spops_dtype", dtypes[i], i);
+        if (counts[i] < 0) return fail(SPOPS_ERR_INVALID_ARG, "negative size of gradient %d", i);
+        if (counts[i] == 0) continue;
+        const void* in = grads[i];
+        const void* out = outs ? outs[i] : in;
+        const size_t es = dtype_size(dtypes[i]);
+        if (!in || !out || !aligned(in, es) || !aligned(out, es))
+            return fail(SPOPS_ERR_INVALID_ARG, "gradient %d or its output is NULL or misaligned", i);
+        const uintptr_t x = reinterpret_cast<uintptr_t>(in), y = reinterpret_cast<uintptr_t>(out);
+        const uintptr_t bytes = (uintptr_t)counts[i] * es;
+        if (x == y) {
+            spans.push_back({x, x + bytes, true});
+        } else {
+            in_place = false;
+            spans.push_back({x, x + bytes, false});
+            spans.push_back({y, y + bytes, true});
+        }
+        chunks += clip_chunks(counts[i]);
+    }
+    std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+    uintptr_t any = 0, written = 0;
+    for (const Span& p : spans) {
+        if (p.lo < written || (p.write && p.lo < any))
+            return fail(SPOPS_ERR_INVALID_ARG, "an output overlaps another gradient or output of the set");
+        any = std::max(any, p.hi);
+        if (p.write) written = std::max(written, p.hi);
+    }
+    int64_t first = 0;
+    for (int32_t i = 0; i < tensors;) {
+        ClipFill f = {};
+        int n = 0;
+        const int32_t at = i;
+        for (; n < kClipFill && i < tensors; ++n, ++i) {
+            f.e[n].in = grads[i];
+            f.e[n].out = outs ? outs[i] : const_cast<void*>(grads[i]);
+            f.e[n].count = counts[i];
+            f.e[n].first = first;
+            f.e[n].dtype = dtypes[i];
+            first += clip_chunks(counts[i]);
+        }
+        const int st = cuda_status(launch_grad_set_fill(static_cast<ClipEntry*>(set), at, f, n, (cudaStream_t)stream),
+                                   "grad_set_build launch");
+        if (st != SPOPS_OK) return st;
+    }
+    *chunks_out = chunks;
+    *in_place_out = in_place ? 1 : 0;
+    return ok();
+}
+
+size_t spops_grad_norm_workspace_size(void) { return grad_norm_ws_bytes(); }
+
+static int grad_norm_call(const void* set, int32_t tensors, int64_t chunks, int in_place, bool scale, double max_norm,
+                          float* norm_out, void* workspace, size_t ws_bytes, void* stream) {
+    if (tensors < 0 || chunks < 0) return fail(SPOPS_ERR_INVALID_ARG, "negative size (tensors=%d)", tensors);
+    if (!set || !aligned(set, 16)) return fail(SPOPS_ERR_INVALID_ARG, "set is NULL or not 16-byte aligned");
+    if (scale && !(max_norm >= 0.0)) return fail(SPOPS_ERR_INVALID_ARG, "max_norm must be >= 0");
+    if (!norm_out || !aligned(norm_out, 4)) return fail(SPOPS_ERR_INVALID_ARG, "norm_out is NULL or misaligned");
+    if (!workspace || !aligned(workspace, 16) || ws_bytes < grad_norm_ws_bytes())
+        return fail(SPOPS_ERR_WORKSPACE, "needs a 16-byte aligned workspace of %zu bytes (got %zu)",
+                    grad_norm_ws_bytes(), ws_bytes);
+    return cuda_status(launch_grad_norm(static_cast<const ClipEntry*>(set), tensors, chunks, in_place != 0, scale,
+                                        max_norm, norm_out, static_cast<double*>(workspace), (cudaStream_t)stream),
+                       scale ? "clip_grads launch" : "grad_norm launch");
+}
+
+int spops_grad_norm(const void* set, int32_t tensors, int64_t chunks, float* norm_out, void* workspace, size_t ws_bytes,
+                    void* stream) {
+    return grad_norm_call(set, tensors, chunks, 1, false, 0.0, norm_out, workspace, ws_bytes, stream);
+}
+
+int spops_clip_grads(const void* set, int32_t tensors, int64_t chunks, int in_place, double max_norm, float* norm_out,
+                     void* workspace, size_t ws_bytes, void* stream) {
+    return grad_norm_call(set, tensors, chunks, in_place, true, max_norm, norm_out, workspace, ws_bytes, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,37 @@
+// The global 2-norm of many gradients and their scaling by it.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace spops {
+
+constexpr int kClipChunk = 8192;  // elements of one tensor that a CTA takes at a time
+constexpr int kClipMaxCtas = 1216;  // partial sums: 8 per SM of a GPU with 152 SMs
+
+// One gradient of a set. out == in: scaled in place. first: its first chunk in the set.
+struct ClipEntry {
+    const void* in;
+    void* out;
+    int64_t count;
+    int64_t first;
+    int32_t dtype;
+    int32_t pad;
+};
+
+inline int64_t clip_chunks(int64_t count) { return (count + kClipChunk - 1) / kClipChunk; }
+inline size_t grad_set_bytes(int64_t tensors) { return sizeof(ClipEntry) * (size_t)(tensors > 0 ? tensors : 1); }
+inline size_t grad_norm_ws_bytes() { return sizeof(double) * kClipMaxCtas; }
+
+constexpr int kClipFill = 64;  // entries per fill launch (kernel parameters)
+struct ClipFill {
+    ClipEntry e[kClipFill];
+};
+
+cudaError_t launch_grad_set_fill(ClipEntry* set, int64_t at, const ClipFill& f, int n, cudaStream_t s);
+// norm_out = the 2-norm of the set's inputs; scale: also out = in * min(1, max_norm / (norm + 1e-6)).
+cudaError_t launch_grad_norm(const ClipEntry* set, int32_t tensors, int64_t chunks, bool in_place, bool scale,
+                             double max_norm, float* norm_out, double* partial, cudaStream_t s);
+
+}  // namespace spops

@@ -1,0 +1,417 @@
+// General kernels of the low-rank adapter operators: any type, size and alignment, fp32
+// arithmetic on the CUDA cores. They also serve small batches (single generated tokens).
+//
+// Products of one adapter's rows, P = U W1 (K -> rank) and O = base + s P W2 (rank -> N), with
+// W1 = A^T, W2 = B^T forward and W1 = B, W2 = A for the input gradient. A thread-block cluster
+// takes a tile of up to 8 rows of one adapter: every CTA multiplies a share of K, the partial
+// P of all ranks are added through distributed shared memory in rank order (every rank forms
+// the same sums, so results are deterministic and P never goes to global memory), and every
+// CTA writes a share of the N columns. P stays in fp32 throughout; O is rounded once.
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+#include "lora.h"
+
+namespace spops {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int R = kLoraRows;
+constexpr int kJW = 4;  // ranks per warp task of the forward product
+
+struct RowsArgs {
+    LoraArgs a;
+    LoraPlanView v;
+    int vec;      // 16-byte loads of U and A/B rows along K (forward)
+    int vec_r;    // 16-byte loads of B rows along rank (forward)
+};
+
+// Elements [i, i + V) of p as floats; vec: one 16-byte load.
+template <typename T>
+__device__ __forceinline__ void load_vec(const T* p, float* f) {
+    Elt<T>::unpack(ld_v4(p), f);
+}
+
+// Forward dot products: part[ks][row][j] = sum over this CTA's and this warp's share of k of
+// U[row, k] A[j, k]. Lanes along k; a warp takes kJW values of j and NR rows.
+template <typename T, int NR, bool kVec>
+__device__ __forceinline__ void dots_forward(const T* const* urow, const T* A, int64_t K, int64_t k0, int64_t k1,
+                                             int j0, int rank, int ks, int ksplit, float (&acc)[kJW][NR]) {
+    constexpr int V = kVec ? Elt<T>::kVec : 1;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int q = 0; q < kJW; ++q)
+#pragma unroll
+        for (int i = 0; i < NR; ++i) acc[q][i] = 0.f;
+    const T* arow[kJW];
+#pragma unroll
+    for (int q = 0; q < kJW; ++q) arow[q] = A + (int64_t)min(j0 + q, rank - 1) * K;
+#pragma unroll 2
+    for (int64_t k = k0 + (int64_t)(ks * 32 + lane) * V; k < k1; k += (int64_t)ksplit * 32 * V) {
+        float w[kJW][V];
+#pragma unroll
+        for (int q = 0; q < kJW; ++q) {
+            if constexpr (kVec) load_vec(arow[q] + k, w[q]);
+            else w[q][0] = Elt<T>::to_f(arow[q][k]);
+        }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            float u[V];
+            if constexpr (kVec) load_vec(urow[i] + k, u);
+            else u[0] = Elt<T>::to_f(urow[i][k]);
+#pragma unroll
+            for (int q = 0; q < kJW; ++q)
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[q][i] = fmaf(w[q][e], u[e], acc[q][i]);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kJW; ++q)
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int d = 16; d; d >>= 1) acc[q][i] += __shfl_xor_sync(0xffffffffu, acc[q][i], d);
+}
+
+template <typename T, int NR, bool kVec>
+__device__ __forceinline__ void phase1_forward(const T* const* urow, const T* A, int64_t K, int64_t k0, int64_t k1,
+                                               int rank, int ksplit, int rp, float* part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int njg = (rank + kJW - 1) / kJW;
+    const int ks = warp / (kWarps / ksplit);  // ksplit is 1, 2, 4 or 8
+    const T* ur[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) ur[i] = urow[i];
+    for (int jg = warp % (kWarps / ksplit); jg < njg; jg += kWarps / ksplit) {
+        float acc[kJW][NR];
+        dots_forward<T, NR, kVec>(ur, A, K, k0, k1, jg * kJW, rank, ks, ksplit, acc);
+        if (lane == 0)
+#pragma unroll
+            for (int q = 0; q < kJW; ++q)
+                if (jg * kJW + q < rank)
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) part[((size_t)ks * R + i) * rp + jg * kJW + q] = acc[q][i];
+    }
+}
+
+// Gradient direction: part[warp][row][j] = sum over k = this CTA's share, dealt to the warps,
+// of U[row, k] B[k, j]. Lanes along j (rank is the contiguous axis of B); with rank <= 16 a
+// warp takes 32 / jl rows of B at once.
+template <typename T>
+__device__ __forceinline__ void phase1_backward(const T* const* urow, int rows, const T* B, int64_t k0, int64_t k1,
+                                                int rank, int rp, float* part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int jl = 32;
+    while (jl > 1 && (jl >> 1) >= rank) jl >>= 1;
+    const int kl = 32 / jl, kq = lane / jl, j0 = lane & (jl - 1);
+    for (int jb = 0; jb < rank; jb += 32) {
+        const int j = jb + j0;
+        float acc[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) acc[i] = 0.f;
+        if (j < rank) {
+#pragma unroll 2
+            for (int64_t k = k0 + warp * kl + kq; k < k1; k += kWarps * kl) {
+                const float w = Elt<T>::to_f(B[k * rank + j]);
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    if (i < rows) acc[i] = fmaf(w, Elt<T>::to_f(urow[i][k]), acc[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float x = acc[i];
+            for (int d = 16; d >= jl; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+            if (lane < jl && j < rank) part[((size_t)warp * R + i) * rp + j] = x;
+        }
+    }
+}
+
+template <typename T, bool kBack>
+__global__ void __launch_bounds__(kThreads) lora_rows_kernel(const RowsArgs g) {
+    extern __shared__ __align__(16) float part[];  // [ksplit][R][rp]
+    __shared__ __align__(16) float hs[kLoraMaxRank][R];
+    __shared__ int s_tok[R];
+    const LoraArgs& a = g.a;
+    const int tid = threadIdx.x;
+    const int C = (int)cluster_size(), crank = (int)cluster_rank();
+    const int cid = blockIdx.x / C, ncl = gridDim.x / C;
+    const int r = a.rank;
+    const int njg = (r + kJW - 1) / kJW;
+    const int ksplit = kBack ? kWarps : (njg >= kWarps ? 1 : kWarps / njg);
+    const int rp = (r + 3) & ~3;
+    const int64_t K = a.K, N = a.N;
+    // shares of K and of the columns in units of 8 elements
+    const int64_t ku = (K + 7) / 8, nu = (N + 7) / 8;
+    const int64_t k0 = ku * crank / C * 8, k1 = min64(K, ku * (crank + 1) / C * 8);
+    const int64_t n0 = nu * crank / C * 8, n1 = min64(N, nu * (crank + 1) / C * 8);
+    const int ntiles = g.v.counts[kLoraCntSmall];
+    const T* U = static_cast<const T*>(a.U);
+    const T* base = static_cast<const T*>(a.base);
+    T* O = static_cast<T*>(a.O);
+
+    // The trip count and every barrier are the same on all CTAs of a cluster.
+    for (int it = cid; it < ntiles; it += ncl) {
+        const LoraTile t = g.v.small[it];
+        __syncthreads();  // the previous tile's tokens and sums have been read
+        if (tid < R) s_tok[tid] = tid < t.rows ? g.v.order[t.pos0 + tid] : -1;
+        __syncthreads();
+        if (t.adapter < 0) {  // no adapter: O = base, P = 0
+            for (int i = 0; i < t.rows; ++i) {
+                const int64_t tok = s_tok[i];
+                if (O && (const T*)O != base)
+                    for (int64_t n = n0 + tid; n < n1; n += kThreads)
+                        O[tok * a.ldo + n] = base ? base[tok * a.ldb + n] : Elt<T>::from_f(0.f);
+                if (a.P && crank == 0)
+                    for (int j = tid; j < r; j += kThreads) a.P[tok * r + j] = 0.f;
+            }
+            continue;
+        }
+        const T* A = static_cast<const T*>(a.A) + (int64_t)t.adapter * r * (kBack ? N : K);
+        const T* B = static_cast<const T*>(a.B) + (int64_t)t.adapter * r * (kBack ? K : N);
+        const T* urow[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) urow[i] = U + (int64_t)s_tok[min(i, t.rows - 1)] * a.ldu;
+        if constexpr (kBack) {
+            phase1_backward<T>(urow, t.rows, B, k0, k1, r, rp, part);
+        } else if (g.vec) {
+            if (t.rows == 1) phase1_forward<T, 1, true>(urow, A, K, k0, k1, r, ksplit, rp, part);
+            else if (t.rows == 2) phase1_forward<T, 2, true>(urow, A, K, k0, k1, r, ksplit, rp, part);
+            else if (t.rows <= 4) phase1_forward<T, 4, true>(urow, A, K, k0, k1, r, ksplit, rp, part);
+            else phase1_forward<T, 8, true>(urow, A, K, k0, k1, r, ksplit, rp, part);
+        } else {
+            phase1_forward<T, 8, false>(urow, A, K, k0, k1, r, ksplit, rp, part);
+        }
+        if (C > 1) cluster_sync();
+        else __syncthreads();
+        const float s = a.scale_all * (a.scale ? a.scale[t.adapter] : 1.f);
+        for (int x = tid; x < t.rows * r; x += kThreads) {
+            const int i = x / r, j = x - i * r;
+            float sum = 0.f;
+            for (int q = 0; q < C; ++q)
+                for (int ks = 0; ks < ksplit; ++ks) {
+                    const float* p = part + ((size_t)ks * R + i) * rp + j;
+                    sum += C > 1 ? __uint_as_float(ld_cluster_u32(cluster_map(smem_u32(p), q))) : *p;
+                }
+            hs[j][i] = sum * s;
+            if (a.P && crank == 0) a.P[(int64_t)s_tok[i] * r + j] = sum;
+        }
+        // every rank has read the partial sums (they are rewritten by the next tile, and no CTA
+        // leaves while another still reads its shared memory)
+        if (C > 1) cluster_sync();
+        else __syncthreads();
+        if (!O) continue;
+        for (int64_t n = n0 + tid; n < n1; n += kThreads) {
+            float acc[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) acc[i] = 0.f;
+            auto step = [&](int j, float w) {
+                const float4 x = *reinterpret_cast<const float4*>(&hs[j][0]);
+                const float4 y = *reinterpret_cast<const float4*>(&hs[j][4]);
+                acc[0] = fmaf(w, x.x, acc[0]);
+                acc[1] = fmaf(w, x.y, acc[1]);
+                acc[2] = fmaf(w, x.z, acc[2]);
+                acc[3] = fmaf(w, x.w, acc[3]);
+                acc[4] = fmaf(w, y.x, acc[4]);
+                acc[5] = fmaf(w, y.y, acc[5]);
+                acc[6] = fmaf(w, y.z, acc[6]);
+                acc[7] = fmaf(w, y.w, acc[7]);
+            };
+            if constexpr (kBack) {
+#pragma unroll 4
+                for (int j = 0; j < r; ++j) step(j, Elt<T>::to_f(A[(int64_t)j * N + n]));
+            } else if (g.vec_r) {
+                constexpr int V = Elt<T>::kVec;
+                for (int j = 0; j < r; j += V) {
+                    float w[V];
+                    load_vec(B + n * r + j, w);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) step(j + e, w[e]);
+                }
+            } else {
+#pragma unroll 4
+                for (int j = 0; j < r; ++j) step(j, Elt<T>::to_f(B[n * r + j]));
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (i < t.rows) {
+                    const int64_t tok = s_tok[i];
+                    const float b = base ? Elt<T>::to_f(base[tok * a.ldb + n]) : 0.f;
+                    O[tok * a.ldo + n] = Elt<T>::from_f(b + acc[i]);
+                }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ weight gradients
+
+constexpr int kWgJ = 16;   // ranks per CTA
+constexpr int kWgT = 32;   // tokens staged at a time
+
+struct WgradRowsArgs {
+    LoraWgradArgs w[2];
+    int blocks[2];  // column blocks of each product
+    int nw, jb;     // products, rank blocks
+    int32_t rank;
+    const float* scale;
+    float scale_all;
+    LoraPlanView v;
+};
+
+// One cluster: 256 columns x 16 ranks of one adapter's gradient; its CTAs split the adapter's
+// tokens and the partial sums are added in rank order through distributed shared memory. A
+// thread owns a column: U is read coalesced, P is broadcast from shared memory.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) lora_wgrad_rows_kernel(const WgradRowsArgs g) {
+    __shared__ __align__(16) float s_p[kWgT][kWgJ];
+    __shared__ int s_tok[kWgT];
+    __shared__ float s_acc[kWgJ][kThreads];
+    const int tid = threadIdx.x;
+    const int C = (int)cluster_size(), crank = (int)cluster_rank();
+    const int per = (g.blocks[0] + (g.nw > 1 ? g.blocks[1] : 0)) * g.jb;
+    const int64_t item = blockIdx.x / C;
+    const int adapter = (int)(item / per);
+    int x = (int)(item - (int64_t)adapter * per);
+    const int j0 = x % g.jb * kWgJ;
+    x /= g.jb;
+    const int which = x >= g.blocks[0];
+    const LoraWgradArgs& w = g.w[which];
+    const int64_t n = (int64_t)(x - (which ? g.blocks[0] : 0)) * kThreads + tid;
+    const int r = g.rank;
+    const int p0 = g.v.off[adapter], cnt = g.v.off[adapter + 1] - p0;
+    const int b0 = p0 + (int)((int64_t)cnt * crank / C), b1 = p0 + (int)((int64_t)cnt * (crank + 1) / C);
+    const T* U = static_cast<const T*>(w.U);
+    float acc[kWgJ];
+#pragma unroll
+    for (int j = 0; j < kWgJ; ++j) acc[j] = 0.f;
+    for (int b = b0; b < b1; b += kWgT) {
+        const int m = min(kWgT, b1 - b);
+        __syncthreads();
+        if (tid < m) s_tok[tid] = g.v.order[b + tid];
+        __syncthreads();
+        for (int i = tid; i < kWgT * kWgJ; i += kThreads) {
+            const int q = i / kWgJ, j = i % kWgJ;
+            s_p[q][j] = q < m && j0 + j < r ? w.P[(int64_t)s_tok[q] * r + j0 + j] : 0.f;
+        }
+        __syncthreads();
+        if (n < w.N) {
+#pragma unroll 4
+            for (int q = 0; q < m; ++q) {
+                const float u = Elt<T>::to_f(U[(int64_t)s_tok[q] * w.ldu + n]);
+#pragma unroll
+                for (int j = 0; j < kWgJ; ++j) acc[j] = fmaf(u, s_p[q][j], acc[j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kWgJ; ++j) s_acc[j][tid] = acc[j];
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+    const float s = g.scale_all * (g.scale ? g.scale[adapter] : 1.f);
+    T* G = static_cast<T*>(w.G) + (int64_t)adapter * r * w.N;
+    if (n < w.N)
+        for (int j = crank; j < kWgJ && j0 + j < r; j += C) {
+            float sum = 0.f;
+            for (int q = 0; q < C; ++q)
+                sum += C > 1 ? __uint_as_float(ld_cluster_u32(cluster_map(smem_u32(&s_acc[j][tid]), q))) : s_acc[j][tid];
+            const T y = Elt<T>::from_f(sum * s);
+            if (w.rank_minor) G[n * r + j0 + j] = y;
+            else G[(int64_t)(j0 + j) * w.N + n] = y;
+        }
+    if (C > 1) cluster_sync();
+}
+
+// Cluster size for `items` clusters: enough CTAs for two per SM, at most 8 (the portable limit).
+int pick_cluster(int64_t items, int64_t most) {
+    const int64_t want = 2 * (int64_t)device_props().sm_count;
+    int c = 1;
+    while (c < 8 && items * c * 2 <= want && c * 2 <= most) c *= 2;
+    return c;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), int64_t clusters, int c, size_t smem, cudaStream_t s,
+                           Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * c));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+    count_launches(1);
+    return e;
+}
+
+template <typename T>
+cudaError_t run_rows(bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) {
+    RowsArgs g;
+    g.a = a;
+    g.v = v;
+    constexpr int V = Elt<T>::kVec;
+    g.vec = a.K % V == 0 && a.ldu % V == 0 && ((uintptr_t)a.U | (uintptr_t)a.A) % 16 == 0;
+    g.vec_r = a.rank % V == 0 && (uintptr_t)a.B % 16 == 0;
+    const int64_t cap = lora_tiles_cap(v.tokens, v.n, kLoraRows);
+    const int c = pick_cluster(cap, max64(1, max64(a.K, a.N) / 64));
+    const int64_t clusters = min64(cap, (int64_t)device_props().sm_count * 8);
+    const int rp = (a.rank + 3) & ~3, njg = (a.rank + kJW - 1) / kJW;
+    const int ksplit = back ? kWarps : (njg >= kWarps ? 1 : kWarps / njg);
+    const size_t smem = (size_t)ksplit * R * rp * sizeof(float);  // at most 32 KB
+    return back ? launch_cluster(lora_rows_kernel<T, true>, clusters, c, smem, s, g)
+                : launch_cluster(lora_rows_kernel<T, false>, clusters, c, smem, s, g);
+}
+
+template <typename T>
+cudaError_t run_wgrad_rows(const LoraWgradArgs* w, int nw, int32_t rank, const float* scale, float scale_all,
+                           const LoraPlanView& v, cudaStream_t s) {
+    WgradRowsArgs g;
+    g.nw = nw;
+    g.jb = (rank + kWgJ - 1) / kWgJ;
+    for (int i = 0; i < nw; ++i) {
+        g.w[i] = w[i];
+        g.blocks[i] = (w[i].N + kThreads - 1) / kThreads;
+    }
+    if (nw == 1) g.blocks[1] = 0;
+    g.rank = rank;
+    g.scale = scale;
+    g.scale_all = scale_all;
+    g.v = v;
+    const int64_t items = (int64_t)v.n * (g.blocks[0] + g.blocks[1]) * g.jb;
+    const int c = pick_cluster(items, max64(1, v.tokens / kWgT));
+    if (items * c > 0x7fffffffll) return cudaErrorInvalidValue;
+    return launch_cluster(lora_wgrad_rows_kernel<T>, items, c, 0, s, g);
+}
+
+}  // namespace
+
+cudaError_t launch_lora_rows(int dt, bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) {
+    if (dt == kF32) return run_rows<float>(back, a, v, s);
+    if (dt == kF16) return run_rows<__half>(back, a, v, s);
+    return run_rows<__nv_bfloat16>(back, a, v, s);
+}
+
+cudaError_t launch_lora_wgrad_rows(int dt, const LoraWgradArgs* w, int nw, int32_t rank, const float* scale,
+                                   float scale_all, const LoraPlanView& v, cudaStream_t s) {
+    if (dt == kF32) return run_wgrad_rows<float>(w, nw, rank, scale, scale_all, v, s);
+    if (dt == kF16) return run_wgrad_rows<__half>(w, nw, rank, scale, scale_all, v, s);
+    return run_wgrad_rows<__nv_bfloat16>(w, nw, rank, scale, scale_all, v, s);
+}
+
+cudaError_t launch_lora(int dt, bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) {
+    return launch_lora_rows(dt, back, a, v, s);
+}
+
+cudaError_t launch_lora_wgrad(int dt, const LoraWgradArgs* w, int nw, int32_t rank, const float* scale,
+                              float scale_all, const LoraPlanView& v, cudaStream_t s) {
+    return launch_lora_wgrad_rows(dt, w, nw, rank, scale, scale_all, v, s);
+}
+
+}  // namespace spops

@@ -1,0 +1,187 @@
+"""Low-rank adapters: the product beside a shared projection, for many requests at once, and
+its gradients.
+
+RoSA adds a low-rank and a sparse update to one frozen projection (spops README, "Sparse
+Operations (spops)"). The sparse half is csr_add / spmm / sddmm; this is the low-rank half:
+
+    lora_add    Y = base + s_i (X A_i^T) B_i^T, adapter i chosen per token
+    lora_grad   dX = dX_base + s_i (dY B_i) A_i,  dA_i = s_i (dY B_i)^T X,  dB_i = s_i dY^T (X A_i^T)
+
+A is [adapters, rank, in], B [adapters, out, rank], X token-major [tokens, in]. The batch's
+plan (``lora_plan``: its tokens sorted by adapter) is built once and serves every projection of
+every layer. Activations may be column slices of a wider matrix (a fused projection): their
+rows need unit stride inside and one row stride; everything else is contiguous.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import _DTYPE, _L, _check, _req
+
+__all__ = ["LoraPlan", "lora_plan", "lora_add", "lora_grad"]
+
+
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _rows(t, name, rows, cols, dtype, device):
+    """Checks a row-strided [rows, cols] operand; returns (address, row stride)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
+        raise ValueError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
+    ld, step = t.stride()
+    if (step != 1 and cols > 1) or (ld < cols and rows > 1):
+        raise ValueError(f"{name} must have contiguous rows at least {cols} elements apart, got strides {(ld, step)}")
+    return t.data_ptr(), ld
+
+
+class LoraPlan:
+    """Which tokens of a batch use which adapter, sorted; built by ``lora_plan``."""
+
+    def __init__(self, buf: torch.Tensor, tokens: int, n_adapters: int):
+        self.buf, self.tokens, self.n_adapters = buf, tokens, n_adapters
+        self.device = buf.device
+        self._ptr = buf.data_ptr()
+
+    def order(self) -> torch.Tensor:
+        """The tokens sorted by adapter (stable; those without an adapter last), int32."""
+        return self.buf[64:64 + 4 * self.tokens].view(torch.int32)
+
+
+def lora_plan(adapter_ids: torch.Tensor | None, n_adapters: int, tokens: int | None = None,
+              device=None) -> LoraPlan:
+    """The plan of a batch (asynchronous on the current stream). adapter_ids: int32 [tokens], the
+    adapter of each token in any order; an id outside 0 .. n_adapters - 1 (-1) means none.
+    adapter_ids=None with tokens (and device): every token uses adapter 0, as in training."""
+    if adapter_ids is None:
+        if tokens is None:
+            raise ValueError("lora_plan needs adapter_ids or tokens")
+        dev = torch.device(device if device is not None else "cuda")
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        ids = 0
+    else:
+        _req(adapter_ids, "adapter_ids", torch.int32)
+        if adapter_ids.dim() != 1 or (tokens is not None and tokens != adapter_ids.numel()):
+            raise ValueError(f"adapter_ids must be a vector with one id per token, got {tuple(adapter_ids.shape)}")
+        tokens, dev, ids = adapter_ids.numel(), adapter_ids.device, adapter_ids.data_ptr()
+    tokens, n_adapters = int(tokens), int(n_adapters)
+    if tokens < 0 or n_adapters < 1:
+        raise ValueError(f"need tokens >= 0 and n_adapters >= 1, got {tokens}, {n_adapters}")
+    lib = _L()
+    size = lib.spops_lora_plan_size(tokens, n_adapters)
+    with torch.cuda.device(dev):
+        buf = torch.empty(size, dtype=torch.uint8, device=dev)
+        _check(lib.spops_lora_plan_build(ids, tokens, n_adapters, buf.data_ptr(), size, _raw_stream(dev.index)),
+               "lora_plan_build")
+    return LoraPlan(buf, tokens, n_adapters)
+
+
+def _weights(X, A, B, plan, scale):
+    """Checks shared by both calls; returns (device, tokens, in, out, rank, n, scale address, factor)."""
+    if not isinstance(plan, LoraPlan):
+        raise TypeError("plan must be a LoraPlan")
+    if not isinstance(X, torch.Tensor):
+        raise TypeError("X must be a torch.Tensor")
+    dev, dt = X.device, X.dtype
+    if not X.is_cuda:
+        raise ValueError("X must be a CUDA tensor")
+    if dt not in _DTYPE:
+        raise ValueError(f"X dtype {dt} not in {list(_DTYPE)}")
+    _req(A, "A", dt, device=dev)
+    _req(B, "B", dt, device=dev)
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A must be [adapters, rank, in] and B [adapters, out, rank]")
+    n, rank, k = A.shape
+    if B.size(0) != n or B.size(2) != rank:
+        raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)} differ in adapters or rank")
+    if plan.n_adapters != n or plan.device != dev:
+        raise ValueError(f"plan was built for {plan.n_adapters} adapters on {plan.device}, not {n} on {dev}")
+    s_ptr, s_all = 0, 1.0
+    if isinstance(scale, torch.Tensor):
+        _req(scale, "scale", torch.float32, device=dev)
+        if scale.numel() != n:
+            raise ValueError(f"scale must have one factor per adapter ({n}), got {scale.numel()}")
+        s_ptr = scale.data_ptr()
+    elif scale is not None:
+        s_all = float(scale)
+    return dev, plan.tokens, k, B.size(1), rank, n, s_ptr, s_all
+
+
+def _on(dev):
+    """Makes dev current (a context that does nothing where it already is)."""
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+class _Nothing:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *a):
+        return False
+
+
+_HERE = _Nothing()
+
+
+def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h: bool = False):
+    """Y = base + s_i (X A_i^T) B_i^T with the adapter i of each token (tokens without one: base).
+    base: the shared projection's output (None: zeros); out=base adds in place. scale: a float,
+    or an fp32 tensor with one factor per adapter. return_h: also return X A_i^T (fp32
+    [tokens, rank]), which lora_grad takes."""
+    dev, T, k, n_out, rank, n, s_ptr, s_all = _weights(X, A, B, plan, scale)
+    dt = X.dtype
+    x, ldx = _rows(X, "X", T, k, dt, dev)
+    b, ldb = _rows(base, "base", T, n_out, dt, dev) if base is not None else (0, n_out)
+    lib = _L()
+    with _on(dev):
+        if out is None:
+            out = torch.empty((T, n_out), dtype=dt, device=dev)
+        y, ldy = _rows(out, "out", T, n_out, dt, dev)
+        h = torch.empty((T, rank), dtype=torch.float32, device=dev) if return_h else None
+        _check(lib.spops_lora_add(x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out, rank, n,
+                                  b, ldb, y, ldy, h.data_ptr() if return_h else 0, plan._ptr, _raw_stream(dev.index)),
+               "lora_add")
+    return (out, h) if return_h else out
+
+
+def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_out=None, need=(True, True, True)):
+    """(dX, dA, dB) of lora_add for the output gradient dY. dX = dX_base + s_i (dY B_i) A_i, so the
+    shared projection's own input gradient goes in as dX_base (dX_out=dX_base: in place). h: the
+    one lora_add returned for this X (None: formed here). need: which of the three to compute;
+    the others come back as None."""
+    dev, T, k, n_out, rank, n, s_ptr, s_all = _weights(X, A, B, plan, scale)
+    dt = X.dtype
+    x, ldx = _rows(X, "X", T, k, dt, dev)
+    dy, lddy = _rows(dY, "dY", T, n_out, dt, dev)
+    hp = 0
+    if h is not None:
+        _req(h, "h", torch.float32, device=dev)
+        if tuple(h.shape) != (T, rank):
+            raise ValueError(f"h must be {T} x {rank}, got {tuple(h.shape)}")
+        hp = h.data_ptr()
+    b, ldb = _rows(dX_base, "dX_base", T, k, dt, dev) if dX_base is not None else (0, k)
+    lib = _L()
+    with _on(dev):
+        dX = dA = dB = None
+        dx, lddx = 0, k
+        if need[0]:
+            dX = dX_out if dX_out is not None else torch.empty((T, k), dtype=dt, device=dev)
+            dx, lddx = _rows(dX, "dX_out", T, k, dt, dev)
+        if need[1]:
+            dA = torch.empty_like(A)
+        if need[2]:
+            dB = torch.empty_like(B)
+        size = lib.spops_lora_grad_workspace_size(T, rank)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        _check(lib.spops_lora_grad(dy, lddy, x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out,
+                                   rank, n, hp, b, ldb, dx, lddx, dA.data_ptr() if need[1] else 0,
+                                   dB.data_ptr() if need[2] else 0, plan._ptr, ws.data_ptr(), size,
+                                   _raw_stream(dev.index)), "lora_grad")
+    return dX, dA, dB
