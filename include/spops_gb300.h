@@ -83,6 +83,7 @@ typedef enum spops_sddmm_backend {
 #define SPOPS_DEV_COL_ORDER 4    /* columns not strictly increasing inside a row */
 #define SPOPS_DEV_ROW_IDX 5      /* row_idx is not a permutation of 0..m-1 */
 #define SPOPS_DEV_TMEM 6         /* tensor-memory allocation failed */
+#define SPOPS_DEV_SMEM_ALIGN 7   /* shared memory of a tensor-core kernel is not 1 KB aligned */
 
 /* Row-bin thresholds the operators use: rows with at least this many entries are "long". */
 #define SPOPS_SPMM_LONG_ROW 256

@@ -406,6 +406,7 @@ cudaError_t launch_lora_wgrad_rows(int dt, const LoraWgradArgs* w, int nw, int32
 }
 
 cudaError_t launch_lora(int dt, bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) {
+    if (v.tokens > 64 && lora_tiles_ok(dt, a, v)) return launch_lora_tiles(dt, back, a, v, s);
     return launch_lora_rows(dt, back, a, v, s);
 }
 

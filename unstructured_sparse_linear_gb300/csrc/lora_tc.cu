@@ -1,0 +1,696 @@
+// Low-rank adapter operators on the tcgen05 tensor cores (fp16 / bf16).
+//
+// lora_tile_kernel   P = U W1 and O = base + s P W2 in one launch, for tiles of up to 128 rows
+//                    that share an adapter (the forward product and the input gradient);
+// lora_wgrad_kernel  G = s P^T U over an adapter's tokens (the weights' gradients).
+//
+// Precision. P stays in 32 bits where it is kept (TMEM, shared memory, global). As an operand
+// of the second product it is the sum of two 16-bit parts, hi = round(P) and lo = round(P - hi),
+// multiplied one after the other into the same fp32 accumulators: 16 bits or more of P take part
+// (a single bf16 part would add an error as large as the output's own rounding). For fp16, whose
+// range P = U W1 leaves easily (small gradients, large activations), a row (or a CTA's rows of
+// a weight gradient) is first scaled by a power of two, which is taken back in fp32.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "internal.h"
+#include "lora.h"
+#include "tc.cuh"
+
+namespace spops {
+namespace {
+
+constexpr int kKC = 64;                       // 16-bit elements per 128-byte swizzled row
+constexpr uint32_t kUBytes = kLoraTile * 128;  // a 128 x 64 tile of U, base or O
+
+// ------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// Four rows of a 2-D tensor (a map whose box is one row of 64 elements) into 4 x 128 bytes.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&y)[4], uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
+// Arrive on the barrier at local address `bar` in CTA `rank` of the cluster; what this thread
+// (and, through a barrier before, its CTA) wrote is visible to whoever then waits there.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar, int rank) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_map(bar, rank)) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity), "n"(kMbarPollNs)
+        : "memory");
+    return done != 0;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) { return __uint_as_float(ld_cluster_u32(addr)); }
+
+// Waits of one CTA. After one has run out of time (2 s) every later one of the CTA gives up at
+// once, so that a kernel whose copy never arrives ends; the roles then skip their work but keep
+// their loops, which hold barriers.
+struct Waits {
+    volatile int* failed;
+    int* err;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        if (*failed) return false;
+        if (mbar_wait(bar, parity, err)) return true;
+        *failed = 1;
+        return false;
+    }
+    __device__ __forceinline__ bool cluster(uint32_t bar, uint32_t parity) const {
+        if (*failed) return false;
+        const uint64_t t0 = global_timer_ns();
+        for (uint32_t it = 1;; ++it) {
+            if (mbar_try_cluster(bar, parity)) return true;
+            if ((it & 255u) == 0 && global_timer_ns() - t0 > kMbarTimeoutNs) {
+                record_error(err, kDevErrMbarTimeout);
+                *failed = 1;
+                return false;
+            }
+        }
+    }
+};
+constexpr uint64_t kDrainNs = 100000000ull;  // after a failed wait: for copies still in flight
+
+// 2^x for the exponent field of a normal fp32 number.
+__device__ __forceinline__ float exp2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
+
+// The power of two that brings m (the largest magnitude) to [2^10, 2^11), and its inverse; 1
+// for zero, infinite and NaN m. Both factors are normal numbers.
+__device__ __forceinline__ void pow2_scale(float m, float& up, float& down) {
+    up = down = 1.f;
+    if (m > 0.f && m <= 3.402823466e38f) {
+        const int e = max(-110, (int)((__float_as_uint(m) >> 23) & 255u) - 127);
+        up = exp2i(10 - e);
+        down = exp2i(e - 10);
+    }
+}
+
+// Eight values as eight hi and eight lo parts.
+template <typename T>
+__device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
+    hi = Elt<T>::pack(x);
+    float h[8], l[8];
+    Elt<T>::unpack(hi, h);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l[i] = fabsf(h[i]) <= 3.402823466e38f ? x[i] - h[i] : 0.f;  // no inf - inf
+    lo = Elt<T>::pack(l);
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// 16 (or 32) consecutive fp32 TMEM columns of the thread's lane.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// A 64-row x RP tile of rows [row0, row0 + 64) of the row-major rows x rank matrix W, by one
+// warp with plain loads (ranks whose rows no 16-byte copy can address): zeros beyond the matrix,
+// 64-column blocks of 8 KB in the 128-byte-swizzled layout.
+template <typename T, int RP>
+__device__ __forceinline__ void load_b_tile(uint32_t dst, const T* W, int64_t row0, int64_t rows, int rank) {
+    const int lane = threadIdx.x & 31;
+    constexpr int kChunks = RP / 8;
+#pragma unroll 2
+    for (int i = lane; i < 64 * kChunks; i += 32) {
+        const int row = i / kChunks, c = i % kChunks;
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (row0 + row < rows) {
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(W + (row0 + row) * rank);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c * 8 + e < rank) w[e >> 1] |= (uint32_t)src[c * 8 + e] << (16 * (e & 1));
+        }
+        st_shared_v4(dst + (c >> 3) * 8192 + tc::sw128_off(row, c & 7), make_uint4(w[0], w[1], w[2], w[3]));
+    }
+}
+
+// ------------------------------------------------------------------ tile kernel
+
+// Warps: 0 loads (TMA), 1 multiplies (one thread), 2 to 5 finish (one row per thread), 6 loads
+// the rank-contiguous weight tiles where TMA cannot.
+constexpr int kTileThreads = 224;
+constexpr int kEpi = 128;
+constexpr uint32_t kTileBars = 1024;  // barriers and flags, behind the stages and P
+
+template <int RP>
+struct TileCfg {
+    static constexpr int kBlocks = (RP + 63) / 64;
+    static constexpr uint32_t kW = RP > 64 ? 16384 : 8192;       // weight tile of a stage
+    static constexpr uint32_t kStage = kUBytes + kW;
+    // The hi and lo parts of P, 2 RP columns in swizzled blocks of 128 rows x 64 columns, or its
+    // fp32 partial sums (128 RP of them).
+    static constexpr uint32_t kH = (2 * RP + 63) / 64 * kUBytes;
+    static_assert(kH >= RP * 512u, "the partial sums fit");
+    static constexpr int kPerSm = RP > 64 ? 1 : 2;
+    // Dynamic shared memory per CTA: all of the SM's 228 KB but 1 KB that the system keeps per CTA.
+    static constexpr uint32_t kBudget = (228 * 1024) / kPerSm - 1024;
+    static constexpr int kStages = (int)((kBudget - kTileBars - kH) / kStage);
+    static constexpr uint32_t kSmem = kStages * kStage + kH + kTileBars;
+    static constexpr uint32_t kTmem = 256;  // P: columns 0 .. RP - 1; O: two buffers of 64 at 128 and 192
+};
+
+struct TileArgs {
+    LoraPlanView v;
+    const void* B;       // for the warp that loads it by hand
+    const float* scale;
+    const void* base;
+    void* O;
+    float* P;
+    int64_t ldb, ldo;
+    int32_t K, N, rank;
+    float scale_all;
+    int hand;  // B tiles are loaded by warp 6
+    int* err;
+};
+
+// A cluster of C CTAs takes a tile: rank c multiplies a share of the K chunks into its TMEM, the
+// fp32 partial P are exchanged through distributed shared memory (every rank adds all of them in
+// rank order), and rank c forms a share of the 64-column chunks of O. One ring of stages carries
+// both phases, so the loads of base run ahead while P is being summed: a stage holds a 128 x 64
+// tile of U with a tile of W1, then a 128 x 64 tile of base, in which O is formed in place, with a
+// tile of W2. Rows come by one TMA box when the tile is full and its tokens consecutive, else four
+// rows at a time (gather4).
+template <typename T, bool kBack, int RP>
+__global__ void __launch_bounds__(kTileThreads, TileCfg<RP>::kPerSm)
+lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, const __grid_constant__ CUtensorMap map_u1,
+                 const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                 const __grid_constant__ CUtensorMap map_base, const __grid_constant__ CUtensorMap map_base1,
+                 const __grid_constant__ CUtensorMap map_o) {
+    using Cfg = TileCfg<RP>;
+    constexpr int S = Cfg::kStages;
+    constexpr bool kF16 = std::is_same<T, __half>::value;
+    constexpr uint32_t kFmt = kF16 ? 0u : 1u;
+    constexpr uint32_t kIdesc1 = tc::instr_desc_f16(kFmt, 0, kBack ? 1 : 0, 128, RP);
+    constexpr uint32_t kIdesc2 = tc::instr_desc_f16(kFmt, 0, kBack ? 1 : 0, 128, 64);
+    constexpr uint32_t kABytes = RP * 128, kBBytes = Cfg::kBlocks * 8192;
+    // No static shared memory, so the dynamic part starts on the 1 KB boundary that the swizzled
+    // tiles need (checked).
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    struct Shared {
+        uint64_t full[S], empty[S], d1, h, d2_full[2], d2_empty[2], pub, read, drain;
+        uint32_t tmem;
+        volatile int failed;
+    };
+    static_assert(sizeof(Shared) <= kTileBars, "barriers");
+    Shared& sh = *reinterpret_cast<Shared*>(smem_raw + S * Cfg::kStage + Cfg::kH);
+    const uint32_t sbase = smem_u32(smem_raw);
+    const uint32_t hbase = sbase + S * Cfg::kStage;
+    if (sbase & 1023u) {  // the same on every CTA
+        record_error(g.err, kDevErrSmemAlign);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int C = (int)cluster_size(), crank = (int)cluster_rank();
+    const int cid = blockIdx.x / C, ncl = gridDim.x / C;
+
+    if (warp == 1) tc::tmem_alloc(smem_u32(&sh.tmem), Cfg::kTmem);
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), g.hand ? 2 : 1);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        mbar_init(smem_u32(&sh.d1), 1);
+        mbar_init(smem_u32(&sh.h), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.d2_full[i]), 1);
+            mbar_init(smem_u32(&sh.d2_empty[i]), 4);
+        }
+        mbar_init(smem_u32(&sh.pub), C);
+        mbar_init(smem_u32(&sh.read), C);
+        mbar_init(smem_u32(&sh.drain), 1);
+        fence_mbar_init();
+        sh.failed = 0;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (C > 1) cluster_sync();  // the other ranks' barriers are initialised
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    const Waits wait{&sh.failed, g.err};
+    const int ntiles = g.v.counts[kLoraCntTiles];
+    const int nkc = (g.K + kKC - 1) / kKC, nnc = g.O ? (g.N + kKC - 1) / kKC : 0;
+    const int ka = (int)((int64_t)nkc * crank / C), kb = (int)((int64_t)nkc * (crank + 1) / C);
+    const int na = (int)((int64_t)nnc * crank / C), nb = (int)((int64_t)nnc * (crank + 1) / C);
+    const int nk = kb - ka, nn = nb - na;
+
+    if (warp == 0) {
+        // ---------------- loads
+        uint32_t q = 0;
+        bool ok = true;
+        for (int it = cid; it < ntiles && ok; it += ncl) {
+            const LoraTile t = g.v.tiles[it];
+            const bool box = t.rows == kLoraTile && t.tok0 >= 0;
+            int y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = box ? 0 : g.v.order[t.pos0 + min(4 * lane + i, t.rows - 1)];
+            const int groups = (t.rows + 3) / 4;
+            const uint32_t ubytes = box ? kUBytes : (uint32_t)groups * 512u;
+            for (int j = 0; j < nk + nn; ++j, ++q) {
+                const bool p1 = j < nk;
+                const uint32_t s = q % S, st = sbase + s * Cfg::kStage, fb = smem_u32(&sh.full[s]);
+                if (q >= S) ok = __all_sync(0xffffffffu, wait(smem_u32(&sh.empty[s]), (q / S - 1) & 1u));
+                if (!ok) break;
+                const bool rows = p1 || g.base;
+                const bool b_tile = p1 ? kBack : !kBack;  // this phase's weights: a tile of B, else of A
+                if (lane == 0) {
+                    const uint32_t w = b_tile ? (g.hand ? 0u : kBBytes) : kABytes;
+                    mbar_arrive_expect_tx(fb, (rows ? ubytes : 0u) + w);
+                }
+                __syncwarp();
+                const int x = (p1 ? ka + j : na + j - nk) * kKC;
+                if (rows) {
+                    if (box) {
+                        if (lane == 0) tma_load_2d(st, p1 ? &map_u : &map_base, x, t.tok0, fb);
+                    } else if (lane < groups) {
+                        tma_gather4(st + lane * 512, p1 ? &map_u1 : &map_base1, x, y, fb);
+                    }
+                }
+                if (lane == 0) {
+                    if (!b_tile) {
+                        tma_load_3d(st + kUBytes, &map_a, x, 0, t.adapter, fb);
+                    } else if (!g.hand) {
+#pragma unroll
+                        for (int b = 0; b < Cfg::kBlocks; ++b)
+                            tma_load_3d(st + kUBytes + b * 8192, &map_b, b * 64, x, t.adapter, fb);
+                    }
+                }
+            }
+        }
+        if (sh.failed) {  // let the copies in flight land before the shared memory is given up
+            for (uint32_t i = q > S ? q - S : 0; i < q; ++i)
+                mbar_wait_for(smem_u32(&sh.full[i % S]), (i / S) & 1u, nullptr, kDrainNs);
+        }
+    } else if (warp == 1) {
+        // ---------------- multiplications
+        if (lane == 0) {
+            uint32_t q = 0, n2 = 0, tt = 0;
+            bool ok = true;
+            for (int it = cid; it < ntiles && ok; it += ncl, ++tt) {
+                for (int j = 0; j < nk && ok; ++j, ++q) {
+                    const uint32_t s = q % S, st = sbase + s * Cfg::kStage;
+                    ok = wait(smem_u32(&sh.full[s]), (q / S) & 1u);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint64_t ad = tc::smem_desc_sw128(st + kk * 32, 16, 1024);
+                        const uint64_t bd = kBack ? tc::smem_desc_sw128(st + kUBytes + kk * 2048, 8192, 1024)
+                                                  : tc::smem_desc_sw128(st + kUBytes + kk * 32, 16, 1024);
+                        tc::mma_f16(tmem, ad, bd, kIdesc1, (j > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    tc::mma_commit(smem_u32(&sh.empty[s]));
+                }
+                if (!ok) break;
+                tc::mma_commit(smem_u32(&sh.d1));
+                ok = wait(smem_u32(&sh.h), tt & 1u);  // P's parts are written, and its columns read
+                if (!ok) break;
+                tc::fence_after_sync();
+                for (int j = 0; j < nn; ++j, ++q, ++n2) {
+                    const uint32_t s = q % S, st = sbase + s * Cfg::kStage, b = n2 & 1u;
+                    ok = wait(smem_u32(&sh.full[s]), (q / S) & 1u);
+                    if (ok && n2 >= 2) ok = wait(smem_u32(&sh.d2_empty[b]), (n2 / 2 - 1) & 1u);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    constexpr int kSteps = RP / 16;
+#pragma unroll
+                    for (int i = 0; i < 2 * kSteps; ++i) {
+                        const int w = i % kSteps;
+                        const uint64_t ad = tc::smem_desc_sw128(hbase + (i / 4) * 16384 + (i % 4) * 32, 16, 1024);
+                        const uint64_t bd = kBack
+                                                ? tc::smem_desc_sw128(st + kUBytes + w * 2048, 8192, 1024)
+                                                : tc::smem_desc_sw128(st + kUBytes + (w / 4) * 8192 + (w % 4) * 32, 16, 1024);
+                        tc::mma_f16(tmem + 128 + b * 64, ad, bd, kIdesc2, i > 0 ? 1u : 0u);
+                    }
+                    tc::mma_commit(smem_u32(&sh.d2_full[b]));
+                }
+            }
+            if (sh.failed) {
+                tc::mma_commit(smem_u32(&sh.drain));
+                mbar_wait_for(smem_u32(&sh.drain), 0, nullptr, kDrainNs);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 6) {
+        // ---------------- B tiles by hand
+        if (g.hand) {
+            uint32_t q = 0;
+            bool ok = true;
+            const int64_t brows = kBack ? g.K : g.N;
+            for (int it = cid; it < ntiles && ok; it += ncl) {
+                const int adapter = g.v.tiles[it].adapter;
+                const T* W = static_cast<const T*>(g.B) + (int64_t)adapter * brows * g.rank;
+                for (int j = 0; j < nk + nn; ++j, ++q) {
+                    const bool p1 = j < nk;
+                    const uint32_t s = q % S, st = sbase + s * Cfg::kStage;
+                    if (q >= S) ok = __all_sync(0xffffffffu, wait(smem_u32(&sh.empty[s]), (q / S - 1) & 1u));
+                    if (!ok) break;
+                    if (p1 == kBack) {
+                        load_b_tile<T, RP>(st + kUBytes, W, (int64_t)(p1 ? ka + j : na + j - nk) * kKC, brows, g.rank);
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
+                }
+            }
+        }
+    } else {
+        // ---------------- P, then O: thread = row
+        const int quarter = warp & 3, row = quarter * 32 + lane, et = tid - 64;
+        const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+        uint32_t q = 0, n2 = 0, tt = 0;
+        for (int it = cid; it < ntiles; it += ncl, ++tt) {
+            const LoraTile t = g.v.tiles[it];
+            const bool full = t.rows == kLoraTile && t.tok0 >= 0, mine = row < t.rows;
+            const int64_t tok = mine ? g.v.order[t.pos0 + row] : 0;
+            const float s = g.scale_all * (g.scale ? g.scale[t.adapter] : 1.f);
+            q += nk;
+            float p[RP];
+            wait(smem_u32(&sh.d1), tt & 1u);
+            tc::fence_after_sync();
+            if (nk > 0) {
+#pragma unroll
+                for (int c = 0; c < RP / 16; ++c) tmem_ld16(lane_addr + c * 16, p + c * 16);
+            } else {
+#pragma unroll
+                for (int j = 0; j < RP; ++j) p[j] = 0.f;
+            }
+            tc::fence_before_sync();
+            if (C > 1) {
+                // publish, add every rank's partial sums in rank order, and tell every rank that its
+                // sums have been read (their place then takes the 16-bit parts)
+                const uint32_t mypart = hbase + row * 4;
+#pragma unroll
+                for (int j = 0; j < RP; ++j) st_shared_f32(mypart + j * 512, p[j]);
+                named_barrier(1, kEpi);
+                if (et < C) mbar_arrive_remote(smem_u32(&sh.pub), et);
+                wait.cluster(smem_u32(&sh.pub), tt & 1u);
+#pragma unroll
+                for (int j = 0; j < RP; ++j) p[j] = 0.f;
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t from = cluster_map(mypart, c);
+#pragma unroll
+                    for (int j = 0; j < RP; ++j) p[j] += ld_cluster_f32(from + j * 512);
+                }
+                named_barrier(1, kEpi);
+                if (et < C) mbar_arrive_remote(smem_u32(&sh.read), et);
+                wait.cluster(smem_u32(&sh.read), tt & 1u);
+            }
+            if (g.P && crank == 0 && mine) {
+                float* dst = g.P + tok * g.rank;
+#pragma unroll
+                for (int j = 0; j < RP; ++j)
+                    if (j < g.rank) dst[j] = p[j];
+            }
+            float up = 1.f, down = 1.f, m = 0.f;
+#pragma unroll
+            for (int j = 0; j < RP; ++j) {
+                p[j] *= s;
+                m = fmaxf(m, fabsf(p[j]));
+            }
+            if (kF16) pow2_scale(m, up, down);
+#pragma unroll
+            for (int c = 0; c < RP / 8; ++c) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = kF16 ? p[c * 8 + e] * up : p[c * 8 + e];
+                uint4 hi, lo;
+                split8<T>(x, hi, lo);
+                constexpr int kC = RP / 8;
+                st_shared_v4(hbase + (c >> 3) * 16384 + tc::sw128_off(row, c & 7), hi);
+                st_shared_v4(hbase + ((c + kC) >> 3) * 16384 + tc::sw128_off(row, (c + kC) & 7), lo);
+            }
+            fence_proxy_async_smem();
+            named_barrier(1, kEpi);
+            if (et == 0) mbar_arrive(smem_u32(&sh.h));
+
+            for (int j = 0; j < nn; ++j, ++q, ++n2) {
+                const uint32_t sl = q % S, st = sbase + sl * Cfg::kStage, b = n2 & 1u;
+                bool ok = wait(smem_u32(&sh.full[sl]), (q / S) & 1u);
+                ok = wait(smem_u32(&sh.d2_full[b]), (n2 / 2) & 1u) && ok;
+                tc::fence_after_sync();
+                const int n0 = (na + j) * kKC;
+                T* dst = static_cast<T*>(g.O) + tok * g.ldo + n0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float x[32];
+                    tc::tmem_ld32(lane_addr + 128 + b * 64 + h * 32, x);
+                    if (h == 1) {
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sh.d2_empty[b]));
+                    }
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t at = st + tc::sw128_off(row, h * 4 + c);
+                        float y[8];
+                        if (g.base) Elt<T>::unpack(ld_shared_v4(at), y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float lr = kF16 ? x[c * 8 + e] * down : x[c * 8 + e];
+                            y[e] = g.base ? y[e] + lr : lr;
+                        }
+                        const uint4 w = Elt<T>::pack(y);
+                        if (full) st_shared_v4(at, w);
+                        else if (ok && mine && n0 + (h * 4 + c) * 8 < g.N) *reinterpret_cast<uint4*>(dst + (h * 4 + c) * 8) = w;
+                    }
+                }
+                if (full) fence_proxy_async_smem();
+                named_barrier(1, kEpi);  // the stage's tile is finished (full) or has been read
+                if (et == 0) {
+                    if (full) {
+                        if (!sh.failed) tma_store_2d(&map_o, n0, t.tok0, st);
+                        bulk_commit();
+                        // the store before this one has been read out: its stage is free
+                        bulk_wait_read<1>();
+                        if (j > 0) mbar_arrive(smem_u32(&sh.empty[(q - 1) % S]));
+                        if (j == nn - 1) {
+                            bulk_wait_read<0>();
+                            mbar_arrive(smem_u32(&sh.empty[sl]));
+                        }
+                    } else {
+                        mbar_arrive(smem_u32(&sh.empty[sl]));
+                    }
+                }
+            }
+        }
+        if (et == 0) bulk_wait<0>();
+        // tokens without an adapter: O = base, P = 0
+        const bool copy = g.O && (g.O != g.base);
+        if (copy || g.P) {
+            for (int64_t pos = (int64_t)g.v.off[g.v.n] + blockIdx.x; pos < g.v.tokens; pos += gridDim.x) {
+                const int64_t t = g.v.order[pos];
+                if (copy) {
+                    const uint4* src = g.base ? reinterpret_cast<const uint4*>(static_cast<const T*>(g.base) + t * g.ldb)
+                                              : nullptr;
+                    uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(g.O) + t * g.ldo);
+                    for (int i = et; i < g.N / 8; i += kEpi) to[i] = src ? src[i] : make_uint4(0, 0, 0, 0);
+                }
+                if (g.P)
+                    for (int j = et; j < g.rank; j += kEpi) g.P[t * g.rank + j] = 0.f;
+            }
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (C > 1) cluster_sync();  // nobody reads this CTA's sums or arrives on its barriers any more
+    if (warp == 1) tc::tmem_dealloc(tmem, Cfg::kTmem);
+}
+
+// ------------------------------------------------------------------ host side
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 f = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return f;
+}
+
+// Tensor map of a dim-dimensional tensor of 16-bit elements (strides in elements, of dimensions
+// 1 ..) with the 128-byte swizzle and boxes 64 elements wide.
+bool encode(CUtensorMap* map, bool bf16, const void* base, int dim, const int64_t* sizes, const int64_t* strides,
+            int box1) {
+    cuuint64_t d[3], st[2];
+    cuuint32_t box[3] = {64, (cuuint32_t)box1, 1}, elem[3] = {1, 1, 1};
+    for (int i = 0; i < dim; ++i) d[i] = (cuuint64_t)sizes[i];
+    for (int i = 0; i + 1 < dim; ++i) st[i] = (cuuint64_t)strides[i] * 2;
+    return encode_fn()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dim,
+                       const_cast<void*>(base), d, st, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_rows(CUtensorMap* map, bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    const int64_t sizes[2] = {cols, rows}, strides[1] = {ld};
+    return encode(map, bf16, p, 2, sizes, strides, box_rows);
+}
+
+// What a row-strided operand needs for 16-byte TMA rows.
+bool rows_ok(const void* p, int64_t cols, int64_t ld) {
+    return cols % 8 == 0 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld < (1ll << 38);
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t clusters, int c, int threads, uint32_t smem, cudaStream_t s,
+                            const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * c));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    count_launches(1);
+    return e;
+}
+
+// The dynamic shared memory limit of a kernel, raised once per device.
+template <typename K>
+cudaError_t allow_smem(K kern, uint32_t smem, bool (&done)[64]) {
+    const int d = device_props().device;
+    if (d >= 0 && d < 64 && done[d]) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess && d >= 0 && d < 64) done[d] = true;
+    return e;
+}
+
+template <typename T, bool kBack, int RP>
+cudaError_t run_tiles(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) {
+    using Cfg = TileCfg<RP>;
+    static bool done[64];
+    auto kern = lora_tile_kernel<T, kBack, RP>;
+    cudaError_t e = allow_smem(kern, Cfg::kSmem, done);
+    if (e != cudaSuccess) return e;
+    constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+    CUtensorMap mu, mu1, ma, mb, mbase, mbase1, mo;
+    const int64_t in = kBack ? a.N : a.K, out = kBack ? a.K : a.N;
+    const int64_t sa[3] = {in, a.rank, v.n}, ta[2] = {in, in * a.rank};
+    const int64_t sb[3] = {a.rank, out, v.n}, tb[2] = {a.rank, out * a.rank};
+    TileArgs g;
+    g.hand = a.rank % 8 != 0;
+    bool ok = encode_rows(&mu, bf, a.U, v.tokens, a.K, a.ldu, kLoraTile) &&
+              encode_rows(&mu1, bf, a.U, v.tokens, a.K, a.ldu, 1) && encode(&ma, bf, a.A, 3, sa, ta, RP);
+    mb = ma;  // unused maps are valid ones
+    mbase = mu;
+    mbase1 = mu1;
+    mo = mu;
+    if (!g.hand) ok = ok && encode(&mb, bf, a.B, 3, sb, tb, 64);
+    if (a.O && a.base)
+        ok = ok && encode_rows(&mbase, bf, a.base, v.tokens, a.N, a.ldb, kLoraTile) &&
+             encode_rows(&mbase1, bf, a.base, v.tokens, a.N, a.ldb, 1);
+    if (a.O) ok = ok && encode_rows(&mo, bf, a.O, v.tokens, a.N, a.ldo, kLoraTile);
+    if (!ok) return cudaErrorInvalidValue;
+    g.v = v;
+    g.B = a.B;
+    g.scale = a.scale;
+    g.base = a.O ? a.base : nullptr;
+    g.O = a.O;
+    g.P = a.P;
+    g.ldb = a.ldb;
+    g.ldo = a.ldo;
+    g.K = a.K;
+    g.N = a.N;
+    g.rank = a.rank;
+    g.scale_all = a.scale_all;
+    g.err = device_error_word();
+    const int64_t slots = (int64_t)device_props().sm_count * Cfg::kPerSm;
+    const int64_t cap = lora_tiles_cap(v.tokens, v.n, kLoraTile);
+    int c = 1;
+    while (c < 8 && cap * c * 2 <= slots + slots / 8) c *= 2;
+    const int64_t clusters = max64(1, min64(cap, slots / c));
+    return launch_clusters(kern, clusters, c, kTileThreads, Cfg::kSmem, s, g, mu, mu1, ma, mb, mbase, mbase1, mo);
+}
+
+template <typename T, bool kBack>
+cudaError_t run_tiles_rank(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) {
+    if (a.rank <= 16) return run_tiles<T, kBack, 16>(a, v, s);
+    if (a.rank <= 32) return run_tiles<T, kBack, 32>(a, v, s);
+    if (a.rank <= 64) return run_tiles<T, kBack, 64>(a, v, s);
+    return run_tiles<T, kBack, 128>(a, v, s);
+}
+
+}  // namespace
+
+bool lora_tiles_ok(int dt, const LoraArgs& a, const LoraPlanView& v) {
+    if (dt == kF32 || !encode_fn()) return false;
+    if (!rows_ok(a.U, a.K, a.ldu) || a.N % 8 != 0) return false;
+    if (a.O && (!rows_ok(a.O, a.N, a.ldo) || (a.base && !rows_ok(a.base, a.N, a.ldb)))) return false;
+    return (reinterpret_cast<uintptr_t>(a.A) | reinterpret_cast<uintptr_t>(a.B)) % 16 == 0;
+}
+
+cudaError_t launch_lora_tiles(int dt, bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) {
+    if (dt == kF16)
+        return back ? run_tiles_rank<__half, true>(a, v, s) : run_tiles_rank<__half, false>(a, v, s);
+    return back ? run_tiles_rank<__nv_bfloat16, true>(a, v, s) : run_tiles_rank<__nv_bfloat16, false>(a, v, s);
+}
+
+}  // namespace spops
