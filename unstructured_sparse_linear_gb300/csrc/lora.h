@@ -101,6 +101,9 @@ cudaError_t launch_lora_wgrad_rows(int dt, const LoraWgradArgs* w, int nw, int32
 // Tensor-core kernels (fp16 / bf16, 16-byte rows).
 bool lora_tiles_ok(int dt, const LoraArgs& a, const LoraPlanView& v);
 cudaError_t launch_lora_tiles(int dt, bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s);
+bool lora_wgrad_tiles_ok(int dt, const LoraWgradArgs* w, int nw);
+cudaError_t launch_lora_wgrad_tiles(int dt, const LoraWgradArgs* w, int nw, int32_t rank, const float* scale,
+                                    float scale_all, const LoraPlanView& v, cudaStream_t s);
 
 // Operators (the dispatch between the kernels).
 cudaError_t launch_lora(int dt, bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s);

@@ -553,6 +553,276 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
     if (warp == 1) tc::tmem_dealloc(tmem, Cfg::kTmem);
 }
 
+// ------------------------------------------------------------------ weight gradients
+
+// Warps: 0 loads U (TMA), 1 multiplies (one thread), 2 to 5 write P's parts into the stages.
+constexpr int kWgThreads = 192;
+constexpr int kWgCols = 256;  // columns of U per cluster: two accumulators of 128
+constexpr int kWgMaxStages = 4;
+
+template <int RP>
+struct WgCfg {
+    static constexpr int kBlocks = (RP + 63) / 64;
+    static constexpr uint32_t kU = kWgCols / 64 * 8192;        // 64 tokens x 256 columns, 64-column blocks
+    static constexpr uint32_t kPart = kBlocks * 8192;           // 64 tokens x RP of one part of P
+    static constexpr uint32_t kStage = kU + 2 * kPart;
+    static constexpr uint32_t kBudget = 227 * 1024;
+    static constexpr int kFit = (int)((kBudget - kTileBars) / kStage);
+    static constexpr int kStages = kFit < kWgMaxStages ? kFit : kWgMaxStages;
+    static constexpr uint32_t kSmem = kStages * kStage + kTileBars;
+    static constexpr uint32_t kTmem = 2 * RP < 32 ? 32 : 2 * RP;  // a power of two
+    static_assert(kStages >= 2 && kStages * kStage >= RP * kWgCols * 4u, "the partial sums fit in the ring");
+};
+
+struct WgArgs {
+    LoraPlanView v;
+    LoraWgradArgs w[2];
+    int blocks[2];  // 256-column blocks of each product
+    const float* scale;
+    float scale_all;
+    int32_t rank;
+    int* err;
+};
+
+// A cluster takes 256 columns of one adapter's gradient; its CTAs split the adapter's tokens in
+// chunks of 64 and their fp32 partial sums are added in rank order through distributed shared
+// memory. U's rows are the K axis: a chunk is 64 rows x 256 columns, an MN-major operand just as
+// TMA writes it (boxes of 64 columns; four rows at a time where the tokens are not consecutive).
+// Rows past the adapter's last token are asked for beyond the tensor, which fills zeros. P is
+// read in fp32 and written to the stage as its two parts by the four warps that later drain the
+// accumulators.
+template <typename T, int RP>
+__global__ void __launch_bounds__(kWgThreads, 1)
+lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, const __grid_constant__ CUtensorMap map_g0,
+                  const __grid_constant__ CUtensorMap map_u1, const __grid_constant__ CUtensorMap map_g1) {
+    using Cfg = WgCfg<RP>;
+    constexpr int S = Cfg::kStages;
+    constexpr bool kF16 = std::is_same<T, __half>::value;
+    constexpr uint32_t kIdesc = tc::instr_desc_f16(kF16 ? 0u : 1u, 1, 1, 128, RP);
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    struct Shared {
+        uint64_t full[S], empty[S], done, drain;
+        uint32_t tmem;
+        volatile int failed;
+        float warp_max[4];
+    };
+    static_assert(sizeof(Shared) <= kTileBars, "barriers");
+    Shared& sh = *reinterpret_cast<Shared*>(smem_raw + S * Cfg::kStage);
+    const uint32_t sbase = smem_u32(smem_raw);
+    if (sbase & 1023u) {  // the same on every CTA
+        record_error(g.err, kDevErrSmemAlign);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int C = (int)cluster_size(), crank = (int)cluster_rank();
+    const int per = g.blocks[0] + g.blocks[1];
+    const int item = blockIdx.x / C;
+    const int adapter = item / per, blk = item % per;
+    const int which = blk >= g.blocks[0];
+    const LoraWgradArgs& w = g.w[which];
+    const int n0 = (which ? blk - g.blocks[0] : blk) * kWgCols;
+    const int p0 = g.v.off[adapter], cnt = g.v.off[adapter + 1] - p0;
+    const int chunks = (cnt + 63) / 64;
+    const int ca = (int)((int64_t)chunks * crank / C), cb = (int)((int64_t)chunks * (crank + 1) / C);
+    const int nc = cb - ca;
+    const int pa = p0 + ca * 64, pe = min(p0 + cnt, p0 + cb * 64);  // this CTA's positions
+
+    if (warp == 1) tc::tmem_alloc(smem_u32(&sh.tmem), Cfg::kTmem);
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), 1 + 4);
+            mbar_init(smem_u32(&sh.empty[s]), 1);
+        }
+        mbar_init(smem_u32(&sh.done), 1);
+        mbar_init(smem_u32(&sh.drain), 1);
+        fence_mbar_init();
+        sh.failed = 0;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    const Waits wait{&sh.failed, g.err};
+    float down = 1.f;  // what the parts of P were scaled by, inverted
+
+    if (warp == 0) {
+        // ---------------- loads of U
+        const CUtensorMap* mu = which ? &map_u1 : &map_u0;
+        const CUtensorMap* mg = which ? &map_g1 : &map_g0;
+        int j = 0;
+        for (; j < nc; ++j) {
+            const int s = j % S;
+            const uint32_t st = sbase + s * Cfg::kStage, fb = smem_u32(&sh.full[s]);
+            const int b = pa + j * 64, m = min(64, pe - b);
+            // lane = 4 tokens (group lane % 16) and two of the four 64-column blocks
+            int y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = (lane & 15) * 4 + i;
+                y[i] = at < m ? g.v.order[b + at] : g.v.tokens;  // past the last row: zeros
+            }
+            const int first = __shfl_sync(0xffffffffu, y[0], 0), last = __shfl_sync(0xffffffffu, y[3], 15);
+            const bool box = m == 64 && last - first == 63;
+            if (j >= S && !__all_sync(0xffffffffu, wait(smem_u32(&sh.empty[s]), (j / S - 1) & 1u))) break;
+            if (lane == 0) mbar_arrive_expect_tx(fb, Cfg::kU);
+            __syncwarp();
+            if (box) {
+                if (lane < kWgCols / 64) tma_load_2d(st + lane * 8192, mu, n0 + lane * 64, first, fb);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int c = (lane >> 4) * 2 + i;
+                    tma_gather4(st + c * 8192 + (lane & 15) * 512, mg, n0 + c * 64, y, fb);
+                }
+            }
+        }
+        if (sh.failed) {
+            for (int i = max(0, j - S); i < j; ++i)
+                mbar_wait_for(smem_u32(&sh.full[i % S]), (i / S) & 1u, nullptr, kDrainNs);
+        }
+    } else if (warp == 1) {
+        // ---------------- multiplications
+        if (lane == 0) {
+            for (int j = 0; j < nc; ++j) {
+                const int s = j % S;
+                const uint32_t st = sbase + s * Cfg::kStage;
+                if (!wait(smem_u32(&sh.full[s]), (j / S) & 1u)) break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint64_t ad = tc::smem_desc_sw128(st + m * 16384 + kk * 2048, 8192, 1024);
+                            const uint64_t bd = tc::smem_desc_sw128(st + Cfg::kU + h * Cfg::kPart + kk * 2048, 8192, 1024);
+                            tc::mma_f16(tmem + m * RP, ad, bd, kIdesc, (j > 0 || kk > 0 || h > 0) ? 1u : 0u);
+                        }
+                tc::mma_commit(smem_u32(&sh.empty[s]));
+            }
+            tc::mma_commit(smem_u32(&sh.done));
+            if (sh.failed) {
+                tc::mma_commit(smem_u32(&sh.drain));
+                mbar_wait_for(smem_u32(&sh.drain), 0, nullptr, kDrainNs);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---------------- P's parts
+        const int et = tid - 64;
+        const int r = g.rank;
+        const bool vec = r % 4 == 0 && (reinterpret_cast<uintptr_t>(w.P) & 15) == 0;
+        // eight values of a token's P from column j0
+        auto load8 = [&](int64_t t, int j0, float* x) {
+            const float* src = w.P + t * r + j0;
+            if (vec) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float4 f = j0 + 4 * i < r ? *reinterpret_cast<const float4*>(src + 4 * i) : make_float4(0, 0, 0, 0);
+                    x[4 * i] = f.x;
+                    x[4 * i + 1] = f.y;
+                    x[4 * i + 2] = f.z;
+                    x[4 * i + 3] = f.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = j0 + i < r ? src[i] : 0.f;
+            }
+        };
+        constexpr int kCh = RP / 8;         // 8-column pieces per token
+        constexpr int kPer = 64 * kCh / kEpi;  // pieces per thread of a chunk
+        float up = 1.f;
+        if (kF16) {  // the largest magnitude among this CTA's tokens
+            float m = 0.f;
+            for (int64_t i = et; i < (int64_t)(pe - pa) * kCh; i += kEpi) {
+                float x[8];
+                load8(g.v.order[pa + i / kCh], (int)(i % kCh) * 8, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+            if (lane == 0) sh.warp_max[warp - 2] = m;
+            named_barrier(1, kEpi);
+            m = fmaxf(fmaxf(sh.warp_max[0], sh.warp_max[1]), fmaxf(sh.warp_max[2], sh.warp_max[3]));
+            pow2_scale(m, up, down);
+        }
+        for (int j = 0; j < nc; ++j) {
+            const int s = j % S;
+            const uint32_t st = sbase + s * Cfg::kStage + Cfg::kU;
+            const int b = pa + j * 64, m = min(64, pe - b);
+            float x[kPer][8];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int at = (et + i * kEpi) / kCh, c = (et + i * kEpi) % kCh;
+                if (at < m) {
+                    load8(g.v.order[b + at], c * 8, x[i]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+                }
+            }
+            if (j >= S) wait(smem_u32(&sh.empty[s]), (j / S - 1) & 1u);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int at = (et + i * kEpi) / kCh, c = (et + i * kEpi) % kCh;
+                if (kF16)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[i][e] *= up;
+                uint4 hi, lo;
+                split8<T>(x[i], hi, lo);
+                const uint32_t o = st + (c >> 3) * 8192 + tc::sw128_off(at, c & 7);
+                st_shared_v4(o, hi);
+                st_shared_v4(o + Cfg::kPart, lo);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
+        }
+        wait(smem_u32(&sh.done), 0);
+        tc::fence_after_sync();
+        // partial sums [j][256 columns] over the ring, which nothing uses any more
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int c = 0; c < RP / 16; ++c) {
+                float x[16];
+                if (nc > 0) {
+                    tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + m * RP + c * 16, x);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    st_shared_f32(sbase + ((c * 16 + i) * kWgCols + m * 128 + row) * 4, x[i] * down);
+            }
+        tc::fence_before_sync();
+    }
+    __syncthreads();
+    if (C > 1) cluster_sync();
+    {
+        // this rank's share of the columns, every sum in rank order
+        const int x0 = kWgCols * crank / C, nx = kWgCols * (crank + 1) / C - x0, r = g.rank;
+        const float s = g.scale_all * (g.scale ? g.scale[adapter] : 1.f);
+        T* G = static_cast<T*>(w.G) + (int64_t)adapter * r * w.N;
+        for (int i = tid; i < nx * r && !sh.failed; i += kWgThreads) {
+            const int x = x0 + (w.rank_minor ? i / r : i % nx), j = w.rank_minor ? i % r : i / nx;
+            if (n0 + x >= w.N) continue;
+            const uint32_t at = sbase + (j * kWgCols + x) * 4;
+            float sum = 0.f;
+            for (int c = 0; c < C; ++c) sum += ld_cluster_f32(cluster_map(at, c));
+            const T y = Elt<T>::from_f(sum * s);
+            if (w.rank_minor) G[(int64_t)(n0 + x) * r + j] = y;
+            else G[(int64_t)j * w.N + n0 + x] = y;
+        }
+    }
+    __syncthreads();
+    if (C > 1) cluster_sync();  // nobody reads this CTA's sums any more
+    if (warp == 1) tc::tmem_dealloc(tmem, Cfg::kTmem);
+}
+
 // ------------------------------------------------------------------ host side
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -670,6 +940,50 @@ cudaError_t run_tiles(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) 
     return launch_clusters(kern, clusters, c, kTileThreads, Cfg::kSmem, s, g, mu, mu1, ma, mb, mbase, mbase1, mo);
 }
 
+template <typename T, int RP>
+cudaError_t run_wgrad(const LoraWgradArgs* w, int nw, int32_t rank, const float* scale, float scale_all,
+                      const LoraPlanView& v, cudaStream_t s) {
+    using Cfg = WgCfg<RP>;
+    static bool done[64];
+    auto kern = lora_wgrad_kernel<T, RP>;
+    cudaError_t e = allow_smem(kern, Cfg::kSmem, done);
+    if (e != cudaSuccess) return e;
+    constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+    CUtensorMap mu[2], mg[2];
+    WgArgs g;
+    g.blocks[1] = 0;
+    for (int i = 0; i < nw; ++i) {
+        g.w[i] = w[i];
+        g.blocks[i] = (w[i].N + kWgCols - 1) / kWgCols;
+        if (!encode_rows(&mu[i], bf, w[i].U, v.tokens, w[i].N, w[i].ldu, 64) ||
+            !encode_rows(&mg[i], bf, w[i].U, v.tokens, w[i].N, w[i].ldu, 1))
+            return cudaErrorInvalidValue;
+    }
+    if (nw == 1) {
+        mu[1] = mu[0];
+        mg[1] = mg[0];
+    }
+    g.v = v;
+    g.scale = scale;
+    g.scale_all = scale_all;
+    g.rank = rank;
+    g.err = device_error_word();
+    const int64_t items = (int64_t)v.n * (g.blocks[0] + g.blocks[1]);
+    int c = 1;
+    while (c < 8 && items * c * 2 <= device_props().sm_count && (int64_t)v.tokens >= 64ll * c * 2) c *= 2;
+    if (items * c > 0x7fffffffll) return cudaErrorInvalidValue;
+    return launch_clusters(kern, items, c, kWgThreads, Cfg::kSmem, s, g, mu[0], mg[0], mu[1], mg[1]);
+}
+
+template <typename T>
+cudaError_t run_wgrad_rank(const LoraWgradArgs* w, int nw, int32_t rank, const float* scale, float scale_all,
+                           const LoraPlanView& v, cudaStream_t s) {
+    if (rank <= 16) return run_wgrad<T, 16>(w, nw, rank, scale, scale_all, v, s);
+    if (rank <= 32) return run_wgrad<T, 32>(w, nw, rank, scale, scale_all, v, s);
+    if (rank <= 64) return run_wgrad<T, 64>(w, nw, rank, scale, scale_all, v, s);
+    return run_wgrad<T, 128>(w, nw, rank, scale, scale_all, v, s);
+}
+
 template <typename T, bool kBack>
 cudaError_t run_tiles_rank(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) {
     if (a.rank <= 16) return run_tiles<T, kBack, 16>(a, v, s);
@@ -691,6 +1005,19 @@ cudaError_t launch_lora_tiles(int dt, bool back, const LoraArgs& a, const LoraPl
     if (dt == kF16)
         return back ? run_tiles_rank<__half, true>(a, v, s) : run_tiles_rank<__half, false>(a, v, s);
     return back ? run_tiles_rank<__nv_bfloat16, true>(a, v, s) : run_tiles_rank<__nv_bfloat16, false>(a, v, s);
+}
+
+bool lora_wgrad_tiles_ok(int dt, const LoraWgradArgs* w, int nw) {
+    if (dt == kF32 || !encode_fn()) return false;
+    for (int i = 0; i < nw; ++i)
+        if (!rows_ok(w[i].U, w[i].N, w[i].ldu)) return false;
+    return true;
+}
+
+cudaError_t launch_lora_wgrad_tiles(int dt, const LoraWgradArgs* w, int nw, int32_t rank, const float* scale,
+                                    float scale_all, const LoraPlanView& v, cudaStream_t s) {
+    return dt == kF16 ? run_wgrad_rank<__half>(w, nw, rank, scale, scale_all, v, s)
+                      : run_wgrad_rank<__nv_bfloat16>(w, nw, rank, scale, scale_all, v, s);
 }
 
 }  // namespace spops
