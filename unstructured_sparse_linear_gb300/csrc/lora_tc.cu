@@ -142,52 +142,135 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
                  : "memory");
     return v;
 }
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint4 v) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+// Orders this thread's earlier memory accesses with later ones of the asynchronous proxy, in
+// any state space.
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+// Where the 16-byte piece c of row r of the partial sums (RP fp32 a row) lies in its row: rows
+// that one warp writes (and reads) at the same piece fall on different banks.
+template <int RP>
+__device__ __forceinline__ int p_piece(int r, int c) {
+    return c ^ (RP >= 32 ? (r & 7) : ((r >> 1) & 3));
+}
+
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// 16 (or 32) consecutive fp32 TMEM columns of the thread's lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float* v) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// N consecutive fp32 TMEM columns of the thread's lane, complete on return (the load and its wait
+// are one statement, so that no use can be scheduled between them).
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t taddr, float* v) {
+    static_assert(N == 8 || N == 16 || N == 32, "shapes");
+    uint32_t r[N];
+    if constexpr (N == 8) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+            : "r"(taddr)
+            : "memory");
+    } else if constexpr (N == 16) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr)
+            : "memory");
+    } else if constexpr (N == 32) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+            "tcgen05.wait::ld.sync.aligned;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+              "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+              "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+              "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+            : "r"(taddr)
+            : "memory");
+    }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+    for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// A 64-row x RP tile of rows [row0, row0 + 64) of the row-major rows x rank matrix W, by one
-// warp with plain loads (ranks whose rows no 16-byte copy can address): zeros beyond the matrix,
-// 64-column blocks of 8 KB in the 128-byte-swizzled layout.
+// Copies of B bytes (4 or 8) from global to shared memory, and the arrival on `bar` of a thread
+// once its earlier ones are complete.
+template <int B>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(B) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// A 64-row x RP tile of rows [row0, row0 + 64) of the row-major rows x rank matrix W, by one warp,
+// for ranks whose rows TMA cannot address (rank not a multiple of 8): zeros beyond the matrix,
+// 64-column blocks of 8 KB in the 128-byte-swizzled layout. Even ranks with aligned rows are
+// copied asynchronously (the caller's cp_async_arrive signals them), odd ones by plain loads.
 template <typename T, int RP>
 __device__ __forceinline__ void load_b_tile(uint32_t dst, const T* W, int64_t row0, int64_t rows, int rank) {
     const int lane = threadIdx.x & 31;
+    const int m = (int)min64(64, rows - row0);
+    const char* src = reinterpret_cast<const char*>(W + row0 * rank);
     constexpr int kChunks = RP / 8;
+    auto at = [&](int row, int col) {  // of 16-bit elements
+        return dst + (col >> 6) * 8192 + tc::sw128_off(row, (col >> 3) & 7) + (col & 7) * 2;
+    };
+    if (rank & 1) {
 #pragma unroll 2
-    for (int i = lane; i < 64 * kChunks; i += 32) {
-        const int row = i / kChunks, c = i % kChunks;
-        uint32_t w[4] = {0, 0, 0, 0};
-        if (row0 + row < rows) {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(W + (row0 + row) * rank);
+        for (int i = lane; i < 64 * kChunks; i += 32) {
+            const int row = i / kChunks, c = i % kChunks;
+            uint32_t w[4] = {0, 0, 0, 0};
+            if (row < m) {
+                const uint16_t* p = reinterpret_cast<const uint16_t*>(src) + (int64_t)row * rank;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c * 8 + e < rank) w[e >> 1] |= (uint32_t)src[c * 8 + e] << (16 * (e & 1));
+                for (int e = 0; e < 8; ++e)
+                    if (c * 8 + e < rank) w[e >> 1] |= (uint32_t)p[c * 8 + e] << (16 * (e & 1));
+            }
+            st_shared_v4(at(row, c * 8), make_uint4(w[0], w[1], w[2], w[3]));
         }
-        st_shared_v4(dst + (c >> 3) * 8192 + tc::sw128_off(row, c & 7), make_uint4(w[0], w[1], w[2], w[3]));
+        return;
+    }
+    // pieces of two or four elements; zeros first in the pieces that hold any
+    const int full = rank / 8;  // whole 16-byte pieces of a row
+    for (int i = lane; i < 64 * (kChunks - full); i += 32) {
+        const int row = i / (kChunks - full), c = full + i % (kChunks - full);
+        if (c * 8 >= rank || row >= m) st_shared_v4(at(row, c * 8), make_uint4(0, 0, 0, 0));
+        else  // the tail of the piece that rank ends in
+            for (int e = rank & 7; e < 8; e += 2)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at(row, c * 8 + e)), "r"(0) : "memory");
+    }
+    if (m < 64)
+        for (int i = lane; i < (64 - m) * full; i += 32)
+            st_shared_v4(at(m + i / full, i % full * 8), make_uint4(0, 0, 0, 0));
+    if (rank % 4 == 0) {
+        const int n = rank / 4;
+        for (int i = lane; i < m * n; i += 32) cp_async_small<8>(at(i / n, i % n * 4), src + (int64_t)i * 8);
+    } else {
+        const int n = rank / 2;
+        for (int i = lane; i < m * n; i += 32) cp_async_small<4>(at(i / n, i % n * 2), src + (int64_t)i * 4);
     }
 }
 
 // ------------------------------------------------------------------ tile kernel
 
-// Warps: 0 loads (TMA), 1 multiplies (one thread), 2 to 5 finish (one row per thread), 6 loads
-// the rank-contiguous weight tiles where TMA cannot.
-constexpr int kTileThreads = 224;
-constexpr int kEpi = 128;
-constexpr uint32_t kTileBars = 1024;  // barriers and flags, behind the stages and P
+// Warps: 0 loads (TMA), 1 multiplies (one thread), 2 to 9 finish (two threads per row, each with
+// half of the columns).
+constexpr int kTileThreads = 320;
+constexpr int kEpi = 256;
+constexpr uint32_t kTileBars = 1024;  // barriers, flags and row factors, behind the stages and P
 
 template <int RP>
 struct TileCfg {
@@ -208,7 +291,7 @@ struct TileCfg {
 
 struct TileArgs {
     LoraPlanView v;
-    const void* B;       // for the warp that loads it by hand
+    const void* B;
     const float* scale;
     const void* base;
     void* O;
@@ -216,13 +299,14 @@ struct TileArgs {
     int64_t ldb, ldo;
     int32_t K, N, rank;
     float scale_all;
-    int hand;  // B tiles are loaded by warp 6
+    int hand;  // B tiles are copied by threads
     int* err;
 };
 
-// A cluster of C CTAs takes a tile: rank c multiplies a share of the K chunks into its TMEM, the
-// fp32 partial P are exchanged through distributed shared memory (every rank adds all of them in
-// rank order), and rank c forms a share of the 64-column chunks of O. One ring of stages carries
+// A cluster of C CTAs takes a tile: rank c multiplies a share of the K chunks into its TMEM; the
+// fp32 partial P are sent through distributed shared memory to the rank that owns the row, which
+// adds them in rank order and sends the two 16-bit parts back to all; and rank c forms a share of
+// the 64-column chunks of O. One ring of stages carries
 // both phases, so the loads of base run ahead while P is being summed: a stage holds a 128 x 64
 // tile of U with a tile of W1, then a 128 x 64 tile of base, in which O is formed in place, with a
 // tile of W2. Rows come by one TMA box when the tile is full and its tokens consecutive, else four
@@ -244,9 +328,10 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
     // tiles need (checked).
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     struct Shared {
-        uint64_t full[S], empty[S], d1, h, d2_full[2], d2_empty[2], pub, read, drain;
+        uint64_t full[S], empty[S], d1, h, d2_full[2], d2_empty[2], pub, read, freed, drain;
         uint32_t tmem;
         volatile int failed;
+        float down[kLoraTile];  // fp16: what a row's parts were scaled by, inverted
     };
     static_assert(sizeof(Shared) <= kTileBars, "barriers");
     Shared& sh = *reinterpret_cast<Shared*>(smem_raw + S * Cfg::kStage + Cfg::kH);
@@ -259,21 +344,35 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = (int)cluster_size(), crank = (int)cluster_rank();
     const int cid = blockIdx.x / C, ncl = gridDim.x / C;
+    // Every CTA's first tile, read while the barriers are set up (the list has a slot per cluster;
+    // what lies behind its end is not used).
+    const int ntiles = g.v.counts[kLoraCntTiles];
+    const LoraTile tile0 = g.v.tiles[cid];
 
     if (warp == 1) tc::tmem_alloc(smem_u32(&sh.tmem), Cfg::kTmem);
+    if (warp == 2 && lane == 0) {
+        tma_prefetch_map(&map_u);
+        tma_prefetch_map(&map_u1);
+        tma_prefetch_map(&map_a);
+        tma_prefetch_map(&map_b);
+        tma_prefetch_map(&map_base);
+        tma_prefetch_map(&map_base1);
+        tma_prefetch_map(&map_o);
+    }
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&sh.full[s]), g.hand ? 2 : 1);
+            mbar_init(smem_u32(&sh.full[s]), g.hand ? 1 + 32 : 1);
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
         mbar_init(smem_u32(&sh.d1), 1);
-        mbar_init(smem_u32(&sh.h), 1);
+        mbar_init(smem_u32(&sh.h), C);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.d2_full[i]), 1);
-            mbar_init(smem_u32(&sh.d2_empty[i]), 4);
+            mbar_init(smem_u32(&sh.d2_empty[i]), kEpi / 32);
         }
         mbar_init(smem_u32(&sh.pub), C);
         mbar_init(smem_u32(&sh.read), C);
+        mbar_init(smem_u32(&sh.freed), C);
         mbar_init(smem_u32(&sh.drain), 1);
         fence_mbar_init();
         sh.failed = 0;
@@ -284,7 +383,6 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
     const Waits wait{&sh.failed, g.err};
-    const int ntiles = g.v.counts[kLoraCntTiles];
     const int nkc = (g.K + kKC - 1) / kKC, nnc = g.O ? (g.N + kKC - 1) / kKC : 0;
     const int ka = (int)((int64_t)nkc * crank / C), kb = (int)((int64_t)nkc * (crank + 1) / C);
     const int na = (int)((int64_t)nnc * crank / C), nb = (int)((int64_t)nnc * (crank + 1) / C);
@@ -294,8 +392,9 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
         // ---------------- loads
         uint32_t q = 0;
         bool ok = true;
+        const int64_t brows = kBack ? g.K : g.N;
         for (int it = cid; it < ntiles && ok; it += ncl) {
-            const LoraTile t = g.v.tiles[it];
+            const LoraTile t = it == cid ? tile0 : g.v.tiles[it];
             const bool box = t.rows == kLoraTile && t.tok0 >= 0;
             int y[4];
 #pragma unroll
@@ -331,6 +430,14 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
                             tma_load_3d(st + kUBytes + b * 8192, &map_b, b * 64, x, t.adapter, fb);
                     }
                 }
+                if (g.hand) {
+                    if (b_tile) {
+                        load_b_tile<T, RP>(st + kUBytes, static_cast<const T*>(g.B) + t.adapter * brows * g.rank, x,
+                                           brows, g.rank);
+                        fence_proxy_async_smem();
+                    }
+                    cp_async_arrive(fb);
+                }
             }
         }
         if (sh.failed) {  // let the copies in flight land before the shared memory is given up
@@ -347,6 +454,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
                     const uint32_t s = q % S, st = sbase + s * Cfg::kStage;
                     ok = wait(smem_u32(&sh.full[s]), (q / S) & 1u);
                     if (!ok) break;
+                    if (g.hand) fence_proxy_async_smem();  // the copies of threads
                     tc::fence_after_sync();
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk) {
@@ -359,14 +467,16 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
                 }
                 if (!ok) break;
                 tc::mma_commit(smem_u32(&sh.d1));
-                ok = wait(smem_u32(&sh.h), tt & 1u);  // P's parts are written, and its columns read
+                ok = wait.cluster(smem_u32(&sh.h), tt & 1u);  // P's parts are here, and its columns read
                 if (!ok) break;
+                fence_proxy_async_smem();  // the parts came from threads of every rank
                 tc::fence_after_sync();
                 for (int j = 0; j < nn; ++j, ++q, ++n2) {
                     const uint32_t s = q % S, st = sbase + s * Cfg::kStage, b = n2 & 1u;
                     ok = wait(smem_u32(&sh.full[s]), (q / S) & 1u);
                     if (ok && n2 >= 2) ok = wait(smem_u32(&sh.d2_empty[b]), (n2 / 2 - 1) & 1u);
                     if (!ok) break;
+                    if (g.hand) fence_proxy_async_smem();
                     tc::fence_after_sync();
                     constexpr int kSteps = RP / 16;
 #pragma unroll
@@ -387,129 +497,141 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
             }
         }
         __syncwarp();
-    } else if (warp == 6) {
-        // ---------------- B tiles by hand
-        if (g.hand) {
-            uint32_t q = 0;
-            bool ok = true;
-            const int64_t brows = kBack ? g.K : g.N;
-            for (int it = cid; it < ntiles && ok; it += ncl) {
-                const int adapter = g.v.tiles[it].adapter;
-                const T* W = static_cast<const T*>(g.B) + (int64_t)adapter * brows * g.rank;
-                for (int j = 0; j < nk + nn; ++j, ++q) {
-                    const bool p1 = j < nk;
-                    const uint32_t s = q % S, st = sbase + s * Cfg::kStage;
-                    if (q >= S) ok = __all_sync(0xffffffffu, wait(smem_u32(&sh.empty[s]), (q / S - 1) & 1u));
-                    if (!ok) break;
-                    if (p1 == kBack) {
-                        load_b_tile<T, RP>(st + kUBytes, W, (int64_t)(p1 ? ka + j : na + j - nk) * kKC, brows, g.rank);
-                        fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
-                }
-            }
-        }
     } else {
-        // ---------------- P, then O: thread = row
-        const int quarter = warp & 3, row = quarter * 32 + lane, et = tid - 64;
+        // ---------------- P, then O
+        // A row has two threads, each with half of the columns of P and of a chunk of O.
+        const int quarter = warp & 3, half = (warp - 2) >> 2, row = quarter * 32 + lane, et = tid - 64;
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int own = kLoraTile / C;  // rows that this rank sums: [crank * own, ...)
         uint32_t q = 0, n2 = 0, tt = 0;
         for (int it = cid; it < ntiles; it += ncl, ++tt) {
-            const LoraTile t = g.v.tiles[it];
+            const LoraTile t = it == cid ? tile0 : g.v.tiles[it];
             const bool full = t.rows == kLoraTile && t.tok0 >= 0, mine = row < t.rows;
             const int64_t tok = mine ? g.v.order[t.pos0 + row] : 0;
             const float s = g.scale_all * (g.scale ? g.scale[t.adapter] : 1.f);
             q += nk;
-            float p[RP];
-            wait(smem_u32(&sh.d1), tt & 1u);
-            tc::fence_after_sync();
-            if (nk > 0) {
+            {
+                // Each rank sends its partial rows to the ranks that sum them: slot (source rank,
+                // row) of `own` rows each, 16-byte pieces permuted by row against bank conflicts.
+                float p[RP / 2];
+                wait(smem_u32(&sh.d1), tt & 1u);
+                tc::fence_after_sync();
+                if (nk > 0) {
+                    constexpr int kLd = RP / 2 < 32 ? RP / 2 : 32;
 #pragma unroll
-                for (int c = 0; c < RP / 16; ++c) tmem_ld16(lane_addr + c * 16, p + c * 16);
-            } else {
+                    for (int c = 0; c < RP / 2 / kLd; ++c)
+                        tmem_load<kLd>(lane_addr + half * (RP / 2) + c * kLd, p + c * kLd);
+                } else {
 #pragma unroll
-                for (int j = 0; j < RP; ++j) p[j] = 0.f;
-            }
-            tc::fence_before_sync();
-            if (C > 1) {
-                // publish, add every rank's partial sums in rank order, and tell every rank that its
-                // sums have been read (their place then takes the 16-bit parts)
-                const uint32_t mypart = hbase + row * 4;
-#pragma unroll
-                for (int j = 0; j < RP; ++j) st_shared_f32(mypart + j * 512, p[j]);
-                named_barrier(1, kEpi);
-                if (et < C) mbar_arrive_remote(smem_u32(&sh.pub), et);
-                wait.cluster(smem_u32(&sh.pub), tt & 1u);
-#pragma unroll
-                for (int j = 0; j < RP; ++j) p[j] = 0.f;
-                for (int c = 0; c < C; ++c) {
-                    const uint32_t from = cluster_map(mypart, c);
-#pragma unroll
-                    for (int j = 0; j < RP; ++j) p[j] += ld_cluster_f32(from + j * 512);
+                    for (int j = 0; j < RP / 2; ++j) p[j] = 0.f;
                 }
-                named_barrier(1, kEpi);
-                if (et < C) mbar_arrive_remote(smem_u32(&sh.read), et);
-                wait.cluster(smem_u32(&sh.read), tt & 1u);
-            }
-            if (g.P && crank == 0 && mine) {
-                float* dst = g.P + tok * g.rank;
+                tc::fence_before_sync();
+                // every rank is done with the last tile's parts of P, whose place the sums take
+                if (tt > 0) wait.cluster(smem_u32(&sh.freed), (tt - 1) & 1u);
+                const uint32_t dst = cluster_map(hbase + (crank * own + row % own) * (RP * 4), row / own);
 #pragma unroll
-                for (int j = 0; j < RP; ++j)
-                    if (j < g.rank) dst[j] = p[j];
+                for (int c = 0; c < RP / 8; ++c)
+                    st_cluster_f4(dst + (uint32_t)p_piece<RP>(row, half * (RP / 8) + c) * 16,
+                                  make_float4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]));
             }
-            float up = 1.f, down = 1.f, m = 0.f;
-#pragma unroll
-            for (int j = 0; j < RP; ++j) {
-                p[j] *= s;
-                m = fmaxf(m, fabsf(p[j]));
-            }
-            if (kF16) pow2_scale(m, up, down);
-#pragma unroll
-            for (int c = 0; c < RP / 8; ++c) {
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = kF16 ? p[c * 8 + e] * up : p[c * 8 + e];
-                uint4 hi, lo;
-                split8<T>(x, hi, lo);
-                constexpr int kC = RP / 8;
-                st_shared_v4(hbase + (c >> 3) * 16384 + tc::sw128_off(row, c & 7), hi);
-                st_shared_v4(hbase + ((c + kC) >> 3) * 16384 + tc::sw128_off(row, (c + kC) & 7), lo);
-            }
-            fence_proxy_async_smem();
             named_barrier(1, kEpi);
-            if (et == 0) mbar_arrive(smem_u32(&sh.h));
+            if (et < C) mbar_arrive_remote(smem_u32(&sh.pub), et);
+            wait.cluster(smem_u32(&sh.pub), tt & 1u);
+            // Sums in rank order: eight columns of one row per thread and step.
+            constexpr int kG = RP / 8, kSteps = kLoraTile * kG / kEpi;
+            float x[kSteps][8];
+            const int groups = own * kG;  // a multiple of 32
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int idx = et + i * kEpi, rl = idx / kG, c8 = idx % kG;
+                if (idx >= groups) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t from = hbase + (c * own + rl) * (RP * 4);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 v = ld_shared_v4(from + (uint32_t)p_piece<RP>(rl, 2 * c8 + h) * 16);
+                        x[i][4 * h] += __uint_as_float(v.x);
+                        x[i][4 * h + 1] += __uint_as_float(v.y);
+                        x[i][4 * h + 2] += __uint_as_float(v.z);
+                        x[i][4 * h + 3] += __uint_as_float(v.w);
+                    }
+                }
+            }
+            named_barrier(1, kEpi);
+            if (et < C) mbar_arrive_remote(smem_u32(&sh.read), et);
+            if (g.P) {
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const int idx = et + i * kEpi, r = crank * own + idx / kG, c8 = idx % kG;
+                    if (idx >= groups || r >= t.rows) continue;
+                    float* to = g.P + (int64_t)g.v.order[t.pos0 + r] * g.rank + c8 * 8;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (c8 * 8 + e < g.rank) to[e] = x[i][e];
+                }
+            }
+            wait.cluster(smem_u32(&sh.read), tt & 1u);  // every rank has read its slots
+            // The two parts of s P go to every rank.
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int idx = et + i * kEpi, r = crank * own + idx / kG, c8 = idx % kG;
+                if (idx >= groups) continue;  // the same for a whole warp
+                float m = 0.f, up = 1.f, down = 1.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[i][e] *= s;
+                    m = fmaxf(m, fabsf(x[i][e]));
+                }
+                if (kF16) {  // the row's pieces lie in kG neighbouring lanes
+#pragma unroll
+                    for (int d = kG / 2; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                    pow2_scale(m, up, down);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[i][e] *= up;
+                }
+                uint4 hi, lo;
+                split8<T>(x[i], hi, lo);
+                const uint32_t at_hi = hbase + (c8 >> 3) * kUBytes + tc::sw128_off(r, c8 & 7);
+                const uint32_t at_lo = hbase + ((c8 + kG) >> 3) * kUBytes + tc::sw128_off(r, (c8 + kG) & 7);
+                for (int c = 0; c < C; ++c) {
+                    st_cluster_v4(cluster_map(at_hi, c), hi);
+                    st_cluster_v4(cluster_map(at_lo, c), lo);
+                    if (kF16 && c8 == 0) st_cluster_f32(cluster_map(smem_u32(&sh.down[r]), c), down);
+                }
+            }
+            fence_proxy_async();
+            named_barrier(1, kEpi);
+            if (et < C) mbar_arrive_remote(smem_u32(&sh.h), et);
+            wait.cluster(smem_u32(&sh.h), tt & 1u);
+            const float down = kF16 ? sh.down[row] : 1.f;
 
             for (int j = 0; j < nn; ++j, ++q, ++n2) {
                 const uint32_t sl = q % S, st = sbase + sl * Cfg::kStage, b = n2 & 1u;
+                const int n0 = (na + j) * kKC + half * 32;
                 bool ok = wait(smem_u32(&sh.full[sl]), (q / S) & 1u);
+                uint4 y[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    y[c] = g.base ? ld_shared_v4(st + tc::sw128_off(row, half * 4 + c)) : make_uint4(0, 0, 0, 0);
                 ok = wait(smem_u32(&sh.d2_full[b]), (n2 / 2) & 1u) && ok;
                 tc::fence_after_sync();
-                const int n0 = (na + j) * kKC;
+                float o[32];
+                tmem_load<32>(lane_addr + 128 + b * 64 + half * 32, o);
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.d2_empty[b]));
                 T* dst = static_cast<T*>(g.O) + tok * g.ldo + n0;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float x[32];
-                    tc::tmem_ld32(lane_addr + 128 + b * 64 + h * 32, x);
-                    if (h == 1) {
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&sh.d2_empty[b]));
-                    }
+                for (int c = 0; c < 4; ++c) {
+                    float f[8];
+                    Elt<T>::unpack(y[c], f);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t at = st + tc::sw128_off(row, h * 4 + c);
-                        float y[8];
-                        if (g.base) Elt<T>::unpack(ld_shared_v4(at), y);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float lr = kF16 ? x[c * 8 + e] * down : x[c * 8 + e];
-                            y[e] = g.base ? y[e] + lr : lr;
-                        }
-                        const uint4 w = Elt<T>::pack(y);
-                        if (full) st_shared_v4(at, w);
-                        else if (ok && mine && n0 + (h * 4 + c) * 8 < g.N) *reinterpret_cast<uint4*>(dst + (h * 4 + c) * 8) = w;
-                    }
+                    for (int e = 0; e < 8; ++e) f[e] = kF16 ? fmaf(o[c * 8 + e], down, f[e]) : f[e] + o[c * 8 + e];
+                    const uint4 w = Elt<T>::pack(f);
+                    if (full) st_shared_v4(st + tc::sw128_off(row, half * 4 + c), w);
+                    else if (ok && mine && n0 + c * 8 < g.N) *reinterpret_cast<uint4*>(dst + c * 8) = w;
                 }
                 if (full) fence_proxy_async_smem();
                 named_barrier(1, kEpi);  // the stage's tile is finished (full) or has been read
@@ -529,6 +651,8 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
                     }
                 }
             }
+            // this rank's products with P's parts are complete (their accumulators were read)
+            if (et < C) mbar_arrive_remote(smem_u32(&sh.freed), et);
         }
         if (et == 0) bulk_wait<0>();
         // tokens without an adapter: O = base, P = 0
@@ -557,6 +681,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
 
 // Warps: 0 loads U (TMA), 1 multiplies (one thread), 2 to 5 write P's parts into the stages.
 constexpr int kWgThreads = 192;
+constexpr int kWgEpi = 128;
 constexpr int kWgCols = 256;  // columns of U per cluster: two accumulators of 128
 constexpr int kWgMaxStages = 4;
 
@@ -730,11 +855,11 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             }
         };
         constexpr int kCh = RP / 8;         // 8-column pieces per token
-        constexpr int kPer = 64 * kCh / kEpi;  // pieces per thread of a chunk
+        constexpr int kPer = 64 * kCh / kWgEpi;  // pieces per thread of a chunk
         float up = 1.f;
         if (kF16) {  // the largest magnitude among this CTA's tokens
             float m = 0.f;
-            for (int64_t i = et; i < (int64_t)(pe - pa) * kCh; i += kEpi) {
+            for (int64_t i = et; i < (int64_t)(pe - pa) * kCh; i += kWgEpi) {
                 float x[8];
                 load8(g.v.order[pa + i / kCh], (int)(i % kCh) * 8, x);
 #pragma unroll
@@ -743,7 +868,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
 #pragma unroll
             for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
             if (lane == 0) sh.warp_max[warp - 2] = m;
-            named_barrier(1, kEpi);
+            named_barrier(1, kWgEpi);
             m = fmaxf(fmaxf(sh.warp_max[0], sh.warp_max[1]), fmaxf(sh.warp_max[2], sh.warp_max[3]));
             pow2_scale(m, up, down);
         }
@@ -754,7 +879,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             float x[kPer][8];
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const int at = (et + i * kEpi) / kCh, c = (et + i * kEpi) % kCh;
+                const int at = (et + i * kWgEpi) / kCh, c = (et + i * kWgEpi) % kCh;
                 if (at < m) {
                     load8(g.v.order[b + at], c * 8, x[i]);
                 } else {
@@ -765,7 +890,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             if (j >= S) wait(smem_u32(&sh.empty[s]), (j / S - 1) & 1u);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const int at = (et + i * kEpi) / kCh, c = (et + i * kEpi) % kCh;
+                const int at = (et + i * kWgEpi) / kCh, c = (et + i * kWgEpi) % kCh;
                 if (kF16)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[i][e] *= up;
@@ -789,7 +914,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             for (int c = 0; c < RP / 16; ++c) {
                 float x[16];
                 if (nc > 0) {
-                    tmem_ld16(tmem + ((uint32_t)(quarter * 32) << 16) + m * RP + c * 16, x);
+                    tmem_load<16>(tmem + ((uint32_t)(quarter * 32) << 16) + m * RP + c * 16, x);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) x[i] = 0.f;
