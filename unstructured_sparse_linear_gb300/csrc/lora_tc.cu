@@ -51,6 +51,13 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// L2 prefetch of a 2-D box: no shared memory, no completion.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
@@ -157,11 +164,14 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
-// Where the 16-byte piece c of row r of the partial sums (RP fp32 a row) lies in its row: rows
-// that one warp writes (and reads) at the same piece fall on different banks.
+// Place (in 16-byte units) of piece c of row r among the partial sums that a rank receives from
+// one rank: `own` rows of RP / 4 pieces, piece-major, so that the 32 rows that a warp sends at one
+// piece are whole 128-byte lines (a line per row and piece took 2.5 us for RP = 64), the rows
+// permuted so that the reads of 256 / RP rows x RP / 8 piece pairs meet no bank conflict.
 template <int RP>
-__device__ __forceinline__ int p_piece(int r, int c) {
-    return c ^ (RP >= 32 ? (r & 7) : ((r >> 1) & 3));
+__device__ __forceinline__ int p_place(int r, int c, int own) {
+    constexpr int rw = 256 / RP;  // rows that a warp reads at once
+    return c * own + (rw >= 8 ? r : r ^ (rw * ((c >> 1) & (8 / rw - 1))));
 }
 
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
@@ -270,6 +280,7 @@ __device__ __forceinline__ void load_b_tile(uint32_t dst, const T* W, int64_t ro
 // half of the columns).
 constexpr int kTileThreads = 320;
 constexpr int kEpi = 256;
+constexpr int kAhead = 8;  // chunks of rows that L2 prefetches run ahead of the ring
 constexpr uint32_t kTileBars = 1024;  // barriers, flags and row factors, behind the stages and P
 
 template <int RP>
@@ -289,6 +300,13 @@ struct TileCfg {
     static constexpr uint32_t kTmem = 256;  // P: columns 0 .. RP - 1; O: two buffers of 64 at 128 and 192
 };
 
+// Row-strided operands come in boxes of 128, 32 or 8 consecutive rows, or four rows anywhere.
+constexpr int kBoxes = 4;
+constexpr int kBoxRows[kBoxes] = {128, 32, 8, 1};
+struct TileMaps {
+    CUtensorMap u[kBoxes], base[kBoxes], a, b, o;  // o: boxes of 32 rows
+};
+
 struct TileArgs {
     LoraPlanView v;
     const void* B;
@@ -303,20 +321,45 @@ struct TileArgs {
     int* err;
 };
 
+// How lane i of the loading warp fetches rows 4 i .. 4 i + 3 of a tile: as (the first lane of) a
+// box of 128, 32 or 8 consecutive tokens (mode 0, 1, 2), as four tokens anywhere (mode 3; rows past
+// the tile repeat its last one), or not at all (mode -1: no such row, or another lane's box).
+// A gather of four rows costs the copy engine about as much as a box: a whole tile of them took
+// 1.2 us a chunk, three times a box of 128 rows.
+struct RowSource {
+    int mode, y[4];
+};
+__device__ __forceinline__ RowSource row_source(const LoraTile& t, const int32_t* order, int lane) {
+    RowSource r;
+    if (t.rows == kLoraTile && t.tok0 >= 0) {
+        r.mode = lane == 0 ? 0 : -1;
+        r.y[0] = t.tok0;
+        r.y[1] = r.y[2] = r.y[3] = 0;
+        return r;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.y[i] = order[t.pos0 + min(4 * lane + i, t.rows - 1)];
+    const bool run4 = 4 * lane + 4 <= t.rows && r.y[3] - r.y[0] == 3;  // ascending, so consecutive
+    const int next = __shfl_down_sync(0xffffffffu, r.y[0], 1);
+    const unsigned runs = __ballot_sync(0xffffffffu, run4);
+    const unsigned links = __ballot_sync(0xffffffffu, next == r.y[3] + 1);  // lane and lane + 1 (not lane 31)
+    const int l8 = lane & ~7, l2 = lane & ~1;
+    if (((runs >> l8) & 0xffu) == 0xffu && ((links >> l8) & 0x7fu) == 0x7fu) r.mode = lane == l8 ? 1 : -1;
+    else if (((runs >> l2) & 3u) == 3u && ((links >> l2) & 1u)) r.mode = lane == l2 ? 2 : -1;
+    else r.mode = 4 * lane < t.rows ? 3 : -1;
+    return r;
+}
+
 // A cluster of C CTAs takes a tile: rank c multiplies a share of the K chunks into its TMEM; the
 // fp32 partial P are sent through distributed shared memory to the rank that owns the row, which
 // adds them in rank order and sends the two 16-bit parts back to all; and rank c forms a share of
-// the 64-column chunks of O. One ring of stages carries
-// both phases, so the loads of base run ahead while P is being summed: a stage holds a 128 x 64
-// tile of U with a tile of W1, then a 128 x 64 tile of base, in which O is formed in place, with a
-// tile of W2. Rows come by one TMA box when the tile is full and its tokens consecutive, else four
-// rows at a time (gather4).
+// the 64-column chunks of O. One ring of stages carries both phases, so the loads of base run
+// ahead while P is being summed (and L2 prefetches further ahead): a stage holds a 128 x 64 tile
+// of U with a tile of W1, then a 128 x 64 tile of base, in which O is formed in place, with a tile
+// of W2.
 template <typename T, bool kBack, int RP>
 __global__ void __launch_bounds__(kTileThreads, TileCfg<RP>::kPerSm)
-lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, const __grid_constant__ CUtensorMap map_u1,
-                 const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                 const __grid_constant__ CUtensorMap map_base, const __grid_constant__ CUtensorMap map_base1,
-                 const __grid_constant__ CUtensorMap map_o) {
+lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
     using Cfg = TileCfg<RP>;
     constexpr int S = Cfg::kStages;
     constexpr bool kF16 = std::is_same<T, __half>::value;
@@ -351,24 +394,24 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
 
     if (warp == 1) tc::tmem_alloc(smem_u32(&sh.tmem), Cfg::kTmem);
     if (warp == 2 && lane == 0) {
-        tma_prefetch_map(&map_u);
-        tma_prefetch_map(&map_u1);
-        tma_prefetch_map(&map_a);
-        tma_prefetch_map(&map_b);
-        tma_prefetch_map(&map_base);
-        tma_prefetch_map(&map_base1);
-        tma_prefetch_map(&map_o);
+        for (int i = 0; i < kBoxes; ++i) {
+            tma_prefetch_map(&maps.u[i]);
+            tma_prefetch_map(&maps.base[i]);
+        }
+        tma_prefetch_map(&maps.a);
+        tma_prefetch_map(&maps.b);
+        tma_prefetch_map(&maps.o);
     }
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(smem_u32(&sh.full[s]), g.hand ? 1 + 32 : 1);
-            mbar_init(smem_u32(&sh.empty[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), 4);  // four commits, or the four warps of a group
         }
         mbar_init(smem_u32(&sh.d1), 1);
         mbar_init(smem_u32(&sh.h), C);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.d2_full[i]), 1);
-            mbar_init(smem_u32(&sh.d2_empty[i]), kEpi / 32);
+            mbar_init(smem_u32(&sh.d2_empty[i]), 4);
         }
         mbar_init(smem_u32(&sh.pub), C);
         mbar_init(smem_u32(&sh.read), C);
@@ -384,9 +427,9 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
     const uint32_t tmem = sh.tmem;
     const Waits wait{&sh.failed, g.err};
     const int nkc = (g.K + kKC - 1) / kKC, nnc = g.O ? (g.N + kKC - 1) / kKC : 0;
-    const int ka = (int)((int64_t)nkc * crank / C), kb = (int)((int64_t)nkc * (crank + 1) / C);
-    const int na = (int)((int64_t)nnc * crank / C), nb = (int)((int64_t)nnc * (crank + 1) / C);
-    const int nk = kb - ka, nn = nb - na;
+    const int clog = 31 - __clz(C);  // C is a power of two; the chunk counts are below 2^26
+    const int ka = (nkc * crank) >> clog, na = (nnc * crank) >> clog;
+    const int nk = ((nkc * (crank + 1)) >> clog) - ka, nn = ((nnc * (crank + 1)) >> clog) - na;
 
     if (warp == 0) {
         // ---------------- loads
@@ -395,39 +438,35 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
         const int64_t brows = kBack ? g.K : g.N;
         for (int it = cid; it < ntiles && ok; it += ncl) {
             const LoraTile t = it == cid ? tile0 : g.v.tiles[it];
-            const bool box = t.rows == kLoraTile && t.tok0 >= 0;
-            int y[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = box ? 0 : g.v.order[t.pos0 + min(4 * lane + i, t.rows - 1)];
-            const int groups = (t.rows + 3) / 4;
-            const uint32_t ubytes = box ? kUBytes : (uint32_t)groups * 512u;
+            const RowSource rows = row_source(t, g.v.order, lane);
+            const uint32_t ubytes = (uint32_t)((t.rows + 3) / 4) * 512u;
+            if (rows.mode == 0 || rows.mode == 1)  // what the ring cannot hold yet is fetched to L2
+                for (int j = S; j < min(nk, S + kAhead); ++j) tma_prefetch_2d(&maps.u[rows.mode], (ka + j) * kKC, rows.y[0]);
             for (int j = 0; j < nk + nn; ++j, ++q) {
                 const bool p1 = j < nk;
                 const uint32_t s = q % S, st = sbase + s * Cfg::kStage, fb = smem_u32(&sh.full[s]);
                 if (q >= S) ok = __all_sync(0xffffffffu, wait(smem_u32(&sh.empty[s]), (q / S - 1) & 1u));
                 if (!ok) break;
-                const bool rows = p1 || g.base;
+                const bool from_rows = p1 || g.base;
                 const bool b_tile = p1 ? kBack : !kBack;  // this phase's weights: a tile of B, else of A
                 if (lane == 0) {
                     const uint32_t w = b_tile ? (g.hand ? 0u : kBBytes) : kABytes;
-                    mbar_arrive_expect_tx(fb, (rows ? ubytes : 0u) + w);
+                    mbar_arrive_expect_tx(fb, (from_rows ? ubytes : 0u) + w);
                 }
                 __syncwarp();
                 const int x = (p1 ? ka + j : na + j - nk) * kKC;
-                if (rows) {
-                    if (box) {
-                        if (lane == 0) tma_load_2d(st, p1 ? &map_u : &map_base, x, t.tok0, fb);
-                    } else if (lane < groups) {
-                        tma_gather4(st + lane * 512, p1 ? &map_u1 : &map_base1, x, y, fb);
-                    }
+                if (from_rows) {
+                    const CUtensorMap* m = p1 ? maps.u : maps.base;
+                    if (rows.mode >= 0 && rows.mode < 3) tma_load_2d(st + lane * 512, m + rows.mode, x, rows.y[0], fb);
+                    else if (rows.mode == 3) tma_gather4(st + lane * 512, m + 3, x, rows.y, fb);
                 }
                 if (lane == 0) {
                     if (!b_tile) {
-                        tma_load_3d(st + kUBytes, &map_a, x, 0, t.adapter, fb);
+                        tma_load_3d(st + kUBytes, &maps.a, x, 0, t.adapter, fb);
                     } else if (!g.hand) {
 #pragma unroll
                         for (int b = 0; b < Cfg::kBlocks; ++b)
-                            tma_load_3d(st + kUBytes + b * 8192, &map_b, b * 64, x, t.adapter, fb);
+                            tma_load_3d(st + kUBytes + b * 8192, &maps.b, b * 64, x, t.adapter, fb);
                     }
                 }
                 if (g.hand) {
@@ -437,6 +476,12 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
                         fence_proxy_async_smem();
                     }
                     cp_async_arrive(fb);
+                }
+                // keep base coming while P is summed: a window of kAhead chunks behind the ring
+                if (g.base && nn > 0 && (rows.mode == 0 || rows.mode == 1) && j >= nk - 1) {
+                    const int first = j == nk - 1 ? S : j - nk + S + kAhead;
+                    for (int i = first; i < min(nn, j - nk + 1 + S + kAhead); ++i)
+                        tma_prefetch_2d(&maps.base[rows.mode], (na + i) * kKC, rows.y[0]);
                 }
             }
         }
@@ -463,7 +508,8 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
                                                   : tc::smem_desc_sw128(st + kUBytes + kk * 32, 16, 1024);
                         tc::mma_f16(tmem, ad, bd, kIdesc1, (j > 0 || kk > 0) ? 1u : 0u);
                     }
-                    tc::mma_commit(smem_u32(&sh.empty[s]));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tc::mma_commit(smem_u32(&sh.empty[s]));
                 }
                 if (!ok) break;
                 tc::mma_commit(smem_u32(&sh.d1));
@@ -499,28 +545,29 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
         __syncwarp();
     } else {
         // ---------------- P, then O
-        // A row has two threads, each with half of the columns of P and of a chunk of O.
-        const int quarter = warp & 3, half = (warp - 2) >> 2, row = quarter * 32 + lane, et = tid - 64;
+        // While P is summed a row has two threads, each with half of its columns.
+        const int quarter = warp & 3, grp = (warp - 2) >> 2, row = quarter * 32 + lane, et = tid - 64;
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
-        const int own = kLoraTile / C;  // rows that this rank sums: [crank * own, ...)
+        const int own = kLoraTile >> clog;  // rows that this rank sums: [crank * own, ...)
         uint32_t q = 0, n2 = 0, tt = 0;
         for (int it = cid; it < ntiles; it += ncl, ++tt) {
             const LoraTile t = it == cid ? tile0 : g.v.tiles[it];
-            const bool full = t.rows == kLoraTile && t.tok0 >= 0, mine = row < t.rows;
-            const int64_t tok = mine ? g.v.order[t.pos0 + row] : 0;
+            const int tok = g.v.order[t.pos0 + min(row, t.rows - 1)];
+            const int tok_first = __shfl_sync(0xffffffffu, tok, 0);
+            const bool run32 = __all_sync(0xffffffffu, row < t.rows && tok == tok_first + lane);
             const float s = g.scale_all * (g.scale ? g.scale[t.adapter] : 1.f);
             q += nk;
             {
-                // Each rank sends its partial rows to the ranks that sum them: slot (source rank,
-                // row) of `own` rows each, 16-byte pieces permuted by row against bank conflicts.
+                // Each rank sends its partial rows to the ranks that sum them, a slot per source.
                 float p[RP / 2];
                 wait(smem_u32(&sh.d1), tt & 1u);
+                __syncwarp();  // (waits end lane by lane; what follows is for the whole warp)
                 tc::fence_after_sync();
                 if (nk > 0) {
                     constexpr int kLd = RP / 2 < 32 ? RP / 2 : 32;
 #pragma unroll
                     for (int c = 0; c < RP / 2 / kLd; ++c)
-                        tmem_load<kLd>(lane_addr + half * (RP / 2) + c * kLd, p + c * kLd);
+                        tmem_load<kLd>(lane_addr + grp * (RP / 2) + c * kLd, p + c * kLd);
                 } else {
 #pragma unroll
                     for (int j = 0; j < RP / 2; ++j) p[j] = 0.f;
@@ -528,15 +575,17 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
                 tc::fence_before_sync();
                 // every rank is done with the last tile's parts of P, whose place the sums take
                 if (tt > 0) wait.cluster(smem_u32(&sh.freed), (tt - 1) & 1u);
-                const uint32_t dst = cluster_map(hbase + (crank * own + row % own) * (RP * 4), row / own);
+                __syncwarp();
+                const uint32_t dst = cluster_map(hbase + crank * own * (RP * 4), row >> (7 - clog));
 #pragma unroll
                 for (int c = 0; c < RP / 8; ++c)
-                    st_cluster_f4(dst + (uint32_t)p_piece<RP>(row, half * (RP / 8) + c) * 16,
+                    st_cluster_f4(dst + (uint32_t)p_place<RP>(row & (own - 1), grp * (RP / 8) + c, own) * 16,
                                   make_float4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]));
             }
             named_barrier(1, kEpi);
             if (et < C) mbar_arrive_remote(smem_u32(&sh.pub), et);
             wait.cluster(smem_u32(&sh.pub), tt & 1u);
+            __syncwarp();
             // Sums in rank order: eight columns of one row per thread and step.
             constexpr int kG = RP / 8, kSteps = kLoraTile * kG / kEpi;
             float x[kSteps][8];
@@ -548,10 +597,10 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
                 for (int c = 0; c < C; ++c) {
-                    const uint32_t from = hbase + (c * own + rl) * (RP * 4);
+                    const uint32_t from = hbase + c * own * (RP * 4);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint4 v = ld_shared_v4(from + (uint32_t)p_piece<RP>(rl, 2 * c8 + h) * 16);
+                        const uint4 v = ld_shared_v4(from + (uint32_t)p_place<RP>(rl, 2 * c8 + h, own) * 16);
                         x[i][4 * h] += __uint_as_float(v.x);
                         x[i][4 * h + 1] += __uint_as_float(v.y);
                         x[i][4 * h + 2] += __uint_as_float(v.z);
@@ -573,6 +622,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
                 }
             }
             wait.cluster(smem_u32(&sh.read), tt & 1u);  // every rank has read its slots
+            __syncwarp();
             // The two parts of s P go to every rank.
 #pragma unroll
             for (int i = 0; i < kSteps; ++i) {
@@ -605,56 +655,81 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_u, co
             named_barrier(1, kEpi);
             if (et < C) mbar_arrive_remote(smem_u32(&sh.h), et);
             wait.cluster(smem_u32(&sh.h), tt & 1u);
+            __syncwarp();
             const float down = kF16 ? sh.down[row] : 1.f;
 
+            // Chunks of O, in turns between the two groups of four warps (thread = row): the steps of
+            // one chunk depend on each other, so two are under way at a time.
+            int held = -1;  // the stage whose store may still be reading it
             for (int j = 0; j < nn; ++j, ++q, ++n2) {
-                const uint32_t sl = q % S, st = sbase + sl * Cfg::kStage, b = n2 & 1u;
-                const int n0 = (na + j) * kKC + half * 32;
-                bool ok = wait(smem_u32(&sh.full[sl]), (q / S) & 1u);
-                uint4 y[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    y[c] = g.base ? ld_shared_v4(st + tc::sw128_off(row, half * 4 + c)) : make_uint4(0, 0, 0, 0);
-                ok = wait(smem_u32(&sh.d2_full[b]), (n2 / 2) & 1u) && ok;
-                tc::fence_after_sync();
-                float o[32];
-                tmem_load<32>(lane_addr + 128 + b * 64 + half * 32, o);
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.d2_empty[b]));
-                T* dst = static_cast<T*>(g.O) + tok * g.ldo + n0;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float f[8];
-                    Elt<T>::unpack(y[c], f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = kF16 ? fmaf(o[c * 8 + e], down, f[e]) : f[e] + o[c * 8 + e];
-                    const uint4 w = Elt<T>::pack(f);
-                    if (full) st_shared_v4(st + tc::sw128_off(row, half * 4 + c), w);
-                    else if (ok && mine && n0 + c * 8 < g.N) *reinterpret_cast<uint4*>(dst + c * 8) = w;
+                if ((int)(n2 & 1u) != grp) continue;
+                const uint32_t sl = q % S, st = sbase + sl * Cfg::kStage;
+                const int n0 = (na + j) * kKC;
+                if (lane == 0 && held >= 0) {
+                    bulk_wait_read<0>();
+                    mbar_arrive(smem_u32(&sh.empty[held]));
                 }
-                if (full) fence_proxy_async_smem();
-                named_barrier(1, kEpi);  // the stage's tile is finished (full) or has been read
-                if (et == 0) {
-                    if (full) {
-                        if (!sh.failed) tma_store_2d(&map_o, n0, t.tok0, st);
-                        bulk_commit();
-                        // the store before this one has been read out: its stage is free
-                        bulk_wait_read<1>();
-                        if (j > 0) mbar_arrive(smem_u32(&sh.empty[(q - 1) % S]));
-                        if (j == nn - 1) {
-                            bulk_wait_read<0>();
-                            mbar_arrive(smem_u32(&sh.empty[sl]));
-                        }
-                    } else {
-                        mbar_arrive(smem_u32(&sh.empty[sl]));
+                bool ok = wait(smem_u32(&sh.full[sl]), (q / S) & 1u);
+                ok = wait(smem_u32(&sh.d2_full[grp]), (n2 / 2) & 1u) && ok;
+                __syncwarp();
+                tc::fence_after_sync();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float o[32];
+                    tmem_load<32>(lane_addr + 128 + grp * 64 + h * 32, o);
+                    if (h == 1) {
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sh.d2_empty[grp]));
+                    }
+                    uint4 y[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        y[c] = g.base ? ld_shared_v4(st + tc::sw128_off(row, h * 4 + c)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float f[8];
+                        Elt<T>::unpack(y[c], f);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            f[e] = kF16 ? fmaf(o[c * 8 + e], down, f[e]) : f[e] + o[c * 8 + e];
+                        st_shared_v4(st + tc::sw128_off(row, h * 4 + c), Elt<T>::pack(f));
                     }
                 }
+                // A warp's 32 rows leave together: by one TMA store where their tokens are consecutive
+                // (drained while the warp goes on), else as rows of 128 bytes by eight lanes each.
+                if (run32) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (ok) tma_store_2d(&maps.o, n0, tok, st + quarter * 4096);
+                        bulk_commit();
+                    }
+                    held = (int)sl;
+                } else {
+                    __syncwarp();
+                    const int c = lane & 7;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = quarter * 32 + i * 4 + (lane >> 3);
+                        const int to = __shfl_sync(0xffffffffu, tok, i * 4 + (lane >> 3));
+                        if (ok && r < t.rows && n0 + c * 8 < g.N)
+                            *reinterpret_cast<uint4*>(static_cast<T*>(g.O) + (int64_t)to * g.ldo + n0 + c * 8) =
+                                ld_shared_v4(st + tc::sw128_off(r, c));
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[sl]));
+                }
             }
+            if (lane == 0 && held >= 0) {
+                bulk_wait_read<0>();
+                mbar_arrive(smem_u32(&sh.empty[held]));
+            }
+            named_barrier(1, kEpi);
             // this rank's products with P's parts are complete (their accumulators were read)
             if (et < C) mbar_arrive_remote(smem_u32(&sh.freed), et);
         }
-        if (et == 0) bulk_wait<0>();
+        if (lane == 0) bulk_wait<0>();
         // tokens without an adapter: O = base, P = 0
         const bool copy = g.O && (g.O != g.base);
         if (copy || g.P) {
@@ -905,6 +980,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
         }
         wait(smem_u32(&sh.done), 0);
+        __syncwarp();
         tc::fence_after_sync();
         // partial sums [j][256 columns] over the ring, which nothing uses any more
         const int quarter = warp & 3, row = quarter * 32 + lane;
@@ -1026,23 +1102,21 @@ cudaError_t run_tiles(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) 
     cudaError_t e = allow_smem(kern, Cfg::kSmem, done);
     if (e != cudaSuccess) return e;
     constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-    CUtensorMap mu, mu1, ma, mb, mbase, mbase1, mo;
+    TileMaps m;
     const int64_t in = kBack ? a.N : a.K, out = kBack ? a.K : a.N;
     const int64_t sa[3] = {in, a.rank, v.n}, ta[2] = {in, in * a.rank};
     const int64_t sb[3] = {a.rank, out, v.n}, tb[2] = {a.rank, out * a.rank};
     TileArgs g;
     g.hand = a.rank % 8 != 0;
-    bool ok = encode_rows(&mu, bf, a.U, v.tokens, a.K, a.ldu, kLoraTile) &&
-              encode_rows(&mu1, bf, a.U, v.tokens, a.K, a.ldu, 1) && encode(&ma, bf, a.A, 3, sa, ta, RP);
-    mb = ma;  // unused maps are valid ones
-    mbase = mu;
-    mbase1 = mu1;
-    mo = mu;
-    if (!g.hand) ok = ok && encode(&mb, bf, a.B, 3, sb, tb, 64);
-    if (a.O && a.base)
-        ok = ok && encode_rows(&mbase, bf, a.base, v.tokens, a.N, a.ldb, kLoraTile) &&
-             encode_rows(&mbase1, bf, a.base, v.tokens, a.N, a.ldb, 1);
-    if (a.O) ok = ok && encode_rows(&mo, bf, a.O, v.tokens, a.N, a.ldo, kLoraTile);
+    bool ok = encode(&m.a, bf, a.A, 3, sa, ta, RP);
+    m.b = m.o = m.a;  // maps that are not used are valid ones
+    if (!g.hand) ok = ok && encode(&m.b, bf, a.B, 3, sb, tb, 64);
+    for (int i = 0; i < kBoxes; ++i) {
+        ok = ok && encode_rows(&m.u[i], bf, a.U, v.tokens, a.K, a.ldu, kBoxRows[i]);
+        m.base[i] = m.u[i];
+        if (a.O && a.base) ok = ok && encode_rows(&m.base[i], bf, a.base, v.tokens, a.N, a.ldb, kBoxRows[i]);
+    }
+    if (a.O) ok = ok && encode_rows(&m.o, bf, a.O, v.tokens, a.N, a.ldo, 32);
     if (!ok) return cudaErrorInvalidValue;
     g.v = v;
     g.B = a.B;
@@ -1062,7 +1136,7 @@ cudaError_t run_tiles(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) 
     int c = 1;
     while (c < 8 && cap * c * 2 <= slots + slots / 8) c *= 2;
     const int64_t clusters = max64(1, min64(cap, slots / c));
-    return launch_clusters(kern, clusters, c, kTileThreads, Cfg::kSmem, s, g, mu, mu1, ma, mb, mbase, mbase1, mo);
+    return launch_clusters(kern, clusters, c, kTileThreads, Cfg::kSmem, s, g, m);
 }
 
 template <typename T, int RP>
