@@ -51,13 +51,6 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-// L2 prefetch of a 2-D box: no shared memory, no completion.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int x, int y) {
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y)
-                 : "memory");
-}
-
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),
@@ -280,7 +273,6 @@ __device__ __forceinline__ void load_b_tile(uint32_t dst, const T* W, int64_t ro
 // half of the columns).
 constexpr int kTileThreads = 320;
 constexpr int kEpi = 256;
-constexpr int kAhead = 8;  // chunks of rows that L2 prefetches run ahead of the ring
 constexpr uint32_t kTileBars = 1024;  // barriers, flags and row factors, behind the stages and P
 
 template <int RP>
@@ -293,6 +285,7 @@ struct TileCfg {
     static constexpr uint32_t kH = (2 * RP + 63) / 64 * kUBytes;
     static_assert(kH >= RP * 512u, "the partial sums fit");
     static constexpr int kPerSm = RP > 64 ? 1 : 2;
+    static constexpr int kMinCluster = kLoraTile * RP / 8 / kEpi;
     // Dynamic shared memory per CTA: all of the SM's 228 KB but 1 KB that the system keeps per CTA.
     static constexpr uint32_t kBudget = (228 * 1024) / kPerSm - 1024;
     static constexpr int kStages = (int)((kBudget - kTileBars - kH) / kStage);
@@ -354,7 +347,7 @@ __device__ __forceinline__ RowSource row_source(const LoraTile& t, const int32_t
 // fp32 partial P are sent through distributed shared memory to the rank that owns the row, which
 // adds them in rank order and sends the two 16-bit parts back to all; and rank c forms a share of
 // the 64-column chunks of O. One ring of stages carries both phases, so the loads of base run
-// ahead while P is being summed (and L2 prefetches further ahead): a stage holds a 128 x 64 tile
+// ahead while P is being summed: a stage holds a 128 x 64 tile
 // of U with a tile of W1, then a 128 x 64 tile of base, in which O is formed in place, with a tile
 // of W2.
 template <typename T, bool kBack, int RP>
@@ -440,8 +433,6 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
             const LoraTile t = it == cid ? tile0 : g.v.tiles[it];
             const RowSource rows = row_source(t, g.v.order, lane);
             const uint32_t ubytes = (uint32_t)((t.rows + 3) / 4) * 512u;
-            if (rows.mode == 0 || rows.mode == 1)  // what the ring cannot hold yet is fetched to L2
-                for (int j = S; j < min(nk, S + kAhead); ++j) tma_prefetch_2d(&maps.u[rows.mode], (ka + j) * kKC, rows.y[0]);
             for (int j = 0; j < nk + nn; ++j, ++q) {
                 const bool p1 = j < nk;
                 const uint32_t s = q % S, st = sbase + s * Cfg::kStage, fb = smem_u32(&sh.full[s]);
@@ -476,12 +467,6 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
                         fence_proxy_async_smem();
                     }
                     cp_async_arrive(fb);
-                }
-                // keep base coming while P is summed: a window of kAhead chunks behind the ring
-                if (g.base && nn > 0 && (rows.mode == 0 || rows.mode == 1) && j >= nk - 1) {
-                    const int first = j == nk - 1 ? S : j - nk + S + kAhead;
-                    for (int i = first; i < min(nn, j - nk + 1 + S + kAhead); ++i)
-                        tma_prefetch_2d(&maps.base[rows.mode], (na + i) * kKC, rows.y[0]);
                 }
             }
         }
@@ -586,63 +571,54 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
             if (et < C) mbar_arrive_remote(smem_u32(&sh.pub), et);
             wait.cluster(smem_u32(&sh.pub), tt & 1u);
             __syncwarp();
-            // Sums in rank order: eight columns of one row per thread and step.
-            constexpr int kG = RP / 8, kSteps = kLoraTile * kG / kEpi;
-            float x[kSteps][8];
-            const int groups = own * kG;  // a multiple of 32
+            // Sums in rank order: eight columns of one row per thread (the cluster is large enough).
+            constexpr int kG = RP / 8;
+            const bool sums = et < own * kG;  // the same for a whole warp
+            const int rl = et / kG, c8 = et % kG, r = crank * own + rl;
+            float x[8];
+            if (sums) {
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int idx = et + i * kEpi, rl = idx / kG, c8 = idx % kG;
-                if (idx >= groups) continue;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
+                for (int e = 0; e < 8; ++e) x[e] = 0.f;
+#pragma unroll 4
                 for (int c = 0; c < C; ++c) {
                     const uint32_t from = hbase + c * own * (RP * 4);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint4 v = ld_shared_v4(from + (uint32_t)p_place<RP>(rl, 2 * c8 + h, own) * 16);
-                        x[i][4 * h] += __uint_as_float(v.x);
-                        x[i][4 * h + 1] += __uint_as_float(v.y);
-                        x[i][4 * h + 2] += __uint_as_float(v.z);
-                        x[i][4 * h + 3] += __uint_as_float(v.w);
+                        x[4 * h] += __uint_as_float(v.x);
+                        x[4 * h + 1] += __uint_as_float(v.y);
+                        x[4 * h + 2] += __uint_as_float(v.z);
+                        x[4 * h + 3] += __uint_as_float(v.w);
                     }
                 }
             }
             named_barrier(1, kEpi);
             if (et < C) mbar_arrive_remote(smem_u32(&sh.read), et);
-            if (g.P) {
+            if (g.P && sums && r < t.rows) {
+                float* to = g.P + (int64_t)g.v.order[t.pos0 + r] * g.rank + c8 * 8;
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    const int idx = et + i * kEpi, r = crank * own + idx / kG, c8 = idx % kG;
-                    if (idx >= groups || r >= t.rows) continue;
-                    float* to = g.P + (int64_t)g.v.order[t.pos0 + r] * g.rank + c8 * 8;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (c8 * 8 + e < g.rank) to[e] = x[i][e];
-                }
+                for (int e = 0; e < 8; ++e)
+                    if (c8 * 8 + e < g.rank) to[e] = x[e];
             }
             wait.cluster(smem_u32(&sh.read), tt & 1u);  // every rank has read its slots
             __syncwarp();
             // The two parts of s P go to every rank.
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) {
-                const int idx = et + i * kEpi, r = crank * own + idx / kG, c8 = idx % kG;
-                if (idx >= groups) continue;  // the same for a whole warp
+            if (sums) {
                 float m = 0.f, up = 1.f, down = 1.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[i][e] *= s;
-                    m = fmaxf(m, fabsf(x[i][e]));
+                    x[e] *= s;
+                    m = fmaxf(m, fabsf(x[e]));
                 }
                 if (kF16) {  // the row's pieces lie in kG neighbouring lanes
 #pragma unroll
                     for (int d = kG / 2; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
                     pow2_scale(m, up, down);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[i][e] *= up;
+                    for (int e = 0; e < 8; ++e) x[e] *= up;
                 }
                 uint4 hi, lo;
-                split8<T>(x[i], hi, lo);
+                split8<T>(x, hi, lo);
                 const uint32_t at_hi = hbase + (c8 >> 3) * kUBytes + tc::sw128_off(r, c8 & 7);
                 const uint32_t at_lo = hbase + ((c8 + kG) >> 3) * kUBytes + tc::sw128_off(r, (c8 + kG) & 7);
                 for (int c = 0; c < C; ++c) {
@@ -1133,7 +1109,8 @@ cudaError_t run_tiles(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) 
     g.err = device_error_word();
     const int64_t slots = (int64_t)device_props().sm_count * Cfg::kPerSm;
     const int64_t cap = lora_tiles_cap(v.tokens, v.n, kLoraTile);
-    int c = 1;
+    // As many CTAs per tile as fill the SMs, and enough that a thread sums eight columns at most.
+    int c = Cfg::kMinCluster;
     while (c < 8 && cap * c * 2 <= slots + slots / 8) c *= 2;
     const int64_t clusters = max64(1, min64(cap, slots / c));
     return launch_clusters(kern, clusters, c, kTileThreads, Cfg::kSmem, s, g, m);
