@@ -733,42 +733,44 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
 // Warps: 0 loads U (TMA), 1 multiplies (one thread), 2 to 5 write P's parts into the stages.
 constexpr int kWgThreads = 192;
 constexpr int kWgEpi = 128;
-constexpr int kWgCols = 256;  // columns of U per cluster: two accumulators of 128
-constexpr int kWgMaxStages = 4;
+constexpr int kWgCols = 128;  // columns of U per cluster (the M of the products)
+constexpr uint32_t kWgBars = 512;
 
 template <int RP>
 struct WgCfg {
-    static constexpr int kBlocks = (RP + 63) / 64;
-    static constexpr uint32_t kU = kWgCols / 64 * 8192;        // 64 tokens x 256 columns, 64-column blocks
-    static constexpr uint32_t kPart = kBlocks * 8192;           // 64 tokens x RP of one part of P
-    static constexpr uint32_t kStage = kU + 2 * kPart;
-    static constexpr uint32_t kBudget = 227 * 1024;
-    static constexpr int kFit = (int)((kBudget - kTileBars) / kStage);
-    static constexpr int kStages = kFit < kWgMaxStages ? kFit : kWgMaxStages;
-    static constexpr uint32_t kSmem = kStages * kStage + kTileBars;
-    static constexpr uint32_t kTmem = 2 * RP < 32 ? 32 : 2 * RP;  // a power of two
+    static constexpr uint32_t kU = kWgCols / 64 * 8192;  // 64 tokens x 128 columns, 64-column blocks
+    // 64 tokens x RP of each part of P in 64-column blocks of 8 KB: up to rank 32 both parts share
+    // a block (hi in its first 32 columns, lo in the others), else a part has blocks of its own.
+    static constexpr uint32_t kLo = RP <= 32 ? 64 : RP * 128;  // bytes from hi to lo
+    static constexpr uint32_t kP = RP <= 32 ? 8192 : RP * 256;
+    static constexpr uint32_t kStage = kU + kP;
+    static constexpr int kPerSm = RP <= 32 ? 3 : 2;
+    static constexpr uint32_t kBudget = (228 * 1024) / kPerSm / 1024 * 1024 - 1024;
+    static constexpr int kStages = (int)((kBudget - kWgBars) / kStage);
+    static constexpr uint32_t kSmem = kStages * kStage + kWgBars;
+    static constexpr uint32_t kTmem = RP < 32 ? 32 : RP;  // a power of two
     static_assert(kStages >= 2 && kStages * kStage >= RP * kWgCols * 4u, "the partial sums fit in the ring");
 };
 
 struct WgArgs {
     LoraPlanView v;
     LoraWgradArgs w[2];
-    int blocks[2];  // 256-column blocks of each product
+    int blocks[2];  // 128-column blocks of each product
     const float* scale;
     float scale_all;
     int32_t rank;
     int* err;
 };
 
-// A cluster takes 256 columns of one adapter's gradient; its CTAs split the adapter's tokens in
+// A cluster takes 128 columns of one adapter's gradient; its CTAs split the adapter's tokens in
 // chunks of 64 and their fp32 partial sums are added in rank order through distributed shared
-// memory. U's rows are the K axis: a chunk is 64 rows x 256 columns, an MN-major operand just as
+// memory. U's rows are the K axis: a chunk is 64 rows x 128 columns, an MN-major operand just as
 // TMA writes it (boxes of 64 columns; four rows at a time where the tokens are not consecutive).
 // Rows past the adapter's last token are asked for beyond the tensor, which fills zeros. P is
 // read in fp32 and written to the stage as its two parts by the four warps that later drain the
 // accumulators.
 template <typename T, int RP>
-__global__ void __launch_bounds__(kWgThreads, 1)
+__global__ void __launch_bounds__(kWgThreads, WgCfg<RP>::kPerSm)
 lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, const __grid_constant__ CUtensorMap map_g0,
                   const __grid_constant__ CUtensorMap map_u1, const __grid_constant__ CUtensorMap map_g1) {
     using Cfg = WgCfg<RP>;
@@ -782,7 +784,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
         volatile int failed;
         float warp_max[4];
     };
-    static_assert(sizeof(Shared) <= kTileBars, "barriers");
+    static_assert(sizeof(Shared) <= kWgBars, "barriers");
     Shared& sh = *reinterpret_cast<Shared*>(smem_raw + S * Cfg::kStage);
     const uint32_t sbase = smem_u32(smem_raw);
     if (sbase & 1023u) {  // the same on every CTA
@@ -830,7 +832,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             const int s = j % S;
             const uint32_t st = sbase + s * Cfg::kStage, fb = smem_u32(&sh.full[s]);
             const int b = pa + j * 64, m = min(64, pe - b);
-            // lane = 4 tokens (group lane % 16) and two of the four 64-column blocks
+            // lane = 4 tokens (group lane % 16) and one of the two 64-column blocks
             int y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -845,11 +847,8 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             if (box) {
                 if (lane < kWgCols / 64) tma_load_2d(st + lane * 8192, mu, n0 + lane * 64, first, fb);
             } else {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int c = (lane >> 4) * 2 + i;
-                    tma_gather4(st + c * 8192 + (lane & 15) * 512, mg, n0 + c * 64, y, fb);
-                }
+                const int c = lane >> 4;
+                tma_gather4(st + c * 8192 + (lane & 15) * 512, mg, n0 + c * 64, y, fb);
             }
         }
         if (sh.failed) {
@@ -867,13 +866,11 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint64_t ad = tc::smem_desc_sw128(st + m * 16384 + kk * 2048, 8192, 1024);
-                            const uint64_t bd = tc::smem_desc_sw128(st + Cfg::kU + h * Cfg::kPart + kk * 2048, 8192, 1024);
-                            tc::mma_f16(tmem + m * RP, ad, bd, kIdesc, (j > 0 || kk > 0 || h > 0) ? 1u : 0u);
-                        }
+                    for (int h = 0; h < 2; ++h) {
+                        const uint64_t ad = tc::smem_desc_sw128(st + kk * 2048, 8192, 1024);
+                        const uint64_t bd = tc::smem_desc_sw128(st + Cfg::kU + h * Cfg::kLo + kk * 2048, 8192, 1024);
+                        tc::mma_f16(tmem, ad, bd, kIdesc, (j > 0 || kk > 0 || h > 0) ? 1u : 0u);
+                    }
                 tc::mma_commit(smem_u32(&sh.empty[s]));
             }
             tc::mma_commit(smem_u32(&sh.done));
@@ -905,16 +902,34 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
                 for (int i = 0; i < 8; ++i) x[i] = j0 + i < r ? src[i] : 0.f;
             }
         };
-        constexpr int kCh = RP / 8;         // 8-column pieces per token
+        constexpr int kCh = RP / 8;            // 8-column pieces per token
         constexpr int kPer = 64 * kCh / kWgEpi;  // pieces per thread of a chunk
-        float up = 1.f;
-        if (kF16) {  // the largest magnitude among this CTA's tokens
-            float m = 0.f;
-            for (int64_t i = et; i < (int64_t)(pe - pa) * kCh; i += kWgEpi) {
-                float x[8];
-                load8(g.v.order[pa + i / kCh], (int)(i % kCh) * 8, x);
+        auto piece_token = [&](int j, int i) {  // the token of this thread's piece i of chunk j, -1: none
+            const int at = pa + j * 64 + (et + i * kWgEpi) / kCh;
+            return at < pe ? g.v.order[at] : -1;
+        };
+        auto load_piece = [&](int tok, int i, float* x) {
+            if (tok >= 0) {
+                load8(tok, (et + i * kWgEpi) % kCh * 8, x);
+            } else {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+                for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            }
+        };
+        float up = 1.f;
+        if (kF16) {  // the largest magnitude among this CTA's tokens, four pieces at a time
+            float m = 0.f;
+            for (int j = 0; j < nc * kPer; j += 4) {
+                int tok[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tok[i] = piece_token((j + i) / kPer, (j + i) % kPer);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x[8];
+                    load_piece(tok[i], (j + i) % kPer, x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+                }
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -923,21 +938,24 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             m = fmaxf(fmaxf(sh.warp_max[0], sh.warp_max[1]), fmaxf(sh.warp_max[2], sh.warp_max[3]));
             pow2_scale(m, up, down);
         }
+        // The next chunk's values, and the tokens of the one after, are on their way while a chunk
+        // is written.
+        float x[kPer][8];
+        int tok[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) tok[i] = nc > 0 ? piece_token(0, i) : -1;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) load_piece(tok[i], i, x[i]);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) tok[i] = nc > 1 ? piece_token(1, i) : -1;
         for (int j = 0; j < nc; ++j) {
             const int s = j % S;
             const uint32_t st = sbase + s * Cfg::kStage + Cfg::kU;
-            const int b = pa + j * 64, m = min(64, pe - b);
-            float x[kPer][8];
+            float xn[kPer][8];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int at = (et + i * kWgEpi) / kCh, c = (et + i * kWgEpi) % kCh;
-                if (at < m) {
-                    load8(g.v.order[b + at], c * 8, x[i]);
-                } else {
+            for (int i = 0; i < kPer; ++i) load_piece(tok[i], i, xn[i]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-                }
-            }
+            for (int i = 0; i < kPer; ++i) tok[i] = piece_token(j + 2, i);
             if (j >= S) wait(smem_u32(&sh.empty[s]), (j / S - 1) & 1u);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
@@ -947,34 +965,36 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
                     for (int e = 0; e < 8; ++e) x[i][e] *= up;
                 uint4 hi, lo;
                 split8<T>(x[i], hi, lo);
-                const uint32_t o = st + (c >> 3) * 8192 + tc::sw128_off(at, c & 7);
-                st_shared_v4(o, hi);
-                st_shared_v4(o + Cfg::kPart, lo);
+                const uint32_t o = st + (c >> 3) * 8192;
+                st_shared_v4(o + tc::sw128_off(at, c & 7), hi);
+                if (RP <= 32) st_shared_v4(o + tc::sw128_off(at, 4 + c), lo);
+                else st_shared_v4(o + Cfg::kLo + tc::sw128_off(at, c & 7), lo);
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[i][e] = xn[i][e];
         }
         wait(smem_u32(&sh.done), 0);
         __syncwarp();
         tc::fence_after_sync();
-        // partial sums [j][256 columns] over the ring, which nothing uses any more
+        // partial sums [j][128 columns] over the ring, which nothing uses any more
         const int quarter = warp & 3, row = quarter * 32 + lane;
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int c = 0; c < RP / 16; ++c) {
+            float y[16];
+            if (nc > 0) {
+                tmem_load<16>(tmem + ((uint32_t)(quarter * 32) << 16) + c * 16, y);
+            } else {
 #pragma unroll
-            for (int c = 0; c < RP / 16; ++c) {
-                float x[16];
-                if (nc > 0) {
-                    tmem_load<16>(tmem + ((uint32_t)(quarter * 32) << 16) + m * RP + c * 16, x);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    st_shared_f32(sbase + ((c * 16 + i) * kWgCols + m * 128 + row) * 4, x[i] * down);
+                for (int i = 0; i < 16; ++i) y[i] = 0.f;
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) st_shared_f32(sbase + ((c * 16 + i) * kWgCols + row) * 4, y[i] * down);
+        }
         tc::fence_before_sync();
     }
     __syncthreads();
@@ -1146,7 +1166,8 @@ cudaError_t run_wgrad(const LoraWgradArgs* w, int nw, int32_t rank, const float*
     g.err = device_error_word();
     const int64_t items = (int64_t)v.n * (g.blocks[0] + g.blocks[1]);
     int c = 1;
-    while (c < 8 && items * c * 2 <= device_props().sm_count && (int64_t)v.tokens >= 64ll * c * 2) c *= 2;
+    const int64_t slots = (int64_t)device_props().sm_count * Cfg::kPerSm;
+    while (c < 8 && items * c * 2 <= slots && (int64_t)v.tokens >= 64ll * c * 2) c *= 2;
     if (items * c > 0x7fffffffll) return cudaErrorInvalidValue;
     return launch_clusters(kern, items, c, kWgThreads, Cfg::kSmem, s, g, mu[0], mg[0], mu[1], mg[1]);
 }
