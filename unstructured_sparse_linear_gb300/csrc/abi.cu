@@ -669,7 +669,8 @@ int spops_lora_grad(const void* dY, int64_t lddy, const void* X, int64_t ldx, co
     if (dX && !(dX_base == dX && (ldb == lddx || tokens == 1)) &&
         rows_overlap(dX, lddx, in_features, dX_base, ldb, in_features, tokens, es))
         return fail(SPOPS_ERR_INVALID_ARG, "dX overlaps dX_base without being it");
-    if (clash(dA, dA ? wa : 0) || clash(dB, dB ? wb : 0) || overlaps(dA, wa, X, xb) || overlaps(dA, wa, dY, dyb) ||
+    const size_t bb = dX && dX_base ? ((size_t)(tokens - 1) * ldb + in_features) * es : 0;
+    if (overlaps(dA, wa, dX_base, bb) || overlaps(dB, wb, dX_base, bb) || clash(dA, dA ? wa : 0) || clash(dB, dB ? wb : 0) || overlaps(dA, wa, X, xb) || overlaps(dA, wa, dY, dyb) ||
         overlaps(dB, wb, X, xb) || overlaps(dB, wb, dY, dyb))
         return fail(SPOPS_ERR_INVALID_ARG, "dA or dB overlaps another array");
     const size_t need = spops_lora_grad_workspace_size(tokens, rank);
@@ -714,6 +715,7 @@ int spops_lora_grad(const void* dY, int64_t lddy, const void* X, int64_t ldx, co
         w[nw].N = in_features;
         w[nw].P = dp;
         w[nw].G = dA;
+        w[nw].dependent = true;
         ++nw;
     }
     if (dB) {
@@ -726,7 +728,7 @@ int spops_lora_grad(const void* dY, int64_t lddy, const void* X, int64_t ldx, co
         ++nw;
     }
     if (nw == 0) return ok();
-    return cuda_status(launch_lora_wgrad(dtype, w, nw, rank, scale, scale_all, v, s), "lora_grad dA dB launch");
+    return cuda_status(launch_lora_wgrad(dtype, w, nw, rank, scale, scale_all, v, dX || dA, s), "lora_grad dA dB launch");
 }
 
 /* ---------------------------------------------------------------- gradient norm and clipping */

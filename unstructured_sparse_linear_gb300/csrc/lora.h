@@ -31,6 +31,7 @@ struct LoraPlanView {
     int32_t* tmp;     // [tokens] scratch of the sort
     int32_t* off;     // [n + 2]
     int32_t* tstart;  // [n + 2] scratch: first tile of each adapter
+    int32_t* aorder;  // [n] the adapters, those with the most tokens first
     LoraTile* tiles;
     LoraTile* small;
     int32_t tokens, n;
@@ -42,7 +43,7 @@ inline int64_t lora_tiles_cap(int32_t tokens, int32_t n, int rows) {
 inline size_t lora_words4(int64_t words) { return (size_t)((words + 3) / 4 * 4); }
 
 inline size_t lora_plan_bytes(int32_t tokens, int32_t n) {
-    return 4 * (kLoraHdr + 2 * lora_words4(tokens) + 2 * lora_words4((int64_t)n + 2)) +
+    return 4 * (kLoraHdr + 2 * lora_words4(tokens) + 3 * lora_words4((int64_t)n + 2)) +
            sizeof(LoraTile) * (size_t)(lora_tiles_cap(tokens, n, kLoraTile) + lora_tiles_cap(tokens, n, kLoraRows));
 }
 
@@ -54,7 +55,8 @@ inline LoraPlanView lora_plan_view(const void* plan, int32_t tokens, int32_t n) 
     v.tmp = v.order + lora_words4(tokens);
     v.off = v.tmp + lora_words4(tokens);
     v.tstart = v.off + lora_words4((int64_t)n + 2);
-    v.tiles = reinterpret_cast<LoraTile*>(v.tstart + lora_words4((int64_t)n + 2));
+    v.aorder = v.tstart + lora_words4((int64_t)n + 2);
+    v.tiles = reinterpret_cast<LoraTile*>(v.aorder + lora_words4((int64_t)n + 2));
     v.small = v.tiles + lora_tiles_cap(tokens, n, kLoraTile);
     v.tokens = tokens;
     v.n = n;
@@ -90,6 +92,7 @@ struct LoraWgradArgs {
     const float* P = nullptr;  // [tokens, rank]
     void* G = nullptr;         // [n, rank, N], or [n, N, rank] when rank_minor
     bool rank_minor = false;
+    bool dependent = false;  // P is written by the launch directly before (else by an earlier one)
 };
 
 cudaError_t launch_lora_plan(const int32_t* ids, const LoraPlanView& v, cudaStream_t s);
@@ -103,11 +106,12 @@ bool lora_tiles_ok(int dt, const LoraArgs& a, const LoraPlanView& v);
 cudaError_t launch_lora_tiles(int dt, bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s);
 bool lora_wgrad_tiles_ok(int dt, const LoraWgradArgs* w, int nw);
 cudaError_t launch_lora_wgrad_tiles(int dt, const LoraWgradArgs* w, int nw, int32_t rank, const float* scale,
-                                    float scale_all, const LoraPlanView& v, cudaStream_t s);
+                                    float scale_all, const LoraPlanView& v, bool pdl, cudaStream_t s);
 
-// Operators (the dispatch between the kernels).
+// Operators (the dispatch between the kernels). after_lora: launch_lora was the launch before
+// this one, on the same stream and in the same call.
 cudaError_t launch_lora(int dt, bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s);
 cudaError_t launch_lora_wgrad(int dt, const LoraWgradArgs* w, int nw, int32_t rank, const float* scale,
-                              float scale_all, const LoraPlanView& v, cudaStream_t s);
+                              float scale_all, const LoraPlanView& v, bool after_lora, cudaStream_t s);
 
 }  // namespace spops

@@ -152,6 +152,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1) lora_plan_kernel(const int32_
     __syncthreads();
     const int tiles = build_tiles(v, n, kLoraTile, v.tiles, s_warp);
     const int small = build_tiles(v, n + 1, kLoraRows, v.small, s_warp);
+    // the adapters by falling number of tokens (a rank by comparing all pairs; as they are where
+    // that would take long)
+    for (int a = tid; a < n; a += kPlanThreads) {
+        int at = a;
+        if (n <= 1024) {
+            const int c = v.off[a + 1] - v.off[a];
+            at = 0;
+            for (int b = 0; b < n; ++b) {
+                const int d = v.off[b + 1] - v.off[b];
+                at += d > c || (d == c && b < a);
+            }
+        }
+        v.aorder[at] = a;
+    }
     if (tid == 0) {
         v.counts[kLoraCntTiles] = tiles;
         v.counts[kLoraCntSmall] = small;

@@ -411,9 +411,9 @@ cudaError_t launch_lora(int dt, bool back, const LoraArgs& a, const LoraPlanView
 }
 
 cudaError_t launch_lora_wgrad(int dt, const LoraWgradArgs* w, int nw, int32_t rank, const float* scale,
-                              float scale_all, const LoraPlanView& v, cudaStream_t s) {
+                              float scale_all, const LoraPlanView& v, bool after_lora, cudaStream_t s) {
     if (v.tokens > 64 && lora_wgrad_tiles_ok(dt, w, nw))
-        return launch_lora_wgrad_tiles(dt, w, nw, rank, scale, scale_all, v, s);
+        return launch_lora_wgrad_tiles(dt, w, nw, rank, scale, scale_all, v, after_lora, s);
     return launch_lora_wgrad_rows(dt, w, nw, rank, scale, scale_all, v, s);
 }
 

@@ -76,6 +76,14 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) 
     return done != 0;
 }
 
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) { return __uint_as_float(ld_cluster_u32(addr)); }
 
 // Waits of one CTA. After one has run out of time (2 s) every later one of the CTA gives up at
@@ -417,6 +425,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
     __syncthreads();
     if (C > 1) cluster_sync();  // the other ranks' barriers are initialised
     tc::fence_after_sync();
+    pdl_trigger();  // (after the allocation of TMEM, which a dependent kernel's CTAs share)
     const uint32_t tmem = sh.tmem;
     const Waits wait{&sh.failed, g.err};
     const int nkc = (g.K + kKC - 1) / kKC, nnc = g.O ? (g.N + kKC - 1) / kKC : 0;
@@ -759,6 +768,7 @@ struct WgArgs {
     const float* scale;
     float scale_all;
     int32_t rank;
+    int pdl;  // launched as a programmatic dependent of the kernel that writes the dependent P
     int* err;
 };
 
@@ -795,10 +805,12 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
     const int C = (int)cluster_size(), crank = (int)cluster_rank();
     const int per = g.blocks[0] + g.blocks[1];
     const int item = blockIdx.x / C;
-    const int adapter = item / per, blk = item % per;
+    const int adapter = g.v.aorder[item / per], blk = item % per;  // the longest first
     const int which = blk >= g.blocks[0];
     const LoraWgradArgs& w = g.w[which];
     const int n0 = (which ? blk - g.blocks[0] : blk) * kWgCols;
+    // 16-byte stores of the gradient
+    const bool vec_out = (reinterpret_cast<uintptr_t>(w.G) & 15) == 0 && (!w.rank_minor || g.rank % 8 == 0);
     const int p0 = g.v.off[adapter], cnt = g.v.off[adapter + 1] - p0;
     const int chunks = (cnt + 63) / 64;
     const int ca = (int)((int64_t)chunks * crank / C), cb = (int)((int64_t)chunks * (crank + 1) / C);
@@ -821,6 +833,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
     const Waits wait{&sh.failed, g.err};
+    const bool dependent = g.pdl && w.dependent;
     float down = 1.f;  // what the parts of P were scaled by, inverted
 
     if (warp == 0) {
@@ -882,6 +895,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
         __syncwarp();
     } else {
         // ---------------- P's parts
+        if (dependent) pdl_wait();  // the kernel before this one writes this P
         const int et = tid - 64;
         const int r = g.rank;
         const bool vec = r % 4 == 0 && (reinterpret_cast<uintptr_t>(w.P) & 15) == 0;
@@ -917,19 +931,20 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             }
         };
         float up = 1.f;
-        if (kF16) {  // the largest magnitude among this CTA's tokens, four pieces at a time
+        if (kF16) {  // the largest magnitude among this CTA's tokens, eight pieces at a time (two
+                     // memory latencies: with four at a time this took a third of the kernel)
             float m = 0.f;
-            for (int j = 0; j < nc * kPer; j += 4) {
-                int tok[4];
+            for (int j = 0; j < nc * kPer; j += 8) {
+                int tok[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) tok[i] = piece_token((j + i) / kPer, (j + i) % kPer);
+                for (int i = 0; i < 8; ++i) tok[i] = piece_token((j + i) / kPer, (j + i) % kPer);
+                float x[8][8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float x[8];
-                    load_piece(tok[i], (j + i) % kPer, x);
+                for (int i = 0; i < 8; ++i) load_piece(tok[i], (j + i) % kPer, x[i]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
-                }
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[i][e]));
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
@@ -1000,21 +1015,63 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
     __syncthreads();
     if (C > 1) cluster_sync();
     {
-        // this rank's share of the columns, every sum in rank order
-        const int x0 = kWgCols * crank / C, nx = kWgCols * (crank + 1) / C - x0, r = g.rank;
+        // this rank's share of the columns, every sum in rank order, eight values at a time: of a
+        // row j (N is a multiple of 8), or of a column where the ranks are the contiguous axis
+        const int nx = kWgCols / C, x0 = nx * crank, r = g.rank;
         const float s = g.scale_all * (g.scale ? g.scale[adapter] : 1.f);
         T* G = static_cast<T*>(w.G) + (int64_t)adapter * r * w.N;
-        for (int i = tid; i < nx * r && !sh.failed; i += kWgThreads) {
-            const int x = x0 + (w.rank_minor ? i / r : i % nx), j = w.rank_minor ? i % r : i / nx;
-            if (n0 + x >= w.N) continue;
-            const uint32_t at = sbase + (j * kWgCols + x) * 4;
-            float sum = 0.f;
-            for (int c = 0; c < C; ++c) sum += ld_cluster_f32(cluster_map(at, c));
-            const T y = Elt<T>::from_f(sum * s);
-            if (w.rank_minor) G[(int64_t)(n0 + x) * r + j] = y;
-            else G[(int64_t)j * w.N + n0 + x] = y;
+        const int r8 = (r + 7) / 8, n8 = nx / 8;
+        const int items = sh.failed ? 0 : (w.rank_minor ? nx * r8 : r * n8);
+        for (int i = tid; i < items; i += kWgThreads) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = 0.f;
+            if (w.rank_minor) {
+                const int j0 = i / nx * 8, x = x0 + i % nx;
+                if (n0 + x >= w.N) continue;
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t from = cluster_map(sbase + (j0 * kWgCols + x) * 4, c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) y[e] += ld_cluster_f32(from + e * kWgCols * 4);  // (j < RP)
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] *= s;
+                T* to = G + (int64_t)(n0 + x) * r + j0;
+                if (vec_out) {
+                    *reinterpret_cast<uint4*>(to) = Elt<T>::pack(y);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (j0 + e < r) to[e] = Elt<T>::from_f(y[e]);
+                }
+            } else {
+                const int j = i / n8, x = x0 + i % n8 * 8;
+                if (n0 + x >= w.N) continue;
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t from = cluster_map(sbase + (j * kWgCols + x) * 4, c);
+                    const float4 a = ld_cluster_f4(from), b = ld_cluster_f4(from + 16);
+                    y[0] += a.x;
+                    y[1] += a.y;
+                    y[2] += a.z;
+                    y[3] += a.w;
+                    y[4] += b.x;
+                    y[5] += b.y;
+                    y[6] += b.z;
+                    y[7] += b.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] *= s;
+                T* to = G + (int64_t)j * w.N + n0 + x;
+                if (vec_out) {
+                    *reinterpret_cast<uint4*>(to) = Elt<T>::pack(y);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) to[e] = Elt<T>::from_f(y[e]);
+                }
+            }
         }
     }
+    if (g.pdl && !dependent) pdl_wait();  // so that the kernel before this one has ended when this one has
     __syncthreads();
     if (C > 1) cluster_sync();  // nobody reads this CTA's sums any more
     if (warp == 1) tc::tmem_dealloc(tmem, Cfg::kTmem);
@@ -1061,20 +1118,22 @@ bool rows_ok(const void* p, int64_t cols, int64_t ld) {
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t clusters, int c, int threads, uint32_t smem, cudaStream_t s,
-                            const Args&... args) {
+cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t clusters, int c, int threads, uint32_t smem, bool pdl,
+                            cudaStream_t s, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * c));
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)c;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = pdl ? 2 : 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     count_launches(1);
     return e;
@@ -1133,12 +1192,12 @@ cudaError_t run_tiles(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) 
     int c = Cfg::kMinCluster;
     while (c < 8 && cap * c * 2 <= slots + slots / 8) c *= 2;
     const int64_t clusters = max64(1, min64(cap, slots / c));
-    return launch_clusters(kern, clusters, c, kTileThreads, Cfg::kSmem, s, g, m);
+    return launch_clusters(kern, clusters, c, kTileThreads, Cfg::kSmem, false, s, g, m);
 }
 
 template <typename T, int RP>
 cudaError_t run_wgrad(const LoraWgradArgs* w, int nw, int32_t rank, const float* scale, float scale_all,
-                      const LoraPlanView& v, cudaStream_t s) {
+                      const LoraPlanView& v, bool pdl, cudaStream_t s) {
     using Cfg = WgCfg<RP>;
     static bool done[64];
     auto kern = lora_wgrad_kernel<T, RP>;
@@ -1163,22 +1222,23 @@ cudaError_t run_wgrad(const LoraWgradArgs* w, int nw, int32_t rank, const float*
     g.scale = scale;
     g.scale_all = scale_all;
     g.rank = rank;
+    g.pdl = pdl;
     g.err = device_error_word();
     const int64_t items = (int64_t)v.n * (g.blocks[0] + g.blocks[1]);
     int c = 1;
     const int64_t slots = (int64_t)device_props().sm_count * Cfg::kPerSm;
     while (c < 8 && items * c * 2 <= slots && (int64_t)v.tokens >= 64ll * c * 2) c *= 2;
     if (items * c > 0x7fffffffll) return cudaErrorInvalidValue;
-    return launch_clusters(kern, items, c, kWgThreads, Cfg::kSmem, s, g, mu[0], mg[0], mu[1], mg[1]);
+    return launch_clusters(kern, items, c, kWgThreads, Cfg::kSmem, pdl, s, g, mu[0], mg[0], mu[1], mg[1]);
 }
 
 template <typename T>
 cudaError_t run_wgrad_rank(const LoraWgradArgs* w, int nw, int32_t rank, const float* scale, float scale_all,
-                           const LoraPlanView& v, cudaStream_t s) {
-    if (rank <= 16) return run_wgrad<T, 16>(w, nw, rank, scale, scale_all, v, s);
-    if (rank <= 32) return run_wgrad<T, 32>(w, nw, rank, scale, scale_all, v, s);
-    if (rank <= 64) return run_wgrad<T, 64>(w, nw, rank, scale, scale_all, v, s);
-    return run_wgrad<T, 128>(w, nw, rank, scale, scale_all, v, s);
+                           const LoraPlanView& v, bool pdl, cudaStream_t s) {
+    if (rank <= 16) return run_wgrad<T, 16>(w, nw, rank, scale, scale_all, v, pdl, s);
+    if (rank <= 32) return run_wgrad<T, 32>(w, nw, rank, scale, scale_all, v, pdl, s);
+    if (rank <= 64) return run_wgrad<T, 64>(w, nw, rank, scale, scale_all, v, pdl, s);
+    return run_wgrad<T, 128>(w, nw, rank, scale, scale_all, v, pdl, s);
 }
 
 template <typename T, bool kBack>
@@ -1212,9 +1272,9 @@ bool lora_wgrad_tiles_ok(int dt, const LoraWgradArgs* w, int nw) {
 }
 
 cudaError_t launch_lora_wgrad_tiles(int dt, const LoraWgradArgs* w, int nw, int32_t rank, const float* scale,
-                                    float scale_all, const LoraPlanView& v, cudaStream_t s) {
-    return dt == kF16 ? run_wgrad_rank<__half>(w, nw, rank, scale, scale_all, v, s)
-                      : run_wgrad_rank<__nv_bfloat16>(w, nw, rank, scale, scale_all, v, s);
+                                    float scale_all, const LoraPlanView& v, bool pdl, cudaStream_t s) {
+    return dt == kF16 ? run_wgrad_rank<__half>(w, nw, rank, scale, scale_all, v, pdl, s)
+                      : run_wgrad_rank<__nv_bfloat16>(w, nw, rank, scale, scale_all, v, pdl, s);
 }
 
 }  // namespace spops
