@@ -1,10 +1,10 @@
 """Global gradient norm and clipping (GradSet, grad_norm, clip_grads) against 64-bit sums.
 
-Bounds, fixed before any run: the squares of a group of at most 16 elements, at most 8 groups
-and 8 single elements are added in fp32 (2^-24 relative per step, at most 34 steps, all terms
-positive), the rest in fp64, then a square root (halves the relative error) and one rounding to
-fp32: the norm is within 2^-19 of itself. A clipped element is the product of g with c, which is
-within 2^-18 of the exact factor, rounded once to the element's type."""
+Bounds, fixed before any run: the squares of a group of at most 32 elements, at most 4 groups and
+4 single elements, and 32 lanes, are added in fp32 (2^-24 relative per step, at most 45 steps, all
+terms positive), the rest in fp64, then a square root (halves the relative error) and one rounding
+to fp32: the norm is within 2^-19 of itself. A clipped element is the product of g with c, which
+is within 2^-18 of the exact factor, rounded once to the element's type."""
 import numpy as np
 import pytest
 import torch

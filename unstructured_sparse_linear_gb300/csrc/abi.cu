@@ -776,7 +776,7 @@ int spops_grad_set_build(const void* const* grads, void* const* outs, const int6
             spans.push_back({x, x + bytes, false});
             spans.push_back({y, y + bytes, true});
         }
-        chunks += clip_chunks(counts[i]);
+        chunks += clip_chunks(counts[i], es);
     }
     std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
     uintptr_t any = 0, written = 0;
@@ -797,7 +797,7 @@ int spops_grad_set_build(const void* const* grads, void* const* outs, const int6
             f.e[n].count = counts[i];
             f.e[n].first = first;
             f.e[n].dtype = dtypes[i];
-            first += clip_chunks(counts[i]);
+            first += clip_chunks(counts[i], dtype_size(dtypes[i]));
         }
         const int st = cuda_status(launch_grad_set_fill(static_cast<ClipEntry*>(set), at, f, n, (cudaStream_t)stream),
                                    "grad_set_build launch");

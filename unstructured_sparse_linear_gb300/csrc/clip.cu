@@ -2,12 +2,12 @@
 //     norm = sqrt(sum of g^2 over every gradient),  c = min(1, max_norm / (norm + 1e-6)),
 //     out = c g (rounded once to the gradient's type).
 // Two launches whatever the number of tensors: the table of the set lies in device memory,
-// with every tensor cut into chunks of 8192 elements; the chunks are dealt to the CTAs in
+// with every tensor cut into chunks of 32 KB; the chunks are dealt to the CTAs in
 // contiguous, equal ranges, so the sums have one order (no atomics) and a CTA looks its first
 // tensor up once. The second kernel adds the CTAs' partial sums itself, in one order, and walks
 // its range backwards: the part of the set that the first pass read last is still in L2.
 //
-// Squares are added in fp32 within a thread's 16 to 32 elements of a chunk, then in fp64. A
+// Squares are added in fp32 within a warp's share of up to 4 chunks, then in fp64. A
 // group whose fp32 sum leaves [1e-30, 1e30] (squares that overflow or vanish in fp32, up to the
 // largest and down to the smallest numbers of the type) is added again in fp64 from the same
 // registers, so the norm itself neither overflows nor underflows before it is rounded.
@@ -21,46 +21,79 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 2;
 
 __global__ void grad_set_fill_kernel(ClipEntry* set, const __grid_constant__ ClipFill f, int n) {
     const int i = threadIdx.x;
     if (i < n) set[i] = f.e[i];
 }
 
-// The sum over the block in a fixed order, in every thread.
-__device__ __forceinline__ double block_sum(double x, double* s_warp) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    if (lane == 0) s_warp[warp] = x;
-    __syncthreads();
-    double t = 0.0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) t += s_warp[w];
-    return t;
-}
+// fp64 runs at a 64th of the fp32 rate here, so it is kept to a few values per CTA: threads and
+// warps add in fp32, what leaves a warp is fp64 (a block reduction in fp64 by every thread took
+// 20 us of a 30 us call).
 
-// The tensor that chunk c belongs to (tensors without elements share their first chunk with
-// the next one; the last tensor with first <= c is the owner).
+// The tensor that chunk c belongs to: the last one with first <= c (tensors without elements share
+// their first chunk with the next one). Called by the whole CTA: `first` does not fall, so the
+// tensors with first <= c are counted, one round of loads per 512 tensors instead of the ten
+// dependent ones of a bisection.
 __device__ __forceinline__ int find_tensor(const ClipEntry* set, int tensors, int64_t c) {
-    int lo = 0, hi = tensors - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (set[mid].first <= c) lo = mid;
-        else hi = mid - 1;
+    int n = 0;
+    for (int b = 0; b < tensors; b += kThreads) {
+        const int i = b + (int)threadIdx.x;
+        n += __syncthreads_count(i < tensors && set[i].first <= c);
     }
-    return lo;
+    return n - 1;
 }
 
-// Leading elements of p before a 16-byte boundary.
-template <typename T>
-__device__ __forceinline__ int head_of(const T* p) {
-    return (int)(((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T));
+// One chunk: len elements of a tensor, the same on every thread.
+struct Piece {
+    const char* in;
+    char* out;
+    int len, dtype, esize;
+    __device__ __forceinline__ int head() const {  // elements before a 16-byte boundary of in
+        return min(len, (int)((16 - (reinterpret_cast<uintptr_t>(in) & 15)) & 15) / esize);
+    }
+};
+
+__device__ __forceinline__ Piece piece_of(const ClipEntry& e, int64_t c) {
+    Piece p;
+    p.dtype = e.dtype;
+    p.esize = e.dtype == kF32 ? 4 : 2;
+    const int64_t per = kClipChunk / p.esize, at = (c - e.first) * per;
+    p.in = static_cast<const char*>(e.in) + at * p.esize;
+    p.out = static_cast<char*>(e.out) + at * p.esize;
+    p.len = (int)min64(per, e.count - at);
+    return p;
+}
+
+__device__ __forceinline__ float load_one(const char* p, int dtype) {
+    if (dtype == kF32) return *reinterpret_cast<const float*>(p);
+    if (dtype == kF16) return __half2float(*reinterpret_cast<const __half*>(p));
+    return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
+}
+
+// A thread's share of a chunk: kVecs 16-byte vectors, and one of the up to 2 * 8 - 1 elements
+// before the first and behind the last of them.
+constexpr int kVecs = kClipChunk / 16 / kThreads;
+struct Share {
+    uint4 v[kVecs];
+    float edge;
+};
+__device__ __forceinline__ void fetch(const Piece& p, Share& s) {
+    const int tid = threadIdx.x, head = p.head(), V = 16 / p.esize;
+    const int nv = (p.len - head) / V, rest = p.len - nv * V;
+    const uint4* q = reinterpret_cast<const uint4*>(p.in + head * p.esize);
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+        const int i = u * kThreads + tid;
+        s.v[u] = i < nv ? ld_v4(q + i) : make_uint4(0, 0, 0, 0);
+    }
+    s.edge = tid < rest ? load_one(p.in + (tid < head ? tid : nv * V + tid) * p.esize, p.dtype) : 0.f;
 }
 
 struct Sum {
     float f = 0.f;   // groups in the range where fp32 squares are safe
-    double d = 0.0;  // the rest, and f so far
+    double d = 0.0;  // the others
 };
 
 // One group: x[0 .. n) of a thread.
@@ -82,133 +115,153 @@ __device__ __forceinline__ void add_group(const float (&x)[N], Sum& s) {
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void chunk_squares(const T* p, int len, Sum& s) {
-    constexpr int V = Elt<T>::kVec;
-    constexpr int U = kClipChunk / V / kThreads;  // vectors per thread of a whole chunk
-    const int tid = threadIdx.x;
-    const int head = min(len, head_of(p));
-    const int nv = (len - head) / V;
-    const uint4* q = reinterpret_cast<const uint4*>(p + head);
-    uint4 v[U];
+// The sum over the warp, in every lane: fp32 where all of it is there.
+__device__ __forceinline__ double warp_sum(const Sum& s) {
+    float f = s.f;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int i = u * kThreads + tid;
-        v[u] = i < nv ? ld_nc_v4(q + i) : make_uint4(0, 0, 0, 0);
+    for (int d = 16; d; d >>= 1) f += __shfl_xor_sync(0xffffffffu, f, d);
+    double x = (double)f;
+    if (__any_sync(0xffffffffu, s.d != 0.0)) {  // (NaN != 0)
+        double y = s.d;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) y += __shfl_xor_sync(0xffffffffu, y, d);
+        x += y;
     }
-    const int rest = len - nv * V;  // head and tail: at most 14 elements
-    float e[1] = {0.f};
-    if (tid < rest) e[0] = Elt<T>::to_f(p[tid < head ? tid : nv * V + tid]);
-    float x[U * V];
-#pragma unroll
-    for (int u = 0; u < U; ++u) Elt<T>::unpack(v[u], x + u * V);
-    add_group(x, s);
-    if (tid < rest) add_group(e, s);
+    return x;
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const ClipEntry* __restrict__ set, int tensors,
+template <typename T>
+__device__ __forceinline__ void squares(const Share& h, Sum& s) {
+    constexpr int V = Elt<T>::kVec;
+    float x[kVecs * V];
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) Elt<T>::unpack(h.v[u], x + u * V);
+    add_group(x, s);
+    if (h.edge != 0.f) {  // (NaN != 0)
+        const float e[1] = {h.edge};
+        add_group(e, s);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_norm_kernel(const ClipEntry* __restrict__ set, int tensors,
                                                              int64_t chunks, double* __restrict__ partial) {
     __shared__ double s_warp[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_trigger();
     const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
-    Sum s;
+    double total = 0.0;  // the warp's
     if (c0 < c1) {
+        Sum s;
         int t = find_tensor(set, tensors, c0);
         int groups = 0;
+        Share now, next;
+        Piece p = piece_of(set[t], c0);
+        fetch(p, now);
         for (int64_t c = c0; c < c1; ++c) {
-            while (t + 1 < tensors && set[t + 1].first <= c) ++t;
-            const ClipEntry e = set[t];
-            const int64_t at = (c - e.first) * kClipChunk;
-            const int len = (int)min64(kClipChunk, e.count - at);
-            if (e.dtype == kF32) chunk_squares(static_cast<const float*>(e.in) + at, len, s);
-            else if (e.dtype == kF16) chunk_squares(static_cast<const __half*>(e.in) + at, len, s);
-            else chunk_squares(static_cast<const __nv_bfloat16*>(e.in) + at, len, s);
-            if (++groups == 8) {  // short fp32 runs: at most 8 groups and 8 single elements
-                s.d += (double)s.f;
-                s.f = 0.f;
+            const int dtype = p.dtype;
+            if (c + 1 < c1) {  // the next chunk's loads are under way while this one is summed
+                while (t + 1 < tensors && set[t + 1].first <= c + 1) ++t;
+                p = piece_of(set[t], c + 1);
+                fetch(p, next);
+            }
+            if (dtype == kF32) squares<float>(now, s);
+            else if (dtype == kF16) squares<__half>(now, s);
+            else squares<__nv_bfloat16>(now, s);
+            now = next;
+            if (++groups == 4 || c + 1 == c1) {  // short fp32 runs: at most 4 groups and 4 single elements
+                total += warp_sum(s);
+                s = Sum();
                 groups = 0;
             }
         }
     }
-    const double total = block_sum(s.d + (double)s.f, s_warp);
-    if (threadIdx.x == 0) partial[blockIdx.x] = total;
+    if (lane == 0) s_warp[warp] = total;
+    __syncthreads();
+    if (warp == 0) {
+        double x = lane < kWarps ? s_warp[lane] : 0.0;
+#pragma unroll
+        for (int d = kWarps / 2; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+        if (lane == 0) partial[blockIdx.x] = x;
+    }
 }
 
-// sqrt of the sum of the partial sums, the same in every thread of every CTA.
-__device__ __forceinline__ double total_norm(const double* partial, int ctas, double* s_warp) {
+// sqrt of the sum of the partial sums in one order, by the calling warp (the same in every lane).
+__device__ __forceinline__ double total_norm(const double* partial, int ctas) {
     double x = 0.0;
-    for (int i = threadIdx.x; i < ctas; i += kThreads) x += __ldcg(partial + i);  // written while this kernel was starting
-    return sqrt(block_sum(x, s_warp));
+    for (int i = threadIdx.x & 31; i < ctas; i += 32) x += __ldcg(partial + i);  // written while this kernel was starting
+#pragma unroll
+    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return sqrt(x);
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_finish_kernel(const double* __restrict__ partial, int ctas,
-                                                                    float* __restrict__ norm_out) {
-    __shared__ double s_warp[kWarps];
+__global__ void __launch_bounds__(32) grad_norm_finish_kernel(const double* __restrict__ partial, int ctas,
+                                                              float* __restrict__ norm_out) {
     pdl_wait();
-    const double norm = total_norm(partial, ctas, s_warp);
+    const double norm = total_norm(partial, ctas);
     if (threadIdx.x == 0) *norm_out = (float)norm;
 }
 
 template <typename T>
-__device__ __forceinline__ void chunk_scale(const T* p, T* o, int len, float c) {
+__device__ __forceinline__ void store_scaled(const Piece& p, const Share& h, float c) {
     constexpr int V = Elt<T>::kVec;
-    constexpr int U = kClipChunk / V / kThreads;
-    const int tid = threadIdx.x;
-    const int head = min(len, head_of(p));
-    if (head_of(o) != head_of(p)) {  // the two sides' 16-byte boundaries differ
-        for (int i = tid; i < len; i += kThreads) o[i] = Elt<T>::from_f(Elt<T>::to_f(p[i]) * c);
-        return;
-    }
-    const int nv = (len - head) / V;
-    const uint4* q = reinterpret_cast<const uint4*>(p + head);
-    uint4* w = reinterpret_cast<uint4*>(o + head);
-    uint4 v[U];
+    const int tid = threadIdx.x, head = p.head();
+    const int nv = (p.len - head) / V, rest = p.len - nv * V;
+    T* o = reinterpret_cast<T*>(p.out);
+    if (tid < rest) o[tid < head ? tid : nv * V + tid] = Elt<T>::from_f(h.edge * c);
+    o += head;
+    const bool vec = (reinterpret_cast<uintptr_t>(o) & 15) == 0;  // out's boundaries are in's
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int i = u * kThreads + tid;
-        if (i < nv) v[u] = ld_v4(q + i);
-    }
-    const int rest = len - nv * V;
-    if (tid < rest) {
-        const int i = tid < head ? tid : nv * V + tid;
-        o[i] = Elt<T>::from_f(Elt<T>::to_f(p[i]) * c);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kVecs; ++u) {
         const int i = u * kThreads + tid;
         if (i < nv) {
             float x[V];
-            Elt<T>::unpack(v[u], x);
+            Elt<T>::unpack(h.v[u], x);
 #pragma unroll
             for (int k = 0; k < V; ++k) x[k] *= c;
-            w[i] = Elt<T>::pack(x);
+            if (vec) {
+                __stcs(reinterpret_cast<uint4*>(o) + i, Elt<T>::pack(x));
+            } else {
+#pragma unroll
+                for (int k = 0; k < V; ++k) o[(int64_t)i * V + k] = Elt<T>::from_f(x[k]);
+            }
         }
     }
 }
 
-__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const ClipEntry* __restrict__ set, int tensors,
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale_kernel(const ClipEntry* __restrict__ set, int tensors,
                                                               int64_t chunks, const double* __restrict__ partial,
                                                               int ctas, double max_norm, int in_place,
                                                               float* __restrict__ norm_out) {
-    __shared__ double s_warp[kWarps];
+    __shared__ float s_c;
     const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
     int t = c0 < c1 ? find_tensor(set, tensors, c1 - 1) : 0;
     pdl_wait();
-    const double norm = total_norm(partial, ctas, s_warp);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-    const double q = max_norm / (norm + 1e-6);
-    const float c = q >= 1.0 || isinf(max_norm) ? 1.f : (float)q;  // NaN stays NaN
+    if (threadIdx.x < 32) {
+        const double norm = total_norm(partial, ctas);
+        if (threadIdx.x == 0) {
+            const double q = max_norm / (norm + 1e-6);
+            s_c = q >= 1.0 || isinf(max_norm) ? 1.f : (float)q;  // NaN stays NaN
+            if (blockIdx.x == 0) *norm_out = (float)norm;
+        }
+    }
+    __syncthreads();
+    const float c = s_c;
     if (c == 1.f && in_place) return;  // every gradient already holds its value
+    if (c0 >= c1) return;
+    Share now, next;
+    Piece p = piece_of(set[t], c1 - 1), q = p;
+    fetch(p, now);
     for (int64_t k = c1 - 1; k >= c0; --k) {
-        while (set[t].first > k) --t;
-        const ClipEntry e = set[t];
-        const int64_t at = (k - e.first) * kClipChunk;
-        const int len = (int)min64(kClipChunk, e.count - at);
-        if (e.dtype == kF32) chunk_scale(static_cast<const float*>(e.in) + at, static_cast<float*>(e.out) + at, len, c);
-        else if (e.dtype == kF16)
-            chunk_scale(static_cast<const __half*>(e.in) + at, static_cast<__half*>(e.out) + at, len, c);
-        else
-            chunk_scale(static_cast<const __nv_bfloat16*>(e.in) + at, static_cast<__nv_bfloat16*>(e.out) + at, len, c);
+        if (k > c0) {
+            while (set[t].first > k - 1) --t;
+            q = piece_of(set[t], k - 1);
+            fetch(q, next);
+        }
+        if (p.dtype == kF32) store_scaled<float>(p, now, c);
+        else if (p.dtype == kF16) store_scaled<__half>(p, now, c);
+        else store_scaled<__nv_bfloat16>(p, now, c);
+        now = next;
+        p = q;
     }
 }
 
@@ -222,7 +275,7 @@ cudaError_t launch_grad_set_fill(ClipEntry* set, int64_t at, const ClipFill& f, 
 
 cudaError_t launch_grad_norm(const ClipEntry* set, int32_t tensors, int64_t chunks, bool in_place, bool scale,
                              double max_norm, float* norm_out, double* partial, cudaStream_t s) {
-    const int64_t want = (int64_t)device_props().sm_count * 4;
+    const int64_t want = (int64_t)device_props().sm_count * kCtasPerSm;
     const int ctas = (int)max64(1, min64(chunks, min64(want, kClipMaxCtas)));
     grad_norm_kernel<<<ctas, kThreads, 0, s>>>(set, tensors, chunks, partial);
     cudaError_t e = cudaGetLastError();
@@ -231,7 +284,7 @@ cudaError_t launch_grad_norm(const ClipEntry* set, int32_t tensors, int64_t chun
         e = launch_pdl(grad_scale_kernel, dim3(ctas), dim3(kThreads), 0, s, set, (int)tensors, chunks,
                        (const double*)partial, ctas, max_norm, (int)in_place, norm_out);
     else
-        e = launch_pdl(grad_norm_finish_kernel, dim3(1), dim3(kThreads), 0, s, (const double*)partial, ctas, norm_out);
+        e = launch_pdl(grad_norm_finish_kernel, dim3(1), dim3(32), 0, s, (const double*)partial, ctas, norm_out);
     count_launches(2);
     return e;
 }

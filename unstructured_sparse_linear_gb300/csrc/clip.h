@@ -7,8 +7,8 @@
 
 namespace spops {
 
-constexpr int kClipChunk = 8192;  // elements of one tensor that a CTA takes at a time
-constexpr int kClipMaxCtas = 1216;  // partial sums: 8 per SM of a GPU with 152 SMs
+constexpr int kClipChunk = 32768;   // bytes of one tensor that a CTA takes at a time
+constexpr int kClipMaxCtas = 1024;  // partial sums
 
 // One gradient of a set. out == in: scaled in place. first: its first chunk in the set.
 struct ClipEntry {
@@ -20,7 +20,10 @@ struct ClipEntry {
     int32_t pad;
 };
 
-inline int64_t clip_chunks(int64_t count) { return (count + kClipChunk - 1) / kClipChunk; }
+inline int64_t clip_chunks(int64_t count, size_t esize) {
+    const int64_t per = kClipChunk / (int64_t)esize;
+    return (count + per - 1) / per;
+}
 inline size_t grad_set_bytes(int64_t tensors) { return sizeof(ClipEntry) * (size_t)(tensors > 0 ? tensors : 1); }
 inline size_t grad_norm_ws_bytes() { return sizeof(double) * kClipMaxCtas; }
 
