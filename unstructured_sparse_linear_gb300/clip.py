@@ -83,6 +83,8 @@ def clip_grads(grads, max_norm: float) -> torch.Tensor:
     with _on(dev):
         norm = torch.empty((), dtype=torch.float32, device=dev)
         ws = torch.empty(s._ws, dtype=torch.uint8, device=dev)
-        _check(_L().spops_clip_grads(s._ptr, s._n, s._chunks, s._in_place, float(max_norm), norm.data_ptr(),
-                                     ws.data_ptr(), s._ws, _raw_stream(dev.index)), "clip_grads")
+        st = _L().spops_clip_grads(s._ptr, s._n, s._chunks, s._in_place, float(max_norm), norm.data_ptr(),
+                                   ws.data_ptr(), s._ws, _raw_stream(dev.index))
+    if st:
+        _check(st, "clip_grads")
     return norm

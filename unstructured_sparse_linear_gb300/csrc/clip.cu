@@ -1,13 +1,19 @@
-// Gradient clipping by the global 2-norm of many tensors:
+// Global 2-norm of many tensors and clipping by it:
 //     norm = sqrt(sum of g^2 over every gradient),  c = min(1, max_norm / (norm + 1e-6)),
 //     out = c g (rounded once to the gradient's type).
-// Two launches whatever the number of tensors: the table of the set lies in device memory,
-// with every tensor cut into chunks of 32 KB; the chunks are dealt to the CTAs in
+// Two launches whatever the number of tensors: the table of the set lies in device memory, with
+// every tensor cut into chunks of 32 KB; the chunks are dealt to the CTAs (one per SM) in
 // contiguous, equal ranges, so the sums have one order (no atomics) and a CTA looks its first
-// tensor up once. The second kernel adds the CTAs' partial sums itself, in one order, and walks
-// its range backwards: the part of the set that the first pass read last is still in L2.
+// tensor up once. One thread keeps a ring of six chunks (192 KB) in flight with bulk copies of
+// whole 16-byte granules (the neighbours' bytes in the first and the last one are masked), 16 warps
+// work on them; scaled chunks leave from where they lie by bulk stores, the elements of granules
+// that belong to a neighbour too by plain ones. With loads to registers instead (two CTAs of 512
+// threads, 64 bytes a thread, two chunks under way) 166 MB of bf16 took 88 us.
+// The second kernel adds the CTAs' partial sums itself, in one order, and walks its range
+// backwards: the part of the set that the first pass read last is still in L2. It fills its ring
+// while the first kernel ends.
 //
-// Squares are added in fp32 within a warp's share of up to 4 chunks, then in fp64. A
+// Squares are added in fp32 within a warp's share of up to 4 chunks, then in fp64. A thread's
 // group whose fp32 sum leaves [1e-30, 1e30] (squares that overflow or vanish in fp32, up to the
 // largest and down to the smallest numbers of the type) is added again in fp64 from the same
 // registers, so the norm itself neither overflows nor underflows before it is rounded.
@@ -19,22 +25,22 @@
 namespace spops {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 2;
+constexpr int kWarps = 16;                // working warps
+constexpr int kWork = kWarps * 32;
+constexpr int kThreads = kWork + 32;      // and one that loads
+constexpr int kStages = 6;
+constexpr uint32_t kStage = 32768;
+constexpr uint32_t kKeep = 96u << 20;  // bytes of the set that the first pass asks L2 to keep
+constexpr int kVecs = kStage / 16 / kWork;  // granules per thread and chunk
 
 __global__ void grad_set_fill_kernel(ClipEntry* set, const __grid_constant__ ClipFill f, int n) {
     const int i = threadIdx.x;
     if (i < n) set[i] = f.e[i];
 }
 
-// fp64 runs at a 64th of the fp32 rate here, so it is kept to a few values per CTA: threads and
-// warps add in fp32, what leaves a warp is fp64 (a block reduction in fp64 by every thread took
-// 20 us of a 30 us call).
-
 // The tensor that chunk c belongs to: the last one with first <= c (tensors without elements share
 // their first chunk with the next one). Called by the whole CTA: `first` does not fall, so the
-// tensors with first <= c are counted, one round of loads per 512 tensors instead of the ten
+// tensors with first <= c are counted, one round of loads per 544 tensors instead of the ten
 // dependent ones of a bisection.
 __device__ __forceinline__ int find_tensor(const ClipEntry* set, int tensors, int64_t c) {
     int n = 0;
@@ -45,50 +51,86 @@ __device__ __forceinline__ int find_tensor(const ClipEntry* set, int tensors, in
     return n - 1;
 }
 
-// One chunk: len elements of a tensor, the same on every thread.
-struct Piece {
-    const char* in;
-    char* out;
-    int len, dtype, esize;
-    __device__ __forceinline__ int head() const {  // elements before a 16-byte boundary of in
-        return min(len, (int)((16 - (reinterpret_cast<uintptr_t>(in) & 15)) & 15) / esize);
-    }
-};
-
-__device__ __forceinline__ Piece piece_of(const ClipEntry& e, int64_t c) {
-    Piece p;
-    p.dtype = e.dtype;
-    p.esize = e.dtype == kF32 ? 4 : 2;
-    const int64_t per = kClipChunk / p.esize, at = (c - e.first) * per;
-    p.in = static_cast<const char*>(e.in) + at * p.esize;
-    p.out = static_cast<char*>(e.out) + at * p.esize;
-    p.len = (int)min64(per, e.count - at);
+// L2 policies for bulk copies, and the copies with one.
+__device__ __forceinline__ uint64_t l2_policy(bool keep) {
+    uint64_t p;
+    if (keep) asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    else asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
-
-__device__ __forceinline__ float load_one(const char* p, int dtype) {
-    if (dtype == kF32) return *reinterpret_cast<const float*>(p);
-    if (dtype == kF16) return __half2float(*reinterpret_cast<const __half*>(p));
-    return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
+__device__ __forceinline__ void bulk_g2s_hint(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_s2g_hint(void* dst, uint32_t src, uint32_t bytes, uint64_t policy) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;" ::"l"(dst), "r"(src),
+                 "r"(bytes), "l"(policy)
+                 : "memory");
 }
 
-// A thread's share of a chunk: kVecs 16-byte vectors, and one of the up to 2 * 8 - 1 elements
-// before the first and behind the last of them.
-constexpr int kVecs = kClipChunk / 16 / kThreads;
-struct Share {
-    uint4 v[kVecs];
-    float edge;
+// A chunk in a stage: len elements from byte `off` of `granules` 16-byte granules on, of type
+// dtype; out: where they go.
+struct Piece {
+    char* out;
+    int len, off, granules, dtype;
 };
-__device__ __forceinline__ void fetch(const Piece& p, Share& s) {
-    const int tid = threadIdx.x, head = p.head(), V = 16 / p.esize;
-    const int nv = (p.len - head) / V, rest = p.len - nv * V;
-    const uint4* q = reinterpret_cast<const uint4*>(p.in + head * p.esize);
-#pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-        const int i = u * kThreads + tid;
-        s.v[u] = i < nv ? ld_v4(q + i) : make_uint4(0, 0, 0, 0);
+
+struct __align__(16) Shared {
+    uint64_t full[kStages], empty[kStages];
+    Piece piece[kStages];
+    double warp[kWarps];
+    float c;
+    volatile int failed;
+    volatile int stop;  // the chunks not yet asked for are not wanted
+};
+constexpr uint32_t kSmem = kStages * kStage + ((sizeof(Shared) + 127) / 128 * 128);
+
+// The loading thread: chunks c0, c0 + step, ... (n of them) of tensor t on into the ring; the last
+// `keep` of them are to stay in L2.
+__device__ __forceinline__ void load_chunks(const ClipEntry* set, int tensors, int t, int64_t c0, int step, int64_t n,
+                                            int64_t keep, uint32_t sbase, Shared& sh, int* err) {
+    uint32_t i = 0;
+    const uint64_t pass = l2_policy(false), stay = l2_policy(true);
+    for (; i < n; ++i) {
+        const int64_t c = c0 + (int64_t)i * step;
+        if (step > 0)
+            while (t + 1 < tensors && set[t + 1].first <= c) ++t;
+        else
+            while (set[t].first > c) --t;
+        const ClipEntry e = set[t];
+        const int esize = e.dtype == kF32 ? 4 : 2;
+        const int64_t per = kClipChunk / esize, at = (c - e.first) * per;
+        Piece p;
+        p.dtype = e.dtype;
+        p.len = (int)min64(per, e.count - at);
+        p.out = static_cast<char*>(e.out) + at * esize;
+        const char* in = static_cast<const char*>(e.in) + at * esize;
+        p.off = (int)(reinterpret_cast<uintptr_t>(in) & 15);
+        p.granules = (p.off + p.len * esize + 15) / 16;
+        const uint32_t s = i % kStages, full = smem_u32(&sh.full[s]);
+        if (i >= kStages && (sh.failed || !mbar_wait(smem_u32(&sh.empty[s]), (i / kStages - 1) & 1u, err))) {
+            sh.failed = 1;
+            break;
+        }
+        if (sh.stop) break;
+        sh.piece[s] = p;
+        mbar_arrive_expect_tx(full, (uint32_t)p.granules * 16);
+        bulk_g2s_hint(sbase + s * kStage, in - p.off, (uint32_t)p.granules * 16, full, i + keep < n ? pass : stay);
     }
-    s.edge = tid < rest ? load_one(p.in + (tid < head ? tid : nv * V + tid) * p.esize, p.dtype) : 0.f;
+    if (sh.failed)  // let the copies in flight land before the shared memory is given up
+        for (uint32_t k = i > kStages ? i - kStages : 0; k < i; ++k)
+            mbar_wait_for(smem_u32(&sh.full[k % kStages]), (k / kStages) & 1u, nullptr, 100000000ull);
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 struct Sum {
@@ -96,7 +138,7 @@ struct Sum {
     double d = 0.0;  // the others
 };
 
-// One group: x[0 .. n) of a thread.
+// One group of a thread: x[0 .. N).
 template <int N>
 __device__ __forceinline__ void add_group(const float (&x)[N], Sum& s) {
     float p = 0.f, m = 0.f;
@@ -115,7 +157,9 @@ __device__ __forceinline__ void add_group(const float (&x)[N], Sum& s) {
     }
 }
 
-// The sum over the warp, in every lane: fp32 where all of it is there.
+// The sum over the warp, in every lane: fp32 where all of it is there. fp64 runs at a 64th of the
+// fp32 rate here, so it is kept to a few values per warp (reductions in fp64 by every thread took
+// 20 us of a 30 us call).
 __device__ __forceinline__ double warp_sum(const Sum& s) {
     float f = s.f;
 #pragma unroll
@@ -131,54 +175,82 @@ __device__ __forceinline__ double warp_sum(const Sum& s) {
 }
 
 template <typename T>
-__device__ __forceinline__ void squares(const Share& h, Sum& s) {
+__device__ __forceinline__ void squares(const Piece& p, uint32_t st, Sum& s) {
     constexpr int V = Elt<T>::kVec;
+    const int tid = threadIdx.x, first = p.off / (int)sizeof(T), last = first + p.len;  // elements of the stage
     float x[kVecs * V];
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) Elt<T>::unpack(h.v[u], x + u * V);
-    add_group(x, s);
-    if (h.edge != 0.f) {  // (NaN != 0)
-        const float e[1] = {h.edge};
-        add_group(e, s);
+    for (int u = 0; u < kVecs; ++u) {
+        const int i = u * kWork + tid;
+        Elt<T>::unpack(i < p.granules ? ld_shared_v4(st + i * 16) : make_uint4(0, 0, 0, 0), x + u * V);
+        if (i == 0 || i == p.granules - 1)
+#pragma unroll
+            for (int k = 0; k < V; ++k)
+                if (i * V + k < first || i * V + k >= last) x[u * V + k] = 0.f;
     }
+    add_group(x, s);
 }
 
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_norm_kernel(const ClipEntry* __restrict__ set, int tensors,
-                                                             int64_t chunks, double* __restrict__ partial) {
-    __shared__ double s_warp[kWarps];
+__device__ __forceinline__ void init_ring(Shared& sh) {
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), 1);
+            mbar_init(smem_u32(&sh.empty[s]), kWarps);
+        }
+        fence_mbar_init();
+        sh.failed = 0;
+        sh.stop = 0;
+    }
+    __syncthreads();
+}
+
+// Waits for chunk i; false (on some lanes perhaps) once a wait has run out of time.
+__device__ __forceinline__ bool wait_stage_one(Shared& sh, uint32_t i, int* err) {
+    if (sh.failed) return false;
+    if (mbar_wait(smem_u32(&sh.full[i % kStages]), (i / kStages) & 1u, err)) return true;
+    sh.failed = 1;
+    return false;
+}
+__device__ __forceinline__ bool wait_stage(Shared& sh, uint32_t i, int* err) {
+    const bool ok = wait_stage_one(sh, i, err);
+    __syncwarp();
+    return ok;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) grad_norm_kernel(const ClipEntry* __restrict__ set, int tensors,
+                                                               int64_t chunks, double* __restrict__ partial, int* err) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem + kStages * kStage);
+    const uint32_t sbase = smem_u32(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_trigger();
-    const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
-    double total = 0.0;  // the warp's
-    if (c0 < c1) {
+    const int64_t c0 = chunks * blockIdx.x / gridDim.x, n = chunks * (blockIdx.x + 1) / gridDim.x - c0;
+    init_ring(sh);
+    const int t = n > 0 ? find_tensor(set, tensors, c0) : 0;
+    if (warp == kWarps) {
+        if (lane == 0 && n > 0) load_chunks(set, tensors, t, c0, 1, n, kKeep / kStage / gridDim.x, sbase, sh, err);
+    } else {
+        double total = 0.0;  // the warp's
         Sum s;
-        int t = find_tensor(set, tensors, c0);
-        int groups = 0;
-        Share now, next;
-        Piece p = piece_of(set[t], c0);
-        fetch(p, now);
-        for (int64_t c = c0; c < c1; ++c) {
-            const int dtype = p.dtype;
-            if (c + 1 < c1) {  // the next chunk's loads are under way while this one is summed
-                while (t + 1 < tensors && set[t + 1].first <= c + 1) ++t;
-                p = piece_of(set[t], c + 1);
-                fetch(p, next);
-            }
-            if (dtype == kF32) squares<float>(now, s);
-            else if (dtype == kF16) squares<__half>(now, s);
-            else squares<__nv_bfloat16>(now, s);
-            now = next;
-            if (++groups == 4 || c + 1 == c1) {  // short fp32 runs: at most 4 groups and 4 single elements
+        for (uint32_t i = 0; i < n; ++i) {
+            const uint32_t st = sbase + (i % kStages) * kStage;
+            wait_stage(sh, i, err);
+            const Piece p = sh.piece[i % kStages];
+            if (p.dtype == kF32) squares<float>(p, st, s);
+            else if (p.dtype == kF16) squares<__half>(p, st, s);
+            else squares<__nv_bfloat16>(p, st, s);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.empty[i % kStages]));
+            if ((i & 3u) == 3u || i + 1 == n) {  // short fp32 runs
                 total += warp_sum(s);
                 s = Sum();
-                groups = 0;
             }
         }
+        if (lane == 0) sh.warp[warp] = total;
     }
-    if (lane == 0) s_warp[warp] = total;
     __syncthreads();
     if (warp == 0) {
-        double x = lane < kWarps ? s_warp[lane] : 0.0;
+        double x = lane < kWarps ? sh.warp[lane] : 0.0;
 #pragma unroll
         for (int d = kWarps / 2; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
         if (lane == 0) partial[blockIdx.x] = x;
@@ -201,68 +273,96 @@ __global__ void __launch_bounds__(32) grad_norm_finish_kernel(const double* __re
     if (threadIdx.x == 0) *norm_out = (float)norm;
 }
 
+// The chunk times c: whole granules of the tensor in place (they leave by a bulk store), elements
+// of shared granules, and everything where out's granules are not in's, straight to out.
 template <typename T>
-__device__ __forceinline__ void store_scaled(const Piece& p, const Share& h, float c) {
+__device__ __forceinline__ void scale_chunk(const Piece& p, uint32_t st, float c, bool bulk) {
     constexpr int V = Elt<T>::kVec;
-    const int tid = threadIdx.x, head = p.head();
-    const int nv = (p.len - head) / V, rest = p.len - nv * V;
-    T* o = reinterpret_cast<T*>(p.out);
-    if (tid < rest) o[tid < head ? tid : nv * V + tid] = Elt<T>::from_f(h.edge * c);
-    o += head;
-    const bool vec = (reinterpret_cast<uintptr_t>(o) & 15) == 0;  // out's boundaries are in's
+    const int tid = threadIdx.x, first = p.off / (int)sizeof(T), last = first + p.len;
+    T* out = reinterpret_cast<T*>(p.out) - first;  // of element 0 of the stage
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
-        const int i = u * kThreads + tid;
-        if (i < nv) {
-            float x[V];
-            Elt<T>::unpack(h.v[u], x);
+        const int i = u * kWork + tid;
+        if (i >= p.granules) continue;
+        float x[V];
+        Elt<T>::unpack(ld_shared_v4(st + i * 16), x);
 #pragma unroll
-            for (int k = 0; k < V; ++k) x[k] *= c;
-            if (vec) {
-                __stcs(reinterpret_cast<uint4*>(o) + i, Elt<T>::pack(x));
-            } else {
+        for (int k = 0; k < V; ++k) x[k] *= c;
+        if (bulk && i * V >= first && i * V + V <= last) {
+            st_shared_v4(st + i * 16, Elt<T>::pack(x));
+        } else {
 #pragma unroll
-                for (int k = 0; k < V; ++k) o[(int64_t)i * V + k] = Elt<T>::from_f(x[k]);
-            }
+            for (int k = 0; k < V; ++k)
+                if (i * V + k >= first && i * V + k < last) out[i * V + k] = Elt<T>::from_f(x[k]);
         }
     }
 }
 
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_scale_kernel(const ClipEntry* __restrict__ set, int tensors,
-                                                              int64_t chunks, const double* __restrict__ partial,
-                                                              int ctas, double max_norm, int in_place,
-                                                              float* __restrict__ norm_out) {
-    __shared__ float s_c;
-    const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
-    int t = c0 < c1 ? find_tensor(set, tensors, c1 - 1) : 0;
-    pdl_wait();
-    if (threadIdx.x < 32) {
-        const double norm = total_norm(partial, ctas);
-        if (threadIdx.x == 0) {
-            const double q = max_norm / (norm + 1e-6);
-            s_c = q >= 1.0 || isinf(max_norm) ? 1.f : (float)q;  // NaN stays NaN
-            if (blockIdx.x == 0) *norm_out = (float)norm;
+__global__ void __launch_bounds__(kThreads, 1)
+grad_scale_kernel(const ClipEntry* __restrict__ set, int tensors, int64_t chunks, const double* __restrict__ partial,
+                  int ctas, double max_norm, int in_place, float* __restrict__ norm_out, int* err) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    Shared& sh = *reinterpret_cast<Shared*>(smem + kStages * kStage);
+    const uint32_t sbase = smem_u32(smem);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c0 = chunks * blockIdx.x / gridDim.x, n = chunks * (blockIdx.x + 1) / gridDim.x - c0;
+    init_ring(sh);
+    const int t = n > 0 ? find_tensor(set, tensors, c0 + n - 1) : 0;
+    if (warp == kWarps) {
+        // The gradients are older than the kernel before this one, so the ring fills before it has
+        // ended (in vain where nothing is to be scaled).
+        if (lane == 0 && n > 0) load_chunks(set, tensors, t, c0 + n - 1, -1, n, 0, sbase, sh, err);
+        pdl_wait();
+    } else {
+        pdl_wait();
+        if (warp == 0) {
+            const double norm = total_norm(partial, ctas);
+            if (lane == 0) {
+                const double q = max_norm / (norm + 1e-6);
+                sh.c = q >= 1.0 || isinf(max_norm) ? 1.f : (float)q;  // NaN stays NaN
+                if (blockIdx.x == 0) *norm_out = (float)norm;
+            }
+        }
+        named_barrier(1, kWork);
+        const float c = sh.c;
+        if (c == 1.f && in_place) {  // every gradient already holds its value
+            if (threadIdx.x == 0) {
+                for (uint32_t i = 0; i < n && i < kStages; ++i) wait_stage_one(sh, i, err);
+                sh.stop = 1;
+                for (int w = 0; w < kWarps; ++w) mbar_arrive(smem_u32(&sh.empty[0]));
+            }
+        } else {
+            const uint64_t pass = l2_policy(false);
+            int held = -1;  // the stage whose store may still be reading it
+            for (uint32_t i = 0; i < n; ++i) {
+                const uint32_t s = i % kStages, st = sbase + s * kStage;
+                const bool ok = wait_stage(sh, i, err);
+                const Piece p = sh.piece[s];
+                const bool bulk = ((reinterpret_cast<uintptr_t>(p.out) & 15) == (uintptr_t)p.off);
+                if (ok) {
+                    if (p.dtype == kF32) scale_chunk<float>(p, st, c, bulk);
+                    else if (p.dtype == kF16) scale_chunk<__half>(p, st, c, bulk);
+                    else scale_chunk<__nv_bfloat16>(p, st, c, bulk);
+                }
+                fence_proxy_async_smem();
+                named_barrier(1, kWork);
+                if (threadIdx.x == 0) {
+                    const int esize = p.dtype == kF32 ? 4 : 2;
+                    const int a = p.off ? 1 : 0, b = (p.off + p.len * esize) / 16;  // whole granules [a, b)
+                    if (ok && bulk && b > a)
+                        bulk_s2g_hint(p.out - p.off + a * 16, st + a * 16, (uint32_t)(b - a) * 16, pass);
+                    bulk_commit();
+                    // the store before this one has been read out: its stage is free
+                    bulk_wait_read<1>();
+                    if (held >= 0)
+                        for (int w = 0; w < kWarps; ++w) mbar_arrive(smem_u32(&sh.empty[held]));
+                    held = (int)s;
+                }
+            }
+            if (threadIdx.x == 0) bulk_wait<0>();
         }
     }
     __syncthreads();
-    const float c = s_c;
-    if (c == 1.f && in_place) return;  // every gradient already holds its value
-    if (c0 >= c1) return;
-    Share now, next;
-    Piece p = piece_of(set[t], c1 - 1), q = p;
-    fetch(p, now);
-    for (int64_t k = c1 - 1; k >= c0; --k) {
-        if (k > c0) {
-            while (set[t].first > k - 1) --t;
-            q = piece_of(set[t], k - 1);
-            fetch(q, next);
-        }
-        if (p.dtype == kF32) store_scaled<float>(p, now, c);
-        else if (p.dtype == kF16) store_scaled<__half>(p, now, c);
-        else store_scaled<__nv_bfloat16>(p, now, c);
-        now = next;
-        p = q;
-    }
 }
 
 }  // namespace
@@ -275,14 +375,24 @@ cudaError_t launch_grad_set_fill(ClipEntry* set, int64_t at, const ClipFill& f, 
 
 cudaError_t launch_grad_norm(const ClipEntry* set, int32_t tensors, int64_t chunks, bool in_place, bool scale,
                              double max_norm, float* norm_out, double* partial, cudaStream_t s) {
-    const int64_t want = (int64_t)device_props().sm_count * kCtasPerSm;
-    const int ctas = (int)max64(1, min64(chunks, min64(want, kClipMaxCtas)));
-    grad_norm_kernel<<<ctas, kThreads, 0, s>>>(set, tensors, chunks, partial);
+    static bool done[64];
+    const int d = device_props().device;
+    if (d < 0 || d >= 64) return cudaErrorInvalidDevice;
+    if (!done[d]) {
+        cudaError_t e = cudaFuncSetAttribute(grad_norm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(grad_scale_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+        if (e != cudaSuccess) return e;
+        done[d] = true;
+    }
+    int* err = device_error_word();
+    const int ctas = (int)max64(1, min64(chunks, min64(device_props().sm_count, kClipMaxCtas)));
+    grad_norm_kernel<<<ctas, kThreads, kSmem, s>>>(set, tensors, chunks, partial, err);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (scale)
-        e = launch_pdl(grad_scale_kernel, dim3(ctas), dim3(kThreads), 0, s, set, (int)tensors, chunks,
-                       (const double*)partial, ctas, max_norm, (int)in_place, norm_out);
+        e = launch_pdl(grad_scale_kernel, dim3(ctas), dim3(kThreads), kSmem, s, set, (int)tensors, chunks,
+                       (const double*)partial, ctas, max_norm, (int)in_place, norm_out, err);
     else
         e = launch_pdl(grad_norm_finish_kernel, dim3(1), dim3(32), 0, s, (const double*)partial, ctas, norm_out);
     count_launches(2);

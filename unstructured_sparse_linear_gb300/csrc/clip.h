@@ -7,7 +7,9 @@
 
 namespace spops {
 
-constexpr int kClipChunk = 32768;   // bytes of one tensor that a CTA takes at a time
+// Bytes of one tensor that a CTA takes at a time: with the bytes before and behind it in their
+// 16-byte granules at most 32 KB.
+constexpr int kClipChunk = 32768 - 16;
 constexpr int kClipMaxCtas = 1024;  // partial sums
 
 // One gradient of a set. out == in: scaled in place. first: its first chunk in the set.

@@ -26,7 +26,12 @@ def _raw_stream(index: int) -> int:
 
 
 def _rows(t, name, rows, cols, dtype, device):
-    """Checks a row-strided [rows, cols] operand; returns (address, row stride)."""
+    """Checks a row-strided [rows, cols] operand; returns (address, row stride). The launch of a
+    small call takes longer than its kernel, so the common case is a handful of tests."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == (rows, cols) and t.device == device:
+        ld, step = t.stride()
+        if step == 1 and ld >= cols:
+            return t.data_ptr(), ld
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -48,6 +53,7 @@ class LoraPlan:
         self.buf, self.tokens, self.n_adapters = buf, tokens, n_adapters
         self.device = buf.device
         self._ptr = buf.data_ptr()
+        self._grad_ws = {}  # lora_grad's workspace bytes by rank
 
     def order(self) -> torch.Tensor:
         """The tokens sorted by adapter (stable; those without an adapter last), int32."""
@@ -84,42 +90,43 @@ def lora_plan(adapter_ids: torch.Tensor | None, n_adapters: int, tokens: int | N
 
 
 def _weights(X, A, B, plan, scale):
-    """Checks shared by both calls; returns (device, tokens, in, out, rank, n, scale address, factor)."""
+    """Checks shared by both calls; returns (device, dtype, in, out, rank, n, scale address, factor)."""
     if not isinstance(plan, LoraPlan):
         raise TypeError("plan must be a LoraPlan")
+    dev = plan.device
     if not isinstance(X, torch.Tensor):
         raise TypeError("X must be a torch.Tensor")
-    dev, dt = X.device, X.dtype
+    dt = X.dtype
     if not X.is_cuda:
         raise ValueError("X must be a CUDA tensor")
     if dt not in _DTYPE:
         raise ValueError(f"X dtype {dt} not in {list(_DTYPE)}")
-    _req(A, "A", dt, device=dev)
-    _req(B, "B", dt, device=dev)
+    if X.device != dev:
+        raise ValueError(f"X is on {X.device} and the plan on {dev}")
+    for name, w in (("A", A), ("B", B)):
+        if not (type(w) is torch.Tensor and w.dtype is dt and w.device == dev and w.is_contiguous()):
+            _req(w, name, dt, device=dev)  # (a Parameter, or what is wrong)
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError("A must be [adapters, rank, in] and B [adapters, out, rank]")
     n, rank, k = A.shape
-    if B.size(0) != n or B.size(2) != rank:
+    nb, n_out, rb = B.shape
+    if nb != n or rb != rank:
         raise ValueError(f"A {tuple(A.shape)} and B {tuple(B.shape)} differ in adapters or rank")
-    if plan.n_adapters != n or plan.device != dev:
-        raise ValueError(f"plan was built for {plan.n_adapters} adapters on {plan.device}, not {n} on {dev}")
-    s_ptr, s_all = 0, 1.0
+    if plan.n_adapters != n:
+        raise ValueError(f"plan was built for {plan.n_adapters} adapters, not {n}")
+    if scale is None:
+        return dev, dt, k, n_out, rank, n, 0, 1.0
     if isinstance(scale, torch.Tensor):
         _req(scale, "scale", torch.float32, device=dev)
         if scale.numel() != n:
             raise ValueError(f"scale must have one factor per adapter ({n}), got {scale.numel()}")
-        s_ptr = scale.data_ptr()
-    elif scale is not None:
-        s_all = float(scale)
-    return dev, plan.tokens, k, B.size(1), rank, n, s_ptr, s_all
+        return dev, dt, k, n_out, rank, n, scale.data_ptr(), 1.0
+    return dev, dt, k, n_out, rank, n, 0, float(scale)
 
 
-def _on(dev):
-    """Makes dev current (a context that does nothing where it already is)."""
-    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+class _Here:
+    """The context where the device is current already."""
 
-
-class _Nothing:
     def __enter__(self):
         pass
 
@@ -127,7 +134,12 @@ class _Nothing:
         return False
 
 
-_HERE = _Nothing()
+_HERE = _Here()
+
+
+def _on(dev):
+    """A context that makes dev current."""
+    return _HERE if torch._C._cuda_getDevice() == dev.index else torch.cuda.device(dev)
 
 
 def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h: bool = False):
@@ -135,8 +147,8 @@ def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h:
     base: the shared projection's output (None: zeros); out=base adds in place. scale: a float,
     or an fp32 tensor with one factor per adapter. return_h: also return X A_i^T (fp32
     [tokens, rank]), which lora_grad takes."""
-    dev, T, k, n_out, rank, n, s_ptr, s_all = _weights(X, A, B, plan, scale)
-    dt = X.dtype
+    dev, dt, k, n_out, rank, n, s_ptr, s_all = _weights(X, A, B, plan, scale)
+    T = plan.tokens
     x, ldx = _rows(X, "X", T, k, dt, dev)
     b, ldb = _rows(base, "base", T, n_out, dt, dev) if base is not None else (0, n_out)
     lib = _L()
@@ -145,9 +157,10 @@ def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h:
             out = torch.empty((T, n_out), dtype=dt, device=dev)
         y, ldy = _rows(out, "out", T, n_out, dt, dev)
         h = torch.empty((T, rank), dtype=torch.float32, device=dev) if return_h else None
-        _check(lib.spops_lora_add(x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out, rank, n,
-                                  b, ldb, y, ldy, h.data_ptr() if return_h else 0, plan._ptr, _raw_stream(dev.index)),
-               "lora_add")
+        st = lib.spops_lora_add(x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out, rank, n,
+                                b, ldb, y, ldy, h.data_ptr() if return_h else 0, plan._ptr, _raw_stream(dev.index))
+    if st:
+        _check(st, "lora_add")
     return (out, h) if return_h else out
 
 
@@ -156,8 +169,8 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
     shared projection's own input gradient goes in as dX_base (dX_out=dX_base: in place). h: the
     one lora_add returned for this X (None: formed here). need: which of the three to compute;
     the others come back as None."""
-    dev, T, k, n_out, rank, n, s_ptr, s_all = _weights(X, A, B, plan, scale)
-    dt = X.dtype
+    dev, dt, k, n_out, rank, n, s_ptr, s_all = _weights(X, A, B, plan, scale)
+    T = plan.tokens
     x, ldx = _rows(X, "X", T, k, dt, dev)
     dy, lddy = _rows(dY, "dY", T, n_out, dt, dev)
     hp = 0
@@ -178,10 +191,14 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
             dA = torch.empty_like(A)
         if need[2]:
             dB = torch.empty_like(B)
-        size = lib.spops_lora_grad_workspace_size(T, rank)
+        size = plan._grad_ws.get(rank)
+        if size is None:
+            size = plan._grad_ws[rank] = int(lib.spops_lora_grad_workspace_size(T, rank))
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
-        _check(lib.spops_lora_grad(dy, lddy, x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out,
-                                   rank, n, hp, b, ldb, dx, lddx, dA.data_ptr() if need[1] else 0,
-                                   dB.data_ptr() if need[2] else 0, plan._ptr, ws.data_ptr(), size,
-                                   _raw_stream(dev.index)), "lora_grad")
+        st = lib.spops_lora_grad(dy, lddy, x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out,
+                                 rank, n, hp, b, ldb, dx, lddx, dA.data_ptr() if need[1] else 0,
+                                 dB.data_ptr() if need[2] else 0, plan._ptr, ws.data_ptr(), size,
+                                 _raw_stream(dev.index))
+    if st:
+        _check(st, "lora_grad")
     return dX, dA, dB
