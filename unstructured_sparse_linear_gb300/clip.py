@@ -22,7 +22,9 @@ class GradSet:
     """Gradients that are clipped together (fp32, fp16 and bf16 mixed; contiguous; on one
     device). Holds the tensors and a device table of their addresses, so it serves every step
     that writes its gradients into the same buffers; new buffers need a new set. out: tensors
-    of the same sizes and types that receive the clipped gradients (default: in place)."""
+    of the same sizes and types that receive the clipped gradients (default: in place). The set
+    keeps the calls' partial sums, so calls on one set run one after the other (on one stream, or on
+    streams that wait for each other)."""
 
     def __init__(self, grads, out=None):
         self.grads = list(grads)
@@ -51,6 +53,9 @@ class GradSet:
         self._ptr, self._n = self._table.data_ptr(), n
         self._chunks, self._in_place = chunks.value, in_place.value
         self._ws = int(lib.spops_grad_norm_workspace_size())
+        with torch.cuda.device(self.device):
+            self._partial = torch.empty(self._ws, dtype=torch.uint8, device=self.device)
+        self._partial_ptr = self._partial.data_ptr()
 
     def __len__(self):
         return self._n
@@ -67,8 +72,7 @@ def grad_norm(grads) -> torch.Tensor:
     dev = s.device
     with _on(dev):
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        ws = torch.empty(s._ws, dtype=torch.uint8, device=dev)
-        _check(_L().spops_grad_norm(s._ptr, s._n, s._chunks, norm.data_ptr(), ws.data_ptr(), s._ws,
+        _check(_L().spops_grad_norm(s._ptr, s._n, s._chunks, norm.data_ptr(), s._partial_ptr, s._ws,
                                     _raw_stream(dev.index)), "grad_norm")
     return norm
 
@@ -82,9 +86,8 @@ def clip_grads(grads, max_norm: float) -> torch.Tensor:
     dev = s.device
     with _on(dev):
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        ws = torch.empty(s._ws, dtype=torch.uint8, device=dev)
         st = _L().spops_clip_grads(s._ptr, s._n, s._chunks, s._in_place, float(max_norm), norm.data_ptr(),
-                                   ws.data_ptr(), s._ws, _raw_stream(dev.index))
+                                   s._partial_ptr, s._ws, _raw_stream(dev.index))
     if st:
         _check(st, "clip_grads")
     return norm

@@ -18,6 +18,14 @@ struct LoraTile {
     int32_t adapter, pos0, rows, tok0;
 };
 
+// A tile of the general kernels, with its tokens in place: these serve small batches too, where
+// every dependent load counts.
+struct alignas(16) LoraSmall {
+    int32_t adapter, rows;
+    int32_t tok[kLoraRows];
+    int32_t pad[2];
+};
+
 constexpr int kLoraHdr = 16;  // header words: counts[kLoraCnt...]
 enum LoraCount { kLoraCntTiles = 0, kLoraCntSmall = 1, kLoraCntWith = 2 };
 
@@ -33,7 +41,7 @@ struct LoraPlanView {
     int32_t* tstart;  // [n + 2] scratch: first tile of each adapter
     int32_t* aorder;  // [n] the adapters, those with the most tokens first
     LoraTile* tiles;
-    LoraTile* small;
+    LoraSmall* small;
     int32_t tokens, n;
 };
 
@@ -44,7 +52,8 @@ inline size_t lora_words4(int64_t words) { return (size_t)((words + 3) / 4 * 4);
 
 inline size_t lora_plan_bytes(int32_t tokens, int32_t n) {
     return 4 * (kLoraHdr + 2 * lora_words4(tokens) + 3 * lora_words4((int64_t)n + 2)) +
-           sizeof(LoraTile) * (size_t)(lora_tiles_cap(tokens, n, kLoraTile) + lora_tiles_cap(tokens, n, kLoraRows));
+           sizeof(LoraTile) * (size_t)lora_tiles_cap(tokens, n, kLoraTile) +
+           sizeof(LoraSmall) * (size_t)lora_tiles_cap(tokens, n, kLoraRows);
 }
 
 inline LoraPlanView lora_plan_view(const void* plan, int32_t tokens, int32_t n) {
@@ -57,7 +66,7 @@ inline LoraPlanView lora_plan_view(const void* plan, int32_t tokens, int32_t n) 
     v.tstart = v.off + lora_words4((int64_t)n + 2);
     v.aorder = v.tstart + lora_words4((int64_t)n + 2);
     v.tiles = reinterpret_cast<LoraTile*>(v.aorder + lora_words4((int64_t)n + 2));
-    v.small = v.tiles + lora_tiles_cap(tokens, n, kLoraTile);
+    v.small = reinterpret_cast<LoraSmall*>(v.tiles + lora_tiles_cap(tokens, n, kLoraTile));
     v.tokens = tokens;
     v.n = n;
     return v;

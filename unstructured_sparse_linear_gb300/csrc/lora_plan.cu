@@ -51,8 +51,28 @@ __device__ __forceinline__ int block_exclusive(int x, int* s_warp, int* total) {
     return inc - x + (warp ? s_warp[warp - 1] : 0);
 }
 
+__device__ __forceinline__ void write_tile(LoraTile* out, const LoraPlanView& v, int adapter, int p0, int n) {
+    const int t0 = v.order[p0];
+    LoraTile t;
+    t.adapter = adapter;
+    t.pos0 = p0;
+    t.rows = n;
+    t.tok0 = v.order[p0 + n - 1] - t0 == n - 1 ? t0 : -1;  // ascending, so consecutive
+    *out = t;
+}
+__device__ __forceinline__ void write_tile(LoraSmall* out, const LoraPlanView& v, int adapter, int p0, int n) {
+    LoraSmall t;
+    t.adapter = adapter;
+    t.rows = n;
+#pragma unroll
+    for (int i = 0; i < kLoraRows; ++i) t.tok[i] = v.order[p0 + min(i, n - 1)];
+    t.pad[0] = t.pad[1] = 0;
+    *out = t;
+}
+
 // Tiles of at most `rows` rows for adapters 0 .. na - 1 of off; returns their number.
-__device__ int build_tiles(const LoraPlanView& v, int na, int rows, LoraTile* tiles, int* s_warp) {
+template <typename Tile>
+__device__ int build_tiles(const LoraPlanView& v, int na, int rows, Tile* tiles, int* s_warp) {
     int carry = 0;
     for (int a0 = 0; a0 < na; a0 += kPlanThreads) {
         const int a = a0 + threadIdx.x;
@@ -72,14 +92,7 @@ __device__ int build_tiles(const LoraPlanView& v, int na, int rows, LoraTile* ti
             else hi = mid - 1;
         }
         const int p0 = v.off[lo] + (i - v.tstart[lo]) * rows;
-        const int n = min(rows, v.off[lo + 1] - p0);
-        const int t0 = v.order[p0];
-        LoraTile t;
-        t.adapter = lo < v.n ? lo : -1;
-        t.pos0 = p0;
-        t.rows = n;
-        t.tok0 = v.order[p0 + n - 1] - t0 == n - 1 ? t0 : -1;  // ascending, so consecutive
-        tiles[i] = t;
+        write_tile(tiles + i, v, lo < v.n ? lo : -1, p0, min(rows, v.off[lo + 1] - p0));
     }
     __syncthreads();
     return carry;

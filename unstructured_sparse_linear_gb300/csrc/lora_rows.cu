@@ -26,6 +26,7 @@ struct RowsArgs {
     LoraPlanView v;
     int vec;      // 16-byte loads of U and A/B rows along K (forward)
     int vec_r;    // 16-byte loads of B rows along rank (forward)
+    int vec_copy;  // 16-byte accesses of base and O
 };
 
 // Elements [i, i + V) of p as floats; vec: one 16-byte load.
@@ -99,8 +100,8 @@ __device__ __forceinline__ void phase1_forward(const T* const* urow, const T* A,
 // Gradient direction: part[warp][row][j] = sum over k = this CTA's share, dealt to the warps,
 // of U[row, k] B[k, j]. Lanes along j (rank is the contiguous axis of B); with rank <= 16 a
 // warp takes 32 / jl rows of B at once.
-template <typename T>
-__device__ __forceinline__ void phase1_backward(const T* const* urow, int rows, const T* B, int64_t k0, int64_t k1,
+template <typename T, int NR>
+__device__ __forceinline__ void phase1_backward(const T* const* urow, const T* B, int64_t k0, int64_t k1,
                                                 int rank, int rp, float* part) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int jl = 32;
@@ -108,20 +109,19 @@ __device__ __forceinline__ void phase1_backward(const T* const* urow, int rows, 
     const int kl = 32 / jl, kq = lane / jl, j0 = lane & (jl - 1);
     for (int jb = 0; jb < rank; jb += 32) {
         const int j = jb + j0;
-        float acc[R];
+        float acc[NR];
 #pragma unroll
-        for (int i = 0; i < R; ++i) acc[i] = 0.f;
+        for (int i = 0; i < NR; ++i) acc[i] = 0.f;
         if (j < rank) {
 #pragma unroll 2
             for (int64_t k = k0 + warp * kl + kq; k < k1; k += kWarps * kl) {
                 const float w = Elt<T>::to_f(B[k * rank + j]);
 #pragma unroll
-                for (int i = 0; i < R; ++i)
-                    if (i < rows) acc[i] = fmaf(w, Elt<T>::to_f(urow[i][k]), acc[i]);
+                for (int i = 0; i < NR; ++i) acc[i] = fmaf(w, Elt<T>::to_f(urow[i][k]), acc[i]);
             }
         }
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
+        for (int i = 0; i < NR; ++i) {
             float x = acc[i];
             for (int d = 16; d >= jl; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
             if (lane < jl && j < rank) part[((size_t)warp * R + i) * rp + j] = x;
@@ -129,118 +129,252 @@ __device__ __forceinline__ void phase1_backward(const T* const* urow, int rows, 
     }
 }
 
+// barrier.cluster in two halves: what a CTA does between them overlaps the others' arrival.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The tile's P of one rank (rows 0 .. NR - 1), from shared memory.
+template <int NR>
+__device__ __forceinline__ void load_h(const float* p, float (&h)[NR]) {
+    if constexpr (NR >= 4) {
+#pragma unroll
+        for (int i = 0; i < NR / 4; ++i) {
+            const float4 v = reinterpret_cast<const float4*>(p)[i];
+            h[4 * i] = v.x;
+            h[4 * i + 1] = v.y;
+            h[4 * i + 2] = v.z;
+            h[4 * i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NR; ++i) h[i] = p[i];
+    }
+}
+
+// Columns [n0, n1) of O = base (zeros) for the rows tok[0 .. rows), several loads under way.
+template <typename T>
+__device__ __forceinline__ void copy_rows(const RowsArgs& g, const int32_t* tok, int rows, int64_t n0, int64_t n1) {
+    const T* base = static_cast<const T*>(g.a.base);
+    T* O = static_cast<T*>(g.a.O);
+    if (!O || (const T*)O == base || n1 <= n0) return;
+    const int64_t ldo = g.a.ldo, ldb = g.a.ldb;
+    if (g.vec_copy) {
+        constexpr int V = Elt<T>::kVec;
+        const int per = (int)((n1 - n0) / V), total = rows * per;
+#pragma unroll 4
+        for (int x = threadIdx.x; x < total; x += kThreads) {
+            const int64_t t = tok[x / per], n = n0 + (int64_t)(x % per) * V;
+            *reinterpret_cast<uint4*>(O + t * ldo + n) = base ? ld_v4(base + t * ldb + n) : make_uint4(0, 0, 0, 0);
+        }
+    } else {
+        const int64_t per = n1 - n0, total = rows * per;
+#pragma unroll 4
+        for (int64_t x = threadIdx.x; x < total; x += kThreads) {
+            const int64_t t = tok[x / per], n = n0 + x % per;
+            O[t * ldo + n] = base ? base[t * ldb + n] : Elt<T>::from_f(0.f);
+        }
+    }
+}
+
+constexpr int kCols = 2;  // columns of O per thread at a time, kThreads apart
+
+// One tile of NR rows at most: this CTA's shares of K and of the columns.
+template <typename T, bool kBack, int NR>
+__device__ __forceinline__ void one_tile(const RowsArgs& g, const LoraSmall* tile, const LoraSmall& t, float* part,
+                                         float (*hs)[R], int C, int crank, int ksplit, int rp, int64_t k0, int64_t k1,
+                                         int64_t n0, int64_t n1) {
+    constexpr int V = Elt<T>::kVec;
+    const LoraArgs& a = g.a;
+    const int tid = threadIdx.x, r = a.rank;
+    const int64_t K = a.K, N = a.N;
+    const T* A = static_cast<const T*>(a.A) + (int64_t)t.adapter * r * (kBack ? N : K);
+    const T* B = static_cast<const T*>(a.B) + (int64_t)t.adapter * r * (kBack ? K : N);
+    const T* base = static_cast<const T*>(a.base);
+    T* O = static_cast<T*>(a.O);
+    const T* urow[NR];
+#pragma unroll
+    for (int i = 0; i < NR; ++i) urow[i] = static_cast<const T*>(a.U) + (int64_t)t.tok[i] * a.ldu;
+
+    // Columns n0 + tid + q kThreads of O at a time. The first ones' weights (16 ranks) and base do
+    // not depend on P: they are on their way while P is formed, where the registers allow. (Two
+    // columns measured better than four, and than loading the next ones ahead: 64 tokens of 48
+    // adapters, 4096 to 11008, 10.8 us against 13.2 and 11.5.)
+    constexpr int kPre = 16 / V;
+    constexpr bool kPrefetch = !kBack && NR <= 2 && sizeof(T) == 2;
+    uint4 w0[kCols][kPre];
+    T b0[kCols][NR];
+    const bool pre = kPrefetch && g.vec_r && r >= 16 && O;
+    const int64_t col = n0 + tid;
+    const int64_t bstep = (int64_t)kThreads * r;
+    if (pre) {
+        const T* b = B + col * r;
+#pragma unroll
+        for (int q = 0; q < kCols; ++q, b += bstep) {
+            const bool in = col + q * kThreads < n1;
+#pragma unroll
+            for (int i = 0; i < kPre; ++i) w0[q][i] = in ? ld_v4(b + i * V) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < NR; ++i)
+                if (base && in) b0[q][i] = base[(int64_t)t.tok[i] * a.ldb + col + q * kThreads];
+        }
+    }
+    const float s = a.scale_all * (a.scale ? a.scale[t.adapter] : 1.f);
+
+    if constexpr (kBack) phase1_backward<T, NR>(urow, B, k0, k1, r, rp, part);
+    else if (g.vec) phase1_forward<T, NR, true>(urow, A, K, k0, k1, r, ksplit, rp, part);
+    else phase1_forward<T, NR, false>(urow, A, K, k0, k1, r, ksplit, rp, part);
+    if (C > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    for (int x = tid; x < t.rows * r; x += kThreads) {
+        const int i = x / r, j = x - i * r;
+        // in the order of (share of K, rank), eight loads under way at a time
+        float sum = 0.f;
+        for (int ks = 0; ks < ksplit; ++ks) {
+            const float* p = part + ((size_t)ks * R + i) * rp + j;
+            if (C > 1) {
+                const uint32_t at = smem_u32(p);
+                float v[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] = q < C ? __uint_as_float(ld_cluster_u32(cluster_map(at, q))) : 0.f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) sum += v[q];
+            } else {
+                sum += *p;
+            }
+        }
+        hs[j][i] = sum * s;
+        if (a.P && crank == 0) a.P[(int64_t)tile->tok[i] * r + j] = sum;
+    }
+    // Every rank has read the partial sums once all have passed the wait below (they are rewritten
+    // by the next tile, and no CTA leaves while another still reads its shared memory).
+    if (C > 1) cluster_arrive();
+    __syncthreads();
+    if (O)
+        for (int64_t n = col; n - tid < n1; n += kCols * kThreads) {
+            float acc[kCols][NR];
+            bool in[kCols];
+            const bool first = pre && n == col;
+#pragma unroll
+            for (int q = 0; q < kCols; ++q) {
+                in[q] = n + q * kThreads < n1;
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    acc[q][i] = 0.f;
+                    if (base && in[q])
+                        acc[q][i] = Elt<T>::to_f(first ? b0[q][i] : base[(int64_t)t.tok[i] * a.ldb + n + q * kThreads]);
+                }
+            }
+            auto step = [&](int j, const float (&w)[kCols]) {
+                float h[NR];
+                load_h<NR>(hs[j], h);
+#pragma unroll
+                for (int q = 0; q < kCols; ++q)
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) acc[q][i] = fmaf(w[q], h[i], acc[q][i]);
+            };
+            if constexpr (kBack) {
+#pragma unroll 4
+                for (int j = 0; j < r; ++j) {
+                    float w[kCols];
+#pragma unroll
+                    for (int q = 0; q < kCols; ++q) w[q] = in[q] ? Elt<T>::to_f(A[(int64_t)j * N + n + q * kThreads]) : 0.f;
+                    step(j, w);
+                }
+            } else if (g.vec_r) {
+                auto steps = [&](int j, const uint4 (&v)[kCols]) {
+                    float f[kCols][V];
+#pragma unroll
+                    for (int q = 0; q < kCols; ++q) Elt<T>::unpack(v[q], f[q]);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        float w[kCols];
+#pragma unroll
+                        for (int q = 0; q < kCols; ++q) w[q] = f[q][e];
+                        step(j + e, w);
+                    }
+                };
+                int j = 0;
+                if (kPrefetch && first) {
+#pragma unroll
+                    for (int i = 0; i < kPre; ++i) {
+                        uint4 v[kCols];
+#pragma unroll
+                        for (int q = 0; q < kCols; ++q) v[q] = w0[q][i];
+                        steps(i * V, v);
+                    }
+                    j = 16;
+                }
+                const T* b = B + n * r;
+                for (; j < r; j += V) {
+                    uint4 v[kCols];
+#pragma unroll
+                    for (int q = 0; q < kCols; ++q) v[q] = in[q] ? ld_v4(b + q * bstep + j) : make_uint4(0, 0, 0, 0);
+                    steps(j, v);
+                }
+            } else {
+                const T* b = B + n * r;
+#pragma unroll 4
+                for (int j = 0; j < r; ++j) {
+                    float w[kCols];
+#pragma unroll
+                    for (int q = 0; q < kCols; ++q) w[q] = in[q] ? Elt<T>::to_f(b[q * bstep + j]) : 0.f;
+                    step(j, w);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < kCols; ++q)
+#pragma unroll
+                for (int i = 0; i < NR; ++i)
+                    if (in[q] && i < t.rows)
+                        O[(int64_t)t.tok[i] * a.ldo + n + q * kThreads] = Elt<T>::from_f(acc[q][i]);
+        }
+    if (C > 1) cluster_wait();
+}
+
 template <typename T, bool kBack>
-__global__ void __launch_bounds__(kThreads) lora_rows_kernel(const RowsArgs g) {
+__global__ void __launch_bounds__(kThreads, 2) lora_rows_kernel(const RowsArgs g) {
     extern __shared__ __align__(16) float part[];  // [ksplit][R][rp]
     __shared__ __align__(16) float hs[kLoraMaxRank][R];
-    __shared__ int s_tok[R];
     const LoraArgs& a = g.a;
     const int tid = threadIdx.x;
     const int C = (int)cluster_size(), crank = (int)cluster_rank();
     const int cid = blockIdx.x / C, ncl = gridDim.x / C;
+    // (the list has a slot for every cluster; what lies behind its end is not used)
+    LoraSmall t = g.v.small[cid];
+    const int ntiles = g.v.counts[kLoraCntSmall];
     const int r = a.rank;
     const int njg = (r + kJW - 1) / kJW;
     const int ksplit = kBack ? kWarps : (njg >= kWarps ? 1 : kWarps / njg);
     const int rp = (r + 3) & ~3;
-    const int64_t K = a.K, N = a.N;
-    // shares of K and of the columns in units of 8 elements
-    const int64_t ku = (K + 7) / 8, nu = (N + 7) / 8;
-    const int64_t k0 = ku * crank / C * 8, k1 = min64(K, ku * (crank + 1) / C * 8);
-    const int64_t n0 = nu * crank / C * 8, n1 = min64(N, nu * (crank + 1) / C * 8);
-    const int ntiles = g.v.counts[kLoraCntSmall];
-    const T* U = static_cast<const T*>(a.U);
-    const T* base = static_cast<const T*>(a.base);
-    T* O = static_cast<T*>(a.O);
+    // shares of K and of the columns in units of 8 elements (C is a power of two)
+    const int clog = 31 - __clz(C);
+    const int64_t ku = (a.K + 7) / 8, nu = (a.N + 7) / 8;
+    const int64_t k0 = (ku * crank >> clog) * 8, k1 = min64(a.K, (ku * (crank + 1) >> clog) * 8);
+    const int64_t n0 = (nu * crank >> clog) * 8, n1 = min64(a.N, (nu * (crank + 1) >> clog) * 8);
 
     // The trip count and every barrier are the same on all CTAs of a cluster.
     for (int it = cid; it < ntiles; it += ncl) {
-        const LoraTile t = g.v.small[it];
-        __syncthreads();  // the previous tile's tokens and sums have been read
-        if (tid < R) s_tok[tid] = tid < t.rows ? g.v.order[t.pos0 + tid] : -1;
-        __syncthreads();
+        if (it != cid) {
+            t = g.v.small[it];
+            __syncthreads();  // the previous tile's P has been read
+        }
         if (t.adapter < 0) {  // no adapter: O = base, P = 0
-            for (int i = 0; i < t.rows; ++i) {
-                const int64_t tok = s_tok[i];
-                if (O && (const T*)O != base)
-                    for (int64_t n = n0 + tid; n < n1; n += kThreads)
-                        O[tok * a.ldo + n] = base ? base[tok * a.ldb + n] : Elt<T>::from_f(0.f);
-                if (a.P && crank == 0)
-                    for (int j = tid; j < r; j += kThreads) a.P[tok * r + j] = 0.f;
-            }
-            continue;
-        }
-        const T* A = static_cast<const T*>(a.A) + (int64_t)t.adapter * r * (kBack ? N : K);
-        const T* B = static_cast<const T*>(a.B) + (int64_t)t.adapter * r * (kBack ? K : N);
-        const T* urow[R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) urow[i] = U + (int64_t)s_tok[min(i, t.rows - 1)] * a.ldu;
-        if constexpr (kBack) {
-            phase1_backward<T>(urow, t.rows, B, k0, k1, r, rp, part);
-        } else if (g.vec) {
-            if (t.rows == 1) phase1_forward<T, 1, true>(urow, A, K, k0, k1, r, ksplit, rp, part);
-            else if (t.rows == 2) phase1_forward<T, 2, true>(urow, A, K, k0, k1, r, ksplit, rp, part);
-            else if (t.rows <= 4) phase1_forward<T, 4, true>(urow, A, K, k0, k1, r, ksplit, rp, part);
-            else phase1_forward<T, 8, true>(urow, A, K, k0, k1, r, ksplit, rp, part);
+            copy_rows<T>(g, g.v.small[it].tok, t.rows, n0, n1);
+            if (a.P && crank == 0)
+                for (int x = tid; x < t.rows * r; x += kThreads)
+                    a.P[(int64_t)g.v.small[it].tok[x / r] * r + x % r] = 0.f;
+        } else if (t.rows == 1) {
+            one_tile<T, kBack, 1>(g, g.v.small + it, t, part, hs, C, crank, ksplit, rp, k0, k1, n0, n1);
+        } else if (t.rows == 2) {
+            one_tile<T, kBack, 2>(g, g.v.small + it, t, part, hs, C, crank, ksplit, rp, k0, k1, n0, n1);
+        } else if (t.rows <= 4) {
+            one_tile<T, kBack, 4>(g, g.v.small + it, t, part, hs, C, crank, ksplit, rp, k0, k1, n0, n1);
         } else {
-            phase1_forward<T, 8, false>(urow, A, K, k0, k1, r, ksplit, rp, part);
-        }
-        if (C > 1) cluster_sync();
-        else __syncthreads();
-        const float s = a.scale_all * (a.scale ? a.scale[t.adapter] : 1.f);
-        for (int x = tid; x < t.rows * r; x += kThreads) {
-            const int i = x / r, j = x - i * r;
-            float sum = 0.f;
-            for (int q = 0; q < C; ++q)
-                for (int ks = 0; ks < ksplit; ++ks) {
-                    const float* p = part + ((size_t)ks * R + i) * rp + j;
-                    sum += C > 1 ? __uint_as_float(ld_cluster_u32(cluster_map(smem_u32(p), q))) : *p;
-                }
-            hs[j][i] = sum * s;
-            if (a.P && crank == 0) a.P[(int64_t)s_tok[i] * r + j] = sum;
-        }
-        // every rank has read the partial sums (they are rewritten by the next tile, and no CTA
-        // leaves while another still reads its shared memory)
-        if (C > 1) cluster_sync();
-        else __syncthreads();
-        if (!O) continue;
-        for (int64_t n = n0 + tid; n < n1; n += kThreads) {
-            float acc[R];
-#pragma unroll
-            for (int i = 0; i < R; ++i) acc[i] = 0.f;
-            auto step = [&](int j, float w) {
-                const float4 x = *reinterpret_cast<const float4*>(&hs[j][0]);
-                const float4 y = *reinterpret_cast<const float4*>(&hs[j][4]);
-                acc[0] = fmaf(w, x.x, acc[0]);
-                acc[1] = fmaf(w, x.y, acc[1]);
-                acc[2] = fmaf(w, x.z, acc[2]);
-                acc[3] = fmaf(w, x.w, acc[3]);
-                acc[4] = fmaf(w, y.x, acc[4]);
-                acc[5] = fmaf(w, y.y, acc[5]);
-                acc[6] = fmaf(w, y.z, acc[6]);
-                acc[7] = fmaf(w, y.w, acc[7]);
-            };
-            if constexpr (kBack) {
-#pragma unroll 4
-                for (int j = 0; j < r; ++j) step(j, Elt<T>::to_f(A[(int64_t)j * N + n]));
-            } else if (g.vec_r) {
-                constexpr int V = Elt<T>::kVec;
-                for (int j = 0; j < r; j += V) {
-                    float w[V];
-                    load_vec(B + n * r + j, w);
-#pragma unroll
-                    for (int e = 0; e < V; ++e) step(j + e, w[e]);
-                }
-            } else {
-#pragma unroll 4
-                for (int j = 0; j < r; ++j) step(j, Elt<T>::to_f(B[n * r + j]));
-            }
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-                if (i < t.rows) {
-                    const int64_t tok = s_tok[i];
-                    const float b = base ? Elt<T>::to_f(base[tok * a.ldb + n]) : 0.f;
-                    O[tok * a.ldo + n] = Elt<T>::from_f(b + acc[i]);
-                }
+            one_tile<T, kBack, 8>(g, g.v.small + it, t, part, hs, C, crank, ksplit, rp, k0, k1, n0, n1);
         }
     }
 }
@@ -323,9 +457,10 @@ __global__ void __launch_bounds__(kThreads) lora_wgrad_rows_kernel(const WgradRo
     if (C > 1) cluster_sync();
 }
 
-// Cluster size for `items` clusters: enough CTAs for two per SM, at most 8 (the portable limit).
+// Cluster size for `items` clusters: CTAs for two per SM and a little more (items is a bound that
+// few batches reach), at most 8 (the portable limit).
 int pick_cluster(int64_t items, int64_t most) {
-    const int64_t want = 2 * (int64_t)device_props().sm_count;
+    const int64_t want = (int64_t)device_props().sm_count * 33 / 10;
     int c = 1;
     while (c < 8 && items * c * 2 <= want && c * 2 <= most) c *= 2;
     return c;
@@ -359,6 +494,7 @@ cudaError_t run_rows(bool back, const LoraArgs& a, const LoraPlanView& v, cudaSt
     constexpr int V = Elt<T>::kVec;
     g.vec = a.K % V == 0 && a.ldu % V == 0 && ((uintptr_t)a.U | (uintptr_t)a.A) % 16 == 0;
     g.vec_r = a.rank % V == 0 && (uintptr_t)a.B % 16 == 0;
+    g.vec_copy = a.N % 8 == 0 && a.ldo % V == 0 && a.ldb % V == 0 && ((uintptr_t)a.O | (uintptr_t)a.base) % 16 == 0;
     const int64_t cap = lora_tiles_cap(v.tokens, v.n, kLoraRows);
     const int c = pick_cluster(cap, max64(1, max64(a.K, a.N) / 64));
     const int64_t clusters = min64(cap, (int64_t)device_props().sm_count * 8);

@@ -164,11 +164,20 @@ def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h:
     return (out, h) if return_h else out
 
 
-def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_out=None, need=(True, True, True)):
+def _like(t, w, name):
+    _req(t, name, w.dtype, device=w.device)
+    if t.shape != w.shape:
+        raise ValueError(f"{name} must be {tuple(w.shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_out=None, dA_out=None, dB_out=None,
+              need=(True, True, True)):
     """(dX, dA, dB) of lora_add for the output gradient dY. dX = dX_base + s_i (dY B_i) A_i, so the
     shared projection's own input gradient goes in as dX_base (dX_out=dX_base: in place). h: the
     one lora_add returned for this X (None: formed here). need: which of the three to compute;
-    the others come back as None."""
+    the others come back as None. dA_out, dB_out: buffers for the weights' gradients (such as those of
+    a GradSet), overwritten."""
     dev, dt, k, n_out, rank, n, s_ptr, s_all = _weights(X, A, B, plan, scale)
     T = plan.tokens
     x, ldx = _rows(X, "X", T, k, dt, dev)
@@ -188,9 +197,9 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
             dX = dX_out if dX_out is not None else torch.empty((T, k), dtype=dt, device=dev)
             dx, lddx = _rows(dX, "dX_out", T, k, dt, dev)
         if need[1]:
-            dA = torch.empty_like(A)
+            dA = _like(dA_out, A, "dA_out") if dA_out is not None else torch.empty_like(A)
         if need[2]:
-            dB = torch.empty_like(B)
+            dB = _like(dB_out, B, "dB_out") if dB_out is not None else torch.empty_like(B)
         size = plan._grad_ws.get(rank)
         if size is None:
             size = plan._grad_ws[rank] = int(lib.spops_lora_grad_workspace_size(T, rank))
