@@ -457,10 +457,10 @@ __global__ void __launch_bounds__(kThreads) lora_wgrad_rows_kernel(const WgradRo
     if (C > 1) cluster_sync();
 }
 
-// Cluster size for `items` clusters: CTAs for two per SM and a little more (items is a bound that
-// few batches reach), at most 8 (the portable limit).
+// Cluster size for `items` clusters: CTAs for at most two per SM at once (384 tokens of one adapter
+// in clusters of 8 were two waves, 16.6 us; 12 us in clusters of 4), at most 8 (the portable limit).
 int pick_cluster(int64_t items, int64_t most) {
-    const int64_t want = (int64_t)device_props().sm_count * 33 / 10;
+    const int64_t want = 2 * (int64_t)device_props().sm_count;
     int c = 1;
     while (c < 8 && items * c * 2 <= want && c * 2 <= most) c *= 2;
     return c;
@@ -496,7 +496,10 @@ cudaError_t run_rows(bool back, const LoraArgs& a, const LoraPlanView& v, cudaSt
     g.vec_r = a.rank % V == 0 && (uintptr_t)a.B % 16 == 0;
     g.vec_copy = a.N % 8 == 0 && a.ldo % V == 0 && a.ldb % V == 0 && ((uintptr_t)a.O | (uintptr_t)a.base) % 16 == 0;
     const int64_t cap = lora_tiles_cap(v.tokens, v.n, kLoraRows);
-    const int c = pick_cluster(cap, max64(1, max64(a.K, a.N) / 64));
+    // the tiles to expect: cap is reached only where every adapter has a token and a last tile of its
+    // own; tokens that pick adapters at random use about 0.6 of them when they are as many
+    const int64_t expected = v.tokens / R + (6 * min64(v.tokens, v.n) + 9) / 10;
+    const int c = pick_cluster(expected, max64(1, max64(a.K, a.N) / 64));
     const int64_t clusters = min64(cap, (int64_t)device_props().sm_count * 8);
     const int rp = (a.rank + 3) & ~3, njg = (a.rank + kJW - 1) / kJW;
     const int ksplit = back ? kWarps : (njg >= kWarps ? 1 : kWarps / njg);
@@ -541,14 +544,29 @@ cudaError_t launch_lora_wgrad_rows(int dt, const LoraWgradArgs* w, int nw, int32
     return run_wgrad_rows<__nv_bfloat16>(w, nw, rank, scale, scale_all, v, s);
 }
 
+// Which kernels: the general one multiplies T r (K + N) times on the CUDA cores and reads an
+// adapter's weights for every 8 rows, the tensor-core one has about 16 us of latency (two phases
+// with an exchange between them) and reads the weights for every 128 rows, so for every adapter of
+// a mixed batch. Measured (bf16, us, general : tensor cores):
+//   forward, 4096 -> 4096, rank 16: 512 tokens of one adapter 12.4 : 16.4, 1024 18.4 : 16.5; of 48
+//   adapters 1024 tokens 19.0 : 32.2; 2048 -> 8192, rank 64: 128 tokens of one adapter 24 : 24, 256
+//   of 8 25 : 26, 384 43 : 31, of 48 adapters 384 41 : 43, 512 59 : 46;
+//   input gradient (whose general form reads B element by element): rank 16, 256 tokens of one adapter
+//   13.4 : 16.2, 512 20 : 16; of 48 256 19.6 : 27.5, 512 33 : 29; rank 64, 16 tokens 46 : 20.
+static bool general_is_faster(bool back, const LoraArgs& a, const LoraPlanView& v) {
+    const int64_t work = (int64_t)v.tokens * a.rank, adapters = min64(v.n, 22);
+    if (back) return a.rank <= 32 && work <= 4096 + 256 * min64(v.n, 8);
+    return work <= 10240 + 1024 * adapters;
+}
+
 cudaError_t launch_lora(int dt, bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) {
-    if (v.tokens > 64 && lora_tiles_ok(dt, a, v)) return launch_lora_tiles(dt, back, a, v, s);
+    if (lora_tiles_ok(dt, a, v) && !general_is_faster(back, a, v)) return launch_lora_tiles(dt, back, a, v, s);
     return launch_lora_rows(dt, back, a, v, s);
 }
 
 cudaError_t launch_lora_wgrad(int dt, const LoraWgradArgs* w, int nw, int32_t rank, const float* scale,
                               float scale_all, const LoraPlanView& v, bool after_lora, cudaStream_t s) {
-    if (v.tokens > 64 && lora_wgrad_tiles_ok(dt, w, nw))
+    if (v.tokens > 16 && lora_wgrad_tiles_ok(dt, w, nw))  // (16 tokens: 5 to 9 us either way)
         return launch_lora_wgrad_tiles(dt, w, nw, rank, scale, scale_all, v, after_lora, s);
     return launch_lora_wgrad_rows(dt, w, nw, rank, scale, scale_all, v, s);
 }
