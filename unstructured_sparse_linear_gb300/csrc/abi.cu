@@ -709,6 +709,15 @@ int spops_lora_grad(const void* dY, int64_t lddy, const void* X, int64_t ldx, co
     }
     LoraWgradArgs w[2];
     int nw = 0;
+    if (dB) {  // first: it depends on nothing that is still running
+        w[nw].U = dY;
+        w[nw].ldu = lddy;
+        w[nw].N = out_features;
+        w[nw].P = h;
+        w[nw].G = dB;
+        w[nw].rank_minor = true;
+        ++nw;
+    }
     if (dA) {
         w[nw].U = X;
         w[nw].ldu = ldx;
@@ -716,15 +725,6 @@ int spops_lora_grad(const void* dY, int64_t lddy, const void* X, int64_t ldx, co
         w[nw].P = dp;
         w[nw].G = dA;
         w[nw].dependent = true;
-        ++nw;
-    }
-    if (dB) {
-        w[nw].U = dY;
-        w[nw].ldu = lddy;
-        w[nw].N = out_features;
-        w[nw].P = h;
-        w[nw].G = dB;
-        w[nw].rank_minor = true;
         ++nw;
     }
     if (nw == 0) return ok();

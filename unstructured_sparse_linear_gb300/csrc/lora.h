@@ -45,8 +45,15 @@ struct LoraPlanView {
     int32_t tokens, n;
 };
 
+// The most tiles of up to `rows` rows that `tokens` tokens in `groups` groups can give: each group
+// that has a token may end with a tile of one row.
+inline int64_t lora_tiles_most(int32_t tokens, int64_t groups, int rows) {
+    const int64_t m = tokens < groups ? tokens : groups;
+    return (tokens - m) / rows + m;
+}
+// Slots of the two lists: adapters, and for the small tiles the tokens without one too.
 inline int64_t lora_tiles_cap(int32_t tokens, int32_t n, int rows) {
-    return (int64_t)tokens / rows + (tokens < n + 1 ? tokens : n + 1) + 1;
+    return lora_tiles_most(tokens, rows == kLoraRows ? (int64_t)n + 1 : n, rows);
 }
 inline size_t lora_words4(int64_t words) { return (size_t)((words + 3) / 4 * 4); }
 

@@ -550,6 +550,11 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
             const int tok_first = __shfl_sync(0xffffffffu, tok, 0);
             const bool run32 = __all_sync(0xffffffffu, row < t.rows && tok == tok_first + lane);
             const float s = g.scale_all * (g.scale ? g.scale[t.adapter] : 1.f);
+            // what this thread sums: columns 8 c8 .. of row r (`sums` is the same for a whole warp)
+            constexpr int kG = RP / 8;
+            const bool sums = et < own * kG;
+            const int rl = et / kG, c8 = et % kG, r = crank * own + rl;
+            const int ptok = g.P && sums && r < t.rows ? g.v.order[t.pos0 + r] : -1;  // and the token of that row
             q += nk;
             {
                 // Each rank sends its partial rows to the ranks that sum them, a slot per source.
@@ -581,9 +586,6 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
             wait.cluster(smem_u32(&sh.pub), tt & 1u);
             __syncwarp();
             // Sums in rank order: eight columns of one row per thread (the cluster is large enough).
-            constexpr int kG = RP / 8;
-            const bool sums = et < own * kG;  // the same for a whole warp
-            const int rl = et / kG, c8 = et % kG, r = crank * own + rl;
             float x[8];
             if (sums) {
 #pragma unroll
@@ -603,8 +605,8 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
             }
             named_barrier(1, kEpi);
             if (et < C) mbar_arrive_remote(smem_u32(&sh.read), et);
-            if (g.P && sums && r < t.rows) {
-                float* to = g.P + (int64_t)g.v.order[t.pos0 + r] * g.rank + c8 * 8;
+            if (ptok >= 0) {
+                float* to = g.P + (int64_t)ptok * g.rank + c8 * 8;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (c8 * 8 + e < g.rank) to[e] = x[e];
@@ -1186,11 +1188,14 @@ cudaError_t run_tiles(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) 
     g.rank = a.rank;
     g.scale_all = a.scale_all;
     g.err = device_error_word();
+    // As many CTAs per tile as the SMs hold at once for the tiles to expect (cap is the most there can
+    // be), and enough that a thread sums eight columns at most.
     const int64_t slots = (int64_t)device_props().sm_count * Cfg::kPerSm;
     const int64_t cap = lora_tiles_cap(v.tokens, v.n, kLoraTile);
-    // As many CTAs per tile as fill the SMs, and enough that a thread sums eight columns at most.
-    int c = Cfg::kMinCluster;
-    while (c < 8 && cap * c * 2 <= slots + slots / 8) c *= 2;
+    const int64_t expected =
+        min64(cap, ((int64_t)v.tokens + kLoraTile - 1) / kLoraTile + (v.n > 1 ? min64(v.tokens, v.n) / 2 : 0));
+    int c = 8;
+    while (c > Cfg::kMinCluster && expected * c > slots) c /= 2;
     const int64_t clusters = max64(1, min64(cap, slots / c));
     return launch_clusters(kern, clusters, c, kTileThreads, Cfg::kSmem, false, s, g, m);
 }
