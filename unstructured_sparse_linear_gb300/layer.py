@@ -18,7 +18,8 @@ from __future__ import annotations
 
 import torch
 
-from . import csr_transpose, permute_values, plan_build, sddmm, sort_rows, spmm
+from . import csr_add, csr_transpose, permute_values, plan_build, sddmm, sort_rows, spmm
+from .lora import lora_add, lora_grad, lora_plan
 
 
 class SparseLinearFunction(torch.autograd.Function):
@@ -65,3 +66,84 @@ class SparseLinear(torch.nn.Module):
 
     def forward(self, Xt: torch.Tensor) -> torch.Tensor:
         return SparseLinearFunction.apply(self.values, Xt.contiguous(), self)
+
+
+class RosaLinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, X, values, A, B, layer, plan):
+        W = layer.merged(values)
+        Y = X @ W.t()
+        Y, h = lora_add(X, A, B, plan, base=Y, scale=layer.scale, out=Y, return_h=True)
+        ctx.save_for_backward(X, values, A, B, h)
+        ctx.layer, ctx.plan = layer, plan
+        return Y
+
+    @staticmethod
+    def backward(ctx, dY):
+        X, values, A, B, h = ctx.saved_tensors
+        L = ctx.layer
+        dY = dY.contiguous()
+        need_x, need_v, need_a, need_b = ctx.needs_input_grad[:4]
+        # The merged weight is formed again: less time than its memory is worth in a deep model.
+        base = dY @ L.merged(values) if need_x else None
+        dX, dA, dB = lora_grad(dY, X, A, B, ctx.plan, scale=L.scale, h=h, dX_base=base, dX_out=base,
+                               need=(need_x, need_a, need_b))
+        dV = None
+        if need_v and values is not None:
+            dV = sddmm(L.row_offsets, L.row_idx, L.col_idx, dY.t().contiguous(), X.t().contiguous(), plan=L.plan)
+        return dX, dV, dA, dB, None, None
+
+
+class RosaLinear(torch.nn.Module):
+    """A frozen projection with a RoSA adapter, a sparse and a low-rank update (spops README,
+    "Sparse Operations (spops)": RoSA's sparse part is added to the weight with csr_add, and its
+    gradient is an SDDMM on the mask):
+
+        Y = X (W + S)^T + s_i (X A_i^T) B_i^T
+
+    weight: W [out, in], fp16 or bf16 (fp32 runs the general kernels), not trained. row_offsets,
+    col_idx, values: S on a fixed CSR mask, shared by all tokens (None: no sparse part). n_adapters
+    low-rank adapters of one rank, their factor `scale` a number or an fp32 tensor with one per
+    adapter; A starts at random and B at zero, so that the adapters start as no change. X is
+    token-major [..., in]; adapter_ids (int32, one per token) or a plan of them choose each token's
+    adapter, by default adapter 0 for all."""
+
+    def __init__(self, weight: torch.Tensor, rank: int, n_adapters: int = 1, scale=1.0, row_offsets=None, col_idx=None,
+                 values=None):
+        super().__init__()
+        self.out_features, self.in_features = weight.shape
+        self.n_adapters, self.scale = int(n_adapters), scale
+        self.register_buffer("weight", weight)
+        dev, dt = weight.device, weight.dtype
+        self.A = torch.nn.Parameter(torch.randn(self.n_adapters, rank, self.in_features, device=dev, dtype=torch.float32)
+                                    .mul_(self.in_features ** -0.5).to(dt))
+        self.B = torch.nn.Parameter(torch.zeros(self.n_adapters, self.out_features, rank, device=dev, dtype=dt))
+        if values is None:
+            self.values = None
+        else:
+            self.register_buffer("row_offsets", row_offsets)
+            self.register_buffer("col_idx", col_idx)
+            self.values = torch.nn.Parameter(values)
+            self.row_idx = sort_rows(row_offsets, nnz=col_idx.numel(), index_dtype=col_idx.dtype)
+            self.plan = plan_build(row_offsets, self.row_idx, col_idx, self.in_features)
+        self._plans = {}  # by number of tokens: every token uses adapter 0
+
+    def merged(self, values):
+        """W + S."""
+        if values is None:
+            return self.weight
+        return csr_add(values, self.row_offsets, self.row_idx, self.col_idx, self.weight)
+
+    def forward(self, X: torch.Tensor, adapter_ids: torch.Tensor | None = None, plan=None) -> torch.Tensor:
+        X2 = X.reshape(-1, self.in_features)
+        if plan is None and adapter_ids is not None:
+            plan = lora_plan(adapter_ids.reshape(-1), self.n_adapters)
+        if plan is None:
+            plan = self._plans.get(X2.shape[0])
+            if plan is None:
+                if len(self._plans) >= 64:  # (lengths that come and go)
+                    self._plans.clear()
+                plan = lora_plan(None, self.n_adapters, tokens=X2.shape[0], device=X2.device)
+                self._plans[X2.shape[0]] = plan
+        Y = RosaLinearFunction.apply(X2.contiguous(), self.values, self.A, self.B, self, plan)
+        return Y.reshape(*X.shape[:-1], self.out_features)
