@@ -150,16 +150,18 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
                  : "memory");
     return v;
 }
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint4 v) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+// Stores to shared memory of a CTA of the cluster that complete on a barrier of that CTA (bar and
+// addr both mapped there): the receiver waits for their bytes, the sender for nothing.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint4 v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar)
                  : "memory");
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void st_async_b32(uint32_t addr, uint32_t v, uint32_t bar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v),
+                 "r"(bar)
+                 : "memory");
 }
-// Orders this thread's earlier memory accesses with later ones of the asynchronous proxy, in
-// any state space.
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -409,12 +411,12 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
             mbar_init(smem_u32(&sh.empty[s]), 4);  // four commits, or the four warps of a group
         }
         mbar_init(smem_u32(&sh.d1), 1);
-        mbar_init(smem_u32(&sh.h), C);
+        mbar_init(smem_u32(&sh.h), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.d2_full[i]), 1);
             mbar_init(smem_u32(&sh.d2_empty[i]), 4);
         }
-        mbar_init(smem_u32(&sh.pub), C);
+        mbar_init(smem_u32(&sh.pub), 1);
         mbar_init(smem_u32(&sh.read), C);
         mbar_init(smem_u32(&sh.freed), C);
         mbar_init(smem_u32(&sh.drain), 1);
@@ -575,14 +577,20 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
                 // every rank is done with the last tile's parts of P, whose place the sums take
                 if (tt > 0) wait.cluster(smem_u32(&sh.freed), (tt - 1) & 1u);
                 __syncwarp();
-                const uint32_t dst = cluster_map(hbase + crank * own * (RP * 4), row >> (7 - clog));
+                const int to = row >> (7 - clog);
+                const uint32_t dst = cluster_map(hbase + crank * own * (RP * 4), to);
+                const uint32_t bar = cluster_map(smem_u32(&sh.pub), to);
 #pragma unroll
                 for (int c = 0; c < RP / 8; ++c)
-                    st_cluster_f4(dst + (uint32_t)p_place<RP>(row & (own - 1), grp * (RP / 8) + c, own) * 16,
-                                  make_float4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]));
+                    st_async_v4(dst + (uint32_t)p_place<RP>(row & (own - 1), grp * (RP / 8) + c, own) * 16,
+                                make_uint4(__float_as_uint(p[4 * c]), __float_as_uint(p[4 * c + 1]),
+                                           __float_as_uint(p[4 * c + 2]), __float_as_uint(p[4 * c + 3])),
+                                bar);
             }
-            named_barrier(1, kEpi);
-            if (et < C) mbar_arrive_remote(smem_u32(&sh.pub), et);
+            if (et == 0) {  // what is to arrive here: every rank's sums of `own` rows, then all rows' parts
+                mbar_arrive_expect_tx(smem_u32(&sh.pub), (uint32_t)kLoraTile * RP * 4);
+                mbar_arrive_expect_tx(smem_u32(&sh.h), (uint32_t)kLoraTile * (RP * 4 + (kF16 ? 4 : 0)));
+            }
             wait.cluster(smem_u32(&sh.pub), tt & 1u);
             __syncwarp();
             // Sums in rank order: eight columns of one row per thread (the cluster is large enough).
@@ -633,14 +641,13 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
                 const uint32_t at_hi = hbase + (c8 >> 3) * kUBytes + tc::sw128_off(r, c8 & 7);
                 const uint32_t at_lo = hbase + ((c8 + kG) >> 3) * kUBytes + tc::sw128_off(r, (c8 + kG) & 7);
                 for (int c = 0; c < C; ++c) {
-                    st_cluster_v4(cluster_map(at_hi, c), hi);
-                    st_cluster_v4(cluster_map(at_lo, c), lo);
-                    if (kF16 && c8 == 0) st_cluster_f32(cluster_map(smem_u32(&sh.down[r]), c), down);
+                    const uint32_t bar = cluster_map(smem_u32(&sh.h), c);
+                    st_async_v4(cluster_map(at_hi, c), hi, bar);
+                    st_async_v4(cluster_map(at_lo, c), lo, bar);
+                    if (kF16 && c8 == 0)
+                        st_async_b32(cluster_map(smem_u32(&sh.down[r]), c), __float_as_uint(down), bar);
                 }
             }
-            fence_proxy_async();
-            named_barrier(1, kEpi);
-            if (et < C) mbar_arrive_remote(smem_u32(&sh.h), et);
             wait.cluster(smem_u32(&sh.h), tt & 1u);
             __syncwarp();
             const float down = kF16 ? sh.down[row] : 1.f;
@@ -735,6 +742,9 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
     }
     tc::fence_before_sync();
     __syncthreads();
+    if (sh.failed && tid == 0)  // the other ranks' stores may still be on their way to this CTA and back
+        for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < kDrainNs / 100;) {
+        }
     if (C > 1) cluster_sync();  // nobody reads this CTA's sums or arrives on its barriers any more
     if (warp == 1) tc::tmem_dealloc(tmem, Cfg::kTmem);
 }
