@@ -141,6 +141,8 @@ SHAPES = [
     (257, 512, 256, 128, 3, "decode"), (515, 384, 1536, 8, 300, "decode"), (1000, 264, 520, 24, 4, "prompts"),
     (200, 64, 64, 2, 2, "none"), (1500, 1024, 768, 16, 1, "one"), (700, 96, 96, 100, 2, "prompts"),
     (260, 37, 51, 6, 3, "prompts"), (33, 1, 3, 1, 2, "decode"), (400, 45, 64, 8, 2, "prompts"),
+    (1, 256, 136, 64, 1, "one"), (3, 64, 72, 128, 2, "decode"), (17, 128, 64, 40, 1, "one"),
+    (3000, 72, 136, 12, 2, "prompts"), (1200, 64, 200, 18, 3, "decode"), (900, 200, 64, 36, 2, "prompts"),
 ]
 
 
@@ -150,6 +152,40 @@ def test_add_and_grad(shape, fmt):
     d = make(fmt, *shape)
     h = check_add(d, fmt)
     check_grad(d, fmt, h=h)
+
+
+# more tiles than the GPU holds at once: clusters of one CTA, of four and of eight, and the general kernel
+@pytest.mark.parametrize("fmt,shape", [("bf16", (45000, 64, 72, 16, 3, "prompts")), ("f16", (45000, 72, 64, 4, 1, "one")),
+                                       ("f16", (12500, 136, 64, 64, 2, "prompts")), ("bf16", (5200, 64, 136, 128, 2, "prompts")),
+                                       ("f32", (12500, 24, 40, 4, 2, "prompts"))], ids=str)
+def test_several_tiles_per_cluster(fmt, shape):
+    d = make(fmt, *shape)
+    h = check_add(d, fmt)
+    check_grad(d, fmt, h=h)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("shape", [(1500, 264, 328, 16, 1, "one"), (1300, 136, 264, 24, 3, "prompts"),
+                                   (800, 264, 136, 64, 2, "prompts")], ids=lambda s: "-".join(map(str, s)))
+def test_parts_alone_on_the_tensor_cores(shape, fmt):
+    """P without O (h formed inside, the weights' gradients without dX), O without base, rows in place."""
+    d = make(fmt, *shape, strided=True)
+    check_add(d, fmt, with_base=False)
+    check_grad(d, fmt, h=None)
+    for need in ((True, False, False), (False, True, False), (False, False, True), (False, True, True)):
+        check_grad(d, fmt, need=need)
+    h = check_add(dict(d, base=d["base"].clone()), fmt)
+    check_grad(d, fmt, h=h, in_place=True)
+
+
+def test_one_row_with_any_stride():
+    d = make("bf16", 1, 256, 136, 64, 1, "one")
+    X, dY = (d[x].t().contiguous().t() for x in ("X", "dY"))
+    X, dY = X.as_strided((1, 256), (3, 1)), dY.as_strided((1, 136), (0, 1))
+    assert torch.equal(sp.lora_add(X, d["A"], d["B"], plan_of(d)), sp.lora_add(d["X"], d["A"], d["B"], plan_of(d)))
+    got = sp.lora_grad(dY, X, d["A"], d["B"], plan_of(d))
+    for x, y in zip(got, sp.lora_grad(d["dY"], d["X"], d["A"], d["B"], plan_of(d))):
+        assert torch.equal(x, y)
 
 
 @pytest.mark.parametrize("fmt", list(DTYPES))
@@ -208,7 +244,7 @@ def test_plan_order_is_the_stable_sort(T, n, kind):
 
 
 @pytest.mark.parametrize("fmt", ["f32", "bf16"])
-@pytest.mark.parametrize("T", [40, 700])
+@pytest.mark.parametrize("T", [40, 700, 2500])
 def test_one_tokens_infinities_and_one_adapters_nan_stay_there(T, fmt):
     d = make(fmt, T, 264, 520, 16, 3, "prompts", seed=3)
     d["ids"][:] = np.arange(T) % 3  # every tile of an adapter lies between the others' tokens
@@ -235,7 +271,7 @@ def test_one_tokens_infinities_and_one_adapters_nan_stay_there(T, fmt):
 @pytest.mark.parametrize("scale", [1e-7, 1e-3, 1e4])
 def test_fp16_keeps_small_and_large_intermediate_values(scale):
     """X A^T far below the smallest and above the largest fp16 number: it stays in fp32."""
-    for T in (5, 300):
+    for T in (5, 300, 2500):
         d = make("f16", T, 256, 256, 16, 1, "one", seed=5)
         d["X"] = (d["X"].float() * (scale if scale < 1 else 300.0)).half()
         d["A"] = (d["A"].float() * (1 if scale < 1 else 3000.0)).half()
@@ -281,7 +317,7 @@ def test_scalar_scale_and_plan_without_ids():
     assert torch.equal(a, b)
 
 
-@pytest.mark.parametrize("T", [3, 600])
+@pytest.mark.parametrize("T", [3, 600, 2500])
 def test_same_bits_every_time_on_a_side_stream_and_in_a_graph(T):
     d = make("bf16", T, 512, 768, 16, 4, "prompts", seed=9)
     plan = plan_of(d)

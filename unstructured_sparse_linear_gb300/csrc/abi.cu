@@ -270,6 +270,9 @@ int check_rows(const char* name, const void* p, int64_t ld, int64_t cols, int32_
     return SPOPS_OK;
 }
 
+// A row stride for a matrix of one row: one that every kernel takes.
+int64_t one_row(int64_t cols) { return (cols + 7) / 8 * 8; }
+
 int check_lora(const void* A, const void* B, const float* scale, float scale_all, int dtype, int32_t tokens,
                int32_t in_features, int32_t out_features, int32_t rank, int32_t n_adapters, const void* plan) {
     if (dtype < SPOPS_F32 || dtype > SPOPS_BF16) return fail(SPOPS_ERR_INVALID_ARG, "dtype %d is not a spops_dtype", dtype);
@@ -584,6 +587,10 @@ int spops_lora_add(const void* X, int64_t ldx, const void* A, const void* B, con
     if (st != SPOPS_OK) return st;
     if (tokens == 0) return ok();
     const size_t es = dtype_size(dtype);
+    if (tokens == 1) {  // one row: no stride is ever taken
+        ldx = one_row(in_features);
+        ldb = ldy = one_row(out_features);
+    }
     if ((st = check_rows("X", X, ldx, in_features, tokens, es)) != SPOPS_OK) return st;
     if (!Y && !h) return fail(SPOPS_ERR_INVALID_ARG, "Y and h are both NULL");
     if (Y && (st = check_rows("Y", Y, ldy, out_features, tokens, es)) != SPOPS_OK) return st;
@@ -649,6 +656,10 @@ int spops_lora_grad(const void* dY, int64_t lddy, const void* X, int64_t ldx, co
         return cuda_status(e, "lora_grad memset");
     }
     if (!dX && !dA && !dB) return ok();
+    if (tokens == 1) {  // one row: no stride is ever taken
+        ldx = lddx = ldb = one_row(in_features);
+        lddy = one_row(out_features);
+    }
     if ((st = check_rows("dY", dY, lddy, out_features, tokens, es)) != SPOPS_OK) return st;
     if ((st = check_rows("X", X, ldx, in_features, tokens, es)) != SPOPS_OK) return st;
     if (dX && (st = check_rows("dX", dX, lddx, in_features, tokens, es)) != SPOPS_OK) return st;
