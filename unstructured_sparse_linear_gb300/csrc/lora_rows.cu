@@ -256,6 +256,7 @@ __device__ __forceinline__ void one_tile(const RowsArgs& g, const LoraSmall* til
     if (O)
         for (int64_t n = col; n - tid < n1; n += kCols * kThreads) {
             float acc[kCols][NR];
+            T bv[kCols][NR];  // base: on its way while the sums are formed, added last
             bool in[kCols];
             const bool first = pre && n == col;
 #pragma unroll
@@ -264,8 +265,8 @@ __device__ __forceinline__ void one_tile(const RowsArgs& g, const LoraSmall* til
 #pragma unroll
                 for (int i = 0; i < NR; ++i) {
                     acc[q][i] = 0.f;
-                    if (base && in[q])
-                        acc[q][i] = Elt<T>::to_f(first ? b0[q][i] : base[(int64_t)t.tok[i] * a.ldb + n + q * kThreads]);
+                    bv[q][i] = Elt<T>::from_f(0.f);
+                    if (base && in[q]) bv[q][i] = first ? b0[q][i] : base[(int64_t)t.tok[i] * a.ldb + n + q * kThreads];
                 }
             }
             auto step = [&](int j, const float (&w)[kCols]) {
@@ -330,7 +331,7 @@ __device__ __forceinline__ void one_tile(const RowsArgs& g, const LoraSmall* til
 #pragma unroll
                 for (int i = 0; i < NR; ++i)
                     if (in[q] && i < t.rows)
-                        O[(int64_t)t.tok[i] * a.ldo + n + q * kThreads] = Elt<T>::from_f(acc[q][i]);
+                        O[(int64_t)t.tok[i] * a.ldo + n + q * kThreads] = Elt<T>::from_f(Elt<T>::to_f(bv[q][i]) + acc[q][i]);
         }
     if (C > 1) cluster_wait();
 }
