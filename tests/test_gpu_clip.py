@@ -131,6 +131,22 @@ def test_same_bits_every_time_and_in_a_graph():
     assert torch.equal(norm, norm2) and all(torch.equal(a, b) for a, b in zip(first, outs))
 
 
+def test_set_made_on_a_busy_stream_and_used_on_another():
+    grads = grads_of([70_000, 33], [BF16])
+    outs = [torch.empty_like(g) for g in grads]
+    want = sp.grad_norm(grads)
+    torch.cuda.synchronize()
+    maker, user = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(maker):
+        torch.cuda._sleep(20_000_000)  # the table is written some 10 ms from now
+        s = sp.GradSet(grads, out=outs)
+    with torch.cuda.stream(user):
+        norm = sp.clip_grads(s, 1.0)
+    user.synchronize()
+    assert torch.equal(norm, want)
+    check_clipped(grads, outs, float(want), 1.0)
+
+
 def test_refusals():
     a, b = torch.ones(10, device=DEV), torch.ones(10, device=DEV, dtype=F16)
     with pytest.raises(ValueError, match="contiguous"):

@@ -342,6 +342,21 @@ def test_same_bits_every_time_on_a_side_stream_and_in_a_graph(T):
         assert torch.equal(x, y) and torch.equal(x, z)
 
 
+def test_plan_made_on_a_busy_stream_and_used_on_another():
+    d = make("bf16", 700, 128, 256, 16, 4, "prompts", seed=13)
+    want = sp.lora_add(d["X"], d["A"], d["B"], plan_of(d), base=d["base"], scale=d["scale"])
+    ids = torch.from_numpy(d["ids"]).to(DEV)
+    torch.cuda.synchronize()
+    maker, user = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(maker):
+        torch.cuda._sleep(20_000_000)  # the plan is written some 10 ms from now
+        plan = sp.lora_plan(ids, d["n"])
+    with torch.cuda.stream(user):
+        got = sp.lora_add(d["X"], d["A"], d["B"], plan, base=d["base"], scale=d["scale"])
+    user.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_gradient_against_differences():
     """Y is linear in X, in A and in B apart, so a central difference of L = sum(Y * W) over a
     step of 1 along a direction equals the gradient's product with it, but for rounding: each Y is

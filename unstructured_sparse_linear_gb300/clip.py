@@ -13,12 +13,12 @@ import ctypes
 import torch
 
 from . import _DTYPE, _L, _check, _req
-from .lora import _on, _raw_stream
+from .lora import Built, _on, _raw_stream
 
 __all__ = ["GradSet", "grad_norm", "clip_grads"]
 
 
-class GradSet:
+class GradSet(Built):
     """Gradients that are clipped together (fp32, fp16 and bf16 mixed; contiguous; on one
     device). Holds the tensors and a device table of their addresses, so it serves every step
     that writes its gradients into the same buffers; new buffers need a new set. out: tensors
@@ -32,30 +32,30 @@ class GradSet:
         if len(self.out) != len(self.grads):
             raise ValueError(f"{len(self.grads)} gradients and {len(self.out)} outputs")
         n = len(self.grads)
-        self.device = self.grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        dev = self.grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
         for i, (g, o) in enumerate(zip(self.grads, self.out)):
-            _req(g, f"gradient {i}", dtypes=_DTYPE, device=self.device)
+            _req(g, f"gradient {i}", dtypes=_DTYPE, device=dev)
             if o is not g:
-                _req(o, f"output {i}", dtype=g.dtype, device=self.device)
+                _req(o, f"output {i}", dtype=g.dtype, device=dev)
                 if o.numel() != g.numel():
                     raise ValueError(f"gradient {i} has {g.numel()} elements and its output {o.numel()}")
         lib = _L()
         size = lib.spops_grad_set_size(n)
+        self._n, self._ws = n, int(lib.spops_grad_norm_workspace_size())
         chunks, in_place = ctypes.c_int64(0), ctypes.c_int32(0)
-        with torch.cuda.device(self.device):
-            self._table = torch.empty(max(size, 16), dtype=torch.uint8, device=self.device)
+        with torch.cuda.device(dev):
+            # the table, then the calls' partial sums
+            at = (size + 255) // 256 * 256
+            table = torch.empty(at + self._ws, dtype=torch.uint8, device=dev)
             _check(lib.spops_grad_set_build(
                 (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads]),
                 (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.out]),
                 (ctypes.c_int64 * n)(*[g.numel() for g in self.grads]),
-                (ctypes.c_int32 * n)(*[_DTYPE[g.dtype] for g in self.grads]), n, self._table.data_ptr(), size,
-                ctypes.byref(chunks), ctypes.byref(in_place), _raw_stream(self.device.index)), "grad_set_build")
-        self._ptr, self._n = self._table.data_ptr(), n
+                (ctypes.c_int32 * n)(*[_DTYPE[g.dtype] for g in self.grads]), n, table.data_ptr(), size,
+                ctypes.byref(chunks), ctypes.byref(in_place), _raw_stream(dev.index)), "grad_set_build")
+            super().__init__(table)
         self._chunks, self._in_place = chunks.value, in_place.value
-        self._ws = int(lib.spops_grad_norm_workspace_size())
-        with torch.cuda.device(self.device):
-            self._partial = torch.empty(self._ws, dtype=torch.uint8, device=self.device)
-        self._partial_ptr = self._partial.data_ptr()
+        self._partial_ptr = self._ptr + at
 
     def __len__(self):
         return self._n
@@ -72,8 +72,10 @@ def grad_norm(grads) -> torch.Tensor:
     dev = s.device
     with _on(dev):
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        _check(_L().spops_grad_norm(s._ptr, s._n, s._chunks, norm.data_ptr(), s._partial_ptr, s._ws,
-                                    _raw_stream(dev.index)), "grad_norm")
+        stream = _raw_stream(dev.index)
+        st = _L().spops_grad_norm(s._on_stream(stream), s._n, s._chunks, norm.data_ptr(), s._partial_ptr, s._ws, stream)
+    if st:
+        _check(st, "grad_norm")
     return norm
 
 
@@ -86,8 +88,9 @@ def clip_grads(grads, max_norm: float) -> torch.Tensor:
     dev = s.device
     with _on(dev):
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        st = _L().spops_clip_grads(s._ptr, s._n, s._chunks, s._in_place, float(max_norm), norm.data_ptr(),
-                                   s._partial_ptr, s._ws, _raw_stream(dev.index))
+        stream = _raw_stream(dev.index)
+        st = _L().spops_clip_grads(s._on_stream(stream), s._n, s._chunks, s._in_place, float(max_norm), norm.data_ptr(),
+                                   s._partial_ptr, s._ws, stream)
     if st:
         _check(st, "clip_grads")
     return norm

@@ -46,13 +46,36 @@ def _rows(t, name, rows, cols, dtype, device):
     return t.data_ptr(), ld
 
 
-class LoraPlan:
+class Built:
+    """A device table that is written on one stream and may be read on others. Kernels follow the
+    addresses and indices in it, so a stream other than the one that wrote it waits for the writing
+    before its first use (in a graph capture the table has to be complete: nothing can be waited
+    for there that is not captured too), and the memory is kept until that stream is done with it."""
+
+    def __init__(self, buf: torch.Tensor):
+        self.device = buf.device
+        self._buf = buf
+        self._ptr = buf.data_ptr()
+        self._streams = {_raw_stream(buf.device.index)}
+        self._written = torch.cuda.Event()
+        self._written.record(torch.cuda.current_stream(buf.device))
+
+    def _on_stream(self, stream: int) -> int:
+        """The table's address, usable by work that is queued on `stream` from now on."""
+        if stream not in self._streams and not torch.cuda.is_current_stream_capturing():
+            s = torch.cuda.current_stream(self.device)
+            s.wait_event(self._written)
+            self._buf.record_stream(s)
+            self._streams.add(stream)
+        return self._ptr
+
+
+class LoraPlan(Built):
     """Which tokens of a batch use which adapter, sorted; built by ``lora_plan``."""
 
     def __init__(self, buf: torch.Tensor, tokens: int, n_adapters: int):
+        super().__init__(buf)
         self.buf, self.tokens, self.n_adapters = buf, tokens, n_adapters
-        self.device = buf.device
-        self._ptr = buf.data_ptr()
         self._grad_ws = {}  # lora_grad's workspace bytes by rank
 
     def order(self) -> torch.Tensor:
@@ -86,7 +109,7 @@ def lora_plan(adapter_ids: torch.Tensor | None, n_adapters: int, tokens: int | N
         buf = torch.empty(size, dtype=torch.uint8, device=dev)
         _check(lib.spops_lora_plan_build(ids, tokens, n_adapters, buf.data_ptr(), size, _raw_stream(dev.index)),
                "lora_plan_build")
-    return LoraPlan(buf, tokens, n_adapters)
+        return LoraPlan(buf, tokens, n_adapters)
 
 
 def _weights(X, A, B, plan, scale):
@@ -157,8 +180,9 @@ def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h:
             out = torch.empty((T, n_out), dtype=dt, device=dev)
         y, ldy = _rows(out, "out", T, n_out, dt, dev)
         h = torch.empty((T, rank), dtype=torch.float32, device=dev) if return_h else None
+        stream = _raw_stream(dev.index)
         st = lib.spops_lora_add(x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out, rank, n,
-                                b, ldb, y, ldy, h.data_ptr() if return_h else 0, plan._ptr, _raw_stream(dev.index))
+                                b, ldb, y, ldy, h.data_ptr() if return_h else 0, plan._on_stream(stream), stream)
     if st:
         _check(st, "lora_add")
     return (out, h) if return_h else out
@@ -204,10 +228,10 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
         if size is None:
             size = plan._grad_ws[rank] = int(lib.spops_lora_grad_workspace_size(T, rank))
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
+        stream = _raw_stream(dev.index)
         st = lib.spops_lora_grad(dy, lddy, x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out,
                                  rank, n, hp, b, ldb, dx, lddx, dA.data_ptr() if need[1] else 0,
-                                 dB.data_ptr() if need[2] else 0, plan._ptr, ws.data_ptr(), size,
-                                 _raw_stream(dev.index))
+                                 dB.data_ptr() if need[2] else 0, plan._on_stream(stream), ws.data_ptr(), size, stream)
     if st:
         _check(st, "lora_grad")
     return dX, dA, dB
