@@ -247,7 +247,7 @@ __device__ __forceinline__ void one_tile(const RowsArgs& g, const LoraSmall* til
             }
         }
         hs[j][i] = sum * s;
-        if (a.P && crank == 0) a.P[(int64_t)tile->tok[i] * r + j] = sum;
+        if (a.P && crank == 0 && blockIdx.y == 0) a.P[(int64_t)tile->tok[i] * r + j] = sum;
     }
     // Every rank has read the partial sums once all have passed the wait below (they are rewritten
     // by the next tile, and no CTA leaves while another still reads its shared memory).
@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_rows_kernel(const RowsArgs g
     const LoraArgs& a = g.a;
     const int tid = threadIdx.x;
     const int C = (int)cluster_size(), crank = (int)cluster_rank();
+    // With few tiles several clusters (gridDim.y) take one: each forms P, and a share of the columns.
     const int cid = blockIdx.x / C, ncl = gridDim.x / C;
     // (the list has a slot for every cluster; what lies behind its end is not used)
     LoraSmall t = g.v.small[cid];
@@ -355,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 2) lora_rows_kernel(const RowsArgs g
     const int clog = 31 - __clz(C);
     const int64_t ku = (a.K + 7) / 8, nu = (a.N + 7) / 8;
     const int64_t k0 = (ku * crank >> clog) * 8, k1 = min64(a.K, (ku * (crank + 1) >> clog) * 8);
-    const int64_t n0 = (nu * crank >> clog) * 8, n1 = min64(a.N, (nu * (crank + 1) >> clog) * 8);
+    const int share = blockIdx.y * C + crank, slog = clog + 31 - __clz(gridDim.y);  // (powers of two both)
+    const int64_t n0 = (nu * share >> slog) * 8, n1 = min64(a.N, (nu * (share + 1) >> slog) * 8);
 
     // The trip count and every barrier are the same on all CTAs of a cluster.
     for (int it = cid; it < ntiles; it += ncl) {
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_rows_kernel(const RowsArgs g
         }
         if (t.adapter < 0) {  // no adapter: O = base, P = 0
             copy_rows<T>(g, g.v.small[it].tok, t.rows, n0, n1);
-            if (a.P && crank == 0)
+            if (a.P && share == 0)
                 for (int x = tid; x < t.rows * r; x += kThreads)
                     a.P[(int64_t)g.v.small[it].tok[x / r] * r + x % r] = 0.f;
         } else if (t.rows == 1) {
@@ -468,10 +470,10 @@ int pick_cluster(int64_t items, int64_t most) {
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kern)(KArgs...), int64_t clusters, int c, size_t smem, cudaStream_t s,
+cudaError_t launch_cluster(void (*kern)(KArgs...), int64_t clusters, int c, int split, size_t smem, cudaStream_t s,
                            Args&&... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * c));
+    cfg.gridDim = dim3((unsigned)(clusters * c), (unsigned)split);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -502,11 +504,20 @@ cudaError_t run_rows(bool back, const LoraArgs& a, const LoraPlanView& v, cudaSt
     const int64_t expected = v.tokens / R + (6 * min64(v.tokens, v.n) + 9) / 10;
     const int c = pick_cluster(expected, max64(1, max64(a.K, a.N) / 64));
     const int64_t clusters = min64(cap, (int64_t)device_props().sm_count * 8);
+    // Few tiles: a tile's columns are shared by several clusters while there is an SM for every CTA and
+    // 8192 products of a column and a rank are left to each. (16 tokens of one adapter, rank 64, 2048 to
+    // 8192: 16.4 us with one cluster of 8 per tile, 11.8 us so; 64 tokens of rank 16, 4096 to 4096, which
+    // this leaves alone: 7.2 us, with two clusters a tile 9.2.)
+    int split = 1;
+    if (a.O)
+        while (split < 16 && expected * c * split * 2 <= (int64_t)device_props().sm_count &&
+               (int64_t)c * split * 2 * 8192 <= (int64_t)a.N * a.rank)
+            split *= 2;
     const int rp = (a.rank + 3) & ~3, njg = (a.rank + kJW - 1) / kJW;
     const int ksplit = back ? kWarps : (njg >= kWarps ? 1 : kWarps / njg);
     const size_t smem = (size_t)ksplit * R * rp * sizeof(float);  // at most 32 KB
-    return back ? launch_cluster(lora_rows_kernel<T, true>, clusters, c, smem, s, g)
-                : launch_cluster(lora_rows_kernel<T, false>, clusters, c, smem, s, g);
+    return back ? launch_cluster(lora_rows_kernel<T, true>, clusters, c, split, smem, s, g)
+                : launch_cluster(lora_rows_kernel<T, false>, clusters, c, split, smem, s, g);
 }
 
 template <typename T>
@@ -527,7 +538,7 @@ cudaError_t run_wgrad_rows(const LoraWgradArgs* w, int nw, int32_t rank, const f
     const int64_t items = (int64_t)v.n * (g.blocks[0] + g.blocks[1]) * g.jb;
     const int c = pick_cluster(items, max64(1, v.tokens / kWgT));
     if (items * c > 0x7fffffffll) return cudaErrorInvalidValue;
-    return launch_cluster(lora_wgrad_rows_kernel<T>, items, c, 0, s, g);
+    return launch_cluster(lora_wgrad_rows_kernel<T>, items, c, 1, 0, s, g);
 }
 
 }  // namespace
