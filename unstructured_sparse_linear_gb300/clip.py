@@ -32,13 +32,26 @@ class GradSet(Built):
         if len(self.out) != len(self.grads):
             raise ValueError(f"{len(self.grads)} gradients and {len(self.out)} outputs")
         n = len(self.grads)
+        if n:
+            _req(self.grads[0], "gradient 0", dtypes=_DTYPE)
         dev = self.grads[0].device if n else torch.device("cuda", torch.cuda.current_device())
+        ins, outs, counts, dtypes = [], [], [], []
         for i, (g, o) in enumerate(zip(self.grads, self.out)):
-            _req(g, f"gradient {i}", dtypes=_DTYPE, device=dev)
-            if o is not g:
-                _req(o, f"output {i}", dtype=g.dtype, device=dev)
-                if o.numel() != g.numel():
-                    raise ValueError(f"gradient {i} has {g.numel()} elements and its output {o.numel()}")
+            # (an address, a size and a type each; what is wrong is found out where something is)
+            if not (type(g) is torch.Tensor and g.dtype in _DTYPE and g.device == dev and g.is_contiguous()):
+                _req(g, f"gradient {i}", dtypes=_DTYPE, device=dev)
+            count, dt = g.numel(), g.dtype
+            ins.append(g.data_ptr())
+            counts.append(count)
+            dtypes.append(_DTYPE[dt])
+            if o is g:
+                outs.append(ins[-1])
+                continue
+            if not (type(o) is torch.Tensor and o.dtype is dt and o.device == dev and o.is_contiguous()):
+                _req(o, f"output {i}", dtype=dt, device=dev)
+            if o.numel() != count:
+                raise ValueError(f"gradient {i} has {count} elements and its output {o.numel()}")
+            outs.append(o.data_ptr())
         lib = _L()
         size = lib.spops_grad_set_size(n)
         self._n, self._ws = n, int(lib.spops_grad_norm_workspace_size())
@@ -48,11 +61,9 @@ class GradSet(Built):
             at = (size + 255) // 256 * 256
             table = torch.empty(at + self._ws, dtype=torch.uint8, device=dev)
             _check(lib.spops_grad_set_build(
-                (ctypes.c_void_p * n)(*[g.data_ptr() for g in self.grads]),
-                (ctypes.c_void_p * n)(*[o.data_ptr() for o in self.out]),
-                (ctypes.c_int64 * n)(*[g.numel() for g in self.grads]),
-                (ctypes.c_int32 * n)(*[_DTYPE[g.dtype] for g in self.grads]), n, table.data_ptr(), size,
-                ctypes.byref(chunks), ctypes.byref(in_place), _raw_stream(dev.index)), "grad_set_build")
+                (ctypes.c_void_p * n)(*ins), (ctypes.c_void_p * n)(*outs), (ctypes.c_int64 * n)(*counts),
+                (ctypes.c_int32 * n)(*dtypes), n, table.data_ptr(), size, ctypes.byref(chunks), ctypes.byref(in_place),
+                _raw_stream(dev.index)), "grad_set_build")
             super().__init__(table)
         self._chunks, self._in_place = chunks.value, in_place.value
         self._partial_ptr = self._ptr + at

@@ -92,6 +92,8 @@ def lora_plan(adapter_ids: torch.Tensor | None, n_adapters: int, tokens: int | N
         if tokens is None:
             raise ValueError("lora_plan needs adapter_ids or tokens")
         dev = torch.device(device if device is not None else "cuda")
+        if dev.type != "cuda":
+            raise ValueError(f"device must be a CUDA device, got {dev}")
         if dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         ids = 0
