@@ -84,6 +84,7 @@ typedef enum spops_sddmm_backend {
 #define SPOPS_DEV_ROW_IDX 5      /* row_idx is not a permutation of 0..m-1 */
 #define SPOPS_DEV_TMEM 6         /* tensor-memory allocation failed */
 #define SPOPS_DEV_SMEM_ALIGN 7   /* shared memory of a tensor-core kernel is not 1 KB aligned */
+#define SPOPS_DEV_GRID_BARRIER 8 /* a cooperative kernel's CTAs did not meet within the time limit */
 
 /* Row-bin thresholds the operators use: rows with at least this many entries are "long". */
 #define SPOPS_SPMM_LONG_ROW 256
@@ -369,10 +370,11 @@ SPOPS_API int spops_grad_norm(const void* set, int32_t tensors, int64_t chunks, 
                               size_t ws_bytes, void* stream);
 
 /* spops_grad_norm, then out = c * grad for every gradient with c = min(1, max_norm / (norm +
- * 1e-6)), each product rounded once. max_norm >= 0 (infinity: c = 1). With c = 1 gradients in
+ * 1e-6)), each product rounded once; one cooperative launch, which counts in `set` the CTAs that wait
+ * for each other, so calls on one set must not overlap. max_norm >= 0 (infinity: c = 1). With c = 1 gradients in
  * place are left alone. An infinite norm gives c = 0 and a NaN one c = NaN, as the formula
  * says. Nothing is read back to the host. */
-SPOPS_API int spops_clip_grads(const void* set, int32_t tensors, int64_t chunks, int in_place, double max_norm,
+SPOPS_API int spops_clip_grads(void* set, int32_t tensors, int64_t chunks, int in_place, double max_norm,
                                float* norm_out, void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- checks */

@@ -2,8 +2,8 @@
 
     norm = sqrt(sum of g^2 over every gradient),  g <- g min(1, max_norm / (norm + 1e-6))
 
-The step between an adapter's gradients (sddmm, lora_grad) and masked_adam. Two kernel launches
-whatever the number of tensors, and nothing is read back to the host: the norm stays on the
+The step between an adapter's gradients (sddmm, lora_grad) and masked_adam. One kernel launch
+whatever the number of tensors (two for the norm alone), and nothing is read back to the host: the norm stays on the
 device. A training loop whose gradient buffers stay where they are keeps a ``GradSet`` of them.
 """
 from __future__ import annotations

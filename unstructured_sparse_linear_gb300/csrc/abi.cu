@@ -798,7 +798,8 @@ int spops_grad_set_build(const void* const* grads, void* const* outs, const int6
         if (p.write) written = std::max(written, p.hi);
     }
     int64_t first = 0;
-    for (int32_t i = 0; i < tensors;) {
+    int32_t i = 0;
+    do {  // (an empty set has its count written too)
         ClipFill f = {};
         int n = 0;
         const int32_t at = i;
@@ -810,10 +811,10 @@ int spops_grad_set_build(const void* const* grads, void* const* outs, const int6
             f.e[n].dtype = dtypes[i];
             first += clip_chunks(counts[i], dtype_size(dtypes[i]));
         }
-        const int st = cuda_status(launch_grad_set_fill(static_cast<ClipEntry*>(set), at, f, n, (cudaStream_t)stream),
+        const int st = cuda_status(launch_grad_set_fill(set, at, f, n, (cudaStream_t)stream),
                                    "grad_set_build launch");
         if (st != SPOPS_OK) return st;
-    }
+    } while (i < tensors);
     *chunks_out = chunks;
     *in_place_out = in_place ? 1 : 0;
     return ok();
@@ -830,7 +831,7 @@ static int grad_norm_call(const void* set, int32_t tensors, int64_t chunks, int 
     if (!workspace || !aligned(workspace, 16) || ws_bytes < grad_norm_ws_bytes())
         return fail(SPOPS_ERR_WORKSPACE, "needs a 16-byte aligned workspace of %zu bytes (got %zu)",
                     grad_norm_ws_bytes(), ws_bytes);
-    return cuda_status(launch_grad_norm(static_cast<const ClipEntry*>(set), tensors, chunks, in_place != 0, scale,
+    return cuda_status(launch_grad_norm(const_cast<void*>(set), tensors, chunks, in_place != 0, scale,
                                         max_norm, norm_out, static_cast<double*>(workspace), (cudaStream_t)stream),
                        scale ? "clip_grads launch" : "grad_norm launch");
 }
@@ -840,7 +841,7 @@ int spops_grad_norm(const void* set, int32_t tensors, int64_t chunks, float* nor
     return grad_norm_call(set, tensors, chunks, 1, false, 0.0, norm_out, workspace, ws_bytes, stream);
 }
 
-int spops_clip_grads(const void* set, int32_t tensors, int64_t chunks, int in_place, double max_norm, float* norm_out,
+int spops_clip_grads(void* set, int32_t tensors, int64_t chunks, int in_place, double max_norm, float* norm_out,
                      void* workspace, size_t ws_bytes, void* stream) {
     return grad_norm_call(set, tensors, chunks, in_place, true, max_norm, norm_out, workspace, ws_bytes, stream);
 }

@@ -21,6 +21,7 @@ enum DeviceError : int {
     kDevErrColOrder = 4,         // columns not strictly increasing inside a row
     kDevErrRowIdxPerm = 5,       // row_idx is not a permutation of 0..m-1
     kDevErrTmemAlloc = 6,        // tensor-memory allocation returned an unusable address
+    kDevErrGridBarrier = 8,      // a cooperative kernel's CTAs did not meet within the time limit
     kDevErrSmemAlign = 7,        // dynamic shared memory does not start on a 1 KB boundary
 };
 
