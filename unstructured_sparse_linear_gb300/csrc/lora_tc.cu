@@ -545,6 +545,22 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
         const int quarter = warp & 3, grp = (warp - 2) >> 2, row = quarter * 32 + lane, et = tid - 64;
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
         const int own = kLoraTile >> clog;  // rows that this rank sums: [crank * own, ...)
+        // Tokens without an adapter, O = base, P = 0: first, while the loads for the first sums are
+        // under way (1037 tokens of 24 adapters, 4096 -> 4096: 22.3 us, and 23.3 with them last).
+        const bool copy = g.O && (g.O != g.base);
+        if (copy || g.P) {
+            for (int64_t pos = (int64_t)g.v.off[g.v.n] + blockIdx.x; pos < g.v.tokens; pos += gridDim.x) {
+                const int64_t t = g.v.order[pos];
+                if (copy) {
+                    const uint4* src = g.base ? reinterpret_cast<const uint4*>(static_cast<const T*>(g.base) + t * g.ldb)
+                                              : nullptr;
+                    uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(g.O) + t * g.ldo);
+                    for (int i = et; i < g.N / 8; i += kEpi) to[i] = src ? src[i] : make_uint4(0, 0, 0, 0);
+                }
+                if (g.P)
+                    for (int j = et; j < g.rank; j += kEpi) g.P[t * g.rank + j] = 0.f;
+            }
+        }
         uint32_t q = 0, n2 = 0, tt = 0;
         for (int it = cid; it < ntiles; it += ncl, ++tt) {
             const LoraTile t = it == cid ? tile0 : g.v.tiles[it];
@@ -724,21 +740,6 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
             if (et < C) mbar_arrive_remote(smem_u32(&sh.freed), et);
         }
         if (lane == 0) bulk_wait<0>();
-        // tokens without an adapter: O = base, P = 0
-        const bool copy = g.O && (g.O != g.base);
-        if (copy || g.P) {
-            for (int64_t pos = (int64_t)g.v.off[g.v.n] + blockIdx.x; pos < g.v.tokens; pos += gridDim.x) {
-                const int64_t t = g.v.order[pos];
-                if (copy) {
-                    const uint4* src = g.base ? reinterpret_cast<const uint4*>(static_cast<const T*>(g.base) + t * g.ldb)
-                                              : nullptr;
-                    uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(g.O) + t * g.ldo);
-                    for (int i = et; i < g.N / 8; i += kEpi) to[i] = src ? src[i] : make_uint4(0, 0, 0, 0);
-                }
-                if (g.P)
-                    for (int j = et; j < g.rank; j += kEpi) g.P[t * g.rank + j] = 0.f;
-            }
-        }
     }
     tc::fence_before_sync();
     __syncthreads();
