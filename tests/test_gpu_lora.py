@@ -282,6 +282,21 @@ def test_fp16_keeps_small_and_large_intermediate_values(scale):
         check_grad(d, "f16", h=h)
 
 
+@pytest.mark.parametrize("x,a,dy", [(1e-6, 1, 1e3), (1e4, 8, 1e-4)])
+def test_fp16_columns_of_db_beside_an_infinite_one(x, a, dy):
+    d = make("f16", 700, 136, 72, 16, 1, "one", seed=17)
+    d["X"], d["A"], d["dY"] = d["X"] * x, d["A"] * a, d["dY"] * dy
+    A = as_f64(d["A"]).copy()
+    d["A"][0, 3, 5] = float("inf")
+    _, _, P, eP = want_rows(d["ids"], as_f64(d["X"]), A.transpose(0, 2, 1), as_f64(d["B"]).transpose(0, 2, 1),
+                            as_f64(d["scale"]), np.zeros((700, 72)))
+    G, eG = want_wgrad(d["ids"], 1, as_f64(d["dY"]), P, eP, as_f64(d["scale"]))
+    dB = sp.lora_grad(d["dY"], d["X"], d["A"], d["B"], plan_of(d), scale=d["scale"], need=(False, False, True))[2]
+    rest = [j for j in range(16) if j != 3]
+    check(dB[:, :, rest], G.transpose(0, 2, 1)[:, :, rest], eG.transpose(0, 2, 1)[:, :, rest], "f16", "dB")
+    assert not np.any(np.isfinite(as_f64(dB[:, :, 3])))
+
+
 @pytest.mark.parametrize("fmt", ["f32", "f16"])
 def test_row_offsets_beyond_32_bits(fmt):
     """Rows so far apart that the last ones lie past 2^31 elements."""

@@ -957,7 +957,10 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[i][e]));
+                    for (int e = 0; e < 8; ++e) {  // (infinite columns leave the others their scale)
+                        const float y = fabsf(x[i][e]);
+                        if (y <= 3.402823466e38f) m = fmaxf(m, y);
+                    }
             }
 #pragma unroll
             for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
