@@ -180,7 +180,9 @@ def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h:
     with _on(dev):
         if out is None:
             out = torch.empty((T, n_out), dtype=dt, device=dev)
-        y, ldy = _rows(out, "out", T, n_out, dt, dev)
+            y, ldy = out.data_ptr(), n_out
+        else:
+            y, ldy = _rows(out, "out", T, n_out, dt, dev)
         h = torch.empty((T, rank), dtype=torch.float32, device=dev) if return_h else None
         stream = _raw_stream(dev.index)
         st = lib.spops_lora_add(x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out, rank, n,
@@ -210,18 +212,21 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
     dy, lddy = _rows(dY, "dY", T, n_out, dt, dev)
     hp = 0
     if h is not None:
-        _req(h, "h", torch.float32, device=dev)
-        if tuple(h.shape) != (T, rank):
-            raise ValueError(f"h must be {T} x {rank}, got {tuple(h.shape)}")
-        hp = h.data_ptr()
+        hp, ldh = _rows(h, "h", T, rank, torch.float32, dev)
+        if ldh != rank and T > 1:
+            raise ValueError(f"h must be contiguous, got strides {h.stride()}")
     b, ldb = _rows(dX_base, "dX_base", T, k, dt, dev) if dX_base is not None else (0, k)
     lib = _L()
     with _on(dev):
         dX = dA = dB = None
         dx, lddx = 0, k
         if need[0]:
-            dX = dX_out if dX_out is not None else torch.empty((T, k), dtype=dt, device=dev)
-            dx, lddx = _rows(dX, "dX_out", T, k, dt, dev)
+            if dX_out is None:
+                dX = torch.empty((T, k), dtype=dt, device=dev)
+                dx = dX.data_ptr()
+            else:
+                dX = dX_out
+                dx, lddx = _rows(dX, "dX_out", T, k, dt, dev)
         if need[1]:
             dA = _like(dA_out, A, "dA_out") if dA_out is not None else torch.empty_like(A)
         if need[2]:
