@@ -372,6 +372,58 @@ def test_plan_made_on_a_busy_stream_and_used_on_another():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("T", [5, 300, 1500])
+def test_inputs_written_just_before_by_kernels_copies_and_other_streams(T):
+    """Each launch may begin while the one before it ends: what that one writes is waited for,
+    whether it is a kernel, a copy or a memset, here or on a stream that this one waits for."""
+    d = make("bf16", T, 512, 384, 16, 3, "prompts", seed=23)
+    p = plan_of(d)
+    args = dict(scale=d["scale"])
+    want = sp.lora_add(d["X"], d["A"], d["B"], p, base=d["base"], **args)
+    want_g = sp.lora_grad(d["dY"], d["X"], d["A"], d["B"], p, dX_base=d["dX_base"], **args)
+    zero = sp.lora_add(d["X"], d["A"], d["B"], p, **args)
+    bufs = {k: torch.empty_like(d[k]) for k in ("X", "A", "B", "base", "dY", "dX_base")}
+    big = torch.empty(1 << 27, device=DEV)
+    other = torch.cuda.Stream()
+
+    def step(wait):
+        for b in bufs.values():
+            b.fill_(float("nan"))
+        if wait:
+            fork = torch.cuda.current_stream().record_event()
+            with torch.cuda.stream(other):
+                other.wait_event(fork)
+                big.fill_(1.0)
+                for k in ("A", "dY"):
+                    bufs[k].copy_(d[k])
+                join = other.record_event()
+        for k in bufs:
+            if not (wait and k in ("A", "dY")):
+                bufs[k].copy_(d[k])
+        if wait:
+            torch.add(bufs["X"], 0, out=bufs["X"])  # a kernel, still running at the wait
+            torch.cuda.current_stream().wait_event(join)
+        y = sp.lora_add(bufs["X"], bufs["A"], bufs["B"], p, base=bufs["base"], **args)
+        bufs["base"].zero_()
+        y2 = sp.lora_add(bufs["X"], bufs["A"], bufs["B"], p, base=bufs["base"], **args)
+        g = sp.lora_grad(bufs["dY"], bufs["X"], bufs["A"], bufs["B"], p, dX_base=bufs["dX_base"], **args)
+        bufs["dX_base"].copy_(d["dX_base"])
+        return (y, y2) + g
+
+    for wait in (False, True):
+        outs = [step(wait) for _ in range(3)]
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            outs.append(step(wait))
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            for got, ref in zip(out, (want, zero) + want_g):
+                assert torch.equal(got, ref)
+
+
 def test_gradient_against_differences():
     """Y is linear in X, in A and in B apart, so a central difference of L = sum(Y * W) over a
     step of 1 along a direction equals the gradient's product with it, but for rounding: each Y is

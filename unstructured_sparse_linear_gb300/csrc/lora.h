@@ -122,7 +122,7 @@ bool lora_tiles_ok(int dt, const LoraArgs& a, const LoraPlanView& v);
 cudaError_t launch_lora_tiles(int dt, bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s);
 bool lora_wgrad_tiles_ok(int dt, const LoraWgradArgs* w, int nw);
 cudaError_t launch_lora_wgrad_tiles(int dt, const LoraWgradArgs* w, int nw, int32_t rank, const float* scale,
-                                    float scale_all, const LoraPlanView& v, bool pdl, cudaStream_t s);
+                                    float scale_all, const LoraPlanView& v, bool after_lora, cudaStream_t s);
 
 // Operators (the dispatch between the kernels). after_lora: launch_lora was the launch before
 // this one, on the same stream and in the same call.

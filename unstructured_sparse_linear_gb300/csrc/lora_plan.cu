@@ -106,6 +106,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) lora_plan_kernel(const int32_
     const int T = v.tokens, n = v.n;
     const int L = ((T + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
     const int64_t w0 = min64((int64_t)warp * L, T), w1 = min64(w0 + L, T);
+    pdl_trigger();
+    pdl_wait();
 
     for (int p = 0; p < passes; ++p) {
         const bool to_order = ((passes - 1 - p) & 1) == 0;
@@ -191,9 +193,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) lora_plan_kernel(const int32_
 cudaError_t launch_lora_plan(const int32_t* ids, const LoraPlanView& v, cudaStream_t s) {
     int passes = 1;
     while (passes < 4 && ((int64_t)v.n >> (8 * passes)) > 0) ++passes;  // keys 0 .. n
-    lora_plan_kernel<<<1, kPlanThreads, 0, s>>>(ids, v, passes);
+    const cudaError_t e = launch_pdl(lora_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, ids, v, passes);
     count_launches(1);
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace spops

@@ -390,12 +390,6 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = (int)cluster_size(), crank = (int)cluster_rank();
     const int cid = blockIdx.x / C, ncl = gridDim.x / C;
-    // Every CTA's first tile, read while the barriers are set up (the list has a slot per cluster;
-    // what lies behind its end is not used).
-    const int ntiles = g.v.counts[kLoraCntTiles];
-    const LoraTile tile0 = g.v.tiles[cid];
-
-    if (warp == 1) tc::tmem_alloc(smem_u32(&sh.tmem), Cfg::kTmem);
     if (warp == 2 && lane == 0) {
         for (int i = 0; i < kBoxes; ++i) {
             tma_prefetch_map(&maps.u[i]);
@@ -423,12 +417,27 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
         fence_mbar_init();
         sh.failed = 0;
     }
-    tc::fence_before_sync();
     __syncthreads();
     if (C > 1) cluster_sync();  // the other ranks' barriers are initialised
-    tc::fence_after_sync();
-    pdl_trigger();  // (after the allocation of TMEM, which a dependent kernel's CTAs share)
-    const uint32_t tmem = sh.tmem;
+    // All before this line overlaps the kernel before this one, and touches no memory that it writes.
+    pdl_wait();
+    // Every cluster's first tile (the list has a slot per cluster; what lies behind its end is not used).
+    const int ntiles = g.v.counts[kLoraCntTiles];
+    const LoraTile tile0 = g.v.tiles[cid];
+    uint32_t tmem = 0;
+    if (warp > 0) {  // (the loads need none, and begin at once)
+        // TMEM is allocated after the wait, so that no CTA holds it while one of the kernel before
+        // wants it, and before the trigger for the same reason. The trigger also tells a dependent
+        // kernel that all before this one is complete (the weight gradients' rely on that).
+        if (warp == 1) {
+            tc::tmem_alloc(smem_u32(&sh.tmem), Cfg::kTmem);
+            pdl_trigger();
+        }
+        tc::fence_before_sync();
+        named_barrier(2, kTileThreads - 32);
+        tc::fence_after_sync();
+        tmem = sh.tmem;
+    }
     const Waits wait{&sh.failed, g.err};
     const int nkc = (g.K + kKC - 1) / kKC, nnc = g.O ? (g.N + kKC - 1) / kKC : 0;
     const int clog = 31 - __clz(C);  // C is a power of two; the chunk counts are below 2^26
@@ -781,7 +790,7 @@ struct WgArgs {
     const float* scale;
     float scale_all;
     int32_t rank;
-    int pdl;  // launched as a programmatic dependent of the kernel that writes the dependent P
+    int early;  // the kernel before this one triggers once all before it is complete, and writes the dependent P
     int* err;
 };
 
@@ -816,6 +825,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int C = (int)cluster_size(), crank = (int)cluster_rank();
+    if (!g.early) pdl_wait();
     const int per = g.blocks[0] + g.blocks[1];
     const int item = blockIdx.x / C;
     const int adapter = g.v.aorder[item / per], blk = item % per;  // the longest first
@@ -830,7 +840,10 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
     const int nc = cb - ca;
     const int pa = p0 + ca * 64, pe = min(p0 + cnt, p0 + cb * 64);  // this CTA's positions
 
-    if (warp == 1) tc::tmem_alloc(smem_u32(&sh.tmem), Cfg::kTmem);
+    if (warp == 1) {
+        tc::tmem_alloc(smem_u32(&sh.tmem), Cfg::kTmem);
+        pdl_trigger();
+    }
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(smem_u32(&sh.full[s]), 1 + 4);
@@ -846,7 +859,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
     const Waits wait{&sh.failed, g.err};
-    const bool dependent = g.pdl && w.dependent;
+    const bool dependent = g.early && w.dependent;
     float down = 1.f;  // what the parts of P were scaled by, inverted
 
     if (warp == 0) {
@@ -1087,7 +1100,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             }
         }
     }
-    if (g.pdl && !dependent) pdl_wait();  // so that the kernel before this one has ended when this one has
+    if (g.early && !dependent) pdl_wait();  // so that the kernel before this one has ended when this one has
     __syncthreads();
     if (C > 1) cluster_sync();  // nobody reads this CTA's sums any more
     if (warp == 1) tc::tmem_dealloc(tmem, Cfg::kTmem);
@@ -1134,23 +1147,10 @@ bool rows_ok(const void* p, int64_t cols, int64_t ld) {
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t clusters, int c, int threads, uint32_t smem, bool pdl,
-                            cudaStream_t s, const Args&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(clusters * c));
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)c;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 2 : 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+cudaError_t launch_clusters(void (*kern)(KArgs...), int64_t clusters, int c, int threads, uint32_t smem, cudaStream_t s,
+                            const Args&... args) {
+    const cudaError_t e = launch_pdl_cluster(kern, dim3((unsigned)(clusters * c)), dim3((unsigned)threads), smem,
+                                             (unsigned)c, s, args...);
     count_launches(1);
     return e;
 }
@@ -1211,12 +1211,12 @@ cudaError_t run_tiles(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) 
     int c = 8;
     while (c > Cfg::kMinCluster && expected * c > slots) c /= 2;
     const int64_t clusters = max64(1, min64(cap, slots / c));
-    return launch_clusters(kern, clusters, c, kTileThreads, Cfg::kSmem, false, s, g, m);
+    return launch_clusters(kern, clusters, c, kTileThreads, Cfg::kSmem, s, g, m);
 }
 
 template <typename T, int RP>
 cudaError_t run_wgrad(const LoraWgradArgs* w, int nw, int32_t rank, const float* scale, float scale_all,
-                      const LoraPlanView& v, bool pdl, cudaStream_t s) {
+                      const LoraPlanView& v, bool early, cudaStream_t s) {
     using Cfg = WgCfg<RP>;
     static bool done[64];
     auto kern = lora_wgrad_kernel<T, RP>;
@@ -1241,23 +1241,23 @@ cudaError_t run_wgrad(const LoraWgradArgs* w, int nw, int32_t rank, const float*
     g.scale = scale;
     g.scale_all = scale_all;
     g.rank = rank;
-    g.pdl = pdl;
+    g.early = early;
     g.err = device_error_word();
     const int64_t items = (int64_t)v.n * (g.blocks[0] + g.blocks[1]);
     int c = 1;
     const int64_t slots = (int64_t)device_props().sm_count * Cfg::kPerSm;
     while (c < 8 && items * c * 2 <= slots && (int64_t)v.tokens >= 64ll * c * 2) c *= 2;
     if (items * c > 0x7fffffffll) return cudaErrorInvalidValue;
-    return launch_clusters(kern, items, c, kWgThreads, Cfg::kSmem, pdl, s, g, mu[0], mg[0], mu[1], mg[1]);
+    return launch_clusters(kern, items, c, kWgThreads, Cfg::kSmem, s, g, mu[0], mg[0], mu[1], mg[1]);
 }
 
 template <typename T>
 cudaError_t run_wgrad_rank(const LoraWgradArgs* w, int nw, int32_t rank, const float* scale, float scale_all,
-                           const LoraPlanView& v, bool pdl, cudaStream_t s) {
-    if (rank <= 16) return run_wgrad<T, 16>(w, nw, rank, scale, scale_all, v, pdl, s);
-    if (rank <= 32) return run_wgrad<T, 32>(w, nw, rank, scale, scale_all, v, pdl, s);
-    if (rank <= 64) return run_wgrad<T, 64>(w, nw, rank, scale, scale_all, v, pdl, s);
-    return run_wgrad<T, 128>(w, nw, rank, scale, scale_all, v, pdl, s);
+                           const LoraPlanView& v, bool early, cudaStream_t s) {
+    if (rank <= 16) return run_wgrad<T, 16>(w, nw, rank, scale, scale_all, v, early, s);
+    if (rank <= 32) return run_wgrad<T, 32>(w, nw, rank, scale, scale_all, v, early, s);
+    if (rank <= 64) return run_wgrad<T, 64>(w, nw, rank, scale, scale_all, v, early, s);
+    return run_wgrad<T, 128>(w, nw, rank, scale, scale_all, v, early, s);
 }
 
 template <typename T, bool kBack>
@@ -1291,9 +1291,9 @@ bool lora_wgrad_tiles_ok(int dt, const LoraWgradArgs* w, int nw) {
 }
 
 cudaError_t launch_lora_wgrad_tiles(int dt, const LoraWgradArgs* w, int nw, int32_t rank, const float* scale,
-                                    float scale_all, const LoraPlanView& v, bool pdl, cudaStream_t s) {
-    return dt == kF16 ? run_wgrad_rank<__half>(w, nw, rank, scale, scale_all, v, pdl, s)
-                      : run_wgrad_rank<__nv_bfloat16>(w, nw, rank, scale, scale_all, v, pdl, s);
+                                    float scale_all, const LoraPlanView& v, bool after_lora, cudaStream_t s) {
+    return dt == kF16 ? run_wgrad_rank<__half>(w, nw, rank, scale, scale_all, v, after_lora, s)
+                      : run_wgrad_rank<__nv_bfloat16>(w, nw, rank, scale, scale_all, v, after_lora, s);
 }
 
 }  // namespace spops
