@@ -28,11 +28,32 @@ constexpr uint32_t kUBytes = kLoraTile * 128;  // a 128 x 64 tile of U, base or 
 
 // ------------------------------------------------------------------ PTX
 
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
+// The L2 policy of a gradient's rows: dY is read twice, by two kernels, beside operands that are read or
+// written once; where all of it leaves L2 first, more of dY is still there for the second read than under
+// the usual order (4096 tokens, 4096 -> 11008, rank 16: 57.2 us, 63.1 without; 8192 94.1, 97.3; with 16384,
+// whose 361 MB of dY L2 does not hold either way, 184 and 180).
+__device__ __forceinline__ uint64_t evict_first_policy() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+// A box of a 2-D tensor. kHint: with the L2 policy (the neutral one is not free: 2 of 61 us for a long
+// prompt's forward product).
+template <bool kHint>
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                            uint64_t policy) {
+    if constexpr (kHint)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
 }
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -43,12 +64,21 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 }
 
 // Four rows of a 2-D tensor (a map whose box is one row of 64 elements) into 4 x 128 bytes.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&y)[4], uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
-        : "memory");
+template <bool kHint>
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, const int (&y)[4], uint32_t bar,
+                                            uint64_t policy) {
+    if constexpr (kHint)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar)
+            : "memory");
 }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
@@ -446,6 +476,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
 
     if (warp == 0) {
         // ---------------- loads
+        const uint64_t policy = kBack ? evict_first_policy() : 0;
         uint32_t q = 0;
         bool ok = true;
         const int64_t brows = kBack ? g.K : g.N;
@@ -468,8 +499,8 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
                 const int x = (p1 ? ka + j : na + j - nk) * kKC;
                 if (from_rows) {
                     const CUtensorMap* m = p1 ? maps.u : maps.base;
-                    if (rows.mode >= 0 && rows.mode < 3) tma_load_2d(st + lane * 512, m + rows.mode, x, rows.y[0], fb);
-                    else if (rows.mode == 3) tma_gather4(st + lane * 512, m + 3, x, rows.y, fb);
+                    if (rows.mode >= 0 && rows.mode < 3) tma_load_2d<kBack>(st + lane * 512, m + rows.mode, x, rows.y[0], fb, policy);
+                    else if (rows.mode == 3) tma_gather4<kBack>(st + lane * 512, m + 3, x, rows.y, fb, policy);
                 }
                 if (lane == 0) {
                     if (!b_tile) {
@@ -864,6 +895,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
 
     if (warp == 0) {
         // ---------------- loads of U
+        const uint64_t policy = evict_first_policy();
         const CUtensorMap* mu = which ? &map_u1 : &map_u0;
         const CUtensorMap* mg = which ? &map_g1 : &map_g0;
         int j = 0;
@@ -884,10 +916,10 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             if (lane == 0) mbar_arrive_expect_tx(fb, Cfg::kU);
             __syncwarp();
             if (box) {
-                if (lane < kWgCols / 64) tma_load_2d(st + lane * 8192, mu, n0 + lane * 64, first, fb);
+                if (lane < kWgCols / 64) tma_load_2d<true>(st + lane * 8192, mu, n0 + lane * 64, first, fb, policy);
             } else {
                 const int c = lane >> 4;
-                tma_gather4(st + c * 8192 + (lane & 15) * 512, mg, n0 + c * 64, y, fb);
+                tma_gather4<true>(st + c * 8192 + (lane & 15) * 512, mg, n0 + c * 64, y, fb, policy);
             }
         }
         if (sh.failed) {
