@@ -273,6 +273,17 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same without the release, which waits for all that the thread wrote, global memory too (a few
+// hundred ns): for barriers initialised before a fence_mbar_init, and for leaving once every remote read
+// has its value and every message has been waited for.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Makes a relaxed arrival after it a release of this CTA's shared memory only: its writes are visible
+// to the cluster's threads that acquire, its reads are done. Global memory is not waited for.
+__device__ __forceinline__ void cluster_release_smem() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
 // Address in CTA `rank`'s shared memory of the local shared address `addr`.
 __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, int rank) {
     uint32_t ra;

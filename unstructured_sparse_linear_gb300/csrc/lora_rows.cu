@@ -130,7 +130,7 @@ __device__ __forceinline__ void phase1_backward(const T* const* urow, const T* B
 }
 
 // barrier.cluster in two halves: what a CTA does between them overlaps the others' arrival.
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // The tile's P of one rank (rows 0 .. NR - 1), from shared memory.
@@ -224,8 +224,8 @@ __device__ __forceinline__ void one_tile(const RowsArgs& g, const LoraSmall* til
     else if (g.vec) phase1_forward<T, NR, true>(urow, A, K, k0, k1, r, ksplit, rp, part);
     else phase1_forward<T, NR, false>(urow, A, K, k0, k1, r, ksplit, rp, part);
     if (C > 1) {
-        cluster_arrive();
-        cluster_wait();
+        cluster_release_smem();
+        cluster_sync_relaxed();
     } else {
         __syncthreads();
     }
@@ -251,7 +251,10 @@ __device__ __forceinline__ void one_tile(const RowsArgs& g, const LoraSmall* til
     }
     // Every rank has read the partial sums once all have passed the wait below (they are rewritten
     // by the next tile, and no CTA leaves while another still reads its shared memory).
-    if (C > 1) cluster_arrive();
+    if (C > 1) {
+        cluster_release_smem();
+        cluster_arrive_relaxed();
+    }
     __syncthreads();
     if (O)
         for (int64_t n = col; n - tid < n1; n += kCols * kThreads) {
@@ -451,8 +454,12 @@ __global__ void __launch_bounds__(kThreads) lora_wgrad_rows_kernel(const WgradRo
     }
 #pragma unroll
     for (int j = 0; j < kWgJ; ++j) s_acc[j][tid] = acc[j];
-    if (C > 1) cluster_sync();
-    else __syncthreads();
+    if (C > 1) {
+        cluster_release_smem();
+        cluster_sync_relaxed();
+    } else {
+        __syncthreads();
+    }
     const float s = g.scale_all * (g.scale ? g.scale[adapter] : 1.f);
     T* G = static_cast<T*>(w.G) + (int64_t)adapter * r * w.N;
     if (n < w.N)
@@ -464,7 +471,7 @@ __global__ void __launch_bounds__(kThreads) lora_wgrad_rows_kernel(const WgradRo
             if (w.rank_minor) G[n * r + j0 + j] = y;
             else G[(int64_t)(j0 + j) * w.N + n] = y;
         }
-    if (C > 1) cluster_sync();
+    if (C > 1) cluster_sync_relaxed();  // nobody reads this CTA's sums any more
 }
 
 // Cluster size for `items` clusters: CTAs for at most two per SM at once (384 tokens of one adapter

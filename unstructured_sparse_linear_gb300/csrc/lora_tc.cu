@@ -88,10 +88,12 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int 
                  : "memory");
 }
 
-// Arrive on the barrier at local address `bar` in CTA `rank` of the cluster; what this thread
-// (and, through a barrier before, its CTA) wrote is visible to whoever then waits there.
+// Arrive on the barrier at local address `bar` in CTA `rank` of the cluster; this CTA's shared memory is
+// then as this thread (and, through a barrier before, its CTA) left it, for whoever waits there. (A
+// release of global memory as well took 0.5 us each time: 1037 tokens 21.7 us, 20.9 so.)
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar, int rank) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_map(bar, rank)) : "memory");
+    cluster_release_smem();
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_map(bar, rank)) : "memory");
 }
 
 __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) {
@@ -448,7 +450,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
         sh.failed = 0;
     }
     __syncthreads();
-    if (C > 1) cluster_sync();  // the other ranks' barriers are initialised
+    if (C > 1) cluster_sync_relaxed();  // the other ranks' barriers are initialised
     // All before this line overlaps the kernel before this one, and touches no memory that it writes.
     pdl_wait();
     // Every cluster's first tile (the list has a slot per cluster; what lies behind its end is not used).
@@ -776,8 +778,9 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
                 mbar_arrive(smem_u32(&sh.empty[held]));
             }
             named_barrier(1, kEpi);
-            // this rank's products with P's parts are complete (their accumulators were read)
-            if (et < C) mbar_arrive_remote(smem_u32(&sh.freed), et);
+            // This rank's products with P's parts are complete (their accumulators were read). Not after the
+            // last tile: nobody would wait for that, and a CTA leaves only when nothing is on its way to it.
+            if (et < C && it + ncl < ntiles) mbar_arrive_remote(smem_u32(&sh.freed), et);
         }
         if (lane == 0) bulk_wait<0>();
     }
@@ -786,7 +789,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
     if (sh.failed && tid == 0)  // the other ranks' stores may still be on their way to this CTA and back
         for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < kDrainNs / 100;) {
         }
-    if (C > 1) cluster_sync();  // nobody reads this CTA's sums or arrives on its barriers any more
+    if (C > 1) cluster_sync_relaxed();  // nobody sends sums, parts or arrivals to this CTA any more
     if (warp == 1) tc::tmem_dealloc(tmem, Cfg::kTmem);
 }
 
@@ -1074,7 +1077,10 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
         tc::fence_before_sync();
     }
     __syncthreads();
-    if (C > 1) cluster_sync();
+    if (C > 1) {
+        cluster_release_smem();
+        cluster_sync_relaxed();
+    }
     {
         // this rank's share of the columns, every sum in rank order, eight values at a time: of a
         // row j (N is a multiple of 8), or of a column where the ranks are the contiguous axis
@@ -1134,7 +1140,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
     }
     if (g.early && !dependent) pdl_wait();  // so that the kernel before this one has ended when this one has
     __syncthreads();
-    if (C > 1) cluster_sync();  // nobody reads this CTA's sums any more
+    if (C > 1) cluster_sync_relaxed();  // nobody reads this CTA's sums any more
     if (warp == 1) tc::tmem_dealloc(tmem, Cfg::kTmem);
 }
 
