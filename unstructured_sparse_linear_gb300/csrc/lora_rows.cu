@@ -176,7 +176,9 @@ __device__ __forceinline__ void copy_rows(const RowsArgs& g, const int32_t* tok,
     }
 }
 
-constexpr int kCols = 2;  // columns of O per thread at a time, kThreads apart
+// Columns of O per thread at a time, kThreads apart. (64 tokens of 48 adapters, 4096 to 11008: 8.6 us; with
+// one 10.3, four 9.0; two whose weights are loaded before P is formed 9.4.)
+constexpr int kCols = 2;
 
 // One tile of NR rows at most: this CTA's shares of K and of the columns.
 template <typename T, bool kBack, int NR>
@@ -195,29 +197,8 @@ __device__ __forceinline__ void one_tile(const RowsArgs& g, const LoraSmall* til
 #pragma unroll
     for (int i = 0; i < NR; ++i) urow[i] = static_cast<const T*>(a.U) + (int64_t)t.tok[i] * a.ldu;
 
-    // Columns n0 + tid + q kThreads of O at a time. The first ones' weights (16 ranks) and base do
-    // not depend on P: they are on their way while P is formed, where the registers allow. (Two
-    // columns measured better than four, and than loading the next ones ahead: 64 tokens of 48
-    // adapters, 4096 to 11008, 10.8 us against 13.2 and 11.5.)
-    constexpr int kPre = 16 / V;
-    constexpr bool kPrefetch = !kBack && NR <= 2 && sizeof(T) == 2;
-    uint4 w0[kCols][kPre];
-    T b0[kCols][NR];
-    const bool pre = kPrefetch && g.vec_r && r >= 16 && O;
     const int64_t col = n0 + tid;
     const int64_t bstep = (int64_t)kThreads * r;
-    if (pre) {
-        const T* b = B + col * r;
-#pragma unroll
-        for (int q = 0; q < kCols; ++q, b += bstep) {
-            const bool in = col + q * kThreads < n1;
-#pragma unroll
-            for (int i = 0; i < kPre; ++i) w0[q][i] = in ? ld_v4(b + i * V) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < NR; ++i)
-                if (base && in) b0[q][i] = base[(int64_t)t.tok[i] * a.ldb + col + q * kThreads];
-        }
-    }
     const float s = a.scale_all * (a.scale ? a.scale[t.adapter] : 1.f);
 
     if constexpr (kBack) phase1_backward<T, NR>(urow, B, k0, k1, r, rp, part);
@@ -261,7 +242,6 @@ __device__ __forceinline__ void one_tile(const RowsArgs& g, const LoraSmall* til
             float acc[kCols][NR];
             T bv[kCols][NR];  // base: on its way while the sums are formed, added last
             bool in[kCols];
-            const bool first = pre && n == col;
 #pragma unroll
             for (int q = 0; q < kCols; ++q) {
                 in[q] = n + q * kThreads < n1;
@@ -269,7 +249,7 @@ __device__ __forceinline__ void one_tile(const RowsArgs& g, const LoraSmall* til
                 for (int i = 0; i < NR; ++i) {
                     acc[q][i] = 0.f;
                     bv[q][i] = Elt<T>::from_f(0.f);
-                    if (base && in[q]) bv[q][i] = first ? b0[q][i] : base[(int64_t)t.tok[i] * a.ldb + n + q * kThreads];
+                    if (base && in[q]) bv[q][i] = base[(int64_t)t.tok[i] * a.ldb + n + q * kThreads];
                 }
             }
             auto step = [&](int j, const float (&w)[kCols]) {
@@ -301,19 +281,9 @@ __device__ __forceinline__ void one_tile(const RowsArgs& g, const LoraSmall* til
                         step(j + e, w);
                     }
                 };
-                int j = 0;
-                if (kPrefetch && first) {
-#pragma unroll
-                    for (int i = 0; i < kPre; ++i) {
-                        uint4 v[kCols];
-#pragma unroll
-                        for (int q = 0; q < kCols; ++q) v[q] = w0[q][i];
-                        steps(i * V, v);
-                    }
-                    j = 16;
-                }
                 const T* b = B + n * r;
-                for (; j < r; j += V) {
+#pragma unroll 2
+                for (int j = 0; j < r; j += V) {
                     uint4 v[kCols];
 #pragma unroll
                     for (int q = 0; q < kCols; ++q) v[q] = in[q] ? ld_v4(b + q * bstep + j) : make_uint4(0, 0, 0, 0);
@@ -351,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_rows_kernel(const RowsArgs g
     pdl_wait();
     // Backward: the weight gradients' kernel begins beside this one, and relies on all before it being
     // complete, so the trigger is behind the wait. Forward: the next call's CTAs come as this one's
-    // leave (waiting beside them they cost 1.5 of 11.5 us: 64 tokens of 48 adapters, 4096 to 11008).
+    // leave (waiting beside them they cost 1.5 us of then 11.5: 64 tokens of 48 adapters, 4096 to 11008).
     if (kBack) pdl_trigger();
     // (the list has a slot for every cluster; what lies behind its end is not used)
     LoraSmall t = g.v.small[cid];
@@ -475,7 +445,7 @@ __global__ void __launch_bounds__(kThreads) lora_wgrad_rows_kernel(const WgradRo
 }
 
 // Cluster size for `items` clusters: CTAs for at most two per SM at once (384 tokens of one adapter
-// in clusters of 8 were two waves, 16.6 us; 12 us in clusters of 4), at most 8 (the portable limit).
+// in clusters of 8 are two waves, 14.2 us; 10.9 us in clusters of 4), at most 8 (the portable limit).
 int pick_cluster(int64_t items, int64_t most) {
     const int64_t want = 2 * (int64_t)device_props().sm_count;
     int c = 1;
@@ -509,8 +479,8 @@ cudaError_t run_rows(bool back, const LoraArgs& a, const LoraPlanView& v, cudaSt
     const int64_t clusters = min64(cap, (int64_t)device_props().sm_count * 8);
     // Few tiles: a tile's columns are shared by several clusters while there is an SM for every CTA and
     // 8192 products of a column and a rank are left to each. (16 tokens of one adapter, rank 64, 2048 to
-    // 8192: 16.4 us with one cluster of 8 per tile, 11.8 us so; 64 tokens of rank 16, 4096 to 4096, which
-    // this leaves alone: 7.2 us, with two clusters a tile 9.2.)
+    // 8192: 15.0 us with one cluster of 8 per tile, 10.3 us so; 64 tokens of 48 adapters, rank 16, 4096 to
+    // 4096, which this leaves alone: 8.4 us, with two clusters a tile 12.5.)
     int split = 1;
     if (a.O)
         while (split < 16 && expected * c * split * 2 <= (int64_t)device_props().sm_count &&
@@ -560,18 +530,19 @@ cudaError_t launch_lora_wgrad_rows(int dt, const LoraWgradArgs* w, int nw, int32
 }
 
 // Which kernels: the general one multiplies T r (K + N) times on the CUDA cores and reads an
-// adapter's weights for every 8 rows, the tensor-core one has about 16 us of latency (two phases
+// adapter's weights for every 8 rows, the tensor-core one has about 13 us of latency (two phases
 // with an exchange between them) and reads the weights for every 128 rows, so for every adapter of
-// a mixed batch. Measured (bf16, us, general : tensor cores):
-//   forward, 4096 -> 4096, rank 16: 512 tokens of one adapter 12.4 : 16.4, 1024 18.4 : 16.5; of 48
-//   adapters 1024 tokens 19.0 : 32.2; 2048 -> 8192, rank 64: 128 tokens of one adapter 24 : 24, 256
-//   of 8 25 : 26, 384 43 : 31, of 48 adapters 384 41 : 43, 512 59 : 46;
+// a mixed batch. Measured (bf16, us, general : tensor cores; adapters picked at random):
+//   forward, 4096 -> 4096, rank 16: 512 tokens of one adapter 11.0 : 13.0, 1024 16.9 : 13.0; of 8
+//   1024 tokens 17.3 : 28.1; of 48 1024 20.9 : 31.0; 2048 -> 8192, rank 64: 96 tokens of one adapter
+//   15.2 : 20.7, 128 22.6 : 21.0; of 8 256 24.2 : 23.7, 384 39 : 28; of 48 384 42.5 : 44.1, 512 71 : 44;
 //   input gradient (whose general form reads B element by element): rank 16, 256 tokens of one adapter
-//   13.4 : 16.2, 512 20 : 16; of 48 256 19.6 : 27.5, 512 33 : 29; rank 64, 16 tokens 46 : 20.
+//   13.0 : 13.3, 384 20 : 13.4; of 8 256 15.0 : 17.3, 384 20.1 : 19.9; of 48 256 19.9 : 27.9, 384 30.8 :
+//   28.5; rank 64, 16 tokens 46 : 18.
 static bool general_is_faster(bool back, const LoraArgs& a, const LoraPlanView& v) {
-    const int64_t work = (int64_t)v.tokens * a.rank, adapters = min64(v.n, 22);
-    if (back) return a.rank <= 32 && work <= 4096 + 256 * min64(v.n, 8);
-    return work <= 10240 + 1024 * adapters;
+    const int64_t work = (int64_t)v.tokens * a.rank;
+    if (back) return a.rank <= 32 && work <= 4096 + 192 * min64(v.n, 8);
+    return work <= 9216 + 960 * min64(v.n, 22);
 }
 
 cudaError_t launch_lora(int dt, bool back, const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) {
