@@ -30,16 +30,16 @@ constexpr uint32_t kUBytes = kLoraTile * 128;  // a 128 x 64 tile of U, base or 
 
 // The L2 policy of a gradient's rows: dY is read twice, by two kernels, beside operands that are read or
 // written once; where all of it leaves L2 first, more of dY is still there for the second read than under
-// the usual order (4096 tokens, 4096 -> 11008, rank 16: 57.2 us, 63.1 without; 8192 94.1, 97.3; with 16384,
-// whose 361 MB of dY L2 does not hold either way, 184 and 180).
+// the usual order (4096 tokens, 4096 -> 11008, rank 16: 51.9 us, 59.2 without; 8192 92.3, 95.0; with 16384,
+// whose 361 MB of dY L2 does not hold either way, 182 and 178).
 __device__ __forceinline__ uint64_t evict_first_policy() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
 
-// A box of a 2-D tensor. kHint: with the L2 policy (the neutral one is not free: 2 of 61 us for a long
-// prompt's forward product).
+// A box of a 2-D tensor. kHint: with the L2 policy (the neutral one is not free: 8192 tokens forward,
+// 2048 -> 8192, 61.4 us, 58.5 without).
 template <bool kHint>
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
                                             uint64_t policy) {
@@ -588,7 +588,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
         const int own = kLoraTile >> clog;  // rows that this rank sums: [crank * own, ...)
         // Tokens without an adapter, O = base, P = 0: first, while the loads for the first sums are
-        // under way (1037 tokens of 24 adapters, 4096 -> 4096: 22.3 us, and 23.3 with them last).
+        // under way (8192 tokens, 2048 -> 8192: 58.5 us, and 58.8 with them last).
         const bool copy = g.O && (g.O != g.base);
         if (copy || g.P) {
             for (int64_t pos = (int64_t)g.v.off[g.v.n] + blockIdx.x; pos < g.v.tokens; pos += gridDim.x) {
