@@ -372,6 +372,53 @@ def test_plan_made_on_a_busy_stream_and_used_on_another():
     assert torch.equal(got, want)
 
 
+def test_one_plan_in_graphs_and_threads_at_the_same_time():
+    """Calls that share a plan but not an order (graphs replayed on two streams, threads on one
+    stream) do not share what lies between their two products."""
+    import threading
+
+    T = 700
+    d = [make("bf16", T, 512, 1024, 16, 1, "one", seed=31 + i) for i in range(4)]
+    p = plan_of(d[0])
+
+    def call(x):
+        return sp.lora_grad(x["dY"], x["X"], x["A"], x["B"], p, scale=x["scale"], dX_base=x["dX_base"])
+
+    want = [call(x) for x in d]
+    graphs, outs = [], []
+    torch.cuda.synchronize()
+    for x in d:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append([call(x) for _ in range(8)])
+    streams = [torch.cuda.Stream() for _ in d]
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for ref, runs in zip(want, outs):
+        for out in runs:
+            assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+    got = [[] for _ in d]
+
+    def work(i):
+        for _ in range(50):
+            got[i].append(call(d[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(d))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for ref, runs in zip(want, got):
+        assert len(runs) == 50
+        for out in runs:
+            assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
 @pytest.mark.parametrize("T", [5, 300, 1500])
 def test_inputs_written_just_before_by_kernels_copies_and_other_streams(T):
     """Each launch may begin while the one before it ends: what that one writes is waited for,

@@ -14,6 +14,8 @@ rows need unit stride inside and one row stride; everything else is contiguous.
 """
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from . import _DTYPE, _L, _check, _req
@@ -76,7 +78,22 @@ class LoraPlan(Built):
     def __init__(self, buf: torch.Tensor, tokens: int, n_adapters: int):
         super().__init__(buf)
         self.buf, self.tokens, self.n_adapters = buf, tokens, n_adapters
-        self._grad_ws = {}  # lora_grad's workspace bytes by rank
+        self._scratch = {}
+
+    def _grad_scratch(self, rank: int, stream: int):
+        """(buffer, address, bytes) of lora_grad's workspace on the current stream. It is kept for the calls
+        of one thread on one stream, which come one after the other (allocating and freeing one took
+        2 of a small call's 29 us); a graph capture has its own, as replays may run beside those."""
+        capturing = torch._C._cuda_isCurrentStreamCapturing()
+        key = (rank, stream, threading.get_ident())
+        ws = None if capturing else self._scratch.get(key)
+        if ws is None:
+            size = int(_L().spops_lora_grad_workspace_size(self.tokens, rank))
+            buf = torch.empty(size, dtype=torch.uint8, device=self.device)
+            ws = (buf, buf.data_ptr(), size)
+            if not capturing:
+                self._scratch[key] = ws
+        return ws
 
     def order(self) -> torch.Tensor:
         """The tokens sorted by adapter (stable; those without an adapter last), int32."""
@@ -231,14 +248,11 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
             dA = _like(dA_out, A, "dA_out") if dA_out is not None else torch.empty_like(A)
         if need[2]:
             dB = _like(dB_out, B, "dB_out") if dB_out is not None else torch.empty_like(B)
-        size = plan._grad_ws.get(rank)
-        if size is None:
-            size = plan._grad_ws[rank] = int(lib.spops_lora_grad_workspace_size(T, rank))
-        ws = torch.empty(size, dtype=torch.uint8, device=dev)
         stream = _raw_stream(dev.index)
+        ws, ws_ptr, size = plan._grad_scratch(rank, stream)
         st = lib.spops_lora_grad(dy, lddy, x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out,
                                  rank, n, hp, b, ldb, dx, lddx, dA.data_ptr() if need[1] else 0,
-                                 dB.data_ptr() if need[2] else 0, plan._on_stream(stream), ws.data_ptr(), size, stream)
+                                 dB.data_ptr() if need[2] else 0, plan._on_stream(stream), ws_ptr, size, stream)
     if st:
         _check(st, "lora_grad")
     return dX, dA, dB
