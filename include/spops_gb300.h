@@ -328,6 +328,25 @@ SPOPS_API int spops_lora_add(const void* X, int64_t ldx, const void* A, const vo
                              int32_t rank, int32_t n_adapters, const void* base, int64_t ldb, void* Y, int64_t ldy,
                              float* h, const void* plan, void* stream);
 
+/* spops_lora_add with its arguments in one block: a binding that converts them one by one takes
+ * longer for that than a small call takes on the device. */
+typedef struct {
+    const void* X;
+    int64_t ldx;
+    const void *A, *B;
+    const float* scale;
+    const void* base;
+    int64_t ldb;
+    void* Y;
+    int64_t ldy;
+    float* h;
+    const void* plan;
+    void* stream;
+    float scale_all;
+    int32_t dtype, tokens, in_features, out_features, rank, n_adapters;
+} spops_lora_add_args;
+SPOPS_API int spops_lora_add_block(const spops_lora_add_args* args);
+
 /* Scratch bytes spops_lora_grad needs. */
 SPOPS_API size_t spops_lora_grad_workspace_size(int32_t tokens, int32_t rank);
 
@@ -343,6 +362,28 @@ SPOPS_API int spops_lora_grad(const void* dY, int64_t lddy, const void* X, int64
                               int32_t out_features, int32_t rank, int32_t n_adapters, const float* h,
                               const void* dX_base, int64_t ldb, void* dX, int64_t lddx, void* dA, void* dB,
                               const void* plan, void* workspace, size_t ws_bytes, void* stream);
+
+/* spops_lora_grad with its arguments in one block. */
+typedef struct {
+    const void* dY;
+    int64_t lddy;
+    const void* X;
+    int64_t ldx;
+    const void *A, *B;
+    const float *scale, *h;
+    const void* dX_base;
+    int64_t ldb;
+    void* dX;
+    int64_t lddx;
+    void *dA, *dB;
+    const void* plan;
+    void* workspace;
+    uint64_t ws_bytes;
+    void* stream;
+    float scale_all;
+    int32_t dtype, tokens, in_features, out_features, rank, n_adapters;
+} spops_lora_grad_args;
+SPOPS_API int spops_lora_grad_block(const spops_lora_grad_args* args);
 
 /* ---------------------------------------------------------------- gradient norm, clipping */
 

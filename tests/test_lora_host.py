@@ -103,3 +103,37 @@ def test_clip_refusals(lib):
     assert f(P(0x1000), 1, 1, 1, 1.0, P(0x2002), P(0x3000), W, None) == 1
     assert f(P(0x1000), 1, 1, 1, 1.0, P(0x2000), P(0x3000), 8, None) == 3
     assert lib.spops_grad_norm(P(0x1000), -1, 1, P(0x2000), P(0x3000), W, None) == 1
+
+
+def test_argument_blocks(lib):
+    """The calls that take their arguments in a block see the same ones: each refusal names the value."""
+    from unstructured_sparse_linear_gb300 import lora
+
+    def add_block(x=0x100000, ldx=64, ldb=32, ldy=32, h=0, plan=0x600000, scale_all=1.0, dtype=2, tokens=8, k=64, n=32,
+                  rank=4, na=2):
+        return lib.spops_lora_add_block(lora._ADD_ARGS(x, ldx, 0x200000, 0x300000, 0, 0x400000, ldb, 0x500000, ldy, h,
+                                                       plan, 0, scale_all, dtype, tokens, k, n, rank, na))
+
+    def grad_block(dy=0x100000, lddy=32, ldx=64, h=0, ldb=64, lddx=64, da=0x600000, db=0x700000, plan=0x800000,
+                   ws=0x900000, size=W, scale_all=1.0, dtype=2, tokens=8, k=64, n=32, rank=4, na=2):
+        return lib.spops_lora_grad_block(lora._GRAD_ARGS(dy, lddy, 0x200000, ldx, 0x300000, 0x400000, 0, h, 0xa00000,
+                                                         ldb, 0x500000, lddx, da, db, plan, ws, size, 0, scale_all,
+                                                         dtype, tokens, k, n, rank, na))
+
+    assert lib.spops_lora_add_block(None) == 1 and lib.spops_lora_grad_block(None) == 1
+    assert add_block(tokens=0) == 0 and grad_block(tokens=0, da=0, db=0) == 0
+    for call in (add_block, grad_block):
+        assert call(dtype=7) == 1 and b"7" in lib.spops_last_error()
+        assert call(tokens=-11) == 1 and b"-11" in lib.spops_last_error()
+        assert call(k=-12) == 1 and b"-12" in lib.spops_last_error()
+        assert call(n=-13) == 1 and b"-13" in lib.spops_last_error()
+        assert call(na=-14) == 1 and b"-14" in lib.spops_last_error()
+        assert call(rank=129) == 2 and b"129" in lib.spops_last_error()
+        assert call(scale_all=float("nan")) == 1 and b"scale_all" in lib.spops_last_error()
+        assert call(plan=0x600004) == 1 and b"plan" in lib.spops_last_error()
+        assert call(ldx=61) == 1 and b"X" in lib.spops_last_error()
+        assert call(h=0x800002) == 1 and b"h is not" in lib.spops_last_error()
+    assert add_block(x=0) == 1 and add_block(ldb=31) == 1 and add_block(ldy=31) == 1
+    assert grad_block(dy=0) == 1 and grad_block(lddy=31) == 1 and grad_block(ldb=63) == 1 and grad_block(lddx=63) == 1
+    assert grad_block(da=0x600001) == 1 and grad_block(db=0x700001) == 1
+    assert grad_block(ws=0x900008) == 3 and grad_block(size=16) == 3

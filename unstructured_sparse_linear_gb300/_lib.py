@@ -53,9 +53,11 @@ SIGNATURES = {
     "spops_lora_plan_build": (_INT, [_P, _I32, _I32, _P, _SZ, _P]),
     "spops_lora_add": (_INT, [_P, _I64, _P, _P, _P, _F32, _INT, _I32, _I32, _I32, _I32, _I32, _P, _I64, _P, _I64, _P,
                               _P, _P]),
+    "spops_lora_add_block": (_INT, [_P]),
     "spops_lora_grad_workspace_size": (_SZ, [_I32, _I32]),
     "spops_lora_grad": (_INT, [_P, _I64, _P, _I64, _P, _P, _P, _F32, _INT, _I32, _I32, _I32, _I32, _I32, _P, _P, _I64,
                                _P, _I64, _P, _P, _P, _P, _SZ, _P]),
+    "spops_lora_grad_block": (_INT, [_P]),
     "spops_grad_set_size": (_SZ, [_I32]),
     "spops_grad_set_build": (_INT, [_P, _P, _P, _P, _I32, _P, _SZ, ctypes.POINTER(_I64), ctypes.POINTER(_I32), _P]),
     "spops_grad_norm_workspace_size": (_SZ, []),

@@ -629,6 +629,13 @@ int spops_lora_add(const void* X, int64_t ldx, const void* A, const void* B, con
                        "lora_add launch");
 }
 
+int spops_lora_add_block(const spops_lora_add_args* a) {
+    if (!a) return fail(SPOPS_ERR_INVALID_ARG, "args is NULL");
+    return spops_lora_add(a->X, a->ldx, a->A, a->B, a->scale, a->scale_all, a->dtype, a->tokens, a->in_features,
+                          a->out_features, a->rank, a->n_adapters, a->base, a->ldb, a->Y, a->ldy, a->h, a->plan,
+                          a->stream);
+}
+
 size_t spops_lora_grad_workspace_size(int32_t tokens, int32_t rank) {
     // dY B (and X A^T, where the caller has no h), fp32
     return tokens < 1 || rank < 1 ? 16 : 2 * align_up((size_t)tokens * rank * 4, 256);
@@ -740,6 +747,13 @@ int spops_lora_grad(const void* dY, int64_t lddy, const void* X, int64_t ldx, co
     }
     if (nw == 0) return ok();
     return cuda_status(launch_lora_wgrad(dtype, w, nw, rank, scale, scale_all, v, dX || dA, s), "lora_grad dA dB launch");
+}
+
+int spops_lora_grad_block(const spops_lora_grad_args* a) {
+    if (!a) return fail(SPOPS_ERR_INVALID_ARG, "args is NULL");
+    return spops_lora_grad(a->dY, a->lddy, a->X, a->ldx, a->A, a->B, a->scale, a->scale_all, a->dtype, a->tokens,
+                           a->in_features, a->out_features, a->rank, a->n_adapters, a->h, a->dX_base, a->ldb, a->dX,
+                           a->lddx, a->dA, a->dB, a->plan, a->workspace, (size_t)a->ws_bytes, a->stream);
 }
 
 /* ---------------------------------------------------------------- gradient norm and clipping */

@@ -14,6 +14,7 @@ rows need unit stride inside and one row stride; everything else is contiguous.
 """
 from __future__ import annotations
 
+import struct
 import threading
 
 import torch
@@ -21,6 +22,11 @@ import torch
 from . import _DTYPE, _L, _check, _req
 
 __all__ = ["LoraPlan", "lora_plan", "lora_add", "lora_grad"]
+
+
+# spops_lora_add_args and spops_lora_grad_args
+_ADD_ARGS = struct.Struct("12qf6i").pack
+_GRAD_ARGS = struct.Struct("18qf6i").pack
 
 
 def _raw_stream(index: int) -> int:
@@ -202,8 +208,9 @@ def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h:
             y, ldy = _rows(out, "out", T, n_out, dt, dev)
         h = torch.empty((T, rank), dtype=torch.float32, device=dev) if return_h else None
         stream = _raw_stream(dev.index)
-        st = lib.spops_lora_add(x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out, rank, n,
-                                b, ldb, y, ldy, h.data_ptr() if return_h else 0, plan._on_stream(stream), stream)
+        st = lib.spops_lora_add_block(_ADD_ARGS(
+            x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, b, ldb, y, ldy, h.data_ptr() if return_h else 0,
+            plan._on_stream(stream), stream, s_all, _DTYPE[dt], T, k, n_out, rank, n))
     if st:
         _check(st, "lora_add")
     return (out, h) if return_h else out
@@ -250,9 +257,10 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
             dB = _like(dB_out, B, "dB_out") if dB_out is not None else torch.empty_like(B)
         stream = _raw_stream(dev.index)
         ws, ws_ptr, size = plan._grad_scratch(rank, stream)
-        st = lib.spops_lora_grad(dy, lddy, x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, s_all, _DTYPE[dt], T, k, n_out,
-                                 rank, n, hp, b, ldb, dx, lddx, dA.data_ptr() if need[1] else 0,
-                                 dB.data_ptr() if need[2] else 0, plan._on_stream(stream), ws_ptr, size, stream)
+        st = lib.spops_lora_grad_block(_GRAD_ARGS(
+            dy, lddy, x, ldx, A.data_ptr(), B.data_ptr(), s_ptr, hp, b, ldb, dx, lddx,
+            dA.data_ptr() if need[1] else 0, dB.data_ptr() if need[2] else 0, plan._on_stream(stream), ws_ptr, size,
+            stream, s_all, _DTYPE[dt], T, k, n_out, rank, n))
     if st:
         _check(st, "lora_grad")
     return dX, dA, dB
