@@ -13,7 +13,7 @@ import ctypes
 import torch
 
 from . import _DTYPE, _L, _check, _req
-from .lora import Built, _on, _raw_stream
+from .lora import Built, _elsewhere, _raw_stream
 
 __all__ = ["GradSet", "grad_norm", "clip_grads"]
 
@@ -81,10 +81,12 @@ def grad_norm(grads) -> torch.Tensor:
     a list of tensors."""
     s = _set(grads)
     dev = s.device
-    with _on(dev):
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        stream = _raw_stream(dev.index)
-        st = _L().spops_grad_norm(s._on_stream(stream), s._n, s._chunks, norm.data_ptr(), s._partial_ptr, s._ws, stream)
+    if _elsewhere(dev.index):
+        with torch.cuda.device(dev):
+            return grad_norm(s)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    stream = _raw_stream(dev.index)
+    st = _L().spops_grad_norm(s._on_stream(stream), s._n, s._chunks, norm.data_ptr(), s._partial_ptr, s._ws, stream)
     if st:
         _check(st, "grad_norm")
     return norm
@@ -97,11 +99,13 @@ def clip_grads(grads, max_norm: float) -> torch.Tensor:
     that matters. grads: a GradSet or a list of tensors."""
     s = _set(grads)
     dev = s.device
-    with _on(dev):
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        stream = _raw_stream(dev.index)
-        st = _L().spops_clip_grads(s._on_stream(stream), s._n, s._chunks, s._in_place, float(max_norm), norm.data_ptr(),
-                                   s._partial_ptr, s._ws, stream)
+    if _elsewhere(dev.index):
+        with torch.cuda.device(dev):
+            return clip_grads(s, max_norm)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    stream = _raw_stream(dev.index)
+    st = _L().spops_clip_grads(s._on_stream(stream), s._n, s._chunks, s._in_place, float(max_norm), norm.data_ptr(),
+                               s._partial_ptr, s._ws, stream)
     if st:
         _check(st, "clip_grads")
     return norm
