@@ -499,11 +499,11 @@ cudaError_t run_wgrad_rows(const LoraWgradArgs* w, int nw, int32_t rank, const f
     WgradRowsArgs g;
     g.nw = nw;
     g.jb = (rank + kWgJ - 1) / kWgJ;
+    g.blocks[0] = g.blocks[1] = 0;
     for (int i = 0; i < nw; ++i) {
         g.w[i] = w[i];
         g.blocks[i] = (w[i].N + kThreads - 1) / kThreads;
     }
-    if (nw == 1) g.blocks[1] = 0;
     g.rank = rank;
     g.scale = scale;
     g.scale_all = scale_all;
