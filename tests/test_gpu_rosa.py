@@ -79,6 +79,26 @@ def test_only_the_gradients_that_are_asked_for():
     assert rel_fro(as_f64(layer.B.grad)[0], np.tile(want.sum(0), (64, 1))) <= REL[torch.bfloat16]
 
 
+def test_first_call_of_a_length_in_a_graph_capture():
+    """The plan of a length that is first seen in a capture belongs to the graph: calls outside make their own."""
+    torch.manual_seed(2)
+    W = torch.randn(72, 48, device=DEV, dtype=torch.bfloat16).mul_(48 ** -0.5)
+    layer = sp.RosaLinear(W, 4)
+    layer.B.data.normal_(0, 0.1)
+    X = torch.randn(300, 48, device=DEV, dtype=torch.bfloat16)
+    with torch.no_grad():
+        layer(X[:7])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            Y = layer(X)
+        assert list(layer._plans) == [7]
+        own = layer(X)
+        graph.replay()
+        assert list(layer._plans) == [7, 300] and torch.equal(Y, own)
+    want = as_f64(X) @ (as_f64(W) + as_f64(layer.B)[0] @ as_f64(layer.A)[0]).T
+    assert rel_fro(as_f64(own), want) <= REL[torch.bfloat16]
+
+
 def test_example_trains_and_serves():
     spec = importlib.util.spec_from_file_location("rosa_example", os.path.join(ROOT, "examples",
                                                                               "rosa_finetune_and_serve.py"))

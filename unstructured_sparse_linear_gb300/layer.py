@@ -141,9 +141,11 @@ class RosaLinear(torch.nn.Module):
         if plan is None:
             plan = self._plans.get(X2.shape[0])
             if plan is None:
-                if len(self._plans) >= 64:  # (lengths that come and go)
-                    self._plans.clear()
                 plan = lora_plan(None, self.n_adapters, tokens=X2.shape[0], device=X2.device)
-                self._plans[X2.shape[0]] = plan
+                # (one made in a graph capture is written by the graph's replays: not for calls outside it)
+                if not torch.cuda.is_current_stream_capturing():
+                    if len(self._plans) >= 64:  # (lengths that come and go)
+                        self._plans.clear()
+                    self._plans[X2.shape[0]] = plan
         Y = RosaLinearFunction.apply(X2.contiguous(), self.values, self.A, self.B, self, plan)
         return Y.reshape(*X.shape[:-1], self.out_features)
