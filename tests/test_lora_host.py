@@ -137,3 +137,10 @@ def test_argument_blocks(lib):
     assert grad_block(dy=0) == 1 and grad_block(lddy=31) == 1 and grad_block(ldb=63) == 1 and grad_block(lddx=63) == 1
     assert grad_block(da=0x600001) == 1 and grad_block(db=0x700001) == 1
     assert grad_block(ws=0x900008) == 3 and grad_block(size=16) == 3
+
+
+def test_plan_sizes_beyond_32_bits():
+    import unstructured_sparse_linear_gb300 as sp
+    for tokens, n in ((2 ** 31, 1), (2 ** 32 + 5, 1), (-1, 1), (5, 2 ** 31), (5, 2 ** 32 + 1), (5, 0)):
+        with pytest.raises(ValueError, match="tokens >= 0"):
+            sp.lora_plan(None, n, tokens=tokens, device="cuda:0")

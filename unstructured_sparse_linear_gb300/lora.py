@@ -126,8 +126,8 @@ def lora_plan(adapter_ids: torch.Tensor | None, n_adapters: int, tokens: int | N
             raise ValueError(f"adapter_ids must be a vector with one id per token, got {tuple(adapter_ids.shape)}")
         tokens, dev, ids = adapter_ids.numel(), adapter_ids.device, adapter_ids.data_ptr()
     tokens, n_adapters = int(tokens), int(n_adapters)
-    if tokens < 0 or n_adapters < 1:
-        raise ValueError(f"need tokens >= 0 and n_adapters >= 1, got {tokens}, {n_adapters}")
+    if not (0 <= tokens < 2 ** 31 and 1 <= n_adapters < 2 ** 31 - 1):
+        raise ValueError(f"need tokens >= 0 and n_adapters >= 1 of 32 bits, got {tokens}, {n_adapters}")
     lib = _L()
     size = lib.spops_lora_plan_size(tokens, n_adapters)
     with torch.cuda.device(dev):
