@@ -1,8 +1,11 @@
 """Host-side checks of the low-rank adapter and clipping calls that need no GPU: sizes, and
 arguments refused before the device is touched (the pointers below are never dereferenced)."""
+import copy
 import ctypes
+import pickle
 
 import pytest
+import torch
 
 P = ctypes.c_void_p
 W = 1 << 30
@@ -144,3 +147,19 @@ def test_plan_sizes_beyond_32_bits():
     for tokens, n in ((2 ** 31, 1), (2 ** 32 + 5, 1), (-1, 1), (5, 2 ** 31), (5, 2 ** 32 + 1), (5, 0)):
         with pytest.raises(ValueError, match="tokens >= 0"):
             sp.lora_plan(None, n, tokens=tokens, device="cuda:0")
+
+
+def test_copies_hold_no_plan_of_the_original():
+    import unstructured_sparse_linear_gb300 as sp
+    from unstructured_sparse_linear_gb300.lora import Built
+    for cls in (sp.LoraPlan, sp.GradSet):
+        table = cls.__new__(cls)
+        assert isinstance(table, Built)
+        for copier in (copy.copy, copy.deepcopy, pickle.dumps):
+            with pytest.raises(TypeError, match=cls.__name__):
+                copier(table)
+    layer = sp.RosaLinear(torch.randn(6, 4), 2)
+    plan = layer._plans[3] = sp.LoraPlan.__new__(sp.LoraPlan)
+    for twin in (copy.copy(layer), copy.deepcopy(layer), pickle.loads(pickle.dumps(layer))):
+        assert twin._plans == {} and torch.equal(twin.A, layer.A) and torch.equal(twin.weight, layer.weight)
+    assert layer._plans == {3: plan}

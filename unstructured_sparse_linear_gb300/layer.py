@@ -128,6 +128,9 @@ class RosaLinear(torch.nn.Module):
             self.plan = plan_build(row_offsets, self.row_idx, col_idx, self.in_features)
         self._plans = {}  # by number of tokens: every token uses adapter 0
 
+    def __getstate__(self):  # a copy or a pickle of the layer makes its own plans
+        return {**super().__getstate__(), "_plans": {}}
+
     def merged(self, values):
         """W + S."""
         if values is None:

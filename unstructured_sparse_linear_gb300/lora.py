@@ -68,6 +68,9 @@ class Built:
         self._written = torch.cuda.Event()
         self._written.record(torch.cuda.current_stream(buf.device))
 
+    def __reduce_ex__(self, protocol):  # (a copy's kernels would follow the original's addresses)
+        raise TypeError(f"a {type(self).__name__} cannot be copied or pickled: it holds device addresses; make a new one")
+
     def _on_stream(self, stream: int) -> int:
         """The table's address, usable by work that is queued on `stream` from now on."""
         if stream not in self._streams and not torch.cuda.is_current_stream_capturing():
