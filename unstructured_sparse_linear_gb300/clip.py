@@ -96,7 +96,7 @@ def clip_grads(grads, max_norm: float) -> torch.Tensor:
     """Scales every gradient by min(1, max_norm / (norm + 1e-6)), in place or into the set's
     outputs, and returns the norm before clipping (an fp32 scalar on the device). An infinite
     norm scales by 0 and a NaN one by NaN, as the formula says: check the returned norm where
-    that matters. grads: a GradSet or a list of tensors."""
+    that matters. max_norm = inf clips nothing, whatever the norm. grads: a GradSet or a list of tensors."""
     s = _set(grads)
     dev = s.device
     if _elsewhere(dev.index):
