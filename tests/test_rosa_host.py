@@ -1,0 +1,69 @@
+"""RosaLinear's own bookkeeping, with stand-ins for the calls that need a GPU."""
+import gc
+import weakref
+
+import pytest
+import torch
+
+import unstructured_sparse_linear_gb300 as sp
+from unstructured_sparse_linear_gb300 import layer as layer_module
+
+
+class FakePlan:
+    def __init__(self, tokens, device):
+        self.tokens, self.device = tokens, device
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    """A layer whose plans are counted and whose forward pass returns the plan that it was given."""
+    state = {"capturing": False, "made": [], "used": None}
+
+    def lora_plan(ids, n, tokens=None, device=None):
+        state["made"].append(tokens)
+        return FakePlan(tokens, device)
+
+    def apply(X, values, A, B, layer, plan):
+        state["used"] = plan
+        return X.new_zeros(X.shape[0], layer.out_features)
+
+    monkeypatch.setattr(layer_module, "lora_plan", lora_plan)
+    monkeypatch.setattr(layer_module.RosaLinearFunction, "apply", apply)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state["capturing"])
+    state["layer"] = sp.RosaLinear(torch.zeros(6, 4), 2)
+    return state
+
+
+def use(fake, tokens, capturing=False):
+    fake["capturing"] = capturing
+    fake["layer"](torch.zeros(tokens, 4))
+    fake["capturing"] = False
+    plan, fake["used"] = fake["used"], None
+    return plan
+
+
+def test_a_plan_that_a_graph_captured_outlives_the_cache(fake):
+    """Warm-up, capture of the same length, then more other lengths than the cache holds: the graph's
+    replays still read the captured plan, which nothing but the layer owns."""
+    use(fake, 5)
+    captured = weakref.ref(use(fake, 5, capturing=True))
+    passing = weakref.ref(use(fake, 6))
+    for tokens in range(100, 230):
+        use(fake, tokens)
+    gc.collect()
+    assert passing() is None  # (the cache did drop plans)
+    assert captured() is not None
+    assert use(fake, 5) is captured() and fake["made"].count(5) == 1  # and it serves the length again
+    use(fake, 200)
+    again = weakref.ref(use(fake, 200, capturing=True))  # a second graph, beside the first
+    for tokens in range(300, 430):
+        use(fake, tokens)
+    gc.collect()
+    assert captured() is not None and again() is not None
+
+
+def test_a_plan_made_in_a_capture_is_not_kept(fake):
+    use(fake, 5, capturing=True)
+    assert fake["layer"]._plans == {}
+    use(fake, 5)
+    assert fake["made"] == [5, 5]

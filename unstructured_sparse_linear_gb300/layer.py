@@ -127,9 +127,10 @@ class RosaLinear(torch.nn.Module):
             self.row_idx = sort_rows(row_offsets, nnz=col_idx.numel(), index_dtype=col_idx.dtype)
             self.plan = plan_build(row_offsets, self.row_idx, col_idx, self.in_features)
         self._plans = {}  # by number of tokens: every token uses adapter 0
+        self._captured = {}  # those of them that a graph's replays read, kept as long as the layer
 
     def __getstate__(self):  # a copy or a pickle of the layer makes its own plans
-        return {**super().__getstate__(), "_plans": {}}
+        return {**super().__getstate__(), "_plans": {}, "_captured": {}}
 
     def merged(self, values):
         """W + S."""
@@ -137,18 +138,25 @@ class RosaLinear(torch.nn.Module):
             return self.weight
         return csr_add(values, self.row_offsets, self.row_idx, self.col_idx, self.weight)
 
+    def _one_adapter_plan(self, tokens, device):
+        capturing = torch.cuda.is_current_stream_capturing()
+        plan = self._plans.get(tokens) or self._captured.get(tokens)
+        if plan is None:
+            plan = lora_plan(None, self.n_adapters, tokens=tokens, device=device)
+            if capturing:  # (written by the graph's replays: not for calls outside it)
+                return plan
+            if len(self._plans) >= 64:  # (lengths that come and go)
+                self._plans.clear()
+            self._plans[tokens] = plan
+        if capturing:  # the graph holds the plan's address and nothing else holds the plan
+            self._captured[tokens] = plan
+        return plan
+
     def forward(self, X: torch.Tensor, adapter_ids: torch.Tensor | None = None, plan=None) -> torch.Tensor:
         X2 = X.reshape(-1, self.in_features)
         if plan is None and adapter_ids is not None:
             plan = lora_plan(adapter_ids.reshape(-1), self.n_adapters)
         if plan is None:
-            plan = self._plans.get(X2.shape[0])
-            if plan is None:
-                plan = lora_plan(None, self.n_adapters, tokens=X2.shape[0], device=X2.device)
-                # (one made in a graph capture is written by the graph's replays: not for calls outside it)
-                if not torch.cuda.is_current_stream_capturing():
-                    if len(self._plans) >= 64:  # (lengths that come and go)
-                        self._plans.clear()
-                    self._plans[X2.shape[0]] = plan
+            plan = self._one_adapter_plan(X2.shape[0], X2.device)
         Y = RosaLinearFunction.apply(X2.contiguous(), self.values, self.A, self.B, self, plan)
         return Y.reshape(*X.shape[:-1], self.out_features)
