@@ -37,3 +37,16 @@ def test_plan_of_a_captured_length_stays_while_other_lengths_pass():
         assert 300 not in layer._plans and keeps() is not None and keeps().buf.data_ptr() == address
         graph.replay()
         assert torch.equal(Y, want) and torch.equal(layer(X), want)
+
+
+def test_gradients_with_a_graph_match_and_refuse_second_derivatives():
+    layer = layer_of()
+    X = torch.randn(200, 48, device=DEV, dtype=BF16, requires_grad=True)
+    dY = torch.randn(200, 72, device=DEV, dtype=BF16, requires_grad=True)
+    inputs = (X, layer.A, layer.B)
+    want = torch.autograd.grad(layer(X), inputs, dY.detach())
+    got = torch.autograd.grad(layer(X), inputs, dY, create_graph=True)
+    for w, g in zip(want, got):
+        assert torch.equal(w, g)
+        with pytest.raises(RuntimeError, match="twice"):
+            g.float().square().sum().backward(retain_graph=True)

@@ -67,3 +67,39 @@ def test_a_plan_made_in_a_capture_is_not_kept(fake):
     assert fake["layer"]._plans == {}
     use(fake, 5)
     assert fake["made"] == [5, 5]
+
+
+@pytest.fixture
+def plain(monkeypatch):
+    """The two low-rank calls as the kernels do them: on the values, outside autograd."""
+    def lora_add(X, A, B, plan, base=None, scale=1.0, out=None, return_h=False):
+        h = X.detach() @ A.detach()[0].t()
+        out.data.add_(h @ B.detach()[0].t(), alpha=scale)
+        return out, h
+
+    def lora_grad(dY, X, A, B, plan, scale=1.0, h=None, dX_base=None, dX_out=None, need=(True,) * 3, **kw):
+        dY, X, A, B, h = (t.detach() for t in (dY, X, A, B, h))
+        dP = scale * (dY @ B[0])
+        if need[0]:
+            dX_out.data.add_(dP @ A[0])
+        return dX_out if need[0] else None, (dP.t() @ X)[None], scale * (dY.t() @ h)[None]
+
+    monkeypatch.setattr(layer_module, "lora_add", lora_add)
+    monkeypatch.setattr(layer_module, "lora_grad", lora_grad)
+    layer = sp.RosaLinear(torch.randn(6, 4, dtype=torch.float64), 2, scale=0.5)
+    layer.B.data.normal_()
+    return layer
+
+
+def test_second_derivatives_are_refused(plain):
+    X = torch.randn(5, 4, dtype=torch.float64, requires_grad=True)
+    dY = torch.randn(5, 6, dtype=torch.float64, requires_grad=True)
+    Y = plain(X, plan=object())
+    dX, dA, dB = torch.autograd.grad(Y, (X, plain.A, plain.B), dY, create_graph=True)
+    want = dY @ (plain.weight + 0.5 * plain.B[0] @ plain.A[0])
+    assert torch.allclose(dX, want)
+    for first in (dX, dA, dB):
+        with pytest.raises(RuntimeError, match="twice"):
+            first.sum().backward(retain_graph=True)
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(first.sum(), dY, retain_graph=True)

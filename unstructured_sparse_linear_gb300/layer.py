@@ -17,6 +17,7 @@ The row permutation, the mask plan and the transpose's structure are built once 
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import csr_add, csr_transpose, permute_values, plan_build, sddmm, sort_rows, spmm
 from .lora import lora_add, lora_grad, lora_plan
@@ -79,6 +80,7 @@ class RosaLinearFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
+    @once_differentiable  # (the kernels' results carry no graph: second derivatives would miss them)
     def backward(ctx, dY):
         X, values, A, B, h = ctx.saved_tensors
         L = ctx.layer
@@ -106,7 +108,8 @@ class RosaLinear(torch.nn.Module):
     low-rank adapters of one rank, their factor `scale` a number or an fp32 tensor with one per
     adapter; A starts at random and B at zero, so that the adapters start as no change. X is
     token-major [..., in]; adapter_ids (int32, one per token) or a plan of them choose each token's
-    adapter, by default adapter 0 for all."""
+    adapter, by default adapter 0 for all. Gradients are first derivatives: differentiating them again
+    raises."""
 
     def __init__(self, weight: torch.Tensor, rank: int, n_adapters: int = 1, scale=1.0, row_offsets=None, col_idx=None,
                  values=None):
