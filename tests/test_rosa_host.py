@@ -103,3 +103,27 @@ def test_second_derivatives_are_refused(plain):
             first.sum().backward(retain_graph=True)
         with pytest.raises(RuntimeError):
             torch.autograd.grad(first.sum(), dY, retain_graph=True)
+
+
+def test_sparse_linear_refuses_second_derivatives(monkeypatch):
+    """As the kernels' results carry no graph, a penalty on a gradient would be left out of a loss in silence."""
+    W = torch.randn(6, 4, dtype=torch.float64)
+    monkeypatch.setattr(layer_module, "spmm", lambda v, ro, ri, ci, X, m, plan=None: v.detach().reshape(ci) @ X.detach())
+    monkeypatch.setattr(layer_module, "sddmm", lambda ro, ri, ci, dY, X, plan=None: (dY @ X.t()).detach().reshape(-1))
+    monkeypatch.setattr(layer_module, "permute_values", lambda v, t: v.detach().reshape(6, 4).t().contiguous())
+
+    class Layer:
+        row_offsets = row_idx = row_idx_t = plan = plan_t = None
+        col_idx, out_features, in_features = (6, 4), 6, 4
+
+        class transpose:
+            row_offsets, col_idx = None, (4, 6)
+
+    values = W.reshape(-1).clone().requires_grad_()
+    X = torch.randn(4, 5, dtype=torch.float64, requires_grad=True)
+    Y = layer_module.SparseLinearFunction.apply(values, X, Layer)
+    dX, dV = torch.autograd.grad(Y.sum(), (X, values), create_graph=True)
+    assert torch.allclose(dX, W.t() @ torch.ones(6, 5, dtype=torch.float64))
+    for first in (dX, dV):
+        with pytest.raises(RuntimeError, match="twice"):
+            (Y.sum() + first.square().sum()).backward(retain_graph=True)

@@ -32,6 +32,7 @@ class SparseLinearFunction(torch.autograd.Function):
         return Yt
 
     @staticmethod
+    @once_differentiable  # (the kernels' results carry no graph: second derivatives would miss them)
     def backward(ctx, dYt):
         values, Xt = ctx.saved_tensors
         L = ctx.layer
@@ -49,7 +50,8 @@ class SparseLinearFunction(torch.autograd.Function):
 class SparseLinear(torch.nn.Module):
     """Y^T = W X^T with W (out_features x in_features) stored as the values of a fixed CSR
     mask (row_offsets int32, col_idx int16/int32); inputs and outputs are feature-major
-    (features x tokens), fp16 or bf16 (fp32 runs the general kernels)."""
+    (features x tokens), fp16 or bf16 (fp32 runs the general kernels). Gradients are first
+    derivatives: differentiating them again raises."""
 
     def __init__(self, row_offsets: torch.Tensor, col_idx: torch.Tensor, values: torch.Tensor, in_features: int):
         super().__init__()
