@@ -39,10 +39,11 @@ def test_plan_of_a_captured_length_stays_while_other_lengths_pass():
         assert torch.equal(Y, want) and torch.equal(layer(X), want)
 
 
-def test_gradients_with_a_graph_match_and_refuse_second_derivatives():
+@pytest.mark.parametrize("own_dy", [True, False])
+def test_gradients_with_a_graph_match_and_refuse_second_derivatives(own_dy):
     layer = layer_of()
     X = torch.randn(200, 48, device=DEV, dtype=BF16, requires_grad=True)
-    dY = torch.randn(200, 72, device=DEV, dtype=BF16, requires_grad=True)
+    dY = torch.randn(200, 72, device=DEV, dtype=BF16, requires_grad=own_dy)
     inputs = (X, layer.A, layer.B)
     want = torch.autograd.grad(layer(X), inputs, dY.detach())
     got = torch.autograd.grad(layer(X), inputs, dY, create_graph=True)

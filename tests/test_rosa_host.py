@@ -91,18 +91,20 @@ def plain(monkeypatch):
     return layer
 
 
-def test_second_derivatives_are_refused(plain):
+@pytest.mark.parametrize("own_dy", [True, False])
+def test_second_derivatives_are_refused(plain, own_dy):
     X = torch.randn(5, 4, dtype=torch.float64, requires_grad=True)
-    dY = torch.randn(5, 6, dtype=torch.float64, requires_grad=True)
+    dY = torch.randn(5, 6, dtype=torch.float64, requires_grad=own_dy)
     Y = plain(X, plan=object())
     dX, dA, dB = torch.autograd.grad(Y, (X, plain.A, plain.B), dY, create_graph=True)
-    want = dY @ (plain.weight + 0.5 * plain.B[0] @ plain.A[0])
-    assert torch.allclose(dX, want)
+    assert torch.allclose(dX, dY @ (plain.weight + 0.5 * plain.B[0] @ plain.A[0]))
+    assert torch.allclose(dB[0], 0.5 * dY.t() @ X @ plain.A[0].t())
     for first in (dX, dA, dB):
         with pytest.raises(RuntimeError, match="twice"):
-            first.sum().backward(retain_graph=True)
-        with pytest.raises(RuntimeError):
-            torch.autograd.grad(first.sum(), dY, retain_graph=True)
+            (Y.sum() + first.square().sum()).backward(retain_graph=True)
+        for one in (dY, X, plain.A, plain.B) if own_dy else (X, plain.A, plain.B):
+            with pytest.raises(RuntimeError, match="twice"):
+                torch.autograd.grad(first.sum(), one, retain_graph=True)
 
 
 def test_sparse_linear_refuses_second_derivatives(monkeypatch):

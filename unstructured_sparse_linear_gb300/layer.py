@@ -16,11 +16,39 @@ The row permutation, the mask plan and the transpose's structure are built once 
 """
 from __future__ import annotations
 
+import functools
+
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import csr_add, csr_transpose, permute_values, plan_build, sddmm, sort_rows, spmm
 from .lora import lora_add, lora_grad, lora_plan
+
+
+class _Refuse(torch.autograd.Function):
+    """The first `count` of its tensors, as results of all of them that cannot be differentiated."""
+
+    @staticmethod
+    def forward(ctx, count, *tensors):
+        return tensors[:count]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the gradients of this layer cannot be differentiated again: its kernels compute first "
+                           "derivatives only, so they cannot be taken twice")
+
+
+def first_derivatives_only(backward):
+    """A backward pass on the kernels, whose results carry no graph. Under create_graph=True the gradients
+    come back tied to the output's gradient and to what the forward pass saved, so that a second derivative raises
+    instead of missing them. (torch's once_differentiable ties them to the output's gradient alone.)"""
+
+    @functools.wraps(backward)
+    def wrapped(ctx, dY):
+        with torch.no_grad():
+            grads = backward(ctx, dY)
+        return _Refuse.apply(len(grads), *grads, dY, *ctx.saved_tensors) if torch.is_grad_enabled() else grads
+
+    return wrapped
 
 
 class SparseLinearFunction(torch.autograd.Function):
@@ -32,7 +60,7 @@ class SparseLinearFunction(torch.autograd.Function):
         return Yt
 
     @staticmethod
-    @once_differentiable  # (the kernels' results carry no graph: second derivatives would miss them)
+    @first_derivatives_only
     def backward(ctx, dYt):
         values, Xt = ctx.saved_tensors
         L = ctx.layer
@@ -82,7 +110,7 @@ class RosaLinearFunction(torch.autograd.Function):
         return Y
 
     @staticmethod
-    @once_differentiable  # (the kernels' results carry no graph: second derivatives would miss them)
+    @first_derivatives_only
     def backward(ctx, dY):
         X, values, A, B, h = ctx.saved_tensors
         L = ctx.layer
