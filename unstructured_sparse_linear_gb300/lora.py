@@ -19,6 +19,8 @@ import threading
 
 import torch
 
+from torch.autograd.graph import increment_version
+
 from . import _DTYPE, _L, _check, _req
 
 __all__ = ["LoraPlan", "lora_plan", "lora_add", "lora_grad"]
@@ -52,6 +54,13 @@ def _rows(t, name, rows, cols, dtype, device):
     if (step != 1 and cols > 1) or (ld < cols and rows > 1):
         raise ValueError(f"{name} must have contiguous rows at least {cols} elements apart, got strides {(ld, step)}")
     return t.data_ptr(), ld
+
+
+def _writable(t, name):
+    """Refuses a caller's tensor whose values autograd believes to know: the kernels write through its address."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise RuntimeError(f"{name} is part of an autograd graph, which would not see that it is written (RosaLinear is "
+                           "the differentiable form; under torch.no_grad() it may be written)")
 
 
 class Built:
@@ -185,7 +194,8 @@ def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h:
     """Y = base + s_i (X A_i^T) B_i^T with the adapter i of each token (tokens without one: base).
     base: the shared projection's output (None: zeros); out=base adds in place. scale: a float,
     or an fp32 tensor with one factor per adapter. return_h: also return X A_i^T (fp32
-    [tokens, rank]), which lora_grad takes."""
+    [tokens, rank]), which lora_grad takes. Autograd records nothing of it (RosaLinear is the form
+    that it differentiates): an out that belongs to an autograd graph is refused."""
     dev, dt, k, n_out, rank, n, s_ptr, s_all = _weights(X, A, B, plan, scale)
     if _elsewhere(dev.index):
         with torch.cuda.device(dev):
@@ -194,11 +204,14 @@ def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h:
     x, ldx = _rows(X, "X", T, k, dt, dev)
     b, ldb = _rows(base, "base", T, n_out, dt, dev) if base is not None else (0, n_out)
     lib = _L()
+    given = False
     if out is None:
         out = torch.empty((T, n_out), dtype=dt, device=dev)
         y, ldy = out.data_ptr(), n_out
     else:
         y, ldy = _rows(out, "out", T, n_out, dt, dev)
+        _writable(out, "out")
+        given = True
     h = torch.empty((T, rank), dtype=torch.float32, device=dev) if return_h else None
     stream = _raw_stream(dev.index)
     st = lib.spops_lora_add_block(_ADD_ARGS(
@@ -206,6 +219,8 @@ def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h:
         plan._on_stream(stream), stream, s_all, _DTYPE[dt], T, k, n_out, rank, n))
     if st:
         _check(st, "lora_add")
+    if given:  # (what autograd saved of it is no longer there)
+        increment_version(out)
     return (out, h) if return_h else out
 
 
@@ -222,7 +237,7 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
     shared projection's own input gradient goes in as dX_base (dX_out=dX_base: in place). h: the
     one lora_add returned for this X (None: formed here). need: which of the three to compute;
     the others come back as None. dA_out, dB_out: buffers for the weights' gradients (such as those of
-    a GradSet), overwritten."""
+    a GradSet), overwritten; as dX_out, they may not belong to an autograd graph."""
     dev, dt, k, n_out, rank, n, s_ptr, s_all = _weights(X, A, B, plan, scale)
     if _elsewhere(dev.index):
         with torch.cuda.device(dev):
@@ -250,6 +265,10 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
         dA = _like(dA_out, A, "dA_out") if dA_out is not None else torch.empty_like(A)
     if need[2]:
         dB = _like(dB_out, B, "dB_out") if dB_out is not None else torch.empty_like(B)
+    given = [(t, name) for t, name, use in ((dX_out, "dX_out", need[0]), (dA_out, "dA_out", need[1]),
+                                            (dB_out, "dB_out", need[2])) if use and t is not None]
+    for t, name in given:
+        _writable(t, name)
     stream = _raw_stream(dev.index)
     ws, ws_ptr, size = plan._grad_scratch(rank, stream)
     st = lib.spops_lora_grad_block(_GRAD_ARGS(
@@ -258,4 +277,6 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
         stream, s_all, _DTYPE[dt], T, k, n_out, rank, n))
     if st:
         _check(st, "lora_grad")
+    for t, _ in given:
+        increment_version(t)
     return dX, dA, dB
