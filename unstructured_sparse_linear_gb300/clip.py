@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _DTYPE, _L, _check, _req
 from .lora import Built, _elsewhere, _raw_stream
@@ -67,6 +68,9 @@ class GradSet(Built):
             super().__init__(table)
         self._chunks, self._in_place = chunks.value, in_place.value
         self._partial_ptr = self._ptr + at
+        # what autograd counts the writes of: views of one buffer share its count
+        owners = [o if o.is_inference() or o._base is None else o._base for o in self.out]
+        self._owners = list({id(o): o for o in owners}.values())
 
     def __len__(self):
         return self._n
@@ -108,4 +112,5 @@ def clip_grads(grads, max_norm: float) -> torch.Tensor:
                                s._partial_ptr, s._ws, stream)
     if st:
         _check(st, "clip_grads")
+    increment_version(s._owners)  # (a backward pass that saved one of the outputs raises)
     return norm
