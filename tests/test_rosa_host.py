@@ -74,7 +74,7 @@ def plain(monkeypatch):
     """The two low-rank calls as the kernels do them: on the values, outside autograd."""
     def lora_add(X, A, B, plan, base=None, scale=1.0, out=None, return_h=False):
         h = X.detach() @ A.detach()[0].t()
-        out.data.add_(h @ B.detach()[0].t(), alpha=scale)
+        out.data.add_(scale * (h @ B.detach()[0].t()))
         return out, h
 
     def lora_grad(dY, X, A, B, plan, scale=1.0, h=None, dX_base=None, dX_out=None, need=(True,) * 3, **kw):
@@ -129,3 +129,26 @@ def test_sparse_linear_refuses_second_derivatives(monkeypatch):
     for first in (dX, dV):
         with pytest.raises(RuntimeError, match="twice"):
             (Y.sum() + first.square().sum()).backward(retain_graph=True)
+
+
+def test_backward_uses_what_the_output_was_computed_with(plain):
+    X = torch.randn(5, 4, dtype=torch.float64)
+    dY = torch.randn(5, 6, dtype=torch.float64)
+    Y = plain(X, plan=object())
+    plain.scale = 3.0
+    (dB,) = torch.autograd.grad(Y, plain.B, dY)
+    assert torch.allclose(dB[0], 0.5 * dY.t() @ X @ plain.A.detach()[0].t())
+    plain.scale = torch.tensor([0.25], dtype=torch.float64)
+    Y = plain(X, plan=object())
+    plain.scale.fill_(2.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(Y, plain.B, dY)
+    Y = plain(X.requires_grad_(), plan=object())
+    W = plain.weight
+    plain.weight = torch.zeros_like(W)
+    want = dY @ (W + 2.0 * plain.B.detach()[0] @ plain.A.detach()[0])
+    assert torch.allclose(torch.autograd.grad(Y, X, dY)[0], want)
+    Y = plain(X, plan=object())
+    plain.weight.add_(1.0)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        torch.autograd.grad(Y, X, dY)

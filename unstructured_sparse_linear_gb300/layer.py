@@ -102,23 +102,24 @@ class SparseLinear(torch.nn.Module):
 class RosaLinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, X, values, A, B, layer, plan):
-        W = layer.merged(values)
-        Y = X @ W.t()
-        Y, h = lora_add(X, A, B, plan, base=Y, scale=layer.scale, out=Y, return_h=True)
-        ctx.save_for_backward(X, values, A, B, h)
-        ctx.layer, ctx.plan = layer, plan
+        weight, scale = layer.weight, layer.scale
+        Y = X @ layer.merged(values).t()
+        Y, h = lora_add(X, A, B, plan, base=Y, scale=scale, out=Y, return_h=True)
+        factors = scale if isinstance(scale, torch.Tensor) else None
+        ctx.save_for_backward(X, values, A, B, h, weight, factors)
+        ctx.layer, ctx.plan, ctx.scale = layer, plan, scale if factors is None else None
         return Y
 
     @staticmethod
     @first_derivatives_only
     def backward(ctx, dY):
-        X, values, A, B, h = ctx.saved_tensors
-        L = ctx.layer
+        X, values, A, B, h, weight, factors = ctx.saved_tensors
+        L, scale = ctx.layer, ctx.scale if factors is None else factors
         dY = dY.contiguous()
         need_x, need_v, need_a, need_b = ctx.needs_input_grad[:4]
         # The merged weight is formed again: less time than its memory is worth in a deep model.
-        base = dY @ L.merged(values) if need_x else None
-        dX, dA, dB = lora_grad(dY, X, A, B, ctx.plan, scale=L.scale, h=h, dX_base=base, dX_out=base,
+        base = dY @ L.merged(values, weight) if need_x else None
+        dX, dA, dB = lora_grad(dY, X, A, B, ctx.plan, scale=scale, h=h, dX_base=base, dX_out=base,
                                need=(need_x, need_a, need_b))
         dV = None
         if need_v and values is not None:
@@ -165,11 +166,12 @@ class RosaLinear(torch.nn.Module):
     def __getstate__(self):  # a copy or a pickle of the layer makes its own plans
         return {**super().__getstate__(), "_plans": {}, "_captured": {}}
 
-    def merged(self, values):
-        """W + S."""
+    def merged(self, values, weight=None):
+        """W + S (of another weight than the layer's, where one is given)."""
+        weight = self.weight if weight is None else weight
         if values is None:
-            return self.weight
-        return csr_add(values, self.row_offsets, self.row_idx, self.col_idx, self.weight)
+            return weight
+        return csr_add(values, self.row_offsets, self.row_idx, self.col_idx, weight)
 
     def _one_adapter_plan(self, tokens, device):
         capturing = torch.cuda.is_current_stream_capturing()
