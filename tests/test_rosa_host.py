@@ -1,5 +1,7 @@
 """RosaLinear's own bookkeeping, with stand-ins for the calls that need a GPU."""
+import copy
 import gc
+import pickle
 import weakref
 
 import pytest
@@ -117,6 +119,7 @@ def test_sparse_linear_refuses_second_derivatives(monkeypatch):
     class Layer:
         row_offsets = row_idx = row_idx_t = plan = plan_t = None
         col_idx, out_features, in_features = (6, 4), 6, 4
+        _follow_mask = _check_mask = staticmethod(lambda *mask: None)
 
         class transpose:
             row_offsets, col_idx = None, (4, 6)
@@ -152,3 +155,112 @@ def test_backward_uses_what_the_output_was_computed_with(plain):
     plain.weight.add_(1.0)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         torch.autograd.grad(Y, X, dY)
+
+
+class Rows:
+    """What is derived of a mask, as tensors that tell it from another one's."""
+    def __init__(self, row_offsets, col_idx):
+        self.buf = torch.cat([row_offsets.long(), col_idx.long()])
+
+    def of(self, layer):
+        return torch.equal(self.buf, torch.cat([layer.row_offsets.long(), layer.col_idx.long()]))
+
+
+class Turned:
+    def __init__(self, row_offsets, col_idx):
+        self.row_offsets, self.col_idx, self.perm = row_offsets + 100, col_idx + 100, col_idx + 200
+
+
+@pytest.fixture
+def masks(monkeypatch, plain):
+    used = {"spmm": [], "sddmm": [], "csr_add": []}
+
+    def note(name, result):
+        def call(*a, plan=None, **kw):
+            used[name].append((a, plan))
+            return result(*a)
+        return call
+
+    monkeypatch.setattr(layer_module, "sort_rows", lambda ro, nnz=None, index_dtype=None: (ro[:-1] * 7).clone())
+    monkeypatch.setattr(layer_module, "plan_build", lambda ro, row_idx, col, n: Rows(ro, col))
+    monkeypatch.setattr(layer_module, "csr_transpose", lambda v, ro, col, n: Turned(ro, col))
+    monkeypatch.setattr(layer_module, "permute_values", lambda v, t: v)
+    monkeypatch.setattr(layer_module, "csr_add", note("csr_add", lambda v, ro, ri, ci, W: W.clone()))
+    monkeypatch.setattr(layer_module, "spmm", note("spmm", lambda v, ro, ri, ci, X, m: X.new_zeros(m, X.shape[1])))
+    monkeypatch.setattr(layer_module, "sddmm", note("sddmm", lambda ro, ri, ci, a, b: a.new_zeros(ci.numel())))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: used.get("capturing", False))
+    return used
+
+
+MASK_A = torch.tensor([0, 1, 2, 2, 3, 3, 4], dtype=torch.int32), torch.tensor([0, 3, 1, 2], dtype=torch.int16)
+MASK_B = torch.tensor([0, 0, 0, 3, 3, 4, 4], dtype=torch.int32), torch.tensor([0, 1, 2, 3], dtype=torch.int16)
+
+
+def masked(kind, mask):
+    ro, col = (t.clone() for t in mask)
+    values = torch.zeros(4, dtype=torch.float64)
+    if kind == "sparse":
+        return sp.SparseLinear(ro, col, values, 4)
+    return sp.RosaLinear(torch.zeros(6, 4, dtype=torch.float64), 2, row_offsets=ro, col_idx=col, values=values)
+
+
+def step(layer):
+    kind = isinstance(layer, sp.SparseLinear)
+    X = torch.zeros(*((4, 5) if kind else (5, 4)), dtype=torch.float64, requires_grad=True)
+    return layer(X) if kind else layer(X, plan=object())
+
+
+@pytest.mark.parametrize("kind", ["sparse", "rosa"])
+def test_what_is_derived_of_the_mask_follows_it(masks, kind):
+    layer = masked(kind, MASK_A)
+    step(layer).sum().backward()
+    plan, row_idx = layer.plan, layer.row_idx
+    assert plan.of(layer) and masks["sddmm"][-1][1] is plan
+    layer.load_state_dict(masked(kind, MASK_B).state_dict())
+    assert torch.equal(layer.col_idx, MASK_B[1])
+    step(layer).sum().backward()
+    a, used = masks["sddmm"][-1]
+    assert used.of(layer) and torch.equal(a[1], MASK_B[0][:-1] * 7)
+    assert used is plan and a[1] is row_idx  # (written where captured graphs read them)
+    if kind == "rosa":
+        assert torch.equal(masks["csr_add"][-1][0][2], MASK_B[0][:-1] * 7)
+    else:
+        assert torch.equal(layer.transpose.perm, MASK_B[1] + 200) and layer.plan_t.buf[0] == 100
+        assert masks["spmm"][-2][1].of(layer)
+    # buffers that another layer shares, replaced ones, and moved ones
+    layer.col_idx.copy_(MASK_A[1])
+    layer.row_offsets.copy_(MASK_A[0])
+    step(layer)
+    assert layer.plan.of(layer)
+    other = masked(kind, MASK_B)
+    layer.load_state_dict({k: v.clone() for k, v in other.state_dict().items()}, assign=True)
+    step(layer)
+    assert layer.plan.of(layer)
+
+
+@pytest.mark.parametrize("kind", ["sparse", "rosa"])
+def test_a_mask_that_changes_between_the_passes_or_in_a_capture(masks, kind):
+    layer = masked(kind, MASK_A)
+    Y = step(layer)
+    layer.col_idx.copy_(MASK_B[1])
+    layer.row_offsets.copy_(MASK_B[0])
+    with pytest.raises(RuntimeError, match="mask of this layer has changed"):
+        Y.sum().backward()
+    step(layer).sum().backward()
+    layer.row_offsets.copy_(MASK_A[0])
+    masks["capturing"] = True
+    with pytest.raises(RuntimeError, match="before it is captured"):
+        step(layer)
+    masks["capturing"] = False
+    step(layer)
+    masks["capturing"] = True
+    step(layer)
+
+
+@pytest.mark.parametrize("kind", ["sparse", "rosa"])
+def test_copies_derive_their_own(masks, kind):
+    layer = masked(kind, MASK_A)
+    for twin in (copy.deepcopy(layer), pickle.loads(pickle.dumps(layer))):
+        step(twin)
+        assert twin.plan is not layer.plan and twin.plan.of(twin)
+        assert layer.plan.of(layer)

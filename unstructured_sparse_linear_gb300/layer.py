@@ -51,9 +51,64 @@ def first_derivatives_only(backward):
     return wrapped
 
 
+def _tensors(x):
+    """The tensors of one that a layer derives from its mask: a tensor, a Plan or a Transpose."""
+    if isinstance(x, torch.Tensor):
+        return [x]
+    return [x.buf] if hasattr(x, "buf") else [x.row_offsets, x.col_idx, x.perm]
+
+
+class _MaskedLayer(torch.nn.Module):
+    """A layer on a CSR mask, its buffers row_offsets and col_idx. What the kernels need of the mask beside it
+    is derived from them (``_derive``, a dict of attributes), and derived again once the buffers hold another mask or
+    have moved, as after load_state_dict or to: a plan leads the kernels to rows and columns, so one of another
+    mask would lead them out of range."""
+
+    _mask = None  # (row_offsets, its version, col_idx, its version) that the derived ones are of
+
+    def _derive(self) -> dict:
+        raise NotImplementedError
+
+    def _follow_mask(self):
+        """Brings the derived ones up to date; returns what tells this mask from others."""
+        now = []
+        for t in (self.row_offsets, self.col_idx):
+            now += [t, None if t.is_inference() else t._version]
+        then = self._mask
+        if then is not None and now[0] is then[0] and now[1] == then[1] and now[2] is then[2] and now[3] == then[3]:
+            return then
+        if then is not None and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the mask of this layer has changed: call the layer once before it is captured in a graph")
+        for name, new in self._derive().items():
+            old = self.__dict__.get(name)
+            if old is not None and all(o.device == n.device and o.shape == n.shape
+                                       for o, n in zip(_tensors(old), _tensors(new))):
+                for o, n in zip(_tensors(old), _tensors(new)):  # (graphs that were captured read them where they are)
+                    o.copy_(n)
+            else:
+                setattr(self, name, new)
+        self._mask = tuple(now)
+        return self._mask
+
+    def _check_mask(self, then):
+        """For a backward pass, with what _follow_mask returned in the forward one."""
+        if then is not None and self._follow_mask() is not then:
+            raise RuntimeError("the mask of this layer has changed since the forward pass")
+
+    def __getstate__(self):  # copies and pickles derive their own
+        made = set(self._derived_names) | {"_mask"}
+        return {k: v for k, v in super().__getstate__().items() if k not in made}
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        if "row_offsets" in self._buffers and self.row_offsets.is_cuda:
+            self._follow_mask()
+
+
 class SparseLinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, values, Xt, layer):
+        ctx.mask = layer._follow_mask()
         Yt = spmm(values, layer.row_offsets, layer.row_idx, layer.col_idx, Xt, layer.out_features, plan=layer.plan)
         ctx.save_for_backward(values, Xt)
         ctx.layer = layer
@@ -64,6 +119,7 @@ class SparseLinearFunction(torch.autograd.Function):
     def backward(ctx, dYt):
         values, Xt = ctx.saved_tensors
         L = ctx.layer
+        L._check_mask(ctx.mask)
         dYt = dYt.contiguous()
         d_values = d_Xt = None
         if ctx.needs_input_grad[0]:
@@ -75,7 +131,7 @@ class SparseLinearFunction(torch.autograd.Function):
         return d_values, d_Xt, None
 
 
-class SparseLinear(torch.nn.Module):
+class SparseLinear(_MaskedLayer):
     """Y^T = W X^T with W (out_features x in_features) stored as the values of a fixed CSR
     mask (row_offsets int32, col_idx int16/int32); inputs and outputs are feature-major
     (features x tokens), fp16 or bf16 (fp32 runs the general kernels). Gradients are first
@@ -88,12 +144,17 @@ class SparseLinear(torch.nn.Module):
         self.register_buffer("row_offsets", row_offsets)
         self.register_buffer("col_idx", col_idx)
         self.values = torch.nn.Parameter(values)
-        self.row_idx = sort_rows(row_offsets, nnz=col_idx.numel(), index_dtype=col_idx.dtype)
-        self.plan = plan_build(row_offsets, self.row_idx, col_idx, self.in_features)
-        self.transpose = csr_transpose(None, row_offsets, col_idx, self.in_features)
-        self.row_idx_t = sort_rows(self.transpose.row_offsets, nnz=col_idx.numel(), index_dtype=col_idx.dtype)
-        self.plan_t = plan_build(self.transpose.row_offsets, self.row_idx_t, self.transpose.col_idx,
-                                 self.out_features)
+        self._follow_mask()
+
+    _derived_names = ("row_idx", "plan", "transpose", "row_idx_t", "plan_t")
+
+    def _derive(self):
+        ro, col = self.row_offsets, self.col_idx
+        row_idx = sort_rows(ro, nnz=col.numel(), index_dtype=col.dtype)
+        t = csr_transpose(None, ro, col, self.in_features)
+        row_idx_t = sort_rows(t.row_offsets, nnz=col.numel(), index_dtype=col.dtype)
+        return dict(row_idx=row_idx, plan=plan_build(ro, row_idx, col, self.in_features), transpose=t,
+                    row_idx_t=row_idx_t, plan_t=plan_build(t.row_offsets, row_idx_t, t.col_idx, self.out_features))
 
     def forward(self, Xt: torch.Tensor) -> torch.Tensor:
         return SparseLinearFunction.apply(self.values, Xt.contiguous(), self)
@@ -104,6 +165,7 @@ class RosaLinearFunction(torch.autograd.Function):
     def forward(ctx, X, values, A, B, layer, plan):
         weight, scale = layer.weight, layer.scale
         Y = X @ layer.merged(values).t()
+        ctx.mask = layer._mask if values is not None else None
         Y, h = lora_add(X, A, B, plan, base=Y, scale=scale, out=Y, return_h=True)
         factors = scale if isinstance(scale, torch.Tensor) else None
         ctx.save_for_backward(X, values, A, B, h, weight, factors)
@@ -115,6 +177,7 @@ class RosaLinearFunction(torch.autograd.Function):
     def backward(ctx, dY):
         X, values, A, B, h, weight, factors = ctx.saved_tensors
         L, scale = ctx.layer, ctx.scale if factors is None else factors
+        L._check_mask(ctx.mask)
         dY = dY.contiguous()
         need_x, need_v, need_a, need_b = ctx.needs_input_grad[:4]
         # The merged weight is formed again: less time than its memory is worth in a deep model.
@@ -127,7 +190,7 @@ class RosaLinearFunction(torch.autograd.Function):
         return dX, dV, dA, dB, None, None
 
 
-class RosaLinear(torch.nn.Module):
+class RosaLinear(_MaskedLayer):
     """A frozen projection with a RoSA adapter, a sparse and a low-rank update (spops README,
     "Sparse Operations (spops)": RoSA's sparse part is added to the weight with csr_add, and its
     gradient is an SDDMM on the mask):
@@ -158,10 +221,15 @@ class RosaLinear(torch.nn.Module):
             self.register_buffer("row_offsets", row_offsets)
             self.register_buffer("col_idx", col_idx)
             self.values = torch.nn.Parameter(values)
-            self.row_idx = sort_rows(row_offsets, nnz=col_idx.numel(), index_dtype=col_idx.dtype)
-            self.plan = plan_build(row_offsets, self.row_idx, col_idx, self.in_features)
+            self._follow_mask()
         self._plans = {}  # by number of tokens: every token uses adapter 0
         self._captured = {}  # those of them that a graph's replays read, kept as long as the layer
+
+    _derived_names = ("row_idx", "plan")
+
+    def _derive(self):
+        row_idx = sort_rows(self.row_offsets, nnz=self.col_idx.numel(), index_dtype=self.col_idx.dtype)
+        return dict(row_idx=row_idx, plan=plan_build(self.row_offsets, row_idx, self.col_idx, self.in_features))
 
     def __getstate__(self):  # a copy or a pickle of the layer makes its own plans
         return {**super().__getstate__(), "_plans": {}, "_captured": {}}
@@ -171,6 +239,7 @@ class RosaLinear(torch.nn.Module):
         weight = self.weight if weight is None else weight
         if values is None:
             return weight
+        self._follow_mask()
         return csr_add(values, self.row_offsets, self.row_idx, self.col_idx, weight)
 
     def _one_adapter_plan(self, tokens, device):
