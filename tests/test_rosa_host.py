@@ -264,3 +264,23 @@ def test_copies_derive_their_own(masks, kind):
         step(twin)
         assert twin.plan is not layer.plan and twin.plan.of(twin)
         assert layer.plan.of(layer)
+
+
+def test_plans_of_a_length_belong_to_a_device(fake, monkeypatch):
+    """A layer that moved makes plans where it is; captured ones of both places stay."""
+    layer = fake["layer"]
+    here, there = torch.device("cuda", 0), torch.device("cuda", 1)
+
+    def on(device, capturing=False):
+        fake["capturing"] = capturing
+        plan = layer._one_adapter_plan(5, device)
+        fake["capturing"] = False
+        return plan
+
+    first = on(here)
+    assert on(here, capturing=True) is first
+    second = on(there)
+    assert (first.device, second.device) == (here, there)
+    assert on(there, capturing=True) is second
+    layer._plans.clear()
+    assert on(here) is first and on(there) is second

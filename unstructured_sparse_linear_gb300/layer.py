@@ -244,8 +244,8 @@ class RosaLinear(_MaskedLayer):
 
     def _one_adapter_plan(self, tokens, device):
         capturing = torch.cuda.is_current_stream_capturing()
-        plan = self._plans.get(tokens) or self._captured.get(tokens)
-        if plan is None:
+        plan = self._captured.get((tokens, device)) or self._plans.get(tokens)
+        if plan is None or plan.device != device:  # (the layer may have moved)
             plan = lora_plan(None, self.n_adapters, tokens=tokens, device=device)
             if capturing:  # (written by the graph's replays: not for calls outside it)
                 return plan
@@ -253,7 +253,7 @@ class RosaLinear(_MaskedLayer):
                 self._plans.clear()
             self._plans[tokens] = plan
         if capturing:  # the graph holds the plan's address and nothing else holds the plan
-            self._captured[tokens] = plan
+            self._captured[tokens, device] = plan
         return plan
 
     def forward(self, X: torch.Tensor, adapter_ids: torch.Tensor | None = None, plan=None) -> torch.Tensor:
