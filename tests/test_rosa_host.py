@@ -284,3 +284,31 @@ def test_plans_of_a_length_belong_to_a_device(fake, monkeypatch):
     assert on(there, capturing=True) is second
     layer._plans.clear()
     assert on(here) is first and on(there) is second
+
+
+def test_factors_per_adapter_are_state():
+    W, factors = torch.randn(6, 4), torch.tensor([0.5, 1.7, 0.3])
+    layer = sp.RosaLinear(W.clone(), 2, n_adapters=3, scale=factors.clone())
+    assert torch.equal(layer.scale, factors)
+    other = sp.RosaLinear(W.clone(), 2, n_adapters=3, scale=torch.ones(3))
+    other.load_state_dict(layer.state_dict())
+    assert torch.equal(other.scale, factors) and torch.equal(other.A, layer.A)
+    for narrow in (torch.float16, torch.bfloat16):  # the factors stay in 32 bits, to the last of them
+        twin = copy.deepcopy(layer).to(narrow)
+        assert twin.A.dtype == narrow and twin.scale.dtype == torch.float32 and torch.equal(twin.scale, factors)
+    assert copy.deepcopy(layer).to("meta").scale.device.type == "meta"
+    twin = pickle.loads(pickle.dumps(layer))
+    assert torch.equal(twin.scale, factors)
+    with pytest.raises(RuntimeError, match="size mismatch"):
+        sp.RosaLinear(W.clone(), 2, n_adapters=2, scale=torch.ones(2)).load_state_dict(layer.state_dict())
+
+
+def test_a_factor_may_be_a_number_or_a_tensor_at_any_time():
+    layer = sp.RosaLinear(torch.randn(6, 4), 2, n_adapters=3, scale=2.0)
+    assert layer.scale == 2.0 and set(layer.state_dict()) == {"weight", "A", "B"}
+    layer.scale = torch.ones(3)
+    assert "factors" in layer.state_dict() and torch.equal(layer.scale, torch.ones(3))
+    layer.scale = 0.5
+    assert layer.scale == 0.5 and set(layer.state_dict()) == {"weight", "A", "B"}
+    layer.scale = torch.ones(3)
+    assert layer.to("meta").to_empty(device="cpu").scale.shape == (3,)

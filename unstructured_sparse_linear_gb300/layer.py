@@ -200,7 +200,7 @@ class RosaLinear(_MaskedLayer):
     weight: W [out, in], fp16 or bf16 (fp32 runs the general kernels), not trained. row_offsets,
     col_idx, values: S on a fixed CSR mask, shared by all tokens (None: no sparse part). n_adapters
     low-rank adapters of one rank, their factor `scale` a number or an fp32 tensor with one per
-    adapter; A starts at random and B at zero, so that the adapters start as no change. X is
+    adapter (then part of the layer's state); A starts at random and B at zero, so that the adapters start as no change. X is
     token-major [..., in]; adapter_ids (int32, one per token) or a plan of them choose each token's
     adapter, by default adapter 0 for all. Gradients are first derivatives: differentiating them again
     raises."""
@@ -209,7 +209,9 @@ class RosaLinear(_MaskedLayer):
                  values=None):
         super().__init__()
         self.out_features, self.in_features = weight.shape
-        self.n_adapters, self.scale = int(n_adapters), scale
+        self.n_adapters = int(n_adapters)
+        self.register_buffer("factors", None)
+        self.scale = scale
         self.register_buffer("weight", weight)
         dev, dt = weight.device, weight.dtype
         self.A = torch.nn.Parameter(torch.randn(self.n_adapters, rank, self.in_features, device=dev, dtype=torch.float32)
@@ -224,6 +226,24 @@ class RosaLinear(_MaskedLayer):
             self._follow_mask()
         self._plans = {}  # by number of tokens: every token uses adapter 0
         self._captured = {}  # those of them that a graph's replays read, kept as long as the layer
+
+    @property
+    def scale(self):
+        """The adapters' factors: a number, or the fp32 tensor of one per adapter, which is part of the state
+        (``factors``) and moves with the layer."""
+        return self._factor if self.factors is None else self.factors
+
+    @scale.setter
+    def scale(self, value):
+        tensor = isinstance(value, torch.Tensor)
+        self.factors, self._factor = (value, None) if tensor else (None, value)
+
+    def _apply(self, *args, **kwargs):
+        factors = self.factors
+        super()._apply(*args, **kwargs)
+        if factors is not None and self.factors.dtype != factors.dtype:  # 32 bits, whatever type the layer is brought to
+            self.factors = factors.to(self.factors.device)
+        return self
 
     _derived_names = ("row_idx", "plan")
 
