@@ -684,7 +684,8 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
                 float m = 0.f, up = 1.f, down = 1.f;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[e] *= s;
+                    // (columns beyond the rank are U times zeros: NaN where U holds an infinity)
+                    x[e] = c8 * 8 + e < g.rank ? x[e] * s : 0.f;
                     m = fmaxf(m, fabsf(x[e]));
                 }
                 if (kF16) {  // the row's pieces lie in kG neighbouring lanes
