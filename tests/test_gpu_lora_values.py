@@ -47,3 +47,22 @@ def test_an_infinity_in_a_row_gives_the_formulas_infinity(fmt, tokens, rank):
     assert (Y[hit] == float("inf")).all() and (h[hit] == float("inf")).all() and (dX[hit] == float("inf")).all()
     want = torch.full((rank, K), float("inf"), device=DEV) * d["X"][hit].float()
     assert torch.equal(dA[0].float(), want)
+
+
+@pytest.mark.parametrize("fmt", ["f16", "bf16"])
+@pytest.mark.parametrize("rank", [16, 64])
+def test_scattered_tokens_give_the_bits_of_tokens_in_runs(fmt, rank):
+    """Rows that come by fours and leave by ordinary stores, through many reuses of every stage of the ring."""
+    T, k, n, adapters = 1900, 1032, 2056, 5
+    d = operands(fmt, T, rank, seed=2, k=k, n=n)
+    A, B = (d[x] * torch.arange(1, adapters + 1, device=DEV, dtype=DTYPES[fmt])[:, None, None] for x in "AB")
+    ids = torch.randint(-1, adapters, (T,), dtype=torch.int32, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    runs = torch.argsort(torch.where(ids < 0, adapters, ids), stable=True)
+    plan, plan_runs = sp.lora_plan(ids, adapters), sp.lora_plan(ids[runs].contiguous(), adapters)
+    Y = sp.lora_add(d["X"][runs], A, B, plan_runs, base=d["base"][runs])
+    dX = sp.lora_grad(d["dY"][runs], d["X"][runs], A, B, plan_runs, dX_base=d["dX_base"][runs])
+    for _ in range(3):
+        got = sp.lora_add(d["X"], A, B, plan, base=d["base"])
+        grads = sp.lora_grad(d["dY"], d["X"], A, B, plan, dX_base=d["dX_base"])
+        assert torch.equal(got[runs], Y) and torch.equal(grads[0][runs], dX[0])
+        assert torch.equal(grads[1], dX[1]) and torch.equal(grads[2], dX[2])

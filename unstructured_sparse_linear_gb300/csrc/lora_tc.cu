@@ -770,6 +770,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
                             *reinterpret_cast<uint4*>(static_cast<T*>(g.O) + (int64_t)to * g.ldo + n0 + c * 8) =
                                 ld_shared_v4(st + tc::sw128_off(r, c));
                     }
+                    fence_proxy_async_smem();  // O was written here by threads, what comes next is by TMA
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sh.empty[sl]));
                 }
