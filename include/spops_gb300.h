@@ -306,8 +306,10 @@ SPOPS_API int spops_masked_adam_csr(float* param, float* exp_avg, float* exp_avg
  * output is rounded once. A token's result depends on no other token and on no other
  * adapter's weights (infinities and NaN stay where they are). Deterministic. */
 #define SPOPS_LORA_MAX_RANK 128
+/* The most tokens of a batch, and the most adapters: the kernels count both in 32 bits and step past the last one. */
+#define SPOPS_LORA_MAX_COUNT 0x7fff0000
 
-/* Bytes of the plan of a batch. */
+/* Bytes of the plan of a batch (0 for sizes that are refused). */
 SPOPS_API size_t spops_lora_plan_size(int32_t tokens, int32_t n_adapters);
 
 /* The plan of a batch: its tokens sorted by adapter, for every projection of every layer that

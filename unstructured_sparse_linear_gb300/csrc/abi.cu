@@ -279,6 +279,9 @@ int check_lora(const void* A, const void* B, const float* scale, float scale_all
     if (tokens < 0 || in_features < 1 || out_features < 1 || rank < 1 || n_adapters < 1)
         return fail(SPOPS_ERR_INVALID_ARG, "need tokens >= 0 and in, out, rank, n_adapters >= 1 (got %d, %d, %d, %d, %d)",
                     tokens, in_features, out_features, rank, n_adapters);
+    if (tokens > SPOPS_LORA_MAX_COUNT || n_adapters > SPOPS_LORA_MAX_COUNT)
+        return fail(SPOPS_ERR_UNSUPPORTED, "%d tokens and %d adapters: more than %d", tokens, n_adapters,
+                    SPOPS_LORA_MAX_COUNT);
     if (rank > SPOPS_LORA_MAX_RANK)
         return fail(SPOPS_ERR_UNSUPPORTED, "rank %d is above the largest supported, %d", rank, SPOPS_LORA_MAX_RANK);
     if (!A || !B) return fail(SPOPS_ERR_INVALID_ARG, "A or B is NULL");
@@ -563,13 +566,18 @@ int spops_get_device_error(void* stream, int32_t* code_out) {
 /* ---------------------------------------------------------------- low-rank adapters */
 
 size_t spops_lora_plan_size(int32_t tokens, int32_t n_adapters) {
-    return tokens < 0 || n_adapters < 1 ? 0 : lora_plan_bytes(tokens, n_adapters);
+    return tokens < 0 || n_adapters < 1 || tokens > SPOPS_LORA_MAX_COUNT || n_adapters > SPOPS_LORA_MAX_COUNT
+               ? 0
+               : lora_plan_bytes(tokens, n_adapters);
 }
 
 int spops_lora_plan_build(const int32_t* adapter_ids, int32_t tokens, int32_t n_adapters, void* plan, size_t plan_size,
                           void* stream) {
     if (tokens < 0 || n_adapters < 1)
         return fail(SPOPS_ERR_INVALID_ARG, "need tokens >= 0 and n_adapters >= 1 (got %d, %d)", tokens, n_adapters);
+    if (tokens > SPOPS_LORA_MAX_COUNT || n_adapters > SPOPS_LORA_MAX_COUNT)
+        return fail(SPOPS_ERR_UNSUPPORTED, "%d tokens and %d adapters: more than %d", tokens, n_adapters,
+                    SPOPS_LORA_MAX_COUNT);
     if (adapter_ids && !aligned(adapter_ids, 4)) return fail(SPOPS_ERR_INVALID_ARG, "adapter_ids is not 4-byte aligned");
     if (tokens == 0) return ok();
     if (!plan || !aligned(plan, 16) || plan_size < spops_lora_plan_size(tokens, n_adapters))

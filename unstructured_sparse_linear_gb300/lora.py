@@ -26,6 +26,8 @@ from . import _DTYPE, _L, _check, _req
 __all__ = ["LoraPlan", "lora_plan", "lora_add", "lora_grad"]
 
 
+_MAX_COUNT = 0x7fff0000  # SPOPS_LORA_MAX_COUNT
+
 # spops_lora_add_args and spops_lora_grad_args
 _ADD_ARGS = struct.Struct("12qf6i").pack
 _GRAD_ARGS = struct.Struct("18qf6i").pack
@@ -138,8 +140,8 @@ def lora_plan(adapter_ids: torch.Tensor | None, n_adapters: int, tokens: int | N
             raise ValueError(f"adapter_ids must be a vector with one id per token, got {tuple(adapter_ids.shape)}")
         tokens, dev, ids = adapter_ids.numel(), adapter_ids.device, adapter_ids.data_ptr()
     tokens, n_adapters = int(tokens), int(n_adapters)
-    if not (0 <= tokens < 2 ** 31 and 1 <= n_adapters < 2 ** 31 - 1):
-        raise ValueError(f"need tokens >= 0 and n_adapters >= 1 of 32 bits, got {tokens}, {n_adapters}")
+    if not (0 <= tokens <= _MAX_COUNT and 1 <= n_adapters <= _MAX_COUNT):
+        raise ValueError(f"need tokens >= 0 and n_adapters >= 1, at most {_MAX_COUNT} of each, got {tokens}, {n_adapters}")
     lib = _L()
     size = lib.spops_lora_plan_size(tokens, n_adapters)
     with torch.cuda.device(dev):
