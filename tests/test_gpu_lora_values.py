@@ -66,3 +66,76 @@ def test_scattered_tokens_give_the_bits_of_tokens_in_runs(fmt, rank):
         grads = sp.lora_grad(d["dY"], d["X"], A, B, plan, dX_base=d["dX_base"])
         assert torch.equal(got[runs], Y) and torch.equal(grads[0][runs], dX[0])
         assert torch.equal(grads[1], dX[1]) and torch.equal(grads[2], dX[2])
+
+
+# What the two fp16 parts of P hold: 22 bits, or what is below 2^-50 of the largest value of its row (second
+# product) or of its rank's column (weight gradients).
+FP16_BITS, FP16_FLOOR = 2.0 ** -22, 2.0 ** -50
+
+
+def spread(rng, exps, *shape):
+    """fp16 values of four bits each, every rank j of about 2^exps[j]; shape[-2] or shape[-1] is the rank."""
+    x = (1 + rng.integers(0, 8, shape) / 8) * rng.choice([-1.0, 1.0], shape)
+    at = 1 if shape[1] == len(exps) else 2
+    return x * (2.0 ** np.asarray(exps)).reshape([-1 if i == at else 1 for i in range(3)])
+
+
+def assert_within(got, want, err, fmt, what):
+    g = as_f64(got)
+    bound = err + 0.5 * ulp(np.abs(want) + err, fmt)
+    diff = np.abs(g - want)
+    assert np.isfinite(g).all() and (diff <= bound).all(), (what, float((diff / bound)[np.isfinite(diff)].max()))
+
+
+@pytest.mark.parametrize("tokens,rank", [(40, 16), (700, 16), (2500, 24), (700, 40), (400, 100)])
+def test_fp16_ranks_of_very_different_magnitudes(tokens, rank):
+    """A's rows fall from 2^14 to 2^-20 while B's columns rise by as much: every rank counts in Y and in dX."""
+    rng = np.random.default_rng([11, tokens, rank])
+    exps = np.round(np.linspace(14, -20, rank))
+    d = operands("f16", tokens, rank, seed=11)
+    A, B = (torch.from_numpy(spread(rng, e, *s)).half().to(DEV) for e, s in ((exps, (1, rank, K)), (-6 - exps, (1, N, rank))))
+    a, b = as_f64(A)[0], as_f64(B)[0]
+    assert (np.abs(a) > 0).all() and (np.abs(b) > 0).all()
+
+    def want(U, W1, W2, base):
+        P, terms = U @ W1, np.abs(U) @ np.abs(W1)
+        e = ACC_UNIT * U.shape[1] * terms + np.maximum(FP16_BITS * np.abs(P), FP16_FLOOR * np.abs(P).max(1, keepdims=True))
+        return base + P @ W2, e @ np.abs(W2) + ACC_UNIT * (rank + 4) * (np.abs(base) + np.abs(P) @ np.abs(W2))
+
+    Y = sp.lora_add(d["X"], A, B, d["plan"], base=d["base"])
+    assert_within(Y, *want(as_f64(d["X"]), a.T, b.T, as_f64(d["base"])), "f16", "Y")
+    dY = d["dY"] * 0.0625
+    dX = sp.lora_grad(dY, d["X"], A, B, d["plan"], dX_base=d["dX_base"], need=(True, False, False))[0]
+    assert_within(dX, *want(as_f64(dY), b, a, as_f64(d["dX_base"])), "f16", "dX")
+
+
+@pytest.mark.parametrize("tokens,rank", [(40, 16), (700, 16), (2500, 24), (700, 40), (400, 100)])
+def test_fp16_weight_gradients_beside_large_ranks_and_tokens(tokens, rank):
+    """Ranks 2^16 apart and one token 2^12 above the others that meets zeros: the small ones keep their bits."""
+    rng = np.random.default_rng([12, tokens, rank])
+    exps = np.round(np.linspace(8, -8, rank))
+    d = operands("f16", tokens, rank, seed=12)
+    X, dY, hit = d["X"].clone(), d["dY"] * 0.0625, tokens // 3
+
+    def weight_gradient(U, W, V):
+        """sum over t of (U W)[t, j] V[t, x] and its bound."""
+        P, terms = U @ W, np.abs(U) @ np.abs(W)
+        e = ACC_UNIT * U.shape[1] * terms + np.maximum(FP16_BITS * np.abs(P), FP16_FLOOR * np.abs(P).max(0, keepdims=True))
+        return P.T @ V, (e + ACC_UNIT * (tokens + 4) * np.abs(P)).T @ np.abs(V)
+
+    # dB: the outlier is a row of X
+    A = torch.from_numpy(spread(rng, exps, 1, rank, K)).half().to(DEV)
+    X1, dY1 = X.clone(), dY.clone()
+    X1[hit] *= 4096
+    dY1[hit] = 0
+    dB = sp.lora_grad(dY1, X1, A, d["B"], d["plan"], need=(False, False, True))[2]
+    G, e = weight_gradient(as_f64(X1), as_f64(A)[0].T, as_f64(dY1))
+    assert_within(dB[0], G.T, e.T, "f16", "dB")
+    # dA: of dY
+    B = torch.from_numpy(spread(rng, exps, 1, N, rank)).half().to(DEV)
+    X2, dY2 = X.clone(), dY.clone()
+    dY2[hit] *= 4096
+    X2[hit] = 0
+    dA = sp.lora_grad(dY2, X2, d["A"], B, d["plan"], need=(False, True, False))[1]
+    G, e = weight_gradient(as_f64(dY2), as_f64(B)[0], as_f64(X2))
+    assert_within(dA[0], G, e, "f16", "dA")

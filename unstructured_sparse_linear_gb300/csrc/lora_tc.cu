@@ -6,10 +6,11 @@
 //
 // Precision. P stays in 32 bits where it is kept (TMEM, shared memory, global). As an operand
 // of the second product it is the sum of two 16-bit parts, hi = round(P) and lo = round(P - hi),
-// multiplied one after the other into the same fp32 accumulators: 16 bits or more of P take part
-// (a single bf16 part would add an error as large as the output's own rounding). For fp16, whose
-// range P = U W1 leaves easily (small gradients, large activations), a row (or a CTA's rows of
-// a weight gradient) is first scaled by a power of two, which is taken back in fp32.
+// whose products have the same fp32 sums: 16 bits or more of P take part (a single bf16 part would
+// add an error as large as the output's own rounding). For fp16, whose range P = U W1 leaves easily
+// (small gradients, large activations), a row (for a weight gradient: a rank's column among a CTA's tokens)
+// is first scaled by a power of two, and lo is kept 2^11 times larger; both are taken back in fp32. So 22 bits
+// of P take part, 16 of values of 2^-34 of the row's or column's largest, and whatever lies above 2^-50 of it.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -148,25 +149,30 @@ constexpr uint64_t kDrainNs = 100000000ull;  // after a failed wait: for copies 
 // 2^x for the exponent field of a normal fp32 number.
 __device__ __forceinline__ float exp2i(int x) { return __uint_as_float((uint32_t)(x + 127) << 23); }
 
-// The power of two that brings m (the largest magnitude) to [2^10, 2^11), and its inverse; 1
+// The power of two that brings m (the largest magnitude) to [2^14, 2^15), and its inverse; 1
 // for zero, infinite and NaN m. Both factors are normal numbers.
 __device__ __forceinline__ void pow2_scale(float m, float& up, float& down) {
     up = down = 1.f;
     if (m > 0.f && m <= 3.402823466e38f) {
         const int e = max(-110, (int)((__float_as_uint(m) >> 23) & 255u) - 127);
-        up = exp2i(10 - e);
-        down = exp2i(e - 10);
+        up = exp2i(14 - e);
+        down = exp2i(e - 14);
     }
 }
 
-// Eight values as eight hi and eight lo parts.
+// The lo part of an fp16 pair is kept times 2^kLoShift: hi is at most 2^15 and drops at most half of one of its
+// units, 2^3, so lo stays below 2^15 as well, and what it cannot hold is below 2^-36 (2^-50 of the largest).
+constexpr int kLoShift = 11;
+
+// Eight values as eight hi and eight lo parts (fp16: of values that pow2_scale has scaled).
 template <typename T>
 __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
+    constexpr float kUp = std::is_same<T, __half>::value ? (float)(1 << kLoShift) : 1.f;
     hi = Elt<T>::pack(x);
     float h[8], l[8];
     Elt<T>::unpack(hi, h);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l[i] = fabsf(h[i]) <= 3.402823466e38f ? x[i] - h[i] : 0.f;  // no inf - inf
+    for (int i = 0; i < 8; ++i) l[i] = fabsf(h[i]) <= 3.402823466e38f ? (x[i] - h[i]) * kUp : 0.f;  // no inf - inf
     lo = Elt<T>::pack(l);
 }
 
@@ -562,15 +568,18 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
                     if (!ok) break;
                     if (g.hand) fence_proxy_async_smem();
                     tc::fence_after_sync();
+                    // fp16: the lo parts' products first; what they add up to is divided by 2^kLoShift as the first of hi's
+                    // is added.
                     constexpr int kSteps = RP / 16;
 #pragma unroll
-                    for (int i = 0; i < 2 * kSteps; ++i) {
-                        const int w = i % kSteps;
+                    for (int n = 0; n < 2 * kSteps; ++n) {
+                        const int i = kF16 ? (n + kSteps) % (2 * kSteps) : n, w = i % kSteps;
                         const uint64_t ad = tc::smem_desc_sw128(hbase + (i / 4) * 16384 + (i % 4) * 32, 16, 1024);
                         const uint64_t bd = kBack
                                                 ? tc::smem_desc_sw128(st + kUBytes + w * 2048, 8192, 1024)
                                                 : tc::smem_desc_sw128(st + kUBytes + (w / 4) * 8192 + (w % 4) * 32, 16, 1024);
-                        tc::mma_f16(tmem + 128 + b * 64, ad, bd, kIdesc2, i > 0 ? 1u : 0u);
+                        if (kF16 && n == kSteps) tc::mma_f16_scaled<kLoShift>(tmem + 128 + b * 64, ad, bd, kIdesc2);
+                        else tc::mma_f16(tmem + 128 + b * 64, ad, bd, kIdesc2, n > 0 ? 1u : 0u);
                     }
                     tc::mma_commit(smem_u32(&sh.d2_full[b]));
                 }
@@ -686,7 +695,8 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
                 for (int e = 0; e < 8; ++e) {
                     // (columns beyond the rank are U times zeros: NaN where U holds an infinity)
                     x[e] = c8 * 8 + e < g.rank ? x[e] * s : 0.f;
-                    m = fmaxf(m, fabsf(x[e]));
+                    const float y = fabsf(x[e]);
+                    if (y <= 3.402823466e38f) m = fmaxf(m, y);  // (infinities leave the others their scale)
                 }
                 if (kF16) {  // the row's pieces lie in kG neighbouring lanes
 #pragma unroll
@@ -812,10 +822,11 @@ struct WgCfg {
     static constexpr uint32_t kP = RP <= 32 ? 8192 : RP * 256;
     static constexpr uint32_t kStage = kU + kP;
     static constexpr int kPerSm = RP <= 32 ? 3 : 2;
+    static constexpr uint32_t kBars = kWgBars + 5 * RP * 4;  // and the columns' largest values and factors
     static constexpr uint32_t kBudget = (228 * 1024) / kPerSm / 1024 * 1024 - 1024;
-    static constexpr int kStages = (int)((kBudget - kWgBars) / kStage);
-    static constexpr uint32_t kSmem = kStages * kStage + kWgBars;
-    static constexpr uint32_t kTmem = RP < 32 ? 32 : RP;  // a power of two
+    static constexpr int kStages = (int)((kBudget - kBars) / kStage);
+    static constexpr uint32_t kSmem = kStages * kStage + kBars;
+    static constexpr uint32_t kTmem = 2 * RP;  // fp16: sums of hi's products, then of lo's; a power of two from 32 on
     static_assert(kStages >= 2 && kStages * kStage >= RP * kWgCols * 4u, "the partial sums fit in the ring");
 };
 
@@ -850,9 +861,10 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
         uint64_t full[S], empty[S], done, drain;
         uint32_t tmem;
         volatile int failed;
-        float warp_max[4];
+        float col_max[4][RP];  // per warp; fp16: the largest of every rank's column of P
+        float down[RP];        // what the columns were scaled by, inverted
     };
-    static_assert(sizeof(Shared) <= kWgBars, "barriers");
+    static_assert(sizeof(Shared) <= Cfg::kBars, "barriers");
     Shared& sh = *reinterpret_cast<Shared*>(smem_raw + S * Cfg::kStage);
     const uint32_t sbase = smem_u32(smem_raw);
     if (sbase & 1023u) {  // the same on every CTA
@@ -896,7 +908,6 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
     const uint32_t tmem = sh.tmem;
     const Waits wait{&sh.failed, g.err};
     const bool dependent = g.early && w.dependent;
-    float down = 1.f;  // what the parts of P were scaled by, inverted
 
     if (warp == 0) {
         // ---------------- loads of U
@@ -945,7 +956,8 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
                     for (int h = 0; h < 2; ++h) {
                         const uint64_t ad = tc::smem_desc_sw128(st + kk * 2048, 8192, 1024);
                         const uint64_t bd = tc::smem_desc_sw128(st + Cfg::kU + h * Cfg::kLo + kk * 2048, 8192, 1024);
-                        tc::mma_f16(tmem, ad, bd, kIdesc, (j > 0 || kk > 0 || h > 0) ? 1u : 0u);
+                        if (kF16) tc::mma_f16(tmem + h * RP, ad, bd, kIdesc, (j > 0 || kk > 0) ? 1u : 0u);
+                        else tc::mma_f16(tmem, ad, bd, kIdesc, (j > 0 || kk > 0 || h > 0) ? 1u : 0u);
                     }
                 tc::mma_commit(smem_u32(&sh.empty[s]));
             }
@@ -993,10 +1005,15 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
                 for (int e = 0; e < 8; ++e) x[e] = 0.f;
             }
         };
-        float up = 1.f;
-        if (kF16) {  // the largest magnitude among this CTA's tokens, eight pieces at a time (two
-                     // memory latencies: with four at a time this took a third of the kernel)
-            float m = 0.f;
+        // fp16: every rank's column has a factor of its own (the sums are taken column by column), from the
+        // largest magnitude among this CTA's tokens, eight pieces at a time (two memory latencies: with four
+        // at a time this took a third of the kernel). A thread's pieces are all of the same eight columns.
+        const int c8 = et % kCh * 8;
+        float up[8];
+        if (kF16) {
+            float m[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m[e] = 0.f;
             for (int j = 0; j < nc * kPer; j += 8) {
                 int tok[8];
 #pragma unroll
@@ -1007,17 +1024,25 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {  // (infinite columns leave the others their scale)
+                    for (int e = 0; e < 8; ++e) {  // (infinities leave the others their scale)
                         const float y = fabsf(x[i][e]);
-                        if (y <= 3.402823466e38f) m = fmaxf(m, y);
+                        if (y <= 3.402823466e38f) m[e] = fmaxf(m[e], y);
                     }
             }
 #pragma unroll
-            for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            if (lane == 0) sh.warp_max[warp - 2] = m;
+            for (int e = 0; e < 8; ++e) {
+#pragma unroll
+                for (int d = 16; d >= kCh; d >>= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], d));
+                if (lane < kCh) sh.col_max[warp - 2][c8 + e] = m[e];
+            }
             named_barrier(1, kWgEpi);
-            m = fmaxf(fmaxf(sh.warp_max[0], sh.warp_max[1]), fmaxf(sh.warp_max[2], sh.warp_max[3]));
-            pow2_scale(m, up, down);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float down;
+                pow2_scale(fmaxf(fmaxf(sh.col_max[0][c8 + e], sh.col_max[1][c8 + e]),
+                                 fmaxf(sh.col_max[2][c8 + e], sh.col_max[3][c8 + e])), up[e], down);
+                if (et < kCh) sh.down[c8 + e] = down;
+            }
         }
         // The next chunk's values, and the tokens of the one after, are on their way while a chunk
         // is written.
@@ -1043,7 +1068,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
                 const int at = (et + i * kWgEpi) / kCh, c = (et + i * kWgEpi) % kCh;
                 if (kF16)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[i][e] *= up;
+                    for (int e = 0; e < 8; ++e) x[i][e] *= up[e];
                 uint4 hi, lo;
                 split8<T>(x[i], hi, lo);
                 const uint32_t o = st + (c >> 3) * 8192;
@@ -1064,17 +1089,25 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
         tc::fence_after_sync();
         // partial sums [j][128 columns] over the ring, which nothing uses any more
         const int quarter = warp & 3, row = quarter * 32 + lane;
+        if (kF16) named_barrier(1, kWgEpi);  // the columns' factors are there
 #pragma unroll
         for (int c = 0; c < RP / 16; ++c) {
+            const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + c * 16;
             float y[16];
             if (nc > 0) {
-                tmem_load<16>(tmem + ((uint32_t)(quarter * 32) << 16) + c * 16, y);
+                tmem_load<16>(at, y);
+                if (kF16) {
+                    float l[16];
+                    tmem_load<16>(at + RP, l);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] = fmaf(l[i], 1.f / (1 << kLoShift), y[i]) * sh.down[c * 16 + i];
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) y[i] = 0.f;
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) st_shared_f32(sbase + ((c * 16 + i) * kWgCols + row) * 4, y[i] * down);
+            for (int i = 0; i < 16; ++i) st_shared_f32(sbase + ((c * 16 + i) * kWgCols + row) * 4, y[i]);
         }
         tc::fence_before_sync();
     }
