@@ -139,3 +139,27 @@ def test_fp16_weight_gradients_beside_large_ranks_and_tokens(tokens, rank):
     dA = sp.lora_grad(dY2, X2, d["A"], B, d["plan"], need=(False, True, False))[1]
     G, e = weight_gradient(as_f64(dY2), as_f64(B)[0], as_f64(X2))
     assert_within(dA[0], G, e, "f16", "dA")
+
+
+@pytest.mark.parametrize("fmt", ["f32", "f16"])
+@pytest.mark.parametrize("tokens,rank", [(5, 3), (700, 16), (2600, 24), (700, 33), (300, 100)])
+def test_an_infinity_beside_p_gives_the_formulas_infinity(fmt, tokens, rank):
+    """An infinity in the operand that meets P: the sign of the sum is P's, whatever parts P is multiplied in."""
+    d = operands(fmt, tokens, rank, seed=4)
+    hit = tokens // 2
+    _, h = sp.lora_add(d["X"], d["A"], d["B"], d["plan"], return_h=True)
+    dY, X, A, B = d["dY"].clone(), d["X"].clone(), d["A"].clone(), d["B"].clone()
+    dY[hit, 2] = float("inf")
+    dB = sp.lora_grad(dY, X, A, B, d["plan"], need=(False, False, True))[2][0]
+    assert torch.equal(dB[2].float(), h[hit] * float("inf")) and dB[3:].isfinite().all()
+    X[hit, 3] = float("inf")
+    dA = sp.lora_grad(d["dY"], X, A, B, d["plan"], need=(False, True, False))[1][0]
+    assert torch.equal(dA[:, 3].double(), (d["dY"][hit].double() @ B[0].double()) * float("inf"))
+    assert dA[:, 4:].isfinite().all()
+    B[0, 7, rank - 1] = float("inf")
+    Y = sp.lora_add(d["X"], A, B, d["plan"], base=d["base"])
+    assert torch.equal(Y[:, 7].float(), h[:, rank - 1] * float("inf")) and Y[:, 8:].isfinite().all()
+    A[0, 0, 5] = float("inf")
+    dX, _, _ = sp.lora_grad(d["dY"], d["X"], A, d["B"], d["plan"], dX_base=d["dX_base"], need=(True, False, False))
+    assert torch.equal(dX[:, 5].double(), (d["dY"].double() @ d["B"][0, :, 0].double()) * float("inf"))
+    assert dX[:, 6:].isfinite().all()

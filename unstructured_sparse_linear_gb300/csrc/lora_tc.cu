@@ -160,20 +160,38 @@ __device__ __forceinline__ void pow2_scale(float m, float& up, float& down) {
     }
 }
 
-// The lo part of an fp16 pair is kept times 2^kLoShift: hi is at most 2^15 and drops at most half of one of its
-// units, 2^3, so lo stays below 2^15 as well, and what it cannot hold is below 2^-36 (2^-50 of the largest).
+// The lo part of an fp16 pair is kept times 2^kLoShift: hi is at most 2^15 and drops less than one of its own
+// units, 2^4, so lo stays below 2^15 as well, and what it cannot hold is below 2^-36 (2^-50 of the largest).
 constexpr int kLoShift = 11;
 
-// Eight values as eight hi and eight lo parts (fp16: of values that pow2_scale has scaled).
+// Eight values as eight hi and eight lo parts. bf16: both rounded. fp16 (values that pow2_scale has scaled): hi
+// is rounded towards zero, and to less than the value itself, so that lo has its sign and is not zero: an
+// infinity in the other operand then meets two parts of one sign.
 template <typename T>
 __device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
-    constexpr float kUp = std::is_same<T, __half>::value ? (float)(1 << kLoShift) : 1.f;
-    hi = Elt<T>::pack(x);
-    float h[8], l[8];
-    Elt<T>::unpack(hi, h);
+    if constexpr (std::is_same<T, __half>::value) {
+        float l[8];
+        uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) l[i] = fabsf(h[i]) <= 3.402823466e38f ? (x[i] - h[i]) * kUp : 0.f;  // no inf - inf
-    lo = Elt<T>::pack(l);
+        for (int i = 0; i < 8; ++i) {
+            h[i] = __half_as_ushort(__float2half_rz(x[i]));
+            float r = x[i] - __half2float(__ushort_as_half((unsigned short)h[i]));
+            if (r == 0.f && (h[i] & 0x7fffu)) {  // (an infinity is left as it is: r is NaN)
+                h[i] -= 1;
+                r = x[i] - __half2float(__ushort_as_half((unsigned short)h[i]));
+            }
+            l[i] = fabsf(x[i]) <= 3.402823466e38f ? r * (float)(1 << kLoShift) : 0.f;
+        }
+        hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        lo = Elt<T>::pack(l);
+    } else {
+        hi = Elt<T>::pack(x);
+        float h[8], l[8];
+        Elt<T>::unpack(hi, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[i] = fabsf(h[i]) <= 3.402823466e38f ? x[i] - h[i] : 0.f;  // no inf - inf
+        lo = Elt<T>::pack(l);
+    }
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
