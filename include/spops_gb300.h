@@ -302,9 +302,9 @@ SPOPS_API int spops_masked_adam_csr(float* param, float* exp_avg, float* exp_avg
  * Activations are token-major: row t of X, Y, ... is token t, rows ld elements apart (ld at
  * least the columns), so a slice of a fused projection's columns can be an operand.
  * rank <= SPOPS_LORA_MAX_RANK. Products accumulate in fp32; X A_i^T stays in 32 bits (as an operand
- * on the tensor cores it is the sum of two 16-bit parts: 16 of its bits for bf16; for fp16 22, and 16 for values
- * of 2^-34 of the largest of their token, or in a weight gradient of their rank), and every output is rounded
- * once. A token's result depends on no other token and on no other
+ * on the tensor cores it is the sum of 16-bit parts: all 24 of its bits for bf16; for fp16 22, and 16 for values of
+ * 2^-34 of the largest of their token, or in a weight gradient of their rank), and every output is rounded once.
+ * A token's result depends on no other token and on no other
  * adapter's weights (infinities and NaN stay where they are). Deterministic. */
 #define SPOPS_LORA_MAX_RANK 128
 /* The most tokens of a batch, and the most adapters: the kernels count both in 32 bits and step past the last one. */

@@ -141,7 +141,7 @@ def test_fp16_weight_gradients_beside_large_ranks_and_tokens(tokens, rank):
     assert_within(dA[0], G, e, "f16", "dA")
 
 
-@pytest.mark.parametrize("fmt", ["f32", "f16"])
+@pytest.mark.parametrize("fmt", list(DTYPES))
 @pytest.mark.parametrize("tokens,rank", [(5, 3), (700, 16), (2600, 24), (700, 33), (300, 100)])
 def test_an_infinity_beside_p_gives_the_formulas_infinity(fmt, tokens, rank):
     """An infinity in the operand that meets P: the sign of the sum is P's, whatever parts P is multiplied in."""
@@ -163,3 +163,59 @@ def test_an_infinity_beside_p_gives_the_formulas_infinity(fmt, tokens, rank):
     dX, _, _ = sp.lora_grad(d["dY"], d["X"], A, d["B"], d["plan"], dX_base=d["dX_base"], need=(True, False, False))
     assert torch.equal(dX[:, 5].double(), (d["dY"].double() @ d["B"][0, :, 0].double()) * float("inf"))
     assert dX[:, 6:].isfinite().all()
+
+
+# What the parts of P hold of it where it meets the second operand (three of 8 bits, two of 11).
+BITS = {"bf16": 2.0 ** -24, "f16": 2.0 ** -22}
+LOW = {"bf16": 128, "f16": 64}  # integers from here to twice it: P is one of 23 bits (bf16), of 21 (fp16)
+
+
+def integers(fmt, rng, rows, cols, pairs_along_rows=True):
+    """Integers; row (or column) 2 i + 1 is row 2 i with one entry changed by one."""
+    x = rng.integers(LOW[fmt], 2 * LOW[fmt], (rows, cols))
+    if not pairs_along_rows:
+        return integers(fmt, rng, cols, rows).T
+    x[1::2] = x[0:rows // 2 * 2:2]
+    at = rng.integers(0, cols, rows // 2)
+    x[2 * np.arange(rows // 2) + 1, at] += np.where(x[2 * np.arange(rows // 2) + 1, at] > LOW[fmt], -1, 1)
+    return x
+
+
+def differences(rows, cols):
+    """[rows, cols] with 1 and -1 at the pair 2 i, 2 i + 1 of columns of row r, i = r mod cols / 2."""
+    d = np.zeros((rows, cols))
+    i = np.arange(rows) % (cols // 2)
+    d[np.arange(rows), 2 * i], d[np.arange(rows), 2 * i + 1] = 1, -1
+    return d
+
+
+@pytest.mark.parametrize("fmt", list(BITS))
+@pytest.mark.parametrize("tokens,rank", [(6, 4), (700, 16), (700, 32), (700, 40), (400, 64), (400, 100), (300, 128)])
+def test_small_differences_of_large_values_of_p(fmt, tokens, rank):
+    """Every sum is of integers below 2^24, so P is exact, and the differences of neighbours that the second
+    products take show each bit that P lost on its way there."""
+    rng = np.random.default_rng([31, tokens, rank])
+    k, n, scale = 128, 136, 2.0 ** -7
+    plan = sp.lora_plan(None, 1, tokens=tokens, device=DEV)
+
+    def dev(x):
+        t = torch.from_numpy(np.ascontiguousarray(x)).to(DTYPES[fmt]).to(DEV)
+        assert np.array_equal(as_f64(t), x)
+        return t
+
+    def near(got, want, P, what):
+        err = 2 * BITS[fmt] * scale * np.abs(P).max()
+        assert_within(got, scale * want, err, fmt, what)
+
+    X, A, D = integers(fmt, rng, tokens, k), integers(fmt, rng, rank, k), differences(n, rank)
+    Y = sp.lora_add(dev(X), dev(A)[None], dev(D)[None], plan, scale=scale)
+    near(Y, (X @ A.T) @ D.T, X @ A.T, "Y")
+    Z = differences(n, tokens).T  # [tokens, n]: pairs of tokens
+    dB = sp.lora_grad(dev(Z), dev(X), dev(A)[None], dev(D)[None], plan, scale=scale, need=(False, False, True))[2]
+    near(dB[0], Z.T @ (X @ A.T), X @ A.T, "dB")
+    dY, B, D = integers(fmt, rng, tokens, n), integers(fmt, rng, n, rank, False), differences(k, rank).T
+    dX = sp.lora_grad(dev(dY), dev(X), dev(D)[None], dev(B)[None], plan, scale=scale, need=(True, False, False))[0]
+    near(dX, (dY @ B) @ D, dY @ B, "dX")
+    Z = differences(k, tokens).T
+    dA = sp.lora_grad(dev(dY), dev(Z), dev(D)[None], dev(B)[None], plan, scale=scale, need=(False, True, False))[1]
+    near(dA[0], (dY @ B).T @ Z, dY @ B, "dA")

@@ -4,13 +4,13 @@
 //                    that share an adapter (the forward product and the input gradient);
 // lora_wgrad_kernel  G = s P^T U over an adapter's tokens (the weights' gradients).
 //
-// Precision. P stays in 32 bits where it is kept (TMEM, shared memory, global). As an operand
-// of the second product it is the sum of two 16-bit parts, hi = round(P) and lo = round(P - hi),
-// whose products have the same fp32 sums: 16 bits or more of P take part (a single bf16 part would
-// add an error as large as the output's own rounding). For fp16, whose range P = U W1 leaves easily
-// (small gradients, large activations), a row (for a weight gradient: a rank's column among a CTA's tokens)
-// is first scaled by a power of two, and lo is kept 2^11 times larger; both are taken back in fp32. So 22 bits
-// of P take part, 16 of values of 2^-34 of the row's or column's largest, and whatever lies above 2^-50 of it.
+// Precision. P stays in 32 bits where it is kept (TMEM, shared memory, global). As an operand of the
+// second product it is the sum of 16-bit parts whose products have fp32 sums (a single bf16 part would add an
+// error as large as the output's own rounding). bf16: three parts, all 24 bits of P. fp16, whose range P = U W1
+// leaves easily (small gradients, large activations): two; a row (for a weight gradient: a rank's column among a CTA's
+// tokens) is first scaled by a power of two, and the second part is kept 2^11 times larger; both are taken back in
+// fp32. So 22 bits of P take part, 16 of values of 2^-34 of the row's or column's largest, and whatever lies
+// above 2^-50 of it.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -164,34 +164,54 @@ __device__ __forceinline__ void pow2_scale(float m, float& up, float& down) {
 // units, 2^4, so lo stays below 2^15 as well, and what it cannot hold is below 2^-36 (2^-50 of the largest).
 constexpr int kLoShift = 11;
 
-// Eight values as eight hi and eight lo parts. bf16: both rounded. fp16 (values that pow2_scale has scaled): hi
-// is rounded towards zero, and to less than the value itself, so that lo has its sign and is not zero: an
-// infinity in the other operand then meets two parts of one sign.
+// The parts that P is multiplied in.
 template <typename T>
-__device__ __forceinline__ void split8(const float* x, uint4& hi, uint4& lo) {
-    if constexpr (std::is_same<T, __half>::value) {
-        float l[8];
-        uint32_t h[8];
+constexpr int kParts = std::is_same<T, __half>::value ? 2 : 3;
+
+// Eight values as eight values of each part. Every part but the last is rounded towards zero and a 2^-25th of the
+// value or less is added to what is left, so that all parts of a value have its sign and none is zero: an
+// infinity in the other operand then meets parts of one sign. bf16: three parts of 8 bits, the value itself (but for
+// the 2^-25th where the last part would be zero). fp16: of values that pow2_scale has scaled.
+template <typename T>
+__device__ __forceinline__ void split8(const float* x, uint4 (&part)[kParts<T>]) {
+    uint32_t w[kParts<T>][4];
+    float zero[2] = {0.f, 0.f};  // NaN once an infinity or a NaN has been multiplied in
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = x[2 * i], b = x[2 * i + 1];
+        zero[0] = fmaf(a, 0.f, zero[0]);
+        zero[1] = fmaf(b, 0.f, zero[1]);
+        if constexpr (std::is_same<T, __half>::value) {
+            const __half2 h = __halves2half2(__float2half_rz(a), __float2half_rz(b));
+            const float2 f = __half22float2(h);
+            const float la = fmaf(a - f.x, (float)(1 << kLoShift), a * (float)(1.0 / (1 << (25 - kLoShift))));
+            const float lb = fmaf(b - f.y, (float)(1 << kLoShift), b * (float)(1.0 / (1 << (25 - kLoShift))));
+            const __half2 l = __floats2half2_rn(la, lb);
+            w[0][i] = reinterpret_cast<const uint32_t&>(h);
+            w[1][i] = reinterpret_cast<const uint32_t&>(l);
+        } else {
+            const uint32_t ha = __float_as_uint(a) & 0xffff0000u, hb = __float_as_uint(b) & 0xffff0000u;
+            const float ra = fmaf(a, 0x1p-26f, a - __uint_as_float(ha)), rb = fmaf(b, 0x1p-26f, b - __uint_as_float(hb));
+            const uint32_t ma = __float_as_uint(ra) & 0xffff0000u, mb = __float_as_uint(rb) & 0xffff0000u;
+            const float la = fmaf(a, 0x1p-28f, ra - __uint_as_float(ma)), lb = fmaf(b, 0x1p-28f, rb - __uint_as_float(mb));
+            w[0][i] = __byte_perm(ha, hb, 0x7632);
+            w[1][i] = __byte_perm(ma, mb, 0x7632);
+            w[2][i] = __byte_perm(__float_as_uint(la), __float_as_uint(lb), 0x7632);
+        }
+    }
+    if (!(zero[0] + zero[1] == 0.f)) {  // infinities and NaN are their first part, beside zeros
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            h[i] = __half_as_ushort(__float2half_rz(x[i]));
-            float r = x[i] - __half2float(__ushort_as_half((unsigned short)h[i]));
-            if (r == 0.f && (h[i] & 0x7fffu)) {  // (an infinity is left as it is: r is NaN)
-                h[i] -= 1;
-                r = x[i] - __half2float(__ushort_as_half((unsigned short)h[i]));
-            }
-            l[i] = fabsf(x[i]) <= 3.402823466e38f ? r * (float)(1 << kLoShift) : 0.f;
-        }
-        hi = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
-        lo = Elt<T>::pack(l);
-    } else {
-        hi = Elt<T>::pack(x);
-        float h[8], l[8];
-        Elt<T>::unpack(hi, h);
+            if (fabsf(x[i]) <= 3.402823466e38f) continue;
+            const uint32_t shift = 16 * (i & 1), keep = ~(0xffffu << shift);
+            const T y = Elt<T>::from_f(x[i]);
+            w[0][i / 2] = (w[0][i / 2] & keep) | (uint32_t) reinterpret_cast<const uint16_t&>(y) << shift;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) l[i] = fabsf(h[i]) <= 3.402823466e38f ? x[i] - h[i] : 0.f;  // no inf - inf
-        lo = Elt<T>::pack(l);
+            for (int p = 1; p < kParts<T>; ++p) w[p][i / 2] &= keep;
+        }
     }
+#pragma unroll
+    for (int p = 0; p < kParts<T>; ++p) part[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint4 v) {
@@ -233,6 +253,10 @@ __device__ __forceinline__ int p_place(int r, int c, int own) {
     return c * own + (rw >= 8 ? r : r ^ (rw * ((c >> 1) & (8 / rw - 1))));
 }
 
+// The same among the sums that every rank receives of all rows: a warp reads 32 rows at one piece, and sends
+// 256 / RP rows x RP / 8 pieces of one half.
+__device__ __forceinline__ int sum_place(int r, int c) { return c * kLoraTile + (r ^ ((c >> 1) & 7)); }
+
 __device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
     asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -272,6 +296,41 @@ __device__ __forceinline__ void tmem_load(uint32_t taddr, float* v) {
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// N 32-bit TMEM columns of the thread's lane, complete on return.
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[N]) {
+    static_assert(N == 4 || N == 8 || N == 16 || N == 32, "shapes");
+    if constexpr (N == 4) {
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n\t"
+            "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+            : "memory");
+    } else if constexpr (N == 8) {
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
+            "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+            : "memory");
+    } else if constexpr (N == 16) {
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
+            "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+            "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+            : "memory");
+    } else {
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
+            "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+            "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+            "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+            "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+            : "memory");
+    }
 }
 
 // Copies of B bytes (4 or 8) from global to shared memory, and the arrival on `bar` of a thread
@@ -341,13 +400,13 @@ constexpr int kTileThreads = 320;
 constexpr int kEpi = 256;
 constexpr uint32_t kTileBars = 1024;  // barriers, flags and row factors, behind the stages and P
 
-template <int RP>
+template <typename T, int RP>
 struct TileCfg {
     static constexpr int kBlocks = (RP + 63) / 64;
     static constexpr uint32_t kW = RP > 64 ? 16384 : 8192;       // weight tile of a stage
     static constexpr uint32_t kStage = kUBytes + kW;
-    // The hi and lo parts of P, 2 RP columns in swizzled blocks of 128 rows x 64 columns, or its
-    // fp32 partial sums (128 RP of them).
+    // fp16: the parts of P, RP columns each in swizzled blocks of 128 rows x 64 columns; its fp32 (partial)
+    // sums, 128 RP of them.
     static constexpr uint32_t kH = (2 * RP + 63) / 64 * kUBytes;
     static_assert(kH >= RP * 512u, "the partial sums fit");
     static constexpr int kPerSm = RP > 64 ? 1 : 2;
@@ -356,7 +415,14 @@ struct TileCfg {
     static constexpr uint32_t kBudget = (228 * 1024) / kPerSm - 1024;
     static constexpr int kStages = (int)((kBudget - kTileBars - kH) / kStage);
     static constexpr uint32_t kSmem = kStages * kStage + kH + kTileBars;
-    static constexpr uint32_t kTmem = 256;  // P: columns 0 .. RP - 1; O: two buffers of 64 at 128 and 192
+    // bf16: parts of P that are operands in TMEM, from column kPartsAt on, RP / 2 columns each. In shared memory three
+    // would take a stage of the ring, and rank 128 be bound by their reads (8192 tokens, 2048 -> 8192: rank 64
+    // 78.5 us, rank 128 188). For rank 64 the first one is left there: two CTAs share the SM's TMEM.
+    static constexpr int kInTmem = kParts<T> == 2 ? 0 : RP == 64 ? 2 : 3;
+    static constexpr uint32_t kPartsAt = RP > 64 ? 256 : 64;
+    // P: columns 0 .. RP - 1; O: two buffers of 64 at 128 and 192
+    static constexpr uint32_t kTmem = kInTmem && RP > 64 ? 512 : 256;
+    static_assert(kPartsAt + kInTmem * RP / 2 <= (RP > 64 ? 512 : 128) && kPartsAt >= (RP > 64 ? 256 : RP), "TMEM columns");
 };
 
 // Row-strided operands come in boxes of 128, 32 or 8 consecutive rows, or four rows anywhere.
@@ -411,15 +477,15 @@ __device__ __forceinline__ RowSource row_source(const LoraTile& t, const int32_t
 
 // A cluster of C CTAs takes a tile: rank c multiplies a share of the K chunks into its TMEM; the
 // fp32 partial P are sent through distributed shared memory to the rank that owns the row, which
-// adds them in rank order and sends the two 16-bit parts back to all; and rank c forms a share of
+// adds them in rank order and sends the sums (fp16: their two parts) to all; and rank c forms a share of
 // the 64-column chunks of O. One ring of stages carries both phases, so the loads of base run
 // ahead while P is being summed: a stage holds a 128 x 64 tile
 // of U with a tile of W1, then a 128 x 64 tile of base, in which O is formed in place, with a tile
 // of W2.
 template <typename T, bool kBack, int RP>
-__global__ void __launch_bounds__(kTileThreads, TileCfg<RP>::kPerSm)
+__global__ void __launch_bounds__(kTileThreads, TileCfg<T, RP>::kPerSm)
 lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
-    using Cfg = TileCfg<RP>;
+    using Cfg = TileCfg<T, RP>;
     constexpr int S = Cfg::kStages;
     constexpr bool kF16 = std::is_same<T, __half>::value;
     constexpr uint32_t kFmt = kF16 ? 0u : 1u;
@@ -430,7 +496,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
     // tiles need (checked).
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     struct Shared {
-        uint64_t full[S], empty[S], d1, h, d2_full[2], d2_empty[2], pub, read, freed, drain;
+        uint64_t full[S], empty[S], d1, h, parts, d2_full[2], d2_empty[2], pub, read, freed, drain;
         uint32_t tmem;
         volatile int failed;
         float down[kLoraTile];  // fp16: what a row's parts were scaled by, inverted
@@ -462,6 +528,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
         }
         mbar_init(smem_u32(&sh.d1), 1);
         mbar_init(smem_u32(&sh.h), 1);
+        mbar_init(smem_u32(&sh.parts), kEpi / 32);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.d2_full[i]), 1);
             mbar_init(smem_u32(&sh.d2_empty[i]), 4);
@@ -575,9 +642,10 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
                 }
                 if (!ok) break;
                 tc::mma_commit(smem_u32(&sh.d1));
-                ok = wait.cluster(smem_u32(&sh.h), tt & 1u);  // P's parts are here, and its columns read
+                // P's parts are here, and its columns read
+                ok = kF16 ? wait.cluster(smem_u32(&sh.h), tt & 1u) : wait(smem_u32(&sh.parts), tt & 1u);
                 if (!ok) break;
-                fence_proxy_async_smem();  // the parts came from threads of every rank
+                fence_proxy_async_smem();  // the parts came from threads (fp16: of every rank)
                 tc::fence_after_sync();
                 for (int j = 0; j < nn; ++j, ++q, ++n2) {
                     const uint32_t s = q % S, st = sbase + s * Cfg::kStage, b = n2 & 1u;
@@ -590,14 +658,20 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
                     // is added.
                     constexpr int kSteps = RP / 16;
 #pragma unroll
-                    for (int n = 0; n < 2 * kSteps; ++n) {
+                    for (int n = 0; n < kParts<T> * kSteps; ++n) {
                         const int i = kF16 ? (n + kSteps) % (2 * kSteps) : n, w = i % kSteps;
-                        const uint64_t ad = tc::smem_desc_sw128(hbase + (i / 4) * 16384 + (i % 4) * 32, 16, 1024);
+                        const uint32_t d = tmem + 128 + b * 64;
                         const uint64_t bd = kBack
                                                 ? tc::smem_desc_sw128(st + kUBytes + w * 2048, 8192, 1024)
                                                 : tc::smem_desc_sw128(st + kUBytes + (w / 4) * 8192 + (w % 4) * 32, 16, 1024);
-                        if (kF16 && n == kSteps) tc::mma_f16_scaled<kLoShift>(tmem + 128 + b * 64, ad, bd, kIdesc2);
-                        else tc::mma_f16(tmem + 128 + b * 64, ad, bd, kIdesc2, n > 0 ? 1u : 0u);
+                        const int in_tmem = i - (kParts<T> - Cfg::kInTmem) * kSteps;
+                        if (in_tmem >= 0) {
+                            tc::mma_f16_ts(d, tmem + Cfg::kPartsAt + in_tmem * 8, bd, kIdesc2, n > 0 ? 1u : 0u);
+                            continue;
+                        }
+                        const uint64_t ad = tc::smem_desc_sw128(hbase + (i / 4) * 16384 + (i % 4) * 32, 16, 1024);
+                        if (kF16 && n == kSteps) tc::mma_f16_scaled<kLoShift>(d, ad, bd, kIdesc2);
+                        else tc::mma_f16(d, ad, bd, kIdesc2, n > 0 ? 1u : 0u);
                     }
                     tc::mma_commit(smem_u32(&sh.d2_full[b]));
                 }
@@ -706,7 +780,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
             }
             wait.cluster(smem_u32(&sh.read), tt & 1u);  // every rank has read its slots
             __syncwarp();
-            // The two parts of s P go to every rank.
+            // s P goes to every rank.
             if (sums) {
                 float m = 0.f, up = 1.f, down = 1.f;
 #pragma unroll
@@ -723,14 +797,28 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] *= up;
                 }
-                uint4 hi, lo;
-                split8<T>(x, hi, lo);
-                const uint32_t at_hi = hbase + (c8 >> 3) * kUBytes + tc::sw128_off(r, c8 & 7);
-                const uint32_t at_lo = hbase + ((c8 + kG) >> 3) * kUBytes + tc::sw128_off(r, (c8 + kG) & 7);
+                // fp16: two parts; bf16: the values, which every rank takes apart itself (as many bytes as two parts)
+                uint4 send[2];
+                uint32_t to[2];
+                if constexpr (kF16) {
+                    split8<T>(x, send);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const int at = c8 + p * kG;
+                        to[p] = hbase + (at >> 3) * kUBytes + tc::sw128_off(r, at & 7);
+                    }
+                } else {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        send[p] = make_uint4(__float_as_uint(x[4 * p]), __float_as_uint(x[4 * p + 1]),
+                                             __float_as_uint(x[4 * p + 2]), __float_as_uint(x[4 * p + 3]));
+                        to[p] = hbase + (uint32_t)sum_place(r, 2 * c8 + p) * 16;
+                    }
+                }
                 for (int c = 0; c < C; ++c) {
                     const uint32_t bar = cluster_map(smem_u32(&sh.h), c);
-                    st_async_v4(cluster_map(at_hi, c), hi, bar);
-                    st_async_v4(cluster_map(at_lo, c), lo, bar);
+                    st_async_v4(cluster_map(to[0], c), send[0], bar);
+                    st_async_v4(cluster_map(to[1], c), send[1], bar);
                     if (kF16 && c8 == 0)
                         st_async_b32(cluster_map(smem_u32(&sh.down[r]), c), __float_as_uint(down), bar);
                 }
@@ -738,6 +826,42 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
             wait.cluster(smem_u32(&sh.h), tt & 1u);
             __syncwarp();
             const float down = kF16 ? sh.down[row] : 1.f;
+            if constexpr (!kF16) {
+                // Half of a row's columns per thread.
+                constexpr int kInSmem = 3 - Cfg::kInTmem;  // (over the place of the values)
+                float p[RP / 2];
+#pragma unroll
+                for (int i = 0; i < RP / 8; ++i) {
+                    const uint4 v = ld_shared_v4(hbase + (uint32_t)sum_place(row, grp * (RP / 8) + i) * 16);
+                    p[4 * i] = __uint_as_float(v.x);
+                    p[4 * i + 1] = __uint_as_float(v.y);
+                    p[4 * i + 2] = __uint_as_float(v.z);
+                    p[4 * i + 3] = __uint_as_float(v.w);
+                }
+                if (kInSmem) named_barrier(1, kEpi);
+                uint32_t words[3][RP / 4];
+#pragma unroll
+                for (int i = 0; i < RP / 16; ++i) {
+                    uint4 part[3];
+                    split8<T>(p + 8 * i, part);
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) {
+                        const int at = grp * (RP / 16) + i + q * kG;
+                        if (q < kInSmem) st_shared_v4(hbase + (at >> 3) * kUBytes + tc::sw128_off(row, at & 7), part[q]);
+                        words[q][4 * i] = part[q].x;
+                        words[q][4 * i + 1] = part[q].y;
+                        words[q][4 * i + 2] = part[q].z;
+                        words[q][4 * i + 3] = part[q].w;
+                    }
+                }
+#pragma unroll
+                for (int q = kInSmem; q < 3; ++q)
+                    tmem_store<RP / 4>(lane_addr + Cfg::kPartsAt + (q - kInSmem) * (RP / 2) + grp * (RP / 4), words[q]);
+                tc::fence_before_sync();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.parts));
+            }
 
             // Chunks of O, in turns between the two groups of four warps (thread = row): the steps of
             // one chunk depend on each other, so two are under way at a time.
@@ -825,26 +949,31 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
 
 // ------------------------------------------------------------------ weight gradients
 
-// Warps: 0 loads U (TMA), 1 multiplies (one thread), 2 to 5 write P's parts into the stages.
-constexpr int kWgThreads = 192;
-constexpr int kWgEpi = 128;
+// Warps: 0 loads U (TMA), 1 multiplies (one thread), the others (four, from rank 17 on eight) write P's parts into
+// the stages.
 constexpr int kWgCols = 128;  // columns of U per cluster (the M of the products)
 constexpr uint32_t kWgBars = 512;
 
-template <int RP>
+template <typename T, int RP>
 struct WgCfg {
-    static constexpr uint32_t kU = kWgCols / 64 * 8192;  // 64 tokens x 128 columns, 64-column blocks
-    // 64 tokens x RP of each part of P in 64-column blocks of 8 KB: up to rank 32 both parts share
-    // a block (hi in its first 32 columns, lo in the others), else a part has blocks of its own.
-    static constexpr uint32_t kLo = RP <= 32 ? 64 : RP * 128;  // bytes from hi to lo
-    static constexpr uint32_t kP = RP <= 32 ? 8192 : RP * 256;
+    static constexpr int kTok = kParts<T> == 3 && RP > 64 ? 32 : 64;  // tokens of a stage
+    static constexpr uint32_t kBlock = kTok * 128;                   // of 64 columns of them
+    static constexpr uint32_t kU = kWgCols / 64 * kBlock;
+    // RP columns of each part of P, one part behind the other, in blocks.
+    static constexpr uint32_t kP = (kParts<T> * RP + 63) / 64 * kBlock;
+    // One product takes all parts, each to sums of its own that are added in the end: the count of products is what
+    // a third part costs (8192 tokens of 4 adapters, 2048 -> 8192, rank 16, a gradient: 82.9 us with two products per 16
+    // tokens, 89.9 with three). At rank 128 the parts are too wide for that; bf16 adds them to the same sums there.
+    static constexpr int kProducts = kParts<T> * RP <= 256 ? 1 : kParts<T>;
+    static constexpr int kN = kParts<T> * RP / kProducts;
     static constexpr uint32_t kStage = kU + kP;
     static constexpr int kPerSm = RP <= 32 ? 3 : 2;
-    static constexpr uint32_t kBars = kWgBars + 5 * RP * 4;  // and the columns' largest values and factors
+    static constexpr int kPWarps = RP <= 16 ? 4 : 8, kEpi = 32 * kPWarps, kThreads = 64 + kEpi;
+    static constexpr uint32_t kBars = kWgBars + (kPWarps + 1) * RP * 4;  // and the columns' largest values and factors
     static constexpr uint32_t kBudget = (228 * 1024) / kPerSm / 1024 * 1024 - 1024;
     static constexpr int kStages = (int)((kBudget - kBars) / kStage);
     static constexpr uint32_t kSmem = kStages * kStage + kBars;
-    static constexpr uint32_t kTmem = 2 * RP;  // fp16: sums of hi's products, then of lo's; a power of two from 32 on
+    static constexpr uint32_t kTmem = kN <= 32 ? 32 : kN <= 64 ? 64 : kN <= 128 ? 128 : 256;
     static_assert(kStages >= 2 && kStages * kStage >= RP * kWgCols * 4u, "the partial sums fit in the ring");
 };
 
@@ -860,26 +989,27 @@ struct WgArgs {
 };
 
 // A cluster takes 128 columns of one adapter's gradient; its CTAs split the adapter's tokens in
-// chunks of 64 and their fp32 partial sums are added in rank order through distributed shared
-// memory. U's rows are the K axis: a chunk is 64 rows x 128 columns, an MN-major operand just as
+// chunks and their fp32 partial sums are added in rank order through distributed shared
+// memory. U's rows are the K axis: a chunk is 64 (or 32) rows x 128 columns, an MN-major operand just as
 // TMA writes it (boxes of 64 columns; four rows at a time where the tokens are not consecutive).
 // Rows past the adapter's last token are asked for beyond the tensor, which fills zeros. P is
-// read in fp32 and written to the stage as its two parts by the four warps that later drain the
+// read in fp32 and written to the stage as its parts by the warps that later drain the
 // accumulators.
 template <typename T, int RP>
-__global__ void __launch_bounds__(kWgThreads, WgCfg<RP>::kPerSm)
+__global__ void __launch_bounds__(WgCfg<T, RP>::kThreads, WgCfg<T, RP>::kPerSm)
 lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, const __grid_constant__ CUtensorMap map_g0,
                   const __grid_constant__ CUtensorMap map_u1, const __grid_constant__ CUtensorMap map_g1) {
-    using Cfg = WgCfg<RP>;
-    constexpr int S = Cfg::kStages;
+    using Cfg = WgCfg<T, RP>;
+    constexpr int S = Cfg::kStages, kTok = Cfg::kTok, kPWarps = Cfg::kPWarps, kEpi = Cfg::kEpi;
+    constexpr uint32_t kBlock = Cfg::kBlock;
     constexpr bool kF16 = std::is_same<T, __half>::value;
-    constexpr uint32_t kIdesc = tc::instr_desc_f16(kF16 ? 0u : 1u, 1, 1, 128, RP);
+    constexpr uint32_t kIdesc = tc::instr_desc_f16(kF16 ? 0u : 1u, 1, 1, 128, Cfg::kN);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     struct Shared {
         uint64_t full[S], empty[S], done, drain;
         uint32_t tmem;
         volatile int failed;
-        float col_max[4][RP];  // per warp; fp16: the largest of every rank's column of P
+        float col_max[kPWarps][RP];  // per warp; fp16: the largest of every rank's column of P
         float down[RP];        // what the columns were scaled by, inverted
     };
     static_assert(sizeof(Shared) <= Cfg::kBars, "barriers");
@@ -901,10 +1031,10 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
     // 16-byte stores of the gradient
     const bool vec_out = (reinterpret_cast<uintptr_t>(w.G) & 15) == 0 && (!w.rank_minor || g.rank % 8 == 0);
     const int p0 = g.v.off[adapter], cnt = g.v.off[adapter + 1] - p0;
-    const int chunks = (cnt + 63) / 64;
+    const int chunks = (cnt + kTok - 1) / kTok;
     const int ca = (int)((int64_t)chunks * crank / C), cb = (int)((int64_t)chunks * (crank + 1) / C);
     const int nc = cb - ca;
-    const int pa = p0 + ca * 64, pe = min(p0 + cnt, p0 + cb * 64);  // this CTA's positions
+    const int pa = p0 + ca * kTok, pe = min(p0 + cnt, p0 + cb * kTok);  // this CTA's positions
 
     if (warp == 1) {
         tc::tmem_alloc(smem_u32(&sh.tmem), Cfg::kTmem);
@@ -912,7 +1042,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
     }
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&sh.full[s]), 1 + 4);
+            mbar_init(smem_u32(&sh.full[s]), 1 + kPWarps);
             mbar_init(smem_u32(&sh.empty[s]), 1);
         }
         mbar_init(smem_u32(&sh.done), 1);
@@ -936,24 +1066,25 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
         for (; j < nc; ++j) {
             const int s = j % S;
             const uint32_t st = sbase + s * Cfg::kStage, fb = smem_u32(&sh.full[s]);
-            const int b = pa + j * 64, m = min(64, pe - b);
-            // lane = 4 tokens (group lane % 16) and one of the two 64-column blocks
+            const int b = pa + j * kTok, m = min(kTok, pe - b);
+            // lane = 4 tokens (group lane % kTok / 4) and one of the two 64-column blocks
+            constexpr int kGroups = kTok / 4;
             int y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int at = (lane & 15) * 4 + i;
+                const int at = lane % kGroups * 4 + i;
                 y[i] = at < m ? g.v.order[b + at] : g.v.tokens;  // past the last row: zeros
             }
-            const int first = __shfl_sync(0xffffffffu, y[0], 0), last = __shfl_sync(0xffffffffu, y[3], 15);
-            const bool box = m == 64 && last - first == 63;
+            const int first = __shfl_sync(0xffffffffu, y[0], 0), last = __shfl_sync(0xffffffffu, y[3], kGroups - 1);
+            const bool box = m == kTok && last - first == kTok - 1;
             if (j >= S && !__all_sync(0xffffffffu, wait(smem_u32(&sh.empty[s]), (j / S - 1) & 1u))) break;
             if (lane == 0) mbar_arrive_expect_tx(fb, Cfg::kU);
             __syncwarp();
             if (box) {
-                if (lane < kWgCols / 64) tma_load_2d<true>(st + lane * 8192, mu, n0 + lane * 64, first, fb, policy);
-            } else {
-                const int c = lane >> 4;
-                tma_gather4<true>(st + c * 8192 + (lane & 15) * 512, mg, n0 + c * 64, y, fb, policy);
+                if (lane < kWgCols / 64) tma_load_2d<true>(st + lane * kBlock, mu, n0 + lane * 64, first, fb, policy);
+            } else if (lane < kWgCols / 64 * kGroups) {
+                const int c = lane / kGroups;
+                tma_gather4<true>(st + c * kBlock + lane % kGroups * 512, mg, n0 + c * 64, y, fb, policy);
             }
         }
         if (sh.failed) {
@@ -969,13 +1100,13 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
                 if (!wait(smem_u32(&sh.full[s]), (j / S) & 1u)) break;
                 tc::fence_after_sync();
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
+                for (int kk = 0; kk < kTok / 16; ++kk)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint64_t ad = tc::smem_desc_sw128(st + kk * 2048, 8192, 1024);
-                        const uint64_t bd = tc::smem_desc_sw128(st + Cfg::kU + h * Cfg::kLo + kk * 2048, 8192, 1024);
-                        if (kF16) tc::mma_f16(tmem + h * RP, ad, bd, kIdesc, (j > 0 || kk > 0) ? 1u : 0u);
-                        else tc::mma_f16(tmem, ad, bd, kIdesc, (j > 0 || kk > 0 || h > 0) ? 1u : 0u);
+                    for (int p = 0; p < Cfg::kProducts; ++p) {
+                        const uint64_t ad = tc::smem_desc_sw128(st + kk * 2048, kBlock, 1024);
+                        const uint64_t bd =
+                            tc::smem_desc_sw128(st + Cfg::kU + p * (RP / 64) * kBlock + kk * 2048, kBlock, 1024);
+                        tc::mma_f16(tmem, ad, bd, kIdesc, (j > 0 || kk > 0 || p > 0) ? 1u : 0u);
                     }
                 tc::mma_commit(smem_u32(&sh.empty[s]));
             }
@@ -1010,37 +1141,38 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             }
         };
         constexpr int kCh = RP / 8;            // 8-column pieces per token
-        constexpr int kPer = 64 * kCh / kWgEpi;  // pieces per thread of a chunk
+        constexpr int kPer = kTok * kCh / kEpi;  // pieces per thread of a chunk
         auto piece_token = [&](int j, int i) {  // the token of this thread's piece i of chunk j, -1: none
-            const int at = pa + j * 64 + (et + i * kWgEpi) / kCh;
+            const int at = pa + j * kTok + (et + i * kEpi) / kCh;
             return at < pe ? g.v.order[at] : -1;
         };
         auto load_piece = [&](int tok, int i, float* x) {
             if (tok >= 0) {
-                load8(tok, (et + i * kWgEpi) % kCh * 8, x);
+                load8(tok, (et + i * kEpi) % kCh * 8, x);
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[e] = 0.f;
             }
         };
         // fp16: every rank's column has a factor of its own (the sums are taken column by column), from the
-        // largest magnitude among this CTA's tokens, eight pieces at a time (two memory latencies: with four
-        // at a time this took a third of the kernel). A thread's pieces are all of the same eight columns.
+        // largest magnitude among this CTA's tokens, eight (of eight warps four) pieces at a time (two memory
+        // latencies: with four of four warps this took a third of the kernel). A thread's pieces are all of the same eight columns.
         const int c8 = et % kCh * 8;
         float up[8];
         if (kF16) {
             float m[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) m[e] = 0.f;
-            for (int j = 0; j < nc * kPer; j += 8) {
-                int tok[8];
+            constexpr int kScan = kPWarps == 4 ? 8 : 4;
+            for (int j = 0; j < nc * kPer; j += kScan) {
+                int tok[kScan];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) tok[i] = piece_token((j + i) / kPer, (j + i) % kPer);
-                float x[8][8];
+                for (int i = 0; i < kScan; ++i) tok[i] = piece_token((j + i) / kPer, (j + i) % kPer);
+                float x[kScan][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) load_piece(tok[i], (j + i) % kPer, x[i]);
+                for (int i = 0; i < kScan; ++i) load_piece(tok[i], (j + i) % kPer, x[i]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < kScan; ++i)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {  // (infinities leave the others their scale)
                         const float y = fabsf(x[i][e]);
@@ -1053,12 +1185,14 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
                 for (int d = 16; d >= kCh; d >>= 1) m[e] = fmaxf(m[e], __shfl_xor_sync(0xffffffffu, m[e], d));
                 if (lane < kCh) sh.col_max[warp - 2][c8 + e] = m[e];
             }
-            named_barrier(1, kWgEpi);
+            named_barrier(1, kEpi);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float down;
-                pow2_scale(fmaxf(fmaxf(sh.col_max[0][c8 + e], sh.col_max[1][c8 + e]),
-                                 fmaxf(sh.col_max[2][c8 + e], sh.col_max[3][c8 + e])), up[e], down);
+                float most = sh.col_max[0][c8 + e];
+#pragma unroll
+                for (int v = 1; v < kPWarps; ++v) most = fmaxf(most, sh.col_max[v][c8 + e]);
+                pow2_scale(most, up[e], down);
                 if (et < kCh) sh.down[c8 + e] = down;
             }
         }
@@ -1067,11 +1201,9 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
         float x[kPer][8];
         int tok[kPer];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) tok[i] = nc > 0 ? piece_token(0, i) : -1;
+        for (int i = 0; i < kPer; ++i) load_piece(piece_token(0, i), i, x[i]);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) load_piece(tok[i], i, x[i]);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) tok[i] = nc > 1 ? piece_token(1, i) : -1;
+        for (int i = 0; i < kPer; ++i) tok[i] = piece_token(1, i);
         for (int j = 0; j < nc; ++j) {
             const int s = j % S;
             const uint32_t st = sbase + s * Cfg::kStage + Cfg::kU;
@@ -1083,16 +1215,17 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
             if (j >= S) wait(smem_u32(&sh.empty[s]), (j / S - 1) & 1u);
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const int at = (et + i * kWgEpi) / kCh, c = (et + i * kWgEpi) % kCh;
+                const int at = (et + i * kEpi) / kCh, c = (et + i * kEpi) % kCh;
                 if (kF16)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[i][e] *= up[e];
-                uint4 hi, lo;
-                split8<T>(x[i], hi, lo);
-                const uint32_t o = st + (c >> 3) * 8192;
-                st_shared_v4(o + tc::sw128_off(at, c & 7), hi);
-                if (RP <= 32) st_shared_v4(o + tc::sw128_off(at, 4 + c), lo);
-                else st_shared_v4(o + Cfg::kLo + tc::sw128_off(at, c & 7), lo);
+                uint4 part[kParts<T>];
+                split8<T>(x[i], part);
+#pragma unroll
+                for (int p = 0; p < kParts<T>; ++p) {
+                    const int col = p * kCh + c;
+                    st_shared_v4(st + (col >> 3) * kBlock + tc::sw128_off(at, col & 7), part[p]);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -1107,19 +1240,26 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
         tc::fence_after_sync();
         // partial sums [j][128 columns] over the ring, which nothing uses any more
         const int quarter = warp & 3, row = quarter * 32 + lane;
-        if (kF16) named_barrier(1, kWgEpi);  // the columns' factors are there
+        if (kF16) named_barrier(1, kEpi);  // the columns' factors are there
 #pragma unroll
-        for (int c = 0; c < RP / 16; ++c) {
+        for (int h = 0; h < RP / (4 * kPWarps); ++h) {
+            const int c = h * (kPWarps / 4) + ((warp - 2) >> 2);
             const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + c * 16;
             float y[16];
             if (nc > 0) {
-                tmem_load<16>(at, y);
-                if (kF16) {
-                    float l[16];
-                    tmem_load<16>(at + RP, l);
+                // the last part's sums first; fp16: the second part was 2^kLoShift times larger
+                constexpr int kSums = kParts<T> / Cfg::kProducts;
+                tmem_load<16>(at + (kSums - 1) * RP, y);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) y[i] = fmaf(l[i], 1.f / (1 << kLoShift), y[i]) * sh.down[c * 16 + i];
+                for (int p = kSums - 2; p >= 0; --p) {
+                    float h[16];
+                    tmem_load<16>(at + p * RP, h);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) y[i] = kF16 ? fmaf(y[i], 1.f / (1 << kLoShift), h[i]) : y[i] + h[i];
                 }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (kF16) y[i] *= sh.down[c * 16 + i];
             } else {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) y[i] = 0.f;
@@ -1142,7 +1282,7 @@ lora_wgrad_kernel(const WgArgs g, const __grid_constant__ CUtensorMap map_u0, co
         T* G = static_cast<T*>(w.G) + (int64_t)adapter * r * w.N;
         const int r8 = (r + 7) / 8, n8 = nx / 8;
         const int items = sh.failed ? 0 : (w.rank_minor ? nx * r8 : r * n8);
-        for (int i = tid; i < items; i += kWgThreads) {
+        for (int i = tid; i < items; i += Cfg::kThreads) {
             float y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) y[e] = 0.f;
@@ -1258,7 +1398,7 @@ cudaError_t allow_smem(K kern, uint32_t smem, bool (&done)[64]) {
 
 template <typename T, bool kBack, int RP>
 cudaError_t run_tiles(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) {
-    using Cfg = TileCfg<RP>;
+    using Cfg = TileCfg<T, RP>;
     static bool done[64];
     auto kern = lora_tile_kernel<T, kBack, RP>;
     cudaError_t e = allow_smem(kern, Cfg::kSmem, done);
@@ -1308,7 +1448,7 @@ cudaError_t run_tiles(const LoraArgs& a, const LoraPlanView& v, cudaStream_t s) 
 template <typename T, int RP>
 cudaError_t run_wgrad(const LoraWgradArgs* w, int nw, int32_t rank, const float* scale, float scale_all,
                       const LoraPlanView& v, bool early, cudaStream_t s) {
-    using Cfg = WgCfg<RP>;
+    using Cfg = WgCfg<T, RP>;
     static bool done[64];
     auto kern = lora_wgrad_kernel<T, RP>;
     cudaError_t e = allow_smem(kern, Cfg::kSmem, done);
@@ -1320,7 +1460,7 @@ cudaError_t run_wgrad(const LoraWgradArgs* w, int nw, int32_t rank, const float*
     for (int i = 0; i < nw; ++i) {
         g.w[i] = w[i];
         g.blocks[i] = (w[i].N + kWgCols - 1) / kWgCols;
-        if (!encode_rows(&mu[i], bf, w[i].U, v.tokens, w[i].N, w[i].ldu, 64) ||
+        if (!encode_rows(&mu[i], bf, w[i].U, v.tokens, w[i].N, w[i].ldu, Cfg::kTok) ||
             !encode_rows(&mg[i], bf, w[i].U, v.tokens, w[i].N, w[i].ldu, 1))
             return cudaErrorInvalidValue;
     }
@@ -1339,7 +1479,7 @@ cudaError_t run_wgrad(const LoraWgradArgs* w, int nw, int32_t rank, const float*
     const int64_t slots = (int64_t)device_props().sm_count * Cfg::kPerSm;
     while (c < 8 && items * c * 2 <= slots && (int64_t)v.tokens >= 64ll * c * 2) c *= 2;
     if (items * c > 0x7fffffffll) return cudaErrorInvalidValue;
-    return launch_clusters(kern, items, c, kWgThreads, Cfg::kSmem, s, g, mu[0], mg[0], mu[1], mg[1]);
+    return launch_clusters(kern, items, c, Cfg::kThreads, Cfg::kSmem, s, g, mu[0], mg[0], mu[1], mg[1]);
 }
 
 template <typename T>
