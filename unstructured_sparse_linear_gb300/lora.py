@@ -58,9 +58,10 @@ def _rows(t, name, rows, cols, dtype, device):
     return t.data_ptr(), ld
 
 
-def _writable(t, name):
-    """Refuses a caller's tensor whose values autograd believes to know: the kernels write through its address."""
-    if t.requires_grad and torch.is_grad_enabled():
+def _check_writable(t, name):
+    """For a caller's tensor that requires a gradient: autograd believes to know its values, and the kernels write
+    through its address."""
+    if torch.is_grad_enabled():
         raise RuntimeError(f"{name} is part of an autograd graph, which would not see that it is written (RosaLinear is "
                            "the differentiable form; under torch.no_grad() it may be written)")
 
@@ -159,15 +160,16 @@ def _weights(X, A, B, plan, scale):
     if not isinstance(X, torch.Tensor):
         raise TypeError("X must be a torch.Tensor")
     dt = X.dtype
-    if not X.is_cuda:
-        raise ValueError("X must be a CUDA tensor")
+    if X.device != dev:
+        if not X.is_cuda:
+            raise ValueError("X must be a CUDA tensor")
+        raise ValueError(f"X is on {X.device} and the plan on {dev}")
     if dt not in _DTYPE:
         raise ValueError(f"X dtype {dt} not in {list(_DTYPE)}")
-    if X.device != dev:
-        raise ValueError(f"X is on {X.device} and the plan on {dev}")
-    for name, w in (("A", A), ("B", B)):
-        if not (type(w) is torch.Tensor and w.dtype is dt and w.device == dev and w.is_contiguous()):
-            _req(w, name, dt, device=dev)  # (a Parameter, or what is wrong)
+    if not (type(A) is torch.Tensor and A.dtype is dt and A.device == dev and A.is_contiguous()):
+        _req(A, "A", dt, device=dev)  # (a Parameter, or what is wrong)
+    if not (type(B) is torch.Tensor and B.dtype is dt and B.device == dev and B.is_contiguous()):
+        _req(B, "B", dt, device=dev)
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError("A must be [adapters, rank, in] and B [adapters, out, rank]")
     n, rank, k = A.shape
@@ -212,7 +214,8 @@ def lora_add(X, A, B, plan: LoraPlan, base=None, scale=None, out=None, return_h:
         y, ldy = out.data_ptr(), n_out
     else:
         y, ldy = _rows(out, "out", T, n_out, dt, dev)
-        _writable(out, "out")
+        if out.requires_grad:
+            _check_writable(out, "out")
         given = True
     h = torch.empty((T, rank), dtype=torch.float32, device=dev) if return_h else None
     stream = _raw_stream(dev.index)
@@ -267,10 +270,11 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
         dA = _like(dA_out, A, "dA_out") if dA_out is not None else torch.empty_like(A)
     if need[2]:
         dB = _like(dB_out, B, "dB_out") if dB_out is not None else torch.empty_like(B)
-    given = [(t, name) for t, name, use in ((dX_out, "dX_out", need[0]), (dA_out, "dA_out", need[1]),
-                                            (dB_out, "dB_out", need[2])) if use and t is not None]
-    for t, name in given:
-        _writable(t, name)
+    given = [t for t, use in ((dX_out, need[0]), (dA_out, need[1]), (dB_out, need[2])) if use and t is not None] \
+        if dX_out is not None or dA_out is not None or dB_out is not None else ()
+    for t in given:
+        if t.requires_grad:
+            _check_writable(t, "dX_out" if t is dX_out else "dA_out" if t is dA_out else "dB_out")
     stream = _raw_stream(dev.index)
     ws, ws_ptr, size = plan._grad_scratch(rank, stream)
     st = lib.spops_lora_grad_block(_GRAD_ARGS(
@@ -279,6 +283,6 @@ def lora_grad(dY, X, A, B, plan: LoraPlan, scale=None, h=None, dX_base=None, dX_
         stream, s_all, _DTYPE[dt], T, k, n_out, rank, n))
     if st:
         _check(st, "lora_grad")
-    for t, _ in given:
+    for t in given:
         increment_version(t)
     return dX, dA, dB
