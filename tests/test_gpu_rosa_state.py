@@ -118,3 +118,14 @@ def test_copies_and_moves_give_the_same_bits(kind):
     layer.cpu().to(DEV)
     for a, b in zip(both_passes(layer), want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", ["sparse", "rosa", "low rank"])
+def test_an_empty_batch_trains(kind):
+    layer = layer_of() if kind == "low rank" else masked_layer(kind, 1)
+    k = 48 if kind == "low rank" else 192
+    X = torch.empty((k, 0) if kind == "sparse" else (0, k), device=DEV, dtype=BF16, requires_grad=True)
+    layer(X).sum().backward()
+    assert X.grad.shape == X.shape
+    for p in layer.parameters():
+        assert p.grad.shape == p.shape and not p.grad.any()

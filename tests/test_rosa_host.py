@@ -312,3 +312,14 @@ def test_a_factor_may_be_a_number_or_a_tensor_at_any_time():
     assert layer.scale == 0.5 and set(layer.state_dict()) == {"weight", "A", "B"}
     layer.scale = torch.ones(3)
     assert layer.to("meta").to_empty(device="cpu").scale.shape == (3,)
+
+
+def test_an_empty_batch_takes_any_strides(plain):
+    """Autograd's gradient of a sum is a broadcast number, which without a token counts as contiguous."""
+    from unstructured_sparse_linear_gb300.lora import _rows
+    cpu = torch.device("cpu")
+    for t in (torch.ones(()).expand(0, 96), torch.ones(96).expand(0, 96), torch.empty(96, 0).t()):
+        assert t.is_contiguous()
+        _rows(t, "dY", 0, 96, torch.float32, cpu)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        _rows(torch.ones(96).expand(2, 96), "dY", 2, 96, torch.float32, cpu)

@@ -53,7 +53,7 @@ def _rows(t, name, rows, cols, dtype, device):
     if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
         raise ValueError(f"{name} must be {rows} x {cols}, got {tuple(t.shape)}")
     ld, step = t.stride()
-    if (step != 1 and cols > 1) or (ld < cols and rows > 1):
+    if rows > 0 and ((step != 1 and cols > 1) or (ld < cols and rows > 1)):
         raise ValueError(f"{name} must have contiguous rows at least {cols} elements apart, got strides {(ld, step)}")
     return t.data_ptr(), ld
 
