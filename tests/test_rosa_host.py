@@ -323,3 +323,16 @@ def test_an_empty_batch_takes_any_strides(plain):
         _rows(t, "dY", 0, 96, torch.float32, cpu)
     with pytest.raises(ValueError, match="contiguous rows"):
         _rows(torch.ones(96).expand(2, 96), "dY", 2, 96, torch.float32, cpu)
+
+
+def test_factors_that_require_a_gradient_are_refused():
+    """They would get none."""
+    W = torch.randn(6, 4)
+    for factors in (torch.ones(3, requires_grad=True), torch.nn.Parameter(torch.ones(3))):
+        with pytest.raises(ValueError, match="not trained"):
+            sp.RosaLinear(W, 2, n_adapters=3, scale=factors)
+    layer = sp.RosaLinear(W, 2, n_adapters=3, scale=torch.ones(3))
+    with pytest.raises(ValueError, match="not trained"):
+        layer.scale = torch.ones(3, requires_grad=True)
+    layer.requires_grad_(True)  # (parameters only)
+    assert not layer.scale.requires_grad and torch.equal(layer.scale, torch.ones(3))

@@ -211,7 +211,7 @@ class RosaLinear(_MaskedLayer):
         self.out_features, self.in_features = weight.shape
         self.n_adapters = int(n_adapters)
         self.register_buffer("factors", None)
-        self.scale = scale
+        RosaLinear.scale.fset(self, scale)  # (a Parameter would be registered under that name)
         self.register_buffer("weight", weight)
         dev, dt = weight.device, weight.dtype
         self.A = torch.nn.Parameter(torch.randn(self.n_adapters, rank, self.in_features, device=dev, dtype=torch.float32)
@@ -236,6 +236,8 @@ class RosaLinear(_MaskedLayer):
     @scale.setter
     def scale(self, value):
         tensor = isinstance(value, torch.Tensor)
+        if tensor and value.requires_grad:
+            raise ValueError("scale requires a gradient, but the factors are not trained: they would get none")
         self.factors, self._factor = (value, None) if tensor else (None, value)
 
     def _apply(self, *args, **kwargs):
