@@ -533,12 +533,16 @@ cudaError_t launch_lora_wgrad_rows(int dt, const LoraWgradArgs* w, int nw, int32
 // adapter's weights for every 8 rows, the tensor-core one has about 13 us of latency (two phases
 // with an exchange between them) and reads the weights for every 128 rows, so for every adapter of
 // a mixed batch. Measured (bf16, us, general : tensor cores; adapters picked at random):
-//   forward, 4096 -> 4096, rank 16: 512 tokens of one adapter 11.0 : 13.0, 1024 16.9 : 13.0; of 8
-//   1024 tokens 17.3 : 28.1; of 48 1024 20.9 : 31.0; 2048 -> 8192, rank 64: 96 tokens of one adapter
-//   15.2 : 20.7, 128 22.6 : 21.0; of 8 256 24.2 : 23.7, 384 39 : 28; of 48 384 42.5 : 44.1, 512 71 : 44;
+//   forward, 4096 -> 4096, rank 16: 512 tokens of one adapter 10.8 : 12.6, 1024 16.5 : 12.8; of 8
+//   1024 tokens 16.6 : 28.2, 1536 27.7 : 28.4, 2048 27.9 : 30.7; of 48 1024 19.5 : 30.6, 2048 28.3 : 37.3; 2048 ->
+//   8192, rank 64: 96 tokens of one adapter 14.2 : 22.5, 128 22.8 : 22.3; of 8 256 24.4 : 25.4, 384 37.3 :
+//   28.3; of 48 384 39.5 : 49.7, 512 67.4 : 50.0;
 //   input gradient (whose general form reads B element by element): rank 16, 256 tokens of one adapter
-//   13.0 : 13.3, 384 20 : 13.4; of 8 256 15.0 : 17.3, 384 20.1 : 19.9; of 48 256 19.9 : 27.9, 384 30.8 :
-//   28.5; rank 64, 16 tokens 46 : 18.
+//   13.0 : 13.2, 384 19.9 : 13.3; of 8 256 14 : 17.2, 384 20.0 : 19.8; of 48 256 19.5 : 28.3, 384 32.2 :
+//   29.4; rank 64, 16 tokens 45 : 19.5.
+// An adapter's tokens in runs, which a plan's sizes do not tell, leave the general kernel's times as they are; the
+// tensor cores then take 15.2 for 8 adapters' 1024 tokens, 16.2 for 1536, 17.5 for 2048, and 27.0 for 2048 of 48. The
+// forward rule lies between the two: past it scattered tokens take up to 9 us more than they could, runs 11 less.
 static bool general_is_faster(bool back, const LoraArgs& a, const LoraPlanView& v) {
     const int64_t work = (int64_t)v.tokens * a.rank;
     if (back) return a.rank <= 32 && work <= 4096 + 192 * min64(v.n, 8);

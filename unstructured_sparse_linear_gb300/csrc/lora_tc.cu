@@ -40,7 +40,7 @@ __device__ __forceinline__ uint64_t evict_first_policy() {
 }
 
 // A box of a 2-D tensor. kHint: with the L2 policy (the neutral one is not free: 8192 tokens forward,
-// 2048 -> 8192, 61.4 us, 58.5 without).
+// 2048 -> 8192, 62.7 us, 60.4 without).
 template <bool kHint>
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
                                             uint64_t policy) {
@@ -416,8 +416,9 @@ struct TileCfg {
     static constexpr int kStages = (int)((kBudget - kTileBars - kH) / kStage);
     static constexpr uint32_t kSmem = kStages * kStage + kH + kTileBars;
     // bf16: parts of P that are operands in TMEM, from column kPartsAt on, RP / 2 columns each. In shared memory three
-    // would take a stage of the ring, and rank 128 be bound by their reads (8192 tokens, 2048 -> 8192: rank 64
-    // 78.5 us, rank 128 188). For rank 64 the first one is left there: two CTAs share the SM's TMEM.
+    // would take a stage of the ring (8192 tokens, 2048 -> 8192, rank 64: 78.5 us, 60.8 so; rank 128 takes 188 either
+    // way, for its 24 products per chunk: with two parts 148). For rank 64 the first one is left in shared memory: two
+    // CTAs share the SM's TMEM.
     static constexpr int kInTmem = kParts<T> == 2 ? 0 : RP == 64 ? 2 : 3;
     static constexpr uint32_t kPartsAt = RP > 64 ? 256 : 64;
     // P: columns 0 .. RP - 1; O: two buffers of 64 at 128 and 192
@@ -689,7 +690,7 @@ lora_tile_kernel(const TileArgs g, const __grid_constant__ TileMaps maps) {
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
         const int own = kLoraTile >> clog;  // rows that this rank sums: [crank * own, ...)
         // Tokens without an adapter, O = base, P = 0: first, while the loads for the first sums are
-        // under way (8192 tokens, 2048 -> 8192: 58.5 us, and 58.8 with them last).
+        // under way (1037 tokens of 24 adapters: 20.7 us, and 21.2 with them last).
         const bool copy = g.O && (g.O != g.base);
         if (copy || g.P) {
             for (int64_t pos = (int64_t)g.v.off[g.v.n] + blockIdx.x; pos < g.v.tokens; pos += gridDim.x) {

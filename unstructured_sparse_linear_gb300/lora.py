@@ -94,7 +94,8 @@ class Built:
 
 
 class LoraPlan(Built):
-    """Which tokens of a batch use which adapter, sorted; built by ``lora_plan``."""
+    """Which tokens of a batch use which adapter, sorted; built by ``lora_plan``. A captured graph holds the
+    plan's address and not the plan: keep it as long as the graph is replayed."""
 
     def __init__(self, buf: torch.Tensor, tokens: int, n_adapters: int):
         super().__init__(buf)
