@@ -388,6 +388,74 @@ typedef struct {
 } spops_lora_grad_args;
 SPOPS_API int spops_lora_grad_block(const spops_lora_grad_args* args);
 
+/* ---------------------------------------------------------------- 4-bit frozen weights */
+
+/* A frozen weight W (rows x cols, the projection X W^T) in microscaled 4-bit floating point: every 32 consecutive
+ * values of a row are a block, stored as 32 E2M1 codes (sign, two exponent bits, one mantissa bit: 0, .5, 1, 1.5, 2, 3,
+ * 4, 6) and one E8M0 scale byte b, the power of two 2^(b - 127) (255: NaN). value = code * scale.
+ *   codes  [rows, blocks, 16] bytes, blocks = ceil(cols / 32), two codes a byte, the first in the low four bits;
+ *          codes behind the last column are zero;
+ *   scales [rows, blocks] bytes.
+ * codes is 16-byte aligned. rows, cols and tokens are at most SPOPS_MX4_MAX_COUNT. */
+#define SPOPS_MX4_MAX_COUNT 0x7fff0000
+
+/* X (rows x cols, rows ldx elements apart) as codes and scales: b = 125 + floor(log2 of the block's largest
+ * magnitude), at least 0; a block of zeros has b = 0; each value is rounded to the nearest code (ties to the even
+ * one, beyond 6 to 6). Nothing in 4 bits stands for an infinity or a NaN: a block that holds one has b = 255 and is
+ * NaN as a whole. The outputs must not overlap X or each other. */
+SPOPS_API int spops_mx4_quantize(const void* X, int64_t ldx, int dtype, int32_t rows, int32_t cols, uint8_t* codes,
+                                 uint8_t* scales, void* stream);
+
+/* Y = the values (rows x cols, rows ldy elements apart), each rounded to dtype: exact but where it leaves the
+ * type's range. */
+SPOPS_API int spops_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t cols, void* Y,
+                                   int64_t ldy, int dtype, void* stream);
+
+/* Products of token-major activations with W, its values rounded to the activations' type (as spops_mx4_dequantize
+ * gives them), fp32 sums, rounded once. Rows of X and Y lie ldx and ldy elements apart (a slice of a fused projection's
+ * columns can be an operand). A token's result depends on no other token. Deterministic. Y must not overlap the other
+ * arrays. */
+typedef struct {
+    const void* X;
+    int64_t ldx;
+    const uint8_t *codes, *scales;
+    void* Y;
+    int64_t ldy;
+    void* stream;
+    int32_t dtype, tokens, rows, cols;
+} spops_mx4_args;
+
+/* Y [tokens, rows] = X [tokens, cols] W^T */
+SPOPS_API int spops_mx4_linear(const spops_mx4_args* args);
+
+/* The input gradient of spops_mx4_linear: Y [tokens, cols] = X [tokens, rows] W (X is the output's gradient). */
+SPOPS_API int spops_mx4_linear_grad(const spops_mx4_args* args);
+
+/* ---------------------------------------------------------------- dropout */
+
+/* Y = base + keep * X / (1 - q) for rows x cols matrices (base NULL: zeros), with the mask from a counter-based
+ * generator and stored nowhere: the same state gives the same mask, so the backward pass is the same call on the output's
+ * gradient. q = t / 65536 with t = floor(65536 p + 1/2). Column c of row r is kept where its 16-bit number is at
+ * least t; the numbers are those of Philox4x32 with 7 rounds (Salmon et al., 2011), key (seed mod 2^32, seed >> 32),
+ * counter (g mod 2^32, g >> 32, call mod 2^32, call >> 32) with g = r * ceil(cols / 8) + c / 8: number c % 8 of the
+ * four words' low and high halves in order. Strides and types change no mask. Sums in fp32, rounded once; what is dropped is
+ * zero whatever it was. 0 <= p <= 1; p = 1 drops all. state (device, 8-byte aligned) holds seed and call; NULL: the two
+ * host values are used. Y == X or Y == base (with the same row stride): in place; no other overlap. */
+typedef struct {
+    const void* X;
+    int64_t ldx;
+    const void* base;
+    int64_t ldb;
+    void* Y;
+    int64_t ldy;
+    const uint64_t* state;
+    uint64_t seed, call;
+    void* stream;
+    double p;
+    int32_t dtype, rows, cols;
+} spops_dropout_args;
+SPOPS_API int spops_dropout(const spops_dropout_args* args);
+
 /* ---------------------------------------------------------------- gradient norm, clipping */
 
 /* Bytes of a set of gradients. */

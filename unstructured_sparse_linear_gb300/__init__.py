@@ -11,8 +11,9 @@ section "Usage"):
 
 plus the row scheduler helpers ``sort_rows`` (builds row_idx) and ``row_bins``, and
 ``check_csr`` (device-side structure check); the low-rank half of the adapters (``lora_plan``,
-``lora_add``, ``lora_grad``); and clipping by the global gradient norm (``GradSet``,
-``grad_norm``, ``clip_grads``). Index lists are int16 (the README's type) or int32 (for matrices
+``lora_add``, ``lora_grad``); frozen weights in microscaled 4-bit floating point (``Mx4``, ``mx4_quantize``,
+``mx4_dequantize``, ``mx4_linear``, ``mx4_linear_grad``); dropout without a stored mask (``dropout``); and clipping by
+the global gradient norm (``GradSet``, ``grad_norm``, ``clip_grads``). Index lists are int16 (the README's type) or int32 (for matrices
 with more than 32768 rows or columns); row_offsets is int32. All inputs must be contiguous CUDA
 tensors on the same device (the low-rank calls' activations may be column slices).
 """
@@ -409,8 +410,11 @@ def masked_adam(param, exp_avg, exp_avg_sq, grad, step: int, lr: float = 1e-3, b
 __all__ += ["Transpose", "csr_transpose", "permute_values", "spmm_grad_b", "masked_adam"]
 
 from .lora import LoraPlan, lora_add, lora_grad, lora_plan  # noqa: E402  (use the functions above)
+from .mx4 import Mx4, mx4_dequantize, mx4_linear, mx4_linear_grad, mx4_quantize  # noqa: E402
+from .dropout import dropout  # noqa: E402
 from .clip import GradSet, clip_grads, grad_norm  # noqa: E402
 from .layer import RosaLinear, RosaLinearFunction, SparseLinear, SparseLinearFunction  # noqa: E402
 
-__all__ += ["LoraPlan", "lora_plan", "lora_add", "lora_grad", "GradSet", "grad_norm", "clip_grads",
+__all__ += ["LoraPlan", "lora_plan", "lora_add", "lora_grad", "Mx4", "mx4_quantize", "mx4_dequantize", "mx4_linear",
+            "mx4_linear_grad", "dropout", "GradSet", "grad_norm", "clip_grads",
             "SparseLinear", "SparseLinearFunction", "RosaLinear", "RosaLinearFunction"]

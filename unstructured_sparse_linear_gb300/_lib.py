@@ -58,6 +58,11 @@ SIGNATURES = {
     "spops_lora_grad": (_INT, [_P, _I64, _P, _I64, _P, _P, _P, _F32, _INT, _I32, _I32, _I32, _I32, _I32, _P, _P, _I64,
                                _P, _I64, _P, _P, _P, _P, _SZ, _P]),
     "spops_lora_grad_block": (_INT, [_P]),
+    "spops_mx4_quantize": (_INT, [_P, _I64, _INT, _I32, _I32, _P, _P, _P]),
+    "spops_mx4_dequantize": (_INT, [_P, _P, _I32, _I32, _P, _I64, _INT, _P]),
+    "spops_mx4_linear": (_INT, [_P]),
+    "spops_mx4_linear_grad": (_INT, [_P]),
+    "spops_dropout": (_INT, [_P]),
     "spops_grad_set_size": (_SZ, [_I32]),
     "spops_grad_set_build": (_INT, [_P, _P, _P, _P, _I32, _P, _SZ, ctypes.POINTER(_I64), ctypes.POINTER(_I32), _P]),
     "spops_grad_norm_workspace_size": (_SZ, []),

@@ -15,6 +15,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "lora.h"
+#include "mx4.h"
 #include "panel.h"
 #include "plan.h"
 
@@ -762,6 +763,117 @@ int spops_lora_grad_block(const spops_lora_grad_args* a) {
     return spops_lora_grad(a->dY, a->lddy, a->X, a->ldx, a->A, a->B, a->scale, a->scale_all, a->dtype, a->tokens,
                            a->in_features, a->out_features, a->rank, a->n_adapters, a->h, a->dX_base, a->ldb, a->dX,
                            a->lddx, a->dA, a->dB, a->plan, a->workspace, (size_t)a->ws_bytes, a->stream);
+}
+
+/* ---------------------------------------------------------------- 4-bit frozen weights, dropout */
+
+static int check_mx4(const uint8_t* codes, const uint8_t* scales, int dtype, int32_t rows, int32_t cols) {
+    if (dtype < SPOPS_F32 || dtype > SPOPS_BF16) return fail(SPOPS_ERR_INVALID_ARG, "dtype %d is not a spops_dtype", dtype);
+    if (rows < 0 || cols < 0) return fail(SPOPS_ERR_INVALID_ARG, "negative size (rows=%d cols=%d)", rows, cols);
+    if (rows > SPOPS_MX4_MAX_COUNT || cols > SPOPS_MX4_MAX_COUNT)
+        return fail(SPOPS_ERR_UNSUPPORTED, "%d rows and %d columns: more than %d", rows, cols, SPOPS_MX4_MAX_COUNT);
+    if (rows == 0 || cols == 0) return SPOPS_OK;
+    if (!codes || !scales) return fail(SPOPS_ERR_INVALID_ARG, "codes or scales is NULL");
+    if (!aligned(codes, 16)) return fail(SPOPS_ERR_INVALID_ARG, "codes is not 16-byte aligned");
+    return SPOPS_OK;
+}
+
+int spops_mx4_quantize(const void* X, int64_t ldx, int dtype, int32_t rows, int32_t cols, uint8_t* codes, uint8_t* scales,
+                       void* stream) {
+    int st = check_mx4(codes, scales, dtype, rows, cols);
+    if (st != SPOPS_OK) return st;
+    if (rows == 0 || cols == 0) return ok();
+    const size_t es = dtype_size(dtype), blocks = (size_t)rows * mx4_blocks(cols);
+    if (rows == 1) ldx = one_row(cols);
+    if ((st = check_rows("X", X, ldx, cols, rows, es)) != SPOPS_OK) return st;
+    const size_t xb = ((size_t)(rows - 1) * ldx + cols) * es;
+    if (overlaps(codes, blocks * 16, X, xb) || overlaps(scales, blocks, X, xb) || overlaps(codes, blocks * 16, scales, blocks))
+        return fail(SPOPS_ERR_INVALID_ARG, "codes or scales overlaps another array");
+    return cuda_status(launch_mx4_quantize(dtype, X, ldx, rows, cols, codes, scales, (cudaStream_t)stream),
+                       "mx4_quantize launch");
+}
+
+int spops_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t cols, void* Y, int64_t ldy,
+                         int dtype, void* stream) {
+    int st = check_mx4(codes, scales, dtype, rows, cols);
+    if (st != SPOPS_OK) return st;
+    if (rows == 0 || cols == 0) return ok();
+    const size_t es = dtype_size(dtype), blocks = (size_t)rows * mx4_blocks(cols);
+    if (rows == 1) ldy = one_row(cols);
+    if ((st = check_rows("Y", Y, ldy, cols, rows, es)) != SPOPS_OK) return st;
+    const size_t yb = ((size_t)(rows - 1) * ldy + cols) * es;
+    if (overlaps(Y, yb, codes, blocks * 16) || overlaps(Y, yb, scales, blocks))
+        return fail(SPOPS_ERR_INVALID_ARG, "Y overlaps codes or scales");
+    return cuda_status(launch_mx4_dequantize(dtype, codes, scales, rows, cols, Y, ldy, (cudaStream_t)stream),
+                       "mx4_dequantize launch");
+}
+
+static int mx4_product(const spops_mx4_args* a, bool back) {
+    if (!a) return fail(SPOPS_ERR_INVALID_ARG, "args is NULL");
+    int st = check_mx4(a->codes, a->scales, a->dtype, a->rows, a->cols);
+    if (st != SPOPS_OK) return st;
+    if (a->tokens < 0) return fail(SPOPS_ERR_INVALID_ARG, "negative number of tokens (%d)", a->tokens);
+    if (a->tokens > SPOPS_MX4_MAX_COUNT)
+        return fail(SPOPS_ERR_UNSUPPORTED, "%d tokens: more than %d", a->tokens, SPOPS_MX4_MAX_COUNT);
+    const int32_t in = back ? a->rows : a->cols, out = back ? a->cols : a->rows;
+    if (a->tokens == 0 || out == 0) return ok();
+    const size_t es = dtype_size(a->dtype), blocks = (size_t)a->rows * mx4_blocks(a->cols);
+    Mx4Args m;
+    m.ldx = a->tokens == 1 ? one_row(in) : a->ldx;  // one row: no stride is ever taken
+    m.ldy = a->tokens == 1 ? one_row(out) : a->ldy;
+    if (in > 0 && (st = check_rows("X", a->X, m.ldx, in, a->tokens, es)) != SPOPS_OK) return st;
+    if ((st = check_rows("Y", a->Y, m.ldy, out, a->tokens, es)) != SPOPS_OK) return st;
+    const size_t yb = ((size_t)(a->tokens - 1) * m.ldy + out) * es;
+    if ((in > 0 && rows_overlap(a->Y, m.ldy, out, a->X, m.ldx, in, a->tokens, es)) || overlaps(a->Y, yb, a->codes, blocks * 16) ||
+        overlaps(a->Y, yb, a->scales, blocks))
+        return fail(SPOPS_ERR_INVALID_ARG, "Y overlaps another array");
+    m.X = a->X;
+    m.codes = a->codes;
+    m.scales = a->scales;
+    m.Y = a->Y;
+    m.tokens = a->tokens;
+    m.rows = a->rows;
+    m.cols = a->cols;
+    return cuda_status(launch_mx4_product(a->dtype, back, m, (cudaStream_t)a->stream),
+                       back ? "mx4_linear_grad launch" : "mx4_linear launch");
+}
+
+int spops_mx4_linear(const spops_mx4_args* args) { return mx4_product(args, false); }
+int spops_mx4_linear_grad(const spops_mx4_args* args) { return mx4_product(args, true); }
+
+int spops_dropout(const spops_dropout_args* a) {
+    if (!a) return fail(SPOPS_ERR_INVALID_ARG, "args is NULL");
+    if (a->dtype < SPOPS_F32 || a->dtype > SPOPS_BF16)
+        return fail(SPOPS_ERR_INVALID_ARG, "dtype %d is not a spops_dtype", a->dtype);
+    if (a->rows < 0 || a->cols < 0) return fail(SPOPS_ERR_INVALID_ARG, "negative size (rows=%d cols=%d)", a->rows, a->cols);
+    if (!(a->p >= 0.0 && a->p <= 1.0)) return fail(SPOPS_ERR_INVALID_ARG, "p must lie in [0, 1] (got %g)", a->p);
+    if (a->state && !aligned(a->state, 8)) return fail(SPOPS_ERR_INVALID_ARG, "state is not 8-byte aligned");
+    if (a->rows == 0 || a->cols == 0) return ok();
+    const size_t es = dtype_size(a->dtype);
+    DropoutArgs d;
+    d.ldx = a->rows == 1 ? one_row(a->cols) : a->ldx;
+    d.ldb = a->rows == 1 ? one_row(a->cols) : a->ldb;
+    d.ldy = a->rows == 1 ? one_row(a->cols) : a->ldy;
+    int st = check_rows("X", a->X, d.ldx, a->cols, a->rows, es);
+    if (st == SPOPS_OK) st = check_rows("Y", a->Y, d.ldy, a->cols, a->rows, es);
+    if (st == SPOPS_OK && a->base) st = check_rows("base", a->base, d.ldb, a->cols, a->rows, es);
+    if (st != SPOPS_OK) return st;
+    if ((!(a->Y == a->X && d.ldy == d.ldx) && rows_overlap(a->Y, d.ldy, a->cols, a->X, d.ldx, a->cols, a->rows, es)) ||
+        (a->base && !(a->Y == a->base && d.ldy == d.ldb) &&
+         rows_overlap(a->Y, d.ldy, a->cols, a->base, d.ldb, a->cols, a->rows, es)))
+        return fail(SPOPS_ERR_INVALID_ARG, "Y overlaps X or base without being it");
+    if (overlaps(a->Y, ((size_t)(a->rows - 1) * d.ldy + a->cols) * es, a->state, 16))
+        return fail(SPOPS_ERR_INVALID_ARG, "Y overlaps state");
+    d.X = a->X;
+    d.base = a->base;
+    d.Y = a->Y;
+    d.state = a->state;
+    d.seed = a->seed;
+    d.call = a->call;
+    d.threshold = (uint32_t)std::floor(a->p * 65536.0 + 0.5);
+    d.rows = a->rows;
+    d.cols = a->cols;
+    return cuda_status(launch_dropout(a->dtype, d, (cudaStream_t)a->stream), "dropout launch");
 }
 
 /* ---------------------------------------------------------------- gradient norm and clipping */

@@ -1,0 +1,112 @@
+// Dropout from a counter-based generator, without a stored mask: Y = base + keep * X * 65536 / (65536 - threshold).
+//
+// Value c of row r is kept where its 16-bit number is not below the threshold. The numbers are those of Philox4x32 with
+// 7 rounds (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy as 1, 2, 3", 2011, where 7 rounds are the
+// fewest that pass all their tests): key = the seed, counter = (r * ceil(cols / 8) + c / 8, call), 128 bits a step,
+// number c % 8 of them. So the mask depends on neither strides, types nor launch shape, and the backward pass forms it
+// again from the same state.
+//
+// A step a thread: eight values. Sixteen bits a value make it one Philox (14 wide products) per eight; with 32 bits
+// the generator and not HBM would bound the kernel.
+#include "common.cuh"
+#include "internal.h"
+#include "mx4.h"
+
+namespace spops {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Numbers {
+    uint32_t w[4];
+};
+__device__ __forceinline__ Numbers philox7(uint64_t index, uint64_t call, uint64_t seed) {
+    uint32_t x0 = (uint32_t)index, x1 = (uint32_t)(index >> 32), x2 = (uint32_t)call, x3 = (uint32_t)(call >> 32);
+    uint32_t k0 = (uint32_t)seed, k1 = (uint32_t)(seed >> 32);
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+        const uint64_t a = (uint64_t)x0 * 0xD2511F53u, b = (uint64_t)x2 * 0xCD9E8D57u;
+        x0 = (uint32_t)(b >> 32) ^ x1 ^ k0;
+        x1 = (uint32_t)b;
+        x2 = (uint32_t)(a >> 32) ^ x3 ^ k1;
+        x3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return Numbers{{x0, x1, x2, x3}};
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&f)[8]) {
+    if (vec && n >= 8) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            Elt<T>::unpack(ld_v4(reinterpret_cast<const char*>(p) + 16 * i), f + i * Elt<T>::kVec);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = i < n ? Elt<T>::to_f(p[i]) : 0.f;
+    }
+}
+
+// groups: eights of a row. vec: every row of every operand begins on a 16-byte boundary.
+template <typename T, bool kBase>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutArgs g, int64_t rows, int64_t cols, int64_t groups,
+                                                           bool vec) {
+    pdl_trigger();
+    pdl_wait();
+    const uint64_t seed = g.state ? g.state[0] : g.seed, call = g.state ? g.state[1] : g.call;
+    const float factor = g.threshold < 65536u ? 65536.f / (float)(65536u - g.threshold) : 0.f;
+    const int64_t items = rows * groups, step = (int64_t)gridDim.x * kThreads;
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < items; i += step) {
+        const int64_t r = rows == 1 ? 0 : i / groups, c = (i - r * groups) * 8;
+        const int n = (int)min64(cols - c, 8);
+        float f[8], y[8];
+        load8(static_cast<const T*>(g.X) + r * g.ldx + c, n, vec, f);
+        if (kBase) load8(static_cast<const T*>(g.base) + r * g.ldb + c, n, vec, y);
+        const Numbers u = philox7((uint64_t)i, call, seed);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t number = e & 1 ? u.w[e / 2] >> 16 : u.w[e / 2] & 0xffffu;
+            const float kept = number >= g.threshold ? f[e] * factor : 0.f;  // (a dropped infinity or NaN is gone)
+            f[e] = kBase ? y[e] + kept : kept;
+        }
+        T* to = static_cast<T*>(g.Y) + r * g.ldy + c;
+        if (vec && n == 8) {
+#pragma unroll
+            for (int e = 0; e < (int)sizeof(T) / 2; ++e)
+                reinterpret_cast<uint4*>(to)[e] = Elt<T>::pack(f + e * Elt<T>::kVec);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) to[e] = Elt<T>::from_f(f[e]);
+        }
+    }
+}
+
+template <typename T>
+cudaError_t run(const DropoutArgs& a, cudaStream_t s) {
+    auto ok = [&](const void* p, int64_t ld) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.rows == 1 || ld * (int64_t)sizeof(T) % 16 == 0);
+    };
+    const bool vec = ok(a.X, a.ldx) && ok(a.Y, a.ldy) && (!a.base || ok(a.base, a.ldb));
+    int64_t rows = a.rows, cols = a.cols;
+    if (cols % 8 == 0 && a.ldx == cols && a.ldy == cols && (!a.base || a.ldb == cols)) {  // one long row
+        cols *= rows;
+        rows = 1;
+    }
+    const int64_t groups = (cols + 7) / 8, items = rows * groups;
+    const unsigned grid = (unsigned)min64((items + kThreads - 1) / kThreads, (int64_t)device_props().sm_count * 8);
+    count_launches(1);
+    return a.base ? launch_pdl(dropout_kernel<T, true>, dim3(grid), dim3(kThreads), 0, s, a, rows, cols, groups, vec)
+                  : launch_pdl(dropout_kernel<T, false>, dim3(grid), dim3(kThreads), 0, s, a, rows, cols, groups, vec);
+}
+
+}  // namespace
+
+cudaError_t launch_dropout(int dt, const DropoutArgs& a, cudaStream_t s) {
+    if (dt == kF32) return run<float>(a, s);
+    if (dt == kF16) return run<__half>(a, s);
+    return run<__nv_bfloat16>(a, s);
+}
+
+}  // namespace spops

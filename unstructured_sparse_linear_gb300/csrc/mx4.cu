@@ -1,0 +1,208 @@
+// Microscaled 4-bit weights: conversion from and to fp32, fp16 and bf16, and the choice between the products'
+// kernels.
+//
+// A block of 32 consecutive values of a row shares the scale 2^e, e = floor(log2 max|x|) - 2 (the exponent of the largest
+// value less that of 4, the grid's last power of two), and each value is rounded to the nearest of 0, .5, 1, 1.5, 2, 3,
+// 4, 6 times it (ties to the even mantissa, beyond 6 to 6).
+//
+// Both kernels stream: four lanes share a block, a lane has eight values (16 bytes of a 16-bit type, 4 bytes of codes),
+// and a warp four steps of 256 values, loaded before any is used, so that 64 bytes a lane are under way. Bound by HBM.
+#include "internal.h"
+#include "mx4.cuh"
+#include "mx4.h"
+
+namespace spops {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSteps = 4;  // of 256 values a warp
+
+// Rows as both kernels walk them: in steps of 256 values. A matrix of whole blocks in contiguous rows is one row.
+struct Walk {
+    int64_t rows, cols, steps, blocks;  // steps and blocks of a row
+};
+inline Walk make_walk(int64_t rows, int64_t cols, int64_t ld) {
+    Walk w{rows, cols, 0, 0};
+    if (rows == 1 || (cols % kMx4Block == 0 && ld == cols)) w = {1, rows * cols, 0, 0};
+    w.blocks = mx4_blocks(w.cols);
+    w.steps = (w.blocks + 7) / 8;
+    return w;
+}
+
+// Up to eight values from p on as fp32 (zeros behind the last). whole: all eight, on a 16-byte boundary.
+template <typename T>
+struct Raw {
+    uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load8(const T* p, int n, bool vec) {
+    Raw<T> r;
+    if (vec && n >= 8) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = ld_nc_v4(reinterpret_cast<const char*>(p) + 16 * i);
+    } else {
+        T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = i < n ? p[i] : Elt<T>::from_f(0.f);
+        memcpy(&r, e, sizeof(r));
+    }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw<T>& r, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) Elt<T>::unpack(r.v[i], f + i * Elt<T>::kVec);
+}
+
+// Two values as two codes, `lo` in the low bits.
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+    uint16_t r;
+    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b16 %0, {t, 0};\n\t}" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* X, int64_t ldx, Walk w, bool vec, uint32_t* codes,
+                                                                uint8_t* scales) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t items = w.rows * w.steps;
+    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+    const int64_t first = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    for (int64_t i0 = first; i0 < items; i0 += kSteps * warps) {
+        Raw<T> raw[kSteps];
+        int64_t at[kSteps];  // the lane's eight values among all of them, in eights
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int64_t i = i0 + u * warps;
+            at[u] = -1;
+            if (i < items) {
+                const int64_t row = w.rows == 1 ? 0 : i / w.steps, eight = (i - row * w.steps) * 32 + lane;
+                if (eight < w.blocks * 4) {
+                    const int64_t left = w.cols - eight * 8;
+                    raw[u] = load8(X + row * ldx + eight * 8, (int)min64(left, 8), vec);
+                    at[u] = row * w.blocks * 4 + eight;
+                }
+            }
+            if (at[u] < 0) raw[u] = Raw<T>{};
+        }
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            float f[8];
+            widen8(raw[u], f);
+            uint32_t m = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            // the exponent field less 2; a block that holds an infinity or a NaN (field 255) is NaN
+            const bool nan = m >= 0x7f800000u;
+            const uint32_t b = nan ? 255u : (uint32_t)max(0, (int)(m >> 23) - 2);
+            const float inv = nan ? 0.f : __uint_as_float((254u - b) << 23);  // 2^(127 - b), b <= 252
+            uint32_t c = 0;
+            if (!nan)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c |= encode2(f[2 * e] * inv, f[2 * e + 1] * inv) << (8 * e);
+            if (at[u] >= 0) {
+                codes[at[u]] = c;
+                if ((lane & 3) == 0) scales[at[u] >> 2] = (uint8_t)b;
+            }
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint32_t* codes, const uint8_t* scales, Walk w, T* Y,
+                                                                  int64_t ldy, bool vec) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t items = w.rows * w.steps;
+    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+    const int64_t first = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    for (int64_t i0 = first; i0 < items; i0 += kSteps * warps) {
+        uint32_t c[kSteps], b[kSteps];
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int64_t i = i0 + u * warps;
+            c[u] = b[u] = 0;
+            if (i < items) {
+                const int64_t row = w.rows == 1 ? 0 : i / w.steps, eight = (i - row * w.steps) * 32 + lane;
+                if (eight < w.blocks * 4) {
+                    c[u] = __ldg(codes + row * w.blocks * 4 + eight);
+                    b[u] = __ldg(scales + row * w.blocks + (eight >> 2));
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kSteps; ++u) {
+            const int64_t i = i0 + u * warps;
+            if (i >= items) break;
+            const int64_t row = w.rows == 1 ? 0 : i / w.steps, eight = (i - row * w.steps) * 32 + lane;
+            const int n = (int)min64(w.cols - eight * 8, 8);
+            if (n <= 0) continue;
+            const float s = mx4::scale_f32(b[u]);
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = mx4::value_f32(c[u] >> (4 * e), s);
+            T* to = Y + row * ldy + eight * 8;
+            if (vec && n == 8) {
+#pragma unroll
+                for (int e = 0; e < (int)sizeof(T) / 2; ++e)
+                    reinterpret_cast<uint4*>(to)[e] = Elt<T>::pack(f + e * Elt<T>::kVec);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n) to[e] = Elt<T>::from_f(f[e]);
+            }
+        }
+    }
+}
+
+unsigned walk_grid(const Walk& w) {
+    const int64_t items = w.rows * w.steps, per = (int64_t)(kThreads / 32) * kSteps;
+    return (unsigned)max64(1, min64((items + per - 1) / per, (int64_t)device_props().sm_count * 8));
+}
+
+template <typename T>
+cudaError_t quantize(const void* X, int64_t ldx, int32_t rows, int32_t cols, uint8_t* codes, uint8_t* scales,
+                     cudaStream_t s) {
+    const Walk w = make_walk(rows, cols, ldx);
+    const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && (w.rows == 1 || ldx * (int64_t)sizeof(T) % 16 == 0);
+    count_launches(1);
+    return launch_pdl(mx4_quantize_kernel<T>, dim3(walk_grid(w)), dim3(kThreads), 0, s, static_cast<const T*>(X), ldx, w,
+                      vec, reinterpret_cast<uint32_t*>(codes), scales);
+}
+
+template <typename T>
+cudaError_t dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t cols, void* Y, int64_t ldy,
+                       cudaStream_t s) {
+    const Walk w = make_walk(rows, cols, ldy);
+    const bool vec = reinterpret_cast<uintptr_t>(Y) % 16 == 0 && (w.rows == 1 || ldy * (int64_t)sizeof(T) % 16 == 0);
+    count_launches(1);
+    return launch_pdl(mx4_dequantize_kernel<T>, dim3(walk_grid(w)), dim3(kThreads), 0, s,
+                      reinterpret_cast<const uint32_t*>(codes), scales, w, static_cast<T*>(Y), ldy, vec);
+}
+
+}  // namespace
+
+cudaError_t launch_mx4_quantize(int dt, const void* X, int64_t ldx, int32_t rows, int32_t cols, uint8_t* codes,
+                                uint8_t* scales, cudaStream_t s) {
+    if (dt == kF32) return quantize<float>(X, ldx, rows, cols, codes, scales, s);
+    if (dt == kF16) return quantize<__half>(X, ldx, rows, cols, codes, scales, s);
+    return quantize<__nv_bfloat16>(X, ldx, rows, cols, codes, scales, s);
+}
+
+cudaError_t launch_mx4_dequantize(int dt, const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t cols,
+                                  void* Y, int64_t ldy, cudaStream_t s) {
+    if (dt == kF32) return dequantize<float>(codes, scales, rows, cols, Y, ldy, s);
+    if (dt == kF16) return dequantize<__half>(codes, scales, rows, cols, Y, ldy, s);
+    return dequantize<__nv_bfloat16>(codes, scales, rows, cols, Y, ldy, s);
+}
+
+cudaError_t launch_mx4_product(int dt, bool back, const Mx4Args& a, cudaStream_t s) {
+    return launch_mx4_general(dt, back, a, s);
+}
+
+}  // namespace spops
