@@ -202,6 +202,7 @@ cudaError_t launch_mx4_dequantize(int dt, const uint8_t* codes, const uint8_t* s
 }
 
 cudaError_t launch_mx4_product(int dt, bool back, const Mx4Args& a, cudaStream_t s) {
+    if (mx4_tiles_ok(dt, a)) return launch_mx4_tiles(dt, back, a, s);
     return launch_mx4_general(dt, back, a, s);
 }
 

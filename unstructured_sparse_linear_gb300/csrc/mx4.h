@@ -32,6 +32,10 @@ cudaError_t launch_mx4_dequantize(int dt, const uint8_t* codes, const uint8_t* s
 // General kernel: any type, size and alignment.
 cudaError_t launch_mx4_general(int dt, bool back, const Mx4Args& a, cudaStream_t s);
 
+// Tensor-core kernel (fp16 / bf16, rows of X and Y that begin on 16-byte boundaries).
+bool mx4_tiles_ok(int dt, const Mx4Args& a);
+cudaError_t launch_mx4_tiles(int dt, bool back, const Mx4Args& a, cudaStream_t s);
+
 // The dispatch between the kernels.
 cudaError_t launch_mx4_product(int dt, bool back, const Mx4Args& a, cudaStream_t s);
 

@@ -1,0 +1,432 @@
+// Products with a microscaled 4-bit weight on the tcgen05 tensor cores (fp16 / bf16, rows of 16 bytes).
+//
+// mx4_tile_kernel  Y[t, f] = sum over c of X[t, c] V(f, c), V = W (forward: f a row of W, c a column) or its transpose
+//                  (back: the input gradient).
+//
+// The weight is the A operand (128 features x 64 of the contraction, decoded from 4 bits to X's type by eight warps: exact),
+// X the B operand (nt tokens x 64, by TMA), so D is features x tokens. Two CTAs form a pair (cta_group::2): 256 features,
+// each CTA decodes its own 128 and holds half of the tokens' rows, so a value is decoded once per nt tokens and X is read
+// from L2 once per 256 features. Forward, a row's codes run along the contraction: the operand is K-major; back, they run
+// along the features: the same decoding writes an MN-major operand, and no code is ever transposed.
+#include <type_traits>
+
+#include "internal.h"
+#include "mx4.cuh"
+#include "mx4.h"
+#include "pipeline.cuh"
+
+namespace spops {
+namespace {
+
+// Warps 0 to 3 finish (a TMEM lane quarter each), 4 to 11 decode, 12 loads X, 13 multiplies.
+constexpr int kThreads = 448, kDecoders = 256, kLoadWarp = 12, kMmaWarp = 13;
+constexpr int kKC = 64;             // contraction elements of a stage: 128-byte rows
+constexpr int kFeatures = 128;      // of a CTA
+constexpr int kMaxTokens = 256;     // of a tile
+constexpr int kStages = 6;
+constexpr uint32_t kWBytes = kFeatures * 128, kXBytes = kMaxTokens / 2 * 128, kStage = kWBytes + kXBytes;
+constexpr int kOutTokens = 32;                              // of a store: 32 x 32 values
+constexpr uint32_t kOutBytes = kOutTokens * 32 * 2;
+constexpr uint32_t kOutAt = kStages * kStage, kBarsAt = kOutAt + 4 * 2 * kOutBytes;
+constexpr uint32_t kSmem = kBarsAt + 1024;
+constexpr int kAhead = 4;  // stages whose codes a decoder has under way
+
+// ------------------------------------------------------------------ PTX of CTA pairs
+
+__device__ __forceinline__ void pair_alloc(uint32_t smem_dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_dealloc(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// D (+)= A B^T over both CTAs of the pair, issued by a thread of the even one.
+__device__ __forceinline__ void pair_mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on the barrier at this address in the CTAs of `mask` once all products issued so far are complete.
+__device__ __forceinline__ void pair_commit(uint32_t bar, uint32_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)mask)
+        : "memory");
+}
+// A box of a 2-D tensor into this CTA's shared memory; its bytes are counted on a barrier of the pair (cluster address).
+__device__ __forceinline__ void pair_tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+struct TileArgs {
+    const uint8_t* codes;
+    const uint8_t* scales;
+    void* Y;
+    int64_t ldy;
+    int64_t blocks;  // of a row of W
+    int64_t tiles;   // ftiles x token tiles
+    int32_t rows, F, tokens, ftiles, chunks, nt;
+    uint32_t idesc;
+    int* err;
+};
+
+// A tile's place: 256 features x nt tokens; the tiles of the same tokens follow each other.
+struct Place {
+    int f0, t0;
+};
+__device__ __forceinline__ Place place_of(const TileArgs& g, int64_t tile, int half) {
+    const int64_t tt = tile / g.ftiles;
+    return {(int)(tile - tt * g.ftiles) * (2 * kFeatures) + half * kFeatures, (int)(tt * g.nt)};
+}
+
+// A cluster is one pair, or S pairs that split a tile's contraction; in the second case (one tile per cluster) the fp32
+// partial sums meet in shared memory and are added in the order of the splits.
+template <typename T, bool kBack>
+__global__ void __launch_bounds__(kThreads, 1)
+mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_y) {
+    // No static shared memory, so the dynamic part starts on the 1 KB boundary that the swizzled tiles need (checked).
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    struct Shared {
+        uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+        uint32_t tmem;
+        volatile int failed;
+    };
+    static_assert(sizeof(Shared) <= kSmem - kBarsAt, "barriers");
+    Shared& sh = *reinterpret_cast<Shared*>(smem_raw + kBarsAt);
+    const uint32_t sbase = smem_u32(smem_raw);
+    if (sbase & 1023u) {  // the same on every CTA
+        record_error(g.err, kDevErrSmemAlign);
+        return;
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int C = (int)cluster_size(), crank = (int)cluster_rank();
+    const int half = crank & 1, lead = crank & ~1, split = crank >> 1, splits = C >> 1;
+    const int64_t cid = blockIdx.x / C, ncl = gridDim.x / C;
+    const int c0 = (int)((int64_t)g.chunks * split / splits), c1 = (int)((int64_t)g.chunks * (split + 1) / splits);
+    const int per = c1 - c0;                                               // chunks of a tile
+    const int64_t mine = cid < g.tiles ? (g.tiles - cid + ncl - 1) / ncl : 0;  // tiles of this cluster
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 2 * kDecoders / 32 + 1);  // decoding warps of the pair, the loader
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.acc_full[i]), 1);
+            mbar_init(smem_u32(&sh.acc_empty[i]), 2 * 4);  // finishing warps of the pair
+        }
+        sh.failed = 0;
+        fence_mbar_init();
+    }
+    if (tid == 32 * kLoadWarp) {
+        tma_prefetch_map(&map_x);
+        tma_prefetch_map(&map_y);
+    }
+    __syncthreads();
+    pdl_wait();
+    if (warp == kMmaWarp) pair_alloc(smem_u32(&sh.tmem), 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();
+    tc::fence_after_sync();
+    pdl_trigger();
+    const uint32_t tmem = sh.tmem;
+    const Waits wait{&sh.failed, g.err};
+
+    if (warp == kLoadWarp) {
+        if (lane == 0) {
+            uint32_t s = 0, ph = 1;
+            for (int64_t i = 0; i < mine; ++i) {
+                const Place at = place_of(g, cid + i * ncl, half);
+                for (int c = c0; c < c1; ++c) {
+                    if (wait.cluster(smem_u32(&sh.empty[s]), ph)) {
+                        const uint32_t bar = smem_u32(&sh.full[s]);
+                        if (half == 0) mbar_arrive_expect_tx(bar, (uint32_t)g.nt * 128);  // both halves
+                        pair_tma_load_2d(sbase + s * kStage + kWBytes, &map_x, c * kKC, at.t0 + half * (g.nt / 2),
+                                         cluster_map(bar, lead));
+                    }
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        if (lane == 0 && half == 0) {
+            const uint32_t mask = 3u << lead;
+            const uint64_t a0 = kBack ? tc::smem_desc_sw128(sbase, 8192, 1024) : tc::smem_desc_sw128(sbase, 0, 1024);
+            const uint64_t b0 = tc::smem_desc_sw128(sbase + kWBytes, 0, 1024);
+            constexpr uint32_t kStepA = kBack ? 2048 / 16 : 32 / 16, kStepB = 32 / 16;  // 16 of the contraction
+            uint32_t s = 0, ph = 0;
+            for (int64_t i = 0; i < mine; ++i) {
+                const uint32_t buf = (uint32_t)i & 1u, d = tmem + buf * kMaxTokens;
+                bool ok = wait.cluster(smem_u32(&sh.acc_empty[buf]), (uint32_t)((i >> 1) & 1) ^ 1u);
+                tc::fence_after_sync();
+                for (int c = 0; c < per; ++c) {
+                    ok = ok && wait.cluster(smem_u32(&sh.full[s]), ph);
+                    if (ok) {
+                        tc::fence_after_sync();
+                        const uint32_t off = s * (kStage / 16);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            pair_mma_f16(d, a0 + off + k * kStepA, b0 + off + k * kStepB, g.idesc, c > 0 || k > 0);
+                        pair_commit(smem_u32(&sh.empty[s]), mask);
+                    }
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+                if (ok) pair_commit(smem_u32(&sh.acc_full[buf]), mask);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // A block of 32 values a thread and chunk. Forward: 128 rows x 2 blocks; back: 64 rows x 4 blocks, whose two
+        // 64-feature halves are operand blocks of their own.
+        const int id = tid - 128, sub = id & 1;
+        const int r = kBack ? (id >> 1) & 63 : id >> 1;
+        const uint32_t to = (kBack ? (uint32_t)(id >> 7) * 8192u : 0u) + (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u;
+        uint4 code[kAhead];
+        uint32_t byte[kAhead];
+        int64_t ai = 0;  // the next block to ask for
+        int ac = c0;
+        int64_t row0 = 0, blk0 = 0;
+        auto aim = [&]() {
+            const Place at = place_of(g, cid + ai * ncl, half);
+            row0 = kBack ? r : at.f0 + r;
+            blk0 = kBack ? at.f0 / kMx4Block + (id >> 7) * 2 + sub : sub;
+        };
+        if (mine > 0) aim();
+        auto ask = [&](uint4& w, uint32_t& b) {
+            w = make_uint4(0, 0, 0, 0);
+            b = 0;
+            if (ai >= mine) return;
+            const int64_t row = kBack ? row0 + (int64_t)ac * kKC : row0, blk = kBack ? blk0 : blk0 + 2 * (int64_t)ac;
+            if (row < g.rows && blk < g.blocks) {
+                w = ld_nc_v4(g.codes + (row * g.blocks + blk) * 16);
+                b = __ldg(g.scales + row * g.blocks + blk);
+            }
+            if (++ac == c1) {
+                ac = c0;
+                if (++ai < mine) aim();
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) ask(code[u], byte[u]);
+        uint32_t s = 0, ph = 1;
+        const int64_t total = mine * per;
+        for (int64_t it = 0; it < total; it += kAhead) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (it + u >= total) break;
+                const uint32_t w[4] = {code[u].x, code[u].y, code[u].z, code[u].w}, b = byte[u];
+                uint4 v[4];
+                if (b <= mx4::kPlain) {
+                    const uint32_t f = mx4::factor2<T>(b);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t o[4];
+                        mx4::decode8<T>(w[k], f, o);
+                        v[k] = make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] = mx4::decode8_large<T>(w[k], b);
+                }
+                ask(code[u], byte[u]);
+                if (wait.cluster(smem_u32(&sh.empty[s]), ph)) {
+                    const uint32_t base = sbase + s * kStage + to;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) st_shared_v4(base + (((uint32_t)(4 * sub + k) ^ (uint32_t)(r & 7)) << 4), v[k]);
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0 && !sh.failed) mbar_arrive_remote(smem_u32(&sh.full[s]), lead);
+                __syncwarp();
+                if (++s == kStages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+    } else {
+        uint32_t stores = 0;
+        for (int64_t i = 0; i < mine; ++i) {
+            const Place at = place_of(g, cid + i * ncl, half);
+            const uint32_t buf = (uint32_t)i & 1u;
+            const bool ok = wait.cluster(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1));
+            const bool all = __all_sync(0xffffffffu, ok);
+            tc::fence_after_sync();
+            const int f = at.f0 + warp * 32;
+            const int live = min(g.nt, g.tokens - at.t0);
+            if (all)
+                for (int c = 0; c < live; c += kOutTokens) {
+                    float y[32];
+                    tmem_load<32>(tmem + ((uint32_t)warp << 21) + buf * kMaxTokens + c, y);
+                    if (splits > 1) {  // [token][128 features], fp32
+                        const uint32_t p = sbase + (uint32_t)(c * kFeatures + warp * 32 + lane) * 4;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            asm volatile("st.shared.f32 [%0], %1;" ::"r"(p + e * kFeatures * 4), "f"(y[e]) : "memory");
+                    } else if (f < g.F) {
+                        const uint32_t st = sbase + kOutAt + (uint32_t)(warp * 2 + (stores & 1)) * kOutBytes;
+                        if (lane == 0) bulk_wait_read<1>();  // the store before the last has left this buffer
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const T t = Elt<T>::from_f(y[e]);
+                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(st + e * 64 + lane * 2),
+                                         "h"(reinterpret_cast<const uint16_t&>(t))
+                                         : "memory");
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&map_y, f, at.t0 + c, st);
+                            bulk_commit();
+                        }
+                        ++stores;
+                    }
+                }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(smem_u32(&sh.acc_empty[buf]), lead);
+            __syncwarp();
+        }
+        if (lane == 0) bulk_wait<0>();
+        __syncwarp();
+    }
+    if (splits > 1) {
+        cluster_sync();
+        const Place at = place_of(g, cid, half);
+        const int n = (g.nt + splits - 1) / splits, t0 = split * n;  // this CTA's tokens of the tile
+        const int live = min(g.nt, g.tokens - at.t0);
+        if (!sh.failed && mine > 0)
+            for (int i = tid; i < n * (kFeatures / 4); i += kThreads) {
+                const int t = t0 + i / (kFeatures / 4), x = i % (kFeatures / 4) * 4, f = at.f0 + x;
+                if (t >= live || t >= t0 + n || f >= g.F) continue;
+                float y[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < splits; ++j) {
+                    const uint32_t from = cluster_map(sbase + (uint32_t)(t * kFeatures + x) * 4, 2 * j + half);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] += __uint_as_float(ld_cluster_u32(from + 4 * e));
+                }
+                T* out = static_cast<T*>(g.Y) + (int64_t)(at.t0 + t) * g.ldy + f;
+                if (f + 4 <= g.F) {  // (rows begin on 16-byte boundaries)
+                    T v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = Elt<T>::from_f(y[e]);
+                    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(v);
+                } else {
+                    for (int e = 0; f + e < g.F; ++e) out[e] = Elt<T>::from_f(y[e]);
+                }
+            }
+    }
+    if (sh.failed)  // copies and products that are still in flight
+        for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < kDrainNs;) {
+        }
+    tc::fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // the pair's products are done, nobody reads this CTA's memory any more
+    if (warp == kMmaWarp) pair_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ host side
+
+// Map of a row-strided matrix of 16-bit elements in boxes of box_cols x box_rows, with the 128-byte swizzle or without.
+bool encode_matrix(CUtensorMap* map, bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_cols,
+                   int box_rows, bool swizzle) {
+    const cuuint64_t d[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, st[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, elem[2] = {1, 1};
+    return encode_fn()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+                       const_cast<void*>(p), d, st, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                       swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tokens per tile and splits of the contraction with the least estimated time, in cycles: a chunk takes its products
+// (2 nt cycles) or its decoding (about 300), whichever is longer.
+struct Shape {
+    int nt, splits;
+};
+Shape choose(int64_t tokens, int64_t ftiles, int chunks, int sms) {
+    Shape best{kMaxTokens, 1};
+    double least = 1e300;
+    for (int nt = 32; nt <= kMaxTokens; nt += 32)
+        for (int s = 1; s <= 4 && s <= chunks; ++s) {
+            const int64_t tiles = ftiles * ((tokens + nt - 1) / nt), at_once = sms / (2 * s);
+            const int64_t waves = (tiles + at_once - 1) / at_once;
+            const double chunk = 2 * nt > 300 ? 2 * nt : 300, steps = (chunks + s - 1) / s;
+            const double t = waves * (steps * chunk + (s > 1 ? 1500.0 : 300.0)) + 3000 + 12.0 * nt;
+            if (t < least) {
+                least = t;
+                best = {nt, s};
+            }
+        }
+    return best;
+}
+
+template <typename T, bool kBack>
+cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
+    static bool done[64];
+    auto kern = mx4_tile_kernel<T, kBack>;
+    cudaError_t e = allow_smem(kern, kSmem, done);
+    if (e != cudaSuccess) return e;
+    constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+    const int32_t F = kBack ? a.cols : a.rows, C = kBack ? a.rows : a.cols;
+    TileArgs g;
+    g.codes = a.codes;
+    g.scales = a.scales;
+    g.Y = a.Y;
+    g.ldy = a.ldy;
+    g.blocks = mx4_blocks(a.cols);
+    g.rows = a.rows;
+    g.F = F;
+    g.tokens = a.tokens;
+    g.ftiles = (int32_t)(((int64_t)F + 2 * kFeatures - 1) / (2 * kFeatures));
+    g.chunks = (int32_t)(((int64_t)C + kKC - 1) / kKC);
+    const int sms = device_props().sm_count;
+    const Shape shape = choose(a.tokens, g.ftiles, g.chunks, sms);
+    g.nt = shape.nt;
+    g.tiles = (int64_t)g.ftiles * (((int64_t)a.tokens + shape.nt - 1) / shape.nt);
+    g.idesc = tc::instr_desc_f16(bf ? 1u : 0u, kBack ? 1u : 0u, 0u, 2 * kFeatures, (uint32_t)shape.nt);
+    g.err = device_error_word();
+    CUtensorMap mx, my;
+    if (!encode_matrix(&mx, bf, a.X, a.tokens, C, a.ldx, kKC, shape.nt / 2, true) ||
+        !encode_matrix(&my, bf, a.Y, a.tokens, F, a.ldy, 32, kOutTokens, false))
+        return cudaErrorInvalidValue;
+    const int c = 2 * shape.splits;
+    const int64_t clusters = shape.splits > 1 ? g.tiles : min64(g.tiles, max64(1, sms / 2));
+    if (clusters * c > 0x7fffffffll) return cudaErrorInvalidValue;
+    count_launches(1);
+    return launch_pdl_cluster(kern, dim3((unsigned)(clusters * c)), dim3(kThreads), kSmem, (unsigned)c, s, g, mx, my);
+}
+
+}  // namespace
+
+bool mx4_tiles_ok(int dt, const Mx4Args& a) {
+    auto rows_ok = [](const void* p, int64_t ld) {
+        return ld % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld < (1ll << 38);
+    };
+    // (TMA stores whole 16-byte granules of a row)
+    return dt != kF32 && a.rows > 0 && a.cols > 0 && a.rows % 8 == 0 && a.cols % 8 == 0 && encode_fn() &&
+           rows_ok(a.X, a.ldx) && rows_ok(a.Y, a.ldy);
+}
+
+cudaError_t launch_mx4_tiles(int dt, bool back, const Mx4Args& a, cudaStream_t s) {
+    if (dt == kF16) return back ? run_tiles<__half, true>(a, s) : run_tiles<__half, false>(a, s);
+    return back ? run_tiles<__nv_bfloat16, true>(a, s) : run_tiles<__nv_bfloat16, false>(a, s);
+}
+
+}  // namespace spops
