@@ -68,12 +68,16 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t factor, uint32_t (&
 
 // The same for scales above kPlain (values from 2 on, infinities and NaN), by way of fp32.
 template <typename T>
-__device__ __noinline__ uint4 decode8_large(uint32_t w, uint32_t b) {
+__device__ __forceinline__ void decode8_large(uint32_t w, uint32_t b, uint32_t (&o)[4]) {
     const float s = scale_f32(b);
     float f[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = value_f32(w >> (4 * j), s);
-    return Elt<T>::pack(f);
+    const uint4 v = Elt<T>::pack(f);
+    o[0] = v.x;
+    o[1] = v.y;
+    o[2] = v.z;
+    o[3] = v.w;
 }
 
 }  // namespace mx4

@@ -18,8 +18,8 @@
 namespace spops {
 namespace {
 
-// Warps 0 to 3 finish (a TMEM lane quarter each), 4 to 11 decode, 12 loads X, 13 multiplies.
-constexpr int kThreads = 448, kDecoders = 256, kLoadWarp = 12, kMmaWarp = 13;
+// Warps 0 to 3 finish (a TMEM lane quarter each), then kGroups groups of four decode, one warp loads X, one multiplies.
+constexpr int kGroups = 5, kLoadWarp = 4 + 4 * kGroups, kMmaWarp = kLoadWarp + 1, kThreads = 32 * (kMmaWarp + 1);
 constexpr int kKC = 64;             // contraction elements of a stage: 128-byte rows
 constexpr int kFeatures = 128;      // of a CTA
 constexpr int kMaxTokens = 256;     // of a tile
@@ -29,7 +29,8 @@ constexpr int kOutTokens = 32;                              // of a store: 32 x 
 constexpr uint32_t kOutBytes = kOutTokens * 32 * 2;
 constexpr uint32_t kOutAt = kStages * kStage, kBarsAt = kOutAt + 4 * 2 * kOutBytes;
 constexpr uint32_t kSmem = kBarsAt + 1024;
-constexpr int kAhead = 4;  // stages whose codes a decoder has under way
+constexpr int kAhead = 1;  // chunks whose codes a decoder has under way
+static_assert(kGroups < kStages, "a group's next chunk is less than one round of the ring away");
 
 // ------------------------------------------------------------------ PTX of CTA pairs
 
@@ -67,6 +68,16 @@ __device__ __forceinline__ void pair_tma_load_2d(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// Arrive on a barrier of the pair (its cluster address); this CTA's shared memory is then as its warp left it.
+__device__ __forceinline__ void pair_arrive(uint32_t bar) {
+    cluster_release_smem();
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// What the pair wrote to its shared memory before the messages that were waited for.
+__device__ __forceinline__ void acquire_pair_smem() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+
 struct TileArgs {
     const uint8_t* codes;
     const uint8_t* scales;
@@ -86,6 +97,38 @@ struct Place {
 __device__ __forceinline__ Place place_of(const TileArgs& g, int64_t tile, int half) {
     const int64_t tt = tile / g.ftiles;
     return {(int)(tile - tt * g.ftiles) * (2 * kFeatures) + half * kFeatures, (int)(tt * g.nt)};
+}
+
+// Waits of a pair. What the barriers announce is read by the tensor core and by TMA or lies in TMEM, so no wait makes
+// the thread's own loads see another CTA's memory: an acquire of the cluster's scope empties the SM's L1 each time
+// (8192 tokens, 2048 -> 8192: TBD1 us against TBD2).
+struct PairWaits {
+    volatile int* failed;
+    int* err;
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+            "mov.u32 n, 256;\n"
+            "AGAIN_%=:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "@p bra DONE_%=;\n\t"
+            "sub.u32 n, n, 1;\n\t"
+            "setp.ne.u32 q, n, 0;\n\t"
+            "@q bra AGAIN_%=;\n"
+            "DONE_%=:\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "n"(kMbarPollNs)
+            : "memory");
+        return done || Waits{failed, err}(bar, parity);  // (with the time limit)
+    }
+};
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 // A cluster is one pair, or S pairs that split a tile's contraction; in the second case (one tile per cluster) the fp32
@@ -116,7 +159,7 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
     const int64_t mine = cid < g.tiles ? (g.tiles - cid + ncl - 1) / ncl : 0;  // tiles of this cluster
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 2 * kDecoders / 32 + 1);  // decoding warps of the pair, the loader
+            mbar_init(smem_u32(&sh.full[i]), 2 * 4 + 1);  // decoding warps of the pair, the loader
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -139,7 +182,7 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
     tc::fence_after_sync();
     pdl_trigger();
     const uint32_t tmem = sh.tmem;
-    const Waits wait{&sh.failed, g.err};
+    const PairWaits wait{&sh.failed, g.err};
 
     if (warp == kLoadWarp) {
         if (lane == 0) {
@@ -147,7 +190,7 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
             for (int64_t i = 0; i < mine; ++i) {
                 const Place at = place_of(g, cid + i * ncl, half);
                 for (int c = c0; c < c1; ++c) {
-                    if (wait.cluster(smem_u32(&sh.empty[s]), ph)) {
+                    if (wait(smem_u32(&sh.empty[s]), ph)) {
                         const uint32_t bar = smem_u32(&sh.full[s]);
                         if (half == 0) mbar_arrive_expect_tx(bar, (uint32_t)g.nt * 128);  // both halves
                         pair_tma_load_2d(sbase + s * kStage + kWBytes, &map_x, c * kKC, at.t0 + half * (g.nt / 2),
@@ -162,100 +205,143 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        if (lane == 0 && half == 0) {
+        // The whole warp walks the chunks and one thread issues: what the products take then lies in uniform registers (a
+        // loop of one thread took 650 cycles a chunk, more than its products). A wait that has run out of time is not
+        // looked at: the products of whatever is there end, and the error is recorded.
+        if (half == 0) {
             const uint32_t mask = 3u << lead;
             const uint64_t a0 = kBack ? tc::smem_desc_sw128(sbase, 8192, 1024) : tc::smem_desc_sw128(sbase, 0, 1024);
             const uint64_t b0 = tc::smem_desc_sw128(sbase + kWBytes, 0, 1024);
             constexpr uint32_t kStepA = kBack ? 2048 / 16 : 32 / 16, kStepB = 32 / 16;  // 16 of the contraction
-            uint32_t s = 0, ph = 0;
+            const bool issues = elect_one();
+            uint32_t s = 0, ph = 0, buf = 0, acc_ph = 1;
             for (int64_t i = 0; i < mine; ++i) {
-                const uint32_t buf = (uint32_t)i & 1u, d = tmem + buf * kMaxTokens;
-                bool ok = wait.cluster(smem_u32(&sh.acc_empty[buf]), (uint32_t)((i >> 1) & 1) ^ 1u);
+                const uint32_t d = tmem + buf * kMaxTokens;
+                wait(smem_u32(&sh.acc_empty[buf]), acc_ph);
                 tc::fence_after_sync();
                 for (int c = 0; c < per; ++c) {
-                    ok = ok && wait.cluster(smem_u32(&sh.full[s]), ph);
-                    if (ok) {
-                        tc::fence_after_sync();
+                    wait(smem_u32(&sh.full[s]), ph);
+                    acquire_pair_smem();
+                    tc::fence_after_sync();
+                    if (issues) {
                         const uint32_t off = s * (kStage / 16);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             pair_mma_f16(d, a0 + off + k * kStepA, b0 + off + k * kStepB, g.idesc, c > 0 || k > 0);
                         pair_commit(smem_u32(&sh.empty[s]), mask);
                     }
+                    __syncwarp();
                     if (++s == kStages) {
                         s = 0;
                         ph ^= 1;
                     }
                 }
-                if (ok) pair_commit(smem_u32(&sh.acc_full[buf]), mask);
+                if (issues) pair_commit(smem_u32(&sh.acc_full[buf]), mask);
+                __syncwarp();
+                buf ^= 1;
+                acc_ph ^= buf ^ 1;
             }
         }
         __syncwarp();
     } else if (warp >= 4) {
-        // A block of 32 values a thread and chunk. Forward: 128 rows x 2 blocks; back: 64 rows x 4 blocks, whose two
-        // 64-feature halves are operand blocks of their own.
-        const int id = tid - 128, sub = id & 1;
-        const int r = kBack ? (id >> 1) & 63 : id >> 1;
-        const uint32_t to = (kBack ? (uint32_t)(id >> 7) * 8192u : 0u) + (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u;
-        uint4 code[kAhead];
-        uint32_t byte[kAhead];
-        int64_t ai = 0;  // the next block to ask for
-        int ac = c0;
-        int64_t row0 = 0, blk0 = 0;
+        // A group of four warps takes every kGroups-th chunk, so that the steps of one chunk (codes that arrive, decoding,
+        // the stores' fence, the message) overlap with those of others. A thread has two blocks of a chunk. Forward: rows
+        // r and r + 64, block `sub` of two; back: row r, block `sub` of both 64-feature halves, which are operand blocks of
+        // their own.
+        const int id = tid & 127, sub = id & 1, r = id >> 1, group = (warp - 4) >> 2;
+        const uint32_t to = sbase + (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u;
+        const uint32_t flip = (uint32_t)(4 * sub ^ (r & 7)) << 4;  // the first 16 bytes' place in their row; the others: ^ k
+        const uint32_t full = cluster_map(smem_u32(&sh.full[0]), lead);
+        // The next chunk to ask for: number ac of tile ai. A thread's blocks lie at pc and pc + second; pos counts what may
+        // end within a chunk (forward: blocks of the row; back: rows).
+        const int64_t second = kBack ? 2 : 64 * g.blocks;
+        const int64_t step = kBack ? (int64_t)kGroups * kKC * g.blocks : kGroups * 2;
+        const int64_t end = kBack ? g.rows : g.blocks;
+        int64_t ai = 0, pos = 0;
+        int ac = group;
+        const uint8_t *pc = g.codes, *ps = g.scales;
+        bool in0 = false, in1 = false;
         auto aim = [&]() {
+            while (ac >= per) {
+                ac -= per;
+                ++ai;
+            }
+            if (ai >= mine) {
+                in0 = in1 = false;
+                return;
+            }
             const Place at = place_of(g, cid + ai * ncl, half);
-            row0 = kBack ? r : at.f0 + r;
-            blk0 = kBack ? at.f0 / kMx4Block + (id >> 7) * 2 + sub : sub;
+            const int64_t c = c0 + ac;
+            const int64_t row = kBack ? c * kKC + r : at.f0 + r, blk = kBack ? at.f0 / kMx4Block + sub : 2 * c + sub;
+            pos = kBack ? row : blk;
+            in0 = kBack ? blk < g.blocks : row < g.rows;
+            in1 = kBack ? blk + 2 < g.blocks : row + 64 < g.rows;
+            pc = g.codes + (row * g.blocks + blk) * 16;
+            ps = g.scales + row * g.blocks + blk;
         };
-        if (mine > 0) aim();
-        auto ask = [&](uint4& w, uint32_t& b) {
-            w = make_uint4(0, 0, 0, 0);
-            b = 0;
-            if (ai >= mine) return;
-            const int64_t row = kBack ? row0 + (int64_t)ac * kKC : row0, blk = kBack ? blk0 : blk0 + 2 * (int64_t)ac;
-            if (row < g.rows && blk < g.blocks) {
-                w = ld_nc_v4(g.codes + (row * g.blocks + blk) * 16);
-                b = __ldg(g.scales + row * g.blocks + blk);
-            }
-            if (++ac == c1) {
-                ac = c0;
-                if (++ai < mine) aim();
-            }
+        aim();
+        struct Blocks {
+            uint4 w[2];
+            uint32_t b[2];
         };
+        auto ask = [&](Blocks& k) {
+            k.w[0] = k.w[1] = make_uint4(0, 0, 0, 0);
+            k.b[0] = k.b[1] = 0;
+            const bool in = pos < end;
+            if (in && in0) {
+                k.w[0] = ld_nc_v4(pc);
+                k.b[0] = __ldg(ps);
+            }
+            if (in && in1) {
+                k.w[1] = ld_nc_v4(pc + second * 16);
+                k.b[1] = __ldg(ps + second);
+            }
+            ac += kGroups;
+            pos += kBack ? kGroups * kKC : kGroups * 2;
+            pc += step * 16;
+            ps += step;
+            if (ac >= per) aim();
+        };
+        Blocks next[kAhead];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) ask(code[u], byte[u]);
-        uint32_t s = 0, ph = 1;
-        const int64_t total = mine * per;
-        for (int64_t it = 0; it < total; it += kAhead) {
+        for (int u = 0; u < kAhead; ++u) ask(next[u]);
+        uint32_t s = group, ph = 1;
+        for (int64_t left = mine * per - group; left > 0; left -= kGroups * kAhead) {
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
-                if (it + u >= total) break;
-                const uint32_t w[4] = {code[u].x, code[u].y, code[u].z, code[u].w}, b = byte[u];
-                uint4 v[4];
-                if (b <= mx4::kPlain) {
-                    const uint32_t f = mx4::factor2<T>(b);
+                if (left <= u * kGroups) break;
+                const bool ok = wait(smem_u32(&sh.empty[s]), ph);
+                if (ok) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t o[4];
-                        mx4::decode8<T>(w[k], f, o);
-                        v[k] = make_uint4(o[0], o[1], o[2], o[3]);
+                    for (int x = 0; x < 2; ++x) {
+                        const uint32_t w[4] = {next[u].w[x].x, next[u].w[x].y, next[u].w[x].z, next[u].w[x].w}, b = next[u].b[x];
+                        const uint32_t at = to + s * kStage + x * 8192u;
+                        if (b <= mx4::kPlain) {
+                            const uint32_t f = mx4::factor2<T>(b);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t v[4];
+                                mx4::decode8<T>(w[k], f, v);
+                                st_shared_v4(at + (flip ^ (uint32_t)(k << 4)), make_uint4(v[0], v[1], v[2], v[3]));
+                            }
+                        } else {
+#pragma unroll 1
+                            for (int k = 0; k < 4; ++k) {
+                                uint32_t v[4];
+                                mx4::decode8_large<T>(k == 0 ? w[0] : k == 1 ? w[1] : k == 2 ? w[2] : w[3], b, v);
+                                st_shared_v4(at + (flip ^ (uint32_t)(k << 4)), make_uint4(v[0], v[1], v[2], v[3]));
+                            }
+                        }
                     }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] = mx4::decode8_large<T>(w[k], b);
-                }
-                ask(code[u], byte[u]);
-                if (wait.cluster(smem_u32(&sh.empty[s]), ph)) {
-                    const uint32_t base = sbase + s * kStage + to;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) st_shared_v4(base + (((uint32_t)(4 * sub + k) ^ (uint32_t)(r & 7)) << 4), v[k]);
                     fence_proxy_async_smem();
                 }
+                ask(next[u]);
                 __syncwarp();
-                if (lane == 0 && !sh.failed) mbar_arrive_remote(smem_u32(&sh.full[s]), lead);
+                if (lane == 0 && ok) pair_arrive(full + s * 8);
                 __syncwarp();
-                if (++s == kStages) {
-                    s = 0;
+                s += kGroups;
+                if (s >= kStages) {
+                    s -= kStages;
                     ph ^= 1;
                 }
             }
@@ -265,7 +351,7 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
         for (int64_t i = 0; i < mine; ++i) {
             const Place at = place_of(g, cid + i * ncl, half);
             const uint32_t buf = (uint32_t)i & 1u;
-            const bool ok = wait.cluster(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1));
+            const bool ok = wait(smem_u32(&sh.acc_full[buf]), (uint32_t)((i >> 1) & 1));
             const bool all = __all_sync(0xffffffffu, ok);
             tc::fence_after_sync();
             const int f = at.f0 + warp * 32;
@@ -324,12 +410,11 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                 }
                 T* out = static_cast<T*>(g.Y) + (int64_t)(at.t0 + t) * g.ldy + f;
                 if (f + 4 <= g.F) {  // (rows begin on 16-byte boundaries)
-                    T v[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = Elt<T>::from_f(y[e]);
-                    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(v);
+                    *reinterpret_cast<uint2*>(out) = make_uint2(Elt<T>::p2(y[0], y[1]), Elt<T>::p2(y[2], y[3]));
                 } else {
-                    for (int e = 0; f + e < g.F; ++e) out[e] = Elt<T>::from_f(y[e]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (f + e < g.F) out[e] = Elt<T>::from_f(y[e]);
                 }
             }
     }
