@@ -23,14 +23,15 @@ constexpr int kGroups = 5, kLoadWarp = 4 + 4 * kGroups, kMmaWarp = kLoadWarp + 1
 constexpr int kKC = 64;             // contraction elements of a stage: 128-byte rows
 constexpr int kFeatures = 128;      // of a CTA
 constexpr int kMaxTokens = 256;     // of a tile
-constexpr int kStages = 6;
-constexpr uint32_t kWBytes = kFeatures * 128, kXBytes = kMaxTokens / 2 * 128, kStage = kWBytes + kXBytes;
+// A stage: 128 features and nt / 2 tokens, 128 bytes each; as many as fit.
+constexpr uint32_t kWBytes = kFeatures * 128, kRing = 6 * (kWBytes + kMaxTokens / 2 * 128);
+constexpr int kMinStages = 6, kMaxStages = 10;
 constexpr int kOutTokens = 32;                              // of a store: 32 x 32 values
 constexpr uint32_t kOutBytes = kOutTokens * 32 * 2;
-constexpr uint32_t kOutAt = kStages * kStage, kBarsAt = kOutAt + 4 * 2 * kOutBytes;
+constexpr uint32_t kOutAt = kRing, kBarsAt = kOutAt + 4 * 2 * kOutBytes;
 constexpr uint32_t kSmem = kBarsAt + 1024;
 constexpr int kAhead = 1;  // chunks whose codes a decoder has under way
-static_assert(kGroups < kStages, "a group's next chunk is less than one round of the ring away");
+static_assert(kGroups < kMinStages, "a group's next chunk is less than one round of the ring away");
 
 // ------------------------------------------------------------------ PTX of CTA pairs
 
@@ -85,7 +86,7 @@ struct TileArgs {
     int64_t ldy;
     int64_t blocks;  // of a row of W
     int64_t tiles;   // ftiles x token tiles
-    int32_t rows, F, tokens, ftiles, chunks, nt;
+    int32_t rows, F, tokens, ftiles, chunks, nt, stages;
     uint32_t idesc;
     int* err;
 };
@@ -139,7 +140,7 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
     // No static shared memory, so the dynamic part starts on the 1 KB boundary that the swizzled tiles need (checked).
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     struct Shared {
-        uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+        uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
         uint32_t tmem;
         volatile int failed;
     };
@@ -151,6 +152,7 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t stages = g.stages, stage_bytes = kWBytes + (uint32_t)g.nt * 64;
     const int C = (int)cluster_size(), crank = (int)cluster_rank();
     const int half = crank & 1, lead = crank & ~1, split = crank >> 1, splits = C >> 1;
     const int64_t cid = blockIdx.x / C, ncl = gridDim.x / C;
@@ -158,7 +160,7 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
     const int per = c1 - c0;                                               // chunks of a tile
     const int64_t mine = cid < g.tiles ? (g.tiles - cid + ncl - 1) / ncl : 0;  // tiles of this cluster
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 2 * 4 + 1);  // decoding warps of the pair, the loader
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
@@ -193,10 +195,10 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                     if (wait(smem_u32(&sh.empty[s]), ph)) {
                         const uint32_t bar = smem_u32(&sh.full[s]);
                         if (half == 0) mbar_arrive_expect_tx(bar, (uint32_t)g.nt * 128);  // both halves
-                        pair_tma_load_2d(sbase + s * kStage + kWBytes, &map_x, c * kKC, at.t0 + half * (g.nt / 2),
+                        pair_tma_load_2d(sbase + s * stage_bytes + kWBytes, &map_x, c * kKC, at.t0 + half * (g.nt / 2),
                                          cluster_map(bar, lead));
                     }
-                    if (++s == kStages) {
+                    if (++s == stages) {
                         s = 0;
                         ph ^= 1;
                     }
@@ -224,14 +226,14 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                     acquire_pair_smem();
                     tc::fence_after_sync();
                     if (issues) {
-                        const uint32_t off = s * (kStage / 16);
+                        const uint32_t off = s * (stage_bytes / 16);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             pair_mma_f16(d, a0 + off + k * kStepA, b0 + off + k * kStepB, g.idesc, c > 0 || k > 0);
                         pair_commit(smem_u32(&sh.empty[s]), mask);
                     }
                     __syncwarp();
-                    if (++s == kStages) {
+                    if (++s == stages) {
                         s = 0;
                         ph ^= 1;
                     }
@@ -315,9 +317,9 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         const uint32_t w[4] = {next[u].w[x].x, next[u].w[x].y, next[u].w[x].z, next[u].w[x].w}, b = next[u].b[x];
-                        const uint32_t at = to + s * kStage + x * 8192u;
-                        if (b <= mx4::kPlain) {
-                            const uint32_t f = mx4::factor2<T>(b);
+                        const uint32_t at = to + s * stage_bytes + x * 8192u;
+                        if (mx4::plain(b) || (b != 255 && (w[0] | w[1] | w[2] | w[3]) == 0)) {  // (or nothing but zeros)
+                            const uint32_t f = mx4::plain(b) ? mx4::factor2(b) : 0;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 uint32_t v[4];
@@ -328,20 +330,20 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
 #pragma unroll 1
                             for (int k = 0; k < 4; ++k) {
                                 uint32_t v[4];
-                                mx4::decode8_large<T>(k == 0 ? w[0] : k == 1 ? w[1] : k == 2 ? w[2] : w[3], b, v);
+                                mx4::decode8_any<T>(k == 0 ? w[0] : k == 1 ? w[1] : k == 2 ? w[2] : w[3], b, v);
                                 st_shared_v4(at + (flip ^ (uint32_t)(k << 4)), make_uint4(v[0], v[1], v[2], v[3]));
                             }
                         }
                     }
                     fence_proxy_async_smem();
                 }
-                ask(next[u]);
                 __syncwarp();
                 if (lane == 0 && ok) pair_arrive(full + s * 8);
                 __syncwarp();
+                ask(next[u]);  // (behind the message, which the multiplying warp waits for)
                 s += kGroups;
-                if (s >= kStages) {
-                    s -= kStages;
+                if (s >= stages) {
+                    s -= stages;
                     ph ^= 1;
                 }
             }
@@ -404,9 +406,11 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                 if (t >= live || t >= t0 + n || f >= g.F) continue;
                 float y[4] = {0.f, 0.f, 0.f, 0.f};
                 for (int j = 0; j < splits; ++j) {
-                    const uint32_t from = cluster_map(sbase + (uint32_t)(t * kFeatures + x) * 4, 2 * j + half);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] += __uint_as_float(ld_cluster_u32(from + 4 * e));
+                    const float4 p = ld_cluster_f4(cluster_map(sbase + (uint32_t)(t * kFeatures + x) * 4, 2 * j + half));
+                    y[0] += p.x;
+                    y[1] += p.y;
+                    y[2] += p.z;
+                    y[3] += p.w;
                 }
                 T* out = static_cast<T*>(g.Y) + (int64_t)(at.t0 + t) * g.ldy + f;
                 if (f + 4 <= g.F) {  // (rows begin on 16-byte boundaries)
@@ -484,6 +488,7 @@ cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
     const int sms = device_props().sm_count;
     const Shape shape = choose(a.tokens, g.ftiles, g.chunks, sms);
     g.nt = shape.nt;
+    g.stages = min((int)(kRing / (kWBytes + shape.nt * 64)), kMaxStages);
     g.tiles = (int64_t)g.ftiles * (((int64_t)a.tokens + shape.nt - 1) / shape.nt);
     g.idesc = tc::instr_desc_f16(bf ? 1u : 0u, kBack ? 1u : 0u, 0u, 2 * kFeatures, (uint32_t)shape.nt);
     g.err = device_error_word();

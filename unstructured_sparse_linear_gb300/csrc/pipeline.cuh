@@ -43,6 +43,15 @@ __device__ __forceinline__ bool mbar_try_cluster(uint32_t bar, uint32_t parity) 
     return done != 0;
 }
 
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
 // Waits of one CTA. After one has run out of time (2 s) every later one of the CTA gives up at
 // once, so that a kernel whose copy never arrives ends; the roles then skip their work but keep
 // their loops, which hold barriers.
