@@ -42,8 +42,8 @@ def test_reference_quantization_by_hand():
 
 def product(lib, back=False, **kw):
     from unstructured_sparse_linear_gb300 import mx4
-    a = dict(X=0x100000, ldx=64, codes=0x200000, scales=0x300000, Y=0x400000, ldy=64, stream=0, dtype=2, tokens=8, rows=64,
-             cols=64)
+    a = dict(X=0x100000, ldx=64, codes=0x200000, scales=0x300000, Y=0x400000, ldy=64, ws=0, size=0, stream=0, dtype=2,
+             tokens=8, rows=64, cols=64)
     a.update(kw)
     f = lib.spops_mx4_linear_grad if back else lib.spops_mx4_linear
     return f(mx4._ARGS(*a.values()))
@@ -58,6 +58,13 @@ def test_product_refusals(lib, back):
                 dict(ldy=63), dict(Y=0x100000), dict(Y=0x100040), dict(Y=0x200000), dict(Y=0x300010)):
         assert product(lib, back, **bad) == 1, bad
         assert lib.spops_last_error()
+    odd = dict(X=0x100002, tokens=20, ldx=72, ldy=72)  # rows that need a copy
+    need = lib.spops_mx4_workspace_size(20, 64, 64)
+    assert need >= 2 * 20 * 64 * 2
+    for bad in (dict(), dict(ws=0x500000, size=need - 1), dict(ws=0x500008, size=need)):
+        assert product(lib, back, **odd, **bad) == 3, bad
+    for bad in (0x400040, 0x100040, 0x200000, 0x300010):
+        assert product(lib, back, **odd, ws=bad, size=need) == 1
     big = 0x7fff0001
     assert product(lib, back, tokens=big) == 2 and product(lib, back, rows=big) == 2 and product(lib, back, cols=big) == 2
 

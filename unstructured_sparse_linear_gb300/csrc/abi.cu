@@ -808,6 +808,12 @@ int spops_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t ro
                        "mx4_dequantize launch");
 }
 
+size_t spops_mx4_workspace_size(int32_t tokens, int32_t in_features, int32_t out_features) {
+    if (tokens < 0 || in_features < 0 || out_features < 0) return 0;
+    const size_t n = mx4_copy_bytes(tokens, in_features) + mx4_copy_bytes(tokens, out_features);
+    return n > 16 ? n : 16;
+}
+
 static int mx4_product(const spops_mx4_args* a, bool back) {
     if (!a) return fail(SPOPS_ERR_INVALID_ARG, "args is NULL");
     int st = check_mx4(a->codes, a->scales, a->dtype, a->rows, a->cols);
@@ -834,7 +840,16 @@ static int mx4_product(const spops_mx4_args* a, bool back) {
     m.tokens = a->tokens;
     m.rows = a->rows;
     m.cols = a->cols;
-    return cuda_status(launch_mx4_product(a->dtype, back, m, (cudaStream_t)a->stream),
+    if (mx4_needs_copies(a->dtype, back, m)) {
+        const size_t need = spops_mx4_workspace_size(a->tokens, in, out);
+        if (!a->workspace || !aligned(a->workspace, 16) || a->ws_bytes < need)
+            return fail(SPOPS_ERR_WORKSPACE, "rows that are no whole aligned 16 bytes need a 16-byte aligned workspace of %zu bytes (got %zu)",
+                        need, (size_t)a->ws_bytes);
+        if (overlaps(a->workspace, need, a->Y, yb) || overlaps(a->workspace, need, a->X, ((size_t)(a->tokens - 1) * m.ldx + in) * es) ||
+            overlaps(a->workspace, need, a->codes, blocks * 16) || overlaps(a->workspace, need, a->scales, blocks))
+            return fail(SPOPS_ERR_INVALID_ARG, "workspace overlaps another array");
+    }
+    return cuda_status(launch_mx4_product(a->dtype, back, m, a->workspace, (cudaStream_t)a->stream),
                        back ? "mx4_linear_grad launch" : "mx4_linear launch");
 }
 

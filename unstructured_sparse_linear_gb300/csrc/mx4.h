@@ -29,15 +29,28 @@ cudaError_t launch_mx4_quantize(int dt, const void* X, int64_t ldx, int32_t rows
 cudaError_t launch_mx4_dequantize(int dt, const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t cols,
                                   void* Y, int64_t ldy, cudaStream_t s);
 
-// General kernel: any type, size and alignment.
-cudaError_t launch_mx4_general(int dt, bool back, const Mx4Args& a, cudaStream_t s);
+// fp32, any size and alignment, on the CUDA cores.
+cudaError_t launch_mx4_general(bool back, const Mx4Args& a, cudaStream_t s);
 
-// Tensor-core kernel (fp16 / bf16, rows of X and Y that begin on 16-byte boundaries).
-bool mx4_tiles_ok(int dt, const Mx4Args& a);
+// fp16 / bf16. Forward for one token, and for up to eight (any alignment):
+cudaError_t launch_mx4_vec(int dt, const Mx4Args& a, cudaStream_t s);
+cudaError_t launch_mx4_rows(int dt, const Mx4Args& a, cudaStream_t s);
+// On the tcgen05 tensor cores, where mx4_tile_rows holds for X and Y.
 cudaError_t launch_mx4_tiles(int dt, bool back, const Mx4Args& a, cudaStream_t s);
 
-// The dispatch between the kernels.
-cudaError_t launch_mx4_product(int dt, bool back, const Mx4Args& a, cudaStream_t s);
+// Rows of 16-bit values as TMA loads and stores them: rows and addresses on 16-byte boundaries, whole 16 bytes (a store
+// writes no less).
+inline bool mx4_tile_rows(const void* p, int64_t ld, int64_t cols) {
+    return cols % 8 == 0 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld < (1ll << 38);
+}
+// Bytes of copies of X [tokens, in] and Y [tokens, out] with such rows.
+inline size_t mx4_copy_bytes(int64_t tokens, int64_t cols) {
+    return ((size_t)tokens * (size_t)((cols + 7) / 8 * 8) * 2 + 255) / 256 * 256;
+}
+
+// The dispatch between the kernels. workspace: for the operands that need a copy (mx4_needs_copies).
+bool mx4_needs_copies(int dt, bool back, const Mx4Args& a);
+cudaError_t launch_mx4_product(int dt, bool back, const Mx4Args& a, void* workspace, cudaStream_t s);
 
 // dropout.cu: Y = base + keep * X * factor. state (device, two words) replaces seed and call.
 struct DropoutArgs {

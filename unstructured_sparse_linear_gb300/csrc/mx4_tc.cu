@@ -473,6 +473,7 @@ cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
     cudaError_t e = allow_smem(kern, kSmem, done);
     if (e != cudaSuccess) return e;
     constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+    if (!encode_fn()) return cudaErrorNotSupported;
     const int32_t F = kBack ? a.cols : a.rows, C = kBack ? a.rows : a.cols;
     TileArgs g;
     g.codes = a.codes;
@@ -493,8 +494,10 @@ cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
     g.idesc = tc::instr_desc_f16(bf ? 1u : 0u, kBack ? 1u : 0u, 0u, 2 * kFeatures, (uint32_t)shape.nt);
     g.err = device_error_word();
     CUtensorMap mx, my;
-    if (!encode_matrix(&mx, bf, a.X, a.tokens, C, a.ldx, kKC, shape.nt / 2, true) ||
-        !encode_matrix(&my, bf, a.Y, a.tokens, F, a.ldy, 32, kOutTokens, false))
+    // (copies of operands whose rows were no whole 16 bytes have zeros, or room, behind their columns)
+    const int64_t C8 = ((int64_t)C + 7) / 8 * 8, F8 = ((int64_t)F + 7) / 8 * 8;
+    if (!encode_matrix(&mx, bf, a.X, a.tokens, C8, a.ldx, kKC, shape.nt / 2, true) ||
+        !encode_matrix(&my, bf, a.Y, a.tokens, F8, a.ldy, 32, kOutTokens, false))
         return cudaErrorInvalidValue;
     const int c = 2 * shape.splits;
     const int64_t clusters = shape.splits > 1 ? g.tiles : min64(g.tiles, max64(1, sms / 2));
@@ -504,15 +507,6 @@ cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
 }
 
 }  // namespace
-
-bool mx4_tiles_ok(int dt, const Mx4Args& a) {
-    auto rows_ok = [](const void* p, int64_t ld) {
-        return ld % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld < (1ll << 38);
-    };
-    // (TMA stores whole 16-byte granules of a row)
-    return dt != kF32 && a.rows > 0 && a.cols > 0 && a.rows % 8 == 0 && a.cols % 8 == 0 && encode_fn() &&
-           rows_ok(a.X, a.ldx) && rows_ok(a.Y, a.ldy);
-}
 
 cudaError_t launch_mx4_tiles(int dt, bool back, const Mx4Args& a, cudaStream_t s) {
     if (dt == kF16) return back ? run_tiles<__half, true>(a, s) : run_tiles<__half, false>(a, s);

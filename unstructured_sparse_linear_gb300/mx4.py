@@ -24,7 +24,7 @@ __all__ = ["Mx4", "mx4_quantize", "mx4_dequantize", "mx4_linear", "mx4_linear_gr
 
 BLOCK = 32
 _MAX_COUNT = 0x7fff0000  # SPOPS_MX4_MAX_COUNT
-_ARGS = struct.Struct("7q4i").pack  # spops_mx4_args
+_ARGS = struct.Struct("9q4i").pack  # spops_mx4_args
 
 
 class Mx4:
@@ -157,8 +157,14 @@ def _product(X, W, out, back, name):
         out = torch.empty((tokens, n_out), dtype=dt, device=dev)
         y, ldy = out.data_ptr(), n_out
     lib = _L()
+    ws, size = 0, 0
+    if (x | y | 2 * ldx | 2 * ldy) & 15 or (n_in | n_out) & 7:  # rows that the tensor cores' kernel gets copies of
+        size = lib.spops_mx4_workspace_size(tokens, n_in, n_out)
+        scratch = torch.empty(size, dtype=torch.uint8, device=dev)
+        ws = scratch.data_ptr()
     st = (lib.spops_mx4_linear_grad if back else lib.spops_mx4_linear)(_ARGS(
-        x, ldx, W._codes.data_ptr(), W._scales.data_ptr(), y, ldy, _raw_stream(dev.index), _DTYPE[dt], tokens, rows, cols))
+        x, ldx, W._codes.data_ptr(), W._scales.data_ptr(), y, ldy, ws, size, _raw_stream(dev.index), _DTYPE[dt],
+        tokens, rows, cols))
     if st:
         _check(st, "mx4_linear_grad" if back else "mx4_linear")
     if given:  # (what autograd saved of it is no longer there)
