@@ -444,20 +444,48 @@ bool encode_matrix(CUtensorMap* map, bool bf16, const void* p, int64_t rows, int
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Tokens per tile and splits of the contraction with the least estimated time, in cycles: a chunk takes its products
-// (2 nt cycles) or its decoding (about 300), whichever is longer.
+// Clusters of `pairs` pairs that the device holds at once (asked once per kernel and device).
+constexpr int kMaxSplits = 4;
+template <typename K>
+int clusters_at_once(K kern, int pairs, int (&known)[64][kMaxSplits + 1]) {
+    const DeviceProps& p = device_props();
+    const int d = p.device;
+    if (d >= 0 && d < 64 && known[d][pairs]) return known[d][pairs];
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * pairs;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = pairs == 1 ? (p.sm_count > 1 ? p.sm_count / 2 : 1) : 1;
+    }
+    if (d >= 0 && d < 64) known[d][pairs] = n;
+    return n;
+}
+
+// Tokens per tile and splits of the contraction with the least estimated time in us, fitted to sweeps over both (64 to
+// 11008 features, 6 to 172 chunks, 16 to 8192 tokens; the choice is within a tenth of the best of a sweep): a chunk takes
+// 0.3 (the handshakes of a stage), from about 210 tokens on its products; a pass without splits 4.4 beside its chunks, and
+// its tiles follow each other; with splits, every wave of clusters begins anew and adds its sums.
 struct Shape {
     int nt, splits;
 };
-Shape choose(int64_t tokens, int64_t ftiles, int chunks, int sms) {
+Shape choose(int64_t tokens, int64_t ftiles, int chunks, const int (&at_once)[kMaxSplits + 1]) {
     Shape best{kMaxTokens, 1};
     double least = 1e300;
     for (int nt = 32; nt <= kMaxTokens; nt += 32)
-        for (int s = 1; s <= 4 && s <= chunks; ++s) {
-            const int64_t tiles = ftiles * ((tokens + nt - 1) / nt), at_once = sms / (2 * s);
-            const int64_t waves = (tiles + at_once - 1) / at_once;
-            const double chunk = 2 * nt > 300 ? 2 * nt : 300, steps = (chunks + s - 1) / s;
-            const double t = waves * (steps * chunk + (s > 1 ? 1500.0 : 300.0)) + 3000 + 12.0 * nt;
+        for (int s = 1; s <= kMaxSplits && s <= chunks; ++s) {
+            const int64_t tiles = ftiles * ((tokens + nt - 1) / nt), waves = (tiles + at_once[s] - 1) / at_once[s];
+            const double chunk = 0.0014 * nt > 0.3 ? 0.0014 * nt : 0.3, steps = (chunks + s - 1) / s;
+            const double t = s == 1 ? 4.4 + waves * (steps * chunk + 0.2) + 0.008 * nt
+                                    : waves * (5.0 + 0.3 * s + 0.012 * nt + steps * chunk);
             if (t < least) {
                 least = t;
                 best = {nt, s};
@@ -486,8 +514,10 @@ cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
     g.tokens = a.tokens;
     g.ftiles = (int32_t)(((int64_t)F + 2 * kFeatures - 1) / (2 * kFeatures));
     g.chunks = (int32_t)(((int64_t)C + kKC - 1) / kKC);
-    const int sms = device_props().sm_count;
-    const Shape shape = choose(a.tokens, g.ftiles, g.chunks, sms);
+    static int known[64][kMaxSplits + 1];
+    int at_once[kMaxSplits + 1];
+    for (int i = 1; i <= kMaxSplits; ++i) at_once[i] = clusters_at_once(kern, i, known);
+    const Shape shape = choose(a.tokens, g.ftiles, g.chunks, at_once);
     g.nt = shape.nt;
     g.stages = min((int)(kRing / (kWBytes + shape.nt * 64)), kMaxStages);
     g.tiles = (int64_t)g.ftiles * (((int64_t)a.tokens + shape.nt - 1) / shape.nt);
@@ -500,7 +530,7 @@ cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
         !encode_matrix(&my, bf, a.Y, a.tokens, F8, a.ldy, 32, kOutTokens, false))
         return cudaErrorInvalidValue;
     const int c = 2 * shape.splits;
-    const int64_t clusters = shape.splits > 1 ? g.tiles : min64(g.tiles, max64(1, sms / 2));
+    const int64_t clusters = shape.splits > 1 ? g.tiles : min64(g.tiles, at_once[1]);
     if (clusters * c > 0x7fffffffll) return cudaErrorInvalidValue;
     count_launches(1);
     return launch_pdl_cluster(kern, dim3((unsigned)(clusters * c)), dim3(kThreads), kSmem, (unsigned)c, s, g, mx, my);
