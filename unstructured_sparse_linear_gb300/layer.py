@@ -21,7 +21,9 @@ import functools
 import torch
 
 from . import csr_add, csr_transpose, permute_values, plan_build, sddmm, sort_rows, spmm
+from .dropout import dropout as _dropout
 from .lora import lora_add, lora_grad, lora_plan
+from .mx4 import Mx4, mx4_dequantize, mx4_linear, mx4_linear_grad
 
 
 class _Refuse(torch.autograd.Function):
@@ -162,32 +164,49 @@ class SparseLinear(_MaskedLayer):
 
 class RosaLinearFunction(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, X, values, A, B, layer, plan):
-        weight, scale = layer.weight, layer.scale
-        Y = X @ layer.merged(values).t()
+    def forward(ctx, X, values, A, B, layer, plan, state=None):
+        scale, quantized = layer.scale, layer.quantized
+        if quantized is not None and values is None:
+            Y = mx4_linear(X, quantized)
+        else:
+            Y = X @ layer.merged(values).t()
         ctx.mask = layer._mask if values is not None else None
-        Y, h = lora_add(X, A, B, plan, base=Y, scale=scale, out=Y, return_h=True)
+        dropped = X if state is None else _dropout(X, layer.dropout, state)
+        Y, h = lora_add(dropped, A, B, plan, base=Y, scale=scale, out=Y, return_h=True)
         factors = scale if isinstance(scale, torch.Tensor) else None
-        ctx.save_for_backward(X, values, A, B, h, weight, factors)
-        ctx.layer, ctx.plan, ctx.scale = layer, plan, scale if factors is None else None
+        kept = (layer.weight, None) if quantized is None else (quantized.codes, quantized.scales)
+        ctx.save_for_backward(X, values, A, B, h, *kept, factors, state)
+        ctx.layer, ctx.plan, ctx.scale, ctx.p = layer, plan, scale if factors is None else None, layer.dropout
         return Y
 
     @staticmethod
     @first_derivatives_only
     def backward(ctx, dY):
-        X, values, A, B, h, weight, factors = ctx.saved_tensors
+        X, values, A, B, h, weight, scales, factors, state = ctx.saved_tensors
         L, scale = ctx.layer, ctx.scale if factors is None else factors
+        if scales is not None:
+            weight = Mx4(weight, scales, L.in_features, X.dtype)
         L._check_mask(ctx.mask)
         dY = dY.contiguous()
         need_x, need_v, need_a, need_b = ctx.needs_input_grad[:4]
-        # The merged weight is formed again: less time than its memory is worth in a deep model.
-        base = dY @ L.merged(values, weight) if need_x else None
-        dX, dA, dB = lora_grad(dY, X, A, B, ctx.plan, scale=scale, h=h, dX_base=base, dX_out=base,
-                               need=(need_x, need_a, need_b))
+        base = None
+        if need_x:
+            if scales is not None and values is None:
+                base = mx4_linear_grad(dY, weight)
+            else:  # the merged weight is formed again: less time than its memory is worth in a deep model
+                base = dY @ L.merged(values, weight)
+        if state is None:
+            dX, dA, dB = lora_grad(dY, X, A, B, ctx.plan, scale=scale, h=h, dX_base=base, dX_out=base,
+                                   need=(need_x, need_a, need_b))
+        else:  # what the factors saw, and its gradient through the same mask
+            dropped = _dropout(X, ctx.p, state) if need_a else X
+            dX, dA, dB = lora_grad(dY, dropped, A, B, ctx.plan, scale=scale, h=h, need=(need_x, need_a, need_b))
+            if need_x:
+                dX = _dropout(dX, ctx.p, state, base=base, out=base)
         dV = None
         if need_v and values is not None:
             dV = sddmm(L.row_offsets, L.row_idx, L.col_idx, dY.t().contiguous(), X.t().contiguous(), plan=L.plan)
-        return dX, dV, dA, dB, None, None
+        return dX, dV, dA, dB, None, None, None
 
 
 class RosaLinear(_MaskedLayer):
@@ -197,22 +216,33 @@ class RosaLinear(_MaskedLayer):
 
         Y = X (W + S)^T + s_i (X A_i^T) B_i^T
 
-    weight: W [out, in], fp16 or bf16 (fp32 runs the general kernels), not trained. row_offsets,
+    weight: W [out, in], fp16 or bf16 (fp32 runs the general kernels), or an Mx4 (4 bits; its products are mx4_linear
+    and mx4_linear_grad, beside a sparse part its values are formed in every pass), not trained. row_offsets,
     col_idx, values: S on a fixed CSR mask, shared by all tokens (None: no sparse part). n_adapters
     low-rank adapters of one rank, their factor `scale` a number or an fp32 tensor with one per
     adapter (then part of the layer's state); A starts at random and B at zero, so that the adapters start as no change. X is
     token-major [..., in]; adapter_ids (int32, one per token) or a plan of them choose each token's
-    adapter, by default adapter 0 for all. Gradients are first derivatives: differentiating them again
-    raises."""
+    adapter, by default adapter 0 for all. dropout: the share of X's values that the low-rank part does not see in
+    training; its mask is not kept but formed again, from two numbers that each forward pass draws from torch's
+    generator of the device (so manual_seed, checkpointing and captured graphs treat it as torch's own). Gradients are
+    first derivatives: differentiating them again raises."""
 
-    def __init__(self, weight: torch.Tensor, rank: int, n_adapters: int = 1, scale=1.0, row_offsets=None, col_idx=None,
-                 values=None):
+    _quantized = None  # the Mx4 of the buffers codes and scales
+
+    def __init__(self, weight, rank: int, n_adapters: int = 1, scale=1.0, row_offsets=None, col_idx=None, values=None,
+                 dropout: float = 0.0):
         super().__init__()
         self.out_features, self.in_features = weight.shape
         self.n_adapters = int(n_adapters)
+        self.dropout = float(dropout)
+        if not 0.0 <= self.dropout <= 1.0:
+            raise ValueError(f"dropout must lie in [0, 1], got {self.dropout}")
         self.register_buffer("factors", None)
         RosaLinear.scale.fset(self, scale)  # (a Parameter would be registered under that name)
-        self.register_buffer("weight", weight)
+        four_bits = isinstance(weight, Mx4)
+        self.register_buffer("weight", None if four_bits else weight)
+        self.register_buffer("codes", weight.codes if four_bits else None)
+        self.register_buffer("scales", weight.scales if four_bits else None)
         dev, dt = weight.device, weight.dtype
         self.A = torch.nn.Parameter(torch.randn(self.n_adapters, rank, self.in_features, device=dev, dtype=torch.float32)
                                     .mul_(self.in_features ** -0.5).to(dt))
@@ -254,15 +284,28 @@ class RosaLinear(_MaskedLayer):
         return dict(row_idx=row_idx, plan=plan_build(self.row_offsets, row_idx, self.col_idx, self.in_features))
 
     def __getstate__(self):  # a copy or a pickle of the layer makes its own plans
-        return {**super().__getstate__(), "_plans": {}, "_captured": {}}
+        return {**super().__getstate__(), "_plans": {}, "_captured": {}, "_quantized": None}
+
+    @property
+    def quantized(self) -> Mx4 | None:
+        """The frozen weight as an Mx4, of the buffers ``codes`` and ``scales`` (None: it is a dense one)."""
+        codes, scales = self.codes, self.scales
+        if codes is None:
+            return None
+        q = self._quantized
+        if q is None or q.codes is not codes or q.scales is not scales or q.dtype != self.A.dtype:  # (moved, loaded)
+            q = self._quantized = Mx4(codes, scales, self.in_features, self.A.dtype)
+        return q
 
     def merged(self, values, weight=None):
-        """W + S (of another weight than the layer's, where one is given)."""
-        weight = self.weight if weight is None else weight
+        """W + S (of another weight than the layer's, where one is given) as a dense matrix."""
+        if weight is None:
+            weight = self.quantized if self.weight is None else self.weight
+        dense = mx4_dequantize(weight) if isinstance(weight, Mx4) else weight
         if values is None:
-            return weight
+            return dense
         self._follow_mask()
-        return csr_add(values, self.row_offsets, self.row_idx, self.col_idx, weight)
+        return csr_add(values, self.row_offsets, self.row_idx, self.col_idx, dense, out=dense if dense is not weight else None)
 
     def _one_adapter_plan(self, tokens, device):
         capturing = torch.cuda.is_current_stream_capturing()
@@ -284,5 +327,8 @@ class RosaLinear(_MaskedLayer):
             plan = lora_plan(adapter_ids.reshape(-1), self.n_adapters)
         if plan is None:
             plan = self._one_adapter_plan(X2.shape[0], X2.device)
-        Y = RosaLinearFunction.apply(X2.contiguous(), self.values, self.A, self.B, self, plan)
+        state = ()
+        if self.dropout > 0.0 and self.training:  # a seed and a call number
+            state = (torch.randint(0, 2 ** 63 - 1, (2,), dtype=torch.int64, device=X2.device),)
+        Y = RosaLinearFunction.apply(X2.contiguous(), self.values, self.A, self.B, self, plan, *state)
         return Y.reshape(*X.shape[:-1], self.out_features)
