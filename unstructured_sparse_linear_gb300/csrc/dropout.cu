@@ -37,48 +37,85 @@ __device__ __forceinline__ Numbers philox7(uint64_t index, uint64_t call, uint64
 }
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&f)[8]) {
+struct Raw {
+    uint4 v[sizeof(T) / 2];
+};
+// Up to eight values from p on, zeros behind the last. vec: on a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ Raw<T> load8(const T* p, int n, bool vec) {
+    Raw<T> r;
     if (vec && n >= 8) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-            Elt<T>::unpack(ld_v4(reinterpret_cast<const char*>(p) + 16 * i), f + i * Elt<T>::kVec);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = ld_v4(reinterpret_cast<const char*>(p) + 16 * i);
     } else {
+        float f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = i < n ? Elt<T>::to_f(p[i]) : 0.f;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = Elt<T>::pack(f + i * Elt<T>::kVec);
     }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw<T>& r, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) Elt<T>::unpack(r.v[i], f + i * Elt<T>::kVec);
 }
 
-// groups: eights of a row. vec: every row of every operand begins on a 16-byte boundary.
+// groups: eights of a row. vec: every row of every operand begins on a 16-byte boundary. A thread has kSteps eights at a
+// time, all loaded before the first is used.
 template <typename T, bool kBase>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutArgs g, int64_t rows, int64_t cols, int64_t groups,
                                                            bool vec) {
+    constexpr int kSteps = sizeof(T) == 2 ? 2 : 1;
     pdl_trigger();
     pdl_wait();
     const uint64_t seed = g.state ? g.state[0] : g.seed, call = g.state ? g.state[1] : g.call;
     const float factor = g.threshold < 65536u ? 65536.f / (float)(65536u - g.threshold) : 0.f;
+    // kept where the number, in a word's upper half, is not below the threshold: compared in 32 bits, the lower half behind it
+    const uint32_t below = g.threshold < 65536u ? g.threshold << 16 : 0u;
     const int64_t items = rows * groups, step = (int64_t)gridDim.x * kThreads;
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < items; i += step) {
-        const int64_t r = rows == 1 ? 0 : i / groups, c = (i - r * groups) * 8;
-        const int n = (int)min64(cols - c, 8);
-        float f[8], y[8];
-        load8(static_cast<const T*>(g.X) + r * g.ldx + c, n, vec, f);
-        if (kBase) load8(static_cast<const T*>(g.base) + r * g.ldb + c, n, vec, y);
-        const Numbers u = philox7((uint64_t)i, call, seed);
+    for (int64_t i0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; i0 < items; i0 += kSteps * step) {
+        Raw<T> x[kSteps], b[kSteps];
+        int64_t r[kSteps], c[kSteps];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint32_t number = e & 1 ? u.w[e / 2] >> 16 : u.w[e / 2] & 0xffffu;
-            const float kept = number >= g.threshold ? f[e] * factor : 0.f;  // (a dropped infinity or NaN is gone)
-            f[e] = kBase ? y[e] + kept : kept;
+        for (int u = 0; u < kSteps; ++u) {
+            const int64_t i = i0 + u * step;
+            if (u > 0 && i >= items) break;
+            r[u] = rows == 1 ? 0 : i / groups;
+            c[u] = (i - r[u] * groups) * 8;
+            const int n = (int)min64(cols - c[u], 8);
+            x[u] = load8(static_cast<const T*>(g.X) + r[u] * g.ldx + c[u], n, vec);
+            if (kBase) b[u] = load8(static_cast<const T*>(g.base) + r[u] * g.ldb + c[u], n, vec);
         }
-        T* to = static_cast<T*>(g.Y) + r * g.ldy + c;
-        if (vec && n == 8) {
 #pragma unroll
-            for (int e = 0; e < (int)sizeof(T) / 2; ++e)
-                reinterpret_cast<uint4*>(to)[e] = Elt<T>::pack(f + e * Elt<T>::kVec);
-        } else {
+        for (int u = 0; u < kSteps; ++u) {
+            const int64_t i = i0 + u * step;
+            if (u > 0 && i >= items) break;
+            const int n = (int)min64(cols - c[u], 8);
+            const Numbers w = philox7((uint64_t)i, call, seed);
+            float f[8], y[8];
+            widen8(x[u], f);
+            if (kBase) widen8(b[u], y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < n) to[e] = Elt<T>::from_f(f[e]);
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t number = e & 1 ? w.w[e / 2] : w.w[e / 2] << 16;
+                const float kept = number >= below ? f[e] * factor : 0.f;  // (a dropped infinity or NaN is gone)
+                f[e] = kBase ? y[e] + kept : kept;
+            }
+            if (g.threshold == 65536u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = kBase ? y[e] : 0.f;
+            T* to = static_cast<T*>(g.Y) + r[u] * g.ldy + c[u];
+            if (vec && n == 8) {
+#pragma unroll
+                for (int e = 0; e < (int)sizeof(T) / 2; ++e)
+                    reinterpret_cast<uint4*>(to)[e] = Elt<T>::pack(f + e * Elt<T>::kVec);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n) to[e] = Elt<T>::from_f(f[e]);
+            }
         }
     }
 }

@@ -55,6 +55,24 @@ __device__ __forceinline__ void widen8(const Raw<T>& r, float (&f)[8]) {
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) Elt<T>::unpack(r.v[i], f + i * Elt<T>::kVec);
 }
 
+// The largest magnitude of eight values as an fp32 bit pattern (16-bit patterns are ordered as their values are).
+template <typename T>
+__device__ __forceinline__ uint32_t largest8(const Raw<T>& r) {
+    if constexpr (sizeof(T) == 4) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            m = max(max(m, max(r.v[i].x & 0x7fffffffu, r.v[i].y & 0x7fffffffu)), max(r.v[i].z & 0x7fffffffu, r.v[i].w & 0x7fffffffu));
+        return m;
+    } else {
+        const uint32_t a = 0x7fff7fffu;
+        uint32_t m = __vmaxu2(__vmaxu2(r.v[0].x & a, r.v[0].y & a), __vmaxu2(r.v[0].z & a, r.v[0].w & a));
+        m = max(m >> 16, m & 0xffffu);
+        const uint16_t h = (uint16_t)m;
+        return __float_as_uint(Elt<T>::to_f(reinterpret_cast<const T&>(h)));
+    }
+}
+
 // Two values as two codes, `lo` in the low bits.
 __device__ __forceinline__ uint32_t encode2(float lo, float hi) {
     uint16_t r;
@@ -92,9 +110,7 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* X, int6
         for (int u = 0; u < kSteps; ++u) {
             float f[8];
             widen8(raw[u], f);
-            uint32_t m = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(f[e]) & 0x7fffffffu);
+            uint32_t m = largest8(raw[u]);
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
             // the exponent field less 2; a block that holds an infinity or a NaN (field 255) is NaN

@@ -34,7 +34,7 @@ def dropout(X: torch.Tensor, p: float, state, base: torch.Tensor | None = None,
     if not isinstance(X, torch.Tensor):
         raise TypeError("X must be a torch.Tensor")
     dev, dt = X.device, X.dtype
-    if not X.is_cuda:
+    if dev.type != "cuda":
         raise ValueError("X must be a CUDA tensor")
     if dt not in _DTYPE:
         raise ValueError(f"X dtype {dt} not in {list(_DTYPE)}")
@@ -51,9 +51,10 @@ def dropout(X: torch.Tensor, p: float, state, base: torch.Tensor | None = None,
         raise ValueError(f"p must lie in [0, 1], got {p}")
     at = seed = call = 0
     if isinstance(state, torch.Tensor):
-        _req(state, "state", torch.int64, device=dev)
-        if state.numel() != 2:
-            raise ValueError(f"state must hold a seed and a call number, got {tuple(state.shape)}")
+        if not (state.dtype is torch.int64 and state.device == dev and state.shape == (2,) and state.is_contiguous()):
+            _req(state, "state", torch.int64, device=dev)
+            if state.numel() != 2:
+                raise ValueError(f"state must hold a seed and a call number, got {tuple(state.shape)}")
         at = state.data_ptr()
     else:
         seed, call = (int(v) for v in state)

@@ -50,6 +50,12 @@ class Mx4:
         self._codes, self._scales, self._shape = codes, scales, (codes.shape[0], cols)
         self.dtype, self.device = dtype, codes.device
 
+    @classmethod
+    def _of(cls, codes, scales, shape, dtype, device):  # (of a conversion: nothing to check)
+        W = object.__new__(cls)
+        W._codes, W._scales, W._shape, W.dtype, W.device = codes, scales, shape, dtype, device
+        return W
+
     @property
     def codes(self) -> torch.Tensor:
         return self._codes
@@ -102,13 +108,17 @@ def mx4_quantize(X: torch.Tensor) -> Mx4:
     the last). A block that holds an infinity or a NaN is NaN as a whole."""
     rows, cols, x, ldx = _strided(X, "X")
     dev = X.device
+    if _elsewhere(dev.index):
+        with torch.cuda.device(dev):
+            return mx4_quantize(X)
     blocks = -(-cols // BLOCK)
     codes = torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=dev)
     scales = torch.empty((rows, blocks), dtype=torch.uint8, device=dev)
-    with torch.cuda.device(dev):
-        _check(_L().spops_mx4_quantize(x, ldx, _DTYPE[X.dtype], rows, cols, codes.data_ptr(), scales.data_ptr(),
-                                       _raw_stream(dev.index)), "mx4_quantize")
-    return Mx4(codes, scales, cols, X.dtype)
+    st = _L().spops_mx4_quantize(x, ldx, _DTYPE[X.dtype], rows, cols, codes.data_ptr(), scales.data_ptr(),
+                                 _raw_stream(dev.index))
+    if st:
+        _check(st, "mx4_quantize")
+    return Mx4._of(codes, scales, (rows, cols), X.dtype, dev)
 
 
 def mx4_dequantize(W: Mx4, dtype: torch.dtype | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -119,14 +129,18 @@ def mx4_dequantize(W: Mx4, dtype: torch.dtype | None = None, out: torch.Tensor |
     if dtype not in _DTYPE:
         raise ValueError(f"dtype {dtype} not in {list(_DTYPE)}")
     dev, given = W.device, out is not None
+    if _elsewhere(dev.index):
+        with torch.cuda.device(dev):
+            return mx4_dequantize(W, dtype, out)
     if given:
         y, ldy = _given(out, "out", rows, cols, dtype, dev)
     else:
         out = torch.empty((rows, cols), dtype=dtype, device=dev)
         y, ldy = out.data_ptr(), cols
-    with torch.cuda.device(dev):
-        _check(_L().spops_mx4_dequantize(W._codes.data_ptr(), W._scales.data_ptr(), rows, cols, y, ldy, _DTYPE[dtype],
-                                         _raw_stream(dev.index)), "mx4_dequantize")
+    st = _L().spops_mx4_dequantize(W._codes.data_ptr(), W._scales.data_ptr(), rows, cols, y, ldy, _DTYPE[dtype],
+                                   _raw_stream(dev.index))
+    if st:
+        _check(st, "mx4_dequantize")
     if given:
         increment_version(out)
     return out
