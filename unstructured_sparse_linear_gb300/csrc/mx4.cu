@@ -5,8 +5,10 @@
 // value less that of 4, the grid's last power of two), and each value is rounded to the nearest of 0, .5, 1, 1.5, 2, 3,
 // 4, 6 times it (ties to the even mantissa, beyond 6 to 6).
 //
-// Both kernels stream: four lanes share a block, a lane has eight values (16 bytes of a 16-bit type, 4 bytes of codes),
-// and a warp four steps of 256 values, loaded before any is used, so that 64 bytes a lane are under way. Bound by HBM.
+// All kernels stream: four lanes share a block, a lane has eight values (16 bytes of a 16-bit type, 4 bytes of codes; from
+// codes to fp32 four values), and a warp several steps of 256 values, loaded before any is used. The flat kernels take
+// matrices of whole blocks without gaps between the rows, on 16-byte boundaries, as one long row, without any bounds but the
+// end: 11008 x 4096 bf16 to 4 bits 22.6 us (37 by rows), back 19.2 (27). Bound by HBM, to 4 bits also by what a warp issues.
 #include "internal.h"
 #include "mx4.cuh"
 #include "mx4.h"
@@ -73,11 +75,61 @@ __device__ __forceinline__ uint32_t largest8(const Raw<T>& r) {
     }
 }
 
-// Two values as two codes, `lo` in the low bits.
-__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
-    uint16_t r;
-    asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tmov.b16 %0, {t, 0};\n\t}" : "=h"(r) : "f"(hi), "f"(lo));
+// Eight values as eight codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t encode8(const float (&f)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
     return r;
+}
+
+// A lane's eight values (of four lanes' block) as codes, and the block's scale.
+template <typename T>
+__device__ __forceinline__ uint32_t convert8(const Raw<T>& raw, uint32_t& b) {
+    uint32_t m = largest8(raw);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    // the exponent field less 2; a block that holds an infinity or a NaN (field 255) is NaN
+    b = m >= 0x7f800000u ? 255u : (uint32_t)max(0, (int)(m >> 23) - 2);
+    const float inv = __uint_as_float((254u - b) << 23);  // 2^(127 - b), b <= 252
+    float f[8];
+    widen8(raw, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= inv;
+    const uint32_t c = encode8(f);
+    return b == 255u ? 0u : c;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) mx4_quantize_flat_kernel(const T* X, int64_t eights, uint32_t* codes,
+                                                                     uint8_t* scales) {
+    constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
+    pdl_trigger();
+    pdl_wait();
+    const int64_t step = (int64_t)gridDim.x * kThreads;
+    const int lane = threadIdx.x & 31;
+    // (a warp's first eight decides, so that its lanes stay together; eights is a multiple of 4)
+    for (int64_t e0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; e0 - lane < eights; e0 += kUnroll * step) {
+        Raw<T> raw[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            raw[u] = Raw<T>{};
+            if (e0 + u * step < eights) raw[u] = load8(X + (e0 + u * step) * 8, 8, true);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            uint32_t b;
+            const uint32_t c = convert8(raw[u], b);
+            if (e0 + u * step < eights) {
+                codes[e0 + u * step] = c;
+                if ((lane & 3) == 0) scales[(e0 + u * step) >> 2] = (uint8_t)b;
+            }
+        }
+    }
 }
 
 template <typename T>
@@ -108,19 +160,8 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T* X, int6
         }
 #pragma unroll
         for (int u = 0; u < kSteps; ++u) {
-            float f[8];
-            widen8(raw[u], f);
-            uint32_t m = largest8(raw[u]);
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            // the exponent field less 2; a block that holds an infinity or a NaN (field 255) is NaN
-            const bool nan = m >= 0x7f800000u;
-            const uint32_t b = nan ? 255u : (uint32_t)max(0, (int)(m >> 23) - 2);
-            const float inv = nan ? 0.f : __uint_as_float((254u - b) << 23);  // 2^(127 - b), b <= 252
-            uint32_t c = 0;
-            if (!nan)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) c |= encode2(f[2 * e] * inv, f[2 * e + 1] * inv) << (8 * e);
+            uint32_t b;
+            const uint32_t c = convert8(raw[u], b);
             if (at[u] >= 0) {
                 codes[at[u]] = c;
                 if ((lane & 3) == 0) scales[at[u] >> 2] = (uint8_t)b;
@@ -177,6 +218,43 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint32_t
     }
 }
 
+// kVals: of a lane and step, 16 bytes of Y.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) mx4_dequantize_flat_kernel(const uint8_t* codes, const uint8_t* scales,
+                                                                       int64_t pieces, T* Y) {
+    constexpr int kVals = Elt<T>::kVec, kUnroll = 4;
+    using Code = typename std::conditional<kVals == 8, uint32_t, uint16_t>::type;
+    pdl_trigger();
+    pdl_wait();
+    const int64_t step = (int64_t)gridDim.x * kThreads;
+    for (int64_t p0 = (int64_t)blockIdx.x * kThreads + threadIdx.x; p0 < pieces; p0 += kUnroll * step) {
+        uint32_t c[kUnroll], b[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t p = p0 + u * step;
+            c[u] = p < pieces ? __ldg(reinterpret_cast<const Code*>(codes) + p) : 0;
+            b[u] = p < pieces ? __ldg(scales + p / (kMx4Block / kVals)) : 127;
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int64_t p = p0 + u * step;
+            if (p >= pieces) break;
+            uint4 v;
+            if constexpr (kVals == 8) {
+                uint32_t o[4];
+                if (mx4::plain(b[u])) mx4::decode8<T>(c[u], mx4::factor2(b[u]), o);
+                else mx4::decode8_any<T>(c[u], b[u], o);
+                v = make_uint4(o[0], o[1], o[2], o[3]);
+            } else {
+                const float s = mx4::scale_f32(b[u]);
+                v = make_uint4(__float_as_uint(mx4::value_f32(c[u], s)), __float_as_uint(mx4::value_f32(c[u] >> 4, s)),
+                               __float_as_uint(mx4::value_f32(c[u] >> 8, s)), __float_as_uint(mx4::value_f32(c[u] >> 12, s)));
+            }
+            reinterpret_cast<uint4*>(Y)[p] = v;
+        }
+    }
+}
+
 // Rows of 16-bit values, zeros behind the last column.
 __global__ void __launch_bounds__(kThreads) mx4_copy_kernel(const uint16_t* from, int64_t ldf, uint16_t* to, int64_t ldt,
                                                             int64_t rows, int64_t cols, int64_t cols_to) {
@@ -199,12 +277,21 @@ unsigned walk_grid(const Walk& w) {
     return (unsigned)max64(1, min64((items + per - 1) / per, (int64_t)device_props().sm_count * 8));
 }
 
+// CTAs of a flat kernel: eight an SM, fewer where its threads would have nothing.
+unsigned flat_grid(int64_t pieces, int unroll) {
+    const int64_t per = (int64_t)kThreads * unroll;
+    return (unsigned)max64(1, min64((pieces + per - 1) / per, (int64_t)device_props().sm_count * 8));
+}
+
 template <typename T>
 cudaError_t quantize(const void* X, int64_t ldx, int32_t rows, int32_t cols, uint8_t* codes, uint8_t* scales,
                      cudaStream_t s) {
     const Walk w = make_walk(rows, cols, ldx);
     const bool vec = reinterpret_cast<uintptr_t>(X) % 16 == 0 && (w.rows == 1 || ldx * (int64_t)sizeof(T) % 16 == 0);
     count_launches(1);
+    if (w.rows == 1 && w.cols % kMx4Block == 0 && vec)
+        return launch_pdl(mx4_quantize_flat_kernel<T>, dim3(flat_grid(w.cols / 8, sizeof(T) == 2 ? 4 : 2)), dim3(kThreads), 0, s,
+                          static_cast<const T*>(X), w.cols / 8, reinterpret_cast<uint32_t*>(codes), scales);
     return launch_pdl(mx4_quantize_kernel<T>, dim3(walk_grid(w)), dim3(kThreads), 0, s, static_cast<const T*>(X), ldx, w,
                       vec, reinterpret_cast<uint32_t*>(codes), scales);
 }
@@ -215,6 +302,9 @@ cudaError_t dequantize(const uint8_t* codes, const uint8_t* scales, int32_t rows
     const Walk w = make_walk(rows, cols, ldy);
     const bool vec = reinterpret_cast<uintptr_t>(Y) % 16 == 0 && (w.rows == 1 || ldy * (int64_t)sizeof(T) % 16 == 0);
     count_launches(1);
+    if (w.rows == 1 && w.cols % kMx4Block == 0 && vec)
+        return launch_pdl(mx4_dequantize_flat_kernel<T>, dim3(flat_grid(w.cols / Elt<T>::kVec, 4)), dim3(kThreads), 0, s, codes, scales,
+                          w.cols / Elt<T>::kVec, static_cast<T*>(Y));
     return launch_pdl(mx4_dequantize_kernel<T>, dim3(walk_grid(w)), dim3(kThreads), 0, s,
                       reinterpret_cast<const uint32_t*>(codes), scales, w, static_cast<T*>(Y), ldy, vec);
 }
