@@ -18,20 +18,28 @@
 namespace spops {
 namespace {
 
-// Warps 0 to 3 finish (a TMEM lane quarter each), then kGroups groups of four decode, one warp loads X, one multiplies.
-constexpr int kGroups = 5, kLoadWarp = 4 + 4 * kGroups, kMmaWarp = kLoadWarp + 1, kThreads = 32 * (kMmaWarp + 1);
 constexpr int kKC = 64;             // contraction elements of a stage: 128-byte rows
 constexpr int kFeatures = 128;      // of a CTA
 constexpr int kMaxTokens = 256;     // of a tile
-// A stage: 128 features and nt / 2 tokens, 128 bytes each; as many as fit.
-constexpr uint32_t kWBytes = kFeatures * 128, kRing = 6 * (kWBytes + kMaxTokens / 2 * 128);
-constexpr int kMinStages = 6, kMaxStages = 10;
-constexpr int kOutTokens = 32;                              // of a store: 32 x 32 values
+constexpr uint32_t kWBytes = kFeatures * 128;  // of 64 of the contraction
+constexpr uint32_t kRing = 6 * (kWBytes + kMaxTokens / 2 * 128);
+constexpr int kMaxStages = 10;
+constexpr int kOutTokens = 32;  // of a store: 32 x 32 values
 constexpr uint32_t kOutBytes = kOutTokens * 32 * 2;
 constexpr uint32_t kOutAt = kRing, kBarsAt = kOutAt + 4 * 2 * kOutBytes;
 constexpr uint32_t kSmem = kBarsAt + 1024;
-constexpr int kAhead = 1;  // chunks whose codes a decoder has under way
-static_assert(kGroups < kMinStages, "a group's next chunk is less than one round of the ring away");
+constexpr int kAhead = 1;  // stages whose codes a decoder has under way
+
+// A stage holds kSub times 64 of the contraction: one, or two where the products of 64 take less time than the messages of a
+// stage (up to 128 tokens). Warps 0 to 3 finish (a TMEM lane quarter each), then kGroups groups of four decode, one warp
+// loads X, one multiplies.
+template <int kSub>
+struct TileCfg {
+    static constexpr int kGroups = kSub == 1 ? 6 : 4;
+    static constexpr int kLoadWarp = 4 + 4 * kGroups, kMmaWarp = kLoadWarp + 1, kThreads = 32 * (kMmaWarp + 1);
+    static constexpr int kTokens = kSub == 1 ? kMaxTokens : kMaxTokens / 2;  // at most
+    static_assert(kGroups <= (int)(kRing / (kSub * (kWBytes + kTokens * 64))), "a group's next stage is at most one round of the ring away");
+};
 
 // ------------------------------------------------------------------ PTX of CTA pairs
 
@@ -69,10 +77,11 @@ __device__ __forceinline__ void pair_tma_load_2d(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-// Arrive on a barrier of the pair (its cluster address); this CTA's shared memory is then as its warp left it.
+// Arrive on a barrier of the pair (its cluster address). What it announces is read by this CTA's tensor core, for which
+// each writer's proxy fence has made it visible, or has left TMEM: no release of the cluster's scope, which took a warp 500
+// cycles for each stage.
 __device__ __forceinline__ void pair_arrive(uint32_t bar) {
-    cluster_release_smem();
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // What the pair wrote to its shared memory before the messages that were waited for.
 __device__ __forceinline__ void acquire_pair_smem() {
@@ -134,9 +143,11 @@ __device__ __forceinline__ bool elect_one() {
 
 // A cluster is one pair, or S pairs that split a tile's contraction; in the second case (one tile per cluster) the fp32
 // partial sums meet in shared memory and are added in the order of the splits.
-template <typename T, bool kBack>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, bool kBack, int kSub>
+__global__ void __launch_bounds__(TileCfg<kSub>::kThreads, 1)
 mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_y) {
+    constexpr int kLoadWarp = TileCfg<kSub>::kLoadWarp, kMmaWarp = TileCfg<kSub>::kMmaWarp, kThreads = TileCfg<kSub>::kThreads;
+    constexpr int kGroups = TileCfg<kSub>::kGroups, kBlocks = 2 * kSub;  // blocks of a decoder and stage
     // No static shared memory, so the dynamic part starts on the 1 KB boundary that the swizzled tiles need (checked).
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     struct Shared {
@@ -152,13 +163,13 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t stages = g.stages, stage_bytes = kWBytes + (uint32_t)g.nt * 64;
+    const uint32_t stages = g.stages, x_bytes = (uint32_t)g.nt * 64, stage_bytes = kSub * (kWBytes + x_bytes);
     const int C = (int)cluster_size(), crank = (int)cluster_rank();
     const int half = crank & 1, lead = crank & ~1, split = crank >> 1, splits = C >> 1;
     const int64_t cid = blockIdx.x / C, ncl = gridDim.x / C;
     const int c0 = (int)((int64_t)g.chunks * split / splits), c1 = (int)((int64_t)g.chunks * (split + 1) / splits);
     const int per = c1 - c0;                                               // chunks of a tile
-    const int64_t mine = cid < g.tiles ? (g.tiles - cid + ncl - 1) / ncl : 0;  // tiles of this cluster
+    const int64_t mine = cid < g.tiles && per > 0 ? (g.tiles - cid + ncl - 1) / ncl : 0;  // tiles of this cluster
     if (tid == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 2 * 4 + 1);  // decoding warps of the pair, the loader
@@ -194,9 +205,11 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                 for (int c = c0; c < c1; ++c) {
                     if (wait(smem_u32(&sh.empty[s]), ph)) {
                         const uint32_t bar = smem_u32(&sh.full[s]);
-                        if (half == 0) mbar_arrive_expect_tx(bar, (uint32_t)g.nt * 128);  // both halves
-                        pair_tma_load_2d(sbase + s * stage_bytes + kWBytes, &map_x, c * kKC, at.t0 + half * (g.nt / 2),
-                                         cluster_map(bar, lead));
+                        if (half == 0) mbar_arrive_expect_tx(bar, 2 * kSub * x_bytes);  // of both CTAs
+#pragma unroll
+                        for (int h = 0; h < kSub; ++h)
+                            pair_tma_load_2d(sbase + s * stage_bytes + kSub * kWBytes + h * x_bytes, &map_x, (c * kSub + h) * kKC,
+                                             at.t0 + half * (g.nt / 2), cluster_map(bar, lead));
                     }
                     if (++s == stages) {
                         s = 0;
@@ -213,7 +226,7 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
         if (half == 0) {
             const uint32_t mask = 3u << lead;
             const uint64_t a0 = kBack ? tc::smem_desc_sw128(sbase, 8192, 1024) : tc::smem_desc_sw128(sbase, 0, 1024);
-            const uint64_t b0 = tc::smem_desc_sw128(sbase + kWBytes, 0, 1024);
+            const uint64_t b0 = tc::smem_desc_sw128(sbase + kSub * kWBytes, 0, 1024);
             constexpr uint32_t kStepA = kBack ? 2048 / 16 : 32 / 16, kStepB = 32 / 16;  // 16 of the contraction
             const bool issues = elect_one();
             uint32_t s = 0, ph = 0, buf = 0, acc_ph = 1;
@@ -228,8 +241,11 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                     if (issues) {
                         const uint32_t off = s * (stage_bytes / 16);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            pair_mma_f16(d, a0 + off + k * kStepA, b0 + off + k * kStepB, g.idesc, c > 0 || k > 0);
+                        for (int h = 0; h < kSub; ++h)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                pair_mma_f16(d, a0 + off + h * (kWBytes / 16) + k * kStepA,
+                                             b0 + off + h * (x_bytes / 16) + k * kStepB, g.idesc, c > 0 || h > 0 || k > 0);
                         pair_commit(smem_u32(&sh.empty[s]), mask);
                     }
                     __syncwarp();
@@ -246,25 +262,26 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
         }
         __syncwarp();
     } else if (warp >= 4) {
-        // A group of four warps takes every kGroups-th chunk, so that the steps of one chunk (codes that arrive, decoding,
-        // the stores' fence, the message) overlap with those of others. A thread has two blocks of a chunk. Forward: rows
-        // r and r + 64, block `sub` of two; back: row r, block `sub` of both 64-feature halves, which are operand blocks of
-        // their own.
+        // A group of four warps takes every kGroups-th stage, so that the steps of one stage (codes that arrive, decoding, the
+        // stores' fence, the message) overlap with those of others. A thread has two blocks of each 64 of the contraction.
+        // Forward: rows r and r + 64, block `sub` of two; back: row r, block `sub` of both 64-feature halves, which are
+        // operand blocks of their own.
         const int id = tid & 127, sub = id & 1, r = id >> 1, group = (warp - 4) >> 2;
         const uint32_t to = sbase + (uint32_t)(r >> 3) * 1024u + (uint32_t)(r & 7) * 128u;
         const uint32_t flip = (uint32_t)(4 * sub ^ (r & 7)) << 4;  // the first 16 bytes' place in their row; the others: ^ k
         const uint32_t full = cluster_map(smem_u32(&sh.full[0]), lead);
-        // The next chunk to ask for: number ac of tile ai. A thread's blocks lie at pc and pc + second; pos counts what may
+        // The next stage to ask for: number ac of tile ai. A thread's blocks lie at pc and pc + second; pos counts what may
         // end within a chunk (forward: blocks of the row; back: rows).
         const int64_t second = kBack ? 2 : 64 * g.blocks;
-        const int64_t step = kBack ? (int64_t)kGroups * kKC * g.blocks : kGroups * 2;
+        const int64_t next64 = kBack ? (int64_t)kKC * g.blocks : 2;  // from 64 of the contraction to the next
+        constexpr int kPos = kBack ? kKC : 2;
         const int64_t end = kBack ? g.rows : g.blocks;
         int64_t ai = 0, pos = 0;
         int ac = group;
         const uint8_t *pc = g.codes, *ps = g.scales;
         bool in0 = false, in1 = false;
         auto aim = [&]() {
-            while (ac >= per) {
+            while (ac >= per && ai < mine) {
                 ac -= per;
                 ++ai;
             }
@@ -273,7 +290,7 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                 return;
             }
             const Place at = place_of(g, cid + ai * ncl, half);
-            const int64_t c = c0 + ac;
+            const int64_t c = (int64_t)(c0 + ac) * kSub;
             const int64_t row = kBack ? c * kKC + r : at.f0 + r, blk = kBack ? at.f0 / kMx4Block + sub : 2 * c + sub;
             pos = kBack ? row : blk;
             in0 = kBack ? blk < g.blocks : row < g.rows;
@@ -283,25 +300,27 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
         };
         aim();
         struct Blocks {
-            uint4 w[2];
-            uint32_t b[2];
+            uint4 w[kBlocks];
+            uint32_t b[kBlocks];
         };
         auto ask = [&](Blocks& k) {
-            k.w[0] = k.w[1] = make_uint4(0, 0, 0, 0);
-            k.b[0] = k.b[1] = 0;
-            const bool in = pos < end;
-            if (in && in0) {
-                k.w[0] = ld_nc_v4(pc);
-                k.b[0] = __ldg(ps);
-            }
-            if (in && in1) {
-                k.w[1] = ld_nc_v4(pc + second * 16);
-                k.b[1] = __ldg(ps + second);
+#pragma unroll
+            for (int h = 0; h < kSub; ++h) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    k.w[2 * h + x] = make_uint4(0, 0, 0, 0);
+                    k.b[2 * h + x] = 0;
+                    if (pos + h * kPos < end && (x ? in1 : in0)) {
+                        const int64_t at = h * next64 + x * second;
+                        k.w[2 * h + x] = ld_nc_v4(pc + at * 16);
+                        k.b[2 * h + x] = __ldg(ps + at);
+                    }
+                }
             }
             ac += kGroups;
-            pos += kBack ? kGroups * kKC : kGroups * 2;
-            pc += step * 16;
-            ps += step;
+            pos += kGroups * kSub * kPos;
+            pc += kGroups * kSub * next64 * 16;
+            ps += kGroups * kSub * next64;
             if (ac >= per) aim();
         };
         Blocks next[kAhead];
@@ -315,9 +334,9 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                 const bool ok = wait(smem_u32(&sh.empty[s]), ph);
                 if (ok) {
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
+                    for (int x = 0; x < kBlocks; ++x) {
                         const uint32_t w[4] = {next[u].w[x].x, next[u].w[x].y, next[u].w[x].z, next[u].w[x].w}, b = next[u].b[x];
-                        const uint32_t at = to + s * stage_bytes + x * 8192u;
+                        const uint32_t at = to + s * stage_bytes + x * 8192u;  // (kWBytes for each 64 of the contraction)
                         if (mx4::plain(b) || (b != 255 && (w[0] | w[1] | w[2] | w[3]) == 0)) {  // (or nothing but zeros)
                             const uint32_t f = mx4::plain(b) ? mx4::factor2(b) : 0;
 #pragma unroll
@@ -389,7 +408,7 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                 }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(smem_u32(&sh.acc_empty[buf]), lead);
+            if (lane == 0) pair_arrive(cluster_map(smem_u32(&sh.acc_empty[buf]), lead));
             __syncwarp();
         }
         if (lane == 0) bulk_wait<0>();
@@ -447,7 +466,7 @@ bool encode_matrix(CUtensorMap* map, bool bf16, const void* p, int64_t rows, int
 // Clusters of `pairs` pairs that the device holds at once (asked once per kernel and device).
 constexpr int kMaxSplits = 4;
 template <typename K>
-int clusters_at_once(K kern, int pairs, int (&known)[64][kMaxSplits + 1]) {
+int clusters_at_once(K kern, int threads, int pairs, int (&known)[64][kMaxSplits + 1]) {
     const DeviceProps& p = device_props();
     const int d = p.device;
     if (d >= 0 && d < 64 && known[d][pairs]) return known[d][pairs];
@@ -457,7 +476,7 @@ int clusters_at_once(K kern, int pairs, int (&known)[64][kMaxSplits + 1]) {
     attr[0].val.clusterDim.x = 2 * pairs;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -475,34 +494,64 @@ int clusters_at_once(K kern, int pairs, int (&known)[64][kMaxSplits + 1]) {
 // 0.3 (the handshakes of a stage), from about 210 tokens on its products; a pass without splits 4.4 beside its chunks, and
 // its tiles follow each other; with splits, every wave of clusters begins anew and adds its sums.
 struct Shape {
-    int nt, splits;
+    int nt, splits, sub, at_once;
 };
 Shape choose(int64_t tokens, int64_t ftiles, int chunks, const int (&at_once)[kMaxSplits + 1]) {
-    Shape best{kMaxTokens, 1};
+    Shape best{kMaxTokens, 1, 1, at_once[1]};
     double least = 1e300;
     for (int nt = 32; nt <= kMaxTokens; nt += 32)
-        for (int s = 1; s <= kMaxSplits && s <= chunks; ++s) {
+        for (int s = 1; s <= kMaxSplits && s <= (nt <= kMaxTokens / 2 ? (chunks + 1) / 2 : chunks); ++s) {
             const int64_t tiles = ftiles * ((tokens + nt - 1) / nt), waves = (tiles + at_once[s] - 1) / at_once[s];
             const double chunk = 0.0014 * nt > 0.3 ? 0.0014 * nt : 0.3, steps = (chunks + s - 1) / s;
             const double t = s == 1 ? 4.4 + waves * (steps * chunk + 0.2) + 0.008 * nt
                                     : waves * (5.0 + 0.3 * s + 0.012 * nt + steps * chunk);
             if (t < least) {
                 least = t;
-                best = {nt, s};
+                best = {nt, s, nt <= kMaxTokens / 2 ? 2 : 1, at_once[s]};
             }
         }
     return best;
 }
 
-template <typename T, bool kBack>
-cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
+template <typename T, bool kBack, int kSub>
+cudaError_t run_shape(const Mx4Args& a, TileArgs& g, Shape shape, cudaStream_t s) {
     static bool done[64];
-    auto kern = mx4_tile_kernel<T, kBack>;
-    cudaError_t e = allow_smem(kern, kSmem, done);
+    auto kern = mx4_tile_kernel<T, kBack, kSub>;
+    const cudaError_t e = allow_smem(kern, kSmem, done);
     if (e != cudaSuccess) return e;
     constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
+    const int32_t C = kBack ? a.rows : a.cols;
+    g.nt = shape.nt;
+    g.chunks = (int32_t)(((int64_t)C + kSub * kKC - 1) / (kSub * kKC));
+    if (shape.splits > g.chunks) return cudaErrorInvalidValue;  // (a split without a chunk would have no sums)
+    g.stages = min((int)(kRing / (kSub * (kWBytes + shape.nt * 64))), kMaxStages);
+    g.tiles = (int64_t)g.ftiles * (((int64_t)a.tokens + shape.nt - 1) / shape.nt);
+    g.idesc = tc::instr_desc_f16(bf ? 1u : 0u, kBack ? 1u : 0u, 0u, 2 * kFeatures, (uint32_t)shape.nt);
+    g.err = device_error_word();
+    // (copies of operands whose rows were no whole 16 bytes have zeros, or room, behind their columns)
+    const int64_t C8 = ((int64_t)C + 7) / 8 * 8, F8 = ((int64_t)g.F + 7) / 8 * 8;
+    CUtensorMap mx, my;
+    if (!encode_matrix(&mx, bf, a.X, a.tokens, C8, a.ldx, kKC, shape.nt / 2, true) ||
+        !encode_matrix(&my, bf, a.Y, a.tokens, F8, a.ldy, 32, kOutTokens, false))
+        return cudaErrorInvalidValue;
+    const int c = 2 * shape.splits;
+    const int64_t clusters = shape.splits > 1 ? g.tiles : min64(g.tiles, shape.at_once);
+    if (clusters * c > 0x7fffffffll) return cudaErrorInvalidValue;
+    count_launches(1);
+    return launch_pdl_cluster(kern, dim3((unsigned)(clusters * c)), dim3(TileCfg<kSub>::kThreads), kSmem, (unsigned)c, s, g, mx,
+                              my);
+}
+
+template <typename T, bool kBack>
+cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
     if (!encode_fn()) return cudaErrorNotSupported;
-    const int32_t F = kBack ? a.cols : a.rows, C = kBack ? a.rows : a.cols;
+    static int known[64][kMaxSplits + 1];
+    static bool done[64];
+    const cudaError_t e = allow_smem(mx4_tile_kernel<T, kBack, 1>, kSmem, done);  // (before its clusters are counted)
+    if (e != cudaSuccess) return e;
+    int at_once[kMaxSplits + 1];
+    for (int i = 1; i <= kMaxSplits; ++i)  // (as many of the other kernel, which has the same shared memory)
+        at_once[i] = clusters_at_once(mx4_tile_kernel<T, kBack, 1>, TileCfg<1>::kThreads, i, known);
     TileArgs g;
     g.codes = a.codes;
     g.scales = a.scales;
@@ -510,30 +559,12 @@ cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
     g.ldy = a.ldy;
     g.blocks = mx4_blocks(a.cols);
     g.rows = a.rows;
-    g.F = F;
+    g.F = kBack ? a.cols : a.rows;
     g.tokens = a.tokens;
-    g.ftiles = (int32_t)(((int64_t)F + 2 * kFeatures - 1) / (2 * kFeatures));
-    g.chunks = (int32_t)(((int64_t)C + kKC - 1) / kKC);
-    static int known[64][kMaxSplits + 1];
-    int at_once[kMaxSplits + 1];
-    for (int i = 1; i <= kMaxSplits; ++i) at_once[i] = clusters_at_once(kern, i, known);
-    const Shape shape = choose(a.tokens, g.ftiles, g.chunks, at_once);
-    g.nt = shape.nt;
-    g.stages = min((int)(kRing / (kWBytes + shape.nt * 64)), kMaxStages);
-    g.tiles = (int64_t)g.ftiles * (((int64_t)a.tokens + shape.nt - 1) / shape.nt);
-    g.idesc = tc::instr_desc_f16(bf ? 1u : 0u, kBack ? 1u : 0u, 0u, 2 * kFeatures, (uint32_t)shape.nt);
-    g.err = device_error_word();
-    CUtensorMap mx, my;
-    // (copies of operands whose rows were no whole 16 bytes have zeros, or room, behind their columns)
-    const int64_t C8 = ((int64_t)C + 7) / 8 * 8, F8 = ((int64_t)F + 7) / 8 * 8;
-    if (!encode_matrix(&mx, bf, a.X, a.tokens, C8, a.ldx, kKC, shape.nt / 2, true) ||
-        !encode_matrix(&my, bf, a.Y, a.tokens, F8, a.ldy, 32, kOutTokens, false))
-        return cudaErrorInvalidValue;
-    const int c = 2 * shape.splits;
-    const int64_t clusters = shape.splits > 1 ? g.tiles : min64(g.tiles, at_once[1]);
-    if (clusters * c > 0x7fffffffll) return cudaErrorInvalidValue;
-    count_launches(1);
-    return launch_pdl_cluster(kern, dim3((unsigned)(clusters * c)), dim3(kThreads), kSmem, (unsigned)c, s, g, mx, my);
+    g.ftiles = (int32_t)(((int64_t)g.F + 2 * kFeatures - 1) / (2 * kFeatures));
+    const int64_t C = kBack ? a.rows : a.cols;
+    Shape shape = choose(a.tokens, g.ftiles, (int)((C + kKC - 1) / kKC), at_once);
+    return shape.sub == 1 ? run_shape<T, kBack, 1>(a, g, shape, s) : run_shape<T, kBack, 2>(a, g, shape, s);
 }
 
 }  // namespace
