@@ -59,7 +59,9 @@ def test_product_refusals(lib, back):
         assert product(lib, back, **bad) == 1, bad
         assert lib.spops_last_error()
     odd = dict(X=0x100002, tokens=20, ldx=72, ldy=72)  # rows that need a copy
-    need = lib.spops_mx4_workspace_size(20, 64, 64)
+    need = lib.spops_mx4_workspace_size(20, 64, 64, 2)
+    assert lib.spops_mx4_workspace_size(20, 64, 64, 0) >= 20 * 64 * (3 * 2 + 4) and lib.spops_mx4_workspace_size(-1, 64, 64, 2) == 0
+    assert product(lib, back, dtype=0) == 3
     assert need >= 2 * 20 * 64 * 2
     for bad in (dict(), dict(ws=0x500000, size=need - 1), dict(ws=0x500008, size=need)):
         assert product(lib, back, **odd, **bad) == 3, bad

@@ -60,7 +60,7 @@ SIGNATURES = {
     "spops_lora_grad_block": (_INT, [_P]),
     "spops_mx4_quantize": (_INT, [_P, _I64, _INT, _I32, _I32, _P, _P, _P]),
     "spops_mx4_dequantize": (_INT, [_P, _P, _I32, _I32, _P, _I64, _INT, _P]),
-    "spops_mx4_workspace_size": (_SZ, [_I32, _I32, _I32]),
+    "spops_mx4_workspace_size": (_SZ, [_I32, _I32, _I32, _INT]),
     "spops_mx4_linear": (_INT, [_P]),
     "spops_mx4_linear_grad": (_INT, [_P]),
     "spops_dropout": (_INT, [_P]),

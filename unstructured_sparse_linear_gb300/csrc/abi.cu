@@ -808,9 +808,10 @@ int spops_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t ro
                        "mx4_dequantize launch");
 }
 
-size_t spops_mx4_workspace_size(int32_t tokens, int32_t in_features, int32_t out_features) {
-    if (tokens < 0 || in_features < 0 || out_features < 0) return 0;
-    const size_t n = mx4_copy_bytes(tokens, in_features) + mx4_copy_bytes(tokens, out_features);
+size_t spops_mx4_workspace_size(int32_t tokens, int32_t in_features, int32_t out_features, int dtype) {
+    if (tokens < 0 || in_features < 0 || out_features < 0 || dtype < SPOPS_F32 || dtype > SPOPS_BF16) return 0;
+    const int64_t es = (int64_t)dtype_size(dtype);
+    const size_t n = mx4_x_bytes(tokens, in_features, es) + mx4_y_bytes(tokens, out_features, es);
     return n > 16 ? n : 16;
 }
 
@@ -841,9 +842,9 @@ static int mx4_product(const spops_mx4_args* a, bool back) {
     m.rows = a->rows;
     m.cols = a->cols;
     if (mx4_needs_copies(a->dtype, back, m)) {
-        const size_t need = spops_mx4_workspace_size(a->tokens, in, out);
+        const size_t need = spops_mx4_workspace_size(a->tokens, in, out, a->dtype);
         if (!a->workspace || !aligned(a->workspace, 16) || a->ws_bytes < need)
-            return fail(SPOPS_ERR_WORKSPACE, "rows that are no whole aligned 16 bytes need a 16-byte aligned workspace of %zu bytes (got %zu)",
+            return fail(SPOPS_ERR_WORKSPACE, "fp32, or rows that are no whole aligned 16 bytes, need a 16-byte aligned workspace of %zu bytes (got %zu)",
                         need, (size_t)a->ws_bytes);
         if (overlaps(a->workspace, need, a->Y, yb) || overlaps(a->workspace, need, a->X, ((size_t)(a->tokens - 1) * m.ldx + in) * es) ||
             overlaps(a->workspace, need, a->codes, blocks * 16) || overlaps(a->workspace, need, a->scales, blocks))

@@ -255,21 +255,49 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_flat_kernel(const uin
     }
 }
 
-// Rows of 16-bit values, zeros behind the last column.
-__global__ void __launch_bounds__(kThreads) mx4_copy_kernel(const uint16_t* from, int64_t ldf, uint16_t* to, int64_t ldt,
-                                                            int64_t rows, int64_t cols, int64_t cols_to) {
+// Rows, zeros behind the last column.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) mx4_copy_kernel(const T* from, int64_t ldf, T* to, int64_t ldt, int64_t rows,
+                                                            int64_t cols, int64_t cols_to) {
     pdl_trigger();
     pdl_wait();
     for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
         for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < cols_to; c += (int64_t)gridDim.x * kThreads)
-            to[r * ldt + c] = c < cols ? from[r * ldf + c] : (uint16_t)0;
+            to[r * ldt + c] = c < cols ? from[r * ldf + c] : (T)0;
+}
+
+// fp32 as the sum of three bf16 parts, rounded towards zero but for the last: 8 bits each, all 24 of a number. part: columns
+// of a part. Infinities and NaN are their first part, beside zeros.
+__global__ void __launch_bounds__(kThreads) mx4_split_kernel(const float* from, int64_t ldf, uint16_t* to, int64_t rows,
+                                                             int64_t cols, int64_t part) {
+    pdl_trigger();
+    pdl_wait();
+    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
+        for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < part; c += (int64_t)gridDim.x * kThreads) {
+            const float x = c < cols ? from[r * ldf + c] : 0.f;
+            const bool finite = fabsf(x) <= 3.402823466e38f;
+            const float a = finite ? __uint_as_float(__float_as_uint(x) & 0xffff0000u) : x;
+            const float y = finite ? x - a : 0.f, b = __uint_as_float(__float_as_uint(y) & 0xffff0000u);
+            const float parts[3] = {a, b, y - b};
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const __nv_bfloat16 h = __float2bfloat16_rn(parts[i]);
+                to[r * 3 * part + i * part + c] = reinterpret_cast<const uint16_t&>(h);
+            }
+        }
+}
+
+dim3 copy_grid(int64_t rows, int64_t cols) {
+    return dim3((unsigned)min64((cols + kThreads - 1) / kThreads, 1024), (unsigned)min64(rows, 4096));
 }
 cudaError_t copy_rows(const void* from, int64_t ldf, void* to, int64_t ldt, int64_t rows, int64_t cols, int64_t cols_to,
-                      cudaStream_t s) {
+                      int64_t es, cudaStream_t s) {
     count_launches(1);
-    return launch_pdl(mx4_copy_kernel, dim3((unsigned)min64((cols_to + kThreads - 1) / kThreads, 1024), (unsigned)min64(rows, 4096)),
-                      dim3(kThreads), 0, s, static_cast<const uint16_t*>(from), ldf, static_cast<uint16_t*>(to), ldt, rows, cols,
-                      cols_to);
+    if (es == 4)
+        return launch_pdl(mx4_copy_kernel<float>, copy_grid(rows, cols_to), dim3(kThreads), 0, s, static_cast<const float*>(from), ldf,
+                          static_cast<float*>(to), ldt, rows, cols, cols_to);
+    return launch_pdl(mx4_copy_kernel<uint16_t>, copy_grid(rows, cols_to), dim3(kThreads), 0, s,
+                      static_cast<const uint16_t*>(from), ldf, static_cast<uint16_t*>(to), ldt, rows, cols, cols_to);
 }
 
 unsigned walk_grid(const Walk& w) {
@@ -326,36 +354,43 @@ cudaError_t launch_mx4_dequantize(int dt, const uint8_t* codes, const uint8_t* s
 }
 
 bool mx4_needs_copies(int dt, bool back, const Mx4Args& a) {
-    if (dt == kF32 || a.rows == 0 || a.cols == 0 || (!back && a.tokens <= kMx4FewTokens)) return false;
-    const int64_t in = back ? a.rows : a.cols, out = back ? a.cols : a.rows;
-    return !mx4_tile_rows(a.X, a.ldx, in) || !mx4_tile_rows(a.Y, a.ldy, out);
+    if (a.rows == 0 || a.cols == 0 || (!back && dt != kF32 && a.tokens <= kMx4FewTokens)) return false;
+    const int64_t in = back ? a.rows : a.cols, out = back ? a.cols : a.rows, es = (int64_t)dtype_size(dt);
+    return dt == kF32 || !mx4_tile_rows(a.X, a.ldx, in, es) || !mx4_tile_rows(a.Y, a.ldy, out, es);
 }
 
 cudaError_t launch_mx4_product(int dt, bool back, const Mx4Args& a, void* workspace, cudaStream_t s) {
-    const int64_t in = back ? a.rows : a.cols, out = back ? a.cols : a.rows;
+    const int64_t in = back ? a.rows : a.cols, out = back ? a.cols : a.rows, es = (int64_t)dtype_size(dt);
     if (in == 0)  // nothing to sum
-        return cudaMemset2DAsync(a.Y, (size_t)a.ldy * dtype_size(dt), 0, (size_t)out * dtype_size(dt), (size_t)a.tokens, s);
-    if (dt == kF32) return launch_mx4_general(back, a, s);
-    // 4096 x 4096, bf16: 1 token 6.8 us (8.0 with the kernel for eight, 12.5 with tiles), 8 tokens 8.0 (tiles 12.5), 16 tokens
-    // 12.5 with tiles (two passes of eight 16); 11008 x 4096: 12.9 (20.6, 25), 21 (25), 25.
-    if (!back && a.tokens == 1) return launch_mx4_vec(dt, a, s);
-    if (!back && a.tokens <= kMx4FewTokens) return launch_mx4_rows(dt, a, s);
+        return cudaMemset2DAsync(a.Y, (size_t)(a.ldy * es), 0, (size_t)(out * es), (size_t)a.tokens, s);
+    // bf16, 4096 x 4096: 1 token 6.4 us (8.0 with the kernel for eight, 11.6 with tiles), 8 tokens 8.0 (tiles 11.6), 16 tokens
+    // 11.6 with tiles (two passes of eight 16); 11008 x 4096: 12.6 (20.8, 21), 21 (21), 22. 4096 x 11008: 14.4 (18.5, 27).
+    if (!back && dt != kF32 && a.tokens == 1) return launch_mx4_vec(dt, a, s);
+    if (!back && dt != kF32 && a.tokens <= kMx4FewTokens) return launch_mx4_rows(dt, a, s);
     Mx4Args t = a;
     cudaError_t e = cudaSuccess;
     char* ws = static_cast<char*>(workspace);
-    if (!mx4_tile_rows(a.X, a.ldx, in)) {
+    if (dt == kF32) {
+        const int64_t part = mx4_split_cols(in) / 3;
+        t.X = ws;
+        t.ldx = 3 * part;
+        count_launches(1);
+        e = launch_pdl(mx4_split_kernel, copy_grid(a.tokens, part), dim3(kThreads), 0, s, static_cast<const float*>(a.X), a.ldx,
+                       reinterpret_cast<uint16_t*>(ws), (int64_t)a.tokens, in, part);
+        ws += mx4_x_bytes(a.tokens, in, es);
+    } else if (!mx4_tile_rows(a.X, a.ldx, in, es)) {
         t.X = ws;
         t.ldx = (in + 7) / 8 * 8;
-        e = copy_rows(a.X, a.ldx, ws, t.ldx, a.tokens, in, t.ldx, s);
-        ws += mx4_copy_bytes(a.tokens, in);
+        e = copy_rows(a.X, a.ldx, ws, t.ldx, a.tokens, in, t.ldx, es, s);
+        ws += mx4_x_bytes(a.tokens, in, es);
     }
-    const bool own = mx4_tile_rows(a.Y, a.ldy, out);
+    const bool own = mx4_tile_rows(a.Y, a.ldy, out, es);
     if (!own) {
         t.Y = ws;
-        t.ldy = (out + 7) / 8 * 8;
+        t.ldy = (out * es + 15) / 16 * 16 / es;
     }
     if (e == cudaSuccess) e = launch_mx4_tiles(dt, back, t, s);
-    if (e == cudaSuccess && !own) e = copy_rows(t.Y, t.ldy, a.Y, a.ldy, a.tokens, out, out, s);
+    if (e == cudaSuccess && !own) e = copy_rows(t.Y, t.ldy, a.Y, a.ldy, a.tokens, out, out, es, s);
     return e;
 }
 

@@ -29,23 +29,24 @@ cudaError_t launch_mx4_quantize(int dt, const void* X, int64_t ldx, int32_t rows
 cudaError_t launch_mx4_dequantize(int dt, const uint8_t* codes, const uint8_t* scales, int32_t rows, int32_t cols,
                                   void* Y, int64_t ldy, cudaStream_t s);
 
-// fp32, any size and alignment, on the CUDA cores.
-cudaError_t launch_mx4_general(bool back, const Mx4Args& a, cudaStream_t s);
-
 // fp16 / bf16. Forward for one token, and for up to eight (any alignment):
 cudaError_t launch_mx4_vec(int dt, const Mx4Args& a, cudaStream_t s);
 cudaError_t launch_mx4_rows(int dt, const Mx4Args& a, cudaStream_t s);
-// On the tcgen05 tensor cores, where mx4_tile_rows holds for X and Y.
+// On the tcgen05 tensor cores, where mx4_tile_rows holds for X and Y. fp32: X is its three bf16 parts, mx4_split_cols
+// columns, each part's behind the others'.
 cudaError_t launch_mx4_tiles(int dt, bool back, const Mx4Args& a, cudaStream_t s);
 
-// Rows of 16-bit values as TMA loads and stores them: rows and addresses on 16-byte boundaries, whole 16 bytes (a store
-// writes no less).
-inline bool mx4_tile_rows(const void* p, int64_t ld, int64_t cols) {
-    return cols % 8 == 0 && ld % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld < (1ll << 38);
+// Rows as TMA loads and stores them: rows and addresses on 16-byte boundaries, whole 16 bytes (a store writes no less).
+inline bool mx4_tile_rows(const void* p, int64_t ld, int64_t cols, int64_t es) {
+    return cols * es % 16 == 0 && ld * es % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld < (1ll << 37);
 }
-// Bytes of copies of X [tokens, in] and Y [tokens, out] with such rows.
-inline size_t mx4_copy_bytes(int64_t tokens, int64_t cols) {
-    return ((size_t)tokens * (size_t)((cols + 7) / 8 * 8) * 2 + 255) / 256 * 256;
+inline int64_t mx4_split_cols(int64_t cols) { return 3 * ((cols + 63) / 64 * 64); }
+// Bytes of a copy of Y [tokens, cols] with such rows, and of X (fp32: of its parts).
+inline size_t mx4_y_bytes(int64_t tokens, int64_t cols, int64_t es) {
+    return ((size_t)tokens * (size_t)((cols * es + 15) / 16 * 16) + 255) / 256 * 256;
+}
+inline size_t mx4_x_bytes(int64_t tokens, int64_t cols, int64_t es) {
+    return es == 4 ? mx4_y_bytes(tokens, mx4_split_cols(cols), 2) : mx4_y_bytes(tokens, cols, es);
 }
 
 // The dispatch between the kernels. workspace: for the operands that need a copy (mx4_needs_copies).

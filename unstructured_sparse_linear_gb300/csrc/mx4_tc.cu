@@ -1,13 +1,15 @@
-// Products with a microscaled 4-bit weight on the tcgen05 tensor cores (fp16 / bf16, rows of 16 bytes).
+// Products with a microscaled 4-bit weight on the tcgen05 tensor cores (rows of whole 16 bytes).
 //
 // mx4_tile_kernel  Y[t, f] = sum over c of X[t, c] V(f, c), V = W (forward: f a row of W, c a column) or its transpose
 //                  (back: the input gradient).
 //
-// The weight is the A operand (128 features x 64 of the contraction, decoded from 4 bits to X's type by eight warps: exact),
+// The weight is the A operand (128 features x 64 of the contraction, decoded from 4 bits to X's type by groups of four warps),
 // X the B operand (nt tokens x 64, by TMA), so D is features x tokens. Two CTAs form a pair (cta_group::2): 256 features,
 // each CTA decodes its own 128 and holds half of the tokens' rows, so a value is decoded once per nt tokens and X is read
 // from L2 once per 256 features. Forward, a row's codes run along the contraction: the operand is K-major; back, they run
 // along the features: the same decoding writes an MN-major operand, and no code is ever transposed.
+// fp32: the weight's values are bf16 numbers, and X is the sum of three bf16 parts (all 24 bits), which multiply the same
+// decoded weight into the same fp32 sums.
 #include <type_traits>
 
 #include "internal.h"
@@ -25,20 +27,21 @@ constexpr uint32_t kWBytes = kFeatures * 128;  // of 64 of the contraction
 constexpr uint32_t kRing = 6 * (kWBytes + kMaxTokens / 2 * 128);
 constexpr int kMaxStages = 10;
 constexpr int kOutTokens = 32;  // of a store: 32 x 32 values
-constexpr uint32_t kOutBytes = kOutTokens * 32 * 2;
-constexpr uint32_t kOutAt = kRing, kBarsAt = kOutAt + 4 * 2 * kOutBytes;
-constexpr uint32_t kSmem = kBarsAt + 1024;
+constexpr uint32_t kOutAt = kRing;
 constexpr int kAhead = 1;  // stages whose codes a decoder has under way
 
 // A stage holds kSub times 64 of the contraction: one, or two where the products of 64 take less time than the messages of a
-// stage (up to 128 tokens). Warps 0 to 3 finish (a TMEM lane quarter each), then kGroups groups of four decode, one warp
-// loads X, one multiplies.
-template <int kSub>
+// stage (up to 128 tokens), and X in kParts parts. Warps 0 to 3 finish (a TMEM lane quarter each), then kGroups groups of
+// four decode, one warp loads X, one multiplies.
+template <typename Out, int kSub>
 struct TileCfg {
-    static constexpr int kGroups = kSub == 1 ? 6 : 4;
+    static constexpr int kParts = sizeof(Out) == 4 ? 3 : 1;
+    static constexpr int kGroups = kSub == 1 && kParts == 1 ? 6 : 4;
     static constexpr int kLoadWarp = 4 + 4 * kGroups, kMmaWarp = kLoadWarp + 1, kThreads = 32 * (kMmaWarp + 1);
-    static constexpr int kTokens = kSub == 1 ? kMaxTokens : kMaxTokens / 2;  // at most
-    static_assert(kGroups <= (int)(kRing / (kSub * (kWBytes + kTokens * 64))), "a group's next stage is at most one round of the ring away");
+    static constexpr int kTokens = kSub == 1 && kParts == 1 ? kMaxTokens : kMaxTokens / 2;  // at most
+    static constexpr uint32_t kOutBytes = kOutTokens * 32 * sizeof(Out), kBarsAt = kOutAt + 4 * 2 * kOutBytes, kSmem = kBarsAt + 1024;
+    static_assert(kGroups <= (int)(kRing / (kSub * (kWBytes + kParts * kTokens * 64))), "a group's next stage is at most one round of the ring away");
+    static_assert(kTokens * kFeatures * 4u <= kRing, "the partial sums fit");
 };
 
 // ------------------------------------------------------------------ PTX of CTA pairs
@@ -111,7 +114,7 @@ __device__ __forceinline__ Place place_of(const TileArgs& g, int64_t tile, int h
 
 // Waits of a pair. What the barriers announce is read by the tensor core and by TMA or lies in TMEM, so no wait makes
 // the thread's own loads see another CTA's memory: an acquire of the cluster's scope empties the SM's L1 each time
-// (8192 tokens, 2048 -> 8192: TBD1 us against TBD2).
+// (with other steps' help, 8192 tokens, 2048 -> 8192 203 us with it and 197 without).
 struct PairWaits {
     volatile int* failed;
     int* err;
@@ -143,11 +146,12 @@ __device__ __forceinline__ bool elect_one() {
 
 // A cluster is one pair, or S pairs that split a tile's contraction; in the second case (one tile per cluster) the fp32
 // partial sums meet in shared memory and are added in the order of the splits.
-template <typename T, bool kBack, int kSub>
-__global__ void __launch_bounds__(TileCfg<kSub>::kThreads, 1)
+template <typename T, typename Out, bool kBack, int kSub>
+__global__ void __launch_bounds__(TileCfg<Out, kSub>::kThreads, 1)
 mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_y) {
-    constexpr int kLoadWarp = TileCfg<kSub>::kLoadWarp, kMmaWarp = TileCfg<kSub>::kMmaWarp, kThreads = TileCfg<kSub>::kThreads;
-    constexpr int kGroups = TileCfg<kSub>::kGroups, kBlocks = 2 * kSub;  // blocks of a decoder and stage
+    using Cfg = TileCfg<Out, kSub>;
+    constexpr int kLoadWarp = Cfg::kLoadWarp, kMmaWarp = Cfg::kMmaWarp, kThreads = Cfg::kThreads, kParts = Cfg::kParts;
+    constexpr int kGroups = Cfg::kGroups, kBlocks = 2 * kSub;  // blocks of a decoder and stage
     // No static shared memory, so the dynamic part starts on the 1 KB boundary that the swizzled tiles need (checked).
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     struct Shared {
@@ -155,15 +159,15 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
         uint32_t tmem;
         volatile int failed;
     };
-    static_assert(sizeof(Shared) <= kSmem - kBarsAt, "barriers");
-    Shared& sh = *reinterpret_cast<Shared*>(smem_raw + kBarsAt);
+    static_assert(sizeof(Shared) <= Cfg::kSmem - Cfg::kBarsAt, "barriers");
+    Shared& sh = *reinterpret_cast<Shared*>(smem_raw + Cfg::kBarsAt);
     const uint32_t sbase = smem_u32(smem_raw);
     if (sbase & 1023u) {  // the same on every CTA
         record_error(g.err, kDevErrSmemAlign);
         return;
     }
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t stages = g.stages, x_bytes = (uint32_t)g.nt * 64, stage_bytes = kSub * (kWBytes + x_bytes);
+    const uint32_t stages = g.stages, x_bytes = (uint32_t)g.nt * 64, stage_bytes = kSub * (kWBytes + kParts * x_bytes);
     const int C = (int)cluster_size(), crank = (int)cluster_rank();
     const int half = crank & 1, lead = crank & ~1, split = crank >> 1, splits = C >> 1;
     const int64_t cid = blockIdx.x / C, ncl = gridDim.x / C;
@@ -205,11 +209,12 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                 for (int c = c0; c < c1; ++c) {
                     if (wait(smem_u32(&sh.empty[s]), ph)) {
                         const uint32_t bar = smem_u32(&sh.full[s]);
-                        if (half == 0) mbar_arrive_expect_tx(bar, 2 * kSub * x_bytes);  // of both CTAs
+                        if (half == 0) mbar_arrive_expect_tx(bar, 2 * kSub * kParts * x_bytes);  // of both CTAs
 #pragma unroll
-                        for (int h = 0; h < kSub; ++h)
-                            pair_tma_load_2d(sbase + s * stage_bytes + kSub * kWBytes + h * x_bytes, &map_x, (c * kSub + h) * kKC,
-                                             at.t0 + half * (g.nt / 2), cluster_map(bar, lead));
+                        for (int h = 0; h < kSub * kParts; ++h)  // (the parts of X lie one behind the other)
+                            pair_tma_load_2d(sbase + s * stage_bytes + kSub * kWBytes + h * x_bytes, &map_x,
+                                             (kParts == 1 ? c * kSub + h : c + h * g.chunks) * kKC, at.t0 + half * (g.nt / 2),
+                                             cluster_map(bar, lead));
                     }
                     if (++s == stages) {
                         s = 0;
@@ -241,10 +246,10 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                     if (issues) {
                         const uint32_t off = s * (stage_bytes / 16);
 #pragma unroll
-                        for (int h = 0; h < kSub; ++h)
+                        for (int h = 0; h < kSub * kParts; ++h)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                pair_mma_f16(d, a0 + off + h * (kWBytes / 16) + k * kStepA,
+                                pair_mma_f16(d, a0 + off + (kParts == 1 ? h : 0) * (kWBytes / 16) + k * kStepA,
                                              b0 + off + h * (x_bytes / 16) + k * kStepB, g.idesc, c > 0 || h > 0 || k > 0);
                         pair_commit(smem_u32(&sh.empty[s]), mask);
                     }
@@ -387,15 +392,19 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                         for (int e = 0; e < 32; ++e)
                             asm volatile("st.shared.f32 [%0], %1;" ::"r"(p + e * kFeatures * 4), "f"(y[e]) : "memory");
                     } else if (f < g.F) {
-                        const uint32_t st = sbase + kOutAt + (uint32_t)(warp * 2 + (stores & 1)) * kOutBytes;
+                        const uint32_t st = sbase + kOutAt + (uint32_t)(warp * 2 + (stores & 1)) * Cfg::kOutBytes;
                         if (lane == 0) bulk_wait_read<1>();  // the store before the last has left this buffer
                         __syncwarp();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            const T t = Elt<T>::from_f(y[e]);
-                            asm volatile("st.shared.b16 [%0], %1;" ::"r"(st + e * 64 + lane * 2),
-                                         "h"(reinterpret_cast<const uint16_t&>(t))
-                                         : "memory");
+                            if constexpr (sizeof(Out) == 4) {
+                                asm volatile("st.shared.f32 [%0], %1;" ::"r"(st + e * 128 + lane * 4), "f"(y[e]) : "memory");
+                            } else {
+                                const Out t = Elt<Out>::from_f(y[e]);
+                                asm volatile("st.shared.b16 [%0], %1;" ::"r"(st + e * 64 + lane * 2),
+                                             "h"(reinterpret_cast<const uint16_t&>(t))
+                                             : "memory");
+                            }
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
@@ -431,13 +440,14 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                     y[2] += p.z;
                     y[3] += p.w;
                 }
-                T* out = static_cast<T*>(g.Y) + (int64_t)(at.t0 + t) * g.ldy + f;
+                Out* out = static_cast<Out*>(g.Y) + (int64_t)(at.t0 + t) * g.ldy + f;
                 if (f + 4 <= g.F) {  // (rows begin on 16-byte boundaries)
-                    *reinterpret_cast<uint2*>(out) = make_uint2(Elt<T>::p2(y[0], y[1]), Elt<T>::p2(y[2], y[3]));
+                    if constexpr (sizeof(Out) == 4) *reinterpret_cast<float4*>(out) = make_float4(y[0], y[1], y[2], y[3]);
+                    else *reinterpret_cast<uint2*>(out) = make_uint2(Elt<Out>::p2(y[0], y[1]), Elt<Out>::p2(y[2], y[3]));
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (f + e < g.F) out[e] = Elt<T>::from_f(y[e]);
+                        if (f + e < g.F) out[e] = Elt<Out>::from_f(y[e]);
                 }
             }
     }
@@ -452,13 +462,17 @@ mx4_tile_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
 
 // ------------------------------------------------------------------ host side
 
-// Map of a row-strided matrix of 16-bit elements in boxes of box_cols x box_rows, with the 128-byte swizzle or without.
-bool encode_matrix(CUtensorMap* map, bool bf16, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_cols,
-                   int box_rows, bool swizzle) {
-    const cuuint64_t d[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, st[1] = {(cuuint64_t)ld * 2};
+template <typename T>
+constexpr CUtensorMapDataType kMapType = sizeof(T) == 4                          ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                         : std::is_same<T, __nv_bfloat16>::value ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+// Map of a row-strided matrix in boxes of box_cols x box_rows, with the 128-byte swizzle or without.
+template <typename T>
+bool encode_matrix(CUtensorMap* map, const void* p, int64_t rows, int64_t cols, int64_t ld, int box_cols, int box_rows,
+                   bool swizzle) {
+    const cuuint64_t d[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, st[1] = {(cuuint64_t)ld * sizeof(T)};
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, elem[2] = {1, 1};
-    return encode_fn()(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-                       const_cast<void*>(p), d, st, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return encode_fn()(map, kMapType<T>, 2, const_cast<void*>(p), d, st, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
                        swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -466,7 +480,7 @@ bool encode_matrix(CUtensorMap* map, bool bf16, const void* p, int64_t rows, int
 // Clusters of `pairs` pairs that the device holds at once (asked once per kernel and device).
 constexpr int kMaxSplits = 4;
 template <typename K>
-int clusters_at_once(K kern, int threads, int pairs, int (&known)[64][kMaxSplits + 1]) {
+int clusters_at_once(K kern, int threads, uint32_t smem, int pairs, int (&known)[64][kMaxSplits + 1]) {
     const DeviceProps& p = device_props();
     const int d = p.device;
     if (d >= 0 && d < 64 && known[d][pairs]) return known[d][pairs];
@@ -477,7 +491,7 @@ int clusters_at_once(K kern, int threads, int pairs, int (&known)[64][kMaxSplits
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(2 * pairs);
     cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
@@ -489,69 +503,74 @@ int clusters_at_once(K kern, int threads, int pairs, int (&known)[64][kMaxSplits
     return n;
 }
 
-// Tokens per tile and splits of the contraction with the least estimated time in us, fitted to sweeps over both (64 to
-// 11008 features, 6 to 172 chunks, 16 to 8192 tokens; the choice is within a tenth of the best of a sweep): a chunk takes
-// 0.3 (the handshakes of a stage), from about 210 tokens on its products; a pass without splits 4.4 beside its chunks, and
-// its tiles follow each other; with splits, every wave of clusters begins anew and adds its sums.
+// Tokens per tile and splits of the contraction with the least estimated time in us, fitted to sweeps over both (384 to
+// 11008 features, 6 to 172 chunks, 9 to 8192 tokens; the choice is within a tenth of the best of a sweep): 64 of the
+// contraction take 0.265 with two of them a stage and 0.3 with one, or their products; a pass without splits 4.4 beside
+// that, and its tiles follow each other; with splits, every wave of clusters begins anew and adds its sums.
 struct Shape {
     int nt, splits, sub, at_once;
 };
-Shape choose(int64_t tokens, int64_t ftiles, int chunks, const int (&at_once)[kMaxSplits + 1]) {
-    Shape best{kMaxTokens, 1, 1, at_once[1]};
+Shape choose(int64_t tokens, int64_t ftiles, int chunks, int parts, const int (&at_once)[kMaxSplits + 1]) {
+    const int most = parts == 1 ? kMaxTokens : kMaxTokens / 2;
+    Shape best{most, 1, 1, at_once[1]};
     double least = 1e300;
-    for (int nt = 32; nt <= kMaxTokens; nt += 32)
-        for (int s = 1; s <= kMaxSplits && s <= (nt <= kMaxTokens / 2 ? (chunks + 1) / 2 : chunks); ++s) {
+    for (int nt = 32; nt <= most; nt += 32) {
+        const int sub = parts == 1 && nt <= kMaxTokens / 2 ? 2 : 1, stages = (chunks + sub - 1) / sub;
+        for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
             const int64_t tiles = ftiles * ((tokens + nt - 1) / nt), waves = (tiles + at_once[s] - 1) / at_once[s];
-            const double chunk = 0.0014 * nt > 0.3 ? 0.0014 * nt : 0.3, steps = (chunks + s - 1) / s;
-            const double t = s == 1 ? 4.4 + waves * (steps * chunk + 0.2) + 0.008 * nt
-                                    : waves * (5.0 + 0.3 * s + 0.012 * nt + steps * chunk);
+            const double products = 0.0014 * nt * parts, least64 = sub == 2 ? 0.265 : 0.3;
+            const double stage = sub * (products > least64 ? products : least64), steps = (stages + s - 1) / s;
+            const double t = s == 1 ? 4.4 + waves * (steps * stage + 0.2) + 0.008 * nt
+                                    : waves * (5.0 + 0.3 * s + 0.012 * nt + steps * stage);
             if (t < least) {
                 least = t;
-                best = {nt, s, nt <= kMaxTokens / 2 ? 2 : 1, at_once[s]};
+                best = {nt, s, sub, at_once[s]};
             }
         }
+    }
     return best;
 }
 
-template <typename T, bool kBack, int kSub>
+template <typename T, typename Out, bool kBack, int kSub>
 cudaError_t run_shape(const Mx4Args& a, TileArgs& g, Shape shape, cudaStream_t s) {
+    using Cfg = TileCfg<Out, kSub>;
     static bool done[64];
-    auto kern = mx4_tile_kernel<T, kBack, kSub>;
-    const cudaError_t e = allow_smem(kern, kSmem, done);
+    auto kern = mx4_tile_kernel<T, Out, kBack, kSub>;
+    const cudaError_t e = allow_smem(kern, Cfg::kSmem, done);
     if (e != cudaSuccess) return e;
-    constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
     const int32_t C = kBack ? a.rows : a.cols;
     g.nt = shape.nt;
     g.chunks = (int32_t)(((int64_t)C + kSub * kKC - 1) / (kSub * kKC));
     if (shape.splits > g.chunks) return cudaErrorInvalidValue;  // (a split without a chunk would have no sums)
-    g.stages = min((int)(kRing / (kSub * (kWBytes + shape.nt * 64))), kMaxStages);
+    g.stages = min((int)(kRing / (kSub * (kWBytes + Cfg::kParts * shape.nt * 64))), kMaxStages);
     g.tiles = (int64_t)g.ftiles * (((int64_t)a.tokens + shape.nt - 1) / shape.nt);
-    g.idesc = tc::instr_desc_f16(bf ? 1u : 0u, kBack ? 1u : 0u, 0u, 2 * kFeatures, (uint32_t)shape.nt);
+    g.idesc = tc::instr_desc_f16(std::is_same<T, __nv_bfloat16>::value ? 1u : 0u, kBack ? 1u : 0u, 0u, 2 * kFeatures, (uint32_t)shape.nt);
     g.err = device_error_word();
-    // (copies of operands whose rows were no whole 16 bytes have zeros, or room, behind their columns)
-    const int64_t C8 = ((int64_t)C + 7) / 8 * 8, F8 = ((int64_t)g.F + 7) / 8 * 8;
+    // (rows of whole 16 bytes: copies of others have zeros, or room, behind their columns)
+    const int64_t x_cols = Cfg::kParts > 1 ? mx4_split_cols(C) : ((int64_t)C + 7) / 8 * 8, y16 = 16 / (int64_t)sizeof(Out);
     CUtensorMap mx, my;
-    if (!encode_matrix(&mx, bf, a.X, a.tokens, C8, a.ldx, kKC, shape.nt / 2, true) ||
-        !encode_matrix(&my, bf, a.Y, a.tokens, F8, a.ldy, 32, kOutTokens, false))
+    if (!encode_matrix<T>(&mx, a.X, a.tokens, x_cols, a.ldx, kKC, shape.nt / 2, true) ||
+        !encode_matrix<Out>(&my, a.Y, a.tokens, ((int64_t)g.F + y16 - 1) / y16 * y16, a.ldy, 32, kOutTokens, false))
         return cudaErrorInvalidValue;
     const int c = 2 * shape.splits;
     const int64_t clusters = shape.splits > 1 ? g.tiles : min64(g.tiles, shape.at_once);
     if (clusters * c > 0x7fffffffll) return cudaErrorInvalidValue;
     count_launches(1);
-    return launch_pdl_cluster(kern, dim3((unsigned)(clusters * c)), dim3(TileCfg<kSub>::kThreads), kSmem, (unsigned)c, s, g, mx,
-                              my);
+    return launch_pdl_cluster(kern, dim3((unsigned)(clusters * c)), dim3(Cfg::kThreads), Cfg::kSmem, (unsigned)c, s, g, mx, my);
 }
 
-template <typename T, bool kBack>
+template <typename T, typename Out, bool kBack>
 cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
     if (!encode_fn()) return cudaErrorNotSupported;
+    using Cfg = TileCfg<Out, 1>;
     static int known[64][kMaxSplits + 1];
     static bool done[64];
-    const cudaError_t e = allow_smem(mx4_tile_kernel<T, kBack, 1>, kSmem, done);  // (before its clusters are counted)
+    auto kern = mx4_tile_kernel<T, Out, kBack, 1>;
+    const cudaError_t e = allow_smem(kern, Cfg::kSmem, done);  // (before its clusters are counted)
     if (e != cudaSuccess) return e;
     int at_once[kMaxSplits + 1];
-    for (int i = 1; i <= kMaxSplits; ++i)  // (as many of the other kernel, which has the same shared memory)
-        at_once[i] = clusters_at_once(mx4_tile_kernel<T, kBack, 1>, TileCfg<1>::kThreads, i, known);
+    for (int i = 1; i <= kMaxSplits; ++i)  // (as many of the kernel with two chunks a stage, which has the same shared memory)
+        at_once[i] = clusters_at_once(kern, Cfg::kThreads, Cfg::kSmem, i, known);
     TileArgs g;
     g.codes = a.codes;
     g.scales = a.scales;
@@ -563,15 +582,19 @@ cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
     g.tokens = a.tokens;
     g.ftiles = (int32_t)(((int64_t)g.F + 2 * kFeatures - 1) / (2 * kFeatures));
     const int64_t C = kBack ? a.rows : a.cols;
-    Shape shape = choose(a.tokens, g.ftiles, (int)((C + kKC - 1) / kKC), at_once);
-    return shape.sub == 1 ? run_shape<T, kBack, 1>(a, g, shape, s) : run_shape<T, kBack, 2>(a, g, shape, s);
+    Shape shape = choose(a.tokens, g.ftiles, (int)((C + kKC - 1) / kKC), Cfg::kParts, at_once);
+    if constexpr (Cfg::kParts == 1)
+        if (shape.sub == 2) return run_shape<T, Out, kBack, 2>(a, g, shape, s);
+    return run_shape<T, Out, kBack, 1>(a, g, shape, s);
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_tiles(int dt, bool back, const Mx4Args& a, cudaStream_t s) {
-    if (dt == kF16) return back ? run_tiles<__half, true>(a, s) : run_tiles<__half, false>(a, s);
-    return back ? run_tiles<__nv_bfloat16, true>(a, s) : run_tiles<__nv_bfloat16, false>(a, s);
+    if (dt == kF32)
+        return back ? run_tiles<__nv_bfloat16, float, true>(a, s) : run_tiles<__nv_bfloat16, float, false>(a, s);
+    if (dt == kF16) return back ? run_tiles<__half, __half, true>(a, s) : run_tiles<__half, __half, false>(a, s);
+    return back ? run_tiles<__nv_bfloat16, __nv_bfloat16, true>(a, s) : run_tiles<__nv_bfloat16, __nv_bfloat16, false>(a, s);
 }
 
 }  // namespace spops

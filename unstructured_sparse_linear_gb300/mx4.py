@@ -172,8 +172,9 @@ def _product(X, W, out, back, name):
         y, ldy = out.data_ptr(), n_out
     lib = _L()
     ws, size = 0, 0
-    if (x | y | 2 * ldx | 2 * ldy) & 15 or (n_in | n_out) & 7:  # rows that the tensor cores' kernel gets copies of
-        size = lib.spops_mx4_workspace_size(tokens, n_in, n_out)
+    # the parts of fp32, and rows that the tensor cores' kernel gets copies of
+    if dt is torch.float32 or (x | y | 2 * ldx | 2 * ldy) & 15 or (n_in | n_out) & 7:
+        size = lib.spops_mx4_workspace_size(tokens, n_in, n_out, _DTYPE[dt])
         scratch = torch.empty(size, dtype=torch.uint8, device=dev)
         ws = scratch.data_ptr()
     st = (lib.spops_mx4_linear_grad if back else lib.spops_mx4_linear)(_ARGS(
@@ -187,7 +188,7 @@ def _product(X, W, out, back, name):
 
 
 def mx4_linear(X: torch.Tensor, W: Mx4, out: torch.Tensor | None = None) -> torch.Tensor:
-    """Y = X W^T for X [tokens, cols] (fp16 and bf16 on the tensor cores, fp32 on the CUDA cores), W's values in X's
+    """Y = X W^T for X [tokens, cols] (on the tensor cores; fp32 as three bf16 parts, all 24 bits), W's values in X's
     type, fp32 sums. Autograd records nothing of it (RosaLinear is the form that it differentiates): an out that belongs
     to an autograd graph is refused."""
     return _product(X, W, out, False, "X")
