@@ -36,31 +36,34 @@ def dropout(X: torch.Tensor, p: float, state, base: torch.Tensor | None = None,
     dev, dt = X.device, X.dtype
     if dev.type != "cuda":
         raise ValueError("X must be a CUDA tensor")
-    if dt not in _DTYPE:
+    code = _DTYPE.get(dt)
+    if code is None:
         raise ValueError(f"X dtype {dt} not in {list(_DTYPE)}")
     if X.dim() != 2:
         raise ValueError(f"X must be 2-D, got {tuple(X.shape)}")
-    if _elsewhere(dev.index):
+    index = dev.index
+    if _elsewhere(index):
         with torch.cuda.device(dev):
             return dropout(X, p, state, base, out)
     rows, cols = X.shape
     if rows > _MAX_COUNT or cols > _MAX_COUNT:
         raise ValueError(f"at most {_MAX_COUNT} rows and columns, got {rows} and {cols}")
-    p = float(p)
     if not 0.0 <= p <= 1.0:
         raise ValueError(f"p must lie in [0, 1], got {p}")
     at = seed = call = 0
     if isinstance(state, torch.Tensor):
-        if not (state.dtype is torch.int64 and state.device == dev and state.shape == (2,) and state.is_contiguous()):
+        if not (state.dtype is torch.int64 and state.device == dev and state.numel() == 2 and state.is_contiguous()):
             _req(state, "state", torch.int64, device=dev)
-            if state.numel() != 2:
-                raise ValueError(f"state must hold a seed and a call number, got {tuple(state.shape)}")
+            raise ValueError(f"state must hold a seed and a call number, got {tuple(state.shape)}")
         at = state.data_ptr()
     else:
         seed, call = (int(v) for v in state)
         if not (0 <= seed < 2 ** 64 and 0 <= call < 2 ** 64):
             raise ValueError(f"seed and call must lie in [0, 2^64), got {seed} and {call}")
-    x, ldx = _rows(X, "X", rows, cols, dt, dev)
+    ldx, step = X.stride()
+    x = X.data_ptr()
+    if step != 1 or ldx < cols:  # (one column or row, or what is wrong)
+        x, ldx = _rows(X, "X", rows, cols, dt, dev)
     b, ldb = _rows(base, "base", rows, cols, dt, dev) if base is not None else (0, cols)
     given = out is not None
     if given:
@@ -68,10 +71,10 @@ def dropout(X: torch.Tensor, p: float, state, base: torch.Tensor | None = None,
         if out.requires_grad:
             _check_writable(out, "out")
     else:
-        out = torch.empty((rows, cols), dtype=dt, device=dev)
+        out = torch.empty_like(X) if ldx == cols and step == 1 and type(X) is torch.Tensor else \
+            torch.empty((rows, cols), dtype=dt, device=dev)
         y, ldy = out.data_ptr(), cols
-    st = _L().spops_dropout(_ARGS(x, ldx, b, ldb, y, ldy, at, seed, call, _raw_stream(dev.index), p, _DTYPE[dt], rows,
-                                  cols))
+    st = _L().spops_dropout(_ARGS(x, ldx, b, ldb, y, ldy, at, seed, call, _raw_stream(index), p, code, rows, cols))
     if st:
         _check(st, "dropout")
     if given:

@@ -72,22 +72,6 @@ class Mx4:
         return f"Mx4({self._shape[0]} x {self._shape[1]}, {self.dtype}, {self.device})"
 
 
-def _strided(t, name):
-    """The (rows, cols, address, row stride) of a matrix with contiguous rows."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _DTYPE:
-        raise ValueError(f"{name} dtype {t.dtype} not in {list(_DTYPE)}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
-    rows, cols = t.shape
-    if rows > _MAX_COUNT or cols > _MAX_COUNT:
-        raise ValueError(f"{name}: at most {_MAX_COUNT} rows and columns, got {rows} and {cols}")
-    return rows, cols, *_rows(t, name, rows, cols, t.dtype, t.device)
-
-
 def _given(out, name, rows, cols, dtype, device):
     """(address, row stride) of an output that the caller gave."""
     at = _rows(out, name, rows, cols, dtype, device)
@@ -97,7 +81,7 @@ def _given(out, name, rows, cols, dtype, device):
 
 
 def _weight(W):
-    if not isinstance(W, Mx4):
+    if type(W) is not Mx4 and not isinstance(W, Mx4):
         raise TypeError(f"W must be an Mx4, got {type(W).__name__}")
     return W
 
@@ -106,26 +90,38 @@ def mx4_quantize(X: torch.Tensor) -> Mx4:
     """The rows of X (fp32, fp16 or bf16, [rows, cols]) in 4 bits: a block's scale is the power of two of its largest
     magnitude's exponent less two, its values are rounded to the nearest code (ties to the even one, beyond the last to
     the last). A block that holds an infinity or a NaN is NaN as a whole."""
-    rows, cols, x, ldx = _strided(X, "X")
-    dev = X.device
+    if not isinstance(X, torch.Tensor):
+        raise TypeError("X must be a torch.Tensor")
+    dev, dt = X.device, X.dtype
+    if dev.type != "cuda":
+        raise ValueError("X must be a CUDA tensor")
+    code = _DTYPE.get(dt)
+    if code is None:
+        raise ValueError(f"X dtype {dt} not in {list(_DTYPE)}")
+    if X.dim() != 2:
+        raise ValueError(f"X must be 2-D, got {tuple(X.shape)}")
+    rows, cols = X.shape
+    if rows > _MAX_COUNT or cols > _MAX_COUNT:
+        raise ValueError(f"at most {_MAX_COUNT} rows and columns, got {rows} and {cols}")
     if _elsewhere(dev.index):
         with torch.cuda.device(dev):
             return mx4_quantize(X)
+    x, ldx = _rows(X, "X", rows, cols, dt, dev)
     blocks = -(-cols // BLOCK)
     codes = torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=dev)
     scales = torch.empty((rows, blocks), dtype=torch.uint8, device=dev)
-    st = _L().spops_mx4_quantize(x, ldx, _DTYPE[X.dtype], rows, cols, codes.data_ptr(), scales.data_ptr(),
+    st = _L().spops_mx4_quantize(x, ldx, code, rows, cols, codes.data_ptr(), scales.data_ptr(),
                                  _raw_stream(dev.index))
     if st:
         _check(st, "mx4_quantize")
-    return Mx4._of(codes, scales, (rows, cols), X.dtype, dev)
+    return Mx4._of(codes, scales, (rows, cols), dt, dev)
 
 
 def mx4_dequantize(W: Mx4, dtype: torch.dtype | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
     """W's values as a dense [rows, cols] matrix of `dtype` (default: W's): exact, but where they leave its range."""
     rows, cols = _weight(W).shape
     if dtype is None:
-        dtype = W.dtype if out is None else out.dtype
+        dtype = getattr(out, "dtype", W.dtype)
     if dtype not in _DTYPE:
         raise ValueError(f"dtype {dtype} not in {list(_DTYPE)}")
     dev, given = W.device, out is not None
@@ -147,20 +143,22 @@ def mx4_dequantize(W: Mx4, dtype: torch.dtype | None = None, out: torch.Tensor |
 
 
 def _product(X, W, out, back, name):
-    rows, cols = _weight(W).shape
+    rows, cols = _weight(W)._shape
     n_in, n_out = (rows, cols) if back else (cols, rows)
     dev = W.device
     if not isinstance(X, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     dt = X.dtype
-    if dt not in _DTYPE:
+    code = _DTYPE.get(dt)
+    if code is None:
         raise ValueError(f"{name} dtype {dt} not in {list(_DTYPE)}")
     if X.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got {tuple(X.shape)}")
     tokens = X.shape[0]
     if tokens > _MAX_COUNT:
         raise ValueError(f"at most {_MAX_COUNT} tokens, got {tokens}")
-    if _elsewhere(dev.index):
+    index = dev.index
+    if _elsewhere(index):
         with torch.cuda.device(dev):
             return _product(X, W, out, back, name)
     x, ldx = _rows(X, name, tokens, n_in, dt, dev)
@@ -174,12 +172,12 @@ def _product(X, W, out, back, name):
     ws, size = 0, 0
     # the parts of fp32, and rows that the tensor cores' kernel gets copies of
     if dt is torch.float32 or (x | y | 2 * ldx | 2 * ldy) & 15 or (n_in | n_out) & 7:
-        size = lib.spops_mx4_workspace_size(tokens, n_in, n_out, _DTYPE[dt])
+        size = lib.spops_mx4_workspace_size(tokens, n_in, n_out, code)
         scratch = torch.empty(size, dtype=torch.uint8, device=dev)
         ws = scratch.data_ptr()
     st = (lib.spops_mx4_linear_grad if back else lib.spops_mx4_linear)(_ARGS(
-        x, ldx, W._codes.data_ptr(), W._scales.data_ptr(), y, ldy, ws, size, _raw_stream(dev.index), _DTYPE[dt],
-        tokens, rows, cols))
+        x, ldx, W._codes.data_ptr(), W._scales.data_ptr(), y, ldy, ws, size, _raw_stream(index), code, tokens,
+        rows, cols))
     if st:
         _check(st, "mx4_linear_grad" if back else "mx4_linear")
     if given:  # (what autograd saved of it is no longer there)
