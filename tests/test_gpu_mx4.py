@@ -260,6 +260,24 @@ def test_bench_shapes(fmt):
                                f"{tokens} {rows} {cols} {back}")
 
 
+@pytest.mark.parametrize("fmt", list(DTYPES))
+@pytest.mark.parametrize("tokens,rows,cols", [(5, 8448, 4096), (1300, 4352, 96), (1300, 4352, 352), (2600, 2304, 352), (2600, 2304, 200),
+                                              (9000, 520, 64), (700, 6400, 416)])
+def test_many_tiles(fmt, tokens, rows, cols):
+    """Tiles that follow each other on an SM, with boxes of codes that end within a stage, and a weight of more values than
+    the kernel for a few tokens takes."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(tokens + cols)
+    W = sp.mx4_quantize(torch.randn(rows, cols, device=DEV, generator=g))
+    w = sp.mx4_dequantize(W).double()
+    for back in (False, True):
+        X = torch.randn(tokens, rows if back else cols, device=DEV, generator=g).to(DTYPES[fmt])
+        call, m = (sp.mx4_linear_grad, w) if back else (sp.mx4_linear, w.t())
+        Y, x = call(X, W), X.double()
+        assert torch.equal(call(X, W), Y)
+        assert_elementwise(Y, (x @ m).cpu().numpy(), (x.abs() @ m.abs()).cpu().numpy(), m.shape[0], fmt, f"{back}")
+
+
 def test_streams_and_graphs():
     """Two streams at once, and a captured run whose replays see new inputs."""
     rng = np.random.default_rng(9)

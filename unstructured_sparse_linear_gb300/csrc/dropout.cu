@@ -7,7 +7,8 @@
 // again from the same state.
 //
 // A step a thread: eight values. Sixteen bits a value make it one Philox (14 wide products) per eight; with 32 bits
-// the generator and not HBM would bound the kernel.
+// the generator and not HBM would bound the kernel. 4096 x 11008 bf16 with a base, 270 MB: 44 us (40.5 at the device's copy
+// rate), without one 34.
 #include "common.cuh"
 #include "internal.h"
 #include "mx4.h"

@@ -19,6 +19,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSteps = 4;  // of 256 values a warp
 constexpr int kMx4FewTokens = 8;
+constexpr int64_t kMx4FewValues = 1 << 25;  // of the weight
 
 // Rows as both kernels walk them: in steps of 256 values. A matrix of whole blocks in contiguous rows is one row.
 struct Walk {
@@ -353,8 +354,17 @@ cudaError_t launch_mx4_dequantize(int dt, const uint8_t* codes, const uint8_t* s
     return dequantize<__nv_bfloat16>(codes, scales, rows, cols, Y, ldy, s);
 }
 
+// The kernels without tensor-core tiles, forward, us as these kernels / the tiles. 1 token: 4096 x 4096 6.3 / 9.2,
+// 11008 x 4096 12.6 / 15.6, 8192 x 8192 16.5 / 17, fp16 14.7 / 15.4. 2 to 8: 4096 x 4096 8.1 / 9.3, 1024 x 16384 8.1 / 15.4,
+// 1536 x 384 3.5 / 4.9, but 4096 x 11008 18.6 / 15.7, 11008 x 4096 21 / 15.7, 8192 x 8192 23 / 17. They take any rows.
+static bool mx4_few(int dt, bool back, const Mx4Args& a) {
+    if (back || dt == kF32 || a.tokens > kMx4FewTokens) return false;
+    return a.tokens == 1 || (int64_t)a.rows * a.cols <= kMx4FewValues || !mx4_tile_rows(a.X, a.ldx, a.cols, 2) ||
+           !mx4_tile_rows(a.Y, a.ldy, a.rows, 2);
+}
+
 bool mx4_needs_copies(int dt, bool back, const Mx4Args& a) {
-    if (a.rows == 0 || a.cols == 0 || (!back && dt != kF32 && a.tokens <= kMx4FewTokens)) return false;
+    if (a.rows == 0 || a.cols == 0 || mx4_few(dt, back, a)) return false;
     const int64_t in = back ? a.rows : a.cols, out = back ? a.cols : a.rows, es = (int64_t)dtype_size(dt);
     return dt == kF32 || !mx4_tile_rows(a.X, a.ldx, in, es) || !mx4_tile_rows(a.Y, a.ldy, out, es);
 }
@@ -363,10 +373,7 @@ cudaError_t launch_mx4_product(int dt, bool back, const Mx4Args& a, void* worksp
     const int64_t in = back ? a.rows : a.cols, out = back ? a.cols : a.rows, es = (int64_t)dtype_size(dt);
     if (in == 0)  // nothing to sum
         return cudaMemset2DAsync(a.Y, (size_t)(a.ldy * es), 0, (size_t)(out * es), (size_t)a.tokens, s);
-    // bf16, 4096 x 4096: 1 token 6.4 us (8.0 with the kernel for eight, 11.6 with tiles), 8 tokens 8.0 (tiles 11.6), 16 tokens
-    // 11.6 with tiles (two passes of eight 16); 11008 x 4096: 12.6 (20.8, 21), 21 (21), 22. 4096 x 11008: 14.4 (18.5, 27).
-    if (!back && dt != kF32 && a.tokens == 1) return launch_mx4_vec(dt, a, s);
-    if (!back && dt != kF32 && a.tokens <= kMx4FewTokens) return launch_mx4_rows(dt, a, s);
+    if (mx4_few(dt, back, a)) return a.tokens == 1 ? launch_mx4_vec(dt, a, s) : launch_mx4_rows(dt, a, s);
     Mx4Args t = a;
     cudaError_t e = cudaSuccess;
     char* ws = static_cast<char*>(workspace);
@@ -389,7 +396,7 @@ cudaError_t launch_mx4_product(int dt, bool back, const Mx4Args& a, void* worksp
         t.Y = ws;
         t.ldy = (out * es + 15) / 16 * 16 / es;
     }
-    if (e == cudaSuccess) e = launch_mx4_tiles(dt, back, t, s);
+    if (e == cudaSuccess) e = back ? launch_mx4_backward(dt, t, s) : launch_mx4_forward(dt, t, s);
     if (e == cudaSuccess && !own) e = copy_rows(t.Y, t.ldy, a.Y, a.ldy, a.tokens, out, out, es, s);
     return e;
 }

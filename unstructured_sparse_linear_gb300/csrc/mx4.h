@@ -34,7 +34,8 @@ cudaError_t launch_mx4_vec(int dt, const Mx4Args& a, cudaStream_t s);
 cudaError_t launch_mx4_rows(int dt, const Mx4Args& a, cudaStream_t s);
 // On the tcgen05 tensor cores, where mx4_tile_rows holds for X and Y. fp32: X is its three bf16 parts, mx4_split_cols
 // columns, each part's behind the others'.
-cudaError_t launch_mx4_tiles(int dt, bool back, const Mx4Args& a, cudaStream_t s);
+cudaError_t launch_mx4_forward(int dt, const Mx4Args& a, cudaStream_t s);
+cudaError_t launch_mx4_backward(int dt, const Mx4Args& a, cudaStream_t s);
 
 // Rows as TMA loads and stores them: rows and addresses on 16-byte boundaries, whole 16 bytes (a store writes no less).
 inline bool mx4_tile_rows(const void* p, int64_t ld, int64_t cols, int64_t es) {
