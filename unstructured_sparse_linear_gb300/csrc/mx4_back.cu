@@ -9,7 +9,7 @@
 // MN-major, which takes them as they are decoded (tensor memory has the contraction along its columns, and would need each
 // code alone).
 // fp32: the weight's values are bf16 numbers, and X is the sum of three bf16 parts (all 24 bits), which multiply the same
-// decoded weight into the same fp32 sums.
+// decoded weight; the first part's products have an accumulator of their own.
 #include "mx4_pair.cuh"
 
 namespace spops {
@@ -135,8 +135,9 @@ mx4_back_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_x, con
                         for (int h = 0; h < kSub * kParts; ++h)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                pair_mma_f16(d, a0 + off + (kParts == 1 ? h : 0) * (kWBytes / 16) + k * kStepA,
-                                             b0 + off + h * (x_bytes / 16) + k * kStepB, g.idesc, c > 0 || h > 0 || k > 0);
+                                pair_mma_f16(kParts > 1 && h > 0 ? d + (uint32_t)g.nt : d, a0 + off + (kParts == 1 ? h : 0) * (kWBytes / 16) + k * kStepA,
+                                             b0 + off + h * (x_bytes / 16) + k * kStepB, g.idesc,
+                                             c > 0 || k > 0 || h > (kParts == 1 ? 0 : 1));
                         pair_commit(smem_u32(&sh.empty[s]), mask);
                     }
                     __syncwarp();

@@ -163,6 +163,19 @@ __device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b) {
     return Elt<Out>::p2(__uint_as_float(a), __uint_as_float(b));
 }
 
+// 32 tokens' sums of a lane. fp32 has two accumulators, the first part's and, nt columns on, the other two's: the tensor core
+// cuts a sum off where it adds to it, and so the small parts' products cost the large ones' sum nothing.
+template <typename Out>
+__device__ __forceinline__ void load_sums(uint32_t from, int nt, float (&y)[32]) {
+    tmem_load<32>(from, y);
+    if constexpr (sizeof(Out) == 4) {
+        float z[32];
+        tmem_load<32>(from + (uint32_t)nt, z);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) y[e] += z[e];
+    }
+}
+
 // Warps 0 to 3, a TMEM lane quarter each: the tiles' sums to Y, by way of shared memory (kOutBufs buffers a warp at out_at), or to
 // the place of the partial sums ([token][128 features], fp32).
 template <typename Out, int kOutBufs>
@@ -185,7 +198,7 @@ __device__ __forceinline__ void finish_tiles(const TileArgs& g, const Share& me,
                 const uint32_t st = sbase + out_at + (uint32_t)(warp * kOutBufs + stores) * kOutBytes;
                 if (me.splits > 1) {
                     float y[32];
-                    tmem_load<32>(from, y);
+                    load_sums<Out>(from, g.nt, y);
                     const uint32_t p = sbase + (uint32_t)(c * kFeatures + warp * 32 + lane) * 4;
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
@@ -195,7 +208,7 @@ __device__ __forceinline__ void finish_tiles(const TileArgs& g, const Share& me,
                     __syncwarp();
                     if constexpr (sizeof(Out) == 4) {
                         float y[32];
-                        tmem_load<32>(from, y);
+                        load_sums<Out>(from, g.nt, y);
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             asm volatile("st.shared.f32 [%0], %1;" ::"r"(st + e * 128 + lane * 4), "f"(y[e]) : "memory");
