@@ -8,6 +8,9 @@
 // from L2 once per 256 features. A row's codes run along the features, across the contraction: the operand in shared memory is
 // MN-major, which takes them as they are decoded (tensor memory has the contraction along its columns, and would need each
 // code alone).
+// Bounds. Per 64 of the contraction shared memory takes the decoded operand twice (written, read) and X twice: 512 cycles at 256
+// tokens, as many as the products (8192 tokens 8192 -> 2048: 91 % of its wavefronts, tensor pipe 82 %). 4096 tokens
+// 11008 -> 4096 213 us, 1736 TFLOP/s; 2048 tokens 4096 -> 4096 fp16 47; 64 tokens 26.5, the latency of a stage's decoding.
 // fp32: the weight's values are bf16 numbers, and X is the sum of three bf16 parts (all 24 bits), which multiply the same
 // decoded weight; the first part's products have an accumulator of their own.
 #include "mx4_pair.cuh"
@@ -128,8 +131,8 @@ mx4_back_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, con
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        // The whole warp walks the chunks and one thread issues: what the products take then lies in uniform registers (a
-        // loop of one thread took 650 cycles a chunk, more than its products). A wait that has run out of time is not
+        // The whole warp walks the stages and one thread issues: what the products take then lies in uniform registers (a
+        // loop of one thread took 650 cycles a stage, more than its products). A wait that has run out of time is not
         // looked at: the products of whatever is there end, and the error is recorded.
         if (me.half == 0) {
             const uint32_t mask = 3u << me.lead;
