@@ -311,6 +311,63 @@ def test_streams_and_graphs():
         assert torch.equal(q, sp.mx4_dequantize(sp.mx4_quantize(xs[3])))
 
 
+def test_two_graphs():
+    """Graphs whose products have workspaces, replayed in turn with other inputs."""
+    rng = np.random.default_rng(11)
+    W, _ = weight(rng, 264, 320)
+    graphs = []
+    for fmt, pad in (("f32", 0), ("bf16", 3)):
+        x = rand(rng, fmt, 50, 320, pad=pad)
+        want = [sp.mx4_linear(x * f, W) for f in (1, 2)]
+        back = [sp.mx4_linear_grad(y, W) for y in want]
+        static = x.clone() if pad == 0 else torch.zeros(50, 320 + 2 * pad, dtype=x.dtype, device=DEV)[:, pad:pad + 320]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = sp.mx4_linear(static, W)
+            d = sp.mx4_linear_grad(y, W)
+        graphs.append((g, static, x, y, d, want, back))
+    for i in (0, 1, 0):
+        for g, static, x, *_ in graphs:
+            static.copy_(x * (i + 1))
+        for g, *_ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for g, static, x, y, d, want, back in graphs:
+            assert torch.equal(y, want[i]) and torch.equal(d, back[i])
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 40])
+def test_scales_of_any_alignment(tokens):
+    rng = np.random.default_rng(12)
+    W, _ = weight(rng, 192, 256)
+    for offset in (1, 2, 3):
+        buf = torch.empty(W.scales.numel() + offset, dtype=torch.uint8, device=DEV)
+        scales = buf[offset:].view(W.scales.shape)
+        scales.copy_(W.scales)
+        V = sp.Mx4(W.codes, scales, 256)
+        for fmt in DTYPES:
+            X, G = rand(rng, fmt, tokens, 256), rand(rng, fmt, tokens, 192)
+            assert torch.equal(sp.mx4_linear(X, V), sp.mx4_linear(X, W))
+            assert torch.equal(sp.mx4_linear_grad(G, V), sp.mx4_linear_grad(G, W))
+        assert torch.equal(sp.mx4_dequantize(V), sp.mx4_dequantize(W))
+
+
+@pytest.mark.parametrize("cols", [4096, 4100])
+def test_conversion_of_more_than_a_pass(cols):
+    """More values than the threads of one grid take at a time."""
+    X = torch.randn(6000, cols, device=DEV, generator=torch.Generator(device=DEV).manual_seed(cols)).bfloat16()
+    W = sp.mx4_quantize(X)
+    back = sp.mx4_dequantize(W)
+    for r in (0, 1, 2999, 4444, 5999):
+        codes, scales = ref.quantize(as_f64(X[r:r + 1]))
+        assert np.array_equal(W.codes[r:r + 1].cpu().numpy(), codes) and np.array_equal(W.scales[r:r + 1].cpu().numpy(), scales)
+        assert np.array_equal(as_f64(back[r:r + 1]), ref.values(codes, scales, cols))
+    for lo in range(0, 6000, 1000):  # and the rows between: the same as by themselves
+        part = sp.mx4_quantize(X[lo:lo + 1000])
+        assert torch.equal(part.codes, W.codes[lo:lo + 1000]) and torch.equal(part.scales, W.scales[lo:lo + 1000])
+        assert torch.equal(sp.mx4_dequantize(part), back[lo:lo + 1000])
+
+
 def test_refusals():
     rng = np.random.default_rng(2)
     W, _ = weight(rng, 64, 96)

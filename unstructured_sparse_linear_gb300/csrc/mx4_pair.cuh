@@ -54,8 +54,8 @@ __device__ __forceinline__ void pair_tma_load_2d(uint32_t dst, const CUtensorMap
 }
 
 // Arrive on a barrier of the pair (its cluster address). What it announces is read by this CTA's tensor core, for which
-// each writer's proxy fence has made it visible, or has left TMEM: no release of the cluster's scope, which took a warp 500
-// cycles for each stage.
+// each writer's proxy fence has made it visible, or lies in TMEM or has left it, which the fences of tcgen05 order: no release of
+// the cluster's scope, which took a warp 500 cycles for each stage.
 __device__ __forceinline__ void pair_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
