@@ -824,7 +824,7 @@ static int mx4_product(const spops_mx4_args* a, bool back) {
         return fail(SPOPS_ERR_UNSUPPORTED, "%d tokens: more than %d", a->tokens, SPOPS_MX4_MAX_COUNT);
     const int32_t in = back ? a->rows : a->cols, out = back ? a->cols : a->rows;
     if (a->dtype == SPOPS_F32 && mx4_split_cols(in) > 0x7fffffff)  // (a copy's coordinates have 32 bits)
-        return fail(SPOPS_ERR_UNSUPPORTED, "%d values in a sum: fp32 takes up to %d", in, 0x7fffffff / 3 / 64 * 64);
+        return fail(SPOPS_ERR_UNSUPPORTED, "%d values in a sum: fp32 takes up to %d", in, 0x7fffffff / 3 / 128 * 128);
     if (a->tokens == 0 || out == 0) return ok();
     const size_t es = dtype_size(a->dtype), blocks = (size_t)a->rows * mx4_blocks(a->cols);
     Mx4Args m;

@@ -41,7 +41,7 @@ cudaError_t launch_mx4_backward(int dt, const Mx4Args& a, cudaStream_t s);
 inline bool mx4_tile_rows(const void* p, int64_t ld, int64_t cols, int64_t es) {
     return cols * es % 16 == 0 && ld * es % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld < (1ll << 37);
 }
-inline int64_t mx4_split_cols(int64_t cols) { return 3 * ((cols + 63) / 64 * 64); }
+inline int64_t mx4_split_cols(int64_t cols) { return 3 * ((cols + 127) / 128 * 128); }
 // Bytes of a copy of Y [tokens, cols] with such rows, and of X (fp32: of its parts).
 inline size_t mx4_y_bytes(int64_t tokens, int64_t cols, int64_t es) {
     return ((size_t)tokens * (size_t)((cols * es + 15) / 16 * 16) + 255) / 256 * 256;

@@ -119,7 +119,7 @@ mx4_back_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, con
 #pragma unroll
                     for (int h = 0; h < kSub * kParts; ++h)  // (the parts of X lie one behind the other)
                         pair_tma_load_2d(sbase + s * stage_bytes + kSub * kWBytes + h * x_bytes, &map_x,
-                                         (kParts == 1 ? c * kSub + h : c + h * g.chunks) * kKC, at.t0 + me.half * (g.nt / 2),
+                                         kParts == 1 ? (c * kSub + h) * kKC : c * kKC + h * g.part, at.t0 + me.half * (g.nt / 2),
                                          full + s * 8);
                 }
                 __syncwarp();

@@ -28,9 +28,9 @@ constexpr int kTmemCols = 512;
 
 // A stage holds kSub times 64 of the contraction, and X in kParts parts. Warps 0 to 3 finish (a TMEM lane quarter each), then
 // groups of four decode, one warp loads X, one multiplies, one loads codes.
-template <typename Out>
+template <typename Out, int kSub_>
 struct FwdCfg {
-    static constexpr int kParts = sizeof(Out) == 4 ? 3 : 1, kSub = kParts == 1 ? 2 : 1;
+    static constexpr int kParts = sizeof(Out) == 4 ? 3 : 1, kSub = kSub_;
     static constexpr int kAccs = kParts == 1 ? 1 : 2;  // of a tile
     static constexpr int kGroups = 4;  // at most
     static constexpr int kOutBufs = kParts == 1 ? 4 : 2;  // (what fits)
@@ -71,13 +71,13 @@ __device__ __forceinline__ void mbar_arrive_count(uint32_t bar, uint32_t n) {
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-template <typename T, typename Out>
-__global__ void __launch_bounds__(FwdCfg<Out>::kThreads, 1)
+template <typename T, typename Out, int kSub>
+__global__ void __launch_bounds__(FwdCfg<Out, kSub>::kThreads, 1)
 mx4_fwd_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                const __grid_constant__ CUtensorMap map_y) {
-    using Cfg = FwdCfg<Out>;
+    using Cfg = FwdCfg<Out, kSub>;
     constexpr int kLoadWarp = Cfg::kLoadWarp, kMmaWarp = Cfg::kMmaWarp, kCodeWarp = Cfg::kCodeWarp, kParts = Cfg::kParts;
-    constexpr int kSub = Cfg::kSub, kBlocks = 2 * kSub;  // of a row and stage
+    constexpr int kBlocks = 2 * kSub, kWords = (kBlocks + 3) / 4;  // of a row and stage; words of its scales
     // No static shared memory, so the dynamic part starts on the 1 KB boundary that the swizzled tiles need (checked).
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     struct Shared {
@@ -142,8 +142,7 @@ mx4_fwd_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, cons
 #pragma unroll
                     for (int h = 0; h < kSub * kParts; ++h)  // (the parts of X lie one behind the other)
                         pair_tma_load_2d(sbase + s * stage_bytes + h * x_bytes, &map_x,
-                                         (kParts == 1 ? c * kSub + h : c + h * g.chunks) * kKC, at.t0 + me.half * (g.nt / 2),
-                                         full + s * 8);
+                                         (c * kSub + h % kSub) * kKC + h / kSub * g.part, at.t0 + me.half * (g.nt / 2), full + s * 8);
                 }
                 __syncwarp();
                 if (++s == stages) {
@@ -197,9 +196,8 @@ mx4_fwd_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, cons
                         for (int h = 0; h < kSub * kParts; ++h)
 #pragma unroll
                             for (int k = 0; k < 4; ++k)  // 16 of the contraction: 8 columns, 32 bytes
-                                pair_mma_f16_ts(kParts > 1 && h > 0 ? d + (uint32_t)g.nt : d, a + (kParts == 1 ? h : 0) * 32 + k * 8,
-                                                b + h * (x_bytes / 16) + k * 2, g.idesc,
-                                                c > 0 || k > 0 || h > (kParts == 1 ? 0 : 1));
+                                pair_mma_f16_ts(h < kSub ? d : d + (uint32_t)g.nt, a + h % kSub * 32 + k * 8, b + h * (x_bytes / 16) + k * 2,
+                                                g.idesc, c > 0 || k > 0 || (h != 0 && h != kSub));
                         pair_commit(smem_u32(&sh.empty[s]), mask);
                     }
                     __syncwarp();
@@ -242,17 +240,30 @@ mx4_fwd_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, cons
             in = row < g.rows;
             ps = g.scales + (int64_t)row * g.blocks + (int64_t)(me.c0 + ac) * kBlocks;
         };
+        struct Scales {
+            uint32_t w[kWords];
+        };
         auto ask = [&]() {
-            uint32_t b = kOnes;
+            Scales b;
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) b.w[k] = kOnes;
             if (in) {
                 if (whole) {
-                    if constexpr (kSub == 2) b = __ldg(reinterpret_cast<const uint32_t*>(ps));
-                    else b = kOnes << 16 | __ldg(reinterpret_cast<const uint16_t*>(ps));
+                    if constexpr (kSub == 4) {
+                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(ps));
+                        b.w[0] = v.x;
+                        b.w[1] = v.y;
+                    } else if constexpr (kSub == 2) {
+                        b.w[0] = __ldg(reinterpret_cast<const uint32_t*>(ps));
+                    } else {
+                        b.w[0] = kOnes << 16 | __ldg(reinterpret_cast<const uint16_t*>(ps));
+                    }
                 } else {
                     const int64_t blk = (int64_t)(me.c0 + ac) * kBlocks;
 #pragma unroll
                     for (int x = 0; x < kBlocks; ++x)
-                        if (blk + x < g.blocks) b = (b & ~(255u << (8 * x))) | (uint32_t)__ldg(ps + x) << (8 * x);
+                        if (blk + x < g.blocks)
+                            b.w[x / 4] = (b.w[x / 4] & ~(255u << (8 * (x % 4)))) | (uint32_t)__ldg(ps + x) << (8 * (x % 4));
                 }
             }
             ac += groups;
@@ -261,7 +272,8 @@ mx4_fwd_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, cons
             return b;
         };
         aim();
-        uint32_t b = ask(), s = group, ph = 1;
+        Scales b = ask();
+        uint32_t s = group, ph = 1;
         // The stage at hand: number c of this pair's tile; the boxes of codes before its tile.
         const uint32_t tile_boxes = (uint32_t)(me.per - 1) / Cfg::kBoxStages + 1;
         uint32_t boxes = 0;
@@ -277,12 +289,14 @@ mx4_fwd_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, cons
             if (ok) {
                 tc::fence_after_sync();
                 const uint32_t codes = from + cs * Cfg::kBoxBytes, first = in_box * kBlocks, col = to + s * (32 * kSub);
-                if (__all_sync(0xffffffffu, ((b - 0x71717171u) & 0xf0f0f0f0u) == 0)) {  // scales of 2^-14 to 2 only
-                    const uint32_t h = b - 0x70707070u;                                  // their exponents as fp16's
+                uint32_t rare = 0;  // scales but 2^-14 to 2
+#pragma unroll
+                for (int k = 0; k < kWords; ++k) rare |= (b.w[k] - 0x71717171u) & 0xf0f0f0f0u;
+                if (__all_sync(0xffffffffu, rare == 0)) {
 #pragma unroll
                     for (int x = 0; x < kBlocks; ++x) {
                         const uint4 w = ld_shared_v4(codes + ((flip ^ (first + x)) << 4));
-                        const uint32_t f = __byte_perm(h, 0, 0x0404 | x << 12 | x << 4) << 2;
+                        const uint32_t f = __byte_perm(b.w[x / 4] - 0x70707070u, 0, 0x0404 | (x % 4) << 12 | (x % 4) << 4) << 2;  // as fp16
                         uint32_t v[16];
                         mx4::decode8<T>(w.x, f, reinterpret_cast<uint32_t(&)[4]>(v[0]));
                         mx4::decode8<T>(w.y, f, reinterpret_cast<uint32_t(&)[4]>(v[4]));
@@ -294,7 +308,7 @@ mx4_fwd_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, cons
 #pragma unroll 1
                     for (int x = 0; x < kBlocks; ++x) {
                         const uint4 w = ld_shared_v4(codes + ((flip ^ (first + x)) << 4));
-                        const uint32_t e = (b >> (8 * x)) & 255u;
+                        const uint32_t e = ((kWords > 1 && x >= 4 ? b.w[kWords - 1] : b.w[0]) >> (8 * (x & 3))) & 255u;
                         uint32_t v[16];
                         const bool plain = mx4::plain(e) || (e != 255 && (w.x | w.y | w.z | w.w) == 0);  // (or nothing but zeros)
                         if (__all_sync(0xffffffffu, plain)) {
@@ -362,18 +376,19 @@ bool two_buffers(int nt, int splits, int64_t tiles, int64_t at_once) {
     return splits == 1 && tiles > at_once && slots<Cfg>(nt, 2) >= 3;
 }
 
-// Tokens per tile and splits of the contraction with the least estimated time in us, fitted to sweeps over both (384 to 11008
-// features, 6 to 172 times 64 of the contraction, 9 to 8192 tokens, 27 problems: the choice takes 4 % more than the best of a
-// sweep at most): a stage takes 0.335 for its decoding, or its products, and 15 % more where the ring has three; tiles follow
-// each other, with one accumulator after its sums have left; with splits, every wave of clusters begins anew and adds its sums.
+// Tokens per tile, splits of the contraction and 64s of it in a stage with the least estimated time in us, fitted to sweeps over
+// them (384 to 11008 features, 6 to 172 times 64 of the contraction, 9 to 8192 tokens): a stage takes its decoding and its
+// messages (kLeast), or its products, and 15 % more where the ring has three of 128; tiles follow each other, with one accumulator after
+// its sums have left; with splits, every wave of clusters begins anew and adds its sums. (Stages of 256 as those of 128, 64 tokens
+// 4096 -> 11008: 14.5 us and 16.3, fp16 12.6 and 14.7, 128 tokens 16.0 and 17.2; 160 tokens leave no room for three.)
 template <typename Cfg>
-Shape choose(int64_t tokens, int64_t F, int64_t C, const int (&at_once)[kMaxSplits + 1]) {
-    const int most = Cfg::kParts == 1 ? kMaxTokens : kMaxTokens / 2;
-    const int64_t ftiles = (F + 2 * kFeatures - 1) / (2 * kFeatures), stages = (C + Cfg::kSub * kKC - 1) / (Cfg::kSub * kKC);
-    Shape best{most, 1, Cfg::kSub, at_once[1]};
-    double least = 1e300;
+void choose(int64_t tokens, int64_t F, int64_t C, const int (&at_once)[kMaxSplits + 1], double& least, Shape& best) {
+    constexpr int kSub = Cfg::kSub;
+    constexpr double kLeast = kSub == 1 ? 0.335 : Cfg::kParts > 1 ? 0.5 : kSub == 2 ? 0.335 : 0.535;
+    const int most = Cfg::kParts > 1 ? (kSub == 1 ? 128 : 96) : kSub == 2 ? kMaxTokens : 128;
+    const int64_t ftiles = (F + 2 * kFeatures - 1) / (2 * kFeatures), stages = (C + kSub * kKC - 1) / (kSub * kKC);
     for (int nt = 32; nt <= most; nt += 32) {
-        const double products = (Cfg::kParts == 1 ? 0.00222 : 0.0042) * nt, stage = products > 0.335 ? products : 0.335;
+        const double products = kSub * (Cfg::kParts == 1 ? 0.00111 : 0.0042) * nt, stage = products > kLeast ? products : kLeast;
         for (int s = 1; s <= kMaxSplits && s <= stages; ++s) {
             const int64_t tiles = ftiles * ((tokens + nt - 1) / nt);
             const double waves = (double)((tiles + at_once[s] - 1) / at_once[s]), steps = (double)((stages + s - 1) / s);
@@ -382,33 +397,28 @@ Shape choose(int64_t tokens, int64_t F, int64_t C, const int (&at_once)[kMaxSpli
                 t = waves * (4.4 + 0.3 * s + 0.015 * nt + steps * stage);
             } else {
                 const bool two = two_buffers<Cfg>(nt, 1, tiles, at_once[1]);
-                t = 3.8 + 0.0095 * nt + waves * steps * stage * (two && slots<Cfg>(nt, 2) == 3 ? 1.15 : 1.0) +
+                t = 3.8 + 0.0095 * nt + waves * steps * stage * (two && kSub == 2 && slots<Cfg>(nt, 2) == 3 ? 1.15 : 1.0) +
                     (waves - 1) * (two ? 0.25 : 0.4 + 0.009 * nt);
             }
             if (t < least) {
                 least = t;
-                best = {nt, s, Cfg::kSub, at_once[s]};
+                best = {nt, s, kSub, at_once[s]};
             }
         }
     }
-    return best;
 }
 
-template <typename T, typename Out>
-cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
-    using Cfg = FwdCfg<Out>;
-    auto kern = mx4_fwd_kernel<T, Out>;
-    static int known[64][kMaxSplits + 1];
+template <typename T, typename Out, int kSub>
+cudaError_t run_shape(const Mx4Args& a, Shape shape, cudaStream_t s) {
+    using Cfg = FwdCfg<Out, kSub>;
+    auto kern = mx4_fwd_kernel<T, Out, kSub>;
     static bool done[64];
-    int at_once[kMaxSplits + 1];
-    const cudaError_t e = count_clusters(kern, Cfg::kThreads, Cfg::kSmem, at_once, known, done);
+    const cudaError_t e = allow_smem(kern, Cfg::kSmem, done);
     if (e != cudaSuccess) return e;
-    const Shape shape = choose<Cfg>(a.tokens, a.rows, a.cols, at_once);
     TileArgs g{};
     CUtensorMap mw, mx, my;
     if (!tile_args<T, Out>(g, a, a.rows, a.cols, shape, Cfg::kParts, &mx, &my) ||
-        !encode_matrix<uint8_t>(&mw, a.codes, a.rows, g.blocks * 16, g.blocks * 16, 128, kFeatures,
-                                CU_TENSOR_MAP_SWIZZLE_128B))
+        !encode_matrix<uint8_t>(&mw, a.codes, a.rows, g.blocks * 16, g.blocks * 16, 128, kFeatures, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     g.bufs = two_buffers<Cfg>(shape.nt, shape.splits, g.tiles, shape.at_once) ? 2 : 1;
     g.stages = slots<Cfg>(shape.nt, g.bufs);
@@ -417,6 +427,24 @@ cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
     const int c = 2 * shape.splits, clusters = shape.splits > 1 || g.tiles < shape.at_once ? g.tiles : shape.at_once;
     count_launches(1);
     return launch_pdl_cluster(kern, dim3((unsigned)(clusters * c)), dim3(Cfg::kThreads), Cfg::kSmem, (unsigned)c, s, g, mw, mx, my);
+}
+
+template <typename T, typename Out>
+cudaError_t run_tiles(const Mx4Args& a, cudaStream_t s) {
+    constexpr int kSub = sizeof(Out) == 4 ? 1 : 2;
+    using Cfg = FwdCfg<Out, kSub>;
+    static int known[64][kMaxSplits + 1];
+    static bool done[64];
+    int at_once[kMaxSplits + 1];
+    // (as many of the kernel with other stages: one CTA fills an SM)
+    const cudaError_t e = count_clusters(mx4_fwd_kernel<T, Out, kSub>, Cfg::kThreads, Cfg::kSmem, at_once, known, done);
+    if (e != cudaSuccess) return e;
+    double least = 1e300;
+    Shape shape{};
+    choose<Cfg>(a.tokens, a.rows, a.cols, at_once, least, shape);
+    choose<FwdCfg<Out, 2 * kSub>>(a.tokens, a.rows, a.cols, at_once, least, shape);
+    if (shape.sub == kSub) return run_shape<T, Out, kSub>(a, shape, s);
+    return run_shape<T, Out, 2 * kSub>(a, shape, s);
 }
 
 }  // namespace

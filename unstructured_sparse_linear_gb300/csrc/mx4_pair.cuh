@@ -71,6 +71,7 @@ struct TileArgs {
     int64_t ldy;
     int64_t blocks;  // of a row of W
     int32_t rows, F, tokens, ftiles, tiles, chunks, nt, stages;
+    int32_t part;    // columns of one of the parts of X
     int32_t groups;  // of decoders
     int32_t bufs;    // accumulators
     uint32_t idesc;
@@ -340,6 +341,7 @@ bool tile_args(TileArgs& g, const Mx4Args& a, int32_t F, int32_t C, Shape shape,
     // (a split without a chunk would have no sums; the indices of tiles and CTAs have 32 bits)
     if (shape.splits > g.chunks || tiles > 0x7fffffff / (4 * kMaxSplits)) return false;
     g.tiles = (int32_t)tiles;
+    g.part = (int32_t)(mx4_split_cols(C) / 3);
     g.err = device_error_word();
     // (rows of whole 16 bytes: copies of others have zeros, or room, behind their columns)
     const int64_t x_cols = parts > 1 ? mx4_split_cols(C) : ((int64_t)C + 7) / 8 * 8, y16 = 16 / (int64_t)sizeof(Out);
