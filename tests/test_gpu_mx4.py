@@ -261,7 +261,7 @@ def test_bench_shapes(fmt):
 
 
 @pytest.mark.parametrize("fmt", list(DTYPES))
-@pytest.mark.parametrize("tokens,rows,cols", [(5, 8448, 4096), (1300, 4352, 96), (1300, 4352, 352), (2600, 2304, 352), (2600, 2304, 200),
+@pytest.mark.parametrize("tokens,rows,cols", [(1, 8200, 8192), (5, 8448, 4096), (1300, 4352, 96), (1300, 4352, 352), (2600, 2304, 352), (2600, 2304, 200),
                                               (9000, 520, 64), (700, 6400, 416)])
 def test_many_tiles(fmt, tokens, rows, cols):
     """Tiles that follow each other on an SM, with boxes of codes that end within a stage, and a weight of more values than

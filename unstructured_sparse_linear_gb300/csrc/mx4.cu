@@ -19,7 +19,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSteps = 4;  // of 256 values a warp
 constexpr int kMx4FewTokens = 8;
-constexpr int64_t kMx4FewValues = 1 << 25;  // of the weight
+constexpr int64_t kMx4FewValues = 1 << 24, kMx4OneValues = 1 << 26;  // of the weight
 
 // Rows as both kernels walk them: in steps of 256 values. A matrix of whole blocks in contiguous rows is one row.
 struct Walk {
@@ -354,12 +354,13 @@ cudaError_t launch_mx4_dequantize(int dt, const uint8_t* codes, const uint8_t* s
     return dequantize<__nv_bfloat16>(codes, scales, rows, cols, Y, ldy, s);
 }
 
-// The kernels without tensor-core tiles, forward, us as these kernels / the tiles. 1 token: 4096 x 4096 6.3 / 9.2,
-// 11008 x 4096 12.6 / 15.6, 8192 x 8192 16.5 / 17, fp16 14.7 / 15.4. 2 to 8: 4096 x 4096 8.1 / 9.3, 1024 x 16384 8.1 / 15.4,
-// 1536 x 384 3.5 / 4.9, but 4096 x 11008 18.6 / 15.7, 11008 x 4096 21 / 15.7, 8192 x 8192 23 / 17. They take any rows.
+// The kernels without tensor-core tiles, forward, us as these kernels / the tiles. 1 token: 4096 x 4096 6.3 / 8.6,
+// 11008 x 4096 12.5 / 13.9, 8192 x 8192 16.5 / 15.2, fp16 14.7 / 13.0. 2 to 8: 4096 x 4096 8.1 / 8.6, fp16 6.7 / 7.6,
+// 1024 x 16384 8.1 / 13.1, 1536 x 384 3.5 / 4.9, but 6144 x 4096 12.5 / 10.1, fp16 9.8 / 8.9, 8192 x 8192 23 / 15. They take any rows.
 static bool mx4_few(int dt, bool back, const Mx4Args& a) {
     if (back || dt == kF32 || a.tokens > kMx4FewTokens) return false;
-    return a.tokens == 1 || (int64_t)a.rows * a.cols <= kMx4FewValues || !mx4_tile_rows(a.X, a.ldx, a.cols, 2) ||
+    const int64_t values = (int64_t)a.rows * a.cols;
+    return (a.tokens == 1 ? values < kMx4OneValues : values <= kMx4FewValues) || !mx4_tile_rows(a.X, a.ldx, a.cols, 2) ||
            !mx4_tile_rows(a.Y, a.ldy, a.rows, 2);
 }
 

@@ -8,11 +8,11 @@
 // per 256 features. Codes come by TMA as well: a thread decodes its own row (a TMEM lane), 16 bytes of it at a time.
 // A weight that is decoded into shared memory is written and read there again by each product, and shared memory's bandwidth is
 // then what bounds the kernel at every size; in tensor memory neither takes any of it (64 tokens 4096 -> 11008 22.4 us so and
-// 16 here, 1037 tokens 4096 -> 4096 fp16 40 and 26).
-// Bounds. 128 features x 128 of the contraction are 64 warps' words of 8 codes: 22 cycles of a scheduler's integer pipe each in
-// bf16 (conversions, byte moves), 14 in fp16, which with the messages makes a stage 650 cycles: what small products take (64
-// tokens: 16 us for 22.5 MB of codes, 14.6 in fp16). From 160 tokens a tile on the products take longer: 8192 tokens
-// 2048 -> 8192 150 us, 1830 TFLOP/s.
+// 14.1 here, 1037 tokens 4096 -> 4096 fp16 40 and 25.4).
+// Bounds. 128 features x 256 of the contraction are 128 warps' words of 8 codes, 32 a scheduler: 22 cycles of its integer pipe each in
+// bf16 (conversions, byte moves), 14 in fp16, which with the messages makes a stage 1000 cycles: what small products take (64
+// tokens: 14.1 us for 22.5 MB of codes, 12.2 in fp16). From 160 tokens a tile on the products take longer: 8192 tokens
+// 2048 -> 8192 149 us, 1840 TFLOP/s.
 // fp32: the weight's values are bf16 numbers, and X is the sum of three bf16 parts (all 24 bits), which multiply the same
 // decoded weight; the first part's products have an accumulator of their own (relative error 4e-8 at 384 of the contraction,
 // 2e-7 at 4096; 1.2e-6 at 384 with one accumulator).
@@ -26,7 +26,8 @@ constexpr int kCodeBoxes = 4;   // of 256 of the contraction: whole 128-byte lin
 constexpr uint32_t kXRing = 128 * 1024;
 constexpr int kTmemCols = 512;
 
-// A stage holds kSub times 64 of the contraction, and X in kParts parts. Warps 0 to 3 finish (a TMEM lane quarter each), then
+// A stage holds kSub times 64 of the contraction (four, or two, which leaves room for tiles of more than 128 tokens; fp32: two, or
+// one), and X in kParts parts. Warps 0 to 3 finish (a TMEM lane quarter each), then
 // groups of four decode, one warp loads X, one multiplies, one loads codes.
 template <typename Out, int kSub_>
 struct FwdCfg {

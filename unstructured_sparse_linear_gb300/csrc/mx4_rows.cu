@@ -8,8 +8,8 @@
 // The codes come by asynchronous copies into rings of the warp's own, X through registers, a phase of the contraction ahead. A
 // CTA's warps have two groups of 16 features and share the contraction by four, a cluster's CTAs share it once more; partial
 // sums are added in one order. Bound by the first loads and by what a warp issues (about 100 instructions a block, a
-// third of them for staging X). 8 tokens, 4096 x 4096: 8.1 us (tcgen05 tiles 9.4), fp16 6.8 (8.7); beyond 2^25 values of W the
-// tiles take less (11008 x 4096 15.7 and 21.4).
+// third of them for staging X). 8 tokens, 4096 x 4096: 8.1 us (tcgen05 tiles 8.7), fp16 6.7 (7.7); beyond 2^24 values of W the
+// tiles take less (11008 x 4096 13.9 and 21.2).
 #include <type_traits>
 
 #include "internal.h"
