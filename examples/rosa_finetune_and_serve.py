@@ -5,7 +5,8 @@
 Training: a frozen two-layer MLP whose projections carry a low-rank and a sparse update
 (RosaLinear: csr_add into the weight, lora_add beside the projection; lora_grad and sddmm
 backward), the gradients clipped by their global norm (clip_grads on a GradSet of fixed buffers)
-and applied by masked_adam to fp32 master copies. Serving: one batch of requests with several
+and applied by masked_adam to fp32 master copies; once more with the frozen weights in 4 bits
+(mx4_linear, mx4_linear_grad) and dropout in front of the low-rank factors. Serving: one batch of requests with several
 adapters, their prompts first and then one token each, through lora_add.
 """
 from __future__ import annotations
@@ -27,11 +28,13 @@ def random_mask(out_features, in_features, density, gen, device):
     return row_offsets, keep.nonzero()[:, 1].to(torch.int16).contiguous()
 
 
-def rosa_layer(out_features, in_features, rank, gen, device, dtype):
+def rosa_layer(out_features, in_features, rank, gen, device, dtype, four_bits=False, dropout=0.0):
     w = torch.randn(out_features, in_features, generator=gen, device=device).mul_(in_features ** -0.5).to(dtype)
+    if four_bits:  # the low-rank part only: beside a sparse one the weight is formed in every pass
+        return sp.RosaLinear(sp.mx4_quantize(w), rank, scale=2.0, dropout=dropout)
     row_offsets, col_idx = random_mask(out_features, in_features, 0.01, gen, device)
     values = torch.zeros(col_idx.numel(), dtype=dtype, device=device)
-    return sp.RosaLinear(w, rank, scale=2.0, row_offsets=row_offsets, col_idx=col_idx, values=values)
+    return sp.RosaLinear(w, rank, scale=2.0, row_offsets=row_offsets, col_idx=col_idx, values=values, dropout=dropout)
 
 
 class Trainer:
@@ -56,10 +59,14 @@ class Trainer:
         return norm
 
 
-def train(steps=20, tokens=1000, hidden=256, inner=512, rank=8, dtype=torch.bfloat16, device="cuda"):
-    """Fits the MLP to a target that differs from it; returns the losses and gradient norms."""
+def train(steps=20, tokens=1000, hidden=256, inner=512, rank=8, dtype=torch.bfloat16, device="cuda", four_bits=False,
+          dropout=0.0):
+    """Fits the MLP to a target that differs from it; returns the losses and gradient norms. four_bits: the frozen
+    weights are kept in 4 bits; dropout: in front of the low-rank factors."""
     gen = torch.Generator(device=device).manual_seed(0)
-    up, down = rosa_layer(inner, hidden, rank, gen, device, dtype), rosa_layer(hidden, inner, rank, gen, device, dtype)
+    torch.manual_seed(0)  # (the layers' dropout draws its states from torch's generator)
+    up, down = (rosa_layer(n_out, n_in, rank, gen, device, dtype, four_bits, dropout)
+                for n_out, n_in in ((inner, hidden), (hidden, inner)))
     X = torch.randn(tokens, hidden, generator=gen, device=device).to(dtype)
     target = torch.randn(tokens, hidden, generator=gen, device=device).to(dtype)
     trainer = Trainer([*up.parameters(), *down.parameters()])
@@ -98,6 +105,8 @@ def main():
     losses, norms = train()
     print("loss", " ".join(f"{x:.3f}" for x in losses))
     print("gradient norm", " ".join(f"{x:.3f}" for x in norms))
+    losses, _ = train(four_bits=True, dropout=0.1)
+    print("loss, frozen weights in 4 bits and dropout", " ".join(f"{x:.3f}" for x in losses))
     for s in serve()["steps"]:
         print(f"served {len(s['ids'])} tokens of {int(s['ids'].max()) + 1} adapters:", tuple(s["Y"].shape))
 

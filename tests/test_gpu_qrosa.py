@@ -5,6 +5,8 @@ Tolerance, fixed before any run: as for the dense layer, each stage rounds to th
 rounding to what the factors see and one to its gradient: relative Frobenius errors within eight half-ulps (2^-8 for bf16,
 2^-11 for fp16), 1e-5 in fp32. The 4-bit values themselves are exact."""
 import copy
+import importlib.util
+import os
 
 import numpy as np
 import pytest
@@ -247,3 +249,12 @@ def test_adapter_training_and_serving_run():
         assert rel_fro(as_f64(whole), want) <= REL[torch.bfloat16]
         for t in (0, 3, 499):
             assert rel_fro(as_f64(layer(X[t:t + 1]))[0], want[t]) <= REL[torch.bfloat16]
+
+
+def test_example_with_four_bits():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "rosa_finetune_and_serve.py")
+    spec = importlib.util.spec_from_file_location("rosa_example_4bit", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    losses, norms = ex.train(steps=4, four_bits=True, dropout=0.1)
+    assert np.isfinite(losses).all() and all(x > 0 for x in norms)

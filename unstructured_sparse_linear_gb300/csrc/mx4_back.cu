@@ -10,7 +10,7 @@
 // code alone).
 // Bounds. Per 64 of the contraction shared memory takes the decoded operand twice (written, read) and X twice: 512 cycles at 256
 // tokens, as many as the products (8192 tokens 8192 -> 2048: 91 % of its wavefronts, tensor pipe 82 %). 4096 tokens
-// 11008 -> 4096 213 us, 1736 TFLOP/s; 2048 tokens 4096 -> 4096 fp16 47; 64 tokens 26.5, the latency of a stage's decoding.
+// 11008 -> 4096 213 us, 1736 TFLOP/s; 2048 tokens 4096 -> 4096 fp16 47; 64 tokens 24 to 28, the latency of a stage's decoding.
 // fp32: the weight's values are bf16 numbers, and X is the sum of three bf16 parts (all 24 bits), which multiply the same
 // decoded weight; the first part's products have an accumulator of their own.
 #include "mx4_pair.cuh"
@@ -81,7 +81,7 @@ mx4_back_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, con
     }
     // Codes are asked for in pieces of 64 bytes a row, by threads that wait for them: for the first token tile, which is the
     // first to read them, the loader has them fetched into L2 kAheadL2 stages before (64 tokens 11008 -> 4096, weight not in
-    // L2: 21.5 us, 28 without).
+    // L2: 23.6 us, 27.5 without; in it 21.2 and 20.7).
     auto fetch = [&](int f0, int c) {
         if (c < me.c1)
             asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(&map_w)),
