@@ -69,7 +69,7 @@ def test_product_refusals(lib, back):
         assert product(lib, back, **odd, ws=bad, size=need) == 1
     big = 0x7fff0001
     assert product(lib, back, tokens=big) == 2 and product(lib, back, rows=big) == 2 and product(lib, back, cols=big) == 2
-    long = dict(rows=715827713) if back else dict(cols=715827713)  # three parts of fp32 beside each other pass 2^31
+    long = dict(rows=715827841) if back else dict(cols=715827841)  # three parts of fp32 beside each other pass 2^31
     assert product(lib, back, dtype=0, **long) == 2 and product(lib, back, dtype=1, tokens=0, **long) == 0
 
 
