@@ -278,6 +278,23 @@ def test_many_tiles(fmt, tokens, rows, cols):
         assert_elementwise(Y, (x @ m).cpu().numpy(), (x.abs() @ m.abs()).cpu().numpy(), m.shape[0], fmt, f"{back}")
 
 
+@pytest.mark.parametrize("tokens,rows,cols,pad", [(3776, 5304, 24, 3), (3776, 5304, 24, 0), (3000, 5000, 96, 8), (2900, 5304, 300, 1)])
+def test_short_sums_of_many_tiles(tokens, rows, cols, pad):
+    """A stage or two of the contraction in each of a pair's many tiles, whose codes may arrive in any order: the same right
+    result every time."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(cols)
+    W = sp.mx4_quantize(torch.randn(rows, cols, device=DEV, generator=g))
+    w = sp.mx4_dequantize(W).double()
+    X = torch.randn(tokens, cols + 2 * pad, device=DEV, generator=g).bfloat16()[:, pad:pad + cols]
+    x = X.double()
+    want, mass = x @ w.t(), x.abs() @ w.t().abs()
+    first = sp.mx4_linear(X, W)
+    assert_elementwise(first, want.cpu().numpy(), mass.cpu().numpy(), cols, "bf16", "Y")
+    for _ in range(300):
+        assert torch.equal(sp.mx4_linear(X, W), first)
+
+
 def test_streams_and_graphs():
     """Two streams at once, and a captured run whose replays see new inputs."""
     rng = np.random.default_rng(9)

@@ -21,8 +21,8 @@
 namespace spops {
 namespace {
 
-constexpr int kMaxSlots = 12;   // stages of X and of the decoded weight
-constexpr int kCodeBoxes = 4;   // of 256 of the contraction: whole 128-byte lines
+constexpr int kCodeBoxes = 4;           // of 256 of the contraction: whole 128-byte lines
+constexpr int kMaxSlots = kCodeBoxes;  // stages of X and of the decoded weight: a stage's box lies at most a round of boxes before it
 constexpr uint32_t kXRing = 128 * 1024;
 constexpr int kTmemCols = 512;
 
@@ -285,8 +285,11 @@ mx4_fwd_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, cons
                 boxes += tile_boxes;
             }
             const uint32_t box = boxes + (uint32_t)c / Cfg::kBoxStages, cs = box % kCodeBoxes, in_box = (uint32_t)c % Cfg::kBoxStages;
-            const bool got = wait(smem_u32(&sh.codes_full[cs]), box / kCodeBoxes & 1);
-            const bool ok = __all_sync(0xffffffffu, wait(smem_u32(&sh.empty[s]), ph) && got);
+            // The slot first: then the stage before it there has been multiplied, so all stages up to that one had their codes, those
+            // of the box before this one in its place among them (kMaxSlots), and the parity can mean no earlier phase. (Boxes
+            // arrive in any order: with the codes first, a box that was not there passed for one.)
+            const bool free = wait(smem_u32(&sh.empty[s]), ph);
+            const bool ok = __all_sync(0xffffffffu, free && wait(smem_u32(&sh.codes_full[cs]), box / kCodeBoxes & 1));
             if (ok) {
                 tc::fence_after_sync();
                 const uint32_t codes = from + cs * Cfg::kBoxBytes, first = in_box * kBlocks, col = to + s * (32 * kSub);
