@@ -44,7 +44,7 @@ __device__ __forceinline__ bool exact_in(uint32_t b) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
-        constexpr bool kF16 = std::is_same<T, __half>::value;
+    constexpr bool kF16 = std::is_same<T, __half>::value;
     __shared__ __align__(16) uint8_t xs[kStaged * kPitch];
     __shared__ float xe[kStaged];  // bf16: what X was divided by
     const int tid = threadIdx.x, lane = tid & 31, L = g.lanes, sub = lane & (L - 1);
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                 if (blk < n_blocks) {
                     const uint32_t c[4] = {w[u].x, w[u].y, w[u].z, w[u].w}, sc = b[u];
                     const uint32_t x = xbase + blk * kPitch;
-                    float scale = mx4::scale_f32(sc);
+                    float scale = mx4::scale_f32(sc), e = kF16 ? 1.f : xe[blk];
                     float sum = 0.f, sum1 = 0.f;
                     if (exact_in<T>(sc) || (c[0] | c[1] | c[2] | c[3]) == 0) {
 #pragma unroll
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                             fma2(p[3], y.w, sum, sum1);
                         }
                         sum += sum1;
-                    } else {  // the values as X's type has them
-                        scale = 1.f;
+                    } else {  // the values as X's type has them, and X as it was given (staged, it may leave fp32's range)
+                        scale = e = 1.f;
 #pragma unroll 1
                         for (int k = 0; k < 4; ++k) {
                             const uint32_t word = k == 0 ? c[0] : k == 1 ? c[1] : k == 2 ? c[2] : c[3];
@@ -157,14 +157,12 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                             mx4::decode8_any<T>(word, sc, o);
                             float f[8];
                             Elt<T>::unpack(make_uint4(o[0], o[1], o[2], o[3]), f);
+                            const int64_t at = (s0 + blk) * kMx4Block + k * 8;
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const __half h = *reinterpret_cast<const __half*>(xs + blk * kPitch + k * 16 + e * 2);
-                                sum = fmaf(f[e], __half2float(h), sum);
-                            }
+                            for (int j = 0; j < 8; ++j) sum = fmaf(f[j], at + j < g.a.cols ? Elt<T>::to_f(X[at + j]) : 0.f, sum);
                         }
                     }
-                    const float e = kF16 ? 1.f : xe[blk], both = scale * e;
+                    const float both = scale * e;
                     acc = both <= 3.402823466e38f ? fmaf(sum, both, acc) : fmaf(sum * scale, e, acc);
                 }
                 ask(u);
