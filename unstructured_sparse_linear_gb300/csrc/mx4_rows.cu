@@ -4,7 +4,7 @@
 // instruction in fp16: the codes become fp16 numbers by conversion (exact, without their scale), a block of 32 is two
 // products into sums of its own, which are then added times the block's scale in fp32. So decoding costs 8 conversions
 // for 16 x 32 values, whatever X's type. bf16 X is staged as fp16 numbers times a power of two for each 32 of them, which is
-// exact down to 2^-31 of their largest and off by 2^-39 of it below.
+// exact where none but zeros lies below 2^-31 of the largest; other blocks of a token are multiplied value by value in fp32.
 // The codes come by asynchronous copies into rings of the warp's own, X through registers, a phase of the contraction ahead. A
 // CTA's warps have two groups of 16 features and share the contraction by four, a cluster's CTAs share it once more; partial
 // sums are added in one order. Bound by the first loads and by what a warp issues (about 100 instructions a block, a
@@ -96,6 +96,24 @@ __device__ __forceinline__ float rare_factor(uint32_t b) {
     return std::is_same<T, __half>::value && b != 255 ? 1.f : mx4::scale_f32(b);
 }
 
+// A block's products with n values of a token, added to two features' sums: value by value, as X's type has them. c0, c1: the
+// features' codes in shared memory.
+template <typename T>
+__device__ __noinline__ float2 add_values(const T* x, int n, uint32_t c0, uint32_t c1, uint32_t b0, uint32_t b1, float2 acc) {
+    const float s0 = mx4::scale_f32(b0), s1 = mx4::scale_f32(b1);
+    uint32_t w0 = 0, w1 = 0;
+    for (int i = 0; i < n; ++i, w0 >>= 4, w1 >>= 4) {
+        if (i % 8 == 0) {
+            w0 = lds_u32(c0 + i / 2);
+            w1 = lds_u32(c1 + i / 2);
+        }
+        const float v = Elt<T>::to_f(x[i]);
+        acc.x = fmaf(Elt<T>::to_f(Elt<T>::from_f(mx4::value_f32(w0, s0))), v, acc.x);
+        acc.y = fmaf(Elt<T>::to_f(Elt<T>::from_f(mx4::value_f32(w1, s1))), v, acc.y);
+    }
+    return acc;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsArgs g) {
     constexpr bool kF16 = std::is_same<T, __half>::value;
@@ -174,7 +192,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
             }
         }
     };
+    // (bf16: where fp16 does not hold a block, as eight bits of a number below 2^-31 of the largest, its power of two is 0)
+    bool unheld = false;  // one of those among this thread's of the phase
     auto store_x = [&](int p) {
+        unheld = false;
         if (p >= phases) return;
         const uint32_t to = sbase + (p & 1) * kX, te = xe_at + (p & 1) * kXe;
 #pragma unroll
@@ -198,10 +219,26 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
                 const uint32_t e14 = max(m >> 7, 31u);                     // the largest comes to 2^14 .. 2^15, tiny ones below
                 const float down = __uint_as_float((268u - e14) << 23);  // 2^(141 - e14)
+                const uint32_t limit = (e14 - 31) << 7;
+                uint32_t least = __vminu2(__vminu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vminu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                least = min(least >> 16, least & 0xffffu);
+                bool low = false;
+                if (least < limit) {  // a zero, or a number that is too small
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t bits = __float_as_uint(f[e]) >> 16 & 0x7fffu;
+                        low |= bits != 0 && bits < limit;
+                    }
+                }
+                if (__any_sync(0xffffffffu, low)) {
+                    low |= __shfl_xor_sync(0xffffffffu, low, 1) != 0;
+                    low |= __shfl_xor_sync(0xffffffffu, low, 2) != 0;
+                    unheld |= low;
+                }
                 v = make_uint4(Elt<__half>::p2(f[0] * down, f[1] * down), Elt<__half>::p2(f[2] * down, f[3] * down),
                                Elt<__half>::p2(f[4] * down, f[5] * down), Elt<__half>::p2(f[6] * down, f[7] * down));
                 if ((c & 3) == 0)
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(te + ((c >> 2) * kTokens + r) * 4), "r"((e14 - 14) << 23)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(te + ((c >> 2) * kTokens + r) * 4), "r"(low ? 0u : (e14 - 14) << 23)
                                  : "memory");
             }
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + r * kRow + c * 16), "r"(v.x), "r"(v.y),
@@ -220,13 +257,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
     int slot = 0;
     for (int p = 0; p < phases; ++p) {
         tc::cp_async_wait<kRing - 2>();
-        __syncthreads();
+        const bool any_unheld = !kF16 && __syncthreads_or(unheld);
+        if (kF16) __syncthreads();
         load_codes(p + kRing - 1);
         store_x(p + 1);
         load_x(p + 2);
         const uint32_t x0 = sbase + (p & 1) * kX + q * kRow + wj * kShare * 64 + t * 16;
         const uint32_t e0 = xe_at + (p & 1) * kXe + (wj * kShare * kTokens + 2 * t) * 4;
         const uint32_t c0 = ring + slot * kSlot + q * kCodesRow + t * 4, s0 = ring + slot * kSlot + kCodes + q * kShare;
+        const int now = slot;
         slot = slot + 1 == kRing ? 0 : slot + 1;
 #pragma unroll 2
         for (int b = 0; b < kShare; ++b) {
@@ -266,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
             } else {
                 float ea, eb;
                 asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ea), "=f"(eb) : "r"(e0 + b * kTokens * 4));
+                const float before[4] = {acc[0], acc[1], acc[2], acc[3]};
                 if (easy) {
                     acc[0] = fmaf(d[0], m0 * ea, acc[0]);
                     acc[1] = fmaf(d[1], m0 * eb, acc[1]);
@@ -277,6 +317,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
                     acc[1] = (float)(acc[1] + (double)d[1] * m0 * eb);
                     acc[2] = (float)(acc[2] + (double)d[2] * m1 * ea);
                     acc[3] = (float)(acc[3] + (double)d[3] * m1 * eb);
+                }
+                if (any_unheld) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if ((e ? eb : ea) == 0.f) {  // (instead of those)
+                            const int64_t k = ((int64_t)(p0 + p) * kBlocks + wj * kShare + b) * kMx4Block;
+                            const uint32_t c0_b = ring + (uint32_t)now * kSlot + q * kCodesRow + b * 16;
+                            const float2 y = add_values(X + (2 * t + e) * g.a.ldx + k, (int)min64(kMx4Block, g.a.cols - k), c0_b,
+                                                        c0_b + 8 * kCodesRow, b0, b1, make_float2(before[e], before[2 + e]));
+                            acc[e] = y.x;
+                            acc[2 + e] = y.y;
+                        }
                 }
             }
         }

@@ -4,8 +4,8 @@
 // values of one block, so a warp reads 512 bytes in a row, and four such loads are under way, the next row's among them.
 // The codes become fp16 numbers by conversion and meet X as fp16 numbers in fused products with fp32 sums (6 cycles of a
 // scheduler for two values and a token; bringing W to X's type first took 9), one sum per block, which is then multiplied with
-// the block's scale. bf16 X is staged as fp16 numbers times a power of two for each 32 of them, which is exact down to 2^-31 of
-// their largest and off by 2^-39 of it below. Sums are added over the lanes in one order. Bound by the call, the first
+// the block's scale. bf16 X is staged as fp16 numbers times a power of two for each 32 of them, which is exact where none but zeros
+// lies below 2^-31 of the largest; other blocks are multiplied value by value in fp32. Sums are added over the lanes in one order. Bound by the call, the first
 // load, and what a warp issues (about 50 instructions a word of codes). 4096 x 4096: 6.3 us (8.0 with the kernel for eight
 // tokens), 11008 x 4096 12.5 (20.8; tcgen05 tiles 13.9).
 #include <type_traits>
@@ -100,14 +100,17 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
             if constexpr (!kF16) {
                 float f[8];
                 Elt<T>::unpack(make_uint4(v[0], v[1], v[2], v[3]), f);
-                uint32_t m = 0;  // the largest finite magnitude
+                uint32_t m = 0, least = 0x7f800000u;  // the largest finite magnitude, the least but zero
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const uint32_t bits = __float_as_uint(f[e]) & 0x7fffffffu;
                     m = max(m, bits < 0x7f800000u ? bits : 0u);
+                    least = min(least, bits ? bits : 0x7f800000u);
                 }
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
                 const int e14 = max((int)(m >> 23), 31);  // the largest comes to 2^14 .. 2^15, small ones below
                 const float down = __uint_as_float((uint32_t)(268 - e14) << 23);  // 2^(141 - e14)
 #pragma unroll
@@ -115,7 +118,9 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                     const __half2 h = __floats2half2_rn(f[2 * e] * down, f[2 * e + 1] * down);
                     v[e] = reinterpret_cast<const uint32_t&>(h);
                 }
-                if ((c & 3) == 0 && c < n_blocks * 4) xe[c >> 2] = __uint_as_float((uint32_t)(e14 - 14) << 23);  // 2^(e14 - 141)
+                // 2^(e14 - 141), or 0 for a block that fp16 does not hold: eight bits of a number below 2^-31 of the largest
+                if ((c & 3) == 0 && c < n_blocks * 4)
+                    xe[c >> 2] = (int)(least >> 23) < e14 - 31 ? 0.f : __uint_as_float((uint32_t)(e14 - 14) << 23);
             }
             if (c < n_blocks * 4)
                 *reinterpret_cast<uint4*>(xs + (c >> 2) * kPitch + (c & 3) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
@@ -133,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                     const uint32_t x = xbase + blk * kPitch;
                     float scale = mx4::scale_f32(sc), e = kF16 ? 1.f : xe[blk];
                     float sum = 0.f, sum1 = 0.f;
-                    if (exact_in<T>(sc) || (c[0] | c[1] | c[2] | c[3]) == 0) {
+                    if ((exact_in<T>(sc) || (c[0] | c[1] | c[2] | c[3]) == 0) && e != 0.f) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint32_t p[4] = {mx4::pair_f16<0>(c[k]), mx4::pair_f16<1>(c[k]), mx4::pair_f16<2>(c[k]),
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                             fma2(p[3], y.w, sum, sum1);
                         }
                         sum += sum1;
-                    } else {  // the values as X's type has them, and X as it was given (staged, it may leave fp32's range)
+                    } else {  // the values as X's type has them, and X as it was given (staged, it may leave fp32's range, or have lost bits)
                         scale = e = 1.f;
 #pragma unroll 1
                         for (int k = 0; k < 4; ++k) {
