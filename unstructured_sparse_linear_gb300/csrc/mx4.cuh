@@ -86,5 +86,12 @@ __device__ __forceinline__ void decode8_any(uint32_t w, uint32_t b, uint32_t (&o
     o[3] = v.w;
 }
 
+// The least magnitude but zero of bf16 numbers, eight of them two a word, as a bit pattern; beyond all of them where there is none.
+__device__ __forceinline__ int least8(const uint4& v) {
+    const uint32_t a = 0x7fff7fffu;  // (a signed half less 32767 + 1: zeros become the largest)
+    const uint32_t m = __vmins2(__vmins2((v.x & a) + a, (v.y & a) + a), __vmins2((v.z & a) + a, (v.w & a) + a));
+    return min((int)m >> 16, (int)(m << 16) >> 16) + 32769;
+}
+
 }  // namespace mx4
 }  // namespace spops

@@ -192,12 +192,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
             }
         }
     };
-    // (bf16: where fp16 does not hold a block, as eight bits of a number below 2^-31 of the largest, its power of two is 0)
-    bool unheld = false;  // one of those among this thread's of the phase
+    bool unheld = false;  // bf16: fp16 does not hold a block of this thread's; it is staged as zeros, its power of two as 0
     auto store_x = [&](int p) {
         unheld = false;
         if (p >= phases) return;
         const uint32_t to = sbase + (p & 1) * kX, te = xe_at + (p & 1) * kXe;
+        bool low = false;  // eight bits of a number below 2^-31 of its block's largest are more than fp16 holds there
+        uint32_t e14s[kLoads];
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
             const int i = u * kThreads + tid, r = i / (kBlocks * 4), c = i % (kBlocks * 4);
@@ -219,31 +220,33 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
                 const uint32_t e14 = max(m >> 7, 31u);                     // the largest comes to 2^14 .. 2^15, tiny ones below
                 const float down = __uint_as_float((268u - e14) << 23);  // 2^(141 - e14)
-                const uint32_t limit = (e14 - 31) << 7;
-                uint32_t least = __vminu2(__vminu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vminu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-                least = min(least >> 16, least & 0xffffu);
-                bool low = false;
-                if (least < limit) {  // a zero, or a number that is too small
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t bits = __float_as_uint(f[e]) >> 16 & 0x7fffu;
-                        low |= bits != 0 && bits < limit;
-                    }
-                }
-                if (__any_sync(0xffffffffu, low)) {
-                    low |= __shfl_xor_sync(0xffffffffu, low, 1) != 0;
-                    low |= __shfl_xor_sync(0xffffffffu, low, 2) != 0;
-                    unheld |= low;
-                }
+                low |= mx4::least8(v) < ((int)e14 - 31) << 7;
                 v = make_uint4(Elt<__half>::p2(f[0] * down, f[1] * down), Elt<__half>::p2(f[2] * down, f[3] * down),
                                Elt<__half>::p2(f[4] * down, f[5] * down), Elt<__half>::p2(f[6] * down, f[7] * down));
+                e14s[u] = e14;
                 if ((c & 3) == 0)
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(te + ((c >> 2) * kTokens + r) * 4), "r"(low ? 0u : (e14 - 14) << 23)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(te + ((c >> 2) * kTokens + r) * 4), "r"((e14 - 14) << 23)
                                  : "memory");
             }
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + r * kRow + c * 16), "r"(v.x), "r"(v.y),
                          "r"(v.z), "r"(v.w)
                          : "memory");
+        }
+        if constexpr (!kF16) {
+            if (!__any_sync(0xffffffffu, low)) return;
+#pragma unroll
+            for (int u = 0; u < kLoads; ++u) {
+                const int i = u * kThreads + tid, r = i / (kBlocks * 4), c = i % (kBlocks * 4);
+                low = mx4::least8(xr[u]) < ((int)e14s[u] - 31) << 7;
+                low |= __shfl_xor_sync(0xffffffffu, low, 1) != 0;
+                low |= __shfl_xor_sync(0xffffffffu, low, 2) != 0;
+                if (low) {
+                    unheld = true;
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(to + r * kRow + c * 16), "r"(0u) : "memory");
+                    if ((c & 3) == 0)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(te + ((c >> 2) * kTokens + r) * 4), "r"(0u) : "memory");
+                }
+            }
         }
     };
 
@@ -305,7 +308,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
             } else {
                 float ea, eb;
                 asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ea), "=f"(eb) : "r"(e0 + b * kTokens * 4));
-                const float before[4] = {acc[0], acc[1], acc[2], acc[3]};
                 if (easy) {
                     acc[0] = fmaf(d[0], m0 * ea, acc[0]);
                     acc[1] = fmaf(d[1], m0 * eb, acc[1]);
@@ -313,25 +315,29 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
                     acc[3] = fmaf(d[3], m1 * eb, acc[3]);
                 } else {
                     // (whose product may leave fp32's range where the sum does not)
-                    acc[0] = (float)(acc[0] + (double)d[0] * m0 * ea);
-                    acc[1] = (float)(acc[1] + (double)d[1] * m0 * eb);
-                    acc[2] = (float)(acc[2] + (double)d[2] * m1 * ea);
-                    acc[3] = (float)(acc[3] + (double)d[3] * m1 * eb);
-                }
-                if (any_unheld) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        if ((e ? eb : ea) == 0.f) {  // (instead of those)
-                            const int64_t k = ((int64_t)(p0 + p) * kBlocks + wj * kShare + b) * kMx4Block;
-                            const uint32_t c0_b = ring + (uint32_t)now * kSlot + q * kCodesRow + b * 16;
-                            const float2 y = add_values(X + (2 * t + e) * g.a.ldx + k, (int)min64(kMx4Block, g.a.cols - k), c0_b,
-                                                        c0_b + 8 * kCodesRow, b0, b1, make_float2(before[e], before[2 + e]));
-                            acc[e] = y.x;
-                            acc[2 + e] = y.y;
-                        }
+                    if (ea != 0.f) {  // (an infinite value's product with the zeros of a block that is not held)
+                        acc[0] = (float)(acc[0] + (double)d[0] * m0 * ea);
+                        acc[2] = (float)(acc[2] + (double)d[2] * m1 * ea);
+                    }
+                    if (eb != 0.f) {
+                        acc[1] = (float)(acc[1] + (double)d[1] * m0 * eb);
+                        acc[3] = (float)(acc[3] + (double)d[3] * m1 * eb);
+                    }
                 }
             }
         }
+        if (any_unheld)
+            for (int b = 0; b < kShare; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (lds_u32(e0 + (b * kTokens + e) * 4) == 0) {
+                        const int64_t k = ((int64_t)(p0 + p) * kBlocks + wj * kShare + b) * kMx4Block;
+                        const uint32_t c = ring + (uint32_t)now * kSlot + q * kCodesRow + b * 16;
+                        const float2 y = add_values(X + (2 * t + e) * g.a.ldx + k, (int)min64(kMx4Block, g.a.cols - k), c, c + 8 * kCodesRow,
+                                                    lds_u8(s0 + b), lds_u8(s0 + 8 * kShare + b), make_float2(acc[e], acc[2 + e]));
+                        acc[e] = y.x;
+                        acc[2 + e] = y.y;
+                    }
     }
     tc::cp_async_wait<0>();
     __syncthreads();

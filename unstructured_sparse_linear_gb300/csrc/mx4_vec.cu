@@ -42,6 +42,19 @@ __device__ __forceinline__ bool exact_in(uint32_t b) {
     return std::is_same<T, __half>::value ? b - 104u <= 36u || b == 255u : b <= 252u || b == 255u;
 }
 
+// A block's products with up to 32 values of X, value by value, as X's type has them.
+template <typename T>
+__device__ __noinline__ float value_sum(const T* x, int64_t left, uint4 codes, uint32_t b) {
+    const float s = mx4::scale_f32(b);
+    float sum = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < kMx4Block && k < left; ++k) {
+        const uint32_t w = k < 8 ? codes.x : k < 16 ? codes.y : k < 24 ? codes.z : codes.w;
+        sum = fmaf(Elt<T>::to_f(Elt<T>::from_f(mx4::value_f32(w >> (4 * (k & 7)), s))), Elt<T>::to_f(x[k]), sum);
+    }
+    return sum;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
     constexpr bool kF16 = std::is_same<T, __half>::value;
@@ -80,6 +93,7 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) ask(u);
         if (s0 > 0) __syncthreads();  // the segment before has been read
+        bool unheld = false;  // bf16: fp16 does not hold a block of this thread's; it is staged as zeros, its xe as 0
         for (int i0 = 0; i0 < n_blocks * 4; i0 += kThreads) {
             const int c = i0 + tid;  // 16 bytes of X
             const int64_t k = s0 * kMx4Block + c * 8;
@@ -100,32 +114,36 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
             if constexpr (!kF16) {
                 float f[8];
                 Elt<T>::unpack(make_uint4(v[0], v[1], v[2], v[3]), f);
-                uint32_t m = 0, least = 0x7f800000u;  // the largest finite magnitude, the least but zero
+                uint32_t m = 0;  // the largest finite magnitude
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const uint32_t bits = __float_as_uint(f[e]) & 0x7fffffffu;
                     m = max(m, bits < 0x7f800000u ? bits : 0u);
-                    least = min(least, bits ? bits : 0x7f800000u);
                 }
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
                 const int e14 = max((int)(m >> 23), 31);  // the largest comes to 2^14 .. 2^15, small ones below
                 const float down = __uint_as_float((uint32_t)(268 - e14) << 23);  // 2^(141 - e14)
+                bool low = mx4::least8(make_uint4(v[0], v[1], v[2], v[3])) < (e14 - 31) << 7;  // (more than fp16 holds there)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const __half2 h = __floats2half2_rn(f[2 * e] * down, f[2 * e + 1] * down);
                     v[e] = reinterpret_cast<const uint32_t&>(h);
                 }
-                // 2^(e14 - 141), or 0 for a block that fp16 does not hold: eight bits of a number below 2^-31 of the largest
-                if ((c & 3) == 0 && c < n_blocks * 4)
-                    xe[c >> 2] = (int)(least >> 23) < e14 - 31 ? 0.f : __uint_as_float((uint32_t)(e14 - 14) << 23);
+                float back = __uint_as_float((uint32_t)(e14 - 14) << 23);  // 2^(e14 - 141)
+                if (__any_sync(0xffffffffu, low)) {
+                    low |= __shfl_xor_sync(0xffffffffu, low, 1) != 0;
+                    low |= __shfl_xor_sync(0xffffffffu, low, 2) != 0;
+                    if (low) back = 0.f, v[0] = v[1] = v[2] = v[3] = 0;
+                    unheld |= low;
+                }
+                if ((c & 3) == 0 && c < n_blocks * 4) xe[c >> 2] = back;
             }
             if (c < n_blocks * 4)
                 *reinterpret_cast<uint4*>(xs + (c >> 2) * kPitch + (c & 3) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        __syncthreads();
+        const bool any_unheld = !kF16 && __syncthreads_or(unheld);
+        if (kF16) __syncthreads();
         int64_t row = row0;
         int blk = sub, step = 0;
         const int total = g.rounds * steps;
@@ -138,7 +156,9 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                     const uint32_t x = xbase + blk * kPitch;
                     float scale = mx4::scale_f32(sc), e = kF16 ? 1.f : xe[blk];
                     float sum = 0.f, sum1 = 0.f;
-                    if ((exact_in<T>(sc) || (c[0] | c[1] | c[2] | c[3]) == 0) && e != 0.f) {
+                    // (the products of a large scale's values and X as staged may leave fp32's range)
+                    const bool alone = !exact_in<T>(sc) && (c[0] | c[1] | c[2] | c[3]) != 0;
+                    if (!alone) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint32_t p[4] = {mx4::pair_f16<0>(c[k]), mx4::pair_f16<1>(c[k]), mx4::pair_f16<2>(c[k]),
@@ -153,19 +173,10 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                             fma2(p[3], y.w, sum, sum1);
                         }
                         sum += sum1;
-                    } else {  // the values as X's type has them, and X as it was given (staged, it may leave fp32's range, or have lost bits)
+                    }
+                    if (alone || (any_unheld && e == 0.f)) {
+                        sum = value_sum(X + (s0 + blk) * kMx4Block, g.a.cols - (s0 + blk) * kMx4Block, w[u], sc);
                         scale = e = 1.f;
-#pragma unroll 1
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t word = k == 0 ? c[0] : k == 1 ? c[1] : k == 2 ? c[2] : c[3];
-                            uint32_t o[4];
-                            mx4::decode8_any<T>(word, sc, o);
-                            float f[8];
-                            Elt<T>::unpack(make_uint4(o[0], o[1], o[2], o[3]), f);
-                            const int64_t at = (s0 + blk) * kMx4Block + k * 8;
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) sum = fmaf(f[j], at + j < g.a.cols ? Elt<T>::to_f(X[at + j]) : 0.f, sum);
-                        }
                     }
                     const float both = scale * e;
                     acc = both <= 3.402823466e38f ? fmaf(sum, both, acc) : fmaf(sum * scale, e, acc);
