@@ -100,3 +100,37 @@ def test_an_infinity_beside_them(fmt, tokens, back):
     X[:, 40] = float("inf")
     want = np.copysign(np.inf, (w if back else w.T)[40])
     assert np.array_equal(as_f64(product(X, W, back)), np.tile(want, (tokens, 1)))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "f32"])
+@pytest.mark.parametrize("tokens", [1, 2, 5, 8, 9, 40])
+@pytest.mark.parametrize("x_exp,w_byte", [(-70, 60), (-20, 10), (-115, 105), (-44, 36), (-47, 61), (-2, 0)])
+@BACK
+def test_small_values_on_both_sides(fmt, tokens, x_exp, w_byte, back):
+    """Sums of 4096 products of about 2^-134 (2^-122 and more), in range although X's power of two times the scale is not. Products
+    are multiples of 2^-149, as fp32's sums are, so the bound on sums holds for them; one more half step for those below a
+    multiple in bf16's and fp32's subnormal numbers is in helpers.ulp."""
+    rng = np.random.default_rng(tokens)
+    C, F = 4096, 40
+    rows, cols = (C, F) if back else (F, C)
+    W, w = stored(rng.integers(4, 8, (rows, cols)), np.full((rows, -(-cols // 32)), w_byte), cols)
+    m = w if back else w.T
+    X = torch.from_numpy((1 + rng.integers(0, 64, (tokens, C)) / 64) * 2.0 ** x_exp).to(DTYPES[fmt]).to(DEV)
+    x = as_f64(X)
+    assert_elementwise(product(X, W, back), x @ m, np.abs(x) @ np.abs(m), C, fmt, "Y")
+
+
+@pytest.mark.parametrize("tokens", [1, 2, 8])
+def test_a_large_scale_and_large_values(tokens):
+    """X's power of two times the scale beyond fp32's range, the products within it."""
+    rng = np.random.default_rng(tokens)
+    C, F = 96, 64
+    x = np.ldexp(1.0, rng.integers(100, 128, (tokens, C))) * rng.choice([-1.0, 1.0], (tokens, C))
+    x[:, ::32] = 2.0 ** 127
+    pick = rng.choice(np.setdiff1d(np.arange(C), [0, 32, 64]), F)
+    x[:, pick] = np.ldexp(1.0, rng.integers(96, 100, F))  # 2^99 at most; times 6 * 2^20 no more than 2^122
+    codes = np.zeros((F, C), dtype=np.int64)
+    codes[np.arange(F), pick] = rng.integers(1, 8, F)
+    W, w = stored(codes, np.full((F, 3), 147), C)
+    X = torch.from_numpy(x).to(torch.bfloat16).to(DEV)
+    assert torch.equal(sp.mx4_linear(X, W).cpu(), torch.from_numpy(as_f64(X) @ w.T).bfloat16())

@@ -66,10 +66,10 @@ __device__ __forceinline__ uint4 lds_v4(uint32_t addr) {
 }
 
 // A scale with which a block's sums can be multiplied as they are: its values are their codes times it in X's type too
-// (fp16), and times X's own power of two it is no infinity (bf16).
+// (fp16), and times X's own power of two, 2^-60 to 2^113, it is a normal number (bf16).
 template <typename T>
 __device__ __forceinline__ bool simple(uint32_t b) {
-    return std::is_same<T, __half>::value ? b - 104u <= 36u : b - 1u <= 140u;
+    return std::is_same<T, __half>::value ? b - 104u <= 36u : b - 61u <= 80u;
 }
 
 // The other scales: a word's values in X's type as fp16 numbers, to be multiplied with rare_factor. fp16: the values
@@ -197,8 +197,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
         unheld = false;
         if (p >= phases) return;
         const uint32_t to = sbase + (p & 1) * kX, te = xe_at + (p & 1) * kXe;
-        bool low = false;  // eight bits of a number below 2^-31 of its block's largest are more than fp16 holds there
-        uint32_t e14s[kLoads];
+        // eight bits of a number below 2^-31 of its block's largest are more than fp16 holds there (and a block of tiny numbers'
+        // power of two would be too small for `simple`)
+        bool low = false;
+        int limit[kLoads];
 #pragma unroll
         for (int u = 0; u < kLoads; ++u) {
             const int i = u * kThreads + tid, r = i / (kBlocks * 4), c = i % (kBlocks * 4);
@@ -220,10 +222,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
                 const uint32_t e14 = max(m >> 7, 31u);                     // the largest comes to 2^14 .. 2^15, tiny ones below
                 const float down = __uint_as_float((268u - e14) << 23);  // 2^(141 - e14)
-                low |= mx4::least8(v) < ((int)e14 - 31) << 7;
+                limit[u] = e14 < 81u ? 0x7f80 : ((int)e14 - 31) << 7;
+                low |= mx4::least8(v) < limit[u];
                 v = make_uint4(Elt<__half>::p2(f[0] * down, f[1] * down), Elt<__half>::p2(f[2] * down, f[3] * down),
                                Elt<__half>::p2(f[4] * down, f[5] * down), Elt<__half>::p2(f[6] * down, f[7] * down));
-                e14s[u] = e14;
                 if ((c & 3) == 0)
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(te + ((c >> 2) * kTokens + r) * 4), "r"((e14 - 14) << 23)
                                  : "memory");
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) mx4_rows_kernel(const RowsAr
 #pragma unroll
             for (int u = 0; u < kLoads; ++u) {
                 const int i = u * kThreads + tid, r = i / (kBlocks * 4), c = i % (kBlocks * 4);
-                low = mx4::least8(xr[u]) < ((int)e14s[u] - 31) << 7;
+                low = mx4::least8(xr[u]) < limit[u];
                 low |= __shfl_xor_sync(0xffffffffu, low, 1) != 0;
                 low |= __shfl_xor_sync(0xffffffffu, low, 2) != 0;
                 if (low) {

@@ -55,6 +55,12 @@ __device__ __noinline__ float value_sum(const T* x, int64_t left, uint4 codes, u
     return sum;
 }
 
+// acc + sum * scale * e where the product of the last two is no normal number in fp32, and the sum may be one. (A call: as
+// predicated instructions the products in 64 bits took a block twice its time.)
+__device__ __noinline__ float add_scaled(float acc, float sum, float scale, float e) {
+    return (float)(acc + (double)sum * scale * e);
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
     constexpr bool kF16 = std::is_same<T, __half>::value;
@@ -122,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                 }
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const int e14 = max((int)(m >> 23), 31);  // the largest comes to 2^14 .. 2^15, small ones below
+                const int e14 = m ? max((int)(m >> 23), 31) : 141;  // the largest comes to 2^14 .. 2^15, small ones below
                 const float down = __uint_as_float((uint32_t)(268 - e14) << 23);  // 2^(141 - e14)
                 bool low = mx4::least8(make_uint4(v[0], v[1], v[2], v[3])) < (e14 - 31) << 7;  // (more than fp16 holds there)
 #pragma unroll
@@ -179,7 +185,8 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                         scale = e = 1.f;
                     }
                     const float both = scale * e;
-                    acc = both <= 3.402823466e38f ? fmaf(sum, both, acc) : fmaf(sum * scale, e, acc);
+                    if (both >= 0x1p-126f && both <= 3.402823466e38f) acc = fmaf(sum, both, acc);
+                    else acc = add_scaled(acc, sum, scale, e);
                 }
                 ask(u);
                 blk += L;
