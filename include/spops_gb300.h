@@ -414,9 +414,9 @@ SPOPS_API int spops_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, 
 /* Products of token-major activations with W, its values rounded to the activations' type (as spops_mx4_dequantize
  * gives them), fp32 sums, rounded once. Rows of X and Y lie ldx and ldy elements apart (a slice of a fused projection's
  * columns can be an operand). No token's values reach another's result. Deterministic. Y must not overlap the other
- * arrays. fp32 X is split into three bf16 parts (all 24 bits), which meet the weight's bf16 values on the tensor cores
- * (sums of up to 715827840 values; more are refused);
- * fp16 and bf16 rows that do not begin on 16-byte boundaries, or whose columns are no multiple of 8, are copied in
+ * arrays. fp32 X is split into three bf16 parts (all 24 bits; numbers below 2^-110 to the nearest multiple of
+ * 2^-133, bf16's least), which meet the weight's bf16 values on the tensor cores (sums of up to 715827840 values; more are
+ * refused); fp16 and bf16 rows that do not begin on 16-byte boundaries, or whose columns are no multiple of 8, are copied in
  * between. These calls (but for fp16 and bf16 forward products of up to 8 tokens) need a 16-byte aligned workspace of at
  * least spops_mx4_workspace_size bytes; others may pass NULL. Values beyond the type's range are infinite (fp32: as far
  * as bf16's), and make what they meet infinite or NaN. */

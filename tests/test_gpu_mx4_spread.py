@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import mx4_reference as ref
-from helpers import as_f64, assert_elementwise
+from helpers import as_f64, assert_elementwise, ulp
 
 pytestmark = pytest.mark.gpu
 
@@ -134,3 +134,23 @@ def test_a_large_scale_and_large_values(tokens):
     W, w = stored(codes, np.full((F, 3), 147), C)
     X = torch.from_numpy(x).to(torch.bfloat16).to(DEV)
     assert torch.equal(sp.mx4_linear(X, W).cpu(), torch.from_numpy(as_f64(X) @ w.T).bfloat16())
+
+
+@pytest.mark.parametrize("tokens", [1, 8, 40, 300])
+@BACK
+def test_small_fp32_numbers(tokens, back):
+    """All 24 bits from 2^-110 on; below, the third bf16 part is off by half of 2^-133. One product an output, of fp32's normal numbers,
+    rounded once."""
+    rng = np.random.default_rng(tokens)
+    C, F = 320, 200
+    codes = np.zeros((C, F) if back else (F, C), dtype=np.int64)
+    pick = rng.integers(0, C, F)
+    codes[(pick, np.arange(F)) if back else (np.arange(F), pick)] = rng.integers(1, 8, F)
+    W, w = stored(codes, np.full((codes.shape[0], -(-codes.shape[1] // 32)), 127 + 60), codes.shape[1])
+    m = w if back else w.T
+    x = (rng.integers(2 ** 23, 2 ** 24, (tokens, C)) * 2.0 ** -23) * np.ldexp(1.0, rng.integers(-126, -104, (tokens, C)))
+    X = torch.from_numpy(x).float().to(DEV)
+    assert np.array_equal(as_f64(X), x)
+    want = x @ m
+    left = np.where(x[:, pick] < 2.0 ** -110, 2.0 ** -134, 0.0) * m[pick, np.arange(F)]
+    assert np.all(np.abs(as_f64(product(X, W, back)) - want) <= left + 0.5 * ulp(want + left, "f32"))

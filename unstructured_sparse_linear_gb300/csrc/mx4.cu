@@ -267,8 +267,9 @@ __global__ void __launch_bounds__(kThreads) mx4_copy_kernel(const T* from, int64
             to[r * ldt + c] = c < cols ? from[r * ldf + c] : (T)0;
 }
 
-// fp32 as the sum of three bf16 parts, rounded towards zero but for the last: 8 bits each, all 24 of a number. part: columns
-// of a part. Infinities and NaN are their first part, beside zeros.
+// fp32 as the sum of three bf16 parts, rounded towards zero but for the last: 8 bits each, all 24 of a number from 2^-110 on. Below,
+// the last part ends at bf16's least number, 2^-133: off by 2^-134 at most (parts times a power of two of their own would need
+// accumulators of their own, or a factor per token behind the product). part: columns of a part. Infinities and NaN are their first part, beside zeros.
 __global__ void __launch_bounds__(kThreads) mx4_split_kernel(const float* from, int64_t ldf, uint16_t* to, int64_t rows,
                                                              int64_t cols, int64_t part) {
     pdl_trigger();

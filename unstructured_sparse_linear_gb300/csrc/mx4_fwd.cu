@@ -13,7 +13,7 @@
 // bf16 (conversions, byte moves), 14 in fp16, which with the messages makes a stage 1000 cycles: what small products take (64
 // tokens: 14.1 us for 22.5 MB of codes, 12.2 in fp16). From 160 tokens a tile on the products take longer: 8192 tokens
 // 2048 -> 8192 149 us, 1840 TFLOP/s.
-// fp32: the weight's values are bf16 numbers, and X is the sum of three bf16 parts (all 24 bits), which multiply the same
+// fp32: the weight's values are bf16 numbers, and X is the sum of three bf16 parts (mx4_split_kernel), which multiply the same
 // decoded weight; the first part's products have an accumulator of their own (relative error 4e-8 at 384 of the contraction,
 // 2e-7 at 4096; 1.2e-6 at 384 with one accumulator).
 #include "mx4_pair.cuh"

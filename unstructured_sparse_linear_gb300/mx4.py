@@ -186,9 +186,9 @@ def _product(X, W, out, back, name):
 
 
 def mx4_linear(X: torch.Tensor, W: Mx4, out: torch.Tensor | None = None) -> torch.Tensor:
-    """Y = X W^T for X [tokens, cols] (on the tensor cores; fp32 as three bf16 parts, all 24 bits), W's values in X's
-    type, fp32 sums. Autograd records nothing of it (RosaLinear is the form that it differentiates): an out that belongs
-    to an autograd graph is refused."""
+    """Y = X W^T for X [tokens, cols] (on the tensor cores; fp32 as three bf16 parts: all 24 bits, below 2^-110 to the
+    nearest multiple of 2^-133), W's values in X's type, fp32 sums. Autograd records nothing of it (RosaLinear is the form
+    that it differentiates): an out that belongs to an autograd graph is refused."""
     return _product(X, W, out, False, "X")
 
 
