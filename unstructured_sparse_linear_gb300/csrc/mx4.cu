@@ -43,7 +43,7 @@ __device__ __forceinline__ Raw<T> load8(const T* p, int n, bool vec) {
     Raw<T> r;
     if (vec && n >= 8) {
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = ld_nc_v4(reinterpret_cast<const char*>(p) + 16 * i);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = ld_v4(reinterpret_cast<const char*>(p) + 16 * i);
     } else {
         T e[8];
 #pragma unroll
@@ -189,8 +189,8 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint32_t
             if (i < items) {
                 const int64_t row = w.rows == 1 ? 0 : i / w.steps, eight = (i - row * w.steps) * 32 + lane;
                 if (eight < w.blocks * 4) {
-                    c[u] = __ldg(codes + row * w.blocks * 4 + eight);
-                    b[u] = __ldg(scales + row * w.blocks + (eight >> 2));
+                    c[u] = codes[row * w.blocks * 4 + eight];
+                    b[u] = scales[row * w.blocks + (eight >> 2)];
                 }
             }
         }
@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_flat_kernel(const uin
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int64_t p = p0 + u * step;
-            c[u] = p < pieces ? __ldg(reinterpret_cast<const Code*>(codes) + p) : 0;
-            b[u] = p < pieces ? __ldg(scales + p / (kMx4Block / kVals)) : 127;
+            c[u] = p < pieces ? reinterpret_cast<const Code*>(codes)[p] : 0;
+            b[u] = p < pieces ? scales[p / (kMx4Block / kVals)] : 127;
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {

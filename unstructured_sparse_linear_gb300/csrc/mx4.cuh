@@ -6,6 +6,9 @@
 
 #include "common.cuh"
 
+// Codes, scales and X are read by plain loads: these kernels begin while the one before them in the stream may still be
+// writing those arrays, and read-only loads (ld.global.nc, __ldg) promise that nobody does as long as a kernel runs.
+
 namespace spops {
 namespace mx4 {
 

@@ -217,8 +217,8 @@ mx4_back_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, con
                     k.b[2 * h + x] = 0;
                     if (row + h * kKC < g.rows && (x ? in1 : in0)) {
                         const int64_t at = h * next64 + x * 2;
-                        k.w[2 * h + x] = ld_nc_v4(pc + at * 16);
-                        k.b[2 * h + x] = __ldg(ps + at);
+                        k.w[2 * h + x] = ld_v4(pc + at * 16);
+                        k.b[2 * h + x] = ps[at];
                     }
                 }
             }

@@ -251,20 +251,20 @@ mx4_fwd_kernel(const TileArgs g, const __grid_constant__ CUtensorMap map_w, cons
             if (in) {
                 if (whole) {
                     if constexpr (kSub == 4) {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(ps));
+                        const uint2 v = *reinterpret_cast<const uint2*>(ps);
                         b.w[0] = v.x;
                         b.w[1] = v.y;
                     } else if constexpr (kSub == 2) {
-                        b.w[0] = __ldg(reinterpret_cast<const uint32_t*>(ps));
+                        b.w[0] = *reinterpret_cast<const uint32_t*>(ps);
                     } else {
-                        b.w[0] = kOnes << 16 | __ldg(reinterpret_cast<const uint16_t*>(ps));
+                        b.w[0] = kOnes << 16 | *reinterpret_cast<const uint16_t*>(ps);
                     }
                 } else {
                     const int64_t blk = (int64_t)(me.c0 + ac) * kBlocks;
 #pragma unroll
                     for (int x = 0; x < kBlocks; ++x)
                         if (blk + x < g.blocks)
-                            b.w[x / 4] = (b.w[x / 4] & ~(255u << (8 * (x % 4)))) | (uint32_t)__ldg(ps + x) << (8 * (x % 4));
+                            b.w[x / 4] = (b.w[x / 4] & ~(255u << (8 * (x % 4)))) | (uint32_t)ps[x] << (8 * (x % 4));
                 }
             }
             ac += groups;

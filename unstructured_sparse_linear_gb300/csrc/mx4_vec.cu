@@ -86,8 +86,8 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
             b[u] = 127;
             if (ask_round < g.rounds && ask_row < g.a.rows && ask_blk < n_blocks) {
                 const int64_t at = ask_row * g.blocks + s0 + ask_blk;
-                w[u] = ld_nc_v4(g.a.codes + at * 16);
-                b[u] = __ldg(g.a.scales + at);
+                w[u] = ld_v4(g.a.codes + at * 16);
+                b[u] = g.a.scales[at];
             }
             ask_blk += L;
             if (ask_blk >= steps * L) {
