@@ -1,0 +1,34 @@
+"""What copies and pickles of 4-bit weights and of their layers hold, without a GPU."""
+import copy
+import io
+import pickle
+
+import pytest
+import torch
+
+sp = pytest.importorskip("unstructured_sparse_linear_gb300")
+
+
+def elsewhere():
+    """A weight whose arrays came back from a file on another device than the one they were on."""
+    codes, scales = torch.arange(96, dtype=torch.uint8).view(3, 32), torch.arange(6, dtype=torch.uint8).view(3, 2)
+    return sp.Mx4._of(codes, scales, (3, 33), torch.float16, torch.device("cuda", 0))
+
+
+def saved(W):
+    f = io.BytesIO()
+    torch.save(W, f)
+    f.seek(0)
+    return torch.load(f, map_location="cpu", weights_only=False)
+
+
+@pytest.mark.parametrize("again", [copy.deepcopy, lambda W: pickle.loads(pickle.dumps(W)), saved], ids=["copy", "pickle", "file"])
+def test_a_weight_is_where_its_arrays_are(again):
+    W = elsewhere()
+    V = again(W)
+    assert V.device == torch.device("cpu") and V.shape == (3, 33) and V.dtype is torch.float16
+    assert torch.equal(V.codes, W.codes) and torch.equal(V.scales, W.scales) and V.codes is not W.codes
+    X = torch.zeros(2, 33, dtype=torch.float16)
+    for call in (lambda: sp.mx4_linear(X, V), lambda: sp.mx4_linear_grad(X[:, :3], V), lambda: sp.mx4_dequantize(V)):
+        with pytest.raises(ValueError, match="W is on cpu"):
+            call()

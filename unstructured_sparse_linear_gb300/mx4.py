@@ -56,6 +56,9 @@ class Mx4:
         W._codes, W._scales, W._shape, W.dtype, W.device = codes, scales, shape, dtype, device
         return W
 
+    def __reduce__(self):  # (a copy from a file is where its arrays were brought to)
+        return _again, (self._codes, self._scales, self._shape, self.dtype)
+
     @property
     def codes(self) -> torch.Tensor:
         return self._codes
@@ -72,6 +75,10 @@ class Mx4:
         return f"Mx4({self._shape[0]} x {self._shape[1]}, {self.dtype}, {self.device})"
 
 
+def _again(codes, scales, shape, dtype):
+    return Mx4._of(codes, scales, shape, dtype, codes.device)
+
+
 def _given(out, name, rows, cols, dtype, device):
     """(address, row stride) of an output that the caller gave."""
     at = _rows(out, name, rows, cols, dtype, device)
@@ -83,6 +90,8 @@ def _given(out, name, rows, cols, dtype, device):
 def _weight(W):
     if type(W) is not Mx4 and not isinstance(W, Mx4):
         raise TypeError(f"W must be an Mx4, got {type(W).__name__}")
+    if W.device.index is None:  # (loaded without its device)
+        raise ValueError(f"W is on {W.device}: it must be on a CUDA device")
     return W
 
 
