@@ -32,3 +32,15 @@ def test_a_weight_is_where_its_arrays_are(again):
     for call in (lambda: sp.mx4_linear(X, V), lambda: sp.mx4_linear_grad(X[:, :3], V), lambda: sp.mx4_dequantize(V)):
         with pytest.raises(ValueError, match="W is on cpu"):
             call()
+
+
+def test_a_layer_pickled_before_it_had_four_bits():
+    layer = sp.RosaLinear(torch.randn(6, 8), 2, scale=0.5)
+    state = layer.__getstate__()
+    state = {k: v for k, v in state.items() if k not in ("dropout", "_quantized")}
+    state["_buffers"] = {k: v for k, v in state["_buffers"].items() if k not in ("codes", "scales")}
+    old = sp.RosaLinear.__new__(sp.RosaLinear)
+    old.__setstate__(state)
+    assert old.dropout == 0.0 and old.quantized is None and old.scale == 0.5
+    assert torch.equal(old.merged(None), layer.weight) and set(old.state_dict()) == set(layer.state_dict())
+    assert set(copy.deepcopy(old)._buffers) == set(layer._buffers)

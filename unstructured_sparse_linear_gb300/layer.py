@@ -286,6 +286,11 @@ class RosaLinear(_MaskedLayer):
     def __getstate__(self):  # a copy or a pickle of the layer makes its own plans
         return {**super().__getstate__(), "_plans": {}, "_captured": {}, "_quantized": None}
 
+    def __setstate__(self, state):  # (one that was pickled before there were 4-bit weights and dropout has none)
+        super().__setstate__({"dropout": 0.0, **state})
+        for name in ("codes", "scales"):
+            self._buffers.setdefault(name, None)
+
     @property
     def quantized(self) -> Mx4 | None:
         """The frozen weight as an Mx4, of the buffers ``codes`` and ``scales`` (None: it is a dense one)."""
