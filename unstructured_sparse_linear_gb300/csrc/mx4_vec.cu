@@ -42,23 +42,21 @@ __device__ __forceinline__ bool exact_in(uint32_t b) {
     return std::is_same<T, __half>::value ? b - 104u <= 36u || b == 255u : b <= 252u || b == 255u;
 }
 
-// A block's products with up to 32 values of X, value by value, as X's type has them.
+// acc with a block's products, where its scale times X's power of two e is no normal number in fp32 or its values are not their
+// codes times the scale. sum: the codes' products with X as staged. (A call: it would crowd the loop.)
 template <typename T>
-__device__ __noinline__ float value_sum(const T* x, int64_t left, uint4 codes, uint32_t b) {
-    const float s = mx4::scale_f32(b);
-    float sum = 0.f;
+__device__ __noinline__ float add_uncommon(float acc, float sum, float e, const T* x, int64_t left, uint4 codes, uint32_t b) {
+    const bool zeros = (codes.x | codes.y | codes.z | codes.w) == 0 && b != 255;
+    if (e != 0.f && zeros) return acc + sum;  // (zeros, or NaN)
+    const float scale = mx4::scale_f32(b);
+    if (e != 0.f && exact_in<T>(b)) return (float)(acc + (double)sum * scale * e);
+    float y = 0.f;  // value by value, as X's type has them, and X as it was given
 #pragma unroll 1
     for (int k = 0; k < kMx4Block && k < left; ++k) {
         const uint32_t w = k < 8 ? codes.x : k < 16 ? codes.y : k < 24 ? codes.z : codes.w;
-        sum = fmaf(Elt<T>::to_f(Elt<T>::from_f(mx4::value_f32(w >> (4 * (k & 7)), s))), Elt<T>::to_f(x[k]), sum);
+        y = fmaf(Elt<T>::to_f(Elt<T>::from_f(mx4::value_f32(w >> (4 * (k & 7)), scale))), Elt<T>::to_f(x[k]), y);
     }
-    return sum;
-}
-
-// acc + sum * scale * e where the product of the last two is no normal number in fp32, and the sum may be one. (A call: as
-// predicated instructions the products in 64 bits took a block twice its time.)
-__device__ __noinline__ float add_scaled(float acc, float sum, float scale, float e) {
-    return (float)(acc + (double)sum * scale * e);
+    return acc + y;
 }
 
 template <typename T>
@@ -99,7 +97,6 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) ask(u);
         if (s0 > 0) __syncthreads();  // the segment before has been read
-        bool unheld = false;  // bf16: fp16 does not hold a block of this thread's; it is staged as zeros, its xe as 0
         for (int i0 = 0; i0 < n_blocks * 4; i0 += kThreads) {
             const int c = i0 + tid;  // 16 bytes of X
             const int64_t k = s0 * kMx4Block + c * 8;
@@ -140,16 +137,14 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                 if (__any_sync(0xffffffffu, low)) {
                     low |= __shfl_xor_sync(0xffffffffu, low, 1) != 0;
                     low |= __shfl_xor_sync(0xffffffffu, low, 2) != 0;
-                    if (low) back = 0.f, v[0] = v[1] = v[2] = v[3] = 0;
-                    unheld |= low;
+                    if (low) back = 0.f;
                 }
                 if ((c & 3) == 0 && c < n_blocks * 4) xe[c >> 2] = back;
             }
             if (c < n_blocks * 4)
                 *reinterpret_cast<uint4*>(xs + (c >> 2) * kPitch + (c & 3) * 16) = make_uint4(v[0], v[1], v[2], v[3]);
         }
-        const bool any_unheld = !kF16 && __syncthreads_or(unheld);
-        if (kF16) __syncthreads();
+        __syncthreads();
         int64_t row = row0;
         int blk = sub, step = 0;
         const int total = g.rounds * steps;
@@ -160,33 +155,28 @@ __global__ void __launch_bounds__(kThreads, 4) mx4_vec_kernel(const VecArgs g) {
                 if (blk < n_blocks) {
                     const uint32_t c[4] = {w[u].x, w[u].y, w[u].z, w[u].w}, sc = b[u];
                     const uint32_t x = xbase + blk * kPitch;
-                    float scale = mx4::scale_f32(sc), e = kF16 ? 1.f : xe[blk];
+                    const float e = kF16 ? 1.f : xe[blk], both = mx4::scale_f32(sc) * e;
                     float sum = 0.f, sum1 = 0.f;
-                    // (the products of a large scale's values and X as staged may leave fp32's range)
-                    const bool alone = !exact_in<T>(sc) && (c[0] | c[1] | c[2] | c[3]) != 0;
-                    if (!alone) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t p[4] = {mx4::pair_f16<0>(c[k]), mx4::pair_f16<1>(c[k]), mx4::pair_f16<2>(c[k]),
-                                                   mx4::pair_f16<3>(c[k])};
-                            uint4 y;
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
-                                         : "r"(x + k * 16));
-                            fma2(p[0], y.x, sum, sum1);
-                            fma2(p[1], y.y, sum, sum1);
-                            fma2(p[2], y.z, sum, sum1);
-                            fma2(p[3], y.w, sum, sum1);
-                        }
-                        sum += sum1;
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t p[4] = {mx4::pair_f16<0>(c[k]), mx4::pair_f16<1>(c[k]), mx4::pair_f16<2>(c[k]),
+                                               mx4::pair_f16<3>(c[k])};
+                        uint4 y;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                                     : "r"(x + k * 16));
+                        fma2(p[0], y.x, sum, sum1);
+                        fma2(p[1], y.y, sum, sum1);
+                        fma2(p[2], y.z, sum, sum1);
+                        fma2(p[3], y.w, sum, sum1);
                     }
-                    if (alone || (any_unheld && e == 0.f)) {
-                        sum = value_sum(X + (s0 + blk) * kMx4Block, g.a.cols - (s0 + blk) * kMx4Block, w[u], sc);
-                        scale = e = 1.f;
+                    sum += sum1;
+                    if (exact_in<T>(sc) && both >= 0x1p-126f && both <= 3.402823466e38f) {
+                        acc = fmaf(sum, both, acc);
+                    } else {
+                        const int64_t k = (s0 + blk) * kMx4Block;
+                        acc = add_uncommon(acc, sum, e, X + k, g.a.cols - k, w[u], sc);
                     }
-                    const float both = scale * e;
-                    if (both >= 0x1p-126f && both <= 3.402823466e38f) acc = fmaf(sum, both, acc);
-                    else acc = add_scaled(acc, sum, scale, e);
                 }
                 ask(u);
                 blk += L;
