@@ -8,7 +8,8 @@
 // All kernels stream: four lanes share a block, a lane has eight values (16 bytes of a 16-bit type, 4 bytes of codes; from
 // codes to fp32 four values), and a warp several steps of 256 values, loaded before any is used. The flat kernels take
 // matrices of whole blocks without gaps between the rows, on 16-byte boundaries, as one long row, without any bounds but the
-// end: 11008 x 4096 bf16 to 4 bits 22.6 us (37 by rows), back 19.2 (27). Bound by HBM, to 4 bits also by what a warp issues.
+// end: 11008 x 4096 bf16 to 4 bits 22.6 us, back 18.7. Bound by HBM, to 4 bits also by what a warp issues. By rows 39 and 35 (a
+// division per step of 256 values), rows that do not begin on 16-byte boundaries value by value: 11008 x 4100 44 and 129.
 #include "internal.h"
 #include "mx4.cuh"
 #include "mx4.h"
@@ -355,9 +356,12 @@ cudaError_t launch_mx4_dequantize(int dt, const uint8_t* codes, const uint8_t* s
     return dequantize<__nv_bfloat16>(codes, scales, rows, cols, Y, ldy, s);
 }
 
-// The kernels without tensor-core tiles, forward, us as these kernels / the tiles. 1 token: 4096 x 4096 6.3 / 8.6,
-// 11008 x 4096 12.5 / 13.9, 8192 x 8192 16.5 / 15.2, fp16 14.7 / 13.0. 2 to 8: 4096 x 4096 8.1 / 8.6, fp16 6.7 / 7.6,
-// 1024 x 16384 8.1 / 13.1, 1536 x 384 3.5 / 4.9, but 6144 x 4096 12.5 / 10.1, fp16 9.8 / 8.9, 8192 x 8192 23 / 15. They take any rows.
+// The kernels without tensor-core tiles, forward, us as these kernels / the tiles. 1 token: 4096 x 4096 6.3 / 8.5, fp16 5.1 /
+// 7.4, 11008 x 4096 12.2 / 13.4, fp16 10.9 / 11.3, 8192 x 8192 16.3 / 14.9, fp16 13.6 / 12.7. 8: 4096 x 4096 8.6 / 8.6, fp16
+// 6.8 / 7.5, 1536 x 384 3.8 / 4.8, but 6144 x 4096 13.6 / 10.0, fp16 10.0 / 8.7, 8192 x 8192 25.4 / 15.0. They take any rows.
+// The number of values decides, which is right for weights about as wide as long. The tiles need features, of which each 256 are
+// a pair's and at most four splits: 8 tokens of 1024 x 16384 8.8 / 13.4, and just above the limit 1024 x 32768 would be 14.7
+// and is 22.0, 512 x 65536 25.8 and 38; 16384 x 1024 is 8.6 and would be 6.9.
 static bool mx4_few(int dt, bool back, const Mx4Args& a) {
     if (back || dt == kF32 || a.tokens > kMx4FewTokens) return false;
     const int64_t values = (int64_t)a.rows * a.cols;

@@ -10,9 +10,12 @@
 // code alone).
 // Bounds. Per 64 of the contraction shared memory takes the decoded operand twice (written, read) and X twice: 512 cycles at 256
 // tokens, as many as the products (8192 tokens 8192 -> 2048: 91 % of its wavefronts, tensor pipe 82 %). 4096 tokens
-// 11008 -> 4096 213 us, 1736 TFLOP/s; 2048 tokens 4096 -> 4096 fp16 47; 64 tokens 24 to 28, the latency of a stage's decoding.
+// 11008 -> 4096 213 us, 1736 TFLOP/s; 2048 tokens 4096 -> 4096 fp16 47; 64 tokens 24 to 28, the latency of
+// a stage's codes, which a decoder asks for one stage ahead (a warp waits for loads in 6.2 of the 15 cycles between two of its
+// instructions; issue 36 %, integer pipe 28 %), on the 96 SMs that have a tile.
 // fp32: the weight's values are bf16 numbers, and X is the sum of three bf16 parts (mx4_split_kernel), which multiply the same
-// decoded weight; the first part's products have an accumulator of their own.
+// decoded weight; the first part's products have an accumulator of their own. 700 tokens 4096 -> 6136 75 us, 2048
+// tokens 4096 -> 4096 172 (1.4 and 1.6 of their operations' time).
 #include "mx4_pair.cuh"
 
 namespace spops {

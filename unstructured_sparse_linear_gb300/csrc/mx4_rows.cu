@@ -4,12 +4,13 @@
 // instruction in fp16: the codes become fp16 numbers by conversion (exact, without their scale), a block of 32 is two
 // products into sums of its own, which are then added times the block's scale in fp32. So decoding costs 8 conversions
 // for 16 x 32 values, whatever X's type. bf16 X is staged as fp16 numbers times a power of two for each 32 of them, which is
-// exact where none but zeros lies below 2^-31 of the largest; other blocks of a token are multiplied value by value in fp32.
+// exact where none but zeros lies below 2^-31 of the largest (looking for that takes 0.5 us of the times below); other blocks of
+// a token are multiplied value by value in fp32.
 // The codes come by asynchronous copies into rings of the warp's own, X through registers, a phase of the contraction ahead. A
 // CTA's warps have two groups of 16 features and share the contraction by four, a cluster's CTAs share it once more; partial
-// sums are added in one order. Bound by the first loads and by what a warp issues (about 100 instructions a block, a
-// third of them for staging X). 8 tokens, 4096 x 4096: 8.1 us (tcgen05 tiles 8.7), fp16 6.7 (7.7); beyond 2^24 values of W the
-// tiles take less (11008 x 4096 13.9 and 21.2).
+// sums are added in one order. Bound by the first loads and by the latency of 130 instructions a block (a third of them for
+// staging X) that depend on each other, with 3.4 warps a scheduler: it issues in 43 % of the cycles, integer pipe 34 %.
+// 8 tokens, 4096 x 4096: 8.6 us (tcgen05 tiles 8.6), fp16 6.8 (7.5); 11008 x 4096 22.7 (13.5).
 #include <type_traits>
 
 #include "internal.h"

@@ -4,10 +4,12 @@
 // values of one block, so a warp reads 512 bytes in a row, and four such loads are under way, the next row's among them.
 // The codes become fp16 numbers by conversion and meet X as fp16 numbers in fused products with fp32 sums (6 cycles of a
 // scheduler for two values and a token; bringing W to X's type first took 9), one sum per block, which is then multiplied with
-// the block's scale. bf16 X is staged as fp16 numbers times a power of two for each 32 of them, which is exact where none but zeros
-// lies below 2^-31 of the largest; other blocks are multiplied value by value in fp32. Sums are added over the lanes in one order. Bound by the call, the first
-// load, and what a warp issues (about 50 instructions a word of codes). 4096 x 4096: 6.3 us (8.0 with the kernel for eight
-// tokens), 11008 x 4096 12.5 (20.8; tcgen05 tiles 13.9).
+// the block's scale. bf16 X is staged as fp16 numbers times a power of two for each 32 of them, which is exact where none but
+// zeros lies below 2^-31 of the largest. A block for which it is not, or whose scale is uncommon, is multiplied value by value or
+// scaled in 64 bits, found by one test behind its products. Sums are added over the lanes in one order. Bound by what a warp
+// issues (45 instructions a word of codes; the schedulers issue in 64 to 70 % of the cycles, the integer pipe is at 53 to 56 %), and
+// the call and the first load. 4096 x 4096: 6.3 us, fp16 5.1 (8.5 with the kernel for eight tokens, fp16 6.6), 11008 x 4096
+// 12.2, fp16 10.8 (tcgen05 tiles 13.5 and 11.3).
 #include <type_traits>
 
 #include "internal.h"

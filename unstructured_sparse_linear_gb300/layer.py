@@ -198,7 +198,9 @@ class RosaLinearFunction(torch.autograd.Function):
         if state is None:
             dX, dA, dB = lora_grad(dY, X, A, B, ctx.plan, scale=scale, h=h, dX_base=base, dX_out=base,
                                    need=(need_x, need_a, need_b))
-        else:  # what the factors saw, and its gradient through the same mask
+        else:  # what the factors saw, and its gradient through the same mask. (That is rounded to X's type before the mask's
+            # factor and the projection's gradient meet it in fp32: half a step of the low-rank part more than without dropout,
+            # where both are summed before the one rounding; an fp32 one in between would be twice as much to write and read.)
             dropped = _dropout(X, ctx.p, state) if need_a else X
             dX, dA, dB = lora_grad(dY, dropped, A, B, ctx.plan, scale=scale, h=h, need=(need_x, need_a, need_b))
             if need_x:
