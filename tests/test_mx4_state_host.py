@@ -44,3 +44,19 @@ def test_a_layer_pickled_before_it_had_four_bits():
     assert old.dropout == 0.0 and old.quantized is None and old.scale == 0.5
     assert torch.equal(old.merged(None), layer.weight) and set(old.state_dict()) == set(layer.state_dict())
     assert set(copy.deepcopy(old)._buffers) == set(layer._buffers)
+
+
+class Named(sp.Mx4):
+    """A weight with an attribute of its own."""
+
+
+def test_a_kind_of_weight_and_an_older_file():
+    W = elsewhere()
+    N = Named._of(W.codes, W.scales, W.shape, W.dtype, W.device)
+    N.name = "up"
+    V = copy.deepcopy(N)
+    assert type(V) is Named and V.name == "up" and V.device == torch.device("cpu")
+    # (what object's own reduction, which earlier files were written with, restores)
+    old = sp.Mx4.__new__(sp.Mx4)
+    old.__setstate__((None, dict(_codes=W.codes, _scales=W.scales, _shape=(3, 33), dtype=W.dtype, device=torch.device("cuda", 0))))
+    assert old.device == torch.device("cpu") and old.shape == (3, 33)

@@ -56,8 +56,11 @@ class Mx4:
         W._codes, W._scales, W._shape, W.dtype, W.device = codes, scales, shape, dtype, device
         return W
 
-    def __reduce__(self):  # (a copy from a file is where its arrays were brought to)
-        return _again, (self._codes, self._scales, self._shape, self.dtype)
+    def __setstate__(self, state):  # (one from a file is where its arrays were brought to)
+        for part in state:
+            for name, value in (part or {}).items():
+                setattr(self, name, value)
+        self.device = self._codes.device
 
     @property
     def codes(self) -> torch.Tensor:
@@ -73,10 +76,6 @@ class Mx4:
 
     def __repr__(self):
         return f"Mx4({self._shape[0]} x {self._shape[1]}, {self.dtype}, {self.device})"
-
-
-def _again(codes, scales, shape, dtype):
-    return Mx4._of(codes, scales, shape, dtype, codes.device)
 
 
 def _given(out, name, rows, cols, dtype, device):
